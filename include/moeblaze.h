@@ -311,6 +311,151 @@ MOEBLAZE_API moeblaze_status moeblaze_router_dispatch_build(const moeblaze_shape
                                                             const moeblaze_dispatch* out, void* ws, size_t ws_bytes,
                                                             moeblaze_stream stream);
 
+/* The router with its logits: moeblaze_router_forward and
+ * moeblaze_router_dispatch_build with one more output,
+ *   logits  device (L,E) fp32, overwritten, 16-byte aligned: the logits the
+ *           ids and gates were chosen by (bias included)
+ * for a loss on the logits (moeblaze_balance_forward).  Everything else is as
+ * for those two calls, bit for bit. */
+MOEBLAZE_API moeblaze_status moeblaze_router_forward_logits(const moeblaze_shape* s, const void* x, const float* Wr,
+                                                            const float* bias, int32_t* topk_ids, float* gates,
+                                                            float* logits, moeblaze_stream stream);
+MOEBLAZE_API moeblaze_status moeblaze_router_dispatch_build_logits(const moeblaze_shape* s, const void* x,
+                                                                   const float* Wr, const float* bias,
+                                                                   int32_t* topk_ids, float* gates, float* logits,
+                                                                   const moeblaze_dispatch* out, void* ws,
+                                                                   size_t ws_bytes, moeblaze_stream stream);
+
+/* moeblaze_router_backward_logits: the router's gradients from a dense
+ * gradient of its logits (moeblaze_balance_backward's dlogits, which carry
+ * the losses' and the gates' share):
+ *   dWr = x^T dlogits, dbias = sum_t dlogits[t], dx = dlogits Wr^T
+ *   dlogits device (L,E) fp32, 16-byte aligned
+ *   x, Wr, dWr, dbias, dx: as moeblaze_router_backward
+ *   ws      device moeblaze_router_backward_logits_workspace_bytes(s) bytes
+ * Shape, limits and repeatability as moeblaze_router_backward (K is not used
+ * but has to be valid). */
+MOEBLAZE_API size_t moeblaze_router_backward_logits_workspace_bytes(const moeblaze_shape* s);
+MOEBLAZE_API moeblaze_status moeblaze_router_backward_logits(const moeblaze_shape* s, const void* x, const float* Wr,
+                                                             const float* dlogits, float* dWr, float* dbias, void* dx,
+                                                             void* ws, size_t ws_bytes, moeblaze_stream stream);
+
+/* ------------------------------------------------------- the router's losses
+ * The load-balance and z losses of a router on its logits, the tokens per
+ * expert, and the gradient of the logits.  Shape fields used: L, E, K
+ * (E <= 512, K <= 8).  A token is active when valid (if given) is nonzero for
+ * it and at least one of its logits is above -inf; N = number of active
+ * tokens, p = softmax of a token's E logits, lse = their log-sum-exp.
+ *   counts[e] = slots of active tokens with id e (ids outside [0,E): none)
+ *   losses[0] = E sum_e f_e P_e, f_e = counts[e]/(N K), P_e = sum_t p[t,e]/N
+ *   losses[1] = sum_t lse[t]^2 / N          (both 0 when no token is active)
+ *
+ * moeblaze_balance_forward:
+ *   logits   device (L,E) fp32, 16-byte aligned (of tokens that are not valid
+ *            nothing is read)
+ *   topk_ids device (L,K) int32     valid device (L) uint8 or NULL
+ *   losses   device (2) fp32        counts device (E+1) int32, counts[E] = N
+ *   lse      device (L) fp32, -inf for tokens that are not active
+ *   ws       device moeblaze_balance_workspace_bytes(s) bytes
+ * moeblaze_balance_backward, dlosses device (2) fp32 = the gradients of the
+ * two losses; logits, lse, counts as the forward took and wrote them:
+ *   dlogits[t,e] = dlosses[0] E/N p (f_e - sum_j f_j p_j)
+ *                + dlosses[1] 2/N lse p              (counts held constant)
+ *   and, when topk_ids, gates and dgates (all (L,K); NULL together) are
+ *   given, + gates_k (dgates_k - sum_j gates_j dgates_j) on the chosen
+ *   experts: the gates' softmax over the chosen logits.  Rows of tokens that
+ *   are not active are 0.
+ * Sums run in a fixed order: results are repeatable to the bit. */
+MOEBLAZE_API size_t moeblaze_balance_workspace_bytes(const moeblaze_shape* s);
+MOEBLAZE_API moeblaze_status moeblaze_balance_forward(const moeblaze_shape* s, const float* logits,
+                                                      const int32_t* topk_ids, const uint8_t* valid, float* losses,
+                                                      int32_t* counts, float* lse, void* ws, size_t ws_bytes,
+                                                      moeblaze_stream stream);
+MOEBLAZE_API moeblaze_status moeblaze_balance_backward(const moeblaze_shape* s, const float* logits, const float* lse,
+                                                       const int32_t* counts, const float* dlosses,
+                                                       const int32_t* topk_ids, const float* gates,
+                                                       const float* dgates, float* dlogits, moeblaze_stream stream);
+
+/* ---------------------------------------------------------------- layer norm
+ * The norm in front of the layer (pre-norm block), with the residual sum, and
+ * its backward.  Shape fields used: L, d, dtype (any d from 1 to 2^24).
+ *   s = x (+ residual);  mean, rstd = 1/sqrt(var + eps) of each row of s
+ *   y = (s - mean) rstd weight (+ bias)
+ * in fp32, each output rounded once.
+ *   x, residual  device (L,d) dtype (residual NULL: s = x)
+ *   weight, bias device (d) fp32, 16-byte aligned (bias NULL: 0)
+ *   sum          device (L,d) dtype, overwritten with s, or NULL; may be x or
+ *                residual itself
+ *   y            device (L,d) dtype   mean, rstd device (L) fp32
+ * moeblaze_layernorm_backward:
+ *   dy           device (L,d) dtype
+ *   sum          device (L,d) dtype: s as stored (x without a residual)
+ *   dsum         device (L,d) dtype: a gradient that reaches s besides the
+ *                norm (the residual stream's), or NULL
+ *   dx           device (L,d) dtype, overwritten: the gradient of s (of x and
+ *                of the residual alike), dsum included
+ *   dweight, dbias device (d) fp32, overwritten (dbias may be NULL), summed
+ *                over the rows in a fixed order (repeatable to the bit)
+ *   ws           device moeblaze_layernorm_backward_workspace_bytes(s) bytes */
+MOEBLAZE_API moeblaze_status moeblaze_layernorm_forward(const moeblaze_shape* s, const void* x, const void* residual,
+                                                        const float* weight, const float* bias, float eps, void* sum,
+                                                        void* y, float* mean, float* rstd, moeblaze_stream stream);
+MOEBLAZE_API size_t moeblaze_layernorm_backward_workspace_bytes(const moeblaze_shape* s);
+MOEBLAZE_API moeblaze_status moeblaze_layernorm_backward(const moeblaze_shape* s, const void* dy, const void* sum,
+                                                         const float* mean, const float* rstd, const float* weight,
+                                                         const void* dsum, void* dx, float* dweight, float* dbias,
+                                                         void* ws, size_t ws_bytes, moeblaze_stream stream);
+
+/* ------------------------------------------------- experts on 4-bit weights
+ * The layer's forward for few tokens (serving) on 4-bit weights with a scale
+ * for each group of reduction rows:
+ *   W[e][r][n] = q[e][r][n] scales[e][r / group][n],  q in -8..7
+ * The layer's matrices as they are elsewhere: W1, W2 (E,d,h), W3 (E,h,d), so
+ * R = d, N = h for the first two and R = h, N = d for the last.  R and N are
+ * multiples of 128, group is 32, 64 or 128, scales are bf16.
+ *
+ * moeblaze_int4_quantize: W device (E,R,N) dtype -> q device (E,R,N) int8,
+ *   scales device (E,R/group,N) bf16: scale = bf16(max |W| of the group / 7),
+ *   q = round(W / scale) (to even) within -8..7; a group of zeros: scale 0, q 0.
+ * moeblaze_int4_pack: q and scales -> the layout the products read, device
+ *   moeblaze_int4_weight_bytes and moeblaze_int4_scale_bytes bytes; done once
+ *   when the weights are loaded.  Only the low 4 bits of q are kept.
+ * moeblaze_int4_dequantize: packed weights -> W device (E,R,N) bf16 (the
+ *   product rounded once), for moeblaze_forward on long prompts. */
+MOEBLAZE_API size_t moeblaze_int4_weight_bytes(int32_t E, int32_t R, int32_t N);
+MOEBLAZE_API size_t moeblaze_int4_scale_bytes(int32_t E, int32_t R, int32_t N, int32_t group);
+MOEBLAZE_API moeblaze_status moeblaze_int4_quantize(int32_t E, int32_t R, int32_t N, int32_t group, int32_t dtype,
+                                                    const void* W, int8_t* q, void* scales, moeblaze_stream stream);
+MOEBLAZE_API moeblaze_status moeblaze_int4_pack(int32_t E, int32_t R, int32_t N, int32_t group, const int8_t* q,
+                                                const void* scales, void* packed, void* packed_scales,
+                                                moeblaze_stream stream);
+MOEBLAZE_API moeblaze_status moeblaze_int4_dequantize(int32_t E, int32_t R, int32_t N, int32_t group,
+                                                      const void* packed, const void* packed_scales, void* W,
+                                                      moeblaze_stream stream);
+
+/* packed weights and scales of one layer (device; w2, s2 NULL for SiLU) */
+typedef struct {
+  const void *w1, *s1, *w2, *s2, *w3, *s3;
+  int32_t group;
+} moeblaze_int4_experts;
+
+/* moeblaze_int4_forward: y[t] = sum_k gates[t,k] expert_{ids[t,k]}(x[t]) on
+ * the packed weights, straight from the router's ids (no dispatch build).
+ * bf16 x and y, SwiGLU or SiLU (others: MOEBLAZE_ERR_UNSUPPORTED).
+ *   x        device (L,d) bf16       topk_ids device (L,K) int32: an id
+ *            outside [0,E) is an empty slot and adds nothing (a token with
+ *            none but empty slots gets a row of zeros)
+ *   gates    device (L,K) fp32       y device (L,d) bf16, overwritten
+ *   ws       device moeblaze_int4_workspace_bytes(s) bytes
+ * The weights are read once per 64 tokens: made for L up to a few tens.  Sums
+ * are fp32 in a fixed order (repeatable to the bit); the hidden activations
+ * are rounded to bf16 between the two products, as the matrix instructions
+ * take them. */
+MOEBLAZE_API size_t moeblaze_int4_workspace_bytes(const moeblaze_shape* s);
+MOEBLAZE_API moeblaze_status moeblaze_int4_forward(const moeblaze_shape* s, const void* x, const int32_t* topk_ids,
+                                                   const float* gates, const moeblaze_int4_experts* w, void* y,
+                                                   void* ws, size_t ws_bytes, moeblaze_stream stream);
+
 /* Synchronise `stream` and read the device error word of `disp->meta`:
  * *code = 0 when every kernel since the last dispatch_build on this meta
  * finished normally; otherwise a bitwise OR of 1 (bad routing), 2 (a

@@ -32,6 +32,12 @@ EXPORTS = [
     "moeblaze_dispatch_build_static", "moeblaze_dispatch_meta_check", "moeblaze_set_fault_injection",
     "moeblaze_router_forward", "moeblaze_router_backward", "moeblaze_router_backward_workspace_bytes",
     "moeblaze_router_dispatch_workspace_bytes", "moeblaze_router_dispatch_build",
+    "moeblaze_router_forward_logits", "moeblaze_router_dispatch_build_logits", "moeblaze_router_backward_logits",
+    "moeblaze_router_backward_logits_workspace_bytes", "moeblaze_balance_workspace_bytes",
+    "moeblaze_balance_forward", "moeblaze_balance_backward", "moeblaze_layernorm_forward",
+    "moeblaze_layernorm_backward", "moeblaze_layernorm_backward_workspace_bytes", "moeblaze_int4_weight_bytes",
+    "moeblaze_int4_scale_bytes", "moeblaze_int4_quantize", "moeblaze_int4_pack", "moeblaze_int4_dequantize",
+    "moeblaze_int4_workspace_bytes", "moeblaze_int4_forward",
 ]
 
 # fixed scratch of moeblaze_dispatch_build_static (MOEBLAZE_STATIC_SCRATCH_BYTES)
@@ -51,6 +57,11 @@ class Dispatch(ctypes.Structure):
     _fields_ = [("expert_token_indices", ctypes.c_void_p), ("expert_token_offsets", ctypes.c_void_p),
                 ("token_expert_indices", ctypes.c_void_p), ("token_index_map", ctypes.c_void_p),
                 ("meta", ctypes.c_void_p)]
+
+
+class Int4Weights(ctypes.Structure):
+    _fields_ = [("w1", ctypes.c_void_p), ("s1", ctypes.c_void_p), ("w2", ctypes.c_void_p), ("s2", ctypes.c_void_p),
+                ("w3", ctypes.c_void_p), ("s3", ctypes.c_void_p), ("group", ctypes.c_int32)]
 
 
 class MoEBlazeError(RuntimeError):
@@ -93,6 +104,26 @@ def lib():
         L.moeblaze_router_dispatch_workspace_bytes.restype = sz
         L.moeblaze_router_dispatch_build.argtypes = [SP, P, P, P, P, P, DP, P, sz, P]
         L.moeblaze_router_dispatch_build.restype = ctypes.c_int
+        L.moeblaze_router_forward_logits.argtypes = [SP, P, P, P, P, P, P, P]
+        L.moeblaze_router_dispatch_build_logits.argtypes = [SP, P, P, P, P, P, P, DP, P, sz, P]
+        L.moeblaze_router_backward_logits.argtypes = [SP, P, P, P, P, P, P, P, sz, P]
+        L.moeblaze_balance_forward.argtypes = [SP, P, P, P, P, P, P, P, sz, P]
+        L.moeblaze_balance_backward.argtypes = [SP, P, P, P, P, P, P, P, P, P]
+        L.moeblaze_layernorm_forward.argtypes = [SP, P, P, P, P, ctypes.c_float, P, P, P, P, P]
+        L.moeblaze_layernorm_backward.argtypes = [SP, P, P, P, P, P, P, P, P, P, P, sz, P]
+        i32 = ctypes.c_int32
+        L.moeblaze_int4_quantize.argtypes = [i32, i32, i32, i32, i32, P, P, P, P]
+        L.moeblaze_int4_pack.argtypes = [i32, i32, i32, i32, P, P, P, P, P]
+        L.moeblaze_int4_dequantize.argtypes = [i32, i32, i32, i32, P, P, P, P]
+        L.moeblaze_int4_forward.argtypes = [SP, P, P, P, ctypes.POINTER(Int4Weights), P, P, sz, P]
+        for n in ["moeblaze_router_backward_logits_workspace_bytes", "moeblaze_balance_workspace_bytes",
+                  "moeblaze_layernorm_backward_workspace_bytes", "moeblaze_int4_workspace_bytes"]:
+            getattr(L, n).argtypes = [SP]
+            getattr(L, n).restype = sz
+        L.moeblaze_int4_weight_bytes.argtypes = [i32, i32, i32]
+        L.moeblaze_int4_weight_bytes.restype = sz
+        L.moeblaze_int4_scale_bytes.argtypes = [i32, i32, i32, i32]
+        L.moeblaze_int4_scale_bytes.restype = sz
         L.moeblaze_device_error.argtypes = [SP, DP, ctypes.POINTER(ctypes.c_int32), P]
         L.moeblaze_device_error.restype = ctypes.c_int
         L.moeblaze_dispatch_meta_check.argtypes = [SP, P]
@@ -178,6 +209,83 @@ def moeblaze_router_dispatch_workspace_bytes(shape: Shape) -> int:
 def moeblaze_router_dispatch_build(shape, x, Wr, bias, topk_ids, gates, disp, ws, ws_bytes, stream) -> int:
     return lib().moeblaze_router_dispatch_build(ctypes.byref(shape), x, Wr, bias, topk_ids, gates, ctypes.byref(disp),
                                                 ws, ws_bytes, stream)
+
+
+def moeblaze_router_forward_logits(shape, x, Wr, bias, topk_ids, gates, logits, stream) -> int:
+    return lib().moeblaze_router_forward_logits(ctypes.byref(shape), x, Wr, bias, topk_ids, gates, logits, stream)
+
+
+def moeblaze_router_dispatch_build_logits(shape, x, Wr, bias, topk_ids, gates, logits, disp, ws, ws_bytes,
+                                          stream) -> int:
+    return lib().moeblaze_router_dispatch_build_logits(ctypes.byref(shape), x, Wr, bias, topk_ids, gates, logits,
+                                                       ctypes.byref(disp), ws, ws_bytes, stream)
+
+
+def moeblaze_router_backward_logits_workspace_bytes(shape: Shape) -> int:
+    return lib().moeblaze_router_backward_logits_workspace_bytes(ctypes.byref(shape))
+
+
+def moeblaze_router_backward_logits(shape, x, Wr, dlogits, dWr, dbias, dx, ws, ws_bytes, stream) -> int:
+    return lib().moeblaze_router_backward_logits(ctypes.byref(shape), x, Wr, dlogits, dWr, dbias, dx, ws, ws_bytes,
+                                                 stream)
+
+
+def moeblaze_balance_workspace_bytes(shape: Shape) -> int:
+    return lib().moeblaze_balance_workspace_bytes(ctypes.byref(shape))
+
+
+def moeblaze_balance_forward(shape, logits, topk_ids, valid, losses, counts, lse, ws, ws_bytes, stream) -> int:
+    return lib().moeblaze_balance_forward(ctypes.byref(shape), logits, topk_ids, valid, losses, counts, lse, ws,
+                                          ws_bytes, stream)
+
+
+def moeblaze_balance_backward(shape, logits, lse, counts, dlosses, topk_ids, gates, dgates, dlogits, stream) -> int:
+    return lib().moeblaze_balance_backward(ctypes.byref(shape), logits, lse, counts, dlosses, topk_ids, gates, dgates,
+                                           dlogits, stream)
+
+
+def moeblaze_layernorm_forward(shape, x, residual, weight, bias, eps, sum, y, mean, rstd, stream) -> int:
+    return lib().moeblaze_layernorm_forward(ctypes.byref(shape), x, residual, weight, bias, eps, sum, y, mean, rstd,
+                                            stream)
+
+
+def moeblaze_layernorm_backward_workspace_bytes(shape: Shape) -> int:
+    return lib().moeblaze_layernorm_backward_workspace_bytes(ctypes.byref(shape))
+
+
+def moeblaze_layernorm_backward(shape, dy, sum, mean, rstd, weight, dsum, dx, dweight, dbias, ws, ws_bytes,
+                                stream) -> int:
+    return lib().moeblaze_layernorm_backward(ctypes.byref(shape), dy, sum, mean, rstd, weight, dsum, dx, dweight,
+                                             dbias, ws, ws_bytes, stream)
+
+
+def moeblaze_int4_weight_bytes(E: int, R: int, N: int) -> int:
+    return lib().moeblaze_int4_weight_bytes(E, R, N)
+
+
+def moeblaze_int4_scale_bytes(E: int, R: int, N: int, group: int) -> int:
+    return lib().moeblaze_int4_scale_bytes(E, R, N, group)
+
+
+def moeblaze_int4_quantize(E, R, N, group, dtype, W, q, scales, stream) -> int:
+    return lib().moeblaze_int4_quantize(E, R, N, group, dtype, W, q, scales, stream)
+
+
+def moeblaze_int4_pack(E, R, N, group, q, scales, packed, packed_scales, stream) -> int:
+    return lib().moeblaze_int4_pack(E, R, N, group, q, scales, packed, packed_scales, stream)
+
+
+def moeblaze_int4_dequantize(E, R, N, group, packed, packed_scales, W, stream) -> int:
+    return lib().moeblaze_int4_dequantize(E, R, N, group, packed, packed_scales, W, stream)
+
+
+def moeblaze_int4_workspace_bytes(shape: Shape) -> int:
+    return lib().moeblaze_int4_workspace_bytes(ctypes.byref(shape))
+
+
+def moeblaze_int4_forward(shape, x, topk_ids, gates, weights, y, ws, ws_bytes, stream) -> int:
+    return lib().moeblaze_int4_forward(ctypes.byref(shape), x, topk_ids, gates, ctypes.byref(weights), y, ws, ws_bytes,
+                                       stream)
 
 
 def moeblaze_device_error(shape, disp, stream):
@@ -418,26 +526,35 @@ class StageEvents:
         return [self.events[i].elapsed_time(self.events[i + 1]) for i in range(len(self.events) - 1)]
 
 
-def router_forward(shape: Shape, x, Wr, bias, topk_ids, gates, stream=None):
-    """Token-choice top-K softmax router: fills topk_ids (L,K) int32 and gates (L,K) fp32."""
+def router_forward(shape: Shape, x, Wr, bias, topk_ids, gates, stream=None, logits=None):
+    """Token-choice top-K softmax router: fills topk_ids (L,K) int32 and gates (L,K) fp32, and the logits
+    (L,E) fp32 when a tensor for them is given."""
     _args((x, "x", (shape.L, shape.d), _TORCH_DTYPE[shape.dtype], False),
           (Wr, "Wr", (shape.d, shape.E), torch.float32, False), (bias, "bias", (shape.E,), torch.float32, True),
           (topk_ids, "topk_ids", (shape.L, shape.K), torch.int32, False),
-          (gates, "gates", (shape.L, shape.K), torch.float32, False))
+          (gates, "gates", (shape.L, shape.K), torch.float32, False),
+          (logits, "logits", (shape.L, shape.E), torch.float32, True))
+    if logits is not None:
+        st = moeblaze_router_forward_logits(shape, _ptr(x), _ptr(Wr), _ptr(bias), _ptr(topk_ids), _ptr(gates),
+                                            _ptr(logits), _stream(stream))
+        _check(st, "moeblaze_router_forward_logits")
+        return
     st = moeblaze_router_forward(shape, _ptr(x), _ptr(Wr), _ptr(bias), _ptr(topk_ids), _ptr(gates), _stream(stream))
     _check(st, "moeblaze_router_forward")
 
 
 def router_dispatch_build(shape: Shape, x, Wr, bias, topk_ids, gates, bufs: Optional["DispatchBuffers"] = None,
-                          ws=None, stream=None) -> "DispatchBuffers":
+                          ws=None, stream=None, logits=None) -> "DispatchBuffers":
     """The router fused with the dispatch build's first step: fills topk_ids
-    (L,K) int32, gates (L,K) fp32 and the dispatch buffers in one call.  `ws`
+    (L,K) int32, gates (L,K) fp32, the dispatch buffers and, when a tensor is
+    given for them, the logits (L,E) fp32 in one call.  `ws`
     is a device byte tensor of moeblaze_router_dispatch_workspace_bytes(shape)
     bytes (allocated here when None)."""
     _args((x, "x", (shape.L, shape.d), _TORCH_DTYPE[shape.dtype], False),
           (Wr, "Wr", (shape.d, shape.E), torch.float32, False), (bias, "bias", (shape.E,), torch.float32, True),
           (topk_ids, "topk_ids", (shape.L, shape.K), torch.int32, False),
-          (gates, "gates", (shape.L, shape.K), torch.float32, False))
+          (gates, "gates", (shape.L, shape.K), torch.float32, False),
+          (logits, "logits", (shape.L, shape.E), torch.float32, True))
     if bufs is None:
         bufs = alloc_dispatch(shape, Wr.device)
     _check_dispatch_bufs(shape, bufs)
@@ -447,6 +564,11 @@ def router_dispatch_build(shape: Shape, x, Wr, bias, topk_ids, gates, bufs: Opti
     if ws is None:
         ws = _bytes(n, Wr.device)
     _bytes_arg(ws, "ws", n)
+    if logits is not None:
+        st = moeblaze_router_dispatch_build_logits(shape, _ptr(x), _ptr(Wr), _ptr(bias), _ptr(topk_ids), _ptr(gates),
+                                                   _ptr(logits), bufs.struct(), _ptr(ws), n, _stream(stream))
+        _check(st, "moeblaze_router_dispatch_build_logits")
+        return bufs
     st = moeblaze_router_dispatch_build(shape, _ptr(x), _ptr(Wr), _ptr(bias), _ptr(topk_ids), _ptr(gates),
                                         bufs.struct(), _ptr(ws), n, _stream(stream))
     _check(st, "moeblaze_router_dispatch_build")
@@ -472,6 +594,145 @@ def router_backward(shape: Shape, x, Wr, topk_ids, gates, dgates, dWr, dbias, dx
     st = moeblaze_router_backward(shape, _ptr(x), _ptr(Wr), _ptr(topk_ids), _ptr(gates), _ptr(dgates), _ptr(dWr),
                                   _ptr(dbias), _ptr(dx), _ptr(ws), n, _stream(stream))
     _check(st, "moeblaze_router_backward")
+
+
+def router_backward_logits(shape: Shape, x, Wr, dlogits, dWr, dbias, dx, ws=None, stream=None):
+    """Router gradients from a dense gradient of its logits: fills dWr (d,E) fp32, dbias (E) fp32 and dx (L,d)
+    (dbias and dx may be None).  `ws` is a device byte tensor of
+    moeblaze_router_backward_logits_workspace_bytes(shape) bytes (allocated here when None)."""
+    dt = _TORCH_DTYPE[shape.dtype]
+    _args((x, "x", (shape.L, shape.d), dt, False), (Wr, "Wr", (shape.d, shape.E), torch.float32, False),
+          (dlogits, "dlogits", (shape.L, shape.E), torch.float32, False),
+          (dWr, "dWr", (shape.d, shape.E), torch.float32, False), (dbias, "dbias", (shape.E,), torch.float32, True),
+          (dx, "dx", (shape.L, shape.d), dt, True))
+    n = moeblaze_router_backward_logits_workspace_bytes(shape)
+    if ws is None:
+        ws = _bytes(n, Wr.device)
+    _bytes_arg(ws, "ws", n)
+    st = moeblaze_router_backward_logits(shape, _ptr(x), _ptr(Wr), _ptr(dlogits), _ptr(dWr), _ptr(dbias), _ptr(dx),
+                                         _ptr(ws), n, _stream(stream))
+    _check(st, "moeblaze_router_backward_logits")
+
+
+def balance_forward(shape: Shape, logits, topk_ids, valid, losses, counts, lse, ws, stream=None):
+    """Load-balance and z loss of a router's logits: fills losses (2) fp32, counts (E+1) int32 (the last one the
+    active tokens) and lse (L) fp32.  valid: (L) uint8 or None."""
+    L, E = shape.L, shape.E
+    _args((logits, "logits", (L, E), torch.float32, False), (topk_ids, "topk_ids", (L, shape.K), torch.int32, False),
+          (valid, "valid", (L,), torch.uint8, True), (losses, "losses", (2,), torch.float32, False),
+          (counts, "counts", (E + 1,), torch.int32, False), (lse, "lse", (L,), torch.float32, False))
+    n = moeblaze_balance_workspace_bytes(shape)
+    _bytes_arg(ws, "ws", n)
+    st = moeblaze_balance_forward(shape, _ptr(logits), _ptr(topk_ids), _ptr(valid), _ptr(losses), _ptr(counts),
+                                  _ptr(lse), _ptr(ws), n, _stream(stream))
+    _check(st, "moeblaze_balance_forward")
+
+
+def balance_backward(shape: Shape, logits, lse, counts, dlosses, topk_ids, gates, dgates, dlogits, stream=None):
+    """Gradient of the logits (L,E) fp32 from the gradients of the two losses and, when topk_ids, gates and dgates
+    are given (all or none), of the gates."""
+    L, E, K = shape.L, shape.E, shape.K
+    _args((logits, "logits", (L, E), torch.float32, False), (lse, "lse", (L,), torch.float32, False),
+          (counts, "counts", (E + 1,), torch.int32, False), (dlosses, "dlosses", (2,), torch.float32, False),
+          (topk_ids, "topk_ids", (L, K), torch.int32, True), (gates, "gates", (L, K), torch.float32, True),
+          (dgates, "dgates", (L, K), torch.float32, True), (dlogits, "dlogits", (L, E), torch.float32, False))
+    if L > 0 and len({topk_ids is None, gates is None, dgates is None}) != 1:
+        raise ValueError("topk_ids, gates and dgates: give all three or none")
+    st = moeblaze_balance_backward(shape, _ptr(logits), _ptr(lse), _ptr(counts), _ptr(dlosses), _ptr(topk_ids),
+                                   _ptr(gates), _ptr(dgates), _ptr(dlogits), _stream(stream))
+    _check(st, "moeblaze_balance_backward")
+
+
+def layernorm_forward(shape: Shape, x, residual, weight, bias, eps, sum, y, mean, rstd, stream=None):
+    """Layer norm of x (+ residual): fills y (L,d), mean and rstd (L) fp32 and, unless None, sum (L,d)."""
+    dt, L, d = _TORCH_DTYPE[shape.dtype], shape.L, shape.d
+    _args((x, "x", (L, d), dt, False), (residual, "residual", (L, d), dt, True),
+          (weight, "weight", (d,), torch.float32, False), (bias, "bias", (d,), torch.float32, True),
+          (sum, "sum", (L, d), dt, True), (y, "y", (L, d), dt, False), (mean, "mean", (L,), torch.float32, False),
+          (rstd, "rstd", (L,), torch.float32, False))
+    st = moeblaze_layernorm_forward(shape, _ptr(x), _ptr(residual), _ptr(weight), _ptr(bias), eps, _ptr(sum), _ptr(y),
+                                    _ptr(mean), _ptr(rstd), _stream(stream))
+    _check(st, "moeblaze_layernorm_forward")
+
+
+def layernorm_backward(shape: Shape, dy, sum, mean, rstd, weight, dsum, dx, dweight, dbias, ws, stream=None):
+    """Layer norm backward: fills dx (L,d), dweight (d) fp32 and, unless None, dbias (d) fp32."""
+    dt, L, d = _TORCH_DTYPE[shape.dtype], shape.L, shape.d
+    _args((dy, "dy", (L, d), dt, False), (sum, "sum", (L, d), dt, False), (mean, "mean", (L,), torch.float32, False),
+          (rstd, "rstd", (L,), torch.float32, False), (weight, "weight", (d,), torch.float32, False),
+          (dsum, "dsum", (L, d), dt, True), (dx, "dx", (L, d), dt, False),
+          (dweight, "dweight", (d,), torch.float32, False), (dbias, "dbias", (d,), torch.float32, True))
+    n = moeblaze_layernorm_backward_workspace_bytes(shape)
+    _bytes_arg(ws, "ws", n)
+    st = moeblaze_layernorm_backward(shape, _ptr(dy), _ptr(sum), _ptr(mean), _ptr(rstd), _ptr(weight), _ptr(dsum),
+                                     _ptr(dx), _ptr(dweight), _ptr(dbias), _ptr(ws), n, _stream(stream))
+    _check(st, "moeblaze_layernorm_backward")
+
+
+def _int4_matrix(E: int, R: int, N: int, group: int, where: str):
+    """Sizes of a packed matrix and its scales; raises for a matrix the library does not take."""
+    wb, sb = moeblaze_int4_weight_bytes(E, R, N), moeblaze_int4_scale_bytes(E, R, N, group)
+    if wb == 0 or sb == 0:
+        raise MoEBlazeError(ERR_UNSUPPORTED, where)
+    return wb, sb
+
+
+def int4_quantize(W, group: int, stream=None):
+    """4-bit values and group scales of W (E,R,N): returns q (E,R,N) int8 in -8..7 and scales (E,R/group,N) bf16."""
+    if not isinstance(W, torch.Tensor) or W.dim() != 3:
+        raise ValueError("W: expected a tensor of shape (E, R, N)")
+    E, R, N = W.shape
+    if W.dtype not in DTYPE:
+        raise ValueError(f"W: dtype {W.dtype}, expected float32 or bfloat16")
+    _int4_matrix(E, R, N, group, "moeblaze_int4_quantize")
+    _args((W, "W", (E, R, N), W.dtype, False))
+    q = torch.empty((E, R, N), dtype=torch.int8, device=W.device)
+    s = torch.empty((E, R // group, N), dtype=torch.bfloat16, device=W.device)
+    st = moeblaze_int4_quantize(E, R, N, group, DTYPE[W.dtype], _ptr(W), _ptr(q), _ptr(s), _stream(stream))
+    _check(st, "moeblaze_int4_quantize")
+    return q, s
+
+
+def int4_pack(q, scales, group: int, packed=None, packed_scales=None, stream=None):
+    """The layout the 4-bit products read, from q (E,R,N) int8 and scales (E,R/group,N) bf16: two byte tensors."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q: expected a tensor of shape (E, R, N)")
+    E, R, N = q.shape
+    wb, sb = _int4_matrix(E, R, N, group, "moeblaze_int4_pack")
+    _args((q, "q", (E, R, N), torch.int8, False), (scales, "scales", (E, R // group, N), torch.bfloat16, False))
+    packed = _bytes(wb, q.device) if packed is None else packed
+    packed_scales = _bytes(sb, q.device) if packed_scales is None else packed_scales
+    _bytes_arg(packed, "packed", wb)
+    _bytes_arg(packed_scales, "packed_scales", sb)
+    st = moeblaze_int4_pack(E, R, N, group, _ptr(q), _ptr(scales), _ptr(packed), _ptr(packed_scales), _stream(stream))
+    _check(st, "moeblaze_int4_pack")
+    return packed, packed_scales
+
+
+def int4_dequantize(packed, packed_scales, E: int, R: int, N: int, group: int, stream=None):
+    """The bf16 weights (E,R,N) a packed matrix stands for."""
+    wb, sb = _int4_matrix(E, R, N, group, "moeblaze_int4_dequantize")
+    _bytes_arg(packed, "packed", wb)
+    _bytes_arg(packed_scales, "packed_scales", sb)
+    W = torch.empty((E, R, N), dtype=torch.bfloat16, device=packed.device)
+    st = moeblaze_int4_dequantize(E, R, N, group, _ptr(packed), _ptr(packed_scales), _ptr(W), _stream(stream))
+    _check(st, "moeblaze_int4_dequantize")
+    return W
+
+
+def int4_forward(shape: Shape, x, topk_ids, gates, weights: Int4Weights, y, ws, stream=None):
+    """The layer's forward on packed 4-bit weights: fills y (L,d) bf16.  `weights` holds device pointers that the
+    caller keeps alive (see int4.Int4Experts)."""
+    dt = _TORCH_DTYPE[shape.dtype]
+    _args((x, "x", (shape.L, shape.d), dt, False), (topk_ids, "topk_ids", (shape.L, shape.K), torch.int32, False),
+          (gates, "gates", (shape.L, shape.K), torch.float32, False), (y, "y", (shape.L, shape.d), dt, False))
+    if not isinstance(ws, torch.Tensor) or not ws.is_contiguous():
+        raise ValueError("ws: expected a contiguous tensor")
+    _on_device((ws, "ws"))
+    st = moeblaze_int4_forward(shape, _ptr(x), _ptr(topk_ids), _ptr(gates), weights, _ptr(y), _ptr(ws), ws.numel(),
+                               _stream(stream))
+    _check(st, "moeblaze_int4_forward")
+    return y
 
 
 def device_error(shape: Shape, disp: DispatchBuffers, stream=None) -> int:

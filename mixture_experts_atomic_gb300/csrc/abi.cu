@@ -1,7 +1,7 @@
 // extern "C" entry points of the moeblaze library (declared in
 // include/moeblaze.h): argument validation, scratch carving and the order of
 // the stages; every stage runs in the kernels of dispatch.cu, identity.cu,
-// simt.cu, gemm_tc.cu and router.cu.
+// simt.cu, gemm_tc.cu, router.cu, router_tc.cu, norm.cu, balance.cu and int4.cu.
 #include <atomic>
 #include <cstring>
 
@@ -85,6 +85,36 @@ moeblaze_status check_router_shape(const moeblaze_shape* s) {
   if (s->dtype != MOEBLAZE_F32 && s->dtype != MOEBLAZE_BF16) return MOEBLAZE_ERR_INVALID_ARG;
   if (s->E > kMaxRouterE || s->K > kMaxK || s->d % 64 != 0) return MOEBLAZE_ERR_UNSUPPORTED;
   if (s->L * (int64_t)s->K >= (int64_t(1) << 31)) return MOEBLAZE_ERR_UNSUPPORTED;
+  return MOEBLAZE_OK;
+}
+
+// shape checks of the layer norm (fields L, d, dtype)
+moeblaze_status check_norm_shape(const moeblaze_shape* s) {
+  if (!s || s->L < 0 || s->d < 1) return MOEBLAZE_ERR_INVALID_ARG;
+  if (s->dtype != MOEBLAZE_F32 && s->dtype != MOEBLAZE_BF16) return MOEBLAZE_ERR_INVALID_ARG;
+  if (s->L >= (int64_t(1) << 31) || s->d > (1 << 24)) return MOEBLAZE_ERR_UNSUPPORTED;
+  return MOEBLAZE_OK;
+}
+
+// shape checks of the router losses (fields L, E, K)
+moeblaze_status check_balance_shape(const moeblaze_shape* s) {
+  if (!s || s->L < 0 || s->E < 1 || s->K < 1 || s->K > s->E) return MOEBLAZE_ERR_INVALID_ARG;
+  if (s->E > kMaxE || s->K > kMaxK || s->L * (int64_t)s->K >= (int64_t(1) << 31)) return MOEBLAZE_ERR_UNSUPPORTED;
+  return MOEBLAZE_OK;
+}
+
+// checks of one 4-bit matrix (E,R,N) and of the layer on such matrices
+moeblaze_status check_int4_matrix(int E, int R, int N, int group) {
+  if (E < 1 || R < 1 || N < 1) return MOEBLAZE_ERR_INVALID_ARG;
+  if (group != 32 && group != 64 && group != 128) return MOEBLAZE_ERR_INVALID_ARG;
+  if (E > kMaxE || R % 128 != 0 || N % 128 != 0) return MOEBLAZE_ERR_UNSUPPORTED;
+  return MOEBLAZE_OK;
+}
+moeblaze_status check_int4_shape(const moeblaze_shape* s, int group) {
+  const moeblaze_status r = check_shape(s);
+  if (r != MOEBLAZE_OK) return r;
+  if (group != 32 && group != 64 && group != 128) return MOEBLAZE_ERR_INVALID_ARG;
+  if (s->act == MOEBLAZE_IDENTITY || s->dtype != MOEBLAZE_BF16 || !int4_shape_ok(*s)) return MOEBLAZE_ERR_UNSUPPORTED;
   return MOEBLAZE_OK;
 }
 
@@ -327,7 +357,7 @@ moeblaze_status moeblaze_router_forward(const moeblaze_shape* s, const void* x, 
   if (r != MOEBLAZE_OK) return r;
   if (!ok_ptr4(Wr) || (bias && !ok_ptr4(bias))) return MOEBLAZE_ERR_INVALID_ARG;
   if (s->L > 0 && (!ok_ptr(x) || !ok_ptr4(topk_ids) || !ok_ptr4(gates))) return MOEBLAZE_ERR_INVALID_ARG;
-  return launch_router_forward(*s, x, Wr, bias, topk_ids, gates, reinterpret_cast<cudaStream_t>(stream));
+  return launch_router_forward(*s, x, Wr, bias, topk_ids, gates, nullptr, reinterpret_cast<cudaStream_t>(stream));
 }
 
 size_t moeblaze_router_dispatch_workspace_bytes(const moeblaze_shape* s) {
@@ -335,10 +365,9 @@ size_t moeblaze_router_dispatch_workspace_bytes(const moeblaze_shape* s) {
   return router_dispatch_fused(*s) ? router_dispatch_ws_bytes(*s) : dispatch_ws_bytes(*s);
 }
 
-moeblaze_status moeblaze_router_dispatch_build(const moeblaze_shape* s, const void* x, const float* Wr,
-                                               const float* bias, int32_t* topk_ids, float* gates,
-                                               const moeblaze_dispatch* out, void* ws, size_t ws_bytes,
-                                               moeblaze_stream stream) {
+static moeblaze_status router_dispatch(const moeblaze_shape* s, const void* x, const float* Wr, const float* bias,
+                                       int32_t* topk_ids, float* gates, float* logits, const moeblaze_dispatch* out,
+                                       void* ws, size_t ws_bytes, moeblaze_stream stream) {
   moeblaze_status r = check_shape(s);
   if (r != MOEBLAZE_OK) return r;
   if ((r = check_router_shape(s)) != MOEBLAZE_OK) return r;
@@ -348,11 +377,37 @@ moeblaze_status moeblaze_router_dispatch_build(const moeblaze_shape* s, const vo
   if (ws_bytes < moeblaze_router_dispatch_workspace_bytes(s)) return MOEBLAZE_ERR_WORKSPACE;
   if (!ok_ptr(ws)) return MOEBLAZE_ERR_INVALID_ARG;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  if (router_dispatch_fused(*s)) return launch_router_dispatch(*s, x, Wr, bias, topk_ids, gates, *out, ws, st);
+  if (router_dispatch_fused(*s)) return launch_router_dispatch(*s, x, Wr, bias, topk_ids, gates, logits, *out, ws, st);
   // shapes the fused kernel does not take (fp32 x, more than 64 experts, no
   // tokens): the router, then the dispatch build on its ids
-  if (s->L > 0 && (r = launch_router_forward(*s, x, Wr, bias, topk_ids, gates, st)) != MOEBLAZE_OK) return r;
+  if (s->L > 0 && (r = launch_router_forward(*s, x, Wr, bias, topk_ids, gates, logits, st)) != MOEBLAZE_OK) return r;
   return launch_dispatch(*s, topk_ids, *out, ws, st);
+}
+
+moeblaze_status moeblaze_router_dispatch_build(const moeblaze_shape* s, const void* x, const float* Wr,
+                                               const float* bias, int32_t* topk_ids, float* gates,
+                                               const moeblaze_dispatch* out, void* ws, size_t ws_bytes,
+                                               moeblaze_stream stream) {
+  return router_dispatch(s, x, Wr, bias, topk_ids, gates, nullptr, out, ws, ws_bytes, stream);
+}
+
+moeblaze_status moeblaze_router_dispatch_build_logits(const moeblaze_shape* s, const void* x, const float* Wr,
+                                                      const float* bias, int32_t* topk_ids, float* gates,
+                                                      float* logits, const moeblaze_dispatch* out, void* ws,
+                                                      size_t ws_bytes, moeblaze_stream stream) {
+  if (s && s->L > 0 && !ok_ptr(logits)) return MOEBLAZE_ERR_INVALID_ARG;
+  return router_dispatch(s, x, Wr, bias, topk_ids, gates, logits, out, ws, ws_bytes, stream);
+}
+
+moeblaze_status moeblaze_router_forward_logits(const moeblaze_shape* s, const void* x, const float* Wr,
+                                               const float* bias, int32_t* topk_ids, float* gates, float* logits,
+                                               moeblaze_stream stream) {
+  moeblaze_status r = check_router_shape(s);
+  if (r != MOEBLAZE_OK) return r;
+  if (!ok_ptr4(Wr) || (bias && !ok_ptr4(bias))) return MOEBLAZE_ERR_INVALID_ARG;
+  if (s->L > 0 && (!ok_ptr(x) || !ok_ptr4(topk_ids) || !ok_ptr4(gates) || !ok_ptr(logits)))
+    return MOEBLAZE_ERR_INVALID_ARG;
+  return launch_router_forward(*s, x, Wr, bias, topk_ids, gates, logits, reinterpret_cast<cudaStream_t>(stream));
 }
 
 moeblaze_status moeblaze_router_backward(const moeblaze_shape* s, const void* x, const float* Wr,
@@ -368,6 +423,143 @@ moeblaze_status moeblaze_router_backward(const moeblaze_shape* s, const void* x,
   if (s->L > 0 && !ok_ptr(ws)) return MOEBLAZE_ERR_INVALID_ARG;
   return launch_router_backward(*s, x, Wr, topk_ids, gates, dgates, dWr, dbias, dx, ws,
                                 reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t moeblaze_router_backward_logits_workspace_bytes(const moeblaze_shape* s) {
+  if (check_router_shape(s) != MOEBLAZE_OK) return 0;
+  return router_dense_ws_bytes(*s);
+}
+
+moeblaze_status moeblaze_router_backward_logits(const moeblaze_shape* s, const void* x, const float* Wr,
+                                                const float* dlogits, float* dWr, float* dbias, void* dx, void* ws,
+                                                size_t ws_bytes, moeblaze_stream stream) {
+  moeblaze_status r = check_router_shape(s);
+  if (r != MOEBLAZE_OK) return r;
+  if (!ok_ptr4(Wr) || !ok_ptr4(dWr) || (dbias && !ok_ptr4(dbias))) return MOEBLAZE_ERR_INVALID_ARG;
+  if (s->L > 0 && (!ok_ptr(x) || !ok_ptr(dlogits) || (dx && !ok_ptr(dx)))) return MOEBLAZE_ERR_INVALID_ARG;
+  if (ws_bytes < router_dense_ws_bytes(*s)) return MOEBLAZE_ERR_WORKSPACE;
+  if (s->L > 0 && !ok_ptr(ws)) return MOEBLAZE_ERR_INVALID_ARG;
+  return launch_router_dense(*s, x, Wr, dlogits, dWr, dbias, dx, ws, reinterpret_cast<cudaStream_t>(stream));
+}
+
+moeblaze_status moeblaze_layernorm_forward(const moeblaze_shape* s, const void* x, const void* residual,
+                                           const float* weight, const float* bias, float eps, void* sum, void* y,
+                                           float* mean, float* rstd, moeblaze_stream stream) {
+  moeblaze_status r = check_norm_shape(s);
+  if (r != MOEBLAZE_OK) return r;
+  if (!(eps >= 0.f) || !ok_ptr(weight) || (bias && !ok_ptr(bias))) return MOEBLAZE_ERR_INVALID_ARG;
+  if (s->L > 0 && (!ok_ptr(x) || !ok_ptr(y) || !ok_ptr4(mean) || !ok_ptr4(rstd) || (residual && !ok_ptr(residual)) ||
+                   (sum && !ok_ptr(sum))))
+    return MOEBLAZE_ERR_INVALID_ARG;
+  return launch_layernorm_forward(*s, x, residual, weight, bias, eps, sum, y, mean, rstd,
+                                  reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t moeblaze_layernorm_backward_workspace_bytes(const moeblaze_shape* s) {
+  if (check_norm_shape(s) != MOEBLAZE_OK) return 0;
+  return norm_ws_bytes(*s);
+}
+
+moeblaze_status moeblaze_layernorm_backward(const moeblaze_shape* s, const void* dy, const void* sum, const float* mean,
+                                            const float* rstd, const float* weight, const void* dsum, void* dx,
+                                            float* dweight, float* dbias, void* ws, size_t ws_bytes,
+                                            moeblaze_stream stream) {
+  moeblaze_status r = check_norm_shape(s);
+  if (r != MOEBLAZE_OK) return r;
+  if (!ok_ptr(weight) || !ok_ptr4(dweight) || (dbias && !ok_ptr4(dbias))) return MOEBLAZE_ERR_INVALID_ARG;
+  if (s->L > 0 && (!ok_ptr(dy) || !ok_ptr(sum) || !ok_ptr(dx) || !ok_ptr4(mean) || !ok_ptr4(rstd) ||
+                   (dsum && !ok_ptr(dsum))))
+    return MOEBLAZE_ERR_INVALID_ARG;
+  if (ws_bytes < norm_ws_bytes(*s)) return MOEBLAZE_ERR_WORKSPACE;
+  if (s->L > 0 && !ok_ptr(ws)) return MOEBLAZE_ERR_INVALID_ARG;
+  return launch_layernorm_backward(*s, dy, sum, mean, rstd, weight, dsum, dx, dweight, dbias, ws,
+                                   reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t moeblaze_balance_workspace_bytes(const moeblaze_shape* s) {
+  if (check_balance_shape(s) != MOEBLAZE_OK) return 0;
+  return balance_ws_bytes(*s);
+}
+
+moeblaze_status moeblaze_balance_forward(const moeblaze_shape* s, const float* logits, const int32_t* topk_ids,
+                                         const uint8_t* valid, float* losses, int32_t* counts, float* lse, void* ws,
+                                         size_t ws_bytes, moeblaze_stream stream) {
+  moeblaze_status r = check_balance_shape(s);
+  if (r != MOEBLAZE_OK) return r;
+  if (!ok_ptr4(losses) || !ok_ptr4(counts)) return MOEBLAZE_ERR_INVALID_ARG;
+  if (s->L > 0 && (!ok_ptr(logits) || !ok_ptr4(topk_ids) || !ok_ptr4(lse))) return MOEBLAZE_ERR_INVALID_ARG;
+  if (ws_bytes < balance_ws_bytes(*s)) return MOEBLAZE_ERR_WORKSPACE;
+  if (!ok_ptr(ws)) return MOEBLAZE_ERR_INVALID_ARG;
+  return launch_balance_forward(*s, logits, topk_ids, valid, losses, counts, lse, ws,
+                                reinterpret_cast<cudaStream_t>(stream));
+}
+
+moeblaze_status moeblaze_balance_backward(const moeblaze_shape* s, const float* logits, const float* lse,
+                                          const int32_t* counts, const float* dlosses, const int32_t* topk_ids,
+                                          const float* gates, const float* dgates, float* dlogits,
+                                          moeblaze_stream stream) {
+  moeblaze_status r = check_balance_shape(s);
+  if (r != MOEBLAZE_OK) return r;
+  if (!ok_ptr4(counts) || !ok_ptr4(dlosses)) return MOEBLAZE_ERR_INVALID_ARG;
+  // the gates' part: all three arguments or none
+  if ((gates != nullptr) != (dgates != nullptr) || (gates != nullptr) != (topk_ids != nullptr))
+    return MOEBLAZE_ERR_INVALID_ARG;
+  if (s->L > 0 && (!ok_ptr(logits) || !ok_ptr4(lse) || !ok_ptr(dlogits))) return MOEBLAZE_ERR_INVALID_ARG;
+  if (gates && (!ok_ptr4(gates) || !ok_ptr4(dgates) || !ok_ptr4(topk_ids))) return MOEBLAZE_ERR_INVALID_ARG;
+  return launch_balance_backward(*s, logits, lse, counts, dlosses, topk_ids, gates, dgates, dlogits,
+                                 reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t moeblaze_int4_weight_bytes(int32_t E, int32_t R, int32_t N) {
+  return check_int4_matrix(E, R, N, 128) == MOEBLAZE_OK ? (size_t)E * R * N / 2 : 0;
+}
+
+size_t moeblaze_int4_scale_bytes(int32_t E, int32_t R, int32_t N, int32_t group) {
+  return check_int4_matrix(E, R, N, group) == MOEBLAZE_OK ? (size_t)E * (R / group) * N * 2 : 0;
+}
+
+moeblaze_status moeblaze_int4_quantize(int32_t E, int32_t R, int32_t N, int32_t group, int32_t dtype, const void* W,
+                                       int8_t* q, void* scales, moeblaze_stream stream) {
+  const moeblaze_status r = check_int4_matrix(E, R, N, group);
+  if (r != MOEBLAZE_OK) return r;
+  if ((dtype != MOEBLAZE_F32 && dtype != MOEBLAZE_BF16) || !ok_ptr(W) || !ok_ptr(q) || !ok_ptr(scales))
+    return MOEBLAZE_ERR_INVALID_ARG;
+  return launch_int4_quantize(E, R, N, group, dtype, W, q, scales, reinterpret_cast<cudaStream_t>(stream));
+}
+
+moeblaze_status moeblaze_int4_pack(int32_t E, int32_t R, int32_t N, int32_t group, const int8_t* q, const void* scales,
+                                   void* packed, void* packed_scales, moeblaze_stream stream) {
+  const moeblaze_status r = check_int4_matrix(E, R, N, group);
+  if (r != MOEBLAZE_OK) return r;
+  if (!ok_ptr(q) || !ok_ptr(scales) || !ok_ptr(packed) || !ok_ptr(packed_scales)) return MOEBLAZE_ERR_INVALID_ARG;
+  return launch_int4_pack(E, R, N, group, q, scales, packed, packed_scales, reinterpret_cast<cudaStream_t>(stream));
+}
+
+moeblaze_status moeblaze_int4_dequantize(int32_t E, int32_t R, int32_t N, int32_t group, const void* packed,
+                                         const void* packed_scales, void* W, moeblaze_stream stream) {
+  const moeblaze_status r = check_int4_matrix(E, R, N, group);
+  if (r != MOEBLAZE_OK) return r;
+  if (!ok_ptr(packed) || !ok_ptr(packed_scales) || !ok_ptr(W)) return MOEBLAZE_ERR_INVALID_ARG;
+  return launch_int4_dequantize(E, R, N, group, packed, packed_scales, W, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t moeblaze_int4_workspace_bytes(const moeblaze_shape* s) {
+  return check_int4_shape(s, 128) == MOEBLAZE_OK ? int4_ws_bytes(*s) : 0;
+}
+
+moeblaze_status moeblaze_int4_forward(const moeblaze_shape* s, const void* x, const int32_t* topk_ids,
+                                      const float* gates, const moeblaze_int4_experts* w, void* y, void* ws,
+                                      size_t ws_bytes, moeblaze_stream stream) {
+  if (!w) return MOEBLAZE_ERR_INVALID_ARG;
+  const moeblaze_status r = check_int4_shape(s, w->group);
+  if (r != MOEBLAZE_OK) return r;
+  if (!ok_ptr(w->w1) || !ok_ptr(w->s1) || !ok_ptr(w->w3) || !ok_ptr(w->s3)) return MOEBLAZE_ERR_INVALID_ARG;
+  if (s->act == MOEBLAZE_SWIGLU && (!ok_ptr(w->w2) || !ok_ptr(w->s2))) return MOEBLAZE_ERR_INVALID_ARG;
+  if (s->L > 0 && (!ok_ptr(x) || !ok_ptr(y) || !ok_ptr4(topk_ids) || !ok_ptr4(gates))) return MOEBLAZE_ERR_INVALID_ARG;
+  if (ws_bytes < int4_ws_bytes(*s)) return MOEBLAZE_ERR_WORKSPACE;
+  if (s->L > 0 && !ok_ptr(ws)) return MOEBLAZE_ERR_INVALID_ARG;
+  return launch_int4_forward(*s, (const __nv_bfloat16*)x, topk_ids, gates, *w, (__nv_bfloat16*)y, ws,
+                             reinterpret_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -135,17 +135,52 @@ moeblaze_status tc_backward(const moeblaze_shape& s, const __nv_bfloat16* dY, co
 constexpr int kMaxRouterE = 256;
 size_t router_ws_bytes(const moeblaze_shape& s);
 moeblaze_status launch_router_forward(const moeblaze_shape& s, const void* x, const float* Wr, const float* bias,
-                                      int32_t* ids, float* gates, cudaStream_t st);
+                                      int32_t* ids, float* gates, float* logits, cudaStream_t st);
 moeblaze_status launch_router_backward(const moeblaze_shape& s, const void* x, const float* Wr, const int32_t* ids,
                                        const float* gates, const float* dgates, float* dWr, float* dbias, void* dx,
                                        void* ws, cudaStream_t st);
+// the router's gradients from a dense gradient of the logits
+size_t router_dense_ws_bytes(const moeblaze_shape& s);
+moeblaze_status launch_router_dense(const moeblaze_shape& s, const void* x, const float* Wr, const float* dl, float* dWr,
+                                    float* dbias, void* dx, void* ws, cudaStream_t st);
+
+// norm.cu
+size_t norm_ws_bytes(const moeblaze_shape& s);
+moeblaze_status launch_layernorm_forward(const moeblaze_shape& s, const void* x, const void* res, const float* w,
+                                         const float* b, float eps, void* sum, void* y, float* mean, float* rstd,
+                                         cudaStream_t st);
+moeblaze_status launch_layernorm_backward(const moeblaze_shape& s, const void* dy, const void* sum, const float* mean,
+                                          const float* rstd, const float* w, const void* dsum, void* dx, float* dw,
+                                          float* db, void* ws, cudaStream_t st);
+
+// balance.cu
+size_t balance_ws_bytes(const moeblaze_shape& s);
+moeblaze_status launch_balance_forward(const moeblaze_shape& s, const float* logits, const int32_t* ids,
+                                       const uint8_t* valid, float* losses, int32_t* counts, float* lse, void* ws,
+                                       cudaStream_t st);
+moeblaze_status launch_balance_backward(const moeblaze_shape& s, const float* logits, const float* lse,
+                                        const int32_t* counts, const float* dloss, const int32_t* ids,
+                                        const float* gates, const float* dgates, float* dlogits, cudaStream_t st);
+
+// int4.cu
+bool int4_shape_ok(const moeblaze_shape& s);  // a token row fits the products' shared memory
+size_t int4_ws_bytes(const moeblaze_shape& s);
+moeblaze_status launch_int4_forward(const moeblaze_shape& s, const __nv_bfloat16* x, const int32_t* ids,
+                                    const float* gates, const moeblaze_int4_experts& w, __nv_bfloat16* y, void* ws,
+                                    cudaStream_t st);
+moeblaze_status launch_int4_quantize(int E, int R, int N, int group, int dtype, const void* W, int8_t* q, void* scales,
+                                     cudaStream_t st);
+moeblaze_status launch_int4_pack(int E, int R, int N, int group, const int8_t* q, const void* scales, void* packed,
+                                 void* packed_scales, cudaStream_t st);
+moeblaze_status launch_int4_dequantize(int E, int R, int N, int group, const void* packed, const void* packed_scales,
+                                       void* W, cudaStream_t st);
 
 // router_tc.cu: the router fused with the dispatch's first step (bf16 x, E <= 64)
 bool router_dispatch_fused(const moeblaze_shape& s);
 size_t router_dispatch_ws_bytes(const moeblaze_shape& s);
 moeblaze_status launch_router_dispatch(const moeblaze_shape& s, const void* x, const float* Wr, const float* bias,
-                                       int32_t* ids, float* gates, const moeblaze_dispatch& out, void* ws,
-                                       cudaStream_t st);
+                                       int32_t* ids, float* gates, float* logits, const moeblaze_dispatch& out,
+                                       void* ws, cudaStream_t st);
 
 // shared helpers (abi.cu)
 int sm_count();

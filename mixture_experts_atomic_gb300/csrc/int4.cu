@@ -1,0 +1,573 @@
+// Expert products on 4-bit weights with group scales, for few tokens (the
+// serving form of the layer): every used expert's weights are read once.
+//
+//   w[r][n] = q[r][n] s[r / group][n],  q in -8..7, s bf16
+//   h[t,k]  = SiLU(x[t] W1_e) (* x[t] W2_e),  e = ids[t,k]
+//   y[t]    = sum_k g[t,k] h[t,k] W3_e        (ids outside [0,E): empty slots)
+//
+// Bound by the HBM reads of the weights (0.5 + 2/group bytes each).  The
+// products run on mma.sync m16n8k16 (bf16, fp32 accumulate): 16 output
+// columns of the weights are the M rows, up to 8 tokens the N columns, so a
+// weight is converted once for 8 tokens, in registers.  tcgen05 takes its
+// operands from shared memory or TMEM: the converted weights would make a
+// round trip of four times their packed size there for a product whose N is
+// a handful of tokens.
+//
+// Packed layout of a matrix (E,R,N): tiles of 16 columns n, chunks of 64
+// reduction rows r; a chunk is 512 bytes, 16 per lane, one 32-bit word per
+// k16 step of the MMA.  Lane (g = lane / 4, t = lane % 4) holds columns g and
+// g + 8 and, in step i, rows r0 = 32 (i / 2) + 8 t + 4 (i % 2) to r0 + 3 of
+// the chunk (the MMA's reduction order is free as long as both operands use
+// it): two steps cover 32 consecutive rows, the smallest group, and a lane's
+// x fragment of them is 16 consecutive bytes.  In a word, nibbles i and i + 4
+// are the halves of the i-th A register (rows r0, r0 + 1 of column g; the
+// same of g + 8; rows r0 + 2, r0 + 3 of g; of g + 8), biased by 8: masked and
+// or-ed with 0x4300 they are the bf16 numbers 128 + q + 8, exactly, from which
+// 136 is subtracted exactly.  The integer products of a chunk (of 32 rows
+// for groups of 32) are summed in fp32 and the scale is applied to that sum,
+// in fp32.
+//
+// Scales: [E][N/16][R/group][8][2] bf16, the pair of columns (g, g + 8).
+#include <algorithm>
+
+#include "common.cuh"
+
+namespace moeblaze {
+namespace {
+
+constexpr int kQThreads = 512;
+constexpr int kQWarps = kQThreads / 32;
+constexpr int kQMaxTokens = 64;                    // tokens of one launch
+constexpr int kQMaxPairs = kQMaxTokens * kMaxK;    // (token, slot) pairs of one launch
+constexpr int kQDepth = 8;                         // 512-byte pieces a warp has in flight
+constexpr size_t kQSmem = 227 * 1024;
+
+__device__ __forceinline__ uint32_t saddr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// the A registers of one k16 step from a packed word
+__device__ __forceinline__ void unpack_word(uint32_t w, uint32_t (&a)[4]) {
+  const __nv_bfloat162 off = __floats2bfloat162_rn(136.f, 136.f);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t v = ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
+    const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v), off);
+    a[i] = *reinterpret_cast<const uint32_t*>(&r);
+  }
+}
+
+// ------------------------------------------------------------------ layouts
+template <typename T>
+__global__ void int4_quantize_kernel(const T* __restrict__ W, int64_t EG, int group, int N, int8_t* __restrict__ q,
+                                     __nv_bfloat16* __restrict__ scales) {
+  // one thread per (expert, group, column); EG = E R / group
+  const int64_t total = EG * N;
+  for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
+    const int64_t eg = i / N, n = i % N, base = eg * group * N + n;
+    float m = 0.f;
+    for (int r = 0; r < group; ++r) m = fmaxf(m, fabsf((float)W[base + (int64_t)r * N]));
+    const __nv_bfloat16 sb = __float2bfloat16_rn(m / 7.f);
+    const float s = __bfloat162float(sb);
+    scales[i] = sb;
+    for (int r = 0; r < group; ++r) {
+      const float v = s > 0.f ? rintf((float)W[base + (int64_t)r * N] / s) : 0.f;
+      q[base + (int64_t)r * N] = (int8_t)fminf(fmaxf(v, -8.f), 7.f);
+    }
+  }
+}
+
+// word i of the packed matrix: [E][N/16][R/64][32 lanes][4 steps]
+__global__ void int4_pack_kernel(const int8_t* __restrict__ q, int64_t words, int R, int N,
+                                 uint32_t* __restrict__ packed) {
+  const int kc = R / 64, nt = N / 16;
+  for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < words; i += (int64_t)gridDim.x * blockDim.x) {
+    const int step = (int)(i & 3), lane = (int)((i >> 2) & 31);
+    int64_t r = i >> 7;
+    const int chunk = (int)(r % kc);
+    r /= kc;
+    const int tile = (int)(r % nt);
+    const int64_t e = r / nt;
+    const int g = lane >> 2, t = lane & 3;
+    const int8_t* src = q + (e * R + chunk * 64 + 32 * (step >> 1) + 8 * t + 4 * (step & 1)) * (int64_t)N + tile * 16 + g;
+    uint32_t w = 0;
+#pragma unroll
+    for (int a = 0; a < 4; ++a)    // register a: rows 2 (a / 2), + 1 of column g + 8 (a % 2)
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const int v = src[(int64_t)(2 * (a >> 1) + b) * N + 8 * (a & 1)] + 8;
+        w |= (uint32_t)(v & 15) << (4 * a + 16 * b);
+      }
+    packed[i] = w;
+  }
+}
+
+__global__ void int4_pack_scales_kernel(const __nv_bfloat16* __restrict__ s, int64_t total, int RG, int N,
+                                        __nv_bfloat16* __restrict__ packed) {
+  const int nt = N / 16;
+  for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
+    const int c = (int)(i & 15);
+    int64_t r = i >> 4;
+    const int grp = (int)(r % RG);
+    r /= RG;
+    const int tile = (int)(r % nt);
+    const int64_t e = r / nt;
+    packed[i] = s[(e * RG + grp) * N + tile * 16 + (c >> 1) + 8 * (c & 1)];
+  }
+}
+
+__global__ void int4_dequantize_kernel(const uint32_t* __restrict__ packed, const __nv_bfloat16* __restrict__ ps,
+                                       int64_t total, int R, int N, int group, __nv_bfloat16* __restrict__ W) {
+  const int kc = R / 64, nt = N / 16, RG = R / group;
+  for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
+    const int n = (int)(i % N);
+    const int64_t er = i / N;
+    const int r = (int)(er % R);
+    const int64_t e = er / R;
+    const int tile = n >> 4, c = n & 15, g = c & 7, hi = c >> 3;
+    const int chunk = r >> 6, t = (r >> 3) & 3, step = 2 * ((r >> 5) & 1) + ((r >> 2) & 1), a = 2 * ((r >> 1) & 1) + hi, b = r & 1;
+    const uint32_t w = packed[((((e * nt + tile) * kc + chunk) * 32) + g * 4 + t) * 4 + step];
+    const int q = (int)((w >> (4 * a + 16 * b)) & 15u) - 8;
+    const float s = __bfloat162float(ps[((e * nt + tile) * (int64_t)RG + r / group) * 16 + 2 * g + hi]);
+    W[i] = __float2bfloat16_rn((float)q * s);
+  }
+}
+
+// ------------------------------------------------------------------ products
+struct QParams {
+  const __nv_bfloat16* src;  // rows of the token operand: x (row = pair / K) or h (row = pair)
+  int64_t src_ld;
+  const uint4* w[2];              // packed weights of the branches
+  const uint32_t* s[2];           // their scales, as (g, g + 8) pairs
+  const int32_t* ids;
+  int pairs, E, K;
+  int R, N;                  // reduction length and output columns of the matrices
+  int slices;                // the reduction axis in slices of R / slices (UP: 1)
+  int cap;                   // token columns of one pass
+  int groupRows;             // rows per scale
+  __nv_bfloat16* H;          // UP: h (pairs x N)
+  float* part;               // else: (slices x pairs x N)
+};
+
+// Work: segments (expert in use, pass of `cap` of its pairs, slice), each
+// with N / 16 tiles; the units (segment, tile) are split evenly and
+// contiguously over the CTAs, and a CTA's units go round its warps.  A
+// segment's token rows are staged in shared memory; the packed weights
+// stream through a ring of cp.async pieces per warp, of which every lane
+// reads back only the bytes it copied itself (no barrier), and which runs on
+// across units and segments.
+template <int NB, int NTL>
+__global__ void __launch_bounds__(kQThreads, 1) int4_product_kernel(const QParams p) {
+  constexpr int PIECES = kQDepth / NB;  // ring entries: one chunk of every branch
+  extern __shared__ __align__(16) uint8_t qsm[];
+  uint8_t* ring = qsm;                                                    // [warps][PIECES][NB][512]
+  uint32_t* sring = reinterpret_cast<uint32_t*>(ring + (size_t)kQWarps * kQDepth * 512);  // [warps][PIECES][NB][2][32]
+  int* ids_s = reinterpret_cast<int*>(sring + kQWarps * kQDepth * 2 * 32);  // [pairs]
+  int* list = ids_s + kQMaxPairs;                                          // [pairs] by expert, ascending
+  int* cnt = list + kQMaxPairs;                                            // [E]
+  int* off = cnt + kMaxE;                                                  // [E]
+  int* pre = off + kMaxE;                                                  // [E + 1] passes before expert e
+  int* tot = pre + kMaxE + 1;                                              // warp totals of the scans [2][16]
+  uint8_t* xs = reinterpret_cast<uint8_t*>(((uintptr_t)(tot + 2 * kQWarps) + 15) & ~(uintptr_t)15);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, tq = lane & 3;
+
+  // ---- pairs by expert
+  for (int i = tid; i < p.pairs; i += kQThreads) ids_s[i] = p.ids[i];
+  __syncthreads();
+  int c = 0;
+  if (tid < p.E)
+    for (int i = 0; i < p.pairs; ++i) c += ids_s[i] == tid;
+  int np = (c + p.cap - 1) / p.cap;
+  int a = c, b = np;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int ua = __shfl_up_sync(0xffffffffu, a, o), ub = __shfl_up_sync(0xffffffffu, b, o);
+    if (lane >= o) {
+      a += ua;
+      b += ub;
+    }
+  }
+  if (lane == 31) {
+    tot[warp] = a;
+    tot[kQWarps + warp] = b;
+  }
+  __syncthreads();
+  for (int w = 0; w < warp; ++w) {
+    a += tot[w];
+    b += tot[kQWarps + w];
+  }
+  if (tid < p.E) {
+    cnt[tid] = c;
+    off[tid] = a - c;
+    pre[tid + 1] = b;
+    int o = a - c;
+    for (int i = 0; i < p.pairs; ++i)
+      if (ids_s[i] == tid) list[o++] = i;
+  }
+  if (tid == 0) pre[0] = 0;
+  __syncthreads();
+
+  const int nt = p.N / 16, SL = p.R / p.slices, kc = SL / 64, allc = p.R / 64;
+  const int64_t units = (int64_t)pre[p.E] * p.slices * nt;
+  const int64_t u0 = units * blockIdx.x / gridDim.x, u1 = units * (blockIdx.x + 1) / gridDim.x;
+  if (u0 >= u1) return;
+  // the expert of pass i: the last e with pre[e] <= i
+  auto expert_of = [&](int i) {
+    int lo = 0, hi = p.E;
+    while (hi - lo > 1) {
+      const int m = (lo + hi) >> 1;
+      if (pre[m] <= i) lo = m;
+      else hi = m;
+    }
+    return lo;
+  };
+  const int half = p.groupRows == 32;  // two scales per chunk
+  const int RG = p.R / p.groupRows;
+
+  // ---- the fetch head of this warp
+  int64_t fu = u0 + warp;
+  int fk = 0, fslot = 0;
+  const uint4* fw[NB];
+  const uint32_t* fs[NB];
+  int fc0 = 0;
+  auto fetch_unit = [&]() {
+    if (fu >= u1) return;
+    const int64_t seg = fu / nt;
+    const int tile = (int)(fu - seg * nt), e = expert_of((int)(seg / p.slices)), sl = (int)(seg % p.slices);
+    fc0 = sl * kc;
+#pragma unroll
+    for (int br = 0; br < NB; ++br) {
+      fw[br] = p.w[br] + (((int64_t)e * nt + tile) * allc + fc0) * 32 + lane;
+      fs[br] = p.s[br] + ((int64_t)e * nt + tile) * RG * 8 + g;
+    }
+  };
+  auto fetch = [&]() {
+    if (fu < u1) {
+#pragma unroll
+      for (int br = 0; br < NB; ++br) {
+        const int at = (warp * PIECES + fslot) * NB + br;
+        cp16(saddr(ring + (size_t)at * 512 + lane * 16), fw[br] + (int64_t)fk * 32);
+        const int row = (fc0 + fk) * 64;
+        cp4(saddr(sring + at * 64 + lane), fs[br] + (row / p.groupRows) * 8);
+        if (half) cp4(saddr(sring + at * 64 + 32 + lane), fs[br] + (row / 32 + 1) * 8);
+      }
+      if (++fk == kc) {
+        fk = 0;
+        fu += kQWarps;
+        fetch_unit();
+      }
+    }
+    cp_commit();
+    if (++fslot == PIECES) fslot = 0;
+  };
+  fetch_unit();
+#pragma unroll
+  for (int i = 0; i < PIECES - 1; ++i) fetch();
+
+  // ---- segments
+  const int pitch = SL * 2 + 64;  // rows 16 banks apart: 2 rows x 64 bytes of a fragment load do not conflict
+  int slot = 0;
+  int64_t u = u0 + warp;
+  for (int64_t seg = u0 / nt; seg * nt < u1; ++seg) {
+    const int pass = (int)(seg / p.slices), sl = (int)(seg % p.slices), e = expert_of(pass);
+    const int first = off[e] + (pass - pre[e]) * p.cap;
+    const int n = min(p.cap, off[e] + cnt[e] - first);
+    __syncthreads();  // every warp is done with the previous segment's rows
+    {
+      const int per_row = SL / 8;
+      for (int i = tid; i < n * per_row; i += kQThreads) {
+        const int r = i / per_row, cc = i % per_row;
+        const int pair = list[first + r];
+        const int64_t row = p.H ? pair / p.K : pair;
+        *reinterpret_cast<uint4*>(xs + (size_t)r * pitch + cc * 16) =
+            *reinterpret_cast<const uint4*>(p.src + row * p.src_ld + (int64_t)sl * SL + cc * 8);
+      }
+    }
+    __syncthreads();
+    const int ntl = (n + 7) / 8;
+    const int64_t send = min((seg + 1) * (int64_t)nt, u1);
+    for (; u < send; u += kQWarps) {
+      float acc[NB][NTL][4];
+#pragma unroll
+      for (int br = 0; br < NB; ++br)
+#pragma unroll
+        for (int i = 0; i < NTL; ++i)
+#pragma unroll
+          for (int v = 0; v < 4; ++v) acc[br][i][v] = 0.f;
+      for (int k = 0; k < kc; ++k) {
+        cp_wait<PIECES - 2>();
+        uint4 wv[NB];
+        uint32_t sc[NB][2];
+#pragma unroll
+        for (int br = 0; br < NB; ++br) {
+          const int at = (warp * PIECES + slot) * NB + br;
+          wv[br] = *reinterpret_cast<const uint4*>(ring + (size_t)at * 512 + lane * 16);
+          sc[br][0] = sring[at * 64 + lane];
+          sc[br][1] = half ? sring[at * 64 + 32 + lane] : 0u;
+        }
+        if (++slot == PIECES) slot = 0;
+        fetch();
+        uint4 xa[NTL], xb[NTL];  // 8 reduction rows of each half chunk, token 8 i + g
+#pragma unroll
+        for (int i = 0; i < NTL; ++i) {
+          xa[i] = xb[i] = make_uint4(0u, 0u, 0u, 0u);
+          if (8 * i + g < n) {
+            const uint4* row = reinterpret_cast<const uint4*>(xs + (size_t)(8 * i + g) * pitch + k * 128 + tq * 16);
+            xa[i] = row[0];
+            xb[i] = row[4];
+          }
+        }
+#pragma unroll
+        for (int br = 0; br < NB; ++br) {
+          float part[NTL][4];
+#pragma unroll
+          for (int i = 0; i < NTL; ++i)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) part[i][v] = 0.f;
+          const uint32_t words[4] = {wv[br].x, wv[br].y, wv[br].z, wv[br].w};
+          auto scale = [&](uint32_t s2) {
+            const float2 s = unpack_bf16x2(s2);
+#pragma unroll
+            for (int i = 0; i < NTL; ++i) {
+              acc[br][i][0] = fmaf(part[i][0], s.x, acc[br][i][0]);
+              acc[br][i][1] = fmaf(part[i][1], s.x, acc[br][i][1]);
+              acc[br][i][2] = fmaf(part[i][2], s.y, acc[br][i][2]);
+              acc[br][i][3] = fmaf(part[i][3], s.y, acc[br][i][3]);
+#pragma unroll
+              for (int v = 0; v < 4; ++v) part[i][v] = 0.f;
+            }
+          };
+#pragma unroll
+          for (int st = 0; st < 4; ++st) {
+            uint32_t A[4];
+            unpack_word(words[st], A);
+#pragma unroll
+            for (int i = 0; i < NTL; ++i) {
+              if (i < ntl) {
+                const uint4 x4 = st < 2 ? xa[i] : xb[i];
+                mma16816(part[i], A, (st & 1) ? x4.z : x4.x, (st & 1) ? x4.w : x4.y);
+              }
+            }
+            if (st == 1 && half) scale(sc[br][0]);
+          }
+          scale(sc[br][half]);
+        }
+      }
+      // ---- this lane: columns n = 16 tile + g and + 8, tokens 8 i + 2 tq and + 1
+      const int col = (int)(u - seg * nt) * 16 + g;
+#pragma unroll
+      for (int i = 0; i < NTL; ++i)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const int tk = 8 * i + 2 * tq + (v & 1), cc = col + 8 * (v >> 1);
+          if (tk >= n) continue;
+          const int pair = list[first + tk];
+          if (p.H) {
+            const float av = acc[0][i][v];
+            float hv = av / (1.f + expf(-av));
+            if constexpr (NB == 2) hv *= acc[NB - 1][i][v];
+            p.H[(int64_t)pair * p.N + cc] = __float2bfloat16_rn(hv);
+          } else {
+            p.part[((int64_t)sl * p.pairs + pair) * p.N + cc] = acc[0][i][v];
+          }
+        }
+    }
+  }
+  cp_wait<0>();
+}
+
+// y[t] = sum_k g[t,k] sum_slices part, in that order
+__global__ void int4_combine_kernel(const float* __restrict__ part, const int32_t* __restrict__ ids,
+                                    const float* __restrict__ gates, int L, int d, int E, int K, int slices,
+                                    __nv_bfloat16* __restrict__ y) {
+  const int64_t total = (int64_t)L * d / 4;
+  const int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x;
+  if (i >= total) return;
+  const int t = (int)(i / (d / 4)), c = (int)(i % (d / 4)) * 4;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int k = 0; k < K; ++k) {
+    const int pair = t * K + k;
+    if ((unsigned)ids[pair] >= (unsigned)E) continue;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s = 0; s < slices; ++s) {
+      const float4 q = *reinterpret_cast<const float4*>(part + ((int64_t)s * L * K + pair) * d + c);
+      v.x += q.x; v.y += q.y; v.z += q.z; v.w += q.w;
+    }
+    const float g = gates[pair];
+    o.x = fmaf(g, v.x, o.x); o.y = fmaf(g, v.y, o.y); o.z = fmaf(g, v.z, o.z); o.w = fmaf(g, v.w, o.w);
+  }
+  *reinterpret_cast<uint2*>(y + (int64_t)t * d + c) = make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
+}
+
+// shared memory besides the token rows
+constexpr size_t kQFixed = (size_t)kQWarps * kQDepth * (512 + 256) + 4 * (2 * kQMaxPairs + 3 * kMaxE + 1 + 2 * kQWarps) + 16;
+
+// token columns of one pass over an expert: up to 32, as many rows of `len`
+// elements as shared memory holds
+int pass_cap(int64_t len) {
+  const int64_t rows = (int64_t)(kQSmem - kQFixed) / (len * 2 + 64);
+  return rows >= 32 ? 32 : (int)rows;
+}
+
+// slices of the down projection's reduction axis: enough units for every
+// warp of the GPU, slices of whole 128-row blocks
+int down_slices(const moeblaze_shape& s, int tokens) {
+  const int blocks = s.h / 128;
+  const int64_t used = std::min<int64_t>(s.E, (int64_t)tokens * s.K);
+  const int64_t units = used * (s.d / 16);
+  const int64_t want = (int64_t)sm_count() * kQWarps;
+  int best = 1;
+  for (int n = 1; n <= blocks; ++n) {
+    if (blocks % n) continue;
+    best = n;
+    const int64_t len = s.h / n;
+    if (units * n >= want && (pass_cap(len) >= std::min(tokens, 32) || len <= 1024)) break;
+    if (len <= 512) break;
+  }
+  return best;
+}
+
+size_t h_bytes(const moeblaze_shape& s, int tokens) {
+  return align_up((size_t)tokens * s.K * s.h * 2, 256);
+}
+
+template <int NB>
+moeblaze_status launch_product(const QParams& p, int tokens, cudaStream_t st) {
+  const int cap8 = std::min(p.cap, (tokens + 7) / 8 * 8);
+  const int rows = std::min(p.cap, tokens);
+  const size_t sm = kQFixed + (size_t)rows * (p.R / p.slices * 2 + 64);
+  auto run = [&](auto kern) -> moeblaze_status {
+    MB_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm));
+    kern<<<sm_count(), kQThreads, sm, st>>>(p);
+    MB_CUDA(cudaGetLastError());
+    count_launch();
+    return MOEBLAZE_OK;
+  };
+  if (cap8 <= 8) return run(int4_product_kernel<NB, 1>);
+  if (cap8 <= 16) return run(int4_product_kernel<NB, 2>);
+  return run(int4_product_kernel<NB, 4>);
+}
+
+}  // namespace
+
+bool int4_shape_ok(const moeblaze_shape& s) { return pass_cap(s.d) >= 1; }
+
+size_t int4_ws_bytes(const moeblaze_shape& s) {
+  const int tokens = (int)std::min<int64_t>(s.L, kQMaxTokens);
+  if (tokens == 0) return 0;
+  // the slices depend on the tokens of a launch: the last one may have fewer
+  size_t most = 0;
+  for (const int t : {tokens, (int)(s.L % kQMaxTokens)}) {
+    if (t == 0) continue;
+    most = std::max(most, (size_t)down_slices(s, t) * t * s.K * s.d * sizeof(float));
+  }
+  return h_bytes(s, tokens) + align_up(most, 256);
+}
+
+moeblaze_status launch_int4_forward(const moeblaze_shape& s, const __nv_bfloat16* x, const int32_t* ids,
+                                    const float* gates, const moeblaze_int4_experts& w, __nv_bfloat16* y, void* ws,
+                                    cudaStream_t st) {
+  for (int64_t t0 = 0; t0 < s.L; t0 += kQMaxTokens) {
+    const int tokens = (int)std::min<int64_t>(s.L - t0, kQMaxTokens);
+    __nv_bfloat16* H = static_cast<__nv_bfloat16*>(ws);
+    float* part = reinterpret_cast<float*>(static_cast<char*>(ws) + h_bytes(s, (int)std::min<int64_t>(s.L, kQMaxTokens)));
+    const bool sw = s.act == MOEBLAZE_SWIGLU;
+    QParams p = {};
+    p.src = x + t0 * s.d;
+    p.src_ld = s.d;
+    p.w[0] = static_cast<const uint4*>(w.w1);
+    p.s[0] = static_cast<const uint32_t*>(w.s1);
+    p.w[1] = static_cast<const uint4*>(w.w2);
+    p.s[1] = static_cast<const uint32_t*>(w.s2);
+    p.ids = ids + t0 * s.K;
+    p.pairs = tokens * s.K;
+    p.E = s.E;
+    p.K = s.K;
+    p.R = s.d;
+    p.N = s.h;
+    p.slices = 1;
+    p.cap = pass_cap(s.d);
+    p.groupRows = w.group;
+    p.H = H;
+    moeblaze_status r = sw ? launch_product<2>(p, tokens, st) : launch_product<1>(p, tokens, st);
+    if (r != MOEBLAZE_OK) return r;
+    p.src = H;
+    p.src_ld = s.h;
+    p.w[0] = static_cast<const uint4*>(w.w3);
+    p.s[0] = static_cast<const uint32_t*>(w.s3);
+    p.R = s.h;
+    p.N = s.d;
+    p.slices = down_slices(s, tokens);
+    p.cap = pass_cap(s.h / p.slices);
+    p.H = nullptr;
+    p.part = part;
+    if ((r = launch_product<1>(p, tokens, st)) != MOEBLAZE_OK) return r;
+    const int64_t n = (int64_t)tokens * s.d / 4;
+    int4_combine_kernel<<<(unsigned)((n + 127) / 128), 128, 0, st>>>(part, ids + t0 * s.K, gates + t0 * s.K, tokens, s.d,
+                                                                   s.E, s.K, p.slices, y + t0 * s.d);
+    MB_CUDA(cudaGetLastError());
+    count_launch();
+  }
+  return MOEBLAZE_OK;
+}
+
+namespace {
+unsigned flat_grid(int64_t n) {
+  int64_t b = (n + 255) / 256;
+  if (b > 32 * (int64_t)sm_count()) b = 32 * (int64_t)sm_count();
+  return (unsigned)b;
+}
+}  // namespace
+
+moeblaze_status launch_int4_quantize(int E, int R, int N, int group, int dtype, const void* W, int8_t* q, void* scales,
+                                     cudaStream_t st) {
+  const int64_t eg = (int64_t)E * (R / group);
+  if (dtype == MOEBLAZE_BF16)
+    int4_quantize_kernel<<<flat_grid(eg * N), 256, 0, st>>>(static_cast<const __nv_bfloat16*>(W), eg, group, N, q,
+                                                            static_cast<__nv_bfloat16*>(scales));
+  else
+    int4_quantize_kernel<<<flat_grid(eg * N), 256, 0, st>>>(static_cast<const float*>(W), eg, group, N, q,
+                                                            static_cast<__nv_bfloat16*>(scales));
+  MB_CUDA(cudaGetLastError());
+  count_launch();
+  return MOEBLAZE_OK;
+}
+
+moeblaze_status launch_int4_pack(int E, int R, int N, int group, const int8_t* q, const void* scales, void* packed,
+                                 void* packed_scales, cudaStream_t st) {
+  const int64_t words = (int64_t)E * R * N / 8, ns = (int64_t)E * (R / group) * N;
+  int4_pack_kernel<<<flat_grid(words), 256, 0, st>>>(q, words, R, N, static_cast<uint32_t*>(packed));
+  MB_CUDA(cudaGetLastError());
+  int4_pack_scales_kernel<<<flat_grid(ns), 256, 0, st>>>(static_cast<const __nv_bfloat16*>(scales), ns, R / group, N,
+                                                         static_cast<__nv_bfloat16*>(packed_scales));
+  MB_CUDA(cudaGetLastError());
+  count_launch(2);
+  return MOEBLAZE_OK;
+}
+
+moeblaze_status launch_int4_dequantize(int E, int R, int N, int group, const void* packed, const void* packed_scales,
+                                       void* W, cudaStream_t st) {
+  const int64_t n = (int64_t)E * R * N;
+  int4_dequantize_kernel<<<flat_grid(n), 256, 0, st>>>(static_cast<const uint32_t*>(packed),
+                                                       static_cast<const __nv_bfloat16*>(packed_scales), n, R, N, group,
+                                                       static_cast<__nv_bfloat16*>(W));
+  MB_CUDA(cudaGetLastError());
+  count_launch();
+  return MOEBLAZE_OK;
+}
+
+}  // namespace moeblaze

@@ -1,0 +1,528 @@
+// Layer norm with the residual sum fused, and its backward: the norm in front
+// of an MoE layer (pre-norm block), over rows of d elements.
+//
+//   s = x (+ residual)     mu = mean(s)     rstd = 1 / sqrt(var(s) + eps)
+//   y = (s - mu) rstd w + b
+//
+//   g = dy w, xh = (s - mu) rstd
+//   ds = rstd (g - mean(g) - xh mean(g xh)) (+ dsum)
+//   dw = sum_t dy xh,  db = sum_t dy
+//
+// Everything is computed in fp32 and rounded once at the store.  Both passes
+// read every input and write every output once: the row lives in registers
+// between the statistics and the normalisation, and the variance is taken of
+// the centred row (a second sum over registers, not E[s^2] - mu^2, which
+// would cancel for rows with an offset).  Bound by HBM.
+//
+// A row is spread over TPR threads (one warp, or a whole CTA), NV vectors of
+// VEC elements per thread.  VEC is the widest power of two up to 16 bytes
+// that divides d, so that every row of a dense matrix starts on a vector.
+#include "common.cuh"
+
+namespace moeblaze {
+namespace {
+
+template <typename T, int VEC>
+struct alignas(sizeof(T) * VEC) Vec {
+  T v[VEC];
+};
+
+__device__ __forceinline__ float ld_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float ld_f32(float v) { return v; }
+__device__ __forceinline__ void st_t(__nv_bfloat16& o, float v) { o = __float2bfloat16_rn(v); }
+__device__ __forceinline__ void st_t(float& o, float v) { o = v; }
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// sum over the TPR threads of a row; `red` holds one float per warp of the
+// row and is not shared with another reduction in flight
+template <int TPR>
+__device__ __forceinline__ float row_sum(float v, float* red) {
+  v = warp_sum(v);
+  if constexpr (TPR > 32) {
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = 0.f;
+#pragma unroll
+    for (int i = 0; i < TPR / 32; ++i) v += red[i];
+  }
+  return v;
+}
+
+constexpr int kNormWarps = 4;  // rows per CTA when a warp holds a row
+
+template <int TPR>
+constexpr int norm_threads() {
+  return TPR == 32 ? 32 * kNormWarps : TPR;
+}
+
+// ------------------------------------------------------------------ forward
+template <typename T, int VEC, int TPR, int NV>
+__global__ void __launch_bounds__(norm_threads<TPR>()) norm_fwd_kernel(const T* x, const T* res,
+                                                                        const float* __restrict__ w,
+                                                                        const float* __restrict__ b, int64_t L, int d,
+                                                                        float eps, T* sum, T* y,
+                                                                        float* __restrict__ mean_out,
+                                                                        float* __restrict__ rstd_out) {
+  using V = Vec<T, VEC>;
+  __shared__ float red[2][32];
+  const int lane = TPR == 32 ? (threadIdx.x & 31) : threadIdx.x;
+  const int64_t t = TPR == 32 ? (int64_t)blockIdx.x * kNormWarps + (threadIdx.x >> 5) : (int64_t)blockIdx.x;
+  if (t >= L) return;  // a whole warp or a whole CTA
+  const int nvec = d / VEC;
+  const V* xr = reinterpret_cast<const V*>(x + t * d);
+  const V* rr = res ? reinterpret_cast<const V*>(res + t * d) : nullptr;
+  float s[NV][VEC];
+  V xv[NV], rv[NV];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int c = lane + j * TPR;
+    if (c < nvec) xv[j] = xr[c];
+  }
+  if (rr) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = lane + j * TPR;
+      if (c < nvec) rv[j] = rr[c];
+    }
+  }
+  float acc = 0.f;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int c = lane + j * TPR;
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+      s[j][i] = 0.f;
+      if (c < nvec) {
+        s[j][i] = ld_f32(xv[j].v[i]);
+        if (rr) s[j][i] += ld_f32(rv[j].v[i]);
+      }
+      acc += s[j][i];
+    }
+  }
+  if (sum) {
+    V* so = reinterpret_cast<V*>(sum + t * d);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = lane + j * TPR;
+      V o;
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) st_t(o.v[i], s[j][i]);
+      if (c < nvec) so[c] = o;
+    }
+  }
+  const float inv_d = 1.f / (float)d;
+  const float mu = row_sum<TPR>(acc, red[0]) * inv_d;
+  acc = 0.f;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const bool in = lane + j * TPR < nvec;
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+      s[j][i] -= mu;
+      acc = in ? fmaf(s[j][i], s[j][i], acc) : acc;
+    }
+  }
+  const float rstd = 1.f / sqrtf(row_sum<TPR>(acc, red[1]) * inv_d + eps);
+  V* yo = reinterpret_cast<V*>(y + t * d);
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int c = lane + j * TPR;
+    if (c < nvec) {
+      using W = Vec<float, (VEC < 4 ? VEC : 4)>;
+      constexpr int WV = VEC < 4 ? VEC : 4;
+      V o;
+#pragma unroll
+      for (int q = 0; q < VEC / WV; ++q) {
+        const W wv = reinterpret_cast<const W*>(w)[c * (VEC / WV) + q];
+        W bv;
+        if (b) bv = reinterpret_cast<const W*>(b)[c * (VEC / WV) + q];
+#pragma unroll
+        for (int i = 0; i < WV; ++i)
+          st_t(o.v[q * WV + i], fmaf(s[j][q * WV + i] * rstd, wv.v[i], b ? bv.v[i] : 0.f));
+      }
+      yo[c] = o;
+    }
+  }
+  if (lane == 0) {
+    mean_out[t] = mu;
+    rstd_out[t] = rstd;
+  }
+}
+
+// rows wider than the register tiles: the row is read again for each of the
+// three steps (the second and third time from L2).  Row t of `sum` may be
+// row t of x or of the residual: it is written in the last step, by the
+// thread that has just read the element for the last time.
+template <typename T>
+__global__ void __launch_bounds__(1024) norm_fwd_wide_kernel(const T* x, const T* res, const float* __restrict__ w,
+                                                             const float* __restrict__ b, int64_t L, int d, float eps,
+                                                             T* sum, T* y, float* __restrict__ mean_out,
+                                                             float* __restrict__ rstd_out) {
+  __shared__ float red[2][32];
+  const int64_t o = (int64_t)blockIdx.x * d;
+  auto at = [&](int c) { return ld_f32(x[o + c]) + (res ? ld_f32(res[o + c]) : 0.f); };
+  float acc = 0.f;
+  for (int c = threadIdx.x; c < d; c += 1024) acc += at(c);
+  const float mu = row_sum<1024>(acc, red[0]) / (float)d;
+  acc = 0.f;
+  for (int c = threadIdx.x; c < d; c += 1024) {
+    const float v = at(c) - mu;
+    acc = fmaf(v, v, acc);
+  }
+  const float rstd = 1.f / sqrtf(row_sum<1024>(acc, red[1]) / (float)d + eps);
+  for (int c = threadIdx.x; c < d; c += 1024) {
+    const float v = at(c);
+    if (sum) st_t(sum[o + c], v);
+    st_t(y[o + c], fmaf((v - mu) * rstd, w[c], b ? b[c] : 0.f));
+  }
+  if (threadIdx.x == 0) {
+    mean_out[blockIdx.x] = mu;
+    rstd_out[blockIdx.x] = rstd;
+  }
+}
+
+// ------------------------------------------------------------------ backward
+// A persistent CTA walks over rows t = first, first + rows in flight, ...;
+// a thread always holds the same columns, so the sums of dw and db over the
+// CTA's rows stay in its registers.  part[cta][0][c] and part[cta][1][c]
+// are added up in a fixed order by norm_wgrad_kernel.
+template <typename T, int VEC, int TPR, int NV>
+__global__ void __launch_bounds__(norm_threads<TPR>()) norm_bwd_kernel(
+    const T* dy, const T* s, const float* __restrict__ mean, const float* __restrict__ rstd,
+    const float* __restrict__ w, const T* dsum, int64_t L, int d, T* dx, float* __restrict__ part) {
+  using V = Vec<T, VEC>;
+  constexpr int ROWS = TPR == 32 ? kNormWarps : 1;
+  __shared__ float red[2][2][32];
+  const int lane = TPR == 32 ? (threadIdx.x & 31) : threadIdx.x;
+  const int nvec = d / VEC;
+  const float inv_d = 1.f / (float)d;
+  float aw[NV][VEC], ab[NV][VEC], wv[NV][VEC];
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+      const int c = lane + j * TPR;
+      aw[j][i] = ab[j][i] = 0.f;
+      wv[j][i] = c < nvec ? w[c * VEC + i] : 0.f;
+    }
+  const int64_t step = (int64_t)gridDim.x * ROWS;
+  const int64_t first = (int64_t)blockIdx.x * ROWS + (TPR == 32 ? (threadIdx.x >> 5) : 0);
+  V nd[NV], ns[NV], nr[NV];
+  float nmu = 0.f, nrs = 0.f;
+  auto fetch = [&](int64_t t) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = lane + j * TPR;
+      if (c < nvec) {
+        nd[j] = reinterpret_cast<const V*>(dy + t * d)[c];
+        ns[j] = reinterpret_cast<const V*>(s + t * d)[c];
+        if (dsum) nr[j] = reinterpret_cast<const V*>(dsum + t * d)[c];
+      }
+    }
+    nmu = mean[t];
+    nrs = rstd[t];
+  };
+  if (first < L) fetch(first);
+  int buf = 0;
+  for (int64_t t = first; t < L; t += step, buf ^= 1) {
+    const float mu = nmu, rs = nrs;
+    float xh[NV][VEC], g[NV][VEC], rr[NV][VEC];
+    float sg = 0.f, sgx = 0.f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const bool in = lane + j * TPR < nvec;
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) {
+        const float dv = in ? ld_f32(nd[j].v[i]) : 0.f;
+        xh[j][i] = in ? (ld_f32(ns[j].v[i]) - mu) * rs : 0.f;
+        rr[j][i] = in && dsum ? ld_f32(nr[j].v[i]) : 0.f;
+        aw[j][i] = fmaf(dv, xh[j][i], aw[j][i]);
+        ab[j][i] += dv;
+        g[j][i] = dv * wv[j][i];
+        sg += g[j][i];
+        sgx = fmaf(g[j][i], xh[j][i], sgx);
+      }
+    }
+    if (t + step < L) fetch(t + step);
+    sg = warp_sum(sg);
+    sgx = warp_sum(sgx);
+    if constexpr (TPR > 32) {
+      // two buffers in turn: a warp can be one row ahead of the slowest
+      // reader of the other buffer, never two
+      if ((threadIdx.x & 31) == 0) {
+        red[buf][0][threadIdx.x >> 5] = sg;
+        red[buf][1][threadIdx.x >> 5] = sgx;
+      }
+      __syncthreads();
+      sg = sgx = 0.f;
+#pragma unroll
+      for (int i = 0; i < TPR / 32; ++i) {
+        sg += red[buf][0][i];
+        sgx += red[buf][1][i];
+      }
+    }
+    const float mg = sg * inv_d, mgx = sgx * inv_d;
+    V* o = reinterpret_cast<V*>(dx + t * d);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = lane + j * TPR;
+      V ov;
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) st_t(ov.v[i], fmaf(rs, g[j][i] - mg - xh[j][i] * mgx, rr[j][i]));
+      if (c < nvec) o[c] = ov;
+    }
+  }
+  float* pw = part + (int64_t)blockIdx.x * 2 * d;
+  if constexpr (TPR > 32) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) {
+        const int c = (lane + j * TPR) * VEC + i;
+        if (c < d) {
+          pw[c] = aw[j][i];
+          pw[d + c] = ab[j][i];
+        }
+      }
+  } else {
+    // the CTA's warps hold the same columns of different rows
+    __shared__ float cw[kNormWarps][32];
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int i = 0; i < VEC; ++i)
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          __syncthreads();
+          cw[threadIdx.x >> 5][lane] = q ? ab[j][i] : aw[j][i];
+          __syncthreads();
+          const int c = (lane + j * 32) * VEC + i;
+          if (threadIdx.x < 32 && c < d) {
+            float a = 0.f;
+#pragma unroll
+            for (int r = 0; r < kNormWarps; ++r) a += cw[r][lane];
+            pw[q * d + c] = a;
+          }
+        }
+  }
+}
+
+// dw and db from the CTAs' partial sums, in the order of the CTAs: 32 columns
+// per block, its 8 warps take every eighth partial
+__global__ void __launch_bounds__(256) norm_wgrad_kernel(const float* __restrict__ part, int G, int d,
+                                                         float* __restrict__ dw, float* __restrict__ db) {
+  __shared__ float acc[8][32];
+  const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + lane;  // column of the (2 d) row [dw | db]
+  float a = 0.f;
+  if (c < 2 * d) {
+#pragma unroll 4
+    for (int g = wp; g < G; g += 8) a += part[(int64_t)g * 2 * d + c];
+  }
+  acc[wp][lane] = a;
+  __syncthreads();
+  if (wp == 0 && c < 2 * d) {
+    a = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) a += acc[i][lane];
+    if (c < d) dw[c] = a;
+    else if (db) db[c - d] = a;
+  }
+}
+
+// rows wider than the register tiles
+template <typename T>
+__global__ void __launch_bounds__(1024) norm_bwd_wide_kernel(const T* dy, const T* s, const float* __restrict__ mean,
+                                                             const float* __restrict__ rstd,
+                                                             const float* __restrict__ w, const T* dsum, int d, T* dx) {
+  __shared__ float red[2][32];
+  const int64_t t = blockIdx.x, o = t * d;
+  const float mu = mean[t], rs = rstd[t];
+  float sg = 0.f, sgx = 0.f;
+  for (int c = threadIdx.x; c < d; c += 1024) {
+    const float g = ld_f32(dy[o + c]) * w[c];
+    sg += g;
+    sgx = fmaf(g, (ld_f32(s[o + c]) - mu) * rs, sgx);
+  }
+  const float mg = row_sum<1024>(sg, red[0]) / (float)d, mgx = row_sum<1024>(sgx, red[1]) / (float)d;
+  for (int c = threadIdx.x; c < d; c += 1024) {
+    const float g = ld_f32(dy[o + c]) * w[c], xh = (ld_f32(s[o + c]) - mu) * rs;
+    st_t(dx[o + c], fmaf(rs, g - mg - xh * mgx, dsum ? ld_f32(dsum[o + c]) : 0.f));
+  }
+}
+
+// partial dw and db of every `step`-th row, a thread per column
+template <typename T>
+__global__ void __launch_bounds__(256) norm_wide_wgrad_kernel(const T* dy, const T* s, const float* __restrict__ mean,
+                                                              const float* __restrict__ rstd, int64_t L, int d,
+                                                              float* __restrict__ part) {
+  const int c = blockIdx.x * 256 + threadIdx.x;
+  if (c >= d) return;
+  float aw = 0.f, ab = 0.f;
+#pragma unroll 4
+  for (int64_t t = blockIdx.y; t < L; t += gridDim.y) {
+    const float dv = ld_f32(dy[t * d + c]);
+    aw = fmaf(dv, (ld_f32(s[t * d + c]) - mean[t]) * rstd[t], aw);
+    ab += dv;
+  }
+  part[(int64_t)blockIdx.y * 2 * d + c] = aw;
+  part[(int64_t)blockIdx.y * 2 * d + d + c] = ab;
+}
+
+constexpr int kWideSplits = 32;
+constexpr int kMaxTileVecs = 4096;  // widest register tile: 1024 threads of 4 vectors
+
+template <typename T>
+int vec_of(int d) {
+  int v = 16 / (int)sizeof(T);
+  while (d % v) v >>= 1;
+  return v;
+}
+
+// CTAs of the backward: enough rows in flight to fill the GPU.  The partial
+// sums are G x 2 d floats.
+int64_t bwd_ctas(const moeblaze_shape& s, int tpr) {
+  const int rows = tpr == 32 ? kNormWarps : 1;
+  int64_t per_sm = tpr == 32 ? 8 : 1024 / tpr;
+  if (per_sm < 1) per_sm = 1;
+  int64_t g = per_sm * sm_count();
+  const int64_t need = (s.L + rows - 1) / rows;
+  return g < need ? g : need;
+}
+
+template <typename T, int VEC, int TPR, int NV>
+moeblaze_status fwd_tile(const moeblaze_shape& s, const void* x, const void* res, const float* w, const float* b,
+                         float eps, void* sum, void* y, float* mean, float* rstd, cudaStream_t st) {
+  const int rows = TPR == 32 ? kNormWarps : 1;
+  norm_fwd_kernel<T, VEC, TPR, NV><<<(unsigned)((s.L + rows - 1) / rows), norm_threads<TPR>(), 0, st>>>(
+      (const T*)x, (const T*)res, w, b, s.L, s.d, eps, (T*)sum, (T*)y, mean, rstd);
+  MB_CUDA(cudaGetLastError());
+  count_launch();
+  return MOEBLAZE_OK;
+}
+
+template <typename T, int VEC, int TPR, int NV>
+moeblaze_status bwd_tile(const moeblaze_shape& s, const void* dy, const void* sum, const float* mean,
+                         const float* rstd, const float* w, const void* dsum, void* dx, float* dw, float* db,
+                         float* part, cudaStream_t st) {
+  const int64_t G = bwd_ctas(s, TPR);
+  norm_bwd_kernel<T, VEC, TPR, NV><<<(unsigned)G, norm_threads<TPR>(), 0, st>>>(
+      (const T*)dy, (const T*)sum, mean, rstd, w, (const T*)dsum, s.L, s.d, (T*)dx, part);
+  MB_CUDA(cudaGetLastError());
+  norm_wgrad_kernel<<<(unsigned)((2 * (int64_t)s.d + 31) / 32), 256, 0, st>>>(part, (int)G, s.d, dw, db);
+  MB_CUDA(cudaGetLastError());
+  count_launch(2);
+  return MOEBLAZE_OK;
+}
+
+// the register tile of a row of n vectors: f(TPR, NV) as integral constants
+#define MB_NORM_TILE(n, CALL)                  \
+  do {                                         \
+    if ((n) <= 32) return CALL(32, 1);         \
+    if ((n) <= 64) return CALL(32, 2);         \
+    if ((n) <= 128) return CALL(32, 4);        \
+    if ((n) <= 256) return CALL(128, 2);       \
+    if ((n) <= 512) return CALL(256, 2);       \
+    if ((n) <= 1024) return CALL(512, 2);      \
+    if ((n) <= 2048) return CALL(1024, 2);     \
+    return CALL(1024, 4);                      \
+  } while (0)
+
+int tile_tpr(int n) { return n <= 128 ? 32 : n <= 256 ? 128 : n <= 512 ? 256 : n <= 1024 ? 512 : 1024; }
+
+template <typename T, int VEC>
+moeblaze_status fwd_vec(const moeblaze_shape& s, const void* x, const void* res, const float* w, const float* b,
+                        float eps, void* sum, void* y, float* mean, float* rstd, cudaStream_t st) {
+#define MB_CALL(TPR, NV) fwd_tile<T, VEC, TPR, NV>(s, x, res, w, b, eps, sum, y, mean, rstd, st)
+  MB_NORM_TILE(s.d / VEC, MB_CALL);
+#undef MB_CALL
+}
+
+template <typename T, int VEC>
+moeblaze_status bwd_vec(const moeblaze_shape& s, const void* dy, const void* sum, const float* mean, const float* rstd,
+                        const float* w, const void* dsum, void* dx, float* dw, float* db, float* part,
+                        cudaStream_t st) {
+#define MB_CALL(TPR, NV) bwd_tile<T, VEC, TPR, NV>(s, dy, sum, mean, rstd, w, dsum, dx, dw, db, part, st)
+  MB_NORM_TILE(s.d / VEC, MB_CALL);
+#undef MB_CALL
+}
+
+template <typename T>
+moeblaze_status fwd_t(const moeblaze_shape& s, const void* x, const void* res, const float* w, const float* b,
+                      float eps, void* sum, void* y, float* mean, float* rstd, cudaStream_t st) {
+  const int v = vec_of<T>(s.d);
+  if (s.d / v > kMaxTileVecs) {
+    norm_fwd_wide_kernel<T><<<(unsigned)s.L, 1024, 0, st>>>((const T*)x, (const T*)res, w, b, s.L, s.d, eps, (T*)sum,
+                                                            (T*)y, mean, rstd);
+    MB_CUDA(cudaGetLastError());
+    count_launch();
+    return MOEBLAZE_OK;
+  }
+  if constexpr (sizeof(T) == 2)
+    if (v == 8) return fwd_vec<T, 8>(s, x, res, w, b, eps, sum, y, mean, rstd, st);
+  if (v == 4) return fwd_vec<T, 4>(s, x, res, w, b, eps, sum, y, mean, rstd, st);
+  if (v == 2) return fwd_vec<T, 2>(s, x, res, w, b, eps, sum, y, mean, rstd, st);
+  return fwd_vec<T, 1>(s, x, res, w, b, eps, sum, y, mean, rstd, st);
+}
+
+template <typename T>
+moeblaze_status bwd_t(const moeblaze_shape& s, const void* dy, const void* sum, const float* mean, const float* rstd,
+                      const float* w, const void* dsum, void* dx, float* dw, float* db, float* part, cudaStream_t st) {
+  const int v = vec_of<T>(s.d);
+  if (s.d / v > kMaxTileVecs) {
+    norm_bwd_wide_kernel<T><<<(unsigned)s.L, 1024, 0, st>>>((const T*)dy, (const T*)sum, mean, rstd, w, (const T*)dsum,
+                                                            s.d, (T*)dx);
+    MB_CUDA(cudaGetLastError());
+    const int64_t G = s.L < kWideSplits ? s.L : kWideSplits;
+    norm_wide_wgrad_kernel<T><<<dim3((unsigned)((s.d + 255) / 256), (unsigned)G), 256, 0, st>>>(
+        (const T*)dy, (const T*)sum, mean, rstd, s.L, s.d, part);
+    MB_CUDA(cudaGetLastError());
+    norm_wgrad_kernel<<<(unsigned)((2 * (int64_t)s.d + 31) / 32), 256, 0, st>>>(part, (int)G, s.d, dw, db);
+    MB_CUDA(cudaGetLastError());
+    count_launch(3);
+    return MOEBLAZE_OK;
+  }
+  if constexpr (sizeof(T) == 2)
+    if (v == 8) return bwd_vec<T, 8>(s, dy, sum, mean, rstd, w, dsum, dx, dw, db, part, st);
+  if (v == 4) return bwd_vec<T, 4>(s, dy, sum, mean, rstd, w, dsum, dx, dw, db, part, st);
+  if (v == 2) return bwd_vec<T, 2>(s, dy, sum, mean, rstd, w, dsum, dx, dw, db, part, st);
+  return bwd_vec<T, 1>(s, dy, sum, mean, rstd, w, dsum, dx, dw, db, part, st);
+}
+
+}  // namespace
+
+size_t norm_ws_bytes(const moeblaze_shape& s) {
+  if (s.L == 0) return 0;
+  const int v = s.dtype == MOEBLAZE_BF16 ? vec_of<__nv_bfloat16>(s.d) : vec_of<float>(s.d);
+  const int n = s.d / v;
+  const int64_t G = n > kMaxTileVecs ? (s.L < kWideSplits ? s.L : kWideSplits) : bwd_ctas(s, tile_tpr(n));
+  return (size_t)G * 2 * s.d * sizeof(float);
+}
+
+moeblaze_status launch_layernorm_forward(const moeblaze_shape& s, const void* x, const void* res, const float* w,
+                                         const float* b, float eps, void* sum, void* y, float* mean, float* rstd,
+                                         cudaStream_t st) {
+  if (s.L == 0) return MOEBLAZE_OK;
+  return s.dtype == MOEBLAZE_BF16 ? fwd_t<__nv_bfloat16>(s, x, res, w, b, eps, sum, y, mean, rstd, st)
+                                  : fwd_t<float>(s, x, res, w, b, eps, sum, y, mean, rstd, st);
+}
+
+moeblaze_status launch_layernorm_backward(const moeblaze_shape& s, const void* dy, const void* sum, const float* mean,
+                                          const float* rstd, const float* w, const void* dsum, void* dx, float* dw,
+                                          float* db, void* ws, cudaStream_t st) {
+  if (s.L == 0) {
+    MB_CUDA(cudaMemsetAsync(dw, 0, sizeof(float) * s.d, st));
+    if (db) MB_CUDA(cudaMemsetAsync(db, 0, sizeof(float) * s.d, st));
+    return MOEBLAZE_OK;
+  }
+  return s.dtype == MOEBLAZE_BF16
+             ? bwd_t<__nv_bfloat16>(s, dy, sum, mean, rstd, w, dsum, dx, dw, db, (float*)ws, st)
+             : bwd_t<float>(s, dy, sum, mean, rstd, w, dsum, dx, dw, db, (float*)ws, st);
+}
+
+}  // namespace moeblaze

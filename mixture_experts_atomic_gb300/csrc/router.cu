@@ -123,7 +123,8 @@ template <typename T, int EP>
 __global__ void __launch_bounds__(kRThreads) router_fwd_kernel(const T* __restrict__ x, const float* __restrict__ Wr,
                                                                const float* __restrict__ bias, int64_t L, int d, int E,
                                                                int K, int32_t* __restrict__ ids,
-                                                               float* __restrict__ gates) {
+                                                               float* __restrict__ gates,
+                                                               float* __restrict__ logits) {
   using Ly = RLayout<EP>;
   constexpr int S = Ly::STAGES, P = XPitch<T>::value;
   constexpr int XS = kRT * P;  // elements of one x stage
@@ -181,7 +182,11 @@ __global__ void __launch_bounds__(kRThreads) router_fwd_kernel(const T* __restri
     const int e = j * Ly::TE + te;
     const float b = (e < E && bias) ? bias[e] : 0.f;
 #pragma unroll
-    for (int i = 0; i < Ly::RPT; ++i) acc[i][j] = e < E ? acc[i][j] + b : -FLT_MAX;
+    for (int i = 0; i < Ly::RPT; ++i) {
+      acc[i][j] = e < E ? acc[i][j] + b : -FLT_MAX;
+      const int64_t t = t0 + tr * Ly::RPT + i;
+      if (logits && e < E && t < L) logits[t * E + e] = acc[i][j];
+    }
   }
 
   // top-K of each row across the TE lanes that hold its experts (consecutive
@@ -252,7 +257,8 @@ template <typename T, int EP>
 __global__ void __launch_bounds__(512) router_fwd_gemv_kernel(const T* __restrict__ x, const float* __restrict__ Wr,
                                                               const float* __restrict__ bias, int64_t L, int d, int E,
                                                               int K, int32_t* __restrict__ ids,
-                                                              float* __restrict__ gates) {
+                                                              float* __restrict__ gates,
+                                                              float* __restrict__ logits) {
   constexpr int TPW = 4;  // tokens per warp pass
   extern __shared__ __align__(16) uint8_t rsm[];
   // Wr as [d][EP] with 4 floats of padding after every 8 rows: the lanes of
@@ -334,6 +340,11 @@ __global__ void __launch_bounds__(512) router_fwd_gemv_kernel(const T* __restric
       float lg[EP];
 #pragma unroll
       for (int e = 0; e < EP; ++e) lg[e] = e < E ? acc[q][e] + (bias ? bias[e] : 0.f) : -FLT_MAX;
+      if (logits) {
+#pragma unroll
+        for (int e = 0; e < EP; ++e)
+          if (e < E) logits[t * E + e] = lg[e];
+      }
       uint32_t taken = 0;
       float selv[kMaxK], w[kMaxK], sum = 0.f;
       int seli[kMaxK];
@@ -673,6 +684,288 @@ __global__ void __launch_bounds__(kBwThreads) router_bwd_small_kernel(
   if (blockIdx.x == 0 && tid < E) part_b[(int64_t)blockIdx.y * E + tid] = bacc;
 }
 
+// ------------------------------------------------------------------ dense logit gradients
+// dWr = x^T dl, dbias = sum_t dl[t], dx = dl Wr^T for a gradient dl (L,E) of
+// every logit (a loss on the logits, such as the load balance, reaches all
+// experts of a token, not the K chosen ones).
+//
+// Few experts (EP <= 16): one pass over x and dx.  A thread owns CPT = 64/EP
+// columns with their rows of Wr and its partial dWr in registers (64 floats
+// each), so that a token costs it one piece of x, one of dx and the token's
+// dl row, which the CTA shares; the products are packed fp32x2 FMAs over
+// pairs of experts.  part[s] holds split s's sums for router_reduce_kernel.
+constexpr int kDgThreads = 128;
+template <int EP>
+constexpr int dg_cpt() {
+  return 64 / EP;
+}
+constexpr int kDgAhead = 8;  // pieces of x each thread has in flight
+template <typename T, int EP>
+constexpr size_t dg_smem() {
+  return 2 * (size_t)kRT * EP * sizeof(float) + (size_t)kDgAhead * kDgThreads * dg_cpt<EP>() * sizeof(T);
+}
+
+template <int BYTES>
+__device__ __forceinline__ void cp_piece(uint32_t dst, const void* src) {
+  if constexpr (BYTES == 8) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+  } else {
+#pragma unroll
+    for (int q = 0; q < BYTES / 16; ++q) cp16(dst + 16 * q, static_cast<const char*>(src) + 16 * q, true);
+  }
+}
+template <int N>
+__device__ __forceinline__ void load_piece(const __nv_bfloat16* p, float (&v)[N]) {
+#pragma unroll
+  for (int q = 0; q < N / 4; ++q) {
+    const uint2 u = reinterpret_cast<const uint2*>(p)[q];
+    const float2 a = unpack_bf16x2(u.x), b = unpack_bf16x2(u.y);
+    v[4 * q] = a.x; v[4 * q + 1] = a.y; v[4 * q + 2] = b.x; v[4 * q + 3] = b.y;
+  }
+}
+template <int N>
+__device__ __forceinline__ void load_piece(const float* p, float (&v)[N]) {
+#pragma unroll
+  for (int q = 0; q < N / 4; ++q) {
+    const float4 u = reinterpret_cast<const float4*>(p)[q];
+    v[4 * q] = u.x; v[4 * q + 1] = u.y; v[4 * q + 2] = u.z; v[4 * q + 3] = u.w;
+  }
+}
+template <int N>
+__device__ __forceinline__ void store_piece(__nv_bfloat16* p, const float (&v)[N]) {
+  if constexpr (N == 8) {
+    store8(p, v);
+  } else {
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+  }
+}
+template <int N>
+__device__ __forceinline__ void store_piece(float* p, const float (&v)[N]) {
+#pragma unroll
+  for (int q = 0; q < N / 4; ++q)
+    reinterpret_cast<float4*>(p)[q] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+}
+
+template <typename T, int EP>
+__global__ void __launch_bounds__(kDgThreads) router_dense_small_kernel(const T* __restrict__ x,
+                                                                        const float* __restrict__ Wr,
+                                                                        const float* __restrict__ dl, int64_t L, int d,
+                                                                        int E, int64_t split, T* __restrict__ dx,
+                                                                        float* __restrict__ part,
+                                                                        float* __restrict__ part_b) {
+  constexpr int CPT = dg_cpt<EP>(), PB = CPT * (int)sizeof(T);
+  extern __shared__ __align__(16) uint8_t rsm[];
+  float* ds = reinterpret_cast<float*>(rsm);             // 2 x [64 tokens][EP], experts >= E zero
+  T* xs = reinterpret_cast<T*>(ds + 2 * kRT * EP);       // [kDgAhead][threads][CPT]: each thread's own pieces
+  const int tid = threadIdx.x;
+  const int j = (blockIdx.x * kDgThreads + tid) * CPT;
+  const bool jv = j < d;
+  float2 w[CPT][EP / 2], acc[CPT][EP / 2];
+#pragma unroll
+  for (int c = 0; c < CPT; ++c)
+#pragma unroll
+    for (int e = 0; e < EP / 2; ++e) {
+      acc[c][e] = make_float2(0.f, 0.f);
+      w[c][e].x = jv && 2 * e < E ? Wr[(int64_t)(j + c) * E + 2 * e] : 0.f;
+      w[c][e].y = jv && 2 * e + 1 < E ? Wr[(int64_t)(j + c) * E + 2 * e + 1] : 0.f;
+    }
+  const int64_t ts = (int64_t)blockIdx.y * split, tend = min(L, ts + split);
+  const int n = (int)(tend - ts);  // at least 1: the host makes no empty split
+  auto fetch_x = [&](int t) {
+    if (jv && t < n) cp_piece<PB>(saddr(xs + ((t % kDgAhead) * kDgThreads + tid) * CPT), x + (ts + t) * d + j);
+  };
+  auto stage_dl = [&](int c) {  // rows c*64 .. of the split into buffer c & 1
+    float* dst = ds + (c & 1) * kRT * EP;
+    for (int i = tid; i < kRT * EP; i += kDgThreads) {
+      const int t = c * kRT + i / EP, e = i % EP;
+      const bool ok = t < n && e < E;
+      cp4(saddr(dst + i), ok ? (const void*)(dl + (ts + t) * E + e) : (const void*)dl, ok);
+    }
+  };
+  // copy groups, in order: [dl chunk 0], x pieces 0..AHEAD-1 (one group
+  // each), then per token one group; a chunk's dl joins the group of the
+  // first token of the chunk before it, so it has landed 64 - AHEAD tokens
+  // before it is read
+  stage_dl(0);
+  cp_commit();
+#pragma unroll
+  for (int t = 0; t < kDgAhead; ++t) {
+    fetch_x(t);
+    cp_commit();
+  }
+  float bacc = 0.f;
+  for (int t = 0; t < n; ++t) {
+    cp_wait<kDgAhead - 1>();  // token t's piece and everything committed before it
+    if ((t & (kRT - 1)) == 0) {
+      __syncthreads();  // chunk t/64 has landed for every thread; chunk t/64 - 1 is read
+      const int c = t / kRT + 1;
+      if (c * kRT < n) stage_dl(c);
+      const float* dr = ds + ((t / kRT) & 1) * kRT * EP;
+      if (blockIdx.x == 0 && tid < EP)
+        for (int i = 0; i < min(kRT, n - t); ++i) bacc += dr[i * EP + tid];
+    }
+    float xv[CPT];
+    load_piece(xs + ((t % kDgAhead) * kDgThreads + tid) * CPT, xv);
+    fetch_x(t + kDgAhead);
+    cp_commit();
+    const float4* dr = reinterpret_cast<const float4*>(ds + ((t / kRT) & 1) * kRT * EP + (t & (kRT - 1)) * EP);
+    float2 o[CPT];
+#pragma unroll
+    for (int c = 0; c < CPT; ++c) o[c] = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int q = 0; q < EP / 4; ++q) {
+      const float4 v = dr[q];
+      const float2 a = make_float2(v.x, v.y), b = make_float2(v.z, v.w);
+#pragma unroll
+      for (int c = 0; c < CPT; ++c) {
+        const float2 x2 = make_float2(xv[c], xv[c]);
+        acc[c][2 * q] = __ffma2_rn(x2, a, acc[c][2 * q]);
+        acc[c][2 * q + 1] = __ffma2_rn(x2, b, acc[c][2 * q + 1]);
+        o[c] = __ffma2_rn(a, w[c][2 * q], o[c]);
+        o[c] = __ffma2_rn(b, w[c][2 * q + 1], o[c]);
+      }
+    }
+    if (dx && jv) {
+      float out[CPT];
+#pragma unroll
+      for (int c = 0; c < CPT; ++c) out[c] = o[c].x + o[c].y;
+      store_piece(dx + (ts + t) * d + j, out);
+    }
+  }
+  cp_wait<0>();
+  if (jv) {
+    float* dst = part + ((int64_t)blockIdx.y * d + j) * E;
+#pragma unroll
+    for (int c = 0; c < CPT; ++c)
+#pragma unroll
+      for (int e = 0; e < EP / 2; ++e) {
+        if (2 * e < E) dst[c * E + 2 * e] = acc[c][e].x;
+        if (2 * e + 1 < E) dst[c * E + 2 * e + 1] = acc[c][e].y;
+      }
+  }
+  if (blockIdx.x == 0 && tid < E) part_b[(int64_t)blockIdx.y * E + tid] = bacc;
+}
+
+// More experts: dx in tiles of 64 tokens x 64 columns with the tokens' dl
+// rows and the columns' rows of Wr staged whole (E is the reduction axis)
+template <typename T, int EP>
+__global__ void __launch_bounds__(kRThreads) router_dense_dx_kernel(const float* __restrict__ Wr,
+                                                                    const float* __restrict__ dl, int64_t L, int d,
+                                                                    int E, T* __restrict__ dx) {
+  constexpr int P = EP + 4;  // pitch: rows 1 apart start 4 banks apart, 16-byte multiples
+  extern __shared__ __align__(16) uint8_t rsm[];
+  float* ds = reinterpret_cast<float*>(rsm);  // [64 tokens][P]
+  float* ws = ds + kRT * P;                   // [64 columns][P]
+  const int tid = threadIdx.x, tr = tid >> 4, tc = tid & 15;
+  const int64_t t0 = (int64_t)blockIdx.y * kRT;
+  const int j0 = blockIdx.x * kRT;
+  for (int i = tid; i < kRT * EP; i += kRThreads) {
+    const int r = i / EP, e = i % EP;
+    ds[r * P + e] = e < E && t0 + r < L ? dl[(t0 + r) * E + e] : 0.f;
+    ws[r * P + e] = e < E ? Wr[(int64_t)(j0 + r) * E + e] : 0.f;
+  }
+  __syncthreads();
+  float2 acc[4][4];
+#pragma unroll
+  for (int a = 0; a < 4; ++a)
+#pragma unroll
+    for (int b = 0; b < 4; ++b) acc[a][b] = make_float2(0.f, 0.f);
+#pragma unroll 4
+  for (int e = 0; e < EP; e += 4) {
+    float4 dv[4], wv[4];
+#pragma unroll
+    for (int a = 0; a < 4; ++a) {
+      dv[a] = *reinterpret_cast<const float4*>(ds + (tr + 16 * a) * P + e);
+      wv[a] = *reinterpret_cast<const float4*>(ws + (tc + 16 * a) * P + e);
+    }
+#pragma unroll
+    for (int a = 0; a < 4; ++a)
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        acc[a][b] = __ffma2_rn(make_float2(dv[a].x, dv[a].y), make_float2(wv[b].x, wv[b].y), acc[a][b]);
+        acc[a][b] = __ffma2_rn(make_float2(dv[a].z, dv[a].w), make_float2(wv[b].z, wv[b].w), acc[a][b]);
+      }
+  }
+#pragma unroll
+  for (int a = 0; a < 4; ++a) {
+    const int64_t t = t0 + tr + 16 * a;
+    if (t >= L) continue;
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      const float v = acc[a][b].x + acc[a][b].y;
+      if constexpr (sizeof(T) == 2) dx[t * d + j0 + tc + 16 * b] = __float2bfloat16_rn(v);
+      else dx[t * d + j0 + tc + 16 * b] = v;
+    }
+  }
+}
+
+// and dWr as the partial sums of a token split, 64 rows of Wr per CTA
+template <typename T, int EP>
+__global__ void __launch_bounds__(kRThreads) router_dense_dwr_kernel(const T* __restrict__ x,
+                                                                     const float* __restrict__ dl, int64_t L, int d,
+                                                                     int E, int64_t split, float* __restrict__ part,
+                                                                     float* __restrict__ part_b) {
+  using Ly = RLayout<EP>;
+  constexpr int S = 2, P = XPitch<T>::value, XS = kRT * P;
+  extern __shared__ __align__(16) uint8_t rsm[];
+  T* xs = reinterpret_cast<T*>(rsm);                                // S x [64 tokens][P]
+  float* dd = reinterpret_cast<float*>(rsm + S * XS * sizeof(T));  // S x [64 tokens][EP]
+  const int tid = threadIdx.x, te = tid % Ly::TE, tr = tid / Ly::TE;
+  const int j0 = blockIdx.x * kRT;
+  const int64_t ts = (int64_t)blockIdx.y * split, tend = min(L, ts + split);
+  const int nch = (int)((tend - ts + kRT - 1) / kRT);
+  float acc[Ly::RPT][Ly::EPT];
+#pragma unroll
+  for (int i = 0; i < Ly::RPT; ++i)
+#pragma unroll
+    for (int j = 0; j < Ly::EPT; ++j) acc[i][j] = 0.f;
+  float bacc = 0.f;
+  auto stage = [&](int c) {
+    const int64_t c0 = ts + (int64_t)c * kRT;
+    stage_rows<T>(xs + (c % S) * XS, x, c0, tend, d, j0, tid);
+    float* dst = dd + (c % S) * kRT * EP;
+    for (int i = tid; i < kRT * EP; i += kRThreads) {
+      const int r = i / EP, e = i % EP;
+      const bool ok = c0 + r < tend && e < E;
+      cp4(saddr(dst + i), ok ? (const void*)(dl + (c0 + r) * E + e) : (const void*)dl, ok);
+    }
+  };
+  if (nch > 0) stage(0);
+  cp_commit();
+  for (int c = 0; c < nch; ++c) {
+    cp_wait<0>();
+    __syncthreads();
+    if (c + 1 < nch) stage(c + 1);
+    cp_commit();
+    const T* xa = xs + (c % S) * XS;
+    const float* db = dd + (c % S) * kRT * EP;
+#pragma unroll 4
+    for (int t = 0; t < kRT; ++t) {
+      float av[Ly::RPT], bv[Ly::EPT];
+#pragma unroll
+      for (int i = 0; i < Ly::RPT; ++i) av[i] = to_f32(xa[t * P + tr * Ly::RPT + i]);
+#pragma unroll
+      for (int j = 0; j < Ly::EPT; ++j) bv[j] = db[t * EP + j * Ly::TE + te];
+#pragma unroll
+      for (int i = 0; i < Ly::RPT; ++i)
+#pragma unroll
+        for (int j = 0; j < Ly::EPT; ++j) acc[i][j] = fmaf(av[i], bv[j], acc[i][j]);
+    }
+    if (blockIdx.x == 0 && tid < EP)
+      for (int t = 0; t < kRT; ++t) bacc += db[t * EP + tid];
+  }
+  cp_wait<0>();
+  float* dst = part + (int64_t)blockIdx.y * d * E;
+#pragma unroll
+  for (int i = 0; i < Ly::RPT; ++i)
+#pragma unroll
+    for (int jj = 0; jj < Ly::EPT; ++jj) {
+      const int e = jj * Ly::TE + te;
+      if (e < E) dst[(int64_t)(j0 + tr * Ly::RPT + i) * E + e] = acc[i][jj];
+    }
+  if (blockIdx.x == 0 && tid < E) part_b[(int64_t)blockIdx.y * E + tid] = bacc;
+}
+
 __global__ void router_reduce_kernel(const float* __restrict__ part, const float* __restrict__ part_b, int64_t n,
                                      int E, int S, float* __restrict__ dWr, float* __restrict__ dbias) {
   for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < n + E; i += (int64_t)gridDim.x * blockDim.x) {
@@ -729,7 +1022,7 @@ constexpr size_t kGemvWrBytes = 160 * 1024;  // largest Wr staged whole by the G
 
 template <typename T, int EP>
 moeblaze_status fwd_ep(const moeblaze_shape& s, const void* x, const float* Wr, const float* bias, int32_t* ids,
-                       float* gates, cudaStream_t st) {
+                       float* gates, float* logits, cudaStream_t st) {
   if constexpr (EP <= 16) {
     const size_t wb = ((size_t)s.d * EP + (size_t)s.d / 2) * sizeof(float);
     if (wb <= kGemvWrBytes) {
@@ -738,7 +1031,8 @@ moeblaze_status fwd_ep(const moeblaze_shape& s, const void* x, const float* Wr, 
       const int threads = 512;
       int64_t blocks = (s.L + (threads / 32) * 4 - 1) / ((threads / 32) * 4);
       if (blocks > (int64_t)sm_count()) blocks = sm_count();  // one persistent CTA per SM
-      kern<<<(unsigned)blocks, threads, wb, st>>>(static_cast<const T*>(x), Wr, bias, s.L, s.d, s.E, s.K, ids, gates);
+      kern<<<(unsigned)blocks, threads, wb, st>>>(static_cast<const T*>(x), Wr, bias, s.L, s.d, s.E, s.K, ids, gates,
+                                                  logits);
       MB_CUDA(cudaGetLastError());
       count_launch();
       return MOEBLAZE_OK;
@@ -748,7 +1042,7 @@ moeblaze_status fwd_ep(const moeblaze_shape& s, const void* x, const float* Wr, 
   const size_t sm = fwd_smem<T, EP>();
   MB_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm));
   const unsigned grid = (unsigned)((s.L + kRT - 1) / kRT);
-  kern<<<grid, kRThreads, sm, st>>>(static_cast<const T*>(x), Wr, bias, s.L, s.d, s.E, s.K, ids, gates);
+  kern<<<grid, kRThreads, sm, st>>>(static_cast<const T*>(x), Wr, bias, s.L, s.d, s.E, s.K, ids, gates, logits);
   MB_CUDA(cudaGetLastError());
   count_launch();
   return MOEBLAZE_OK;
@@ -801,14 +1095,14 @@ moeblaze_status bwd_ep(const moeblaze_shape& s, const void* x, const float* Wr, 
 
 template <typename T>
 moeblaze_status fwd_t(const moeblaze_shape& s, const void* x, const float* Wr, const float* bias, int32_t* ids,
-                      float* gates, cudaStream_t st) {
+                      float* gates, float* logits, cudaStream_t st) {
   switch (padded_experts(s.E)) {
-    case 8: return fwd_ep<T, 8>(s, x, Wr, bias, ids, gates, st);
-    case 16: return fwd_ep<T, 16>(s, x, Wr, bias, ids, gates, st);
-    case 32: return fwd_ep<T, 32>(s, x, Wr, bias, ids, gates, st);
-    case 64: return fwd_ep<T, 64>(s, x, Wr, bias, ids, gates, st);
-    case 128: return fwd_ep<T, 128>(s, x, Wr, bias, ids, gates, st);
-    case 256: return fwd_ep<T, 256>(s, x, Wr, bias, ids, gates, st);
+    case 8: return fwd_ep<T, 8>(s, x, Wr, bias, ids, gates, logits, st);
+    case 16: return fwd_ep<T, 16>(s, x, Wr, bias, ids, gates, logits, st);
+    case 32: return fwd_ep<T, 32>(s, x, Wr, bias, ids, gates, logits, st);
+    case 64: return fwd_ep<T, 64>(s, x, Wr, bias, ids, gates, logits, st);
+    case 128: return fwd_ep<T, 128>(s, x, Wr, bias, ids, gates, logits, st);
+    case 256: return fwd_ep<T, 256>(s, x, Wr, bias, ids, gates, logits, st);
   }
   return MOEBLAZE_ERR_UNSUPPORTED;
 }
@@ -828,7 +1122,100 @@ moeblaze_status bwd_t(const moeblaze_shape& s, const void* x, const float* Wr, c
   return MOEBLAZE_ERR_UNSUPPORTED;
 }
 
+// column blocks and token splits of the dense gradient: about three resident
+// CTAs per SM (few experts) or a few waves (more), no empty split
+int64_t dense_col_blocks(const moeblaze_shape& s) {
+  const int ep = padded_experts(s.E);
+  const int cols = ep <= 16 ? kDgThreads * (64 / ep) : kRT;
+  return (s.d + cols - 1) / cols;
+}
+int64_t dense_split(const moeblaze_shape& s) {
+  const int64_t jb = dense_col_blocks(s), per_sm = padded_experts(s.E) <= 16 ? 3 : 4;
+  const int64_t S = (per_sm * sm_count() + jb - 1) / jb;
+  const int64_t rows = (s.L + S - 1) / S;
+  return (rows + kRT - 1) / kRT * kRT;
+}
+int64_t dense_splits(const moeblaze_shape& s) {
+  const int64_t sp = dense_split(s);
+  return sp > 0 ? (s.L + sp - 1) / sp : 0;
+}
+
+template <typename T, int EP>
+moeblaze_status dense_ep(const moeblaze_shape& s, const void* x, const float* Wr, const float* dl, float* dWr,
+                         float* dbias, void* dx, void* ws, cudaStream_t st) {
+  const int64_t split = dense_split(s), S = dense_splits(s);
+  float* part = static_cast<float*>(ws);
+  float* part_b = part + (size_t)S * s.d * s.E;
+  const dim3 grid((unsigned)dense_col_blocks(s), (unsigned)S);
+  if constexpr (EP <= 16) {
+    auto kern = router_dense_small_kernel<T, EP>;
+    const size_t sm = dg_smem<T, EP>();
+    MB_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm));
+    kern<<<grid, kDgThreads, sm, st>>>(static_cast<const T*>(x), Wr, dl, s.L, s.d, s.E, split, static_cast<T*>(dx), part,
+                                       part_b);
+    MB_CUDA(cudaGetLastError());
+    count_launch();
+  } else {
+    if (dx) {
+      auto kern = router_dense_dx_kernel<T, EP>;
+      const size_t sm = 2 * (size_t)kRT * (EP + 4) * sizeof(float);
+      MB_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm));
+      // grid.y is limited to 65535 blocks of 64 tokens
+      const int64_t most = (int64_t)65535 * kRT;
+      for (int64_t t = 0; t < s.L; t += most) {
+        const int64_t n = s.L - t < most ? s.L - t : most;
+        kern<<<dim3((unsigned)(s.d / kRT), (unsigned)((n + kRT - 1) / kRT)), kRThreads, sm, st>>>(
+            Wr, dl + t * s.E, n, s.d, s.E, static_cast<T*>(dx) + t * s.d);
+        MB_CUDA(cudaGetLastError());
+        count_launch();
+      }
+    }
+    auto kern = router_dense_dwr_kernel<T, EP>;
+    const size_t sm = 2 * ((size_t)kRT * XPitch<T>::value * sizeof(T) + (size_t)kRT * EP * sizeof(float));
+    MB_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm));
+    kern<<<grid, kRThreads, sm, st>>>(static_cast<const T*>(x), dl, s.L, s.d, s.E, split, part, part_b);
+    MB_CUDA(cudaGetLastError());
+    count_launch();
+  }
+  const int64_t n = (int64_t)s.d * s.E;
+  int64_t blocks = (n + s.E + 255) / 256;
+  if (blocks > 8 * (int64_t)sm_count()) blocks = 8 * (int64_t)sm_count();
+  router_reduce_kernel<<<(unsigned)blocks, 256, 0, st>>>(part, part_b, n, s.E, (int)S, dWr, dbias);
+  MB_CUDA(cudaGetLastError());
+  count_launch();
+  return MOEBLAZE_OK;
+}
+
+template <typename T>
+moeblaze_status dense_t(const moeblaze_shape& s, const void* x, const float* Wr, const float* dl, float* dWr,
+                        float* dbias, void* dx, void* ws, cudaStream_t st) {
+  switch (padded_experts(s.E)) {
+    case 8: return dense_ep<T, 8>(s, x, Wr, dl, dWr, dbias, dx, ws, st);
+    case 16: return dense_ep<T, 16>(s, x, Wr, dl, dWr, dbias, dx, ws, st);
+    case 32: return dense_ep<T, 32>(s, x, Wr, dl, dWr, dbias, dx, ws, st);
+    case 64: return dense_ep<T, 64>(s, x, Wr, dl, dWr, dbias, dx, ws, st);
+    case 128: return dense_ep<T, 128>(s, x, Wr, dl, dWr, dbias, dx, ws, st);
+    case 256: return dense_ep<T, 256>(s, x, Wr, dl, dWr, dbias, dx, ws, st);
+  }
+  return MOEBLAZE_ERR_UNSUPPORTED;
+}
+
 }  // namespace
+
+size_t router_dense_ws_bytes(const moeblaze_shape& s) {
+  return align_up(sizeof(float) * (size_t)dense_splits(s) * ((size_t)s.d * s.E + s.E), 256);
+}
+
+moeblaze_status launch_router_dense(const moeblaze_shape& s, const void* x, const float* Wr, const float* dl, float* dWr,
+                                    float* dbias, void* dx, void* ws, cudaStream_t st) {
+  if (s.L == 0) {
+    MB_CUDA(cudaMemsetAsync(dWr, 0, sizeof(float) * s.d * s.E, st));
+    if (dbias) MB_CUDA(cudaMemsetAsync(dbias, 0, sizeof(float) * s.E, st));
+    return MOEBLAZE_OK;
+  }
+  return s.dtype == MOEBLAZE_BF16 ? dense_t<__nv_bfloat16>(s, x, Wr, dl, dWr, dbias, dx, ws, st)
+                                  : dense_t<float>(s, x, Wr, dl, dWr, dbias, dx, ws, st);
+}
 
 size_t router_ws_bytes(const moeblaze_shape& s) {
   const int64_t S = router_splits(s);
@@ -836,10 +1223,10 @@ size_t router_ws_bytes(const moeblaze_shape& s) {
 }
 
 moeblaze_status launch_router_forward(const moeblaze_shape& s, const void* x, const float* Wr, const float* bias,
-                                      int32_t* ids, float* gates, cudaStream_t st) {
+                                      int32_t* ids, float* gates, float* logits, cudaStream_t st) {
   if (s.L == 0) return MOEBLAZE_OK;
-  return s.dtype == MOEBLAZE_BF16 ? fwd_t<__nv_bfloat16>(s, x, Wr, bias, ids, gates, st)
-                                  : fwd_t<float>(s, x, Wr, bias, ids, gates, st);
+  return s.dtype == MOEBLAZE_BF16 ? fwd_t<__nv_bfloat16>(s, x, Wr, bias, ids, gates, logits, st)
+                                  : fwd_t<float>(s, x, Wr, bias, ids, gates, logits, st);
 }
 
 moeblaze_status launch_router_backward(const moeblaze_shape& s, const void* x, const float* Wr, const int32_t* ids,

@@ -64,6 +64,7 @@ struct RtParams {
   int d, E, K, kblocks;
   int32_t* ids;
   float* gates;
+  float* logits;  // (L,E) or NULL
   int32_t* D3;
   int32_t* packed;
   int32_t* cnt;
@@ -218,6 +219,11 @@ __global__ void __launch_bounds__(kRtThreads, 1) router_k1_kernel(const __grid_c
       if (valid) {
 #pragma unroll
         for (int e = 0; e < EP; ++e) lg[e] = e < p.E ? lg[e] + (p.bias ? p.bias[e] : 0.f) : -FLT_MAX;
+        if (p.logits) {
+#pragma unroll
+          for (int e = 0; e < EP; ++e)
+            if (e < p.E) p.logits[t * p.E + e] = lg[e];
+        }
         unsigned long long taken = 0ull;
         float selv[kMaxK];
 #pragma unroll
@@ -316,7 +322,7 @@ __global__ void __launch_bounds__(kRtThreads, 1) router_k1_kernel(const __grid_c
 
 template <int EP>
 moeblaze_status launch_ep(const moeblaze_shape& s, const void* x, const float* Wr, const float* bias, int32_t* ids,
-                          float* gates, const moeblaze_dispatch& out, int32_t* packed, int32_t* cnt,
+                          float* gates, float* logits, const moeblaze_dispatch& out, int32_t* packed, int32_t* cnt,
                           __nv_bfloat16* wsplit, cudaStream_t st) {
   constexpr int N = rt_n(EP);
   {
@@ -340,6 +346,7 @@ moeblaze_status launch_ep(const moeblaze_shape& s, const void* x, const float* W
   p.kblocks = s.d / 64;
   p.ids = ids;
   p.gates = gates;
+  p.logits = logits;
   p.D3 = out.token_expert_indices;
   p.packed = packed;
   p.cnt = cnt;
@@ -385,18 +392,18 @@ bool router_dispatch_fused(const moeblaze_shape& s) {
 }
 
 moeblaze_status launch_router_dispatch(const moeblaze_shape& s, const void* x, const float* Wr, const float* bias,
-                                       int32_t* ids, float* gates, const moeblaze_dispatch& out, void* ws,
-                                       cudaStream_t st) {
+                                       int32_t* ids, float* gates, float* logits, const moeblaze_dispatch& out,
+                                       void* ws, cudaStream_t st) {
   int32_t* packed = nullptr;
   int32_t* cnt = nullptr;
   dispatch_ws_parts(s, ws, &packed, &cnt);
   auto* wsplit = reinterpret_cast<__nv_bfloat16*>(static_cast<char*>(ws) + dispatch_ws_bytes(s));
   moeblaze_status r = MOEBLAZE_OK;
   switch (tc::padded_router_experts(s.E)) {
-    case 8: r = tc::launch_ep<8>(s, x, Wr, bias, ids, gates, out, packed, cnt, wsplit, st); break;
-    case 16: r = tc::launch_ep<16>(s, x, Wr, bias, ids, gates, out, packed, cnt, wsplit, st); break;
-    case 32: r = tc::launch_ep<32>(s, x, Wr, bias, ids, gates, out, packed, cnt, wsplit, st); break;
-    default: r = tc::launch_ep<64>(s, x, Wr, bias, ids, gates, out, packed, cnt, wsplit, st); break;
+    case 8: r = tc::launch_ep<8>(s, x, Wr, bias, ids, gates, logits, out, packed, cnt, wsplit, st); break;
+    case 16: r = tc::launch_ep<16>(s, x, Wr, bias, ids, gates, logits, out, packed, cnt, wsplit, st); break;
+    case 32: r = tc::launch_ep<32>(s, x, Wr, bias, ids, gates, logits, out, packed, cnt, wsplit, st); break;
+    default: r = tc::launch_ep<64>(s, x, Wr, bias, ids, gates, logits, out, packed, cnt, wsplit, st); break;
   }
   if (r != MOEBLAZE_OK) return r;
   return launch_dispatch_tail(s, out, ws, st);
