@@ -446,12 +446,12 @@ typedef struct {
  *            outside [0,E) is an empty slot and adds nothing (a token with
  *            none but empty slots gets a row of zeros)
  *   gates    device (L,K) fp32       y device (L,d) bf16, overwritten
- *   ws       device moeblaze_int4_workspace_bytes(s) bytes
+ *   ws       device moeblaze_int4_workspace_bytes(s, group) bytes
  * The weights are read once per 64 tokens: made for L up to a few tens.  Sums
  * are fp32 in a fixed order (repeatable to the bit); the hidden activations
  * are rounded to bf16 between the two products, as the matrix instructions
  * take them. */
-MOEBLAZE_API size_t moeblaze_int4_workspace_bytes(const moeblaze_shape* s);
+MOEBLAZE_API size_t moeblaze_int4_workspace_bytes(const moeblaze_shape* s, int32_t group);
 MOEBLAZE_API moeblaze_status moeblaze_int4_forward(const moeblaze_shape* s, const void* x, const int32_t* topk_ids,
                                                    const float* gates, const moeblaze_int4_experts* w, void* y,
                                                    void* ws, size_t ws_bytes, moeblaze_stream stream);

@@ -117,9 +117,11 @@ def lib():
         L.moeblaze_int4_dequantize.argtypes = [i32, i32, i32, i32, P, P, P, P]
         L.moeblaze_int4_forward.argtypes = [SP, P, P, P, ctypes.POINTER(Int4Weights), P, P, sz, P]
         for n in ["moeblaze_router_backward_logits_workspace_bytes", "moeblaze_balance_workspace_bytes",
-                  "moeblaze_layernorm_backward_workspace_bytes", "moeblaze_int4_workspace_bytes"]:
+                  "moeblaze_layernorm_backward_workspace_bytes"]:
             getattr(L, n).argtypes = [SP]
             getattr(L, n).restype = sz
+        L.moeblaze_int4_workspace_bytes.argtypes = [SP, i32]
+        L.moeblaze_int4_workspace_bytes.restype = sz
         L.moeblaze_int4_weight_bytes.argtypes = [i32, i32, i32]
         L.moeblaze_int4_weight_bytes.restype = sz
         L.moeblaze_int4_scale_bytes.argtypes = [i32, i32, i32, i32]
@@ -279,8 +281,8 @@ def moeblaze_int4_dequantize(E, R, N, group, packed, packed_scales, W, stream) -
     return lib().moeblaze_int4_dequantize(E, R, N, group, packed, packed_scales, W, stream)
 
 
-def moeblaze_int4_workspace_bytes(shape: Shape) -> int:
-    return lib().moeblaze_int4_workspace_bytes(ctypes.byref(shape))
+def moeblaze_int4_workspace_bytes(shape: Shape, group: int) -> int:
+    return lib().moeblaze_int4_workspace_bytes(ctypes.byref(shape), group)
 
 
 def moeblaze_int4_forward(shape, x, topk_ids, gates, weights, y, ws, ws_bytes, stream) -> int:

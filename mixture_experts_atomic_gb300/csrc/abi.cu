@@ -114,7 +114,7 @@ moeblaze_status check_int4_shape(const moeblaze_shape* s, int group) {
   const moeblaze_status r = check_shape(s);
   if (r != MOEBLAZE_OK) return r;
   if (group != 32 && group != 64 && group != 128) return MOEBLAZE_ERR_INVALID_ARG;
-  if (s->act == MOEBLAZE_IDENTITY || s->dtype != MOEBLAZE_BF16 || !int4_shape_ok(*s)) return MOEBLAZE_ERR_UNSUPPORTED;
+  if (s->act == MOEBLAZE_IDENTITY || s->dtype != MOEBLAZE_BF16 || !int4_shape_ok(*s, group)) return MOEBLAZE_ERR_UNSUPPORTED;
   return MOEBLAZE_OK;
 }
 
@@ -543,8 +543,8 @@ moeblaze_status moeblaze_int4_dequantize(int32_t E, int32_t R, int32_t N, int32_
   return launch_int4_dequantize(E, R, N, group, packed, packed_scales, W, reinterpret_cast<cudaStream_t>(stream));
 }
 
-size_t moeblaze_int4_workspace_bytes(const moeblaze_shape* s) {
-  return check_int4_shape(s, 128) == MOEBLAZE_OK ? int4_ws_bytes(*s) : 0;
+size_t moeblaze_int4_workspace_bytes(const moeblaze_shape* s, int32_t group) {
+  return check_int4_shape(s, group) == MOEBLAZE_OK ? int4_ws_bytes(*s, group) : 0;
 }
 
 moeblaze_status moeblaze_int4_forward(const moeblaze_shape* s, const void* x, const int32_t* topk_ids,
@@ -556,7 +556,7 @@ moeblaze_status moeblaze_int4_forward(const moeblaze_shape* s, const void* x, co
   if (!ok_ptr(w->w1) || !ok_ptr(w->s1) || !ok_ptr(w->w3) || !ok_ptr(w->s3)) return MOEBLAZE_ERR_INVALID_ARG;
   if (s->act == MOEBLAZE_SWIGLU && (!ok_ptr(w->w2) || !ok_ptr(w->s2))) return MOEBLAZE_ERR_INVALID_ARG;
   if (s->L > 0 && (!ok_ptr(x) || !ok_ptr(y) || !ok_ptr4(topk_ids) || !ok_ptr4(gates))) return MOEBLAZE_ERR_INVALID_ARG;
-  if (ws_bytes < int4_ws_bytes(*s)) return MOEBLAZE_ERR_WORKSPACE;
+  if (ws_bytes < int4_ws_bytes(*s, w->group)) return MOEBLAZE_ERR_WORKSPACE;
   if (s->L > 0 && !ok_ptr(ws)) return MOEBLAZE_ERR_INVALID_ARG;
   return launch_int4_forward(*s, (const __nv_bfloat16*)x, topk_ids, gates, *w, (__nv_bfloat16*)y, ws,
                              reinterpret_cast<cudaStream_t>(stream));

@@ -22,12 +22,14 @@
 // x fragment of them is 16 consecutive bytes.  In a word, nibbles i and i + 4
 // are the halves of the i-th A register (rows r0, r0 + 1 of column g; the
 // same of g + 8; rows r0 + 2, r0 + 3 of g; of g + 8), biased by 8: masked and
-// or-ed with 0x4300 they are the bf16 numbers 128 + q + 8, exactly, from which
-// 136 is subtracted exactly.  The integer products of a chunk (of 32 rows
-// for groups of 32) are summed in fp32 and the scale is applied to that sum,
-// in fp32.
+// or-ed with 0x4300 they are the bf16 numbers 128 + q + 8, exactly.  The sum
+// over a group starts at -136 sum x (formed once per token and group when
+// the token rows are staged), which takes the bias of all its terms off
+// again: one accumulator start instead of a subtraction per weight.  The
+// group's sum is fp32, and the scale is applied to it in fp32.
 //
-// Scales: [E][N/16][R/group][8][2] bf16, the pair of columns (g, g + 8).
+// Scales: [E][N/16][R/128][8][128/group][2] bf16: column g's and g + 8's
+// scales of 128 rows, the piece a warp reads at a time.
 #include <algorithm>
 
 #include "common.cuh"
@@ -39,15 +41,20 @@ constexpr int kQThreads = 512;
 constexpr int kQWarps = kQThreads / 32;
 constexpr int kQMaxTokens = 64;                    // tokens of one launch
 constexpr int kQMaxPairs = kQMaxTokens * kMaxK;    // (token, slot) pairs of one launch
-constexpr int kQDepth = 8;                         // 512-byte pieces a warp has in flight
+// entries of a warp's ring, each a 128-row piece of a tile of nb matrices
+__host__ __device__ constexpr int ring_depth(int nb) { return nb == 1 ? 4 : 3; }
 constexpr size_t kQSmem = 227 * 1024;
+// ids, list, counts, offsets, pass prefix, scan totals
+constexpr size_t kQIntBytes = 4 * (2 * kQMaxPairs + 3 * kMaxE + 1 + 2 * kQWarps);
 
 __device__ __forceinline__ uint32_t saddr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ void cp4(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+// 4, 8 or 16 bytes
+template <int BYTES>
+__device__ __forceinline__ void cp_small(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -60,15 +67,10 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// the A registers of one k16 step from a packed word
+// the A registers of one k16 step from a packed word: 136 + q
 __device__ __forceinline__ void unpack_word(uint32_t w, uint32_t (&a)[4]) {
-  const __nv_bfloat162 off = __floats2bfloat162_rn(136.f, 136.f);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t v = ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
-    const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v), off);
-    a[i] = *reinterpret_cast<const uint32_t*>(&r);
-  }
+  for (int i = 0; i < 4; ++i) a[i] = ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
 }
 
 // ------------------------------------------------------------------ layouts
@@ -116,23 +118,24 @@ __global__ void int4_pack_kernel(const int8_t* __restrict__ q, int64_t words, in
   }
 }
 
-__global__ void int4_pack_scales_kernel(const __nv_bfloat16* __restrict__ s, int64_t total, int RG, int N,
+// element i of the packed scales: [E][N/16][R/128][8][128/group][2]
+__global__ void int4_pack_scales_kernel(const __nv_bfloat16* __restrict__ s, int64_t total, int RG, int N, int group,
                                         __nv_bfloat16* __restrict__ packed) {
-  const int nt = N / 16;
+  const int nt = N / 16, per = 128 / group;  // groups of a piece
   for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
-    const int c = (int)(i & 15);
-    int64_t r = i >> 4;
-    const int grp = (int)(r % RG);
-    r /= RG;
+    const int hi = (int)(i & 1), j = (int)((i >> 1) % per), g = (int)(i / (2 * per)) & 7;
+    int64_t r = i / (16 * per);
+    const int piece = (int)(r % (RG / per));
+    r /= RG / per;
     const int tile = (int)(r % nt);
     const int64_t e = r / nt;
-    packed[i] = s[(e * RG + grp) * N + tile * 16 + (c >> 1) + 8 * (c & 1)];
+    packed[i] = s[(e * RG + piece * per + j) * N + tile * 16 + g + 8 * hi];
   }
 }
 
 __global__ void int4_dequantize_kernel(const uint32_t* __restrict__ packed, const __nv_bfloat16* __restrict__ ps,
                                        int64_t total, int R, int N, int group, __nv_bfloat16* __restrict__ W) {
-  const int kc = R / 64, nt = N / 16, RG = R / group;
+  const int kc = R / 64, nt = N / 16;
   for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
     const int n = (int)(i % N);
     const int64_t er = i / N;
@@ -142,7 +145,9 @@ __global__ void int4_dequantize_kernel(const uint32_t* __restrict__ packed, cons
     const int chunk = r >> 6, t = (r >> 3) & 3, step = 2 * ((r >> 5) & 1) + ((r >> 2) & 1), a = 2 * ((r >> 1) & 1) + hi, b = r & 1;
     const uint32_t w = packed[((((e * nt + tile) * kc + chunk) * 32) + g * 4 + t) * 4 + step];
     const int q = (int)((w >> (4 * a + 16 * b)) & 15u) - 8;
-    const float s = __bfloat162float(ps[((e * nt + tile) * (int64_t)RG + r / group) * 16 + 2 * g + hi]);
+    const int per = 128 / group;
+    const float s = __bfloat162float(ps[(((e * nt + tile) * (int64_t)(R / 128) + (r >> 7)) * 8 + g) * 2 * per +
+                                        2 * ((r & 127) / group) + hi]);
     W[i] = __float2bfloat16_rn((float)q * s);
   }
 }
@@ -151,14 +156,14 @@ __global__ void int4_dequantize_kernel(const uint32_t* __restrict__ packed, cons
 struct QParams {
   const __nv_bfloat16* src;  // rows of the token operand: x (row = pair / K) or h (row = pair)
   int64_t src_ld;
-  const uint4* w[2];              // packed weights of the branches
-  const uint32_t* s[2];           // their scales, as (g, g + 8) pairs
+  const uint8_t* w[2];       // packed weights of the branches
+  const uint8_t* s[2];       // their packed scales
   const int32_t* ids;
   int pairs, E, K;
   int R, N;                  // reduction length and output columns of the matrices
   int slices;                // the reduction axis in slices of R / slices (UP: 1)
   int cap;                   // token columns of one pass
-  int groupRows;             // rows per scale
+  int rows;                  // token rows that shared memory holds (<= cap)
   __nv_bfloat16* H;          // UP: h (pairs x N)
   float* part;               // else: (slices x pairs x N)
 };
@@ -170,19 +175,20 @@ struct QParams {
 // stream through a ring of cp.async pieces per warp, of which every lane
 // reads back only the bytes it copied itself (no barrier), and which runs on
 // across units and segments.
-template <int NB, int NTL>
+template <int NB, int NTL, int GROUP>
 __global__ void __launch_bounds__(kQThreads, 1) int4_product_kernel(const QParams p) {
-  constexpr int PIECES = kQDepth / NB;  // ring entries: one chunk of every branch
+  constexpr int PIECES = ring_depth(NB);
+  constexpr int SW = 128 / GROUP;                   // groups, and scale words of a lane, in a piece
+  constexpr int BRANCH = 1024 + 128 * SW;           // ring bytes of a piece of one matrix: weights, scale words
+  constexpr int ENTRY = NB * BRANCH;
   extern __shared__ __align__(16) uint8_t qsm[];
-  uint8_t* ring = qsm;                                                    // [warps][PIECES][NB][512]
-  uint32_t* sring = reinterpret_cast<uint32_t*>(ring + (size_t)kQWarps * kQDepth * 512);  // [warps][PIECES][NB][2][32]
-  int* ids_s = reinterpret_cast<int*>(sring + kQWarps * kQDepth * 2 * 32);  // [pairs]
-  int* list = ids_s + kQMaxPairs;                                          // [pairs] by expert, ascending
-  int* cnt = list + kQMaxPairs;                                            // [E]
-  int* off = cnt + kMaxE;                                                  // [E]
-  int* pre = off + kMaxE;                                                  // [E + 1] passes before expert e
-  int* tot = pre + kMaxE + 1;                                              // warp totals of the scans [2][16]
-  uint8_t* xs = reinterpret_cast<uint8_t*>(((uintptr_t)(tot + 2 * kQWarps) + 15) & ~(uintptr_t)15);
+  int* ids_s = reinterpret_cast<int*>(qsm + (size_t)kQWarps * PIECES * ENTRY);  // [pairs]
+  int* list = ids_s + kQMaxPairs;                                               // [pairs] by expert, ascending
+  int* cnt = list + kQMaxPairs;                                                 // [E]
+  int* off = cnt + kMaxE;                                                       // [E]
+  int* pre = off + kMaxE;                                                       // [E + 1] passes before expert e
+  int* tot = pre + kMaxE + 1;                                                   // warp totals of the scans [2][16]
+  uint8_t* xs = qsm + (((size_t)kQWarps * PIECES * ENTRY + kQIntBytes + 15) & ~(size_t)15);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, tq = lane & 3;
 
   // ---- pairs by expert
@@ -215,13 +221,14 @@ __global__ void __launch_bounds__(kQThreads, 1) int4_product_kernel(const QParam
     off[tid] = a - c;
     pre[tid + 1] = b;
     int o = a - c;
-    for (int i = 0; i < p.pairs; ++i)
-      if (ids_s[i] == tid) list[o++] = i;
+    if (c > 0)
+      for (int i = 0; i < p.pairs; ++i)
+        if (ids_s[i] == tid) list[o++] = i;
   }
   if (tid == 0) pre[0] = 0;
   __syncthreads();
 
-  const int nt = p.N / 16, SL = p.R / p.slices, kc = SL / 64, allc = p.R / 64;
+  const int nt = p.N / 16, SL = p.R / p.slices, kp = SL / 128, allp = p.R / 128;
   const int64_t units = (int64_t)pre[p.E] * p.slices * nt;
   const int64_t u0 = units * blockIdx.x / gridDim.x, u1 = units * (blockIdx.x + 1) / gridDim.x;
   if (u0 >= u1) return;
@@ -235,44 +242,44 @@ __global__ void __launch_bounds__(kQThreads, 1) int4_product_kernel(const QParam
     }
     return lo;
   };
-  const int half = p.groupRows == 32;  // two scales per chunk
-  const int RG = p.R / p.groupRows;
 
-  // ---- the fetch head of this warp
+  // ---- the fetch head of this warp: unit, pieces left of it, addresses
+  const uint32_t ring = saddr(qsm) + warp * PIECES * ENTRY + lane * 16;
+  const uint32_t ring_s = saddr(qsm) + warp * PIECES * ENTRY + 1024 + lane * 4 * SW;
   int64_t fu = u0 + warp;
-  int fk = 0, fslot = 0;
-  const uint4* fw[NB];
-  const uint32_t* fs[NB];
-  int fc0 = 0;
+  int left = 0;
+  uint32_t fslot = 0;  // byte offset of the ring entry to fill
+  const uint8_t* fw[NB];
+  const uint8_t* fs[NB];
   auto fetch_unit = [&]() {
     if (fu >= u1) return;
     const int64_t seg = fu / nt;
     const int tile = (int)(fu - seg * nt), e = expert_of((int)(seg / p.slices)), sl = (int)(seg % p.slices);
-    fc0 = sl * kc;
+    const int64_t at = ((int64_t)e * nt + tile) * allp + sl * kp;
 #pragma unroll
     for (int br = 0; br < NB; ++br) {
-      fw[br] = p.w[br] + (((int64_t)e * nt + tile) * allc + fc0) * 32 + lane;
-      fs[br] = p.s[br] + ((int64_t)e * nt + tile) * RG * 8 + g;
+      fw[br] = p.w[br] + at * 1024 + lane * 16;
+      fs[br] = p.s[br] + at * (32 * SW) + g * (4 * SW);
     }
+    left = kp;
   };
   auto fetch = [&]() {
-    if (fu < u1) {
+    if (left > 0) {
 #pragma unroll
       for (int br = 0; br < NB; ++br) {
-        const int at = (warp * PIECES + fslot) * NB + br;
-        cp16(saddr(ring + (size_t)at * 512 + lane * 16), fw[br] + (int64_t)fk * 32);
-        const int row = (fc0 + fk) * 64;
-        cp4(saddr(sring + at * 64 + lane), fs[br] + (row / p.groupRows) * 8);
-        if (half) cp4(saddr(sring + at * 64 + 32 + lane), fs[br] + (row / 32 + 1) * 8);
+        cp16(ring + fslot + br * BRANCH, fw[br]);
+        cp16(ring + fslot + br * BRANCH + 512, fw[br] + 512);
+        cp_small<4 * SW>(ring_s + fslot + br * BRANCH, fs[br]);
+        fw[br] += 1024;
+        fs[br] += 32 * SW;
       }
-      if (++fk == kc) {
-        fk = 0;
+      if (--left == 0) {
         fu += kQWarps;
         fetch_unit();
       }
     }
     cp_commit();
-    if (++fslot == PIECES) fslot = 0;
+    fslot = fslot == (PIECES - 1) * ENTRY ? 0u : fslot + ENTRY;
   };
   fetch_unit();
 #pragma unroll
@@ -280,7 +287,9 @@ __global__ void __launch_bounds__(kQThreads, 1) int4_product_kernel(const QParam
 
   // ---- segments
   const int pitch = SL * 2 + 64;  // rows 16 banks apart: 2 rows x 64 bytes of a fragment load do not conflict
-  int slot = 0;
+  const int groups = SL / GROUP;
+  float* nsx = reinterpret_cast<float*>(xs + (size_t)p.rows * pitch);  // [groups][8 NTL]: -136 sum x
+  uint32_t slot = 0;
   int64_t u = u0 + warp;
   for (int64_t seg = u0 / nt; seg * nt < u1; ++seg) {
     const int pass = (int)(seg / p.slices), sl = (int)(seg % p.slices), e = expert_of(pass);
@@ -298,7 +307,25 @@ __global__ void __launch_bounds__(kQThreads, 1) int4_product_kernel(const QParam
       }
     }
     __syncthreads();
+    for (int i = tid; i < n * groups; i += kQThreads) {
+      const int r = i / groups, gr = i % groups;
+      const uint4* row = reinterpret_cast<const uint4*>(xs + (size_t)r * pitch + gr * (GROUP * 2));
+      float s = 0.f;
+#pragma unroll
+      for (int q = 0; q < GROUP / 8; ++q) {
+        const uint4 v = row[q];
+        const float2 a0 = unpack_bf16x2(v.x), a1 = unpack_bf16x2(v.y), a2 = unpack_bf16x2(v.z), a3 = unpack_bf16x2(v.w);
+        s += ((a0.x + a0.y) + (a1.x + a1.y)) + ((a2.x + a2.y) + (a3.x + a3.y));
+      }
+      nsx[gr * (8 * NTL) + r] = -136.f * s;
+    }
+    __syncthreads();
     const int ntl = (n + 7) / 8;
+    // fragment rows; columns past n repeat the last token: no column of the
+    // product sees another, and those are not stored
+    const uint8_t* xrow[NTL];
+#pragma unroll
+    for (int i = 0; i < NTL; ++i) xrow[i] = xs + (size_t)min(8 * i + g, n - 1) * pitch + tq * 16;
     const int64_t send = min((seg + 1) * (int64_t)nt, u1);
     for (; u < send; u += kQWarps) {
       float acc[NB][NTL][4];
@@ -308,63 +335,63 @@ __global__ void __launch_bounds__(kQThreads, 1) int4_product_kernel(const QParam
         for (int i = 0; i < NTL; ++i)
 #pragma unroll
           for (int v = 0; v < 4; ++v) acc[br][i][v] = 0.f;
-      for (int k = 0; k < kc; ++k) {
+#pragma unroll 1
+      for (int k = 0; k < kp; ++k) {
         cp_wait<PIECES - 2>();
-        uint4 wv[NB];
-        uint32_t sc[NB][2];
+        uint4 wv[NB][2];
+        uint32_t sc[NB][SW];
 #pragma unroll
         for (int br = 0; br < NB; ++br) {
-          const int at = (warp * PIECES + slot) * NB + br;
-          wv[br] = *reinterpret_cast<const uint4*>(ring + (size_t)at * 512 + lane * 16);
-          sc[br][0] = sring[at * 64 + lane];
-          sc[br][1] = half ? sring[at * 64 + 32 + lane] : 0u;
+          const uint8_t* at = qsm + warp * PIECES * ENTRY + slot + br * BRANCH;
+          wv[br][0] = *reinterpret_cast<const uint4*>(at + lane * 16);
+          wv[br][1] = *reinterpret_cast<const uint4*>(at + 512 + lane * 16);
+#pragma unroll
+          for (int j = 0; j < SW; ++j) sc[br][j] = reinterpret_cast<const uint32_t*>(at + 1024)[lane * SW + j];
         }
-        if (++slot == PIECES) slot = 0;
+        slot = slot == (PIECES - 1) * ENTRY ? 0u : slot + ENTRY;
         fetch();
-        uint4 xa[NTL], xb[NTL];  // 8 reduction rows of each half chunk, token 8 i + g
+        float part[NB][NTL][4];
 #pragma unroll
-        for (int i = 0; i < NTL; ++i) {
-          xa[i] = xb[i] = make_uint4(0u, 0u, 0u, 0u);
-          if (8 * i + g < n) {
-            const uint4* row = reinterpret_cast<const uint4*>(xs + (size_t)(8 * i + g) * pitch + k * 128 + tq * 16);
-            xa[i] = row[0];
-            xb[i] = row[4];
-          }
-        }
-#pragma unroll
-        for (int br = 0; br < NB; ++br) {
-          float part[NTL][4];
-#pragma unroll
-          for (int i = 0; i < NTL; ++i)
-#pragma unroll
-            for (int v = 0; v < 4; ++v) part[i][v] = 0.f;
-          const uint32_t words[4] = {wv[br].x, wv[br].y, wv[br].z, wv[br].w};
-          auto scale = [&](uint32_t s2) {
-            const float2 s = unpack_bf16x2(s2);
+        for (int hw = 0; hw < 4; ++hw) {  // 32 rows: two words of a lane, 16 bytes of a token
+          if ((hw * 32) % GROUP == 0) {
 #pragma unroll
             for (int i = 0; i < NTL; ++i) {
-              acc[br][i][0] = fmaf(part[i][0], s.x, acc[br][i][0]);
-              acc[br][i][1] = fmaf(part[i][1], s.x, acc[br][i][1]);
-              acc[br][i][2] = fmaf(part[i][2], s.y, acc[br][i][2]);
-              acc[br][i][3] = fmaf(part[i][3], s.y, acc[br][i][3]);
+              const float2 s2 = *reinterpret_cast<const float2*>(
+                  nsx + (k * SW + hw * 32 / GROUP) * (8 * NTL) + 8 * i + 2 * tq);
 #pragma unroll
-              for (int v = 0; v < 4; ++v) part[i][v] = 0.f;
-            }
-          };
-#pragma unroll
-          for (int st = 0; st < 4; ++st) {
-            uint32_t A[4];
-            unpack_word(words[st], A);
-#pragma unroll
-            for (int i = 0; i < NTL; ++i) {
-              if (i < ntl) {
-                const uint4 x4 = st < 2 ? xa[i] : xb[i];
-                mma16816(part[i], A, (st & 1) ? x4.z : x4.x, (st & 1) ? x4.w : x4.y);
+              for (int br = 0; br < NB; ++br) {
+                part[br][i][0] = part[br][i][2] = s2.x;
+                part[br][i][1] = part[br][i][3] = s2.y;
               }
             }
-            if (st == 1 && half) scale(sc[br][0]);
           }
-          scale(sc[br][half]);
+          uint4 xv[NTL];
+#pragma unroll
+          for (int i = 0; i < NTL; ++i)
+            if (i < ntl) xv[i] = *reinterpret_cast<const uint4*>(xrow[i] + k * 256 + hw * 64);
+#pragma unroll
+          for (int br = 0; br < NB; ++br) {
+            const uint4 w4 = wv[br][hw >> 1];
+            uint32_t A[4];
+            unpack_word((hw & 1) ? w4.z : w4.x, A);
+#pragma unroll
+            for (int i = 0; i < NTL; ++i)
+              if (i < ntl) mma16816(part[br][i], A, xv[i].x, xv[i].y);
+            unpack_word((hw & 1) ? w4.w : w4.y, A);
+#pragma unroll
+            for (int i = 0; i < NTL; ++i)
+              if (i < ntl) mma16816(part[br][i], A, xv[i].z, xv[i].w);
+            if (((hw + 1) * 32) % GROUP == 0) {
+              const float2 s = unpack_bf16x2(sc[br][hw * 32 / GROUP]);
+#pragma unroll
+              for (int i = 0; i < NTL; ++i) {
+                acc[br][i][0] = fmaf(part[br][i][0], s.x, acc[br][i][0]);
+                acc[br][i][1] = fmaf(part[br][i][1], s.x, acc[br][i][1]);
+                acc[br][i][2] = fmaf(part[br][i][2], s.y, acc[br][i][2]);
+                acc[br][i][3] = fmaf(part[br][i][3], s.y, acc[br][i][3]);
+              }
+            }
+          }
         }
       }
       // ---- this lane: columns n = 16 tile + g and + 8, tokens 8 i + 2 tq and + 1
@@ -413,19 +440,26 @@ __global__ void int4_combine_kernel(const float* __restrict__ part, const int32_
   *reinterpret_cast<uint2*>(y + (int64_t)t * d + c) = make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
 }
 
-// shared memory besides the token rows
-constexpr size_t kQFixed = (size_t)kQWarps * kQDepth * (512 + 256) + 4 * (2 * kQMaxPairs + 3 * kMaxE + 1 + 2 * kQWarps) + 16;
+// shared memory besides the token rows: the ring of a launch on nb matrices
+size_t ring_bytes(int nb, int group) { return (size_t)kQWarps * ring_depth(nb) * nb * (1024 + 128 * (128 / group)); }
+size_t fixed_bytes(int nb, int group) { return align_up(ring_bytes(nb, group) + kQIntBytes, 16); }
+// token columns are padded to whole MMAs in the table of group sums
+int pad_cols(int cols) { return cols <= 8 ? 8 : cols <= 16 ? 16 : 32; }
+size_t token_bytes(int64_t len, int group, int rows) {
+  return (size_t)rows * (len * 2 + 64) + (size_t)(len / group) * pad_cols(rows) * sizeof(float);
+}
 
 // token columns of one pass over an expert: up to 32, as many rows of `len`
 // elements as shared memory holds
-int pass_cap(int64_t len) {
-  const int64_t rows = (int64_t)(kQSmem - kQFixed) / (len * 2 + 64);
-  return rows >= 32 ? 32 : (int)rows;
+int pass_cap(int64_t len, int nb, int group) {
+  int rows = 32;
+  while (rows > 0 && fixed_bytes(nb, group) + token_bytes(len, group, rows) > kQSmem) --rows;
+  return rows;
 }
 
 // slices of the down projection's reduction axis: enough units for every
 // warp of the GPU, slices of whole 128-row blocks
-int down_slices(const moeblaze_shape& s, int tokens) {
+int down_slices(const moeblaze_shape& s, int group, int tokens) {
   const int blocks = s.h / 128;
   const int64_t used = std::min<int64_t>(s.E, (int64_t)tokens * s.K);
   const int64_t units = used * (s.d / 16);
@@ -435,7 +469,7 @@ int down_slices(const moeblaze_shape& s, int tokens) {
     if (blocks % n) continue;
     best = n;
     const int64_t len = s.h / n;
-    if (units * n >= want && (pass_cap(len) >= std::min(tokens, 32) || len <= 1024)) break;
+    if (units * n >= want && (pass_cap(len, 1, group) >= std::min(tokens, 32) || len <= 1024)) break;
     if (len <= 512) break;
   }
   return best;
@@ -445,11 +479,12 @@ size_t h_bytes(const moeblaze_shape& s, int tokens) {
   return align_up((size_t)tokens * s.K * s.h * 2, 256);
 }
 
-template <int NB>
-moeblaze_status launch_product(const QParams& p, int tokens, cudaStream_t st) {
-  const int cap8 = std::min(p.cap, (tokens + 7) / 8 * 8);
-  const int rows = std::min(p.cap, tokens);
-  const size_t sm = kQFixed + (size_t)rows * (p.R / p.slices * 2 + 64);
+template <int NB, int GROUP>
+moeblaze_status launch_product_g(QParams p, int tokens, cudaStream_t st) {
+  const int64_t len = p.R / p.slices;
+  p.cap = pass_cap(len, NB, GROUP);
+  p.rows = std::min(p.cap, tokens);
+  const size_t sm = fixed_bytes(NB, GROUP) + token_bytes(len, GROUP, p.rows);
   auto run = [&](auto kern) -> moeblaze_status {
     MB_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm));
     kern<<<sm_count(), kQThreads, sm, st>>>(p);
@@ -457,23 +492,36 @@ moeblaze_status launch_product(const QParams& p, int tokens, cudaStream_t st) {
     count_launch();
     return MOEBLAZE_OK;
   };
-  if (cap8 <= 8) return run(int4_product_kernel<NB, 1>);
-  if (cap8 <= 16) return run(int4_product_kernel<NB, 2>);
-  return run(int4_product_kernel<NB, 4>);
+  switch (pad_cols(p.rows)) {
+    case 8: return run(int4_product_kernel<NB, 1, GROUP>);
+    case 16: return run(int4_product_kernel<NB, 2, GROUP>);
+  }
+  return run(int4_product_kernel<NB, 4, GROUP>);
+}
+
+template <int NB>
+moeblaze_status launch_product(const QParams& p, int group, int tokens, cudaStream_t st) {
+  switch (group) {
+    case 32: return launch_product_g<NB, 32>(p, tokens, st);
+    case 64: return launch_product_g<NB, 64>(p, tokens, st);
+  }
+  return launch_product_g<NB, 128>(p, tokens, st);
 }
 
 }  // namespace
 
-bool int4_shape_ok(const moeblaze_shape& s) { return pass_cap(s.d) >= 1; }
+bool int4_shape_ok(const moeblaze_shape& s, int group) {
+  return pass_cap(s.d, s.act == MOEBLAZE_SWIGLU ? 2 : 1, group) >= 1;
+}
 
-size_t int4_ws_bytes(const moeblaze_shape& s) {
+size_t int4_ws_bytes(const moeblaze_shape& s, int group) {
   const int tokens = (int)std::min<int64_t>(s.L, kQMaxTokens);
   if (tokens == 0) return 0;
   // the slices depend on the tokens of a launch: the last one may have fewer
   size_t most = 0;
   for (const int t : {tokens, (int)(s.L % kQMaxTokens)}) {
     if (t == 0) continue;
-    most = std::max(most, (size_t)down_slices(s, t) * t * s.K * s.d * sizeof(float));
+    most = std::max(most, (size_t)down_slices(s, group, t) * t * s.K * s.d * sizeof(float));
   }
   return h_bytes(s, tokens) + align_up(most, 256);
 }
@@ -489,10 +537,10 @@ moeblaze_status launch_int4_forward(const moeblaze_shape& s, const __nv_bfloat16
     QParams p = {};
     p.src = x + t0 * s.d;
     p.src_ld = s.d;
-    p.w[0] = static_cast<const uint4*>(w.w1);
-    p.s[0] = static_cast<const uint32_t*>(w.s1);
-    p.w[1] = static_cast<const uint4*>(w.w2);
-    p.s[1] = static_cast<const uint32_t*>(w.s2);
+    p.w[0] = static_cast<const uint8_t*>(w.w1);
+    p.s[0] = static_cast<const uint8_t*>(w.s1);
+    p.w[1] = static_cast<const uint8_t*>(w.w2);
+    p.s[1] = static_cast<const uint8_t*>(w.s2);
     p.ids = ids + t0 * s.K;
     p.pairs = tokens * s.K;
     p.E = s.E;
@@ -500,22 +548,19 @@ moeblaze_status launch_int4_forward(const moeblaze_shape& s, const __nv_bfloat16
     p.R = s.d;
     p.N = s.h;
     p.slices = 1;
-    p.cap = pass_cap(s.d);
-    p.groupRows = w.group;
     p.H = H;
-    moeblaze_status r = sw ? launch_product<2>(p, tokens, st) : launch_product<1>(p, tokens, st);
+    moeblaze_status r = sw ? launch_product<2>(p, w.group, tokens, st) : launch_product<1>(p, w.group, tokens, st);
     if (r != MOEBLAZE_OK) return r;
     p.src = H;
     p.src_ld = s.h;
-    p.w[0] = static_cast<const uint4*>(w.w3);
-    p.s[0] = static_cast<const uint32_t*>(w.s3);
+    p.w[0] = static_cast<const uint8_t*>(w.w3);
+    p.s[0] = static_cast<const uint8_t*>(w.s3);
     p.R = s.h;
     p.N = s.d;
-    p.slices = down_slices(s, tokens);
-    p.cap = pass_cap(s.h / p.slices);
+    p.slices = down_slices(s, w.group, tokens);
     p.H = nullptr;
     p.part = part;
-    if ((r = launch_product<1>(p, tokens, st)) != MOEBLAZE_OK) return r;
+    if ((r = launch_product<1>(p, w.group, tokens, st)) != MOEBLAZE_OK) return r;
     const int64_t n = (int64_t)tokens * s.d / 4;
     int4_combine_kernel<<<(unsigned)((n + 127) / 128), 128, 0, st>>>(part, ids + t0 * s.K, gates + t0 * s.K, tokens, s.d,
                                                                    s.E, s.K, p.slices, y + t0 * s.d);
@@ -553,7 +598,7 @@ moeblaze_status launch_int4_pack(int E, int R, int N, int group, const int8_t* q
   int4_pack_kernel<<<flat_grid(words), 256, 0, st>>>(q, words, R, N, static_cast<uint32_t*>(packed));
   MB_CUDA(cudaGetLastError());
   int4_pack_scales_kernel<<<flat_grid(ns), 256, 0, st>>>(static_cast<const __nv_bfloat16*>(scales), ns, R / group, N,
-                                                         static_cast<__nv_bfloat16*>(packed_scales));
+                                                         group, static_cast<__nv_bfloat16*>(packed_scales));
   MB_CUDA(cudaGetLastError());
   count_launch(2);
   return MOEBLAZE_OK;

@@ -116,7 +116,7 @@ def test_int4_status():
     assert B.moeblaze_int4_pack(2, 128, 128, 32, BAD, OKP, OKP, OKP, None) == B.ERR_INVALID_ARG
     assert B.moeblaze_int4_quantize(2, 128, 128, 32, 9, OKP, OKP, OKP, None) == B.ERR_INVALID_ARG
     sh = B.make_shape(4, 256, 384, 8, 2, B.BF16, "swiglu")
-    need = B.moeblaze_int4_workspace_bytes(sh)
+    need = B.moeblaze_int4_workspace_bytes(sh, 64)
     assert need > 0
     P = 0x100000
 
@@ -137,7 +137,7 @@ def test_int4_status():
     for bad in (B.make_shape(4, 256, 384, 8, 2, B.F32, "swiglu"), B.make_shape(4, 256, 0, 8, 2, B.BF16, "identity"),
                 B.make_shape(4, 192, 384, 8, 2, B.BF16, "swiglu")):
         assert fwd(s=bad) == B.ERR_UNSUPPORTED
-        assert B.moeblaze_int4_workspace_bytes(bad) == 0
+        assert B.moeblaze_int4_workspace_bytes(bad, 64) == 0
     assert fwd(s=B.make_shape(0, 256, 384, 8, 2, B.BF16, "silu"), x=None, ids=None, g=None, y=None, ws=None,
                wt=w(w2=None, s2=None)) == B.OK
 
