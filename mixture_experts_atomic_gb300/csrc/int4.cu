@@ -31,6 +31,7 @@
 // Scales: [E][N/16][R/128][8][128/group][2] bf16: column g's and g + 8's
 // scales of 128 rows, the piece a warp reads at a time.
 #include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 
@@ -67,10 +68,13 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// the A registers of one k16 step from a packed word: 136 + q
+// the A registers of one k16 step from a packed word: 136 + q.  One
+// three-input logic operation takes a nibble pair (left to itself the
+// compiler makes it two, and the ALU pipe is what the products wait for).
 __device__ __forceinline__ void unpack_word(uint32_t w, uint32_t (&a)[4]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) a[i] = ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
+  for (int i = 0; i < 4; ++i)
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(a[i]) : "r"(w >> (4 * i)), "r"(0x000F000Fu), "r"(0x43004300u));
 }
 
 // ------------------------------------------------------------------ layouts
@@ -320,99 +324,103 @@ __global__ void __launch_bounds__(kQThreads, 1) int4_product_kernel(const QParam
       nsx[gr * (8 * NTL) + r] = -136.f * s;
     }
     __syncthreads();
-    const int ntl = (n + 7) / 8;
-    // fragment rows; columns past n repeat the last token: no column of the
-    // product sees another, and those are not stored
-    const uint8_t* xrow[NTL];
-#pragma unroll
-    for (int i = 0; i < NTL; ++i) xrow[i] = xs + (size_t)min(8 * i + g, n - 1) * pitch + tq * 16;
     const int64_t send = min((seg + 1) * (int64_t)nt, u1);
-    for (; u < send; u += kQWarps) {
-      float acc[NB][NTL][4];
+    // the segment's units of this warp, for T tiles of 8 token columns
+    auto run_units = [&](auto tiles) {
+      constexpr int T = decltype(tiles)::value;
+      // fragment rows; columns past n repeat the last token: no column of the
+      // product sees another, and those are not stored
+      const uint8_t* xrow[T];
 #pragma unroll
-      for (int br = 0; br < NB; ++br)
+      for (int i = 0; i < T; ++i) xrow[i] = xs + (size_t)min(8 * i + g, n - 1) * pitch + tq * 16;
+      const float* sums = nsx + 2 * tq;
+      for (; u < send; u += kQWarps) {
+        float acc[NB][T][4];
 #pragma unroll
-        for (int i = 0; i < NTL; ++i)
+        for (int br = 0; br < NB; ++br)
 #pragma unroll
-          for (int v = 0; v < 4; ++v) acc[br][i][v] = 0.f;
+          for (int i = 0; i < T; ++i)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) acc[br][i][v] = 0.f;
 #pragma unroll 1
-      for (int k = 0; k < kp; ++k) {
-        cp_wait<PIECES - 2>();
-        uint4 wv[NB][2];
-        uint32_t sc[NB][SW];
-#pragma unroll
-        for (int br = 0; br < NB; ++br) {
-          const uint8_t* at = qsm + warp * PIECES * ENTRY + slot + br * BRANCH;
-          wv[br][0] = *reinterpret_cast<const uint4*>(at + lane * 16);
-          wv[br][1] = *reinterpret_cast<const uint4*>(at + 512 + lane * 16);
-#pragma unroll
-          for (int j = 0; j < SW; ++j) sc[br][j] = reinterpret_cast<const uint32_t*>(at + 1024)[lane * SW + j];
-        }
-        slot = slot == (PIECES - 1) * ENTRY ? 0u : slot + ENTRY;
-        fetch();
-        float part[NB][NTL][4];
-#pragma unroll
-        for (int hw = 0; hw < 4; ++hw) {  // 32 rows: two words of a lane, 16 bytes of a token
-          if ((hw * 32) % GROUP == 0) {
-#pragma unroll
-            for (int i = 0; i < NTL; ++i) {
-              const float2 s2 = *reinterpret_cast<const float2*>(
-                  nsx + (k * SW + hw * 32 / GROUP) * (8 * NTL) + 8 * i + 2 * tq);
-#pragma unroll
-              for (int br = 0; br < NB; ++br) {
-                part[br][i][0] = part[br][i][2] = s2.x;
-                part[br][i][1] = part[br][i][3] = s2.y;
-              }
-            }
-          }
-          uint4 xv[NTL];
-#pragma unroll
-          for (int i = 0; i < NTL; ++i)
-            if (i < ntl) xv[i] = *reinterpret_cast<const uint4*>(xrow[i] + k * 256 + hw * 64);
+        for (int k = 0; k < kp; ++k) {
+          cp_wait<PIECES - 2>();
+          uint4 wv[NB][2];
+          uint32_t sc[NB][SW];
 #pragma unroll
           for (int br = 0; br < NB; ++br) {
-            const uint4 w4 = wv[br][hw >> 1];
-            uint32_t A[4];
-            unpack_word((hw & 1) ? w4.z : w4.x, A);
+            const uint8_t* at = qsm + warp * PIECES * ENTRY + slot + br * BRANCH;
+            wv[br][0] = *reinterpret_cast<const uint4*>(at + lane * 16);
+            wv[br][1] = *reinterpret_cast<const uint4*>(at + 512 + lane * 16);
 #pragma unroll
-            for (int i = 0; i < NTL; ++i)
-              if (i < ntl) mma16816(part[br][i], A, xv[i].x, xv[i].y);
-            unpack_word((hw & 1) ? w4.w : w4.y, A);
+            for (int j = 0; j < SW; ++j) sc[br][j] = reinterpret_cast<const uint32_t*>(at + 1024)[lane * SW + j];
+          }
+          slot = slot == (PIECES - 1) * ENTRY ? 0u : slot + ENTRY;
+          fetch();
+          float part[NB][T][4];
 #pragma unroll
-            for (int i = 0; i < NTL; ++i)
-              if (i < ntl) mma16816(part[br][i], A, xv[i].z, xv[i].w);
-            if (((hw + 1) * 32) % GROUP == 0) {
-              const float2 s = unpack_bf16x2(sc[br][hw * 32 / GROUP]);
+          for (int hw = 0; hw < 4; ++hw) {  // 32 rows: two words of a lane, 16 bytes of a token
+            if ((hw * 32) % GROUP == 0) {
 #pragma unroll
-              for (int i = 0; i < NTL; ++i) {
-                acc[br][i][0] = fmaf(part[br][i][0], s.x, acc[br][i][0]);
-                acc[br][i][1] = fmaf(part[br][i][1], s.x, acc[br][i][1]);
-                acc[br][i][2] = fmaf(part[br][i][2], s.y, acc[br][i][2]);
-                acc[br][i][3] = fmaf(part[br][i][3], s.y, acc[br][i][3]);
+              for (int i = 0; i < T; ++i) {
+                const float2 s2 =
+                    *reinterpret_cast<const float2*>(sums + (k * SW + hw * 32 / GROUP) * (8 * NTL) + 8 * i);
+#pragma unroll
+                for (int br = 0; br < NB; ++br) {
+                  part[br][i][0] = part[br][i][2] = s2.x;
+                  part[br][i][1] = part[br][i][3] = s2.y;
+                }
+              }
+            }
+            uint4 xv[T];
+#pragma unroll
+            for (int i = 0; i < T; ++i) xv[i] = *reinterpret_cast<const uint4*>(xrow[i] + k * 256 + hw * 64);
+#pragma unroll
+            for (int br = 0; br < NB; ++br) {
+              const uint4 w4 = wv[br][hw >> 1];
+              uint32_t A[4];
+              unpack_word((hw & 1) ? w4.z : w4.x, A);
+#pragma unroll
+              for (int i = 0; i < T; ++i) mma16816(part[br][i], A, xv[i].x, xv[i].y);
+              unpack_word((hw & 1) ? w4.w : w4.y, A);
+#pragma unroll
+              for (int i = 0; i < T; ++i) mma16816(part[br][i], A, xv[i].z, xv[i].w);
+              if (((hw + 1) * 32) % GROUP == 0) {
+                const float2 s = unpack_bf16x2(sc[br][hw * 32 / GROUP]);
+#pragma unroll
+                for (int i = 0; i < T; ++i) {
+                  acc[br][i][0] = fmaf(part[br][i][0], s.x, acc[br][i][0]);
+                  acc[br][i][1] = fmaf(part[br][i][1], s.x, acc[br][i][1]);
+                  acc[br][i][2] = fmaf(part[br][i][2], s.y, acc[br][i][2]);
+                  acc[br][i][3] = fmaf(part[br][i][3], s.y, acc[br][i][3]);
+                }
               }
             }
           }
         }
-      }
-      // ---- this lane: columns n = 16 tile + g and + 8, tokens 8 i + 2 tq and + 1
-      const int col = (int)(u - seg * nt) * 16 + g;
+        // ---- this lane: columns n = 16 tile + g and + 8, tokens 8 i + 2 tq and + 1
+        const int col = (int)(u - seg * nt) * 16 + g;
 #pragma unroll
-      for (int i = 0; i < NTL; ++i)
+        for (int i = 0; i < T; ++i)
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          const int tk = 8 * i + 2 * tq + (v & 1), cc = col + 8 * (v >> 1);
-          if (tk >= n) continue;
-          const int pair = list[first + tk];
-          if (p.H) {
-            const float av = acc[0][i][v];
-            float hv = av / (1.f + expf(-av));
-            if constexpr (NB == 2) hv *= acc[NB - 1][i][v];
-            p.H[(int64_t)pair * p.N + cc] = __float2bfloat16_rn(hv);
-          } else {
-            p.part[((int64_t)sl * p.pairs + pair) * p.N + cc] = acc[0][i][v];
+          for (int v = 0; v < 4; ++v) {
+            const int tk = 8 * i + 2 * tq + (v & 1), cc = col + 8 * (v >> 1);
+            if (tk >= n) continue;
+            const int pair = list[first + tk];
+            if (p.H) {
+              const float av = acc[0][i][v];
+              float hv = av / (1.f + expf(-av));
+              if constexpr (NB == 2) hv *= acc[NB - 1][i][v];
+              p.H[(int64_t)pair * p.N + cc] = __float2bfloat16_rn(hv);
+            } else {
+              p.part[((int64_t)sl * p.pairs + pair) * p.N + cc] = acc[0][i][v];
+            }
           }
-        }
-    }
+      }
+    };
+    if (NTL == 1 || n <= 8) run_units(std::integral_constant<int, 1>());
+    else if (NTL == 2 || n <= 16) run_units(std::integral_constant<int, (NTL < 2 ? NTL : 2)>());
+    else run_units(std::integral_constant<int, NTL>());
   }
   cp_wait<0>();
 }
