@@ -40,13 +40,15 @@ namespace {
 
 constexpr int kQThreads = 512;
 constexpr int kQWarps = kQThreads / 32;
+constexpr int kQTeam = 4;                          // warps that share a unit's reduction rows
+constexpr int kQTeams = kQWarps / kQTeam;
 constexpr int kQMaxTokens = 64;                    // tokens of one launch
 constexpr int kQMaxPairs = kQMaxTokens * kMaxK;    // (token, slot) pairs of one launch
 // entries of a warp's ring, each a 128-row piece of a tile of nb matrices
 __host__ __device__ constexpr int ring_depth(int nb) { return nb == 1 ? 4 : 3; }
 constexpr size_t kQSmem = 227 * 1024;
-// ids, list, counts, offsets, pass prefix, scan totals
-constexpr size_t kQIntBytes = 4 * (2 * kQMaxPairs + 3 * kMaxE + 1 + 2 * kQWarps);
+// list, counts, offsets, pass prefix, scan totals
+constexpr size_t kQIntBytes = 4 * (kQMaxPairs + 3 * kMaxE + 1 + 2 * kQWarps);
 
 __device__ __forceinline__ uint32_t saddr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
@@ -75,6 +77,11 @@ __device__ __forceinline__ void unpack_word(uint32_t w, uint32_t (&a)[4]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(a[i]) : "r"(w >> (4 * i)), "r"(0x000F000Fu), "r"(0x43004300u));
+}
+
+// barrier of one team of warps (barrier 0 is the CTA's)
+__device__ __forceinline__ void team_sync(int team) {
+  asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "n"(kQTeam * 32) : "memory");
 }
 
 // ------------------------------------------------------------------ layouts
@@ -174,11 +181,14 @@ struct QParams {
 
 // Work: segments (expert in use, pass of `cap` of its pairs, slice), each
 // with N / 16 tiles; the units (segment, tile) are split evenly and
-// contiguously over the CTAs, and a CTA's units go round its warps.  A
+// contiguously over the CTAs, and a CTA's units go round its teams of four
+// warps, which share a unit's reduction rows: a CTA's last round then costs a
+// quarter of a unit's time, and few units still keep every warp loading.  A
 // segment's token rows are staged in shared memory; the packed weights
 // stream through a ring of cp.async pieces per warp, of which every lane
 // reads back only the bytes it copied itself (no barrier), and which runs on
-// across units and segments.
+// across units and segments.  The team's sums meet in shared memory, in the
+// order of its warps.
 template <int NB, int NTL, int GROUP>
 __global__ void __launch_bounds__(kQThreads, 1) int4_product_kernel(const QParams p) {
   constexpr int PIECES = ring_depth(NB);
@@ -186,56 +196,74 @@ __global__ void __launch_bounds__(kQThreads, 1) int4_product_kernel(const QParam
   constexpr int BRANCH = 1024 + 128 * SW;           // ring bytes of a piece of one matrix: weights, scale words
   constexpr int ENTRY = NB * BRANCH;
   extern __shared__ __align__(16) uint8_t qsm[];
-  int* ids_s = reinterpret_cast<int*>(qsm + (size_t)kQWarps * PIECES * ENTRY);  // [pairs]
-  int* list = ids_s + kQMaxPairs;                                               // [pairs] by expert, ascending
-  int* cnt = list + kQMaxPairs;                                                 // [E]
-  int* off = cnt + kMaxE;                                                       // [E]
-  int* pre = off + kMaxE;                                                       // [E + 1] passes before expert e
-  int* tot = pre + kMaxE + 1;                                                   // warp totals of the scans [2][16]
-  uint8_t* xs = qsm + (((size_t)kQWarps * PIECES * ENTRY + kQIntBytes + 15) & ~(size_t)15);
+  int* list = reinterpret_cast<int*>(qsm + (size_t)kQWarps * PIECES * ENTRY);  // [pairs] by expert, ascending
+  int* cnt = list + kQMaxPairs;                                                // [E]
+  int* off = cnt + kMaxE;                                                      // [E]
+  int* pre = off + kMaxE;                                                      // [E + 1] passes before expert e
+  int* tot = pre + kMaxE + 1;                                                  // warp totals of the scans [2][16]
+  float* swap = reinterpret_cast<float*>(qsm + (((size_t)kQWarps * PIECES * ENTRY + kQIntBytes + 15) & ~(size_t)15));
+  uint8_t* xs = reinterpret_cast<uint8_t*>(swap + kQWarps * NB * 128);         // swap: [warps][NB][4][32]
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, tq = lane & 3;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the next kernel's CTAs may take freed SMs
 
-  // ---- pairs by expert
-  for (int i = tid; i < p.pairs; i += kQThreads) ids_s[i] = p.ids[i];
-  __syncthreads();
-  int c = 0;
-  if (tid < p.E)
-    for (int i = 0; i < p.pairs; ++i) c += ids_s[i] == tid;
-  int np = (c + p.cap - 1) / p.cap;
-  int a = c, b = np;
+  // ---- pairs by expert: thread i ranks pair i among its warp's pairs of the
+  // same expert; per-warp counts (in the ring, which is still empty) order the warps
+  {
+    uint16_t* tbl = reinterpret_cast<uint16_t*>(qsm);  // [warps][E]
+    for (int i = tid; i < kQWarps * p.E / 2; i += kQThreads) reinterpret_cast<uint32_t*>(tbl)[i] = 0u;
+    int id = tid < p.pairs ? p.ids[tid] : -1;
+    if ((unsigned)id >= (unsigned)p.E) id = -1;
+    __syncthreads();
+    const uint32_t same = __match_any_sync(0xffffffffu, id);
+    const int rank = __popc(same & ((1u << lane) - 1u));
+    if (id >= 0 && rank == 0) tbl[warp * p.E + id] = (uint16_t)__popc(same);
+    __syncthreads();
+    int c = 0;
+    if (tid < p.E) {
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int ua = __shfl_up_sync(0xffffffffu, a, o), ub = __shfl_up_sync(0xffffffffu, b, o);
-    if (lane >= o) {
-      a += ua;
-      b += ub;
+      for (int w = 0; w < kQWarps; ++w) {
+        const int v = tbl[w * p.E + tid];
+        tbl[w * p.E + tid] = (uint16_t)c;
+        c += v;
+      }
     }
+    int a = c, b = (c + p.cap - 1) / p.cap;
+    const int passes = b;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int ua = __shfl_up_sync(0xffffffffu, a, o), ub = __shfl_up_sync(0xffffffffu, b, o);
+      if (lane >= o) {
+        a += ua;
+        b += ub;
+      }
+    }
+    if (lane == 31) {
+      tot[warp] = a;
+      tot[kQWarps + warp] = b;
+    }
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) {
+      a += tot[w];
+      b += tot[kQWarps + w];
+    }
+    if (tid < p.E) {
+      cnt[tid] = c;
+      off[tid] = a - c;
+      pre[tid] = b - passes;
+      if (tid == p.E - 1) pre[p.E] = b;
+    }
+    __syncthreads();
+    if (id >= 0) list[off[id] + tbl[warp * p.E + id] + rank] = tid;
+    __syncthreads();
   }
-  if (lane == 31) {
-    tot[warp] = a;
-    tot[kQWarps + warp] = b;
-  }
-  __syncthreads();
-  for (int w = 0; w < warp; ++w) {
-    a += tot[w];
-    b += tot[kQWarps + w];
-  }
-  if (tid < p.E) {
-    cnt[tid] = c;
-    off[tid] = a - c;
-    pre[tid + 1] = b;
-    int o = a - c;
-    if (c > 0)
-      for (int i = 0; i < p.pairs; ++i)
-        if (ids_s[i] == tid) list[o++] = i;
-  }
-  if (tid == 0) pre[0] = 0;
-  __syncthreads();
 
   const int nt = p.N / 16, SL = p.R / p.slices, kp = SL / 128, allp = p.R / 128;
   const int64_t units = (int64_t)pre[p.E] * p.slices * nt;
   const int64_t u0 = units * blockIdx.x / gridDim.x, u1 = units * (blockIdx.x + 1) / gridDim.x;
-  if (u0 >= u1) return;
+  if (u0 >= u1) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    return;
+  }
   // the expert of pass i: the last e with pre[e] <= i
   auto expert_of = [&](int i) {
     int lo = 0, hi = p.E;
@@ -250,22 +278,24 @@ __global__ void __launch_bounds__(kQThreads, 1) int4_product_kernel(const QParam
   // ---- the fetch head of this warp: unit, pieces left of it, addresses
   const uint32_t ring = saddr(qsm) + warp * PIECES * ENTRY + lane * 16;
   const uint32_t ring_s = saddr(qsm) + warp * PIECES * ENTRY + 1024 + lane * 4 * SW;
-  int64_t fu = u0 + warp;
+  const int team = warp / kQTeam, mate = warp % kQTeam;
+  const int k0 = kp * mate / kQTeam, k1 = kp * (mate + 1) / kQTeam;  // this warp's pieces of a unit
+  int64_t fu = u0 + team;
   int left = 0;
   uint32_t fslot = 0;  // byte offset of the ring entry to fill
   const uint8_t* fw[NB];
   const uint8_t* fs[NB];
   auto fetch_unit = [&]() {
-    if (fu >= u1) return;
+    if (fu >= u1 || k0 == k1) return;
     const int64_t seg = fu / nt;
     const int tile = (int)(fu - seg * nt), e = expert_of((int)(seg / p.slices)), sl = (int)(seg % p.slices);
-    const int64_t at = ((int64_t)e * nt + tile) * allp + sl * kp;
+    const int64_t at = ((int64_t)e * nt + tile) * allp + sl * kp + k0;
 #pragma unroll
     for (int br = 0; br < NB; ++br) {
       fw[br] = p.w[br] + at * 1024 + lane * 16;
       fs[br] = p.s[br] + at * (32 * SW) + g * (4 * SW);
     }
-    left = kp;
+    left = k1 - k0;
   };
   auto fetch = [&]() {
     if (left > 0) {
@@ -278,7 +308,7 @@ __global__ void __launch_bounds__(kQThreads, 1) int4_product_kernel(const QParam
         fs[br] += 32 * SW;
       }
       if (--left == 0) {
-        fu += kQWarps;
+        fu += kQTeams;
         fetch_unit();
       }
     }
@@ -288,13 +318,17 @@ __global__ void __launch_bounds__(kQThreads, 1) int4_product_kernel(const QParam
   fetch_unit();
 #pragma unroll
   for (int i = 0; i < PIECES - 1; ++i) fetch();
+  // everything so far reads the routing and the weights, which the caller
+  // provides; the rows staged below are the kernel before's (the down
+  // projection's: h)
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 
   // ---- segments
   const int pitch = SL * 2 + 64;  // rows 16 banks apart: 2 rows x 64 bytes of a fragment load do not conflict
   const int groups = SL / GROUP;
   float* nsx = reinterpret_cast<float*>(xs + (size_t)p.rows * pitch);  // [groups][8 NTL]: -136 sum x
   uint32_t slot = 0;
-  int64_t u = u0 + warp;
+  int64_t u = u0 + team;
   for (int64_t seg = u0 / nt; seg * nt < u1; ++seg) {
     const int pass = (int)(seg / p.slices), sl = (int)(seg % p.slices), e = expert_of(pass);
     const int first = off[e] + (pass - pre[e]) * p.cap;
@@ -325,7 +359,7 @@ __global__ void __launch_bounds__(kQThreads, 1) int4_product_kernel(const QParam
     }
     __syncthreads();
     const int64_t send = min((seg + 1) * (int64_t)nt, u1);
-    // the segment's units of this warp, for T tiles of 8 token columns
+    // the segment's units of this team, for T tiles of 8 token columns
     auto run_units = [&](auto tiles) {
       constexpr int T = decltype(tiles)::value;
       // fragment rows; columns past n repeat the last token: no column of the
@@ -334,7 +368,7 @@ __global__ void __launch_bounds__(kQThreads, 1) int4_product_kernel(const QParam
 #pragma unroll
       for (int i = 0; i < T; ++i) xrow[i] = xs + (size_t)min(8 * i + g, n - 1) * pitch + tq * 16;
       const float* sums = nsx + 2 * tq;
-      for (; u < send; u += kQWarps) {
+      for (; u < send; u += kQTeams) {
         float acc[NB][T][4];
 #pragma unroll
         for (int br = 0; br < NB; ++br)
@@ -343,7 +377,7 @@ __global__ void __launch_bounds__(kQThreads, 1) int4_product_kernel(const QParam
 #pragma unroll
             for (int v = 0; v < 4; ++v) acc[br][i][v] = 0.f;
 #pragma unroll 1
-        for (int k = 0; k < kp; ++k) {
+        for (int k = k0; k < k1; ++k) {
           cp_wait<PIECES - 2>();
           uint4 wv[NB][2];
           uint32_t sc[NB][SW];
@@ -398,24 +432,38 @@ __global__ void __launch_bounds__(kQThreads, 1) int4_product_kernel(const QParam
             }
           }
         }
-        // ---- this lane: columns n = 16 tile + g and + 8, tokens 8 i + 2 tq and + 1
-        const int col = (int)(u - seg * nt) * 16 + g;
+        // ---- the team's sums of 8 token columns at a time: accumulator v of
+        // a lane is column n = 16 tile + g + 8 (v / 2), token 8 i + 2 tq + v % 2;
+        // warp v of the team adds up and stores accumulator v
 #pragma unroll
-        for (int i = 0; i < T; ++i)
+        for (int i = 0; i < T; ++i) {
+          if (i > 0) team_sync(team);  // the tile before is read
 #pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            const int tk = 8 * i + 2 * tq + (v & 1), cc = col + 8 * (v >> 1);
-            if (tk >= n) continue;
+          for (int br = 0; br < NB; ++br)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) swap[((warp * NB + br) * 4 + v) * 32 + lane] = acc[br][i][v];
+          team_sync(team);
+          float sum[NB];
+#pragma unroll
+          for (int br = 0; br < NB; ++br) {
+            sum[br] = 0.f;
+#pragma unroll
+            for (int w = 0; w < kQTeam; ++w)
+              sum[br] += swap[(((team * kQTeam + w) * NB + br) * 4 + mate) * 32 + lane];
+          }
+          const int tk = 8 * i + 2 * tq + (mate & 1), col = (int)(u - seg * nt) * 16 + g + 8 * (mate >> 1);
+          if (tk < n) {
             const int pair = list[first + tk];
             if (p.H) {
-              const float av = acc[0][i][v];
-              float hv = av / (1.f + expf(-av));
-              if constexpr (NB == 2) hv *= acc[NB - 1][i][v];
-              p.H[(int64_t)pair * p.N + cc] = __float2bfloat16_rn(hv);
+              float hv = sum[0] / (1.f + expf(-sum[0]));
+              if constexpr (NB == 2) hv *= sum[NB - 1];
+              p.H[(int64_t)pair * p.N + col] = __float2bfloat16_rn(hv);
             } else {
-              p.part[((int64_t)sl * p.pairs + pair) * p.N + cc] = acc[0][i][v];
+              p.part[((int64_t)sl * p.pairs + pair) * p.N + col] = sum[0];
             }
           }
+        }
+        team_sync(team);  // the last tile is read before the next unit's sums overwrite it
       }
     };
     if (NTL == 1 || n <= 8) run_units(std::integral_constant<int, 1>());
@@ -431,6 +479,7 @@ __global__ void int4_combine_kernel(const float* __restrict__ part, const int32_
                                     __nv_bfloat16* __restrict__ y) {
   const int64_t total = (int64_t)L * d / 4;
   const int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (i >= total) return;
   const int t = (int)(i / (d / 4)), c = (int)(i % (d / 4)) * 4;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -438,6 +487,7 @@ __global__ void int4_combine_kernel(const float* __restrict__ part, const int32_
     const int pair = t * K + k;
     if ((unsigned)ids[pair] >= (unsigned)E) continue;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
     for (int s = 0; s < slices; ++s) {
       const float4 q = *reinterpret_cast<const float4*>(part + ((int64_t)s * L * K + pair) * d + c);
       v.x += q.x; v.y += q.y; v.z += q.z; v.w += q.w;
@@ -450,7 +500,9 @@ __global__ void int4_combine_kernel(const float* __restrict__ part, const int32_
 
 // shared memory besides the token rows: the ring of a launch on nb matrices
 size_t ring_bytes(int nb, int group) { return (size_t)kQWarps * ring_depth(nb) * nb * (1024 + 128 * (128 / group)); }
-size_t fixed_bytes(int nb, int group) { return align_up(ring_bytes(nb, group) + kQIntBytes, 16); }
+size_t fixed_bytes(int nb, int group) {
+  return align_up(ring_bytes(nb, group) + kQIntBytes, 16) + (size_t)kQWarps * nb * 128 * sizeof(float);
+}
 // token columns are padded to whole MMAs in the table of group sums
 int pad_cols(int cols) { return cols <= 8 ? 8 : cols <= 16 ? 16 : 32; }
 size_t token_bytes(int64_t len, int group, int rows) {
@@ -465,26 +517,49 @@ int pass_cap(int64_t len, int nb, int group) {
   return rows;
 }
 
-// slices of the down projection's reduction axis: enough units for every
-// warp of the GPU, slices of whole 128-row blocks
+// Slices of the down projection's reduction axis (whole 128-row pieces): the
+// teams' rounds times a warp's pieces of a unit, plus about a piece's time a
+// round for its start and end; slices whose token rows fit shared memory for
+// the usual load (16 tokens of an expert) only, where there are such.
 int down_slices(const moeblaze_shape& s, int group, int tokens) {
   const int blocks = s.h / 128;
   const int64_t used = std::min<int64_t>(s.E, (int64_t)tokens * s.K);
-  const int64_t units = used * (s.d / 16);
-  const int64_t want = (int64_t)sm_count() * kQWarps;
-  int best = 1;
-  for (int n = 1; n <= blocks; ++n) {
+  int best = blocks;
+  int64_t least = INT64_MAX;
+  for (int n = 1; n <= blocks && n <= 64; ++n) {
     if (blocks % n) continue;
-    best = n;
-    const int64_t len = s.h / n;
-    if (units * n >= want && (pass_cap(len, 1, group) >= std::min(tokens, 32) || len <= 1024)) break;
-    if (len <= 512) break;
+    if (n < blocks && pass_cap(s.h / n, 1, group) < std::min(tokens, 16)) continue;
+    const int64_t units = used * (s.d / 16) * n, per_cta = (units + sm_count() - 1) / sm_count();
+    const int64_t rounds = (per_cta + kQTeams - 1) / kQTeams, pieces = (blocks / n + kQTeam - 1) / kQTeam;
+    const int64_t cost = rounds * (pieces + 1);
+    if (cost < least) {
+      least = cost;
+      best = n;
+    }
   }
   return best;
 }
 
 size_t h_bytes(const moeblaze_shape& s, int tokens) {
   return align_up((size_t)tokens * s.K * s.h * 2, 256);
+}
+
+// `early`: the kernel may start while the one before it in the stream ends
+// (it waits for it, griddepcontrol.wait, before it touches its results)
+template <typename... Params, typename... Args>
+cudaError_t launch_q(void (*kern)(Params...), unsigned grid, unsigned block, size_t smem, bool early, cudaStream_t st,
+                     Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = early ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, static_cast<Params>(args)...);
 }
 
 template <int NB, int GROUP>
@@ -495,8 +570,8 @@ moeblaze_status launch_product_g(QParams p, int tokens, cudaStream_t st) {
   const size_t sm = fixed_bytes(NB, GROUP) + token_bytes(len, GROUP, p.rows);
   auto run = [&](auto kern) -> moeblaze_status {
     MB_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm));
-    kern<<<sm_count(), kQThreads, sm, st>>>(p);
-    MB_CUDA(cudaGetLastError());
+    // the down projection's h comes from the launch before it, its routing and weights from before that
+    MB_CUDA(launch_q(kern, (unsigned)sm_count(), kQThreads, sm, p.H == nullptr, st, p));
     count_launch();
     return MOEBLAZE_OK;
   };
@@ -570,9 +645,8 @@ moeblaze_status launch_int4_forward(const moeblaze_shape& s, const __nv_bfloat16
     p.part = part;
     if ((r = launch_product<1>(p, w.group, tokens, st)) != MOEBLAZE_OK) return r;
     const int64_t n = (int64_t)tokens * s.d / 4;
-    int4_combine_kernel<<<(unsigned)((n + 127) / 128), 128, 0, st>>>(part, ids + t0 * s.K, gates + t0 * s.K, tokens, s.d,
-                                                                   s.E, s.K, p.slices, y + t0 * s.d);
-    MB_CUDA(cudaGetLastError());
+    MB_CUDA(launch_q(int4_combine_kernel, (unsigned)((n + 127) / 128), 128, 0, true, st, (const float*)part,
+                     ids + t0 * s.K, gates + t0 * s.K, tokens, (int)s.d, (int)s.E, (int)s.K, p.slices, y + t0 * s.d));
     count_launch();
   }
   return MOEBLAZE_OK;
