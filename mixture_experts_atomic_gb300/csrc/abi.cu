@@ -114,7 +114,8 @@ moeblaze_status check_int4_shape(const moeblaze_shape* s, int group) {
   const moeblaze_status r = check_shape(s);
   if (r != MOEBLAZE_OK) return r;
   if (group != 32 && group != 64 && group != 128) return MOEBLAZE_ERR_INVALID_ARG;
-  if (s->act == MOEBLAZE_IDENTITY || s->dtype != MOEBLAZE_BF16 || !int4_shape_ok(*s, group)) return MOEBLAZE_ERR_UNSUPPORTED;
+  if (s->act == MOEBLAZE_IDENTITY || s->dtype != MOEBLAZE_BF16 || s->h > (1 << 22) || !int4_shape_ok(*s, group))
+    return MOEBLAZE_ERR_UNSUPPORTED;
   return MOEBLAZE_OK;
 }
 

@@ -47,8 +47,8 @@ constexpr int kQMaxPairs = kQMaxTokens * kMaxK;    // (token, slot) pairs of one
 // entries of a warp's ring, each a 128-row piece of a tile of nb matrices
 __host__ __device__ constexpr int ring_depth(int nb) { return nb == 1 ? 4 : 3; }
 constexpr size_t kQSmem = 227 * 1024;
-// list, counts, offsets, pass prefix, scan totals
-constexpr size_t kQIntBytes = 4 * (kQMaxPairs + 3 * kMaxE + 1 + 2 * kQWarps);
+// list, counts, offsets, pass and weight prefixes, scan totals
+constexpr size_t kQIntBytes = 4 * (kQMaxPairs + 4 * kMaxE + 2 + 3 * kQWarps);
 
 __device__ __forceinline__ uint32_t saddr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
@@ -78,6 +78,22 @@ __device__ __forceinline__ void unpack_word(uint32_t w, uint32_t (&a)[4]) {
   for (int i = 0; i < 4; ++i)
     asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(a[i]) : "r"(w >> (4 * i)), "r"(0x000F000Fu), "r"(0x43004300u));
 }
+
+// the last i < n with table[i] <= v (table[0] <= v).  Not inlined, as loops of
+// the kernel's start are not unrolled: its code is read once, and from L2
+__device__ __noinline__ int last_at_most(const int* table, int n, int v) {
+  int lo = 0;
+  while (n - lo > 1) {
+    const int m = (lo + n) >> 1;
+    if (table[m] <= v) lo = m;
+    else n = m;
+  }
+  return lo;
+}
+
+// relative time of a unit whose segment has n token columns: one MMA column
+// tile is hidden behind the weights' loads, more are not
+__device__ __forceinline__ int pass_weight(int n) { return n <= 8 ? 10 : n <= 16 ? 14 : n <= 24 ? 19 : 25; }
 
 // barrier of one team of warps (barrier 0 is the CTA's)
 __device__ __forceinline__ void team_sync(int team) {
@@ -200,7 +216,8 @@ __global__ void __launch_bounds__(kQThreads, 1) int4_product_kernel(const QParam
   int* cnt = list + kQMaxPairs;                                                // [E]
   int* off = cnt + kMaxE;                                                      // [E]
   int* pre = off + kMaxE;                                                      // [E + 1] passes before expert e
-  int* tot = pre + kMaxE + 1;                                                  // warp totals of the scans [2][16]
+  int* wpre = pre + kMaxE + 1;                                                 // [E + 1] the passes' weights before e
+  int* tot = wpre + kMaxE + 1;                                                 // warp totals of the scans [3][16]
   float* swap = reinterpret_cast<float*>(qsm + (((size_t)kQWarps * PIECES * ENTRY + kQIntBytes + 15) & ~(size_t)15));
   uint8_t* xs = reinterpret_cast<uint8_t*>(swap + kQWarps * NB * 128);         // swap: [warps][NB][4][32]
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, tq = lane & 3;
@@ -220,37 +237,47 @@ __global__ void __launch_bounds__(kQThreads, 1) int4_product_kernel(const QParam
     __syncthreads();
     int c = 0;
     if (tid < p.E) {
-#pragma unroll
+#pragma unroll 4
       for (int w = 0; w < kQWarps; ++w) {
         const int v = tbl[w * p.E + tid];
         tbl[w * p.E + tid] = (uint16_t)c;
         c += v;
       }
     }
-    int a = c, b = (c + p.cap - 1) / p.cap;
-    const int passes = b;
+    // inclusive scans over the experts of pairs, passes and the passes' weights
+    const int full = c / p.cap, rest = c % p.cap;
+    const int passes = full + (rest > 0), weight = full * pass_weight(p.cap) + (rest > 0 ? pass_weight(rest) : 0);
+    int a = c, b = passes, q = weight;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int ua = __shfl_up_sync(0xffffffffu, a, o), ub = __shfl_up_sync(0xffffffffu, b, o);
+      const int uq = __shfl_up_sync(0xffffffffu, q, o);
       if (lane >= o) {
         a += ua;
         b += ub;
+        q += uq;
       }
     }
     if (lane == 31) {
       tot[warp] = a;
       tot[kQWarps + warp] = b;
+      tot[2 * kQWarps + warp] = q;
     }
     __syncthreads();
     for (int w = 0; w < warp; ++w) {
       a += tot[w];
       b += tot[kQWarps + w];
+      q += tot[2 * kQWarps + w];
     }
     if (tid < p.E) {
       cnt[tid] = c;
       off[tid] = a - c;
       pre[tid] = b - passes;
-      if (tid == p.E - 1) pre[p.E] = b;
+      wpre[tid] = q - weight;
+      if (tid == p.E - 1) {
+        pre[p.E] = b;
+        wpre[p.E] = q;
+      }
     }
     __syncthreads();
     if (id >= 0) list[off[id] + tbl[warp * p.E + id] + rank] = tid;
@@ -258,37 +285,44 @@ __global__ void __launch_bounds__(kQThreads, 1) int4_product_kernel(const QParam
   }
 
   const int nt = p.N / 16, SL = p.R / p.slices, kp = SL / 128, allp = p.R / 128;
-  const int64_t units = (int64_t)pre[p.E] * p.slices * nt;
-  const int64_t u0 = units * blockIdx.x / gridDim.x, u1 = units * (blockIdx.x + 1) / gridDim.x;
+  const int per_pass = p.slices * nt;
+  // This CTA's units: an even share of the weights.  Lanes 0 and 1 map the
+  // share's ends, blockIdx W / gridDim of the total weight W, to units; a
+  // CTA's end and the next one's start are the same computation, which never
+  // decreases from one to the next.
+  int u0, u1;
+  {
+    const int share = wpre[p.E] * (int)(blockIdx.x + (lane & 1));
+    const int q = share / (int)gridDim.x, r = share % (int)gridDim.x;
+    int u = pre[p.E] * per_pass;
+    if (q < wpre[p.E]) {
+      const int e = last_at_most(wpre, p.E, q);
+      const int wf = pass_weight(p.cap), pass = min((q - wpre[e]) / wf, cnt[e] / p.cap);
+      const int n = min(p.cap, cnt[e] - pass * p.cap);
+      const float in = (float)((q - wpre[e] - pass * wf) * (int)gridDim.x + r) / (float)(pass_weight(n) * (int)gridDim.x);
+      u = (pre[e] + pass) * per_pass + min(per_pass, (int)(in * (float)per_pass));
+    }
+    u0 = __shfl_sync(0xffffffffu, u, 0);
+    u1 = __shfl_sync(0xffffffffu, u, 1);
+  }
   if (u0 >= u1) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     return;
   }
-  // the expert of pass i: the last e with pre[e] <= i
-  auto expert_of = [&](int i) {
-    int lo = 0, hi = p.E;
-    while (hi - lo > 1) {
-      const int m = (lo + hi) >> 1;
-      if (pre[m] <= i) lo = m;
-      else hi = m;
-    }
-    return lo;
-  };
 
   // ---- the fetch head of this warp: unit, pieces left of it, addresses
   const uint32_t ring = saddr(qsm) + warp * PIECES * ENTRY + lane * 16;
   const uint32_t ring_s = saddr(qsm) + warp * PIECES * ENTRY + 1024 + lane * 4 * SW;
   const int team = warp / kQTeam, mate = warp % kQTeam;
   const int k0 = kp * mate / kQTeam, k1 = kp * (mate + 1) / kQTeam;  // this warp's pieces of a unit
-  int64_t fu = u0 + team;
+  int fu = u0 + team;
   int left = 0;
   uint32_t fslot = 0;  // byte offset of the ring entry to fill
   const uint8_t* fw[NB];
   const uint8_t* fs[NB];
   auto fetch_unit = [&]() {
     if (fu >= u1 || k0 == k1) return;
-    const int64_t seg = fu / nt;
-    const int tile = (int)(fu - seg * nt), e = expert_of((int)(seg / p.slices)), sl = (int)(seg % p.slices);
+    const int seg = fu / nt, tile = fu - seg * nt, sl = seg % p.slices, e = last_at_most(pre, p.E, seg / p.slices);
     const int64_t at = ((int64_t)e * nt + tile) * allp + sl * kp + k0;
 #pragma unroll
     for (int br = 0; br < NB; ++br) {
@@ -316,7 +350,7 @@ __global__ void __launch_bounds__(kQThreads, 1) int4_product_kernel(const QParam
     fslot = fslot == (PIECES - 1) * ENTRY ? 0u : fslot + ENTRY;
   };
   fetch_unit();
-#pragma unroll
+#pragma unroll 1
   for (int i = 0; i < PIECES - 1; ++i) fetch();
   // everything so far reads the routing and the weights, which the caller
   // provides; the rows staged below are the kernel before's (the down
@@ -325,40 +359,48 @@ __global__ void __launch_bounds__(kQThreads, 1) int4_product_kernel(const QParam
 
   // ---- segments
   const int pitch = SL * 2 + 64;  // rows 16 banks apart: 2 rows x 64 bytes of a fragment load do not conflict
-  const int groups = SL / GROUP;
   float* nsx = reinterpret_cast<float*>(xs + (size_t)p.rows * pitch);  // [groups][8 NTL]: -136 sum x
   uint32_t slot = 0;
-  int64_t u = u0 + team;
-  for (int64_t seg = u0 / nt; seg * nt < u1; ++seg) {
-    const int pass = (int)(seg / p.slices), sl = (int)(seg % p.slices), e = expert_of(pass);
+  int u = u0 + team;
+  for (int seg = u0 / nt; seg * nt < u1; ++seg) {
+    const int pass = seg / p.slices, sl = seg % p.slices, e = last_at_most(pre, p.E, pass);
     const int first = off[e] + (pass - pre[e]) * p.cap;
     const int n = min(p.cap, off[e] + cnt[e] - first);
     __syncthreads();  // every warp is done with the previous segment's rows
+    // a warp per 1024 elements of a row: 8 elements a lane, four times, all
+    // in flight together; their sums meet over the GROUP / 8 lanes of a group
     {
-      const int per_row = SL / 8;
-      for (int i = tid; i < n * per_row; i += kQThreads) {
-        const int r = i / per_row, cc = i % per_row;
+      const int m = SL / 8, parts = (m + 127) / 128;  // m is a multiple of 16
+#pragma unroll 1
+      for (int i = warp; i < n * parts; i += kQWarps) {
+        const int r = i / parts, c0 = (i - r * parts) * 128;
         const int pair = list[first + r];
         const int64_t row = p.H ? pair / p.K : pair;
-        *reinterpret_cast<uint4*>(xs + (size_t)r * pitch + cc * 16) =
-            *reinterpret_cast<const uint4*>(p.src + row * p.src_ld + (int64_t)sl * SL + cc * 8);
-      }
-    }
-    __syncthreads();
-    for (int i = tid; i < n * groups; i += kQThreads) {
-      const int r = i / groups, gr = i % groups;
-      const uint4* row = reinterpret_cast<const uint4*>(xs + (size_t)r * pitch + gr * (GROUP * 2));
-      float s = 0.f;
+        const uint4* src = reinterpret_cast<const uint4*>(p.src + row * p.src_ld + (int64_t)sl * SL);
+        uint4* dst = reinterpret_cast<uint4*>(xs + (size_t)r * pitch);
+        uint4 v[4];
 #pragma unroll
-      for (int q = 0; q < GROUP / 8; ++q) {
-        const uint4 v = row[q];
-        const float2 a0 = unpack_bf16x2(v.x), a1 = unpack_bf16x2(v.y), a2 = unpack_bf16x2(v.z), a3 = unpack_bf16x2(v.w);
-        s += ((a0.x + a0.y) + (a1.x + a1.y)) + ((a2.x + a2.y) + (a3.x + a3.y));
+        for (int j = 0; j < 4; ++j) {
+          const int c = c0 + 32 * j + lane;
+          v[j] = c < m ? src[c] : make_uint4(0u, 0u, 0u, 0u);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int c = c0 + 32 * j + lane;
+          const float2 a0 = unpack_bf16x2(v[j].x), a1 = unpack_bf16x2(v[j].y), a2 = unpack_bf16x2(v[j].z),
+                       a3 = unpack_bf16x2(v[j].w);
+          float t = ((a0.x + a0.y) + (a1.x + a1.y)) + ((a2.x + a2.y) + (a3.x + a3.y));
+#pragma unroll
+          for (int o = 1; o < GROUP / 8; o <<= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+          if (c < m) {
+            dst[c] = v[j];
+            if (lane % (GROUP / 8) == 0) nsx[(c / (GROUP / 8)) * (8 * NTL) + r] = -136.f * t;
+          }
+        }
       }
-      nsx[gr * (8 * NTL) + r] = -136.f * s;
     }
     __syncthreads();
-    const int64_t send = min((seg + 1) * (int64_t)nt, u1);
+    const int send = min((seg + 1) * nt, u1);
     // the segment's units of this team, for T tiles of 8 token columns
     auto run_units = [&](auto tiles) {
       constexpr int T = decltype(tiles)::value;
@@ -451,7 +493,7 @@ __global__ void __launch_bounds__(kQThreads, 1) int4_product_kernel(const QParam
             for (int w = 0; w < kQTeam; ++w)
               sum[br] += swap[(((team * kQTeam + w) * NB + br) * 4 + mate) * 32 + lane];
           }
-          const int tk = 8 * i + 2 * tq + (mate & 1), col = (int)(u - seg * nt) * 16 + g + 8 * (mate >> 1);
+          const int tk = 8 * i + 2 * tq + (mate & 1), col = (u - seg * nt) * 16 + g + 8 * (mate >> 1);
           if (tk < n) {
             const int pair = list[first + tk];
             if (p.H) {
@@ -468,6 +510,7 @@ __global__ void __launch_bounds__(kQThreads, 1) int4_product_kernel(const QParam
     };
     if (NTL == 1 || n <= 8) run_units(std::integral_constant<int, 1>());
     else if (NTL == 2 || n <= 16) run_units(std::integral_constant<int, (NTL < 2 ? NTL : 2)>());
+    else if (n <= 24) run_units(std::integral_constant<int, (NTL < 3 ? NTL : 3)>());
     else run_units(std::integral_constant<int, NTL>());
   }
   cp_wait<0>();
