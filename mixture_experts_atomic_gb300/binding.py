@@ -317,12 +317,14 @@ def moeblaze_kernel_launches() -> int:
 # ---------------------------------------------------------------- torch helpers
 
 def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    # the argument types of the entry points turn an int into a void*
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream=None):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def make_shape(L, d, h, E, K, dtype, act, flags: int = 0) -> Shape:
@@ -345,26 +347,34 @@ def _args(*specs):
     for t, name, shape, dtype, optional in specs:
         if t is None:
             # an empty buffer (no tokens) may be passed as NULL
-            if optional or any(int(v) == 0 for v in shape):
+            if optional or 0 in shape:
                 continue
             raise ValueError(f"{name}: a tensor is required")
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
-        want = tuple(int(v) for v in shape)
-        if tuple(t.shape) != want:
-            raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {want}")
-        if t.dtype != dtype:
+        if t.shape != shape:
+            raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(int(v) for v in shape)}")
+        if t.dtype is not dtype:
             raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
         if not t.is_contiguous():
             raise ValueError(f"{name}: must be contiguous (row-major)")
-    _on_device(*[(spec[0], spec[1]) for spec in specs if spec[0] is not None])
+    current = None
+    for spec in specs:
+        t = spec[0]
+        if t is not None:
+            if not t.is_cuda:
+                raise ValueError(f"{spec[1]}: must be a CUDA tensor")
+            if current is None:
+                current = torch.cuda.current_device()
+            if t.get_device() != current:
+                raise ValueError(f"{spec[1]}: on {t.device}, but the current device is cuda:{current}")
 
 
 def _on_device(*named):
     for t, name in named:
         if not t.is_cuda:
             raise ValueError(f"{name}: must be a CUDA tensor")
-        if t.device.index != torch.cuda.current_device():
+        if t.get_device() != torch.cuda.current_device():
             raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
 
 
