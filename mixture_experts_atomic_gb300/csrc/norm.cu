@@ -189,16 +189,47 @@ __global__ void __launch_bounds__(1024) norm_fwd_wide_kernel(const T* x, const T
 // ------------------------------------------------------------------ backward
 // A persistent CTA walks over rows t = first, first + rows in flight, ...;
 // a thread always holds the same columns, so the sums of dw and db over the
-// CTA's rows stay in its registers.  part[cta][0][c] and part[cta][1][c]
-// are added up in a fixed order by norm_wgrad_kernel.
+// CTA's rows stay in its registers.  The rows to come are copied ahead by
+// cp.async into a ring in which every thread reads back only its own pieces
+// (no barrier, no registers): 1024 threads x 192 bytes keep an SM's loads in
+// flight while a row's two sums go through the CTA's one barrier.
+// part[cta][0][c] and part[cta][1][c] are added up in a fixed order by
+// norm_wgrad_kernel.
+template <int BYTES>
+__device__ __forceinline__ void copy_ahead(void* dst, const void* src) {
+  const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
+  else if constexpr (BYTES >= 4)
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(d), "l"(src), "n"(BYTES) : "memory");
+  else  // too small to copy asynchronously
+    *static_cast<__nv_bfloat16*>(dst) = *static_cast<const __nv_bfloat16*>(src);
+}
+
+template <typename T, int VEC, int NV>
+constexpr int bwd_depth() {
+  constexpr int row = 3 * VEC * NV * (int)sizeof(T);  // bytes of a row a thread holds
+  return 192 / row >= 4 ? 4 : 192 / row >= 2 ? 192 / row : 2;
+}
 template <typename T, int VEC, int TPR, int NV>
-__global__ void __launch_bounds__(norm_threads<TPR>()) norm_bwd_kernel(
+constexpr size_t bwd_smem() {
+  return (size_t)bwd_depth<T, VEC, NV>() * 3 * VEC * NV * sizeof(T) * norm_threads<TPR>();
+}
+template <int TPR>
+constexpr int bwd_per_sm() {
+  return TPR == 32 ? 4 : 1024 / TPR;  // a warp's rows: up to 16 elements a lane need 128 registers
+}
+
+template <typename T, int VEC, int TPR, int NV>
+__global__ void __launch_bounds__(norm_threads<TPR>(), bwd_per_sm<TPR>()) norm_bwd_kernel(
     const T* dy, const T* s, const float* __restrict__ mean, const float* __restrict__ rstd,
     const float* __restrict__ w, const T* dsum, int64_t L, int d, T* dx, float* __restrict__ part) {
   using V = Vec<T, VEC>;
-  constexpr int ROWS = TPR == 32 ? kNormWarps : 1;
-  __shared__ float red[2][2][32];
-  const int lane = TPR == 32 ? (threadIdx.x & 31) : threadIdx.x;
+  constexpr int ROWS = TPR == 32 ? kNormWarps : 1, D = bwd_depth<T, VEC, NV>(), NT = norm_threads<TPR>();
+  extern __shared__ __align__(16) uint8_t nsm[];
+  V* ring = reinterpret_cast<V*>(nsm);  // [D][3][NV][threads]: dy, s, dsum
+  __shared__ float2 red[2][32];
+  const int tid = threadIdx.x, lane = TPR == 32 ? (tid & 31) : tid;
   const int nvec = d / VEC;
   const float inv_d = 1.f / (float)d;
   float aw[NV][VEC], ab[NV][VEC], wv[NV][VEC];
@@ -211,72 +242,93 @@ __global__ void __launch_bounds__(norm_threads<TPR>()) norm_bwd_kernel(
       wv[j][i] = c < nvec ? w[c * VEC + i] : 0.f;
     }
   const int64_t step = (int64_t)gridDim.x * ROWS;
-  const int64_t first = (int64_t)blockIdx.x * ROWS + (TPR == 32 ? (threadIdx.x >> 5) : 0);
-  V nd[NV], ns[NV], nr[NV];
-  float nmu = 0.f, nrs = 0.f;
-  auto fetch = [&](int64_t t) {
+  const int64_t first = (int64_t)blockIdx.x * ROWS + (TPR == 32 ? (tid >> 5) : 0);
+  // pieces past the row's end stay zero
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int c = lane + j * TPR;
-      if (c < nvec) {
-        nd[j] = reinterpret_cast<const V*>(dy + t * d)[c];
-        ns[j] = reinterpret_cast<const V*>(s + t * d)[c];
-        if (dsum) nr[j] = reinterpret_cast<const V*>(dsum + t * d)[c];
+  for (int q = 0; q < D * 3 * NV; ++q)
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) st_t(ring[q * NT + tid].v[i], 0.f);
+  auto fetch = [&](int64_t t, int at) {
+    if (t < L) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int c = lane + j * TPR;
+        if (c < nvec) {
+          const int64_t o = t * nvec + c;
+          V* dst = ring + (at * 3 * NV + j) * NT + tid;
+          copy_ahead<sizeof(V)>(dst, reinterpret_cast<const V*>(dy) + o);
+          copy_ahead<sizeof(V)>(dst + NV * NT, reinterpret_cast<const V*>(s) + o);
+          if (dsum) copy_ahead<sizeof(V)>(dst + 2 * NV * NT, reinterpret_cast<const V*>(dsum) + o);
+        }
       }
     }
-    nmu = mean[t];
-    nrs = rstd[t];
+    asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  if (first < L) fetch(first);
-  int buf = 0;
+#pragma unroll
+  for (int i = 0; i < D - 1; ++i) fetch(first + i * step, i);
+  float nmu = 0.f, nrs = 0.f;
+  if (first < L) {
+    nmu = mean[first];
+    nrs = rstd[first];
+  }
+  int buf = 0, slot = 0;
   for (int64_t t = first; t < L; t += step, buf ^= 1) {
-    const float mu = nmu, rs = nrs;
-    float xh[NV][VEC], g[NV][VEC], rr[NV][VEC];
+    const float rs = nrs, off = -nmu * nrs;
+    if (t + step < L) {
+      nmu = mean[t + step];
+      nrs = rstd[t + step];
+    }
+    asm volatile("cp.async.wait_group %0;" ::"n"(D - 2) : "memory");
+    float xh[NV][VEC], g[NV][VEC];
+    V rv[NV];
     float sg = 0.f, sgx = 0.f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const bool in = lane + j * TPR < nvec;
+      const V* src = ring + (slot * 3 * NV + j) * NT + tid;
+      const V dv = src[0], sv = src[NV * NT];
+      rv[j] = src[2 * NV * NT];
+      // a piece past the row's end: dy = 0 and w = 0 keep it out of the sums
 #pragma unroll
       for (int i = 0; i < VEC; ++i) {
-        const float dv = in ? ld_f32(nd[j].v[i]) : 0.f;
-        xh[j][i] = in ? (ld_f32(ns[j].v[i]) - mu) * rs : 0.f;
-        rr[j][i] = in && dsum ? ld_f32(nr[j].v[i]) : 0.f;
-        aw[j][i] = fmaf(dv, xh[j][i], aw[j][i]);
-        ab[j][i] += dv;
-        g[j][i] = dv * wv[j][i];
+        const float dyv = ld_f32(dv.v[i]);
+        xh[j][i] = fmaf(ld_f32(sv.v[i]), rs, off);
+        aw[j][i] = fmaf(dyv, xh[j][i], aw[j][i]);
+        ab[j][i] += dyv;
+        g[j][i] = dyv * wv[j][i];
         sg += g[j][i];
         sgx = fmaf(g[j][i], xh[j][i], sgx);
       }
     }
-    if (t + step < L) fetch(t + step);
+    fetch(t + (D - 1) * step, slot == 0 ? D - 1 : slot - 1);
+    slot = slot == D - 1 ? 0 : slot + 1;
     sg = warp_sum(sg);
     sgx = warp_sum(sgx);
     if constexpr (TPR > 32) {
       // two buffers in turn: a warp can be one row ahead of the slowest
       // reader of the other buffer, never two
-      if ((threadIdx.x & 31) == 0) {
-        red[buf][0][threadIdx.x >> 5] = sg;
-        red[buf][1][threadIdx.x >> 5] = sgx;
-      }
+      if ((tid & 31) == 0) red[buf][tid >> 5] = make_float2(sg, sgx);
       __syncthreads();
       sg = sgx = 0.f;
 #pragma unroll
       for (int i = 0; i < TPR / 32; ++i) {
-        sg += red[buf][0][i];
-        sgx += red[buf][1][i];
+        const float2 v = red[buf][i];
+        sg += v.x;
+        sgx += v.y;
       }
     }
-    const float mg = sg * inv_d, mgx = sgx * inv_d;
-    V* o = reinterpret_cast<V*>(dx + t * d);
+    const float mg = -sg * inv_d, mgx = -sgx * inv_d;
+    V* o = reinterpret_cast<V*>(dx) + t * nvec;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int c = lane + j * TPR;
       V ov;
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) st_t(ov.v[i], fmaf(rs, g[j][i] - mg - xh[j][i] * mgx, rr[j][i]));
+      for (int i = 0; i < VEC; ++i)
+        st_t(ov.v[i], fmaf(rs, fmaf(xh[j][i], mgx, g[j][i] + mg), dsum ? ld_f32(rv[j].v[i]) : 0.f));
       if (c < nvec) o[c] = ov;
     }
   }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
   float* pw = part + (int64_t)blockIdx.x * 2 * d;
   if constexpr (TPR > 32) {
 #pragma unroll
@@ -299,10 +351,10 @@ __global__ void __launch_bounds__(norm_threads<TPR>()) norm_bwd_kernel(
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
           __syncthreads();
-          cw[threadIdx.x >> 5][lane] = q ? ab[j][i] : aw[j][i];
+          cw[tid >> 5][lane] = q ? ab[j][i] : aw[j][i];
           __syncthreads();
           const int c = (lane + j * 32) * VEC + i;
-          if (threadIdx.x < 32 && c < d) {
+          if (tid < 32 && c < d) {
             float a = 0.f;
 #pragma unroll
             for (int r = 0; r < kNormWarps; ++r) a += cw[r][lane];
@@ -313,23 +365,24 @@ __global__ void __launch_bounds__(norm_threads<TPR>()) norm_bwd_kernel(
 }
 
 // dw and db from the CTAs' partial sums, in the order of the CTAs: 32 columns
-// per block, its 8 warps take every eighth partial
-__global__ void __launch_bounds__(256) norm_wgrad_kernel(const float* __restrict__ part, int G, int d,
+// per block, warp i of its 32 takes partials i, i + 32, ...
+constexpr int kWgradWarps = 32;
+__global__ void __launch_bounds__(32 * kWgradWarps) norm_wgrad_kernel(const float* __restrict__ part, int G, int d,
                                                          float* __restrict__ dw, float* __restrict__ db) {
-  __shared__ float acc[8][32];
+  __shared__ float acc[kWgradWarps][32];
   const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;  // column of the (2 d) row [dw | db]
   float a = 0.f;
   if (c < 2 * d) {
-#pragma unroll 4
-    for (int g = wp; g < G; g += 8) a += part[(int64_t)g * 2 * d + c];
+#pragma unroll 8
+    for (int g = wp; g < G; g += kWgradWarps) a += part[(int64_t)g * 2 * d + c];
   }
   acc[wp][lane] = a;
   __syncthreads();
   if (wp == 0 && c < 2 * d) {
     a = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) a += acc[i][lane];
+    for (int i = 0; i < kWgradWarps; ++i) a += acc[i][lane];
     if (c < d) dw[c] = a;
     else if (db) db[c - d] = a;
   }
@@ -384,14 +437,17 @@ int vec_of(int d) {
   return v;
 }
 
-// CTAs of the backward: enough rows in flight to fill the GPU.  The partial
-// sums are G x 2 d floats.
-int64_t bwd_ctas(const moeblaze_shape& s, int tpr) {
-  const int rows = tpr == 32 ? kNormWarps : 1;
-  int64_t per_sm = tpr == 32 ? 8 : 1024 / tpr;
-  if (per_sm < 1) per_sm = 1;
-  int64_t g = per_sm * sm_count();
-  const int64_t need = (s.L + rows - 1) / rows;
+// The backward's tile: up to 8 elements a thread (their two sums, weights and
+// both operands in registers), rows of up to 512 elements in a warp, longer
+// ones in a CTA of as many threads as they need; 16 elements a thread for
+// bf16 rows of 8193 to 16384 (of fp32 rows shared memory holds no ring).
+int bwd_tile_max(const moeblaze_shape& s) { return s.dtype == MOEBLAZE_BF16 ? 16384 : 8192; }
+int bwd_tpr(int d) { return d <= 512 ? 32 : d <= 1024 ? 128 : d <= 2048 ? 256 : d <= 4096 ? 512 : 1024; }
+
+// CTAs of the backward: 1024 threads per SM (512 of a warp a row).  The partial sums are G x 2 d floats.
+int64_t bwd_ctas(const moeblaze_shape& s) {
+  const int tpr = bwd_tpr(s.d), rows = tpr == 32 ? kNormWarps : 1, per_sm = tpr == 32 ? 4 : 1024 / tpr;
+  const int64_t g = (int64_t)per_sm * sm_count(), need = (s.L + rows - 1) / rows;
   return g < need ? g : need;
 }
 
@@ -410,11 +466,14 @@ template <typename T, int VEC, int TPR, int NV>
 moeblaze_status bwd_tile(const moeblaze_shape& s, const void* dy, const void* sum, const float* mean,
                          const float* rstd, const float* w, const void* dsum, void* dx, float* dw, float* db,
                          float* part, cudaStream_t st) {
-  const int64_t G = bwd_ctas(s, TPR);
-  norm_bwd_kernel<T, VEC, TPR, NV><<<(unsigned)G, norm_threads<TPR>(), 0, st>>>(
-      (const T*)dy, (const T*)sum, mean, rstd, w, (const T*)dsum, s.L, s.d, (T*)dx, part);
+  const int64_t G = bwd_ctas(s);
+  auto kern = norm_bwd_kernel<T, VEC, TPR, NV>;
+  constexpr size_t sm = bwd_smem<T, VEC, TPR, NV>();
+  MB_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm));
+  kern<<<(unsigned)G, norm_threads<TPR>(), sm, st>>>((const T*)dy, (const T*)sum, mean, rstd, w, (const T*)dsum, s.L,
+                                                     s.d, (T*)dx, part);
   MB_CUDA(cudaGetLastError());
-  norm_wgrad_kernel<<<(unsigned)((2 * (int64_t)s.d + 31) / 32), 256, 0, st>>>(part, (int)G, s.d, dw, db);
+  norm_wgrad_kernel<<<(unsigned)((2 * (int64_t)s.d + 31) / 32), 32 * kWgradWarps, 0, st>>>(part, (int)G, s.d, dw, db);
   MB_CUDA(cudaGetLastError());
   count_launch(2);
   return MOEBLAZE_OK;
@@ -433,8 +492,6 @@ moeblaze_status bwd_tile(const moeblaze_shape& s, const void* dy, const void* su
     return CALL(1024, 4);                      \
   } while (0)
 
-int tile_tpr(int n) { return n <= 128 ? 32 : n <= 256 ? 128 : n <= 512 ? 256 : n <= 1024 ? 512 : 1024; }
-
 template <typename T, int VEC>
 moeblaze_status fwd_vec(const moeblaze_shape& s, const void* x, const void* res, const float* w, const float* b,
                         float eps, void* sum, void* y, float* mean, float* rstd, cudaStream_t st) {
@@ -447,8 +504,18 @@ template <typename T, int VEC>
 moeblaze_status bwd_vec(const moeblaze_shape& s, const void* dy, const void* sum, const float* mean, const float* rstd,
                         const float* w, const void* dsum, void* dx, float* dw, float* db, float* part,
                         cudaStream_t st) {
-#define MB_CALL(TPR, NV) bwd_tile<T, VEC, TPR, NV>(s, dy, sum, mean, rstd, w, dsum, dx, dw, db, part, st)
-  MB_NORM_TILE(s.d / VEC, MB_CALL);
+  constexpr int NV = 8 / VEC;  // pieces of a thread
+#define MB_CALL(TPR, N) bwd_tile<T, VEC, TPR, N>(s, dy, sum, mean, rstd, w, dsum, dx, dw, db, part, st)
+  if (s.d <= 256) return MB_CALL(32, NV);
+  switch (bwd_tpr(s.d)) {
+    case 32: return MB_CALL(32, 2 * NV);
+    case 128: return MB_CALL(128, NV);
+    case 256: return MB_CALL(256, NV);
+    case 512: return MB_CALL(512, NV);
+  }
+  if constexpr (sizeof(T) == 2)
+    if (s.d > 8192) return MB_CALL(1024, 2 * NV);
+  return MB_CALL(1024, NV);
 #undef MB_CALL
 }
 
@@ -474,7 +541,7 @@ template <typename T>
 moeblaze_status bwd_t(const moeblaze_shape& s, const void* dy, const void* sum, const float* mean, const float* rstd,
                       const float* w, const void* dsum, void* dx, float* dw, float* db, float* part, cudaStream_t st) {
   const int v = vec_of<T>(s.d);
-  if (s.d / v > kMaxTileVecs) {
+  if (s.d > bwd_tile_max(s)) {
     norm_bwd_wide_kernel<T><<<(unsigned)s.L, 1024, 0, st>>>((const T*)dy, (const T*)sum, mean, rstd, w, (const T*)dsum,
                                                             s.d, (T*)dx);
     MB_CUDA(cudaGetLastError());
@@ -482,7 +549,7 @@ moeblaze_status bwd_t(const moeblaze_shape& s, const void* dy, const void* sum, 
     norm_wide_wgrad_kernel<T><<<dim3((unsigned)((s.d + 255) / 256), (unsigned)G), 256, 0, st>>>(
         (const T*)dy, (const T*)sum, mean, rstd, s.L, s.d, part);
     MB_CUDA(cudaGetLastError());
-    norm_wgrad_kernel<<<(unsigned)((2 * (int64_t)s.d + 31) / 32), 256, 0, st>>>(part, (int)G, s.d, dw, db);
+    norm_wgrad_kernel<<<(unsigned)((2 * (int64_t)s.d + 31) / 32), 32 * kWgradWarps, 0, st>>>(part, (int)G, s.d, dw, db);
     MB_CUDA(cudaGetLastError());
     count_launch(3);
     return MOEBLAZE_OK;
@@ -498,9 +565,7 @@ moeblaze_status bwd_t(const moeblaze_shape& s, const void* dy, const void* sum, 
 
 size_t norm_ws_bytes(const moeblaze_shape& s) {
   if (s.L == 0) return 0;
-  const int v = s.dtype == MOEBLAZE_BF16 ? vec_of<__nv_bfloat16>(s.d) : vec_of<float>(s.d);
-  const int n = s.d / v;
-  const int64_t G = n > kMaxTileVecs ? (s.L < kWideSplits ? s.L : kWideSplits) : bwd_ctas(s, tile_tpr(n));
+  const int64_t G = s.d > bwd_tile_max(s) ? (s.L < kWideSplits ? s.L : kWideSplits) : bwd_ctas(s);
   return (size_t)G * 2 * s.d * sizeof(float);
 }
 
