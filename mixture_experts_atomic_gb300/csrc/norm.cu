@@ -32,6 +32,37 @@ __device__ __forceinline__ float ld_f32(float v) { return v; }
 __device__ __forceinline__ void st_t(__nv_bfloat16& o, float v) { o = __float2bfloat16_rn(v); }
 __device__ __forceinline__ void st_t(float& o, float v) { o = v; }
 
+// a piece's elements as floats, and back; pairs of bf16 in one conversion
+template <typename T, int VEC>
+__device__ __forceinline__ void to_floats(const Vec<T, VEC>& p, float (&v)[VEC]) {
+  if constexpr (sizeof(T) == 2 && VEC >= 2) {
+#pragma unroll
+    for (int i = 0; i < VEC / 2; ++i) {
+      const float2 f = unpack_bf16x2(reinterpret_cast<const uint32_t*>(&p)[i]);
+      v[2 * i] = f.x;
+      v[2 * i + 1] = f.y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) v[i] = ld_f32(p.v[i]);
+  }
+}
+template <typename T, int VEC>
+__device__ __forceinline__ Vec<T, VEC> from_floats(const float (&v)[VEC]) {
+  Vec<T, VEC> p;
+  if constexpr (sizeof(T) == 2 && VEC >= 2) {
+#pragma unroll
+    for (int i = 0; i < VEC / 2; ++i) reinterpret_cast<uint32_t*>(&p)[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) st_t(p.v[i], v[i]);
+  }
+  return p;
+}
+
+// fp32 pairs: each half an ordinary fp32 operation, one instruction for both
+__device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
+
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -195,6 +226,15 @@ __global__ void __launch_bounds__(1024) norm_fwd_wide_kernel(const T* x, const T
 // flight while a row's two sums go through the CTA's one barrier.
 // part[cta][0][c] and part[cta][1][c] are added up in a fixed order by
 // norm_wgrad_kernel.
+// the two sums of a warp, a in lanes 0-15 and b in lanes 16-31
+__device__ __forceinline__ float warp_sum2(float a, float b) {
+  const bool hi = threadIdx.x & 16;
+  float v = (hi ? b : a) + __shfl_xor_sync(0xffffffffu, hi ? a : b, 16);
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
 template <int BYTES>
 __device__ __forceinline__ void copy_ahead(void* dst, const void* src) {
   const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
@@ -206,41 +246,56 @@ __device__ __forceinline__ void copy_ahead(void* dst, const void* src) {
     *static_cast<__nv_bfloat16*>(dst) = *static_cast<const __nv_bfloat16*>(src);
 }
 
-template <typename T, int VEC, int NV>
+// threads on an SM: 512 where a row of 8 fp32 elements a thread, or the 16
+// elements of a lane that holds a short row, take more registers and ring
+template <typename T, int TPR>
+constexpr int bwd_per_sm() {
+  return TPR == 32 ? 4 : TPR == 1024 ? 1 : (sizeof(T) == 4 ? 512 : 1024) / TPR;
+}
+// rows in the ring: two at work, the others on their way (with two, a row is
+// fetched as soon as its place is free)
+template <typename T, int VEC, int TPR, int NV>
 constexpr int bwd_depth() {
   constexpr int row = 3 * VEC * NV * (int)sizeof(T);  // bytes of a row a thread holds
-  return 192 / row >= 4 ? 4 : 192 / row >= 2 ? 192 / row : 2;
+  constexpr int room = 200 * 1024 / (bwd_per_sm<T, TPR>() * norm_threads<TPR>()) / row;
+  return room >= 4 ? 4 : room < 2 ? 2 : room;
 }
 template <typename T, int VEC, int TPR, int NV>
 constexpr size_t bwd_smem() {
-  return (size_t)bwd_depth<T, VEC, NV>() * 3 * VEC * NV * sizeof(T) * norm_threads<TPR>();
-}
-template <int TPR>
-constexpr int bwd_per_sm() {
-  return TPR == 32 ? 4 : 1024 / TPR;  // a warp's rows: up to 16 elements a lane need 128 registers
+  return (size_t)bwd_depth<T, VEC, TPR, NV>() * 3 * VEC * NV * sizeof(T) * norm_threads<TPR>();
 }
 
 template <typename T, int VEC, int TPR, int NV>
-__global__ void __launch_bounds__(norm_threads<TPR>(), bwd_per_sm<TPR>()) norm_bwd_kernel(
+__global__ void __launch_bounds__(norm_threads<TPR>(), bwd_per_sm<T, TPR>()) norm_bwd_kernel(
     const T* dy, const T* s, const float* __restrict__ mean, const float* __restrict__ rstd,
     const float* __restrict__ w, const T* dsum, int64_t L, int d, T* dx, float* __restrict__ part) {
   using V = Vec<T, VEC>;
-  constexpr int ROWS = TPR == 32 ? kNormWarps : 1, D = bwd_depth<T, VEC, NV>(), NT = norm_threads<TPR>();
+  constexpr int ROWS = TPR == 32 ? kNormWarps : 1, D = bwd_depth<T, VEC, TPR, NV>(), NT = norm_threads<TPR>();
   extern __shared__ __align__(16) uint8_t nsm[];
   V* ring = reinterpret_cast<V*>(nsm);  // [D][3][NV][threads]: dy, s, dsum
-  __shared__ float2 red[2][32];
+  __shared__ float red[2][2][32];  // [buffer][sum][warp]
   const int tid = threadIdx.x, lane = TPR == 32 ? (tid & 31) : tid;
   const int nvec = d / VEC;
   const float inv_d = 1.f / (float)d;
-  float aw[NV][VEC], ab[NV][VEC], wv[NV][VEC];
+  // sums and weights of this thread's columns, in pairs of elements
+  constexpr int P = NV * VEC / 2;
+  auto column = [&](int q) { return (lane + (q / VEC) * TPR) * VEC + q % VEC; };  // of element q
+  float2 aw[P], ab[P], wv[P];
 #pragma unroll
-  for (int j = 0; j < NV; ++j)
+  for (int i = 0; i < P; ++i) {
+    aw[i] = ab[i] = both(0.f);
+    wv[i].x = column(2 * i) < d ? w[column(2 * i)] : 0.f;
+    wv[i].y = column(2 * i + 1) < d ? w[column(2 * i + 1)] : 0.f;
+  }
+  // array a of ring slot `at`, as pairs
+  auto read = [&](int at, int a, float2 (&v)[P]) {
+    float f[NV][VEC];
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-      const int c = lane + j * TPR;
-      aw[j][i] = ab[j][i] = 0.f;
-      wv[j][i] = c < nvec ? w[c * VEC + i] : 0.f;
-    }
+    for (int j = 0; j < NV; ++j) to_floats(ring[((at * 3 + a) * NV + j) * NT + tid], f[j]);
+#pragma unroll
+    for (int i = 0; i < P; ++i)
+      v[i] = make_float2(f[2 * i / VEC][2 * i % VEC], f[(2 * i + 1) / VEC][(2 * i + 1) % VEC]);
+  };
   const int64_t step = (int64_t)gridDim.x * ROWS;
   const int64_t first = (int64_t)blockIdx.x * ROWS + (TPR == 32 ? (tid >> 5) : 0);
   // pieces past the row's end stay zero
@@ -264,103 +319,130 @@ __global__ void __launch_bounds__(norm_threads<TPR>(), bwd_per_sm<TPR>()) norm_b
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
+  // A row's two sums meet at the CTA's barrier.  They are formed one row
+  // ahead: in one iteration the threads sum up row i + 1 and finish row i,
+  // whose sums passed the barrier of the iteration before, so that neither
+  // the barrier nor the shuffles stand in a row's way (all in one row's
+  // order measured 187 us at 32768 x 4096 bf16, and 206 us with the
+  // shuffles below in place of a read of all warps' sums).
 #pragma unroll
-  for (int i = 0; i < D - 1; ++i) fetch(first + i * step, i);
-  float nmu = 0.f, nrs = 0.f;
+  for (int i = 0; i < D; ++i) fetch(first + i * step, i);
+  float mu = 0.f, rs = 0.f, nmu = 0.f, nrs = 0.f;  // of the row to sum up, and of the one after
   if (first < L) {
-    nmu = mean[first];
-    nrs = rstd[first];
+    mu = mean[first];
+    rs = rstd[first];
   }
-  int buf = 0, slot = 0;
-  for (int64_t t = first; t < L; t += step, buf ^= 1) {
-    const float rs = nrs, off = -nmu * nrs;
-    if (t + step < L) {
-      nmu = mean[t + step];
-      nrs = rstd[t + step];
-    }
-    asm volatile("cp.async.wait_group %0;" ::"n"(D - 2) : "memory");
-    float xh[NV][VEC], g[NV][VEC];
-    V rv[NV];
-    float sg = 0.f, sgx = 0.f;
+  if (first + step < L) {
+    nmu = mean[first + step];
+    nrs = rstd[first + step];
+  }
+  float2 mine = make_float2(0.f, 0.f);  // a warp's row: the sums of the row to finish
+  // the sums of row t, in ring slot `at`, into red[buf] (or mine)
+  auto sum_up = [&](int at, int buf) {
+    const float2 rs2 = both(rs), off2 = both(-mu * rs);
+    float2 sg = both(0.f), sgx = both(0.f);
+    float2 dv[P], sv[P];
+    read(at, 0, dv);
+    read(at, 1, sv);
+    // a piece past the row's end: dy = 0 and w = 0 keep it out of the sums
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const V* src = ring + (slot * 3 * NV + j) * NT + tid;
-      const V dv = src[0], sv = src[NV * NT];
-      rv[j] = src[2 * NV * NT];
-      // a piece past the row's end: dy = 0 and w = 0 keep it out of the sums
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        const float dyv = ld_f32(dv.v[i]);
-        xh[j][i] = fmaf(ld_f32(sv.v[i]), rs, off);
-        aw[j][i] = fmaf(dyv, xh[j][i], aw[j][i]);
-        ab[j][i] += dyv;
-        g[j][i] = dyv * wv[j][i];
-        sg += g[j][i];
-        sgx = fmaf(g[j][i], xh[j][i], sgx);
-      }
+    for (int i = 0; i < P; ++i) {
+      const float2 xh = __ffma2_rn(sv[i], rs2, off2), g = __fmul2_rn(dv[i], wv[i]);
+      aw[i] = __ffma2_rn(dv[i], xh, aw[i]);
+      ab[i] = __fadd2_rn(ab[i], dv[i]);
+      sg = __fadd2_rn(sg, g);
+      sgx = __ffma2_rn(g, xh, sgx);
     }
-    fetch(t + (D - 1) * step, slot == 0 ? D - 1 : slot - 1);
-    slot = slot == D - 1 ? 0 : slot + 1;
-    sg = warp_sum(sg);
-    sgx = warp_sum(sgx);
+    const float v = warp_sum2(sg.x + sg.y, sgx.x + sgx.y);
     if constexpr (TPR > 32) {
-      // two buffers in turn: a warp can be one row ahead of the slowest
-      // reader of the other buffer, never two
-      if ((tid & 31) == 0) red[buf][tid >> 5] = make_float2(sg, sgx);
-      __syncthreads();
-      sg = sgx = 0.f;
-#pragma unroll
-      for (int i = 0; i < TPR / 32; ++i) {
-        const float2 v = red[buf][i];
-        sg += v.x;
-        sgx += v.y;
-      }
+      if ((tid & 15) == 0) red[buf][(tid >> 4) & 1][tid >> 5] = v;
+    } else {
+      mine = make_float2(__shfl_sync(0xffffffffu, v, 0), __shfl_sync(0xffffffffu, v, 16));
     }
-    const float mg = -sg * inv_d, mgx = -sgx * inv_d;
+  };
+  // dx of row t, in ring slot `at`, from its sums
+  auto finish = [&](int64_t t, int at, int buf, float rs, float off, float2 sums) {
+    if constexpr (TPR > 32) {
+      // lanes 0-15 add up the first sum over the warps, lanes 16-31 the second
+      constexpr int W = TPR / 32, H = W < 16 ? W : 16;
+      const float* r = red[buf][(tid >> 4) & 1];
+      float v = r[tid & (H - 1)];
+      if constexpr (W == 32) v += r[16 + (tid & 15)];
+#pragma unroll
+      for (int o = H / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+      sums = make_float2(__shfl_sync(0xffffffffu, v, 0), __shfl_sync(0xffffffffu, v, 16));
+    }
+    const float2 rs2 = both(rs), off2 = both(off), mg = both(-sums.x * inv_d), mgx = both(-sums.y * inv_d);
     V* o = reinterpret_cast<V*>(dx) + t * nvec;
+    float2 dv[P], sv[P], rv[P];
+    read(at, 0, dv);
+    read(at, 1, sv);
+    read(at, 2, rv);
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      const float2 xh = __ffma2_rn(sv[i], rs2, off2);
+      rv[i] = __ffma2_rn(rs2, __ffma2_rn(xh, mgx, __ffma2_rn(dv[i], wv[i], mg)), rv[i]);
+    }
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int c = lane + j * TPR;
-      V ov;
+      float f[VEC];
 #pragma unroll
-      for (int i = 0; i < VEC; ++i)
-        st_t(ov.v[i], fmaf(rs, fmaf(xh[j][i], mgx, g[j][i] + mg), dsum ? ld_f32(rv[j].v[i]) : 0.f));
-      if (c < nvec) o[c] = ov;
+      for (int i = 0; i < VEC; ++i) f[i] = (j * VEC + i) % 2 ? rv[(j * VEC + i) / 2].y : rv[(j * VEC + i) / 2].x;
+      if (c < nvec) o[c] = from_floats<T, VEC>(f);
     }
+  };
+  asm volatile("cp.async.wait_group %0;" ::"n"(D - 1) : "memory");
+  if (first < L) sum_up(0, 0);  // (whole warps, and whole CTAs where a CTA holds a row)
+  if constexpr (TPR > 32) __syncthreads();
+  int buf = 0, slot = 0;
+  for (int64_t t = first; t < L; t += step, buf ^= 1) {
+    const float rs0 = rs, off0 = -mu * rs;
+    const float2 sums = mine;
+    mu = nmu;
+    rs = nrs;
+    if (t + 2 * step < L) {
+      nmu = mean[t + 2 * step];
+      nrs = rstd[t + 2 * step];
+    }
+    const int next = slot == D - 1 ? 0 : slot + 1;
+    asm volatile("cp.async.wait_group %0;" ::"n"(D - 2) : "memory");
+    if (t + step < L) sum_up(next, buf ^ 1);
+    finish(t, slot, buf, rs0, off0, sums);
+    fetch(t + (int64_t)D * step, slot);
+    slot = next;
+    if constexpr (TPR > 32) __syncthreads();
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
   float* pw = part + (int64_t)blockIdx.x * 2 * d;
   if constexpr (TPR > 32) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        const int c = (lane + j * TPR) * VEC + i;
-        if (c < d) {
-          pw[c] = aw[j][i];
-          pw[d + c] = ab[j][i];
-        }
+    for (int q = 0; q < 2 * P; ++q) {
+      const int c = column(q);
+      if (c < d) {
+        pw[c] = q % 2 ? aw[q / 2].y : aw[q / 2].x;
+        pw[d + c] = q % 2 ? ab[q / 2].y : ab[q / 2].x;
       }
+    }
   } else {
     // the CTA's warps hold the same columns of different rows
     __shared__ float cw[kNormWarps][32];
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
+    for (int q = 0; q < 2 * P; ++q)
 #pragma unroll
-      for (int i = 0; i < VEC; ++i)
+      for (int k = 0; k < 2; ++k) {
+        const float2 two = k ? ab[q / 2] : aw[q / 2];
+        __syncthreads();
+        cw[tid >> 5][lane] = q % 2 ? two.y : two.x;
+        __syncthreads();
+        const int c = column(q);
+        if (tid < 32 && c < d) {
+          float a = 0.f;
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          __syncthreads();
-          cw[tid >> 5][lane] = q ? ab[j][i] : aw[j][i];
-          __syncthreads();
-          const int c = (lane + j * 32) * VEC + i;
-          if (tid < 32 && c < d) {
-            float a = 0.f;
-#pragma unroll
-            for (int r = 0; r < kNormWarps; ++r) a += cw[r][lane];
-            pw[q * d + c] = a;
-          }
+          for (int r = 0; r < kNormWarps; ++r) a += cw[r][lane];
+          pw[k * d + c] = a;
         }
+      }
   }
 }
 
@@ -444,9 +526,12 @@ int vec_of(int d) {
 int bwd_tile_max(const moeblaze_shape& s) { return s.dtype == MOEBLAZE_BF16 ? 16384 : 8192; }
 int bwd_tpr(int d) { return d <= 512 ? 32 : d <= 1024 ? 128 : d <= 2048 ? 256 : d <= 4096 ? 512 : 1024; }
 
-// CTAs of the backward: 1024 threads per SM (512 of a warp a row).  The partial sums are G x 2 d floats.
+// CTAs of the backward: as many as are resident.  The partial sums are G x 2 d floats.
 int64_t bwd_ctas(const moeblaze_shape& s) {
-  const int tpr = bwd_tpr(s.d), rows = tpr == 32 ? kNormWarps : 1, per_sm = tpr == 32 ? 4 : 1024 / tpr;
+  const int tpr = bwd_tpr(s.d), rows = tpr == 32 ? kNormWarps : 1, per_sm =
+      s.dtype == MOEBLAZE_BF16
+          ? (tpr == 32 ? 4 : tpr == 128 ? 8 : tpr == 256 ? 4 : tpr == 512 ? 2 : 1)
+          : (tpr == 32 || tpr == 128 ? 4 : tpr == 256 ? 2 : 1);  // bwd_per_sm
   const int64_t g = (int64_t)per_sm * sm_count(), need = (s.L + rows - 1) / rows;
   return g < need ? g : need;
 }

@@ -693,7 +693,8 @@ __global__ void __launch_bounds__(kBwThreads) router_bwd_small_kernel(
 // columns with their rows of Wr and its partial dWr in registers (64 floats
 // each), so that a token costs it one piece of x, one of dx and the token's
 // dl row, which the CTA shares; the products are packed fp32x2 FMAs over
-// pairs of experts.  part[s] holds split s's sums for router_reduce_kernel.
+// pairs of columns, for which the dl row is held twice over in shared memory
+// (a broadcast load then gives both halves).  part[s] holds split s's sums.
 constexpr int kDgThreads = 128;
 template <int EP>
 constexpr int dg_cpt() {
@@ -702,7 +703,7 @@ constexpr int dg_cpt() {
 constexpr int kDgAhead = 8;  // pieces of x each thread has in flight
 template <typename T, int EP>
 constexpr size_t dg_smem() {
-  return 2 * (size_t)kRT * EP * sizeof(float) + (size_t)kDgAhead * kDgThreads * dg_cpt<EP>() * sizeof(T);
+  return 2 * (size_t)kRT * EP * sizeof(float2) + (size_t)kDgAhead * kDgThreads * dg_cpt<EP>() * sizeof(T);
 }
 
 template <int BYTES>
@@ -747,101 +748,118 @@ __device__ __forceinline__ void store_piece(float* p, const float (&v)[N]) {
 }
 
 template <typename T, int EP>
-__global__ void __launch_bounds__(kDgThreads) router_dense_small_kernel(const T* __restrict__ x,
-                                                                        const float* __restrict__ Wr,
-                                                                        const float* __restrict__ dl, int64_t L, int d,
-                                                                        int E, int64_t split, T* __restrict__ dx,
-                                                                        float* __restrict__ part,
-                                                                        float* __restrict__ part_b) {
+__global__ void __launch_bounds__(kDgThreads, 3) router_dense_small_kernel(const T* __restrict__ x,
+                                                                           const float* __restrict__ Wr,
+                                                                           const float* __restrict__ dl, int64_t L,
+                                                                           int d, int E, int64_t split,
+                                                                           T* __restrict__ dx, float* __restrict__ part,
+                                                                           float* __restrict__ part_b) {
   constexpr int CPT = dg_cpt<EP>(), PB = CPT * (int)sizeof(T);
   extern __shared__ __align__(16) uint8_t rsm[];
-  float* ds = reinterpret_cast<float*>(rsm);             // 2 x [64 tokens][EP], experts >= E zero
+  float2* ds = reinterpret_cast<float2*>(rsm);           // 2 x [64 tokens][EP] (v, v), experts >= E zero
   T* xs = reinterpret_cast<T*>(ds + 2 * kRT * EP);       // [kDgAhead][threads][CPT]: each thread's own pieces
   const int tid = threadIdx.x;
   const int j = (blockIdx.x * kDgThreads + tid) * CPT;
   const bool jv = j < d;
-  float2 w[CPT][EP / 2], acc[CPT][EP / 2];
+  float2 w[CPT / 2][EP], acc[CPT / 2][EP];
 #pragma unroll
-  for (int c = 0; c < CPT; ++c)
+  for (int c = 0; c < CPT / 2; ++c)
 #pragma unroll
-    for (int e = 0; e < EP / 2; ++e) {
+    for (int e = 0; e < EP; ++e) {
       acc[c][e] = make_float2(0.f, 0.f);
-      w[c][e].x = jv && 2 * e < E ? Wr[(int64_t)(j + c) * E + 2 * e] : 0.f;
-      w[c][e].y = jv && 2 * e + 1 < E ? Wr[(int64_t)(j + c) * E + 2 * e + 1] : 0.f;
+      w[c][e].x = jv && e < E ? Wr[(int64_t)(j + 2 * c) * E + e] : 0.f;
+      w[c][e].y = jv && e < E ? Wr[(int64_t)(j + 2 * c + 1) * E + e] : 0.f;
     }
   const int64_t ts = (int64_t)blockIdx.y * split, tend = min(L, ts + split);
   const int n = (int)(tend - ts);  // at least 1: the host makes no empty split
-  auto fetch_x = [&](int t) {
-    if (jv && t < n) cp_piece<PB>(saddr(xs + ((t % kDgAhead) * kDgThreads + tid) * CPT), x + (ts + t) * d + j);
-  };
-  auto stage_dl = [&](int c) {  // rows c*64 .. of the split into buffer c & 1
-    float* dst = ds + (c & 1) * kRT * EP;
-    for (int i = tid; i < kRT * EP; i += kDgThreads) {
-      const int t = c * kRT + i / EP, e = i % EP;
-      const bool ok = t < n && e < E;
-      cp4(saddr(dst + i), ok ? (const void*)(dl + (ts + t) * E + e) : (const void*)dl, ok);
+  const T* xp = x + ts * d + j;    // the piece to copy next
+  const uint32_t xa = saddr(xs + tid * CPT);
+  constexpr uint32_t XS = kDgThreads * PB;
+  // chunk c of dl (64 tokens) into buffer c & 1: through registers, since both halves get a copy
+  float dreg[kRT * EP / kDgThreads];
+  auto load_dl = [&](int c) {
+#pragma unroll
+    for (int q = 0; q < kRT * EP / kDgThreads; ++q) {
+      const int i = q * kDgThreads + tid, t = c * kRT + i / EP, e = i % EP;
+      dreg[q] = t < n && e < E ? dl[(ts + t) * E + e] : 0.f;
     }
   };
-  // copy groups, in order: [dl chunk 0], x pieces 0..AHEAD-1 (one group
-  // each), then per token one group; a chunk's dl joins the group of the
-  // first token of the chunk before it, so it has landed 64 - AHEAD tokens
-  // before it is read
-  stage_dl(0);
-  cp_commit();
+  auto store_dl = [&](int c) {
+#pragma unroll
+    for (int q = 0; q < kRT * EP / kDgThreads; ++q)
+      ds[(c & 1) * kRT * EP + q * kDgThreads + tid] = make_float2(dreg[q], dreg[q]);
+  };
+  load_dl(0);
 #pragma unroll
   for (int t = 0; t < kDgAhead; ++t) {
-    fetch_x(t);
+    if (jv && t < n) cp_piece<PB>(xa + t * XS, xp);
+    xp += d;
     cp_commit();
   }
+  T* op = dx ? dx + ts * d + j : nullptr;
   float bacc = 0.f;
-  for (int t = 0; t < n; ++t) {
-    cp_wait<kDgAhead - 1>();  // token t's piece and everything committed before it
-    if ((t & (kRT - 1)) == 0) {
-      __syncthreads();  // chunk t/64 has landed for every thread; chunk t/64 - 1 is read
-      const int c = t / kRT + 1;
-      if (c * kRT < n) stage_dl(c);
-      const float* dr = ds + ((t / kRT) & 1) * kRT * EP;
-      if (blockIdx.x == 0 && tid < EP)
-        for (int i = 0; i < min(kRT, n - t); ++i) bacc += dr[i * EP + tid];
-    }
-    float xv[CPT];
-    load_piece(xs + ((t % kDgAhead) * kDgThreads + tid) * CPT, xv);
-    fetch_x(t + kDgAhead);
-    cp_commit();
-    const float4* dr = reinterpret_cast<const float4*>(ds + ((t / kRT) & 1) * kRT * EP + (t & (kRT - 1)) * EP);
-    float2 o[CPT];
+  for (int c0 = 0; c0 < n; c0 += kRT) {
+    const int c = c0 / kRT;
+    store_dl(c);
+    __syncthreads();  // chunk c is stored; its buffer's last readers were done a chunk ago
+    if (c0 + kRT < n) load_dl(c + 1);
+    const float2* dr = ds + (c & 1) * kRT * EP;
+    const int m = min(kRT, n - c0);
+    if (blockIdx.x == 0 && tid < EP)
+      for (int i = 0; i < m; ++i) bacc += dr[i * EP + tid].x;
+#pragma unroll 1
+    for (int t8 = 0; t8 < m; t8 += kDgAhead, dr += kDgAhead * EP) {
 #pragma unroll
-    for (int c = 0; c < CPT; ++c) o[c] = make_float2(0.f, 0.f);
+      for (int u = 0; u < kDgAhead; ++u) {
+        // (a token past the split's end: its dl are zero, its piece is stale, its dx is not stored)
+        cp_wait<kDgAhead - 1>();
+        float xv[CPT];
+        load_piece(xs + (u * kDgThreads + tid) * CPT, xv);
+        if (jv && c0 + t8 + u + kDgAhead < n) cp_piece<PB>(xa + u * XS, xp);
+        xp += d;
+        cp_commit();
+        if (t8 + u < m) {
+          float2 o[CPT / 2];
 #pragma unroll
-    for (int q = 0; q < EP / 4; ++q) {
-      const float4 v = dr[q];
-      const float2 a = make_float2(v.x, v.y), b = make_float2(v.z, v.w);
+          for (int q = 0; q < CPT / 2; ++q) o[q] = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int c = 0; c < CPT; ++c) {
-        const float2 x2 = make_float2(xv[c], xv[c]);
-        acc[c][2 * q] = __ffma2_rn(x2, a, acc[c][2 * q]);
-        acc[c][2 * q + 1] = __ffma2_rn(x2, b, acc[c][2 * q + 1]);
-        o[c] = __ffma2_rn(a, w[c][2 * q], o[c]);
-        o[c] = __ffma2_rn(b, w[c][2 * q + 1], o[c]);
+          for (int e = 0; e < EP; e += 2) {
+            const float4 v = *reinterpret_cast<const float4*>(dr + u * EP + e);
+            const float2 d0 = make_float2(v.x, v.y), d1 = make_float2(v.z, v.w);
+#pragma unroll
+            for (int q = 0; q < CPT / 2; ++q) {
+              const float2 x2 = make_float2(xv[2 * q], xv[2 * q + 1]);
+              acc[q][e] = __ffma2_rn(x2, d0, acc[q][e]);
+              acc[q][e + 1] = __ffma2_rn(x2, d1, acc[q][e + 1]);
+              o[q] = __ffma2_rn(d0, w[q][e], o[q]);
+              o[q] = __ffma2_rn(d1, w[q][e + 1], o[q]);
+            }
+          }
+          if (op && jv) {
+            float out[CPT];
+#pragma unroll
+            for (int q = 0; q < CPT / 2; ++q) {
+              out[2 * q] = o[q].x;
+              out[2 * q + 1] = o[q].y;
+            }
+            store_piece(op + (int64_t)u * d, out);
+          }
+        }
       }
-    }
-    if (dx && jv) {
-      float out[CPT];
-#pragma unroll
-      for (int c = 0; c < CPT; ++c) out[c] = o[c].x + o[c].y;
-      store_piece(dx + (ts + t) * d + j, out);
+      if (op) op += (int64_t)kDgAhead * d;
     }
   }
   cp_wait<0>();
   if (jv) {
     float* dst = part + ((int64_t)blockIdx.y * d + j) * E;
 #pragma unroll
-    for (int c = 0; c < CPT; ++c)
+    for (int c = 0; c < CPT / 2; ++c)
 #pragma unroll
-      for (int e = 0; e < EP / 2; ++e) {
-        if (2 * e < E) dst[c * E + 2 * e] = acc[c][e].x;
-        if (2 * e + 1 < E) dst[c * E + 2 * e + 1] = acc[c][e].y;
-      }
+      for (int e = 0; e < EP; ++e)
+        if (e < E) {
+          dst[(2 * c) * E + e] = acc[c][e].x;
+          dst[(2 * c + 1) * E + e] = acc[c][e].y;
+        }
   }
   if (blockIdx.x == 0 && tid < E) part_b[(int64_t)blockIdx.y * E + tid] = bacc;
 }
@@ -979,6 +997,34 @@ __global__ void router_reduce_kernel(const float* __restrict__ part, const float
       for (int s = 0; s < S; ++s) a += part_b[(int64_t)s * E + e];
       dbias[e] = a;
     }
+  }
+}
+
+// dWr and dbias from S splits' sums, in their order: 32 values per block,
+// warp i of its 8 takes splits i, i + 8, ...
+constexpr int kDrWarps = 8;
+__global__ void __launch_bounds__(32 * kDrWarps) router_dense_reduce_kernel(const float* __restrict__ part,
+                                                                            const float* __restrict__ part_b, int64_t n,
+                                                                            int E, int S, float* __restrict__ dWr,
+                                                                            float* __restrict__ dbias) {
+  __shared__ float acc[kDrWarps][32];
+  const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
+  const int64_t i = (int64_t)blockIdx.x * 32 + lane;
+  float a = 0.f;
+  if (i < n + E) {
+    const float* src = i < n ? part + i : part_b + (i - n);
+    const int64_t ld = i < n ? n : E;
+#pragma unroll 8
+    for (int s = wp; s < S; s += kDrWarps) a += src[s * ld];
+  }
+  acc[wp][lane] = a;
+  __syncthreads();
+  if (wp == 0 && i < n + E) {
+    a = 0.f;
+#pragma unroll
+    for (int q = 0; q < kDrWarps; ++q) a += acc[q][lane];
+    if (i < n) dWr[i] = a;
+    else if (dbias) dbias[i - n] = a;
   }
 }
 
@@ -1133,6 +1179,7 @@ int64_t dense_split(const moeblaze_shape& s) {
   const int64_t jb = dense_col_blocks(s), per_sm = padded_experts(s.E) <= 16 ? 3 : 4;
   const int64_t S = (per_sm * sm_count() + jb - 1) / jb;
   const int64_t rows = (s.L + S - 1) / S;
+  if (padded_experts(s.E) <= 16) return rows < kRT ? kRT : rows;
   return (rows + kRT - 1) / kRT * kRT;
 }
 int64_t dense_splits(const moeblaze_shape& s) {
@@ -1178,9 +1225,8 @@ moeblaze_status dense_ep(const moeblaze_shape& s, const void* x, const float* Wr
     count_launch();
   }
   const int64_t n = (int64_t)s.d * s.E;
-  int64_t blocks = (n + s.E + 255) / 256;
-  if (blocks > 8 * (int64_t)sm_count()) blocks = 8 * (int64_t)sm_count();
-  router_reduce_kernel<<<(unsigned)blocks, 256, 0, st>>>(part, part_b, n, s.E, (int)S, dWr, dbias);
+  router_dense_reduce_kernel<<<(unsigned)((n + s.E + 31) / 32), 32 * kDrWarps, 0, st>>>(part, part_b, n, s.E, (int)S,
+                                                                                       dWr, dbias);
   MB_CUDA(cudaGetLastError());
   count_launch();
   return MOEBLAZE_OK;
