@@ -144,6 +144,12 @@ size_t router_dense_ws_bytes(const moeblaze_shape& s);
 moeblaze_status launch_router_dense(const moeblaze_shape& s, const void* x, const float* Wr, const float* dl, float* dWr,
                                     float* dbias, void* dx, void* ws, cudaStream_t st);
 
+// router_grad_tc.cu: the same on the tensor cores (bf16 x, E <= 64)
+bool router_grad_tc(const moeblaze_shape& s);
+size_t router_grad_tc_ws_bytes(const moeblaze_shape& s);
+moeblaze_status launch_router_grad_tc(const moeblaze_shape& s, const void* x, const float* Wr, const float* dl, float* dWr,
+                                      float* dbias, void* dx, void* ws, cudaStream_t st);
+
 // norm.cu
 size_t norm_ws_bytes(const moeblaze_shape& s);
 moeblaze_status launch_layernorm_forward(const moeblaze_shape& s, const void* x, const void* res, const float* w,

@@ -1249,6 +1249,7 @@ moeblaze_status dense_t(const moeblaze_shape& s, const void* x, const float* Wr,
 }  // namespace
 
 size_t router_dense_ws_bytes(const moeblaze_shape& s) {
+  if (router_grad_tc(s)) return router_grad_tc_ws_bytes(s);
   return align_up(sizeof(float) * (size_t)dense_splits(s) * ((size_t)s.d * s.E + s.E), 256);
 }
 
@@ -1259,6 +1260,7 @@ moeblaze_status launch_router_dense(const moeblaze_shape& s, const void* x, cons
     if (dbias) MB_CUDA(cudaMemsetAsync(dbias, 0, sizeof(float) * s.E, st));
     return MOEBLAZE_OK;
   }
+  if (router_grad_tc(s)) return launch_router_grad_tc(s, x, Wr, dl, dWr, dbias, dx, ws, st);
   return s.dtype == MOEBLAZE_BF16 ? dense_t<__nv_bfloat16>(s, x, Wr, dl, dWr, dbias, dx, ws, st)
                                   : dense_t<float>(s, x, Wr, dl, dWr, dbias, dx, ws, st);
 }

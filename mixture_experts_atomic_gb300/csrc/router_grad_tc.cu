@@ -1,0 +1,558 @@
+// The router's gradients from a dense gradient of its logits, on the tensor
+// cores (bf16 x, up to 64 experts):
+//
+//   dWr = x^T dl,  dx = dl Wr^T,  dbias = sum_t dl[t]
+//
+// Both products have the expert count as their small extent and are bound by
+// HBM: dWr reads x once, dx is written once.  dl and Wr are fp32.  They are
+// split into bf16 parts, v = hi + mid + lo (each the rounding of what the
+// parts before it leave), so that every product of two parts is exact and
+// the sums are fp32 in TMEM:
+//   dWr: x . hi + x . mid + x . lo              (dWr is fp32: 24 bits of dl)
+//   dx:  hi . Whi + hi . Wmid + mid . Whi       (dx is bf16: 16 bits of each)
+//
+// split_kernel writes dl's parts as rows [hi | mid | lo] of EP columns each
+// (EP = 16, 32 or 64 experts, padded to whole 64-column blocks), Wr's as
+// [hi | mid], and the CTAs' sums of dl for dbias.
+//
+// dwr_kernel: a CTA owns 256 columns of x and a range of tokens; TMA brings
+// 64 tokens x (256 columns of x, the parts of dl) per stage, both operands
+// MN-major (tokens are the reduction); two M = 128 MMAs share the dl tile,
+// N = 3 EP.  At the end the three parts' sums are added and stored as the
+// range's partial dWr.  dx_kernel: a CTA owns 256 columns of dx, whose rows
+// of Wr stay in shared memory, and walks over 128-token tiles, two TMEM
+// accumulators in turn, so that the epilogue (round, stage, TMA store) of one
+// tile runs under the MMAs of the next.  grad_reduce_kernel adds the partial
+// sums up in a fixed order.
+#include <algorithm>
+
+#include "common.cuh"
+#include "tc_ptx.cuh"
+
+namespace moeblaze {
+namespace tc {
+namespace {
+
+constexpr int kGThreads = 320;  // warp 0 TMA, warp 1 MMA, warps 2-9 epilogue
+constexpr int kGCols = 256;     // columns of x (dx) of a CTA
+constexpr int kDxTokens = 128;
+constexpr int kDxStages = 3;
+constexpr int kDwStages = 4;
+constexpr int kDwTokens = 64;
+
+constexpr int dl_width(int ep) { return (3 * ep + 63) / 64 * 64; }
+constexpr int wr_width(int ep) { return (2 * ep + 63) / 64 * 64; }
+constexpr int dx_blocks(int ep) { return wr_width(ep) / 64; }   // 64-column blocks of hi | mid
+constexpr int dw_atoms(int ep) { return dl_width(ep) / 64; }
+constexpr int dx_smem(int ep) {  // Wr | token tiles | store staging | barriers | alignment
+  return dx_blocks(ep) * kGCols * 128 + kDxStages * dx_blocks(ep) * kDxTokens * 128 + 8 * 2 * 4096 + 256 + 1024;
+}
+constexpr int dw_stage(int ep) { return (kGCols / 64 + dw_atoms(ep)) * 8192; }
+constexpr int dw_smem(int ep) { return kDwStages * dw_stage(ep) + 256 + 1024; }
+
+// ------------------------------------------------------------------ parts
+// rows of dl (L x E fp32) -> [hi | mid | lo], one thread per pair of columns;
+// part_b[block][e] = the block's tokens' sum.  Blocks past the tokens' split
+// Wr (d x E) -> [hi | mid].
+constexpr int kSplitThreads = 256;
+__device__ __forceinline__ void parts(float v, float& hi, float& mid, float& lo) {
+  hi = __bfloat162float(__float2bfloat16_rn(v));
+  const float r = v - hi;  // exact
+  mid = __bfloat162float(__float2bfloat16_rn(r));
+  lo = r - mid;  // exact; rounded when stored
+}
+template <int EP>
+__global__ void __launch_bounds__(kSplitThreads) split_kernel(const float* __restrict__ dl, const float* __restrict__ Wr,
+                                                              int64_t L, int d, int E, int64_t rows, int tblocks,
+                                                              __nv_bfloat16* __restrict__ dls,
+                                                              __nv_bfloat16* __restrict__ ws,
+                                                              float* __restrict__ part_b, int32_t* __restrict__ err) {
+  constexpr int PR = EP / 2, SIDE = kSplitThreads / PR;  // threads of a row, rows side by side
+  const int tid = threadIdx.x, c = (tid % PR) * 2, r0 = tid / PR;
+  if (blockIdx.x == 0 && tid == 0) *err = 0;
+  if ((int)blockIdx.x < tblocks) {
+    constexpr int W = dl_width(EP);
+    const int64_t t0 = blockIdx.x * rows, t1 = min(L, t0 + rows);
+    float2 sum = make_float2(0.f, 0.f);
+#pragma unroll 4
+    for (int64_t t = t0 + r0; t < t1; t += SIDE) {
+      const float a = c < E ? dl[t * E + c] : 0.f, b = c + 1 < E ? dl[t * E + c + 1] : 0.f;
+      sum.x += a;
+      sum.y += b;
+      float ah, am, al, bh, bm, bl;
+      parts(a, ah, am, al);
+      parts(b, bh, bm, bl);
+      uint32_t* o = reinterpret_cast<uint32_t*>(dls + t * W);
+      o[c / 2] = pack_bf16x2(ah, bh);
+      o[(EP + c) / 2] = pack_bf16x2(am, bm);
+      o[(2 * EP + c) / 2] = pack_bf16x2(al, bl);
+      if (W > 3 * EP && c < W - 3 * EP) o[(3 * EP + c) / 2] = 0u;  // (W - 3 EP is EP or 0)
+    }
+    __shared__ float2 acc[kSplitThreads];
+    acc[tid] = sum;
+    __syncthreads();
+    if (tid < PR) {
+      float2 s = make_float2(0.f, 0.f);
+      for (int i = 0; i < SIDE; ++i) {
+        s.x += acc[i * PR + tid].x;
+        s.y += acc[i * PR + tid].y;
+      }
+      if (c < E) part_b[(int64_t)blockIdx.x * E + c] = s.x;
+      if (c + 1 < E) part_b[(int64_t)blockIdx.x * E + c + 1] = s.y;
+    }
+  } else {
+    constexpr int W = wr_width(EP);
+    const int wblocks = (int)gridDim.x - tblocks;
+    for (int j = ((int)blockIdx.x - tblocks) * SIDE + r0; j < d; j += wblocks * SIDE) {
+      const float a = c < E ? Wr[(int64_t)j * E + c] : 0.f, b = c + 1 < E ? Wr[(int64_t)j * E + c + 1] : 0.f;
+      float ah, am, al, bh, bm, bl;
+      parts(a, ah, am, al);
+      parts(b, bh, bm, bl);
+      uint32_t* o = reinterpret_cast<uint32_t*>(ws + (int64_t)j * W);
+      o[c / 2] = pack_bf16x2(ah, bh);
+      o[(EP + c) / 2] = pack_bf16x2(am, bm);
+      if (W > 2 * EP) o[(2 * EP + c) / 2] = o[(3 * EP + c) / 2] = 0u;  // EP = 16: 64 columns
+    }
+  }
+}
+
+struct GParams {
+  CUtensorMap tmA, tmB, tmO;  // dx: dl parts, Wr parts, dx;  dwr: x, dl parts
+  int64_t L;
+  int d, E, tiles, splits;    // tiles: 256-column tiles; splits: CTAs per tile
+  int64_t chunks;             // dwr: 64-token chunks of a split
+  float* part;
+  int32_t* err;
+  uint64_t wait_ns;
+};
+
+__device__ __forceinline__ void tmem_alloc_512(uint32_t slot) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(slot) : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_free_512(uint32_t base) {
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(base) : "memory");
+}
+
+// ------------------------------------------------------------------ dx
+template <int EP>
+__global__ void __launch_bounds__(kGThreads, 1) dx_kernel(const __grid_constant__ GParams p) {
+  constexpr int NB = dx_blocks(EP), SA = NB * kDxTokens * 128, SW = NB * kGCols * 128;
+  extern __shared__ uint8_t g_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(g_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sw = smem;                             // Wr: [block][256 rows][128 bytes]
+  uint8_t* sa = sw + SW;                          // ring: [stage][block][128 tokens][128 bytes]
+  uint8_t* so = sa + kDxStages * SA;              // [warp][2][32 rows][128 bytes]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(so + 8 * 2 * 4096);
+  // full[3], empty[3], wfull, dfull[2], dempty[2], done
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 12);
+  volatile int* abort_s = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  auto full = [&](int s) { return smem_u32(bars + s); };
+  auto empty = [&](int s) { return smem_u32(bars + 3 + s); };
+  const uint32_t wfull = smem_u32(bars + 6), done = smem_u32(bars + 11);
+  auto dfull = [&](int b) { return smem_u32(bars + 7 + b); };
+  auto dempty = [&](int b) { return smem_u32(bars + 9 + b); };
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int n0 = (int)(blockIdx.x % p.tiles) * kGCols, split = (int)(blockIdx.x / p.tiles);
+  const int nw = min(kGCols, p.d - n0);  // a multiple of 64
+  const int64_t tblocks = (p.L + kDxTokens - 1) / kDxTokens;
+  const uint64_t lim = p.wait_ns;
+
+  if (tid == 0) {
+    for (int s = 0; s < kDxStages; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(empty(s), 1);
+    }
+    mbar_init(wfull, 1);
+    mbar_init(done, 1);
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(dfull(b), 1);
+      mbar_init(dempty(b), 8);
+    }
+    *abort_s = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) tmem_alloc_512(smem_u32(tmem_slot));
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 0) {
+    // ============================================================ TMA producer
+    if (lane == 0) {
+      mbar_expect_tx(wfull, (uint32_t)SW);
+      for (int b = 0; b < NB; ++b)
+        for (int r = 0; r < kGCols; r += 128)  // rows past d are filled with zeros
+          tma_load_2d(smem_u32(sw + b * kGCols * 128 + r * 128), &p.tmB, b * 64, n0 + r, wfull);
+      int s = 0;
+      uint32_t ph = 0, armed = 0, armed_par = 0;
+      for (int64_t t = split; t < tblocks; t += p.splits) {
+        if (!wait_bounded(empty(s), ph ^ 1u, abort_s, p.err, lim)) break;
+        mbar_expect_tx(full(s), (uint32_t)SA);
+        for (int b = 0; b < NB; ++b)
+          tma_load_2d(smem_u32(sa + s * SA + b * kDxTokens * 128), &p.tmA, b * 64, (int)(t * kDxTokens), full(s));
+        armed |= 1u << s;
+        armed_par = (armed_par & ~(1u << s)) | (ph << s);
+        if (++s == kDxStages) { s = 0; ph ^= 1u; }
+      }
+      // a CTA that gave up lets its copies in flight land before it exits
+      if (*abort_s) {
+        wait_bounded(wfull, 0u, nullptr, nullptr, kDrainNs);
+        for (int i = 0; i < kDxStages; ++i)
+          if ((armed >> i) & 1u) wait_bounded(full(i), (armed_par >> i) & 1u, nullptr, nullptr, kDrainNs);
+      }
+    }
+  } else if (warp == 1) {
+    // ============================================================ MMA issuer
+    if (lane == 0) {
+      const uint32_t idesc = instr_desc(nw, false, false);
+      const uint32_t w0 = smem_u32(sw);
+      int s = 0, b = 0;
+      uint32_t ph = 0, dph = 0;
+      bool ok = wait_bounded(wfull, 0u, abort_s, p.err, lim);
+      for (int64_t t = split; ok && t < tblocks; t += p.splits) {
+        ok = wait_bounded(dempty(b), dph ^ 1u, abort_s, p.err, lim) && wait_bounded(full(s), ph, abort_s, p.err, lim);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t a0 = smem_u32(sa + s * SA);
+        // slice q (16 experts) of part h: 64-column block (h EP / 16 + q) / 4
+        auto da = [&](int h, int q) {
+          const int i = h * (EP / 16) + q;
+          return smem_desc(a0 + (i / 4) * kDxTokens * 128 + (i % 4) * 32, 16, 1024);
+        };
+        auto dw = [&](int h, int q) {
+          const int i = h * (EP / 16) + q;
+          return smem_desc(w0 + (i / 4) * kGCols * 128 + (i % 4) * 32, 16, 1024);
+        };
+        const uint32_t acc = tmem + b * 256;
+#pragma unroll
+        for (int q = 0; q < EP / 16; ++q) {
+          mma_bf16(acc, da(0, q), dw(0, q), idesc, q > 0);
+          mma_bf16(acc, da(0, q), dw(1, q), idesc, 1u);
+          mma_bf16(acc, da(1, q), dw(0, q), idesc, 1u);
+        }
+        mma_commit(empty(s));
+        mma_commit(dfull(b));
+        if (++s == kDxStages) { s = 0; ph ^= 1u; }
+        b ^= 1;
+        if (b == 0) dph ^= 1u;
+      }
+      mma_commit(done);  // every MMA issued retires before TMEM is freed
+      wait_bounded(done, 0u, nullptr, nullptr, *abort_s ? kDrainNs : lim);
+    }
+    __syncwarp();
+  } else {
+    // ============================================================ epilogue
+    // warp: 32 tokens (its quarter of the TMEM lanes) x half of the columns,
+    // 64 at a time through two staging buffers of its own
+    const int quarter = warp & 3, half = (warp - 2) >> 2;
+    uint8_t* buf = so + (warp - 2) * 2 * 4096;
+    int b = 0, q = 0;
+    uint32_t dph = 0;
+    for (int64_t t = split; t < tblocks; t += p.splits) {
+      // warp-uniform: the TMEM loads below are warp-collective
+      if (!__all_sync(0xffffffffu, wait_bounded(dfull(b), dph, abort_s, p.err, lim))) break;
+      tc_fence_after();
+      const int64_t row0 = t * kDxTokens + quarter * 32;
+      for (int c = half * 128; c < half * 128 + 128; c += 64) {
+        if (c >= nw) break;
+        uint32_t v[64];
+        const uint32_t at = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(b * 256 + c);
+        MB_TMEM_LD32(at, v);
+        {
+          uint32_t* v2 = v + 32;
+          MB_TMEM_LD32(at + 32, v2);
+        }
+        tmem_wait_ld();
+        if (lane == 0) bulk_wait_read<1>();  // the store from this buffer two steps ago has been read
+        __syncwarp();
+        const uint32_t dst = smem_u32(buf + q * 4096) + lane * 128;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          uint4 o;
+          o.x = pack_bf16x2(__uint_as_float(v[8 * i]), __uint_as_float(v[8 * i + 1]));
+          o.y = pack_bf16x2(__uint_as_float(v[8 * i + 2]), __uint_as_float(v[8 * i + 3]));
+          o.z = pack_bf16x2(__uint_as_float(v[8 * i + 4]), __uint_as_float(v[8 * i + 5]));
+          o.w = pack_bf16x2(__uint_as_float(v[8 * i + 6]), __uint_as_float(v[8 * i + 7]));
+          st_shared_v4(dst + ((i ^ (lane & 7)) << 4), o);  // the 128-byte swizzle of the store's map
+        }
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0 && row0 < p.L) tma_store_2d(&p.tmO, smem_u32(buf + q * 4096), n0 + c, (int)row0);
+        if (lane == 0) bulk_commit();
+        q ^= 1;
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(dempty(b));
+      b ^= 1;
+      if (b == 0) dph ^= 1u;
+    }
+    if (lane == 0) bulk_wait<0>();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_free_512(tmem);
+}
+
+// ------------------------------------------------------------------ dWr
+template <int EP>
+__global__ void __launch_bounds__(kGThreads, 1) dwr_kernel(const __grid_constant__ GParams p) {
+  constexpr int NA = kGCols / 64, NB = dw_atoms(EP), SB = dw_stage(EP), N = 3 * EP;
+  extern __shared__ uint8_t g_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(g_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kDwStages * SB);  // full[4], empty[4], done
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kDwStages + 1);
+  volatile int* abort_s = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  auto full = [&](int s) { return smem_u32(bars + s); };
+  auto empty = [&](int s) { return smem_u32(bars + kDwStages + s); };
+  const uint32_t done = smem_u32(bars + 2 * kDwStages);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int m0 = (int)(blockIdx.x % p.tiles) * kGCols, split = (int)(blockIdx.x / p.tiles);
+  const int64_t all = (p.L + kDwTokens - 1) / kDwTokens;
+  const int64_t c0 = split * p.chunks, c1 = min(all, c0 + p.chunks);  // at least one: the host makes no empty split
+  const uint64_t lim = p.wait_ns;
+  if (tid == 0) {
+    for (int s = 0; s < kDwStages; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(empty(s), 1);
+    }
+    mbar_init(done, 1);
+    *abort_s = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) tmem_alloc_512(smem_u32(tmem_slot));
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int s = 0;
+      uint32_t ph = 0, armed = 0, armed_par = 0;
+      for (int64_t c = c0; c < c1; ++c) {
+        if (!wait_bounded(empty(s), ph ^ 1u, abort_s, p.err, lim)) break;
+        mbar_expect_tx(full(s), (uint32_t)SB);
+        const uint32_t at = smem_u32(smem + s * SB);
+        // tokens past L and columns past d are filled with zeros
+        for (int a = 0; a < NA; ++a) tma_load_2d(at + a * 8192, &p.tmA, m0 + a * 64, (int)(c * kDwTokens), full(s));
+        for (int a = 0; a < NB; ++a) tma_load_2d(at + (NA + a) * 8192, &p.tmB, a * 64, (int)(c * kDwTokens), full(s));
+        armed |= 1u << s;
+        armed_par = (armed_par & ~(1u << s)) | (ph << s);
+        if (++s == kDwStages) { s = 0; ph ^= 1u; }
+      }
+      if (*abort_s)
+        for (int i = 0; i < kDwStages; ++i)
+          if ((armed >> i) & 1u) wait_bounded(full(i), (armed_par >> i) & 1u, nullptr, nullptr, kDrainNs);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint32_t idesc = instr_desc(N, true, true);
+      int s = 0;
+      uint32_t ph = 0;
+      for (int64_t c = c0; c < c1; ++c) {
+        if (!wait_bounded(full(s), ph, abort_s, p.err, lim)) break;
+        tc_fence_after();
+        const uint32_t sA = smem_u32(smem + s * SB), sB = sA + NA * 8192;
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+          const uint64_t bd = smem_desc(sB + kk * 2048, 8192, 1024);
+#pragma unroll
+          for (int h = 0; h < 2; ++h)  // columns 0-127 and 128-255 of the tile
+            mma_bf16(tmem + h * 256, smem_desc(sA + h * 16384 + kk * 2048, 8192, 1024), bd, idesc,
+                     (c > c0 || kk > 0) ? 1u : 0u);
+        }
+        mma_commit(empty(s));
+        if (++s == kDwStages) { s = 0; ph ^= 1u; }
+      }
+      mma_commit(done);
+      wait_bounded(done, 0u, nullptr, nullptr, *abort_s ? kDrainNs : lim);
+    }
+    __syncwarp();
+  } else {
+    // warp: 32 columns of x (its quarter of the TMEM lanes) of one 128-column half
+    const int quarter = warp & 3, half = (warp - 2) >> 2;
+    if (__all_sync(0xffffffffu, wait_bounded(done, 0u, abort_s, p.err, lim))) {
+      tc_fence_after();
+      const int m = m0 + half * 128 + quarter * 32 + lane;
+      const uint32_t at = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(half * 256);
+      float* dst = p.part + ((int64_t)split * p.d + m) * p.E;
+#pragma unroll
+      for (int e0 = 0; e0 < EP; e0 += 32) {
+        float sum[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) sum[i] = 0.f;
+        if constexpr (EP == 16) {  // columns hi 0-15, mid 16-31, lo 32-47
+          uint32_t v[32], v2[32];
+          MB_TMEM_LD32(at, v);
+          MB_TMEM_LD32(at + 32, v2);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            sum[i] = (__uint_as_float(v[i]) + __uint_as_float(v[16 + i])) + __uint_as_float(v2[i]);
+        } else {
+#pragma unroll
+          for (int h = 0; h < 3; ++h) {
+            uint32_t v[32];
+            MB_TMEM_LD32(at + h * EP + e0, v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) sum[i] += __uint_as_float(v[i]);
+          }
+        }
+        if (m < p.d) {
+#pragma unroll
+          for (int i = 0; i < (EP < 32 ? EP : 32); ++i)
+            if (e0 + i < p.E) dst[e0 + i] = sum[i];
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_free_512(tmem);
+}
+
+// dWr and dbias: the partial sums in their order, 32 values per block, warp i
+// of its 8 takes partials i, i + 8, ...  A wait that ran out in the kernels
+// before leaves NaN, not a number that looks like a gradient.
+constexpr int kGrWarps = 8;
+__global__ void __launch_bounds__(32 * kGrWarps) grad_reduce_kernel(const float* __restrict__ part,
+                                                                    const float* __restrict__ part_b, int64_t n, int E,
+                                                                    int S, int SB, const int32_t* __restrict__ err,
+                                                                    float* __restrict__ dWr,
+                                                                    float* __restrict__ dbias) {
+  __shared__ float acc[kGrWarps][32];
+  const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
+  const int64_t i = (int64_t)blockIdx.x * 32 + lane;
+  float a = 0.f;
+  if (i < n) {
+#pragma unroll 4
+    for (int s = wp; s < S; s += kGrWarps) a += part[s * n + i];
+  } else if (i < n + E) {
+#pragma unroll 8
+    for (int s = wp; s < SB; s += kGrWarps) a += part_b[(int64_t)s * E + (i - n)];
+  }
+  acc[wp][lane] = a;
+  __syncthreads();
+  if (wp == 0 && i < n + E) {
+    a = 0.f;
+#pragma unroll
+    for (int q = 0; q < kGrWarps; ++q) a += acc[q][lane];
+    if (*err) a = __int_as_float(0x7fc00000);
+    if (i < n) dWr[i] = a;
+    else if (dbias) dbias[i - n] = a;
+  }
+}
+
+int padded(int E) { return E <= 16 ? 16 : E <= 32 ? 32 : 64; }
+
+struct Plan {
+  int tiles, dw_splits, dx_splits, tblocks;
+  int64_t chunks, rows;  // chunks of a dWr split; tokens of a split_kernel block
+  size_t dls, ws, part, part_b, err, bytes;  // offsets in the workspace
+};
+Plan plan_of(const moeblaze_shape& s) {
+  Plan p;
+  const int ep = padded(s.E);
+  p.tiles = (s.d + kGCols - 1) / kGCols;
+  const int64_t all = (s.L + kDwTokens - 1) / kDwTokens;
+  int64_t S = std::max<int64_t>(1, sm_count() / p.tiles);
+  S = std::min(S, all);
+  p.chunks = (all + S - 1) / S;
+  p.dw_splits = (int)((all + p.chunks - 1) / p.chunks);
+  const int64_t tb = (s.L + kDxTokens - 1) / kDxTokens;
+  p.dx_splits = (int)std::min<int64_t>(std::max<int64_t>(1, sm_count() / p.tiles), tb);
+  p.rows = std::max<int64_t>(64, (s.L + 4 * sm_count() - 1) / (4 * sm_count()));
+  p.tblocks = (int)((s.L + p.rows - 1) / p.rows);
+  size_t o = 0;
+  auto take = [&](size_t n) {
+    const size_t at = o;
+    o += align_up(n, 256);
+    return at;
+  };
+  p.dls = take((size_t)s.L * dl_width(ep) * 2);
+  p.ws = take((size_t)s.d * wr_width(ep) * 2);
+  p.part = take((size_t)p.dw_splits * s.d * s.E * sizeof(float));
+  p.part_b = take((size_t)p.tblocks * s.E * sizeof(float));
+  p.err = take(sizeof(int32_t));
+  p.bytes = o;
+  return p;
+}
+
+template <int EP>
+moeblaze_status launch_ep(const moeblaze_shape& s, const void* x, const float* Wr, const float* dl, float* dWr,
+                          float* dbias, void* dx, void* ws, cudaStream_t st) {
+  const Plan pl = plan_of(s);
+  char* w = static_cast<char*>(ws);
+  auto* dls = reinterpret_cast<__nv_bfloat16*>(w + pl.dls);
+  auto* wsp = reinterpret_cast<__nv_bfloat16*>(w + pl.ws);
+  float* part_b = reinterpret_cast<float*>(w + pl.part_b);
+  GParams p;
+  memset(&p, 0, sizeof(p));
+  p.L = s.L;
+  p.d = s.d;
+  p.E = s.E;
+  p.tiles = pl.tiles;
+  p.part = reinterpret_cast<float*>(w + pl.part);
+  p.err = reinterpret_cast<int32_t*>(w + pl.err);
+  int withhold = 0;
+  fault_injection(&p.wait_ns, &withhold);
+  if (p.wait_ns == 0) p.wait_ns = kTimeoutNs;
+
+  const int wblocks = dx ? std::max(1, std::min(sm_count(), s.d / 16)) : 0;
+  split_kernel<EP><<<(unsigned)(pl.tblocks + wblocks), kSplitThreads, 0, st>>>(dl, Wr, s.L, s.d, s.E, pl.rows,
+                                                                               pl.tblocks, dls, wsp, part_b, p.err);
+  MB_CUDA(cudaGetLastError());
+  count_launch();
+  if (dx) {
+    if (!make_map(&p.tmA, dls, dl_width(EP), (uint64_t)s.L, 64, kDxTokens) ||
+        !make_map(&p.tmB, wsp, wr_width(EP), (uint64_t)s.d, 64, 128) ||
+        !make_map(&p.tmO, dx, (uint64_t)s.d, (uint64_t)s.L, 64, 32))
+      return MOEBLAZE_ERR_CUDA;
+    p.splits = pl.dx_splits;
+    MB_CUDA(cudaFuncSetAttribute(dx_kernel<EP>, cudaFuncAttributeMaxDynamicSharedMemorySize, dx_smem(EP)));
+    dx_kernel<EP><<<(unsigned)(pl.tiles * pl.dx_splits), kGThreads, dx_smem(EP), st>>>(p);
+    MB_CUDA(cudaGetLastError());
+    count_launch();
+  }
+  if (!make_map(&p.tmA, x, (uint64_t)s.d, (uint64_t)s.L, 64, kDwTokens) ||
+      !make_map(&p.tmB, dls, dl_width(EP), (uint64_t)s.L, 64, kDwTokens))
+    return MOEBLAZE_ERR_CUDA;
+  p.splits = pl.dw_splits;
+  p.chunks = pl.chunks;
+  MB_CUDA(cudaFuncSetAttribute(dwr_kernel<EP>, cudaFuncAttributeMaxDynamicSharedMemorySize, dw_smem(EP)));
+  dwr_kernel<EP><<<(unsigned)(pl.tiles * pl.dw_splits), kGThreads, dw_smem(EP), st>>>(p);
+  MB_CUDA(cudaGetLastError());
+  const int64_t n = (int64_t)s.d * s.E;
+  grad_reduce_kernel<<<(unsigned)((n + s.E + 31) / 32), 32 * kGrWarps, 0, st>>>(p.part, part_b, n, s.E, pl.dw_splits,
+                                                                                pl.tblocks, p.err, dWr, dbias);
+  MB_CUDA(cudaGetLastError());
+  count_launch(2);
+  return MOEBLAZE_OK;
+}
+
+}  // namespace
+}  // namespace tc
+
+// whole TMA boxes of x, dl and Wr
+bool router_grad_tc(const moeblaze_shape& s) {
+  return s.dtype == MOEBLAZE_BF16 && s.E <= 64 && s.L >= 128 && s.d >= 256;
+}
+
+size_t router_grad_tc_ws_bytes(const moeblaze_shape& s) { return tc::plan_of(s).bytes; }
+
+moeblaze_status launch_router_grad_tc(const moeblaze_shape& s, const void* x, const float* Wr, const float* dl, float* dWr,
+                                      float* dbias, void* dx, void* ws, cudaStream_t st) {
+  switch (tc::padded(s.E)) {
+    case 16: return tc::launch_ep<16>(s, x, Wr, dl, dWr, dbias, dx, ws, st);
+    case 32: return tc::launch_ep<32>(s, x, Wr, dl, dWr, dbias, dx, ws, st);
+  }
+  return tc::launch_ep<64>(s, x, Wr, dl, dWr, dbias, dx, ws, st);
+}
+
+}  // namespace moeblaze
