@@ -17,9 +17,12 @@
 //
 // dwr_kernel: a CTA owns 256 columns of x and a range of tokens; TMA brings
 // 64 tokens x (256 columns of x, the parts of dl) per stage, both operands
-// MN-major (tokens are the reduction); two M = 128 MMAs share the dl tile,
-// N = 3 EP.  At the end the three parts' sums are added and stored as the
-// range's partial dWr.  dx_kernel: a CTA owns 256 columns of dx, whose rows
+// MN-major (tokens are the reduction); two M = 128 MMAs share the dl tile.
+// The tensor cores' fp32 sums are truncated, not rounded, at every step: over
+// thousands of tokens the error is six times a rounded sum's (4.2e-6 of the
+// norm at 3,640 tokens).  So the accumulator is emptied every 512 tokens
+// into fp32 sums in the epilogue warps' registers, two accumulators in turn,
+// and stored at the end as the range's partial dWr.  dx_kernel: a CTA owns 256 columns of dx, whose rows
 // of Wr stay in shared memory, and walks over 128-token tiles, two TMEM
 // accumulators in turn, so that the epilogue (round, stage, TMA store) of one
 // tile runs under the MMAs of the next.  grad_reduce_kernel adds the partial
@@ -39,6 +42,7 @@ constexpr int kDxTokens = 128;
 constexpr int kDxStages = 3;
 constexpr int kDwStages = 4;
 constexpr int kDwTokens = 64;
+constexpr int kDwFlush = 8;     // stages summed in TMEM before the registers take over
 
 constexpr int dl_width(int ep) { return (3 * ep + 63) / 64 * 64; }
 constexpr int wr_width(int ep) { return (2 * ep + 63) / 64 * 64; }
@@ -54,6 +58,7 @@ constexpr int dw_smem(int ep) { return kDwStages * dw_stage(ep) + 256 + 1024; }
 // rows of dl (L x E fp32) -> [hi | mid | lo], one thread per pair of columns;
 // part_b[block][e] = the block's tokens' sum.  Blocks past the tokens' split
 // Wr (d x E) -> [hi | mid].
+__device__ __forceinline__ void allow_dependents();
 constexpr int kSplitThreads = 256;
 __device__ __forceinline__ void parts(float v, float& hi, float& mid, float& lo) {
   hi = __bfloat162float(__float2bfloat16_rn(v));
@@ -69,6 +74,7 @@ __global__ void __launch_bounds__(kSplitThreads) split_kernel(const float* __res
                                                               float* __restrict__ part_b, int32_t* __restrict__ err) {
   constexpr int PR = EP / 2, SIDE = kSplitThreads / PR;  // threads of a row, rows side by side
   const int tid = threadIdx.x, c = (tid % PR) * 2, r0 = tid / PR;
+  allow_dependents();
   if (blockIdx.x == 0 && tid == 0) *err = 0;
   if ((int)blockIdx.x < tblocks) {
     constexpr int W = dl_width(EP);
@@ -126,6 +132,11 @@ struct GParams {
   uint64_t wait_ns;
 };
 
+// programmatic dependents: the next kernel of the call may set itself up on
+// SMs this one has left, and waits for it before it reads anything
+__device__ __forceinline__ void allow_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_prior() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 __device__ __forceinline__ void tmem_alloc_512(uint32_t slot) {
   asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(slot) : "memory");
   asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -157,6 +168,7 @@ __global__ void __launch_bounds__(kGThreads, 1) dx_kernel(const __grid_constant_
   const int nw = min(kGCols, p.d - n0);  // a multiple of 64
   const int64_t tblocks = (p.L + kDxTokens - 1) / kDxTokens;
   const uint64_t lim = p.wait_ns;
+  allow_dependents();
 
   if (tid == 0) {
     for (int s = 0; s < kDxStages; ++s) {
@@ -177,6 +189,7 @@ __global__ void __launch_bounds__(kGThreads, 1) dx_kernel(const __grid_constant_
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  wait_for_prior();
 
   if (warp == 0) {
     // ============================================================ TMA producer
@@ -300,26 +313,37 @@ __global__ void __launch_bounds__(kGThreads, 1) dx_kernel(const __grid_constant_
 // ------------------------------------------------------------------ dWr
 template <int EP>
 __global__ void __launch_bounds__(kGThreads, 1) dwr_kernel(const __grid_constant__ GParams p) {
-  constexpr int NA = kGCols / 64, NB = dw_atoms(EP), SB = dw_stage(EP), N = 3 * EP;
+  // EP = 16, 32: the parts side by side, N = 3 EP columns.  EP = 64: hi | mid,
+  // N = 128, and a second MMA that adds lo to mid's columns (two accumulators
+  // of 3 x 64 do not fit; all three in 64 columns truncate the large hi sum
+  // three times as often, 1.8e-6 instead of 6e-7 of the norm)
+  constexpr int NA = kGCols / 64, NB = dw_atoms(EP), SB = dw_stage(EP), N = EP == 64 ? 128 : 3 * EP;
   extern __shared__ uint8_t g_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(g_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kDwStages * SB);  // full[4], empty[4], done
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kDwStages + 1);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kDwStages * SB);  // full[4], empty[4], done, dfull[2], dempty[2]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kDwStages + 5);
   volatile int* abort_s = reinterpret_cast<volatile int*>(tmem_slot + 1);
   auto full = [&](int s) { return smem_u32(bars + s); };
   auto empty = [&](int s) { return smem_u32(bars + kDwStages + s); };
   const uint32_t done = smem_u32(bars + 2 * kDwStages);
+  auto dfull = [&](int b) { return smem_u32(bars + 2 * kDwStages + 1 + b); };
+  auto dempty = [&](int b) { return smem_u32(bars + 2 * kDwStages + 3 + b); };
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int m0 = (int)(blockIdx.x % p.tiles) * kGCols, split = (int)(blockIdx.x / p.tiles);
   const int64_t all = (p.L + kDwTokens - 1) / kDwTokens;
   const int64_t c0 = split * p.chunks, c1 = min(all, c0 + p.chunks);  // at least one: the host makes no empty split
   const uint64_t lim = p.wait_ns;
+  allow_dependents();
   if (tid == 0) {
     for (int s = 0; s < kDwStages; ++s) {
       mbar_init(full(s), 1);
       mbar_init(empty(s), 1);
     }
     mbar_init(done, 1);
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(dfull(b), 1);
+      mbar_init(dempty(b), 8);
+    }
     *abort_s = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -328,8 +352,10 @@ __global__ void __launch_bounds__(kGThreads, 1) dwr_kernel(const __grid_constant
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  wait_for_prior();
 
   if (warp == 0) {
+    // ============================================================ TMA producer
     if (lane == 0) {
       int s = 0;
       uint32_t ph = 0, armed = 0, armed_par = 0;
@@ -349,66 +375,94 @@ __global__ void __launch_bounds__(kGThreads, 1) dwr_kernel(const __grid_constant
           if ((armed >> i) & 1u) wait_bounded(full(i), (armed_par >> i) & 1u, nullptr, nullptr, kDrainNs);
     }
   } else if (warp == 1) {
+    // ============================================================ MMA issuer
     if (lane == 0) {
       const uint32_t idesc = instr_desc(N, true, true);
-      int s = 0;
-      uint32_t ph = 0;
-      for (int64_t c = c0; c < c1; ++c) {
-        if (!wait_bounded(full(s), ph, abort_s, p.err, lim)) break;
-        tc_fence_after();
-        const uint32_t sA = smem_u32(smem + s * SB), sB = sA + NA * 8192;
+      int s = 0, b = 0;
+      uint32_t ph = 0, dph = 0;
+      bool ok = true;
+      for (int64_t g = c0; ok && g < c1; g += kDwFlush) {
+        ok = wait_bounded(dempty(b), dph ^ 1u, abort_s, p.err, lim);
+        for (int64_t c = g; ok && c < min(c1, g + kDwFlush); ++c) {
+          ok = wait_bounded(full(s), ph, abort_s, p.err, lim);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t sA = smem_u32(smem + s * SB), sB = sA + NA * 8192;
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-          const uint64_t bd = smem_desc(sB + kk * 2048, 8192, 1024);
+          for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
-          for (int h = 0; h < 2; ++h)  // columns 0-127 and 128-255 of the tile
-            mma_bf16(tmem + h * 256, smem_desc(sA + h * 16384 + kk * 2048, 8192, 1024), bd, idesc,
-                     (c > c0 || kk > 0) ? 1u : 0u);
+            for (int h = 0; h < 2; ++h) {  // columns 0-127 and 128-255 of the tile
+              const uint64_t ad = smem_desc(sA + h * 16384 + kk * 2048, 8192, 1024);
+              const uint32_t acc = tmem + b * 256 + h * 128;
+              mma_bf16(acc, ad, smem_desc(sB + kk * 2048, 8192, 1024), idesc, (c > g || kk > 0) ? 1u : 0u);
+              if constexpr (EP == 64)
+                mma_bf16(acc + 64, ad, smem_desc(sB + 2 * 8192 + kk * 2048, 8192, 1024), instr_desc(64, true, true), 1u);
+            }
+          mma_commit(empty(s));
+          if (++s == kDwStages) { s = 0; ph ^= 1u; }
         }
-        mma_commit(empty(s));
-        if (++s == kDwStages) { s = 0; ph ^= 1u; }
+        if (!ok) break;
+        mma_commit(dfull(b));
+        b ^= 1;
+        if (b == 0) dph ^= 1u;
       }
       mma_commit(done);
       wait_bounded(done, 0u, nullptr, nullptr, *abort_s ? kDrainNs : lim);
     }
     __syncwarp();
   } else {
+    // ============================================================ sums
     // warp: 32 columns of x (its quarter of the TMEM lanes) of one 128-column half
     const int quarter = warp & 3, half = (warp - 2) >> 2;
-    if (__all_sync(0xffffffffu, wait_bounded(done, 0u, abort_s, p.err, lim))) {
+    float sum[EP];
+#pragma unroll
+    for (int e = 0; e < EP; ++e) sum[e] = 0.f;
+    int b = 0;
+    uint32_t dph = 0;
+    for (int64_t g = c0; g < c1; g += kDwFlush) {
+      if (!__all_sync(0xffffffffu, wait_bounded(dfull(b), dph, abort_s, p.err, lim))) break;
       tc_fence_after();
-      const int m = m0 + half * 128 + quarter * 32 + lane;
-      const uint32_t at = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(half * 256);
-      float* dst = p.part + ((int64_t)split * p.d + m) * p.E;
+      const uint32_t at = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(b * 256 + half * 128);
+      if constexpr (EP == 16) {  // columns hi 0-15, mid 16-31, lo 32-47 (48-63: not used)
+        uint32_t v[32], v2[32];
+        MB_TMEM_LD32(at, v);
+        MB_TMEM_LD32(at + 32, v2);
+        tmem_wait_ld();
 #pragma unroll
-      for (int e0 = 0; e0 < EP; e0 += 32) {
-        float sum[32];
+        for (int i = 0; i < 16; ++i)
+          sum[i] += __uint_as_float(v[i]) + (__uint_as_float(v[16 + i]) + __uint_as_float(v2[i]));
+      } else if constexpr (EP == 32) {
+        uint32_t v[32], v2[32], v3[32];
+        MB_TMEM_LD32(at, v);
+        MB_TMEM_LD32(at + 32, v2);
+        MB_TMEM_LD32(at + 64, v3);
+        tmem_wait_ld();
 #pragma unroll
-        for (int i = 0; i < 32; ++i) sum[i] = 0.f;
-        if constexpr (EP == 16) {  // columns hi 0-15, mid 16-31, lo 32-47
+        for (int i = 0; i < 32; ++i)
+          sum[i] += __uint_as_float(v[i]) + (__uint_as_float(v2[i]) + __uint_as_float(v3[i]));
+      } else {
+#pragma unroll
+        for (int e0 = 0; e0 < EP; e0 += 32) {
           uint32_t v[32], v2[32];
-          MB_TMEM_LD32(at, v);
-          MB_TMEM_LD32(at + 32, v2);
+          MB_TMEM_LD32(at + e0, v);
+          MB_TMEM_LD32(at + 64 + e0, v2);
           tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            sum[i] = (__uint_as_float(v[i]) + __uint_as_float(v[16 + i])) + __uint_as_float(v2[i]);
-        } else {
-#pragma unroll
-          for (int h = 0; h < 3; ++h) {
-            uint32_t v[32];
-            MB_TMEM_LD32(at + h * EP + e0, v);
-            tmem_wait_ld();
-#pragma unroll
-            for (int i = 0; i < 32; ++i) sum[i] += __uint_as_float(v[i]);
-          }
-        }
-        if (m < p.d) {
-#pragma unroll
-          for (int i = 0; i < (EP < 32 ? EP : 32); ++i)
-            if (e0 + i < p.E) dst[e0 + i] = sum[i];
+          for (int i = 0; i < 32; ++i) sum[e0 + i] += __uint_as_float(v[i]) + __uint_as_float(v2[i]);
         }
       }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(dempty(b));
+      b ^= 1;
+      if (b == 0) dph ^= 1u;
+    }
+    const int m = m0 + half * 128 + quarter * 32 + lane;
+    if (m < p.d) {
+      float* dst = p.part + ((int64_t)split * p.d + m) * p.E;
+#pragma unroll
+      for (int e = 0; e < EP; ++e)
+        if (e < p.E) dst[e] = sum[e];
     }
   }
   tc_fence_before();
@@ -417,35 +471,52 @@ __global__ void __launch_bounds__(kGThreads, 1) dwr_kernel(const __grid_constant
   if (warp == 1) tmem_free_512(tmem);
 }
 
-// dWr and dbias: the partial sums in their order, 32 values per block, warp i
-// of its 8 takes partials i, i + 8, ...  A wait that ran out in the kernels
-// before leaves NaN, not a number that looks like a gradient.
+// dWr and dbias: the partial sums in their order.  A block takes 128 values
+// of dWr (four a lane; d E is a multiple of 64), its warp i partials i, i + 8,
+// ...; the last blocks take dbias, a lane a value.  A wait that ran out in the
+// kernels before leaves NaN, not a number that looks like a gradient.
 constexpr int kGrWarps = 8;
 __global__ void __launch_bounds__(32 * kGrWarps) grad_reduce_kernel(const float* __restrict__ part,
                                                                     const float* __restrict__ part_b, int64_t n, int E,
                                                                     int S, int SB, const int32_t* __restrict__ err,
                                                                     float* __restrict__ dWr,
                                                                     float* __restrict__ dbias) {
-  __shared__ float acc[kGrWarps][32];
+  __shared__ float4 acc[kGrWarps][32];
+  wait_for_prior();
   const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
-  const int64_t i = (int64_t)blockIdx.x * 32 + lane;
-  float a = 0.f;
-  if (i < n) {
+  const int64_t blocks = (n + 127) / 128;
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+  const bool weights = blockIdx.x < blocks;
+  const int64_t i = weights ? ((int64_t)blockIdx.x * 32 + lane) * 4 : ((int64_t)blockIdx.x - blocks) * 32 + lane;
+  if (weights) {
+    if (i < n) {
 #pragma unroll 4
-    for (int s = wp; s < S; s += kGrWarps) a += part[s * n + i];
-  } else if (i < n + E) {
+      for (int s = wp; s < S; s += kGrWarps) {
+        const float4 v = *reinterpret_cast<const float4*>(part + s * n + i);
+        a.x += v.x; a.y += v.y; a.z += v.z; a.w += v.w;
+      }
+    }
+  } else if (i < E) {
 #pragma unroll 8
-    for (int s = wp; s < SB; s += kGrWarps) a += part_b[(int64_t)s * E + (i - n)];
+    for (int s = wp; s < SB; s += kGrWarps) a.x += part_b[(int64_t)s * E + i];
   }
   acc[wp][lane] = a;
   __syncthreads();
-  if (wp == 0 && i < n + E) {
-    a = 0.f;
+  if (wp != 0 || i >= (weights ? n : E)) return;
+  a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int q = 0; q < kGrWarps; ++q) a += acc[q][lane];
-    if (*err) a = __int_as_float(0x7fc00000);
-    if (i < n) dWr[i] = a;
-    else if (dbias) dbias[i - n] = a;
+  for (int q = 0; q < kGrWarps; ++q) {
+    const float4 v = acc[q][lane];
+    a.x += v.x; a.y += v.y; a.z += v.z; a.w += v.w;
+  }
+  if (*err) a.x = a.y = a.z = a.w = __int_as_float(0x7fc00000);
+  if (!weights) {
+    if (dbias) dbias[i] = a.x;
+  } else {  // dWr itself may start on any float
+    dWr[i] = a.x;
+    dWr[i + 1] = a.y;
+    dWr[i + 2] = a.z;
+    dWr[i + 3] = a.w;
   }
 }
 
@@ -484,6 +555,21 @@ Plan plan_of(const moeblaze_shape& s) {
   return p;
 }
 
+template <typename... Params, typename... Args>
+cudaError_t launch_after(void (*kern)(Params...), int64_t grid, int block, size_t smem, cudaStream_t st, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3((unsigned)block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, static_cast<Params>(args)...);
+}
+
 template <int EP>
 moeblaze_status launch_ep(const moeblaze_shape& s, const void* x, const float* Wr, const float* dl, float* dWr,
                           float* dbias, void* dx, void* ws, cudaStream_t st) {
@@ -516,8 +602,7 @@ moeblaze_status launch_ep(const moeblaze_shape& s, const void* x, const float* W
       return MOEBLAZE_ERR_CUDA;
     p.splits = pl.dx_splits;
     MB_CUDA(cudaFuncSetAttribute(dx_kernel<EP>, cudaFuncAttributeMaxDynamicSharedMemorySize, dx_smem(EP)));
-    dx_kernel<EP><<<(unsigned)(pl.tiles * pl.dx_splits), kGThreads, dx_smem(EP), st>>>(p);
-    MB_CUDA(cudaGetLastError());
+    MB_CUDA(launch_after(dx_kernel<EP>, (int64_t)pl.tiles * pl.dx_splits, kGThreads, dx_smem(EP), st, p));
     count_launch();
   }
   if (!make_map(&p.tmA, x, (uint64_t)s.d, (uint64_t)s.L, 64, kDwTokens) ||
@@ -526,12 +611,10 @@ moeblaze_status launch_ep(const moeblaze_shape& s, const void* x, const float* W
   p.splits = pl.dw_splits;
   p.chunks = pl.chunks;
   MB_CUDA(cudaFuncSetAttribute(dwr_kernel<EP>, cudaFuncAttributeMaxDynamicSharedMemorySize, dw_smem(EP)));
-  dwr_kernel<EP><<<(unsigned)(pl.tiles * pl.dw_splits), kGThreads, dw_smem(EP), st>>>(p);
-  MB_CUDA(cudaGetLastError());
+  MB_CUDA(launch_after(dwr_kernel<EP>, (int64_t)pl.tiles * pl.dw_splits, kGThreads, dw_smem(EP), st, p));
   const int64_t n = (int64_t)s.d * s.E;
-  grad_reduce_kernel<<<(unsigned)((n + s.E + 31) / 32), 32 * kGrWarps, 0, st>>>(p.part, part_b, n, s.E, pl.dw_splits,
-                                                                                pl.tblocks, p.err, dWr, dbias);
-  MB_CUDA(cudaGetLastError());
+  MB_CUDA(launch_after(grad_reduce_kernel, (n + 127) / 128 + (s.E + 31) / 32, 32 * kGrWarps, 0, st, (const float*)p.part,
+                       (const float*)part_b, n, (int)s.E, pl.dw_splits, pl.tblocks, (const int32_t*)p.err, dWr, dbias));
   count_launch(2);
   return MOEBLAZE_OK;
 }
