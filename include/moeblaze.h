@@ -351,8 +351,8 @@ MOEBLAZE_API moeblaze_status moeblaze_router_backward_logits(const moeblaze_shap
  *   losses[1] = sum_t lse[t]^2 / N          (both 0 when no token is active)
  *
  * moeblaze_balance_forward:
- *   logits   device (L,E) fp32, 16-byte aligned (of tokens that are not valid
- *            nothing is read)
+ *   logits   device (L,E) fp32, 16-byte aligned (those of tokens that are not
+ *            valid may hold anything, NaN included)
  *   topk_ids device (L,K) int32     valid device (L) uint8 or NULL
  *   losses   device (2) fp32        counts device (E+1) int32, counts[E] = N
  *   lse      device (L) fp32, -inf for tokens that are not active

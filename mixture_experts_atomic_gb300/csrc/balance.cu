@@ -19,15 +19,16 @@
 //
 // A token's row of logits lies in TE lanes of a warp, EPT vectors of VEC
 // experts each; P_e is summed in a lane's registers over the CTA's tokens,
-// then over the warps and (balance_losses_kernel, in double) over the CTAs,
-// always in the same order: repeatable to the bit.
+// then over the warps and (balance_losses_kernel) over the CTAs, always in
+// the same order: repeatable to the bit.
 #include "common.cuh"
 
 namespace moeblaze {
 namespace {
 
-constexpr int kBalThreads = 256;
+constexpr int kBalThreads = 1024;  // forward: one CTA an SM, few partial sums
 constexpr int kBalWarps = kBalThreads / 32;
+constexpr int kBwdThreads = 256;
 
 // floats of one CTA's partial sums: P[E], z, counts[E] (int), active (int)
 __host__ __device__ inline int bal_cols(int E) { return 2 * E + 2; }
@@ -71,12 +72,14 @@ __global__ void __launch_bounds__(kBalThreads) balance_fwd_kernel(const float* _
                                                                   int K, float* __restrict__ lse_out,
                                                                   float* __restrict__ part) {
   constexpr int GROUPS = kBalThreads / TE;  // tokens side by side in the CTA
+  constexpr int KL = (kMaxK + TE - 1) / TE;  // slots a lane counts
   extern __shared__ float sm[];
   float* ps = sm;                                               // [warps][E]
   int* cs = reinterpret_cast<int*>(sm + kBalWarps * E);         // [E]
   float* zs = reinterpret_cast<float*>(cs + E);                 // [warps]
   int* as = reinterpret_cast<int*>(zs + kBalWarps);             // [warps]
   const int tid = threadIdx.x, te = tid % TE, grp = tid / TE, warp = tid >> 5, lane = tid & 31;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   for (int e = tid; e < E; e += kBalThreads) cs[e] = 0;
   __syncthreads();
   float pa[EPT][VEC];
@@ -89,27 +92,36 @@ __global__ void __launch_bounds__(kBalThreads) balance_fwd_kernel(const float* _
   // every lane of a warp runs the same number of passes: the shuffles below are warp-wide
   for (int64_t t0 = (int64_t)blockIdx.x * GROUPS * U; t0 < L; t0 += (int64_t)gridDim.x * GROUPS * U) {
     float l[U][EPT][VEC];
+    int id[U][KL];
     bool on[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int64_t t = t0 + u * GROUPS + grp;
       on[u] = t < L && (!valid || valid[t]);
+#pragma unroll
+      for (int q = 0; q < KL; ++q) id[u][q] = q * TE + te < K && t < L ? ids[t * K + q * TE + te] : -1;
       load_row<VEC, TE, EPT>(logits + t * E, E, te, on[u], l[u]);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int64_t t = t0 + u * GROUPS + grp;
       float m = -INFINITY;
-      bool some = false;  // a logit above -inf (or NaN, which the sum then carries)
 #pragma unroll
       for (int j = 0; j < EPT; ++j)
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          m = fmaxf(m, l[u][j][i]);
-          some = some || !(l[u][j][i] == -INFINITY);
-        }
+        for (int i = 0; i < VEC; ++i) m = fmaxf(m, l[u][j][i]);
       m = group_max<TE>(m);
-      const bool act = group_max<TE>(some ? 1.f : 0.f) > 0.f;
+      bool act = m > -INFINITY;
+      if (__any_sync(0xffffffffu, on[u] && !act)) {
+        // the maximum leaves NaN out: a row of NaN (and -inf) is active, and its sum NaN
+        bool nan = false;
+#pragma unroll
+        for (int j = 0; j < EPT; ++j)
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) nan = nan || l[u][j][i] != l[u][j][i];
+        const float any_nan = group_max<TE>(nan ? 1.f : 0.f);  // by every lane: a shuffle
+        if (any_nan > 0.f) act = true;
+      }
       float s = 0.f;
 #pragma unroll
       for (int j = 0; j < EPT; ++j)
@@ -125,10 +137,9 @@ __global__ void __launch_bounds__(kBalThreads) balance_fwd_kernel(const float* _
         for (int j = 0; j < EPT; ++j)
 #pragma unroll
           for (int i = 0; i < VEC; ++i) pa[j][i] = fmaf(l[u][j][i], inv, pa[j][i]);
-        for (int k = te; k < K; k += TE) {
-          const int e = ids[t * K + k];
-          if ((unsigned)e < (unsigned)E) atomicAdd(&cs[e], 1);
-        }
+#pragma unroll
+        for (int q = 0; q < KL; ++q)
+          if ((unsigned)id[u][q] < (unsigned)E) atomicAdd(&cs[id[u][q]], 1);
         if (te == 0) {
           za = fmaf(lse, lse, za);
           ++na;
@@ -178,61 +189,110 @@ __global__ void __launch_bounds__(kBalThreads) balance_fwd_kernel(const float* _
   }
 }
 
-// One CTA adds the G partial rows up (double, in a fixed order) and forms the
-// two losses and the counts (the last one: the active tokens).
-constexpr int kLossThreads = 1024;
+// One cluster adds the G partial rows up, each of its CTAs an equal range of
+// them, and its first CTA forms the two losses and the counts (the last one:
+// the active tokens).  Sums of positive fp32 numbers in trees of a few levels.
+constexpr int kLossThreads = 512;
+constexpr int kLossCluster = 8;
 __global__ void __launch_bounds__(kLossThreads) balance_losses_kernel(const float* __restrict__ part, int G, int E,
                                                                       int K, float* __restrict__ losses,
                                                                       int32_t* __restrict__ counts) {
-  extern __shared__ double dsm[];
+  extern __shared__ float fsm[];
   const int C = bal_cols(E);           // at most 1026 columns
   const int tid = threadIdx.x;
   const int rows = C >= kLossThreads ? 1 : kLossThreads / C;  // threads side by side on a column
-  double* col = dsm;                   // [rows][C]
+  float* col = fsm;                    // [rows][C]; the integer columns hold int bits
+  int rank, ranks;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(ranks));
+  const int g0 = G * rank / ranks, g1 = G * (rank + 1) / ranks;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   for (int i = tid; i < rows * C; i += kLossThreads) {
     const int c = i % C, r = i / C;
-    const bool is_int = c > E;
-    double a = 0.0;
-#pragma unroll 8
-    for (int g = r; g < G; g += rows) {
+    float a = 0.f;
+    int n = 0;
+#pragma unroll 4
+    for (int g = g0 + r; g < g1; g += rows) {
       const float v = part[(int64_t)g * C + c];
-      a += is_int ? (double)__float_as_int(v) : (double)v;
+      if (c > E) n += __float_as_int(v);
+      else a += v;
     }
-    col[r * C + c] = a;
+    col[i] = c > E ? __int_as_float(n) : a;
+  }
+  // column c over n values, ld floats apart; integer columns as integers
+  auto add_up = [&](const float* p, int c, int n, int ld) {
+    float a = 0.f;
+    int k = 0;
+    for (int r = 0; r < n; ++r) {
+      const float v = p[r * ld];
+      if (c > E) k += __float_as_int(v);
+      else a += v;
+    }
+    return c > E ? __int_as_float(k) : a;
+  };
+  __syncthreads();
+  for (int c = tid; c < C; c += kLossThreads) col[c] = add_up(col + c, c, rows, C);
+  if (ranks > 1) {
+    // the first CTA reads the others' columns
+    __syncthreads();
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    float v[3];
+    if (rank == 0) {
+      int q = 0;
+      for (int c = tid; c < C; c += kLossThreads, ++q) {
+        float a = 0.f;
+        int k = 0;
+        for (int r = 0; r < ranks; ++r) {
+          uint32_t at;
+          float x;
+          asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                       : "=r"(at)
+                       : "r"((uint32_t)__cvta_generic_to_shared(col + c)), "r"(r));
+          asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(at) : "memory");
+          if (c > E) k += __float_as_int(x);
+          else a += x;
+        }
+        v[q] = c > E ? __int_as_float(k) : a;
+      }
+    }
+    __syncthreads();
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    if (rank != 0) return;
+    int q = 0;
+    for (int c = tid; c < C; c += kLossThreads, ++q) col[c] = v[q];
   }
   __syncthreads();
-  for (int c = tid; c < C; c += kLossThreads) {
-    double a = col[c];
-    for (int r = 1; r < rows; ++r) a += col[r * C + c];
-    col[c] = a;
-  }
-  __syncthreads();
-  const double n = col[2 * E + 1], inv = n > 0.0 ? 1.0 / n : 0.0;
-  for (int e = tid; e < E; e += kLossThreads) counts[e] = (int32_t)col[E + 1 + e];
-  if (tid == 0) counts[E] = (int32_t)n;
+  const int n = __float_as_int(col[2 * E + 1]);
+  for (int e = tid; e < E; e += kLossThreads) counts[e] = __float_as_int(col[E + 1 + e]);
+  if (tid == 0) counts[E] = n;
   if (tid < 32) {
-    double b = 0.0;
-    for (int e = tid; e < E; e += 32) b += (col[E + 1 + e] * inv / K) * (col[e] * inv);
+    float b = 0.f;  // sum_e count_e (sum_t p_te)
+    for (int e = tid; e < E; e += 32) b = fmaf((float)__float_as_int(col[E + 1 + e]), col[e], b);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) b += __shfl_xor_sync(0xffffffffu, b, o);
     if (tid == 0) {
-      losses[0] = (float)(E * b);
-      losses[1] = (float)(col[E] * inv);
+      const float inv = n > 0 ? 1.f / (float)n : 0.f;
+      losses[0] = ((float)E / (float)K) * (b * inv) * inv;
+      losses[1] = inv * col[E];
     }
   }
 }
 
 template <int VEC, int TE, int EPT, int U>
-__global__ void __launch_bounds__(kBalThreads) balance_bwd_kernel(
+__global__ void __launch_bounds__(kBwdThreads) balance_bwd_kernel(
     const float* __restrict__ logits, const float* __restrict__ lse_in, const int32_t* __restrict__ counts,
     const float* __restrict__ dloss, const int32_t* __restrict__ ids, const float* __restrict__ gates,
     const float* __restrict__ dgates, int64_t L, int E, int K, float* __restrict__ dlogits) {
-  constexpr int GROUPS = kBalThreads / TE;
+  constexpr int GROUPS = kBwdThreads / TE;
+  constexpr int KL = (kMaxK + TE - 1) / TE;  // slots a lane holds
+  constexpr int ROW = EPT * TE * VEC + 4;    // a group's row in shared memory (rows 4 banks apart)
+  __shared__ __align__(16) float rows[GROUPS * ROW];
   const int tid = threadIdx.x, te = tid % TE, grp = tid / TE;
+  float* row = rows + grp * ROW;
   const int n = counts[E];
   const float inv_n = n > 0 ? 1.f / (float)n : 0.f;
   const float A = dloss[0] * (float)E * inv_n, Z = 2.f * dloss[1] * inv_n;
-  // loads relative to the mean load, exact until the last product: E count_e - sum of counts
+  // loads relative to the mean load: the integer part of the difference is exact
   __shared__ int total_s;
   if (tid < 32) {
     int a = 0;
@@ -242,28 +302,40 @@ __global__ void __launch_bounds__(kBalThreads) balance_bwd_kernel(
     if (tid == 0) total_s = a;
   }
   __syncthreads();
-  const double scale = n > 0 ? 1.0 / ((double)n * K * E) : 0.0;
+  // (in fp32 and integers: fp64 runs at 1/64 of its rate, and this is every CTA's start)
+  const int mean = total_s / E;
+  const float rest = (float)(total_s % E) / (float)E, scale = n > 0 ? 1.f / ((float)n * (float)K) : 0.f;
   float f[EPT][VEC];
 #pragma unroll
   for (int j = 0; j < EPT; ++j)
 #pragma unroll
     for (int i = 0; i < VEC; ++i) {
       const int e = (j * TE + te) * VEC + i;
-      f[j][i] = e < E ? (float)((double)((int64_t)E * counts[e] - total_s) * scale) : 0.f;
+      f[j][i] = e < E ? ((float)(counts[e] - mean) - rest) * scale : 0.f;
     }
   for (int64_t t0 = (int64_t)blockIdx.x * GROUPS * U; t0 < L; t0 += (int64_t)gridDim.x * GROUPS * U) {
-    float l[U][EPT][VEC], lse[U];
+    float l[U][EPT][VEC], lse[U], g[U][KL], dg[U][KL];
+    int id[U][KL];
     bool act[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int64_t t = t0 + u * GROUPS + grp;
       lse[u] = t < L ? lse_in[t] : -INFINITY;
-      act[u] = !(lse[u] == -INFINITY);
-      load_row<VEC, TE, EPT>(logits + t * E, E, te, act[u], l[u]);
+      // (the logits of a token that is not active are loaded and not used)
+      load_row<VEC, TE, EPT>(logits + t * E, E, te, t < L, l[u]);
+#pragma unroll
+      for (int q = 0; q < KL; ++q) {
+        const int k = q * TE + te;
+        const bool in = gates && k < K && t < L;
+        g[u][q] = in ? gates[t * K + k] : 0.f;
+        dg[u][q] = in ? dgates[t * K + k] : 0.f;
+        id[u][q] = in ? ids[t * K + k] : -1;
+      }
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int64_t t = t0 + u * GROUPS + grp;
+      act[u] = !(lse[u] == -INFINITY);
       float dot = 0.f;
 #pragma unroll
       for (int j = 0; j < EPT; ++j)
@@ -278,23 +350,36 @@ __global__ void __launch_bounds__(kBalThreads) balance_bwd_kernel(
       for (int j = 0; j < EPT; ++j)
 #pragma unroll
         for (int i = 0; i < VEC; ++i) l[u][j][i] *= fmaf(A, f[j][i] - dot, zl);
-      if (gates && act[u]) {
-        float g[kMaxK], dg[kMaxK], sd = 0.f;
+      if (gates) {
+        // the chosen experts' share: the row goes through shared memory,
+        // where the lane that holds a slot adds to that slot's expert, slot
+        // after slot (an expert named twice gets both, in their order)
+        float sd = 0.f;
 #pragma unroll
-        for (int k = 0; k < kMaxK; ++k) {
-          g[k] = k < K ? gates[t * K + k] : 0.f;
-          dg[k] = k < K ? dgates[t * K + k] : 0.f;
-          sd = fmaf(g[k], dg[k], sd);
+        for (int q = 0; q < KL; ++q) sd = fmaf(g[u][q], dg[u][q], sd);
+        sd = group_sum<TE>(sd);
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < EPT; ++j) {
+          FVec<VEC> o;
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) o.v[i] = l[u][j][i];
+          *reinterpret_cast<FVec<VEC>*>(row + (j * TE + te) * VEC) = o;
         }
 #pragma unroll
         for (int k = 0; k < kMaxK; ++k) {
-          const int e = k < K ? ids[t * K + k] : -1;
-          const float v = g[k] * (dg[k] - sd);
+          if (k < K) {
+            __syncwarp();
+            const int e = id[u][k / TE];
+            if (te == k % TE && (unsigned)e < (unsigned)E) row[e] += g[u][k / TE] * (dg[u][k / TE] - sd);
+          }
+        }
+        __syncwarp();
 #pragma unroll
-          for (int j = 0; j < EPT; ++j)
+        for (int j = 0; j < EPT; ++j) {
+          const FVec<VEC> o = *reinterpret_cast<const FVec<VEC>*>(row + (j * TE + te) * VEC);
 #pragma unroll
-            for (int i = 0; i < VEC; ++i)
-              if (e == (j * TE + te) * VEC + i) l[u][j][i] += v;
+          for (int i = 0; i < VEC; ++i) l[u][j][i] = o.v[i];
         }
       }
       if (t < L) {
@@ -312,9 +397,9 @@ __global__ void __launch_bounds__(kBalThreads) balance_bwd_kernel(
 }
 
 // tokens of one pass of a CTA
-template <int TE, int U>
+template <int THREADS, int TE, int U>
 constexpr int pass_tokens() {
-  return kBalThreads / TE * U;
+  return THREADS / TE * U;
 }
 
 int64_t bal_ctas(int64_t L, int tokens, int per_sm) {
@@ -331,9 +416,9 @@ constexpr int kBwdPerSm = 4;
 #define MB_BAL_LAYOUT(E, CALL)                            \
   do {                                                    \
     if ((E) % 4 == 0) {                                   \
-      if ((E) <= 8) return CALL(4, 2, 1, 4);              \
-      if ((E) <= 16) return CALL(4, 4, 1, 4);             \
-      if ((E) <= 32) return CALL(4, 8, 1, 4);             \
+      if ((E) <= 8) return CALL(4, 2, 1, 2);              \
+      if ((E) <= 16) return CALL(4, 4, 1, 2);             \
+      if ((E) <= 32) return CALL(4, 8, 1, 2);             \
       if ((E) <= 64) return CALL(4, 8, 2, 2);             \
       if ((E) <= 128) return CALL(4, 16, 2, 2);           \
       if ((E) <= 256) return CALL(4, 16, 4, 1);           \
@@ -351,13 +436,30 @@ constexpr int kBwdPerSm = 4;
 template <int VEC, int TE, int EPT, int U>
 moeblaze_status fwd_layout(const moeblaze_shape& s, const float* logits, const int32_t* ids, const uint8_t* valid,
                            float* losses, int32_t* counts, float* lse, float* part, cudaStream_t st) {
-  const int64_t G = bal_ctas(s.L, pass_tokens<TE, U>(), kFwdPerSm);
+  const int64_t G = bal_ctas(s.L, pass_tokens<kBalThreads, TE, U>(), kFwdPerSm);
   const size_t sm = sizeof(float) * ((size_t)kBalWarps * s.E + s.E + 2 * kBalWarps);
-  balance_fwd_kernel<VEC, TE, EPT, U><<<(unsigned)G, kBalThreads, sm, st>>>(logits, ids, valid, s.L, s.E, s.K, lse, part);
+  auto kern = balance_fwd_kernel<VEC, TE, EPT, U>;
+  MB_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm));
+  kern<<<(unsigned)G, kBalThreads, sm, st>>>(logits, ids, valid, s.L, s.E, s.K, lse, part);
   MB_CUDA(cudaGetLastError());
   const int C = bal_cols(s.E), rows = C >= kLossThreads ? 1 : kLossThreads / C;
-  balance_losses_kernel<<<1, kLossThreads, sizeof(double) * rows * C, st>>>(part, (int)G, s.E, s.K, losses, counts);
-  MB_CUDA(cudaGetLastError());
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  // few partial rows: one CTA adds them up as fast
+  const unsigned cluster = G >= 4 * kLossCluster ? kLossCluster : 1;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.gridDim = dim3(cluster);
+  cfg.blockDim = dim3(kLossThreads);
+  cfg.dynamicSmemBytes = sizeof(float) * rows * C;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  MB_CUDA(cudaLaunchKernelEx(&cfg, balance_losses_kernel, (const float*)part, (int)G, (int)s.E, (int)s.K, losses,
+                             counts));
   count_launch(2);
   return MOEBLAZE_OK;
 }
@@ -366,8 +468,8 @@ template <int VEC, int TE, int EPT, int U>
 moeblaze_status bwd_layout(const moeblaze_shape& s, const float* logits, const float* lse, const int32_t* counts,
                            const float* dloss, const int32_t* ids, const float* gates, const float* dgates,
                            float* dlogits, cudaStream_t st) {
-  const int64_t G = bal_ctas(s.L, pass_tokens<TE, U>(), kBwdPerSm);
-  balance_bwd_kernel<VEC, TE, EPT, U><<<(unsigned)G, kBalThreads, 0, st>>>(logits, lse, counts, dloss, ids, gates,
+  const int64_t G = bal_ctas(s.L, pass_tokens<kBwdThreads, TE, U>(), kBwdPerSm);
+  balance_bwd_kernel<VEC, TE, EPT, U><<<(unsigned)G, kBwdThreads, 0, st>>>(logits, lse, counts, dloss, ids, gates,
                                                                            dgates, s.L, s.E, s.K, dlogits);
   MB_CUDA(cudaGetLastError());
   count_launch();
