@@ -331,14 +331,17 @@ MOEBLAZE_API moeblaze_status moeblaze_router_dispatch_build_logits(const moeblaz
  * the losses' and the gates' share):
  *   dWr = x^T dlogits, dbias = sum_t dlogits[t], dx = dlogits Wr^T
  *   dlogits device (L,E) fp32, 16-byte aligned
- *   x, Wr, dWr, dbias, dx: as moeblaze_router_backward
+ *   x, Wr, dWr, dbias, dx: as moeblaze_router_backward; accumulate != 0: dx
+ *           is added to what is there (moeblaze_backward's dX, say; a bf16 dx
+ *           may be rounded before the sum as well as after it)
  *   ws      device moeblaze_router_backward_logits_workspace_bytes(s) bytes
  * Shape, limits and repeatability as moeblaze_router_backward (K is not used
  * but has to be valid). */
 MOEBLAZE_API size_t moeblaze_router_backward_logits_workspace_bytes(const moeblaze_shape* s);
 MOEBLAZE_API moeblaze_status moeblaze_router_backward_logits(const moeblaze_shape* s, const void* x, const float* Wr,
                                                              const float* dlogits, float* dWr, float* dbias, void* dx,
-                                                             void* ws, size_t ws_bytes, moeblaze_stream stream);
+                                                             int32_t accumulate, void* ws, size_t ws_bytes,
+                                                             moeblaze_stream stream);
 
 /* ------------------------------------------------------- the router's losses
  * The load-balance and z losses of a router on its logits, the tokens per

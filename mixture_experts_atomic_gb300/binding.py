@@ -106,7 +106,7 @@ def lib():
         L.moeblaze_router_dispatch_build.restype = ctypes.c_int
         L.moeblaze_router_forward_logits.argtypes = [SP, P, P, P, P, P, P, P]
         L.moeblaze_router_dispatch_build_logits.argtypes = [SP, P, P, P, P, P, P, DP, P, sz, P]
-        L.moeblaze_router_backward_logits.argtypes = [SP, P, P, P, P, P, P, P, sz, P]
+        L.moeblaze_router_backward_logits.argtypes = [SP, P, P, P, P, P, P, ctypes.c_int32, P, sz, P]
         L.moeblaze_balance_forward.argtypes = [SP, P, P, P, P, P, P, P, sz, P]
         L.moeblaze_balance_backward.argtypes = [SP, P, P, P, P, P, P, P, P, P]
         L.moeblaze_layernorm_forward.argtypes = [SP, P, P, P, P, ctypes.c_float, P, P, P, P, P]
@@ -227,9 +227,9 @@ def moeblaze_router_backward_logits_workspace_bytes(shape: Shape) -> int:
     return lib().moeblaze_router_backward_logits_workspace_bytes(ctypes.byref(shape))
 
 
-def moeblaze_router_backward_logits(shape, x, Wr, dlogits, dWr, dbias, dx, ws, ws_bytes, stream) -> int:
-    return lib().moeblaze_router_backward_logits(ctypes.byref(shape), x, Wr, dlogits, dWr, dbias, dx, ws, ws_bytes,
-                                                 stream)
+def moeblaze_router_backward_logits(shape, x, Wr, dlogits, dWr, dbias, dx, accumulate, ws, ws_bytes, stream) -> int:
+    return lib().moeblaze_router_backward_logits(ctypes.byref(shape), x, Wr, dlogits, dWr, dbias, dx, int(accumulate),
+                                                 ws, ws_bytes, stream)
 
 
 def moeblaze_balance_workspace_bytes(shape: Shape) -> int:
@@ -608,9 +608,9 @@ def router_backward(shape: Shape, x, Wr, topk_ids, gates, dgates, dWr, dbias, dx
     _check(st, "moeblaze_router_backward")
 
 
-def router_backward_logits(shape: Shape, x, Wr, dlogits, dWr, dbias, dx, ws=None, stream=None):
+def router_backward_logits(shape: Shape, x, Wr, dlogits, dWr, dbias, dx, ws=None, stream=None, accumulate=False):
     """Router gradients from a dense gradient of its logits: fills dWr (d,E) fp32, dbias (E) fp32 and dx (L,d)
-    (dbias and dx may be None).  `ws` is a device byte tensor of
+    (dbias and dx may be None); with accumulate dx is added to what is there.  `ws` is a device byte tensor of
     moeblaze_router_backward_logits_workspace_bytes(shape) bytes (allocated here when None)."""
     dt = _TORCH_DTYPE[shape.dtype]
     _args((x, "x", (shape.L, shape.d), dt, False), (Wr, "Wr", (shape.d, shape.E), torch.float32, False),
@@ -622,7 +622,7 @@ def router_backward_logits(shape: Shape, x, Wr, dlogits, dWr, dbias, dx, ws=None
         ws = _bytes(n, Wr.device)
     _bytes_arg(ws, "ws", n)
     st = moeblaze_router_backward_logits(shape, _ptr(x), _ptr(Wr), _ptr(dlogits), _ptr(dWr), _ptr(dbias), _ptr(dx),
-                                         _ptr(ws), n, _stream(stream))
+                                         accumulate, _ptr(ws), n, _stream(stream))
     _check(st, "moeblaze_router_backward_logits")
 
 

@@ -79,15 +79,21 @@ class RouterGrad:
 
     def __init__(self, L: int, d: int, E: int, dtype: torch.dtype, device="cuda"):
         self.shape = B.make_shape(L, d, 0, E, 1, dtype, "identity")
-        self.dx = torch.empty((L, d), dtype=dtype, device=device)
+        self._dx: Optional[torch.Tensor] = None
         self.dWr = torch.empty((d, E), dtype=torch.float32, device=device)
         self.dbias = torch.empty((E,), dtype=torch.float32, device=device)
         self._ws = B._bytes(B.moeblaze_router_backward_logits_workspace_bytes(self.shape), device)
 
-    def backward(self, x, Wr, dlogits):
-        """(dx, dWr, dbias)"""
-        B.router_backward_logits(self.shape, x, Wr, dlogits, self.dWr, self.dbias, self.dx, self._ws)
-        return self.dx, self.dWr, self.dbias
+    def backward(self, x, Wr, dlogits, add_to=None):
+        """(dx, dWr, dbias); with add_to (L,d) dx is added to it in place, and it is returned."""
+        dx = add_to
+        if dx is None:
+            if self._dx is None:
+                self._dx = torch.empty_like(x)
+            dx = self._dx
+        B.router_backward_logits(self.shape, x, Wr, dlogits, self.dWr, self.dbias, dx, self._ws,
+                                 accumulate=add_to is not None)
+        return dx, self.dWr, self.dbias
 
 
 class MoEBlock:
@@ -123,7 +129,6 @@ class MoEBlock:
         self._kept = None
         du, dW1, dW2, dW3, dgates = self.layer.backward(dout, u, gates, p["W1"], p.get("W2"), p["W3"])
         dlogits = self.loss.backward(self.logits, dlosses, None, ids, gates, dgates)
-        du_r, dWr, dbias = self.grad.backward(u, p["Wr"], dlogits)
-        du.add_(du_r)
+        du, dWr, dbias = self.grad.backward(u, p["Wr"], dlogits, add_to=du)
         dx, dnw, dnb = self.norm.backward(du, s, mean, rstd, p["norm_w"], dsum)
         return {"x": dx, "norm_w": dnw, "norm_b": dnb, "Wr": dWr, "bias": dbias, "W1": dW1, "W2": dW2, "W3": dW3}

@@ -432,15 +432,17 @@ size_t moeblaze_router_backward_logits_workspace_bytes(const moeblaze_shape* s) 
 }
 
 moeblaze_status moeblaze_router_backward_logits(const moeblaze_shape* s, const void* x, const float* Wr,
-                                                const float* dlogits, float* dWr, float* dbias, void* dx, void* ws,
-                                                size_t ws_bytes, moeblaze_stream stream) {
+                                                const float* dlogits, float* dWr, float* dbias, void* dx,
+                                                int32_t accumulate, void* ws, size_t ws_bytes,
+                                                moeblaze_stream stream) {
   moeblaze_status r = check_router_shape(s);
   if (r != MOEBLAZE_OK) return r;
   if (!ok_ptr4(Wr) || !ok_ptr4(dWr) || (dbias && !ok_ptr4(dbias))) return MOEBLAZE_ERR_INVALID_ARG;
   if (s->L > 0 && (!ok_ptr(x) || !ok_ptr(dlogits) || (dx && !ok_ptr(dx)))) return MOEBLAZE_ERR_INVALID_ARG;
   if (ws_bytes < router_dense_ws_bytes(*s)) return MOEBLAZE_ERR_WORKSPACE;
   if (s->L > 0 && !ok_ptr(ws)) return MOEBLAZE_ERR_INVALID_ARG;
-  return launch_router_dense(*s, x, Wr, dlogits, dWr, dbias, dx, ws, reinterpret_cast<cudaStream_t>(stream));
+  return launch_router_dense(*s, x, Wr, dlogits, dWr, dbias, dx, accumulate != 0, ws,
+                             reinterpret_cast<cudaStream_t>(stream));
 }
 
 moeblaze_status moeblaze_layernorm_forward(const moeblaze_shape* s, const void* x, const void* residual,

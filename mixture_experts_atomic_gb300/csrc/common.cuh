@@ -139,16 +139,16 @@ moeblaze_status launch_router_forward(const moeblaze_shape& s, const void* x, co
 moeblaze_status launch_router_backward(const moeblaze_shape& s, const void* x, const float* Wr, const int32_t* ids,
                                        const float* gates, const float* dgates, float* dWr, float* dbias, void* dx,
                                        void* ws, cudaStream_t st);
-// the router's gradients from a dense gradient of the logits
+// the router's gradients from a dense gradient of the logits; add: dx is added to what is there
 size_t router_dense_ws_bytes(const moeblaze_shape& s);
 moeblaze_status launch_router_dense(const moeblaze_shape& s, const void* x, const float* Wr, const float* dl, float* dWr,
-                                    float* dbias, void* dx, void* ws, cudaStream_t st);
+                                    float* dbias, void* dx, bool add, void* ws, cudaStream_t st);
 
 // router_grad_tc.cu: the same on the tensor cores (bf16 x, E <= 64)
 bool router_grad_tc(const moeblaze_shape& s);
 size_t router_grad_tc_ws_bytes(const moeblaze_shape& s);
 moeblaze_status launch_router_grad_tc(const moeblaze_shape& s, const void* x, const float* Wr, const float* dl, float* dWr,
-                                      float* dbias, void* dx, void* ws, cudaStream_t st);
+                                      float* dbias, void* dx, bool add, void* ws, cudaStream_t st);
 
 // norm.cu
 size_t norm_ws_bytes(const moeblaze_shape& s);

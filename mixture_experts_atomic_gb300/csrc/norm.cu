@@ -235,15 +235,20 @@ __device__ __forceinline__ float warp_sum2(float a, float b) {
   return v;
 }
 
+// the first n of 16 bytes, the rest zeros (not read)
+__device__ __forceinline__ void copy_part(void* dst, const void* src, int n) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src),
+               "r"(n)
+               : "memory");
+}
 template <int BYTES>
 __device__ __forceinline__ void copy_ahead(void* dst, const void* src) {
+  static_assert(BYTES == 4 || BYTES == 8 || BYTES == 16, "");
   const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
   if constexpr (BYTES == 16)
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
-  else if constexpr (BYTES >= 4)
+  else
     asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(d), "l"(src), "n"(BYTES) : "memory");
-  else  // too small to copy asynchronously
-    *static_cast<__nv_bfloat16*>(dst) = *static_cast<const __nv_bfloat16*>(src);
 }
 
 // threads on an SM: 512 where a row of 8 fp32 elements a thread, or the 16
@@ -265,7 +270,15 @@ constexpr size_t bwd_smem() {
   return (size_t)bwd_depth<T, VEC, TPR, NV>() * 3 * VEC * NV * sizeof(T) * norm_threads<TPR>();
 }
 
-template <typename T, int VEC, int TPR, int NV>
+// Rows that do not start on 16 bytes (SHIFT): the 16-byte words of a dense
+// matrix lie at the same places of every VEC-th row, and a CTA's rows are a
+// multiple of VEC apart.  So a thread still holds whole words, whose columns
+// begin `shift` before the row, the same for all of the CTA's rows; the first
+// and the last word of a row are shared with its neighbours and masked.
+// (Measured at 8191 x 1409 fp32 and 32768 x 1409 bf16 before: 41 and 248 us
+// with pieces of one element, 50 and 161 us with rows copied whole and read
+// by element.)
+template <typename T, int VEC, int TPR, int NV, bool SHIFT>
 __global__ void __launch_bounds__(norm_threads<TPR>(), bwd_per_sm<T, TPR>()) norm_bwd_kernel(
     const T* dy, const T* s, const float* __restrict__ mean, const float* __restrict__ rstd,
     const float* __restrict__ w, const T* dsum, int64_t L, int d, T* dx, float* __restrict__ part) {
@@ -275,19 +288,29 @@ __global__ void __launch_bounds__(norm_threads<TPR>(), bwd_per_sm<T, TPR>()) nor
   V* ring = reinterpret_cast<V*>(nsm);  // [D][3][NV][threads]: dy, s, dsum
   __shared__ float red[2][2][32];  // [buffer][sum][warp]
   const int tid = threadIdx.x, lane = TPR == 32 ? (tid & 31) : tid;
-  const int nvec = d / VEC;
+  const int64_t step = (int64_t)gridDim.x * ROWS;
+  const int64_t first = (int64_t)blockIdx.x * ROWS + (TPR == 32 ? (tid >> 5) : 0);
+  // a word's columns: word c of a row holds columns c VEC - shift, ...
+  const int shift = SHIFT ? (int)((first * d) % VEC) : 0;
+  const int nvec = SHIFT ? (shift + d + VEC - 1) / VEC : d / VEC;
   const float inv_d = 1.f / (float)d;
   // sums and weights of this thread's columns, in pairs of elements
   constexpr int P = NV * VEC / 2;
-  auto column = [&](int q) { return (lane + (q / VEC) * TPR) * VEC + q % VEC; };  // of element q
+  auto column = [&](int q) { return (lane + (q / VEC) * TPR) * VEC + q % VEC - shift; };  // of element q
+  auto inside = [&](int c) { return SHIFT ? (unsigned)c < (unsigned)d : c < d; };
   float2 aw[P], ab[P], wv[P];
 #pragma unroll
   for (int i = 0; i < P; ++i) {
     aw[i] = ab[i] = both(0.f);
-    wv[i].x = column(2 * i) < d ? w[column(2 * i)] : 0.f;
-    wv[i].y = column(2 * i + 1) < d ? w[column(2 * i + 1)] : 0.f;
+    wv[i].x = inside(column(2 * i)) ? w[column(2 * i)] : 0.f;
+    wv[i].y = inside(column(2 * i + 1)) ? w[column(2 * i + 1)] : 0.f;
   }
-  // array a of ring slot `at`, as pairs
+  // whether one of this thread's words is a row's first or last
+  bool edge = false;
+  if constexpr (SHIFT)
+#pragma unroll
+    for (int j = 0; j < NV; ++j) edge = edge || lane + j * TPR == 0 || lane + j * TPR == nvec - 1;
+  // array a of ring slot `at`, as pairs, the neighbours' elements as zeros
   auto read = [&](int at, int a, float2 (&v)[P]) {
     float f[NV][VEC];
 #pragma unroll
@@ -295,9 +318,14 @@ __global__ void __launch_bounds__(norm_threads<TPR>(), bwd_per_sm<T, TPR>()) nor
 #pragma unroll
     for (int i = 0; i < P; ++i)
       v[i] = make_float2(f[2 * i / VEC][2 * i % VEC], f[(2 * i + 1) / VEC][(2 * i + 1) % VEC]);
+    if (SHIFT && edge) {
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        if (!inside(column(2 * i))) v[i].x = 0.f;
+        if (!inside(column(2 * i + 1))) v[i].y = 0.f;
+      }
+    }
   };
-  const int64_t step = (int64_t)gridDim.x * ROWS;
-  const int64_t first = (int64_t)blockIdx.x * ROWS + (TPR == 32 ? (tid >> 5) : 0);
   // pieces past the row's end stay zero
 #pragma unroll
   for (int q = 0; q < D * 3 * NV; ++q)
@@ -309,11 +337,18 @@ __global__ void __launch_bounds__(norm_threads<TPR>(), bwd_per_sm<T, TPR>()) nor
       for (int j = 0; j < NV; ++j) {
         const int c = lane + j * TPR;
         if (c < nvec) {
-          const int64_t o = t * nvec + c;
+          const int64_t o = t * d - shift + c * VEC;
           V* dst = ring + (at * 3 * NV + j) * NT + tid;
-          copy_ahead<sizeof(V)>(dst, reinterpret_cast<const V*>(dy) + o);
-          copy_ahead<sizeof(V)>(dst + NV * NT, reinterpret_cast<const V*>(s) + o);
-          if (dsum) copy_ahead<sizeof(V)>(dst + 2 * NV * NT, reinterpret_cast<const V*>(dsum) + o);
+          if (SHIFT && o + VEC > L * d) {  // the tensor ends inside this word
+            const int n = (int)(L * d - o) * (int)sizeof(T);
+            copy_part(dst, dy + o, n);
+            copy_part(dst + NV * NT, s + o, n);
+            if (dsum) copy_part(dst + 2 * NV * NT, dsum + o, n);
+          } else {
+            copy_ahead<sizeof(V)>(dst, dy + o);
+            copy_ahead<sizeof(V)>(dst + NV * NT, s + o);
+            if (dsum) copy_ahead<sizeof(V)>(dst + 2 * NV * NT, dsum + o);
+          }
         }
       }
     }
@@ -373,7 +408,7 @@ __global__ void __launch_bounds__(norm_threads<TPR>(), bwd_per_sm<T, TPR>()) nor
       sums = make_float2(__shfl_sync(0xffffffffu, v, 0), __shfl_sync(0xffffffffu, v, 16));
     }
     const float2 rs2 = both(rs), off2 = both(off), mg = both(-sums.x * inv_d), mgx = both(-sums.y * inv_d);
-    V* o = reinterpret_cast<V*>(dx) + t * nvec;
+    T* o = dx + t * d - shift;
     float2 dv[P], sv[P], rv[P];
     read(at, 0, dv);
     read(at, 1, sv);
@@ -389,7 +424,13 @@ __global__ void __launch_bounds__(norm_threads<TPR>(), bwd_per_sm<T, TPR>()) nor
       float f[VEC];
 #pragma unroll
       for (int i = 0; i < VEC; ++i) f[i] = (j * VEC + i) % 2 ? rv[(j * VEC + i) / 2].y : rv[(j * VEC + i) / 2].x;
-      if (c < nvec) o[c] = from_floats<T, VEC>(f);
+      if (SHIFT && edge) {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i)
+          if (inside(c * VEC + i - shift)) st_t(o[(int64_t)c * VEC + i], f[i]);
+      } else if (c < nvec) {
+        *reinterpret_cast<V*>(o + (int64_t)c * VEC) = from_floats<T, VEC>(f);
+      }
     }
   };
   asm volatile("cp.async.wait_group %0;" ::"n"(D - 1) : "memory");
@@ -410,8 +451,8 @@ __global__ void __launch_bounds__(norm_threads<TPR>(), bwd_per_sm<T, TPR>()) nor
     if (t + step < L) sum_up(next, buf ^ 1);
     finish(t, slot, buf, rs0, off0, sums);
     fetch(t + (int64_t)D * step, slot);
-    slot = next;
     if constexpr (TPR > 32) __syncthreads();
+    slot = next;
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
   float* pw = part + (int64_t)blockIdx.x * 2 * d;
@@ -419,30 +460,32 @@ __global__ void __launch_bounds__(norm_threads<TPR>(), bwd_per_sm<T, TPR>()) nor
 #pragma unroll
     for (int q = 0; q < 2 * P; ++q) {
       const int c = column(q);
-      if (c < d) {
+      if (inside(c)) {
         pw[c] = q % 2 ? aw[q / 2].y : aw[q / 2].x;
         pw[d + c] = q % 2 ? ab[q / 2].y : ab[q / 2].x;
       }
     }
   } else {
-    // the CTA's warps hold the same columns of different rows
-    __shared__ float cw[kNormWarps][32];
+    // the CTA's warps hold rows of their own (and, with SHIFT, the columns
+    // in places of their own): one warp after the other adds its sums
+    __shared__ float csum[2][32 * NV * VEC];
+    for (int r = 0; r < kNormWarps; ++r) {
+      if ((tid >> 5) == r) {
 #pragma unroll
-    for (int q = 0; q < 2 * P; ++q)
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const float2 two = k ? ab[q / 2] : aw[q / 2];
-        __syncthreads();
-        cw[tid >> 5][lane] = q % 2 ? two.y : two.x;
-        __syncthreads();
-        const int c = column(q);
-        if (tid < 32 && c < d) {
-          float a = 0.f;
-#pragma unroll
-          for (int r = 0; r < kNormWarps; ++r) a += cw[r][lane];
-          pw[k * d + c] = a;
+        for (int q = 0; q < 2 * P; ++q) {
+          const int c = column(q);
+          if (inside(c)) {
+            csum[0][c] = (r ? csum[0][c] : 0.f) + (q % 2 ? aw[q / 2].y : aw[q / 2].x);
+            csum[1][c] = (r ? csum[1][c] : 0.f) + (q % 2 ? ab[q / 2].y : ab[q / 2].x);
+          }
         }
       }
+      __syncthreads();
+    }
+    for (int c = tid; c < d; c += NT) {
+      pw[c] = csum[0][c];
+      pw[d + c] = csum[1][c];
+    }
   }
 }
 
@@ -524,15 +567,21 @@ int vec_of(int d) {
 // ones in a CTA of as many threads as they need; 16 elements a thread for
 // bf16 rows of 8193 to 16384 (of fp32 rows shared memory holds no ring).
 int bwd_tile_max(const moeblaze_shape& s) { return s.dtype == MOEBLAZE_BF16 ? 16384 : 8192; }
+bool bwd_aligned(const moeblaze_shape& s) { return s.d % (s.dtype == MOEBLAZE_BF16 ? 8 : 4) == 0; }
+// elements of the words a row lies in
+int bwd_room(const moeblaze_shape& s) { return bwd_aligned(s) ? s.d : s.d + (s.dtype == MOEBLAZE_BF16 ? 14 : 6); }
 int bwd_tpr(int d) { return d <= 512 ? 32 : d <= 1024 ? 128 : d <= 2048 ? 256 : d <= 4096 ? 512 : 1024; }
 
 // CTAs of the backward: as many as are resident.  The partial sums are G x 2 d floats.
+// A multiple of 8, so that a CTA's rows are one (SHIFT), unless each has one row.
 int64_t bwd_ctas(const moeblaze_shape& s) {
-  const int tpr = bwd_tpr(s.d), rows = tpr == 32 ? kNormWarps : 1, per_sm =
-      s.dtype == MOEBLAZE_BF16
-          ? (tpr == 32 ? 4 : tpr == 128 ? 8 : tpr == 256 ? 4 : tpr == 512 ? 2 : 1)
-          : (tpr == 32 || tpr == 128 ? 4 : tpr == 256 ? 2 : 1);  // bwd_per_sm
-  const int64_t g = (int64_t)per_sm * sm_count(), need = (s.L + rows - 1) / rows;
+  const int tpr = bwd_tpr(bwd_room(s)), rows = tpr == 32 ? kNormWarps : 1;
+  const int per_sm = s.dtype == MOEBLAZE_BF16
+                         ? (tpr == 32 ? 4 : tpr == 128 ? 8 : tpr == 256 ? 4 : tpr == 512 ? 2 : 1)
+                         : (tpr == 32 || tpr == 128 ? 4 : tpr == 256 ? 2 : 1);  // bwd_per_sm
+  int64_t g = (int64_t)per_sm * sm_count();
+  if (g > 8) g -= g % 8;
+  const int64_t need = (s.L + rows - 1) / rows;
   return g < need ? g : need;
 }
 
@@ -547,12 +596,12 @@ moeblaze_status fwd_tile(const moeblaze_shape& s, const void* x, const void* res
   return MOEBLAZE_OK;
 }
 
-template <typename T, int VEC, int TPR, int NV>
+template <typename T, int VEC, int TPR, int NV, bool SHIFT>
 moeblaze_status bwd_tile(const moeblaze_shape& s, const void* dy, const void* sum, const float* mean,
                          const float* rstd, const float* w, const void* dsum, void* dx, float* dw, float* db,
                          float* part, cudaStream_t st) {
   const int64_t G = bwd_ctas(s);
-  auto kern = norm_bwd_kernel<T, VEC, TPR, NV>;
+  auto kern = norm_bwd_kernel<T, VEC, TPR, NV, SHIFT>;
   constexpr size_t sm = bwd_smem<T, VEC, TPR, NV>();
   MB_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm));
   kern<<<(unsigned)G, norm_threads<TPR>(), sm, st>>>((const T*)dy, (const T*)sum, mean, rstd, w, (const T*)dsum, s.L,
@@ -585,21 +634,22 @@ moeblaze_status fwd_vec(const moeblaze_shape& s, const void* x, const void* res,
 #undef MB_CALL
 }
 
-template <typename T, int VEC>
-moeblaze_status bwd_vec(const moeblaze_shape& s, const void* dy, const void* sum, const float* mean, const float* rstd,
-                        const float* w, const void* dsum, void* dx, float* dw, float* db, float* part,
-                        cudaStream_t st) {
-  constexpr int NV = 8 / VEC;  // pieces of a thread
-#define MB_CALL(TPR, N) bwd_tile<T, VEC, TPR, N>(s, dy, sum, mean, rstd, w, dsum, dx, dw, db, part, st)
-  if (s.d <= 256) return MB_CALL(32, NV);
-  switch (bwd_tpr(s.d)) {
+template <typename T, bool SHIFT>
+moeblaze_status bwd_shift(const moeblaze_shape& s, const void* dy, const void* sum, const float* mean,
+                          const float* rstd, const float* w, const void* dsum, void* dx, float* dw, float* db,
+                          float* part, cudaStream_t st) {
+  constexpr int VEC = 16 / (int)sizeof(T), NV = 8 / VEC;  // words of a thread
+#define MB_CALL(TPR, N) bwd_tile<T, VEC, TPR, N, SHIFT>(s, dy, sum, mean, rstd, w, dsum, dx, dw, db, part, st)
+  const int room = bwd_room(s);
+  if (room <= 256) return MB_CALL(32, NV);
+  switch (bwd_tpr(room)) {
     case 32: return MB_CALL(32, 2 * NV);
     case 128: return MB_CALL(128, NV);
     case 256: return MB_CALL(256, NV);
     case 512: return MB_CALL(512, NV);
   }
   if constexpr (sizeof(T) == 2)
-    if (s.d > 8192) return MB_CALL(1024, 2 * NV);
+    if (room > 8192) return MB_CALL(1024, 2 * NV);
   return MB_CALL(1024, NV);
 #undef MB_CALL
 }
@@ -625,8 +675,7 @@ moeblaze_status fwd_t(const moeblaze_shape& s, const void* x, const void* res, c
 template <typename T>
 moeblaze_status bwd_t(const moeblaze_shape& s, const void* dy, const void* sum, const float* mean, const float* rstd,
                       const float* w, const void* dsum, void* dx, float* dw, float* db, float* part, cudaStream_t st) {
-  const int v = vec_of<T>(s.d);
-  if (s.d > bwd_tile_max(s)) {
+  if (bwd_room(s) > bwd_tile_max(s)) {
     norm_bwd_wide_kernel<T><<<(unsigned)s.L, 1024, 0, st>>>((const T*)dy, (const T*)sum, mean, rstd, w, (const T*)dsum,
                                                             s.d, (T*)dx);
     MB_CUDA(cudaGetLastError());
@@ -639,18 +688,15 @@ moeblaze_status bwd_t(const moeblaze_shape& s, const void* dy, const void* sum, 
     count_launch(3);
     return MOEBLAZE_OK;
   }
-  if constexpr (sizeof(T) == 2)
-    if (v == 8) return bwd_vec<T, 8>(s, dy, sum, mean, rstd, w, dsum, dx, dw, db, part, st);
-  if (v == 4) return bwd_vec<T, 4>(s, dy, sum, mean, rstd, w, dsum, dx, dw, db, part, st);
-  if (v == 2) return bwd_vec<T, 2>(s, dy, sum, mean, rstd, w, dsum, dx, dw, db, part, st);
-  return bwd_vec<T, 1>(s, dy, sum, mean, rstd, w, dsum, dx, dw, db, part, st);
+  return bwd_aligned(s) ? bwd_shift<T, false>(s, dy, sum, mean, rstd, w, dsum, dx, dw, db, part, st)
+                        : bwd_shift<T, true>(s, dy, sum, mean, rstd, w, dsum, dx, dw, db, part, st);
 }
 
 }  // namespace
 
 size_t norm_ws_bytes(const moeblaze_shape& s) {
   if (s.L == 0) return 0;
-  const int64_t G = s.d > bwd_tile_max(s) ? (s.L < kWideSplits ? s.L : kWideSplits) : bwd_ctas(s);
+  const int64_t G = bwd_room(s) > bwd_tile_max(s) ? (s.L < kWideSplits ? s.L : kWideSplits) : bwd_ctas(s);
   return (size_t)G * 2 * s.d * sizeof(float);
 }
 

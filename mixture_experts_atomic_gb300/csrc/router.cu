@@ -119,7 +119,9 @@ __device__ __forceinline__ void stage_wr(float* dst, const float* Wr, int k0, in
 }
 
 // ------------------------------------------------------------------ forward
-template <typename T, int EP>
+// LG: the logits are stored too (a variant of its own: the stores cost the
+// widest layouts registers)
+template <typename T, int EP, bool LG>
 __global__ void __launch_bounds__(kRThreads) router_fwd_kernel(const T* __restrict__ x, const float* __restrict__ Wr,
                                                                const float* __restrict__ bias, int64_t L, int d, int E,
                                                                int K, int32_t* __restrict__ ids,
@@ -185,7 +187,7 @@ __global__ void __launch_bounds__(kRThreads) router_fwd_kernel(const T* __restri
     for (int i = 0; i < Ly::RPT; ++i) {
       acc[i][j] = e < E ? acc[i][j] + b : -FLT_MAX;
       const int64_t t = t0 + tr * Ly::RPT + i;
-      if (logits && e < E && t < L) logits[t * E + e] = acc[i][j];
+      if (LG && e < E && t < L) logits[t * E + e] = acc[i][j];
     }
   }
 
@@ -752,7 +754,7 @@ __global__ void __launch_bounds__(kDgThreads, 3) router_dense_small_kernel(const
                                                                            const float* __restrict__ Wr,
                                                                            const float* __restrict__ dl, int64_t L,
                                                                            int d, int E, int64_t split,
-                                                                           T* __restrict__ dx, float* __restrict__ part,
+                                                                           T* dx, bool add, float* __restrict__ part,
                                                                            float* __restrict__ part_b) {
   constexpr int CPT = dg_cpt<EP>(), PB = CPT * (int)sizeof(T);
   extern __shared__ __align__(16) uint8_t rsm[];
@@ -842,6 +844,12 @@ __global__ void __launch_bounds__(kDgThreads, 3) router_dense_small_kernel(const
               out[2 * q] = o[q].x;
               out[2 * q + 1] = o[q].y;
             }
+            if (add) {
+              float old[CPT];
+              load_piece(op + (int64_t)u * d, old);
+#pragma unroll
+              for (int q = 0; q < CPT; ++q) out[q] += old[q];
+            }
             store_piece(op + (int64_t)u * d, out);
           }
         }
@@ -869,7 +877,7 @@ __global__ void __launch_bounds__(kDgThreads, 3) router_dense_small_kernel(const
 template <typename T, int EP>
 __global__ void __launch_bounds__(kRThreads) router_dense_dx_kernel(const float* __restrict__ Wr,
                                                                     const float* __restrict__ dl, int64_t L, int d,
-                                                                    int E, T* __restrict__ dx) {
+                                                                    int E, T* dx, bool add) {
   constexpr int P = EP + 4;  // pitch: rows 1 apart start 4 banks apart, 16-byte multiples
   extern __shared__ __align__(16) uint8_t rsm[];
   float* ds = reinterpret_cast<float*>(rsm);  // [64 tokens][P]
@@ -910,9 +918,10 @@ __global__ void __launch_bounds__(kRThreads) router_dense_dx_kernel(const float*
     if (t >= L) continue;
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
-      const float v = acc[a][b].x + acc[a][b].y;
-      if constexpr (sizeof(T) == 2) dx[t * d + j0 + tc + 16 * b] = __float2bfloat16_rn(v);
-      else dx[t * d + j0 + tc + 16 * b] = v;
+      T* o = dx + t * d + j0 + tc + 16 * b;
+      const float v = acc[a][b].x + acc[a][b].y + (add ? to_f32(*o) : 0.f);
+      if constexpr (sizeof(T) == 2) *o = __float2bfloat16_rn(v);
+      else *o = v;
     }
   }
 }
@@ -1084,7 +1093,7 @@ moeblaze_status fwd_ep(const moeblaze_shape& s, const void* x, const float* Wr, 
       return MOEBLAZE_OK;
     }
   }
-  auto kern = router_fwd_kernel<T, EP>;
+  auto kern = logits ? router_fwd_kernel<T, EP, true> : router_fwd_kernel<T, EP, false>;
   const size_t sm = fwd_smem<T, EP>();
   MB_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm));
   const unsigned grid = (unsigned)((s.L + kRT - 1) / kRT);
@@ -1189,7 +1198,7 @@ int64_t dense_splits(const moeblaze_shape& s) {
 
 template <typename T, int EP>
 moeblaze_status dense_ep(const moeblaze_shape& s, const void* x, const float* Wr, const float* dl, float* dWr,
-                         float* dbias, void* dx, void* ws, cudaStream_t st) {
+                         float* dbias, void* dx, bool add, void* ws, cudaStream_t st) {
   const int64_t split = dense_split(s), S = dense_splits(s);
   float* part = static_cast<float*>(ws);
   float* part_b = part + (size_t)S * s.d * s.E;
@@ -1198,8 +1207,8 @@ moeblaze_status dense_ep(const moeblaze_shape& s, const void* x, const float* Wr
     auto kern = router_dense_small_kernel<T, EP>;
     const size_t sm = dg_smem<T, EP>();
     MB_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm));
-    kern<<<grid, kDgThreads, sm, st>>>(static_cast<const T*>(x), Wr, dl, s.L, s.d, s.E, split, static_cast<T*>(dx), part,
-                                       part_b);
+    kern<<<grid, kDgThreads, sm, st>>>(static_cast<const T*>(x), Wr, dl, s.L, s.d, s.E, split, static_cast<T*>(dx), add,
+                                       part, part_b);
     MB_CUDA(cudaGetLastError());
     count_launch();
   } else {
@@ -1212,7 +1221,7 @@ moeblaze_status dense_ep(const moeblaze_shape& s, const void* x, const float* Wr
       for (int64_t t = 0; t < s.L; t += most) {
         const int64_t n = s.L - t < most ? s.L - t : most;
         kern<<<dim3((unsigned)(s.d / kRT), (unsigned)((n + kRT - 1) / kRT)), kRThreads, sm, st>>>(
-            Wr, dl + t * s.E, n, s.d, s.E, static_cast<T*>(dx) + t * s.d);
+            Wr, dl + t * s.E, n, s.d, s.E, static_cast<T*>(dx) + t * s.d, add);
         MB_CUDA(cudaGetLastError());
         count_launch();
       }
@@ -1234,14 +1243,14 @@ moeblaze_status dense_ep(const moeblaze_shape& s, const void* x, const float* Wr
 
 template <typename T>
 moeblaze_status dense_t(const moeblaze_shape& s, const void* x, const float* Wr, const float* dl, float* dWr,
-                        float* dbias, void* dx, void* ws, cudaStream_t st) {
+                        float* dbias, void* dx, bool add, void* ws, cudaStream_t st) {
   switch (padded_experts(s.E)) {
-    case 8: return dense_ep<T, 8>(s, x, Wr, dl, dWr, dbias, dx, ws, st);
-    case 16: return dense_ep<T, 16>(s, x, Wr, dl, dWr, dbias, dx, ws, st);
-    case 32: return dense_ep<T, 32>(s, x, Wr, dl, dWr, dbias, dx, ws, st);
-    case 64: return dense_ep<T, 64>(s, x, Wr, dl, dWr, dbias, dx, ws, st);
-    case 128: return dense_ep<T, 128>(s, x, Wr, dl, dWr, dbias, dx, ws, st);
-    case 256: return dense_ep<T, 256>(s, x, Wr, dl, dWr, dbias, dx, ws, st);
+    case 8: return dense_ep<T, 8>(s, x, Wr, dl, dWr, dbias, dx, add, ws, st);
+    case 16: return dense_ep<T, 16>(s, x, Wr, dl, dWr, dbias, dx, add, ws, st);
+    case 32: return dense_ep<T, 32>(s, x, Wr, dl, dWr, dbias, dx, add, ws, st);
+    case 64: return dense_ep<T, 64>(s, x, Wr, dl, dWr, dbias, dx, add, ws, st);
+    case 128: return dense_ep<T, 128>(s, x, Wr, dl, dWr, dbias, dx, add, ws, st);
+    case 256: return dense_ep<T, 256>(s, x, Wr, dl, dWr, dbias, dx, add, ws, st);
   }
   return MOEBLAZE_ERR_UNSUPPORTED;
 }
@@ -1254,15 +1263,15 @@ size_t router_dense_ws_bytes(const moeblaze_shape& s) {
 }
 
 moeblaze_status launch_router_dense(const moeblaze_shape& s, const void* x, const float* Wr, const float* dl, float* dWr,
-                                    float* dbias, void* dx, void* ws, cudaStream_t st) {
+                                    float* dbias, void* dx, bool add, void* ws, cudaStream_t st) {
   if (s.L == 0) {
     MB_CUDA(cudaMemsetAsync(dWr, 0, sizeof(float) * s.d * s.E, st));
     if (dbias) MB_CUDA(cudaMemsetAsync(dbias, 0, sizeof(float) * s.E, st));
     return MOEBLAZE_OK;
   }
-  if (router_grad_tc(s)) return launch_router_grad_tc(s, x, Wr, dl, dWr, dbias, dx, ws, st);
-  return s.dtype == MOEBLAZE_BF16 ? dense_t<__nv_bfloat16>(s, x, Wr, dl, dWr, dbias, dx, ws, st)
-                                  : dense_t<float>(s, x, Wr, dl, dWr, dbias, dx, ws, st);
+  if (router_grad_tc(s)) return launch_router_grad_tc(s, x, Wr, dl, dWr, dbias, dx, add, ws, st);
+  return s.dtype == MOEBLAZE_BF16 ? dense_t<__nv_bfloat16>(s, x, Wr, dl, dWr, dbias, dx, add, ws, st)
+                                  : dense_t<float>(s, x, Wr, dl, dWr, dbias, dx, add, ws, st);
 }
 
 size_t router_ws_bytes(const moeblaze_shape& s) {

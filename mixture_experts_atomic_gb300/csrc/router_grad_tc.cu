@@ -127,6 +127,7 @@ struct GParams {
   int64_t L;
   int d, E, tiles, splits;    // tiles: 256-column tiles; splits: CTAs per tile
   int64_t chunks;             // dwr: 64-token chunks of a split
+  int add;                    // dx: added to what is there
   float* part;
   int32_t* err;
   uint64_t wait_ns;
@@ -143,6 +144,13 @@ __device__ __forceinline__ void tmem_alloc_512(uint32_t slot) {
 }
 __device__ __forceinline__ void tmem_free_512(uint32_t base) {
   asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(base) : "memory");
+}
+
+// a tile added to the one in memory (bf16 sums, rounded to nearest, in L2)
+__device__ __forceinline__ void tma_add_2d(const CUtensorMap* map, uint32_t src, int c0, int c1) {
+  asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(map),
+               "r"(src), "r"(c0), "r"(c1)
+               : "memory");
 }
 
 // ------------------------------------------------------------------ dx
@@ -292,7 +300,10 @@ __global__ void __launch_bounds__(kGThreads, 1) dx_kernel(const __grid_constant_
         }
         fence_proxy_async();
         __syncwarp();
-        if (lane == 0 && row0 < p.L) tma_store_2d(&p.tmO, smem_u32(buf + q * 4096), n0 + c, (int)row0);
+        if (lane == 0 && row0 < p.L) {
+          if (p.add) tma_add_2d(&p.tmO, smem_u32(buf + q * 4096), n0 + c, (int)row0);
+          else tma_store_2d(&p.tmO, smem_u32(buf + q * 4096), n0 + c, (int)row0);
+        }
         if (lane == 0) bulk_commit();
         q ^= 1;
       }
@@ -572,7 +583,7 @@ cudaError_t launch_after(void (*kern)(Params...), int64_t grid, int block, size_
 
 template <int EP>
 moeblaze_status launch_ep(const moeblaze_shape& s, const void* x, const float* Wr, const float* dl, float* dWr,
-                          float* dbias, void* dx, void* ws, cudaStream_t st) {
+                          float* dbias, void* dx, bool add, void* ws, cudaStream_t st) {
   const Plan pl = plan_of(s);
   char* w = static_cast<char*>(ws);
   auto* dls = reinterpret_cast<__nv_bfloat16*>(w + pl.dls);
@@ -601,6 +612,7 @@ moeblaze_status launch_ep(const moeblaze_shape& s, const void* x, const float* W
         !make_map(&p.tmO, dx, (uint64_t)s.d, (uint64_t)s.L, 64, 32))
       return MOEBLAZE_ERR_CUDA;
     p.splits = pl.dx_splits;
+    p.add = add ? 1 : 0;
     MB_CUDA(cudaFuncSetAttribute(dx_kernel<EP>, cudaFuncAttributeMaxDynamicSharedMemorySize, dx_smem(EP)));
     MB_CUDA(launch_after(dx_kernel<EP>, (int64_t)pl.tiles * pl.dx_splits, kGThreads, dx_smem(EP), st, p));
     count_launch();
@@ -630,12 +642,12 @@ bool router_grad_tc(const moeblaze_shape& s) {
 size_t router_grad_tc_ws_bytes(const moeblaze_shape& s) { return tc::plan_of(s).bytes; }
 
 moeblaze_status launch_router_grad_tc(const moeblaze_shape& s, const void* x, const float* Wr, const float* dl, float* dWr,
-                                      float* dbias, void* dx, void* ws, cudaStream_t st) {
+                                      float* dbias, void* dx, bool add, void* ws, cudaStream_t st) {
   switch (tc::padded(s.E)) {
-    case 16: return tc::launch_ep<16>(s, x, Wr, dl, dWr, dbias, dx, ws, st);
-    case 32: return tc::launch_ep<32>(s, x, Wr, dl, dWr, dbias, dx, ws, st);
+    case 16: return tc::launch_ep<16>(s, x, Wr, dl, dWr, dbias, dx, add, ws, st);
+    case 32: return tc::launch_ep<32>(s, x, Wr, dl, dWr, dbias, dx, add, ws, st);
   }
-  return tc::launch_ep<64>(s, x, Wr, dl, dWr, dbias, dx, ws, st);
+  return tc::launch_ep<64>(s, x, Wr, dl, dWr, dbias, dx, add, ws, st);
 }
 
 }  // namespace moeblaze

@@ -89,7 +89,7 @@ def test_router_logits_status():
     need = B.moeblaze_router_backward_logits_workspace_bytes(sh)
     assert need > 0
     call = lambda s=sh, x=OKP, W=OKP, dl=OKP, dW=OKP, db=OKP, dx=OKP, ws=OKP, n=need: \
-        B.moeblaze_router_backward_logits(s, x, W, dl, dW, db, dx, ws, n, None)  # noqa: E731
+        B.moeblaze_router_backward_logits(s, x, W, dl, dW, db, dx, 0, ws, n, None)  # noqa: E731
     for k in ("x", "W", "dl", "dW", "ws"):
         assert call(**{k: None}) == B.ERR_INVALID_ARG, k
     for k in ("x", "dl", "dx", "ws"):

@@ -27,7 +27,8 @@ def _built():
 
 NORM_CASES = [(L, d, dt) for dt in (BF16, F32) for L, d in
               [(1, 1), (3, 2), (5, 3), (7, 64), (1, 256), (33, 257), (9, 1000), (130, 1024), (65, 1410), (64, 1409),
-               (21, 2048), (17, 4096), (3, 4100), (4, 8192), (2, 16384), (2, 33000), (2, 9001)]]
+               (21, 2048), (17, 4096), (3, 4100), (4, 8192), (2, 16384), (2, 33000), (2, 9001), (700, 1411),
+               (3, 8191), (5, 700), (2, 5001)]]
 
 
 def _norm_inputs(L, d, dt, seed, offset=0.5):
@@ -289,6 +290,28 @@ def test_router_grad(L, d, E, dt):
     R.inside(db, D.sum(0), n * U * D.abs().sum(0), "dbias")
     a = [t.clone() for t in (dx, dWr, db)]
     assert all(torch.equal(u, v) for u, v in zip(a, grad.backward(x, Wr, dl)))
+
+
+@pytest.mark.parametrize("dt", [BF16, F32])
+@pytest.mark.parametrize("L,d,E", [(70, 64, 8), (333, 448, 64), (300, 320, 100), (1000, 576, 7)])
+def test_router_grad_added_to_a_gradient(L, d, E, dt):
+    g = torch.Generator().manual_seed(L + d + E)
+    x = torch.randn(L, d, generator=g).to(dt).cuda()
+    Wr = torch.randn(d, E, generator=g).cuda()
+    dl = torch.randn(L, E, generator=g).cuda()
+    base = torch.randn(L, d, generator=g).to(dt).cuda()
+    grad = RouterGrad(L, d, E, dt)
+    into = base.clone()
+    dx, dWr, _ = grad.backward(x, Wr, dl, add_to=into)
+    assert dx is into
+    part = R.d64(dl) @ R.d64(Wr).t()
+    want = part + R.d64(base)
+    sx = R.d64(dl).abs() @ R.d64(Wr).abs().t()
+    h = R.HALF[dt]
+    R.inside(dx, want, h * (want.abs() + 2 * part.abs()) + ((E + 16) * U + (2.0 ** -15 if dt == BF16 else 0)) * sx
+             + 2 * U * want.abs(), "dx")
+    alone, dWr2, _ = grad.backward(x, Wr, dl)
+    R.inside(alone, part, h * part.abs() + ((E + 16) * U + (2.0 ** -15 if dt == BF16 else 0)) * sx, "dx alone")
 
 
 def test_router_grad_without_dx_and_tokens():
