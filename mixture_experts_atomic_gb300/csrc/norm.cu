@@ -241,33 +241,25 @@ __device__ __forceinline__ void copy_part(void* dst, const void* src, int n) {
                "r"(n)
                : "memory");
 }
-template <int BYTES>
 __device__ __forceinline__ void copy_ahead(void* dst, const void* src) {
-  static_assert(BYTES == 4 || BYTES == 8 || BYTES == 16, "");
-  const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
-  if constexpr (BYTES == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(d), "l"(src), "n"(BYTES) : "memory");
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
+               : "memory");
 }
 
-// threads on an SM: 512 where a row of 8 fp32 elements a thread, or the 16
-// elements of a lane that holds a short row, take more registers and ring
-template <typename T, int TPR>
-constexpr int bwd_per_sm() {
-  return TPR == 32 ? 4 : TPR == 1024 ? 1 : (sizeof(T) == 4 ? 512 : 1024) / TPR;
-}
-// rows in the ring: two at work, the others on their way (with two, a row is
-// fetched as soon as its place is free)
-template <typename T, int VEC, int TPR, int NV>
+// The backward's shapes.  WARP: four rows per CTA, a warp each; else a row per
+// CTA, of as many threads as its words need.  BUDGET: threads of an SM, which
+// set the registers a thread may have and the ring's depth (two rows at work,
+// the others on their way; with two, a row is fetched as soon as its place is
+// free).
+template <typename T, int NV, int BUDGET>
 constexpr int bwd_depth() {
-  constexpr int row = 3 * VEC * NV * (int)sizeof(T);  // bytes of a row a thread holds
-  constexpr int room = 200 * 1024 / (bwd_per_sm<T, TPR>() * norm_threads<TPR>()) / row;
+  constexpr int row = 3 * 16 * NV;  // bytes of a row a thread holds
+  constexpr int room = 200 * 1024 / BUDGET / row;
   return room >= 4 ? 4 : room < 2 ? 2 : room;
 }
-template <typename T, int VEC, int TPR, int NV>
-constexpr size_t bwd_smem() {
-  return (size_t)bwd_depth<T, VEC, TPR, NV>() * 3 * VEC * NV * sizeof(T) * norm_threads<TPR>();
+template <typename T, int NV, int BUDGET>
+constexpr size_t bwd_smem(int threads) {
+  return (size_t)bwd_depth<T, NV, BUDGET>() * 3 * 16 * NV * threads;
 }
 
 // Rows that do not start on 16 bytes (SHIFT): the 16-byte words of a dense
@@ -278,18 +270,23 @@ constexpr size_t bwd_smem() {
 // (Measured at 8191 x 1409 fp32 and 32768 x 1409 bf16 before: 41 and 248 us
 // with pieces of one element, 50 and 161 us with rows copied whole and read
 // by element.)
-template <typename T, int VEC, int TPR, int NV, bool SHIFT>
-__global__ void __launch_bounds__(norm_threads<TPR>(), bwd_per_sm<T, TPR>()) norm_bwd_kernel(
+// THREADS: the CTA's threads where they are known here, 0 where not (the ring's
+// and the sums' places then cost instructions: 182 us against 194 us at
+// 32768 x 4096 bf16).
+template <typename T, int NV, bool WARP, int BUDGET, int THREADS, bool SHIFT>
+__global__ void __launch_bounds__(WARP ? 32 * kNormWarps : BUDGET, WARP ? 4 : 1) norm_bwd_kernel(
     const T* dy, const T* s, const float* __restrict__ mean, const float* __restrict__ rstd,
     const float* __restrict__ w, const T* dsum, int64_t L, int d, T* dx, float* __restrict__ part) {
+  constexpr int VEC = 16 / (int)sizeof(T), ROWS = WARP ? kNormWarps : 1, D = bwd_depth<T, NV, BUDGET>();
   using V = Vec<T, VEC>;
-  constexpr int ROWS = TPR == 32 ? kNormWarps : 1, D = bwd_depth<T, VEC, TPR, NV>(), NT = norm_threads<TPR>();
   extern __shared__ __align__(16) uint8_t nsm[];
-  V* ring = reinterpret_cast<V*>(nsm);  // [D][3][NV][threads]: dy, s, dsum
+  uint4* ring = reinterpret_cast<uint4*>(nsm);  // [D][3][NV][threads]: dy, s, dsum
   __shared__ float red[2][2][32];  // [buffer][sum][warp]
-  const int tid = threadIdx.x, lane = TPR == 32 ? (tid & 31) : tid;
+  const int tid = threadIdx.x, NT = WARP ? 32 * kNormWarps : THREADS ? THREADS : (int)blockDim.x, TPR = WARP ? 32 : NT;
+  const int lane = WARP ? (tid & 31) : tid;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // norm_wgrad_kernel sets itself up meanwhile
   const int64_t step = (int64_t)gridDim.x * ROWS;
-  const int64_t first = (int64_t)blockIdx.x * ROWS + (TPR == 32 ? (tid >> 5) : 0);
+  const int64_t first = (int64_t)blockIdx.x * ROWS + (WARP ? (tid >> 5) : 0);
   // a word's columns: word c of a row holds columns c VEC - shift, ...
   const int shift = SHIFT ? (int)((first * d) % VEC) : 0;
   const int nvec = SHIFT ? (shift + d + VEC - 1) / VEC : d / VEC;
@@ -305,32 +302,41 @@ __global__ void __launch_bounds__(norm_threads<TPR>(), bwd_per_sm<T, TPR>()) nor
     wv[i].x = inside(column(2 * i)) ? w[column(2 * i)] : 0.f;
     wv[i].y = inside(column(2 * i + 1)) ? w[column(2 * i + 1)] : 0.f;
   }
-  // whether one of this thread's words is a row's first or last
+  // the elements of this thread's words that belong to the row, as bits; and
+  // whether one of the words is shared with a neighbouring row
+  uint32_t keep[NV][4];
   bool edge = false;
-  if constexpr (SHIFT)
+  if constexpr (SHIFT) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) edge = edge || lane + j * TPR == 0 || lane + j * TPR == nvec - 1;
-  // array a of ring slot `at`, as pairs, the neighbours' elements as zeros
-  auto read = [&](int at, int a, float2 (&v)[P]) {
+    for (int q = 0; q < NV * VEC; ++q) {
+      constexpr int PER = 4 / (int)sizeof(T);  // elements of 32 bits
+      const int j = q / VEC, i = q % VEC / PER;
+      if (q % PER == 0) keep[j][i] = 0u;
+      if (inside(column(q))) keep[j][i] |= PER == 1 ? 0xFFFFFFFFu : 0xFFFFu << (16 * (q % PER));
+      else edge = edge || lane + j * TPR < nvec;
+    }
+  }
+  // array a of ring slot `at`, as pairs; clean: the neighbours' elements as zeros
+  auto read = [&](int at, int a, float2 (&v)[P], bool clean) {
     float f[NV][VEC];
 #pragma unroll
-    for (int j = 0; j < NV; ++j) to_floats(ring[((at * 3 + a) * NV + j) * NT + tid], f[j]);
+    for (int j = 0; j < NV; ++j) {
+      uint4 u = ring[((at * 3 + a) * NV + j) * NT + tid];
+      if (SHIFT && clean) {
+        u.x &= keep[j][0];
+        u.y &= keep[j][1];
+        u.z &= keep[j][2];
+        u.w &= keep[j][3];
+      }
+      to_floats(*reinterpret_cast<const V*>(&u), f[j]);
+    }
 #pragma unroll
     for (int i = 0; i < P; ++i)
       v[i] = make_float2(f[2 * i / VEC][2 * i % VEC], f[(2 * i + 1) / VEC][(2 * i + 1) % VEC]);
-    if (SHIFT && edge) {
-#pragma unroll
-      for (int i = 0; i < P; ++i) {
-        if (!inside(column(2 * i))) v[i].x = 0.f;
-        if (!inside(column(2 * i + 1))) v[i].y = 0.f;
-      }
-    }
   };
   // pieces past the row's end stay zero
 #pragma unroll
-  for (int q = 0; q < D * 3 * NV; ++q)
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) st_t(ring[q * NT + tid].v[i], 0.f);
+  for (int q = 0; q < D * 3 * NV; ++q) ring[q * NT + tid] = make_uint4(0u, 0u, 0u, 0u);
   auto fetch = [&](int64_t t, int at) {
     if (t < L) {
 #pragma unroll
@@ -338,16 +344,16 @@ __global__ void __launch_bounds__(norm_threads<TPR>(), bwd_per_sm<T, TPR>()) nor
         const int c = lane + j * TPR;
         if (c < nvec) {
           const int64_t o = t * d - shift + c * VEC;
-          V* dst = ring + (at * 3 * NV + j) * NT + tid;
+          uint4* dst = ring + (at * 3 * NV + j) * NT + tid;
           if (SHIFT && o + VEC > L * d) {  // the tensor ends inside this word
             const int n = (int)(L * d - o) * (int)sizeof(T);
             copy_part(dst, dy + o, n);
             copy_part(dst + NV * NT, s + o, n);
             if (dsum) copy_part(dst + 2 * NV * NT, dsum + o, n);
           } else {
-            copy_ahead<sizeof(V)>(dst, dy + o);
-            copy_ahead<sizeof(V)>(dst + NV * NT, s + o);
-            if (dsum) copy_ahead<sizeof(V)>(dst + 2 * NV * NT, dsum + o);
+            copy_ahead(dst, dy + o);
+            copy_ahead(dst + NV * NT, s + o);
+            if (dsum) copy_ahead(dst + 2 * NV * NT, dsum + o);
           }
         }
       }
@@ -377,8 +383,8 @@ __global__ void __launch_bounds__(norm_threads<TPR>(), bwd_per_sm<T, TPR>()) nor
     const float2 rs2 = both(rs), off2 = both(-mu * rs);
     float2 sg = both(0.f), sgx = both(0.f);
     float2 dv[P], sv[P];
-    read(at, 0, dv);
-    read(at, 1, sv);
+    read(at, 0, dv, true);
+    read(at, 1, sv, true);
     // a piece past the row's end: dy = 0 and w = 0 keep it out of the sums
 #pragma unroll
     for (int i = 0; i < P; ++i) {
@@ -389,7 +395,7 @@ __global__ void __launch_bounds__(norm_threads<TPR>(), bwd_per_sm<T, TPR>()) nor
       sgx = __ffma2_rn(g, xh, sgx);
     }
     const float v = warp_sum2(sg.x + sg.y, sgx.x + sgx.y);
-    if constexpr (TPR > 32) {
+    if constexpr (!WARP) {
       if ((tid & 15) == 0) red[buf][(tid >> 4) & 1][tid >> 5] = v;
     } else {
       mine = make_float2(__shfl_sync(0xffffffffu, v, 0), __shfl_sync(0xffffffffu, v, 16));
@@ -397,22 +403,32 @@ __global__ void __launch_bounds__(norm_threads<TPR>(), bwd_per_sm<T, TPR>()) nor
   };
   // dx of row t, in ring slot `at`, from its sums
   auto finish = [&](int64_t t, int at, int buf, float rs, float off, float2 sums) {
-    if constexpr (TPR > 32) {
+    if constexpr (!WARP) {
       // lanes 0-15 add up the first sum over the warps, lanes 16-31 the second
-      constexpr int W = TPR / 32, H = W < 16 ? W : 16;
       const float* r = red[buf][(tid >> 4) & 1];
-      float v = r[tid & (H - 1)];
-      if constexpr (W == 32) v += r[16 + (tid & 15)];
+      float v;
+      if constexpr (THREADS != 0) {
+        constexpr int W = THREADS / 32, H = W < 16 ? W : 16;
+        v = r[tid & (H - 1)];
+        if constexpr (W == 32) v += r[16 + (tid & 15)];
 #pragma unroll
-      for (int o = H / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        for (int o = H / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+      } else {
+        const int i = tid & 15, nw = NT / 32;
+        v = i < nw ? r[i] : 0.f;
+        if (i + 16 < nw) v += r[i + 16];
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+      }
       sums = make_float2(__shfl_sync(0xffffffffu, v, 0), __shfl_sync(0xffffffffu, v, 16));
     }
     const float2 rs2 = both(rs), off2 = both(off), mg = both(-sums.x * inv_d), mgx = both(-sums.y * inv_d);
     T* o = dx + t * d - shift;
     float2 dv[P], sv[P], rv[P];
-    read(at, 0, dv);
-    read(at, 1, sv);
-    read(at, 2, rv);
+    // (a neighbour's elements give results that are not stored)
+    read(at, 0, dv, false);
+    read(at, 1, sv, false);
+    read(at, 2, rv, false);
 #pragma unroll
     for (int i = 0; i < P; ++i) {
       const float2 xh = __ffma2_rn(sv[i], rs2, off2);
@@ -435,7 +451,7 @@ __global__ void __launch_bounds__(norm_threads<TPR>(), bwd_per_sm<T, TPR>()) nor
   };
   asm volatile("cp.async.wait_group %0;" ::"n"(D - 1) : "memory");
   if (first < L) sum_up(0, 0);  // (whole warps, and whole CTAs where a CTA holds a row)
-  if constexpr (TPR > 32) __syncthreads();
+  if constexpr (!WARP) __syncthreads();
   int buf = 0, slot = 0;
   for (int64_t t = first; t < L; t += step, buf ^= 1) {
     const float rs0 = rs, off0 = -mu * rs;
@@ -451,12 +467,12 @@ __global__ void __launch_bounds__(norm_threads<TPR>(), bwd_per_sm<T, TPR>()) nor
     if (t + step < L) sum_up(next, buf ^ 1);
     finish(t, slot, buf, rs0, off0, sums);
     fetch(t + (int64_t)D * step, slot);
-    if constexpr (TPR > 32) __syncthreads();
+    if constexpr (!WARP) __syncthreads();
     slot = next;
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
   float* pw = part + (int64_t)blockIdx.x * 2 * d;
-  if constexpr (TPR > 32) {
+  if constexpr (!WARP) {
 #pragma unroll
     for (int q = 0; q < 2 * P; ++q) {
       const int c = column(q);
@@ -498,6 +514,7 @@ __global__ void __launch_bounds__(32 * kWgradWarps) norm_wgrad_kernel(const floa
   const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;  // column of the (2 d) row [dw | db]
   float a = 0.f;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (c < 2 * d) {
 #pragma unroll 8
     for (int g = wp; g < G; g += kWgradWarps) a += part[(int64_t)g * 2 * d + c];
@@ -562,27 +579,63 @@ int vec_of(int d) {
   return v;
 }
 
-// The backward's tile: up to 8 elements a thread (their two sums, weights and
-// both operands in registers), rows of up to 512 elements in a warp, longer
-// ones in a CTA of as many threads as they need; 16 elements a thread for
-// bf16 rows of 8193 to 16384 (of fp32 rows shared memory holds no ring).
-int bwd_tile_max(const moeblaze_shape& s) { return s.dtype == MOEBLAZE_BF16 ? 16384 : 8192; }
-bool bwd_aligned(const moeblaze_shape& s) { return s.d % (s.dtype == MOEBLAZE_BF16 ? 8 : 4) == 0; }
-// elements of the words a row lies in
-int bwd_room(const moeblaze_shape& s) { return bwd_aligned(s) ? s.d : s.d + (s.dtype == MOEBLAZE_BF16 ? 14 : 6); }
-int bwd_tpr(int d) { return d <= 512 ? 32 : d <= 1024 ? 128 : d <= 2048 ? 256 : d <= 4096 ? 512 : 1024; }
-
-// CTAs of the backward: as many as are resident.  The partial sums are G x 2 d floats.
-// A multiple of 8, so that a CTA's rows are one (SHIFT), unless each has one row.
-int64_t bwd_ctas(const moeblaze_shape& s) {
-  const int tpr = bwd_tpr(bwd_room(s)), rows = tpr == 32 ? kNormWarps : 1;
-  const int per_sm = s.dtype == MOEBLAZE_BF16
-                         ? (tpr == 32 ? 4 : tpr == 128 ? 8 : tpr == 256 ? 4 : tpr == 512 ? 2 : 1)
-                         : (tpr == 32 || tpr == 128 ? 4 : tpr == 256 ? 2 : 1);  // bwd_per_sm
-  int64_t g = (int64_t)per_sm * sm_count();
-  if (g > 8) g -= g % 8;
+// The backward's shape for a row of d elements: 8 elements a thread (their
+// two sums and weights in registers), 16 in a lane of a warp that holds a
+// short row, and where rows of just over half an SM's threads would leave the
+// other half idle.  Wider rows than any: words = 0.
+struct BwdShape {
+  int words, nv, threads, budget, ctas;  // ctas: the resident ones, or as many as there are rows
+  bool warp, shift;
+};
+BwdShape bwd_shape(const moeblaze_shape& s) {
+  BwdShape b = {};
+  const bool half = s.dtype == MOEBLAZE_BF16;
+  const int vec = half ? 8 : 4;
+  b.shift = s.d % vec != 0;
+  const int words = b.shift ? (s.d + 2 * vec - 2) / vec : s.d / vec;
+  b.words = words;
+  auto wide = [&](int nv, int budget) {
+    b.nv = nv;
+    b.budget = budget;
+    b.threads = ((words + nv - 1) / nv + 31) / 32 * 32;
+  };
+  if (words <= (half ? 64 : 128)) {
+    b.warp = true;
+    b.nv = words <= (half ? 32 : 64) ? (half ? 1 : 2) : (half ? 2 : 4);
+    b.threads = 32 * kNormWarps;
+    b.budget = 512;
+  } else if (half) {
+    if (words <= 512) wide(1, 1024);
+    else if (words <= 640) wide(2, 640);
+    else if (words <= 1024) wide(1, 1024);
+    else if (words <= 2048) wide(2, 1024);
+    else b.words = 0;
+  } else {
+    if (words <= 1280) wide(2, 640);
+    else if (words <= 2048) wide(2, 1024);
+    else b.words = 0;
+  }
+  if (b.words == 0) return b;
+  const int rows = b.warp ? kNormWarps : 1;
+  int64_t g = (int64_t)(b.warp ? 4 : b.budget / b.threads) * sm_count();
+  if (g > 8) g -= g % 8;  // a CTA's rows are a multiple of 8 apart (shift), unless each has one row
   const int64_t need = (s.L + rows - 1) / rows;
-  return g < need ? g : need;
+  b.ctas = (int)(g < need ? g : need);
+  return b;
+}
+
+moeblaze_status launch_wgrad(const float* part, int G, int d, float* dw, float* db, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3((unsigned)((2 * (int64_t)d + 31) / 32));
+  cfg.blockDim = dim3(32 * kWgradWarps);
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  MB_CUDA(cudaLaunchKernelEx(&cfg, norm_wgrad_kernel, part, G, d, dw, db));
+  return MOEBLAZE_OK;
 }
 
 template <typename T, int VEC, int TPR, int NV>
@@ -596,21 +649,18 @@ moeblaze_status fwd_tile(const moeblaze_shape& s, const void* x, const void* res
   return MOEBLAZE_OK;
 }
 
-template <typename T, int VEC, int TPR, int NV, bool SHIFT>
-moeblaze_status bwd_tile(const moeblaze_shape& s, const void* dy, const void* sum, const float* mean,
+template <typename T, int NV, bool WARP, int BUDGET, int THREADS, bool SHIFT>
+moeblaze_status bwd_tile(const moeblaze_shape& s, const BwdShape& b, const void* dy, const void* sum, const float* mean,
                          const float* rstd, const float* w, const void* dsum, void* dx, float* dw, float* db,
                          float* part, cudaStream_t st) {
-  const int64_t G = bwd_ctas(s);
-  auto kern = norm_bwd_kernel<T, VEC, TPR, NV, SHIFT>;
-  constexpr size_t sm = bwd_smem<T, VEC, TPR, NV>();
+  auto kern = norm_bwd_kernel<T, NV, WARP, BUDGET, THREADS, SHIFT>;
+  const size_t sm = bwd_smem<T, NV, BUDGET>(b.threads);
   MB_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm));
-  kern<<<(unsigned)G, norm_threads<TPR>(), sm, st>>>((const T*)dy, (const T*)sum, mean, rstd, w, (const T*)dsum, s.L,
-                                                     s.d, (T*)dx, part);
-  MB_CUDA(cudaGetLastError());
-  norm_wgrad_kernel<<<(unsigned)((2 * (int64_t)s.d + 31) / 32), 32 * kWgradWarps, 0, st>>>(part, (int)G, s.d, dw, db);
+  kern<<<(unsigned)b.ctas, b.threads, sm, st>>>((const T*)dy, (const T*)sum, mean, rstd, w, (const T*)dsum, s.L, s.d,
+                                                (T*)dx, part);
   MB_CUDA(cudaGetLastError());
   count_launch(2);
-  return MOEBLAZE_OK;
+  return launch_wgrad(part, b.ctas, s.d, dw, db, st);
 }
 
 // the register tile of a row of n vectors: f(TPR, NV) as integral constants
@@ -635,22 +685,28 @@ moeblaze_status fwd_vec(const moeblaze_shape& s, const void* x, const void* res,
 }
 
 template <typename T, bool SHIFT>
-moeblaze_status bwd_shift(const moeblaze_shape& s, const void* dy, const void* sum, const float* mean,
-                          const float* rstd, const float* w, const void* dsum, void* dx, float* dw, float* db,
-                          float* part, cudaStream_t st) {
-  constexpr int VEC = 16 / (int)sizeof(T), NV = 8 / VEC;  // words of a thread
-#define MB_CALL(TPR, N) bwd_tile<T, VEC, TPR, N, SHIFT>(s, dy, sum, mean, rstd, w, dsum, dx, dw, db, part, st)
-  const int room = bwd_room(s);
-  if (room <= 256) return MB_CALL(32, NV);
-  switch (bwd_tpr(room)) {
-    case 32: return MB_CALL(32, 2 * NV);
-    case 128: return MB_CALL(128, NV);
-    case 256: return MB_CALL(256, NV);
-    case 512: return MB_CALL(512, NV);
+moeblaze_status bwd_shaped(const moeblaze_shape& s, const BwdShape& b, const void* dy, const void* sum,
+                           const float* mean, const float* rstd, const float* w, const void* dsum, void* dx, float* dw,
+                           float* db, float* part, cudaStream_t st) {
+  constexpr bool half = sizeof(T) == 2;
+#define MB_CALL(NV, WARP, BUDGET, THREADS) \
+  bwd_tile<T, NV, WARP, BUDGET, THREADS, SHIFT>(s, b, dy, sum, mean, rstd, w, dsum, dx, dw, db, part, st)
+  if (b.warp)
+    return b.nv == (half ? 1 : 2) ? MB_CALL((half ? 1 : 2), true, 512, 0) : MB_CALL((half ? 2 : 4), true, 512, 0);
+  if constexpr (half) {
+    if (b.nv == 1) {
+      if constexpr (!SHIFT) {
+        switch (b.threads) {
+          case 128: return MB_CALL(1, false, 1024, 128);
+          case 256: return MB_CALL(1, false, 1024, 256);
+          case 512: return MB_CALL(1, false, 1024, 512);
+          case 1024: return MB_CALL(1, false, 1024, 1024);
+        }
+      }
+      return MB_CALL(1, false, 1024, 0);
+    }
   }
-  if constexpr (sizeof(T) == 2)
-    if (room > 8192) return MB_CALL(1024, 2 * NV);
-  return MB_CALL(1024, NV);
+  return b.budget == 640 ? MB_CALL(2, false, 640, 0) : MB_CALL(2, false, 1024, 0);
 #undef MB_CALL
 }
 
@@ -675,7 +731,8 @@ moeblaze_status fwd_t(const moeblaze_shape& s, const void* x, const void* res, c
 template <typename T>
 moeblaze_status bwd_t(const moeblaze_shape& s, const void* dy, const void* sum, const float* mean, const float* rstd,
                       const float* w, const void* dsum, void* dx, float* dw, float* db, float* part, cudaStream_t st) {
-  if (bwd_room(s) > bwd_tile_max(s)) {
+  const BwdShape b = bwd_shape(s);
+  if (b.words == 0) {
     norm_bwd_wide_kernel<T><<<(unsigned)s.L, 1024, 0, st>>>((const T*)dy, (const T*)sum, mean, rstd, w, (const T*)dsum,
                                                             s.d, (T*)dx);
     MB_CUDA(cudaGetLastError());
@@ -683,20 +740,19 @@ moeblaze_status bwd_t(const moeblaze_shape& s, const void* dy, const void* sum, 
     norm_wide_wgrad_kernel<T><<<dim3((unsigned)((s.d + 255) / 256), (unsigned)G), 256, 0, st>>>(
         (const T*)dy, (const T*)sum, mean, rstd, s.L, s.d, part);
     MB_CUDA(cudaGetLastError());
-    norm_wgrad_kernel<<<(unsigned)((2 * (int64_t)s.d + 31) / 32), 32 * kWgradWarps, 0, st>>>(part, (int)G, s.d, dw, db);
-    MB_CUDA(cudaGetLastError());
     count_launch(3);
-    return MOEBLAZE_OK;
+    return launch_wgrad(part, (int)G, s.d, dw, db, st);
   }
-  return bwd_aligned(s) ? bwd_shift<T, false>(s, dy, sum, mean, rstd, w, dsum, dx, dw, db, part, st)
-                        : bwd_shift<T, true>(s, dy, sum, mean, rstd, w, dsum, dx, dw, db, part, st);
+  return b.shift ? bwd_shaped<T, true>(s, b, dy, sum, mean, rstd, w, dsum, dx, dw, db, part, st)
+                 : bwd_shaped<T, false>(s, b, dy, sum, mean, rstd, w, dsum, dx, dw, db, part, st);
 }
 
 }  // namespace
 
 size_t norm_ws_bytes(const moeblaze_shape& s) {
   if (s.L == 0) return 0;
-  const int64_t G = bwd_room(s) > bwd_tile_max(s) ? (s.L < kWideSplits ? s.L : kWideSplits) : bwd_ctas(s);
+  const BwdShape b = bwd_shape(s);
+  const int64_t G = b.words == 0 ? (s.L < kWideSplits ? s.L : kWideSplits) : b.ctas;
   return (size_t)G * 2 * s.d * sizeof(float);
 }
 
