@@ -14,9 +14,8 @@
 // the centred row (a second sum over registers, not E[s^2] - mu^2, which
 // would cancel for rows with an offset).  Bound by HBM.
 //
-// A row is spread over TPR threads (one warp, or a whole CTA), NV vectors of
-// VEC elements per thread.  VEC is the widest power of two up to 16 bytes
-// that divides d, so that every row of a dense matrix starts on a vector.
+// A row is spread over TPR threads (one warp, or a whole CTA), NV 16-byte
+// words of VEC elements per thread.
 #include "common.cuh"
 
 namespace moeblaze {
@@ -92,58 +91,97 @@ constexpr int norm_threads() {
 }
 
 // ------------------------------------------------------------------ forward
-template <typename T, int VEC, int TPR, int NV>
+// SHIFT: rows that do not start on 16 bytes.  A thread still loads the whole
+// words the row lies in, whose columns then begin `shift` before the row; the
+// first and the last word are shared with its neighbours and masked.  (With
+// pieces of one element instead: 290 us at 32768 x 1409 bf16.)
+template <typename T, int TPR, int NV, bool SHIFT>
 __global__ void __launch_bounds__(norm_threads<TPR>()) norm_fwd_kernel(const T* x, const T* res,
                                                                         const float* __restrict__ w,
                                                                         const float* __restrict__ b, int64_t L, int d,
                                                                         float eps, T* sum, T* y,
                                                                         float* __restrict__ mean_out,
                                                                         float* __restrict__ rstd_out) {
+  constexpr int VEC = 16 / (int)sizeof(T);
   using V = Vec<T, VEC>;
   __shared__ float red[2][32];
   const int lane = TPR == 32 ? (threadIdx.x & 31) : threadIdx.x;
   const int64_t t = TPR == 32 ? (int64_t)blockIdx.x * kNormWarps + (threadIdx.x >> 5) : (int64_t)blockIdx.x;
   if (t >= L) return;  // a whole warp or a whole CTA
-  const int nvec = d / VEC;
-  const V* xr = reinterpret_cast<const V*>(x + t * d);
-  const V* rr = res ? reinterpret_cast<const V*>(res + t * d) : nullptr;
+  const int shift = SHIFT ? (int)((t * d) % VEC) : 0;
+  const int nvec = SHIFT ? (shift + d + VEC - 1) / VEC : d / VEC;
+  const int64_t row = t * d - shift;  // element of the row's first word
+  auto whole = [&](int c) {           // every element of word c is of the row
+    return c * VEC >= shift && (c + 1) * VEC <= shift + d;
+  };
+  auto load = [&](const T* p, int c) {
+    V v;
+    if (!SHIFT || row + (int64_t)(c + 1) * VEC <= L * d) {
+      v = *reinterpret_cast<const V*>(p + row + (int64_t)c * VEC);
+    } else {  // the tensor ends inside this word
+#pragma unroll
+      for (int i = 0; i < VEC; ++i)
+        if (row + (int64_t)c * VEC + i < L * d) v.v[i] = p[row + (int64_t)c * VEC + i];
+        else st_t(v.v[i], 0.f);
+    }
+    return v;
+  };
+  auto store = [&](T* p, int c, const float (&f)[VEC]) {
+    if (!SHIFT || whole(c)) {
+      *reinterpret_cast<V*>(p + row + (int64_t)c * VEC) = from_floats<T, VEC>(f);
+    } else {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i)
+        if ((unsigned)(c * VEC + i - shift) < (unsigned)d) st_t(p[row + (int64_t)c * VEC + i], f[i]);
+    }
+  };
   float s[NV][VEC];
   V xv[NV], rv[NV];
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     const int c = lane + j * TPR;
-    if (c < nvec) xv[j] = xr[c];
+    if (c < nvec) xv[j] = load(x, c);
   }
-  if (rr) {
+  if (res) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int c = lane + j * TPR;
-      if (c < nvec) rv[j] = rr[c];
+      if (c < nvec) rv[j] = load(res, c);
     }
   }
+  // elements outside the row are kept at zero
+  auto clear_outside = [&](int j) {
+    const int c = lane + j * TPR;
+    if (SHIFT && c < nvec && !whole(c)) {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i)
+        if ((unsigned)(c * VEC + i - shift) >= (unsigned)d) s[j][i] = 0.f;
+    }
+  };
   float acc = 0.f;
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     const int c = lane + j * TPR;
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-      s[j][i] = 0.f;
-      if (c < nvec) {
-        s[j][i] = ld_f32(xv[j].v[i]);
-        if (rr) s[j][i] += ld_f32(rv[j].v[i]);
+    for (int i = 0; i < VEC; ++i) s[j][i] = 0.f;
+    if (c < nvec) {
+      to_floats(xv[j], s[j]);
+      if (res) {
+        float r[VEC];
+        to_floats(rv[j], r);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) s[j][i] += r[i];
       }
-      acc += s[j][i];
     }
+    clear_outside(j);
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) acc += s[j][i];
   }
   if (sum) {
-    V* so = reinterpret_cast<V*>(sum + t * d);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int c = lane + j * TPR;
-      V o;
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) st_t(o.v[i], s[j][i]);
-      if (c < nvec) so[c] = o;
+      if (c < nvec) store(sum, c, s[j]);
     }
   }
   const float inv_d = 1.f / (float)d;
@@ -153,30 +191,59 @@ __global__ void __launch_bounds__(norm_threads<TPR>()) norm_fwd_kernel(const T* 
   for (int j = 0; j < NV; ++j) {
     const bool in = lane + j * TPR < nvec;
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-      s[j][i] -= mu;
-      acc = in ? fmaf(s[j][i], s[j][i], acc) : acc;
-    }
+    for (int i = 0; i < VEC; ++i) s[j][i] -= mu;
+    clear_outside(j);
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) acc = in ? fmaf(s[j][i], s[j][i], acc) : acc;
   }
   const float rstd = 1.f / sqrtf(row_sum<TPR>(acc, red[1]) * inv_d + eps);
-  V* yo = reinterpret_cast<V*>(y + t * d);
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     const int c = lane + j * TPR;
     if (c < nvec) {
-      using W = Vec<float, (VEC < 4 ? VEC : 4)>;
-      constexpr int WV = VEC < 4 ? VEC : 4;
-      V o;
+      float o[VEC];
+      if constexpr (SHIFT) {
+        const int k0 = c * VEC - shift, a0 = k0 & ~3;  // of the word's columns, and of w's and b's words around them
+        if (VEC == 8 && whole(c) && a0 + 12 <= d) {
+          // twelve elements in three 16-byte loads, of which the word's eight
+          // begin at the row's k0 % 4 (lanes are 32 bytes apart: eight loads of
+          // one element each would pass over the same lines eight times)
+          float wb[2][12];
 #pragma unroll
-      for (int q = 0; q < VEC / WV; ++q) {
-        const W wv = reinterpret_cast<const W*>(w)[c * (VEC / WV) + q];
-        W bv;
-        if (b) bv = reinterpret_cast<const W*>(b)[c * (VEC / WV) + q];
+          for (int q = 0; q < 3; ++q) {
+            const float4 wv = reinterpret_cast<const float4*>(w + a0)[q];
+            const float4 bv = b ? reinterpret_cast<const float4*>(b + a0)[q] : make_float4(0.f, 0.f, 0.f, 0.f);
+            wb[0][4 * q] = wv.x; wb[0][4 * q + 1] = wv.y; wb[0][4 * q + 2] = wv.z; wb[0][4 * q + 3] = wv.w;
+            wb[1][4 * q] = bv.x; wb[1][4 * q + 1] = bv.y; wb[1][4 * q + 2] = bv.z; wb[1][4 * q + 3] = bv.w;
+          }
+          const int r = k0 & 3;  // the same for the whole row
 #pragma unroll
-        for (int i = 0; i < WV; ++i)
-          st_t(o.v[q * WV + i], fmaf(s[j][q * WV + i] * rstd, wv.v[i], b ? bv.v[i] : 0.f));
+          for (int i = 0; i < VEC; ++i) {
+            const float wv = r == 0 ? wb[0][i] : r == 1 ? wb[0][i + 1] : r == 2 ? wb[0][i + 2] : wb[0][i + 3];
+            const float bv = r == 0 ? wb[1][i] : r == 1 ? wb[1][i + 1] : r == 2 ? wb[1][i + 2] : wb[1][i + 3];
+            o[i] = fmaf(s[j][i] * rstd, wv, bv);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) {
+            const int k = k0 + i;
+            const bool in = (unsigned)k < (unsigned)d;
+            o[i] = fmaf(s[j][i] * rstd, in ? w[k] : 0.f, in && b ? b[k] : 0.f);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int q = 0; q < VEC / 4; ++q) {
+          const float4 wv = reinterpret_cast<const float4*>(w)[c * (VEC / 4) + q];
+          const float4 bv =
+              b ? reinterpret_cast<const float4*>(b)[c * (VEC / 4) + q] : make_float4(0.f, 0.f, 0.f, 0.f);
+          o[4 * q] = fmaf(s[j][4 * q] * rstd, wv.x, bv.x);
+          o[4 * q + 1] = fmaf(s[j][4 * q + 1] * rstd, wv.y, bv.y);
+          o[4 * q + 2] = fmaf(s[j][4 * q + 2] * rstd, wv.z, bv.z);
+          o[4 * q + 3] = fmaf(s[j][4 * q + 3] * rstd, wv.w, bv.w);
+        }
       }
-      yo[c] = o;
+      store(y, c, o);
     }
   }
   if (lane == 0) {
@@ -570,14 +637,7 @@ __global__ void __launch_bounds__(256) norm_wide_wgrad_kernel(const T* dy, const
 }
 
 constexpr int kWideSplits = 32;
-constexpr int kMaxTileVecs = 4096;  // widest register tile: 1024 threads of 4 vectors
-
-template <typename T>
-int vec_of(int d) {
-  int v = 16 / (int)sizeof(T);
-  while (d % v) v >>= 1;
-  return v;
-}
+constexpr int kMaxTileWords = 4096;  // widest register tile of the forward: 1024 threads of 4 words
 
 // The backward's shape for a row of d elements: 8 elements a thread (their
 // two sums and weights in registers), 16 in a lane of a warp that holds a
@@ -638,11 +698,11 @@ moeblaze_status launch_wgrad(const float* part, int G, int d, float* dw, float* 
   return MOEBLAZE_OK;
 }
 
-template <typename T, int VEC, int TPR, int NV>
+template <typename T, int TPR, int NV, bool SHIFT>
 moeblaze_status fwd_tile(const moeblaze_shape& s, const void* x, const void* res, const float* w, const float* b,
                          float eps, void* sum, void* y, float* mean, float* rstd, cudaStream_t st) {
   const int rows = TPR == 32 ? kNormWarps : 1;
-  norm_fwd_kernel<T, VEC, TPR, NV><<<(unsigned)((s.L + rows - 1) / rows), norm_threads<TPR>(), 0, st>>>(
+  norm_fwd_kernel<T, TPR, NV, SHIFT><<<(unsigned)((s.L + rows - 1) / rows), norm_threads<TPR>(), 0, st>>>(
       (const T*)x, (const T*)res, w, b, s.L, s.d, eps, (T*)sum, (T*)y, mean, rstd);
   MB_CUDA(cudaGetLastError());
   count_launch();
@@ -663,24 +723,23 @@ moeblaze_status bwd_tile(const moeblaze_shape& s, const BwdShape& b, const void*
   return launch_wgrad(part, b.ctas, s.d, dw, db, st);
 }
 
-// the register tile of a row of n vectors: f(TPR, NV) as integral constants
-#define MB_NORM_TILE(n, CALL)                  \
-  do {                                         \
-    if ((n) <= 32) return CALL(32, 1);         \
-    if ((n) <= 64) return CALL(32, 2);         \
-    if ((n) <= 128) return CALL(32, 4);        \
-    if ((n) <= 256) return CALL(128, 2);       \
-    if ((n) <= 512) return CALL(256, 2);       \
-    if ((n) <= 1024) return CALL(512, 2);      \
-    if ((n) <= 2048) return CALL(1024, 2);     \
-    return CALL(1024, 4);                      \
-  } while (0)
-
-template <typename T, int VEC>
-moeblaze_status fwd_vec(const moeblaze_shape& s, const void* x, const void* res, const float* w, const float* b,
-                        float eps, void* sum, void* y, float* mean, float* rstd, cudaStream_t st) {
-#define MB_CALL(TPR, NV) fwd_tile<T, VEC, TPR, NV>(s, x, res, w, b, eps, sum, y, mean, rstd, st)
-  MB_NORM_TILE(s.d / VEC, MB_CALL);
+// the forward's register tile of a row of n words
+template <typename T, bool SHIFT>
+moeblaze_status fwd_words(const moeblaze_shape& s, int n, const void* x, const void* res, const float* w,
+                          const float* b, float eps, void* sum, void* y, float* mean, float* rstd, cudaStream_t st) {
+#define MB_CALL(TPR, NV) fwd_tile<T, TPR, NV, SHIFT>(s, x, res, w, b, eps, sum, y, mean, rstd, st)
+  if (n <= 32) return MB_CALL(32, 1);
+  if (n <= 64) return MB_CALL(32, 2);
+  if (n <= 128) return MB_CALL(32, 4);
+  if (n <= 256) return MB_CALL(128, 2);
+  if (n <= 384) return MB_CALL(128, 3);
+  // (without a residual twice the words a thread, for as many loads in flight:
+  // 105 us instead of 117 at 32768 x 4096 bf16)
+  if (n <= 512) return res ? MB_CALL(256, 2) : MB_CALL(128, 4);
+  if (n <= 768) return MB_CALL(256, 3);
+  if (n <= 1024) return MB_CALL(512, 2);
+  if (n <= 2048) return MB_CALL(1024, 2);
+  return MB_CALL(1024, 4);
 #undef MB_CALL
 }
 
@@ -713,19 +772,18 @@ moeblaze_status bwd_shaped(const moeblaze_shape& s, const BwdShape& b, const voi
 template <typename T>
 moeblaze_status fwd_t(const moeblaze_shape& s, const void* x, const void* res, const float* w, const float* b,
                       float eps, void* sum, void* y, float* mean, float* rstd, cudaStream_t st) {
-  const int v = vec_of<T>(s.d);
-  if (s.d / v > kMaxTileVecs) {
+  constexpr int vec = 16 / (int)sizeof(T);
+  const bool shift = s.d % vec != 0;
+  const int words = shift ? (s.d + 2 * vec - 2) / vec : s.d / vec;
+  if (words > kMaxTileWords) {
     norm_fwd_wide_kernel<T><<<(unsigned)s.L, 1024, 0, st>>>((const T*)x, (const T*)res, w, b, s.L, s.d, eps, (T*)sum,
                                                             (T*)y, mean, rstd);
     MB_CUDA(cudaGetLastError());
     count_launch();
     return MOEBLAZE_OK;
   }
-  if constexpr (sizeof(T) == 2)
-    if (v == 8) return fwd_vec<T, 8>(s, x, res, w, b, eps, sum, y, mean, rstd, st);
-  if (v == 4) return fwd_vec<T, 4>(s, x, res, w, b, eps, sum, y, mean, rstd, st);
-  if (v == 2) return fwd_vec<T, 2>(s, x, res, w, b, eps, sum, y, mean, rstd, st);
-  return fwd_vec<T, 1>(s, x, res, w, b, eps, sum, y, mean, rstd, st);
+  return shift ? fwd_words<T, true>(s, words, x, res, w, b, eps, sum, y, mean, rstd, st)
+               : fwd_words<T, false>(s, words, x, res, w, b, eps, sum, y, mean, rstd, st);
 }
 
 template <typename T>
