@@ -522,21 +522,29 @@ __global__ void int4_combine_kernel(const float* __restrict__ part, const int32_
                                     __nv_bfloat16* __restrict__ y) {
   const int64_t total = (int64_t)L * d / 4;
   const int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x;
+  const int t = (int)(i / (d / 4)), c = (int)(i % (d / 4)) * 4;
+  // the routing is the caller's: read while the products still run
+  float g[kMaxK];
+  bool on[kMaxK];
+#pragma unroll
+  for (int k = 0; k < kMaxK; ++k) {
+    on[k] = i < total && k < K && (unsigned)ids[t * K + k] < (unsigned)E;
+    g[k] = on[k] ? gates[t * K + k] : 0.f;
+  }
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (i >= total) return;
-  const int t = (int)(i / (d / 4)), c = (int)(i % (d / 4)) * 4;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int k = 0; k < K; ++k) {
-    const int pair = t * K + k;
-    if ((unsigned)ids[pair] >= (unsigned)E) continue;
+#pragma unroll
+  for (int k = 0; k < kMaxK; ++k) {
+    if (!on[k]) continue;
+    const float* src = part + (int64_t)(t * K + k) * d + c;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
     for (int s = 0; s < slices; ++s) {
-      const float4 q = *reinterpret_cast<const float4*>(part + ((int64_t)s * L * K + pair) * d + c);
+      const float4 q = *reinterpret_cast<const float4*>(src + (int64_t)s * L * K * d);
       v.x += q.x; v.y += q.y; v.z += q.z; v.w += q.w;
     }
-    const float g = gates[pair];
-    o.x = fmaf(g, v.x, o.x); o.y = fmaf(g, v.y, o.y); o.z = fmaf(g, v.z, o.z); o.w = fmaf(g, v.w, o.w);
+    o.x = fmaf(g[k], v.x, o.x); o.y = fmaf(g[k], v.y, o.y); o.z = fmaf(g[k], v.z, o.z); o.w = fmaf(g[k], v.w, o.w);
   }
   *reinterpret_cast<uint2*>(y + (int64_t)t * d + c) = make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
 }
