@@ -445,3 +445,18 @@ def test_block_bf16_on_another_stream_and_in_a_graph():
         else:
             assert torch.equal(a, b), i
     assert block.layer.device_error() == 0
+
+
+def test_example_trains_and_serves():
+    """The example's training steps lower the error, and its 4-bit batch agrees with the bf16 layer."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "moe_block.py")
+    spec = importlib.util.spec_from_file_location("moe_block_example", path)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    p, history = m.train(512, 256, 256, 8, 2, 30)
+    assert history[-1][0] < 0.98 * history[0][0], history
+    assert all(h[1] == h[1] for h in history)
+    y4, y16 = m.serve(p, 7, 2, group=64)
+    assert (y4.float() - y16.float()).abs().max() <= 2e-2 * y16.float().abs().max()
