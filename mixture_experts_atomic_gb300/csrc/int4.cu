@@ -44,8 +44,11 @@ constexpr int kQTeam = 4;                          // warps that share a unit's 
 constexpr int kQTeams = kQWarps / kQTeam;
 constexpr int kQMaxTokens = 64;                    // tokens of one launch
 constexpr int kQMaxPairs = kQMaxTokens * kMaxK;    // (token, slot) pairs of one launch
-// entries of a warp's ring, each a 128-row piece of a tile of nb matrices
-__host__ __device__ constexpr int ring_depth(int nb) { return nb == 1 ? 4 : 3; }
+// What a launch computes.  A unit is two tiles, so that a token fragment
+// serves two weight tiles: the same tile of W1 and W2 (GATED), or two
+// neighbouring tiles of one matrix (SINGLE: SiLU experts' W1; DOWN: W3).
+enum QMode : int { GATED = 0, SINGLE = 1, DOWN = 2 };
+constexpr int kQDepth = 3;                         // entries of a warp's ring, each a 128-row piece of a unit
 constexpr size_t kQSmem = 227 * 1024;
 // list, counts, offsets, pass and weight prefixes, scan totals
 constexpr size_t kQIntBytes = 4 * (kQMaxPairs + 4 * kMaxE + 2 + 3 * kQWarps);
@@ -188,16 +191,16 @@ struct QParams {
   const int32_t* ids;
   int pairs, E, K;
   int R, N;                  // reduction length and output columns of the matrices
-  int slices;                // the reduction axis in slices of R / slices (UP: 1)
+  int slices;                // the reduction axis in slices of R / slices (DOWN; else 1)
   int cap;                   // token columns of one pass
   int rows;                  // token rows that shared memory holds (<= cap)
-  __nv_bfloat16* H;          // UP: h (pairs x N)
-  float* part;               // else: (slices x pairs x N)
+  __nv_bfloat16* H;          // GATED, SINGLE: h (pairs x N)
+  float* part;               // DOWN: (slices x pairs x N)
 };
 
 // Work: segments (expert in use, pass of `cap` of its pairs, slice), each
-// with N / 16 tiles; the units (segment, tile) are split evenly and
-// contiguously over the CTAs, and a CTA's units go round its teams of four
+// with N / 16 tiles of a pair of matrices or N / 32 pairs of tiles; the units
+// are split by weight, contiguously, over the CTAs, and a CTA's units go round its teams of four
 // warps, which share a unit's reduction rows: a CTA's last round then costs a
 // quarter of a unit's time, and few units still keep every warp loading.  A
 // segment's token rows are staged in shared memory; the packed weights
@@ -205,11 +208,11 @@ struct QParams {
 // reads back only the bytes it copied itself (no barrier), and which runs on
 // across units and segments.  The team's sums meet in shared memory, in the
 // order of its warps.
-template <int NB, int NTL, int GROUP>
+template <int MODE, int NTL, int GROUP>
 __global__ void __launch_bounds__(kQThreads, 1) int4_product_kernel(const QParams p) {
-  constexpr int PIECES = ring_depth(NB);
-  constexpr int SW = 128 / GROUP;                   // groups, and scale words of a lane, in a piece
-  constexpr int BRANCH = 1024 + 128 * SW;           // ring bytes of a piece of one matrix: weights, scale words
+  constexpr int PIECES = kQDepth, NB = 2;
+  constexpr int SW = 128 / GROUP;                   // groups, and scale words of a column pair, in a piece
+  constexpr int BRANCH = 1024 + 32 * SW;            // ring bytes of a piece of one tile: weights, scale words
   constexpr int ENTRY = NB * BRANCH;
   extern __shared__ __align__(16) uint8_t qsm[];
   int* list = reinterpret_cast<int*>(qsm + (size_t)kQWarps * PIECES * ENTRY);  // [pairs] by expert, ascending
@@ -284,7 +287,8 @@ __global__ void __launch_bounds__(kQThreads, 1) int4_product_kernel(const QParam
     __syncthreads();
   }
 
-  const int nt = p.N / 16, SL = p.R / p.slices, kp = SL / 128, allp = p.R / 128;
+  const int nt = p.N / (MODE == GATED ? 16 : 32);  // units of a segment
+  const int SL = p.R / p.slices, kp = SL / 128, allp = p.R / 128;
   const int per_pass = p.slices * nt;
   // This CTA's units: an even share of the weights.  Lanes 0 and 1 map the
   // share's ends, blockIdx W / gridDim of the total weight W, to units; a
@@ -312,7 +316,7 @@ __global__ void __launch_bounds__(kQThreads, 1) int4_product_kernel(const QParam
 
   // ---- the fetch head of this warp: unit, pieces left of it, addresses
   const uint32_t ring = saddr(qsm) + warp * PIECES * ENTRY + lane * 16;
-  const uint32_t ring_s = saddr(qsm) + warp * PIECES * ENTRY + 1024 + lane * 4 * SW;
+  const uint32_t ring_s = saddr(qsm) + warp * PIECES * ENTRY + 1024 + g * 4 * SW;
   const int team = warp / kQTeam, mate = warp % kQTeam;
   const int k0 = kp * mate / kQTeam, k1 = kp * (mate + 1) / kQTeam;  // this warp's pieces of a unit
   int fu = u0 + team;
@@ -323,11 +327,12 @@ __global__ void __launch_bounds__(kQThreads, 1) int4_product_kernel(const QParam
   auto fetch_unit = [&]() {
     if (fu >= u1 || k0 == k1) return;
     const int seg = fu / nt, tile = fu - seg * nt, sl = seg % p.slices, e = last_at_most(pre, p.E, seg / p.slices);
-    const int64_t at = ((int64_t)e * nt + tile) * allp + sl * kp + k0;
 #pragma unroll
     for (int br = 0; br < NB; ++br) {
-      fw[br] = p.w[br] + at * 1024 + lane * 16;
-      fs[br] = p.s[br] + at * (32 * SW) + g * (4 * SW);
+      const int64_t row = MODE == GATED ? (int64_t)e * nt + tile : ((int64_t)e * nt + tile) * 2 + br;
+      const int64_t at = row * allp + sl * kp + k0;
+      fw[br] = p.w[MODE == GATED ? br : 0] + at * 1024 + lane * 16;
+      fs[br] = p.s[MODE == GATED ? br : 0] + at * (32 * SW) + g * (4 * SW);
     }
     left = k1 - k0;
   };
@@ -337,7 +342,7 @@ __global__ void __launch_bounds__(kQThreads, 1) int4_product_kernel(const QParam
       for (int br = 0; br < NB; ++br) {
         cp16(ring + fslot + br * BRANCH, fw[br]);
         cp16(ring + fslot + br * BRANCH + 512, fw[br] + 512);
-        cp_small<4 * SW>(ring_s + fslot + br * BRANCH, fs[br]);
+        if (tq == 0) cp_small<4 * SW>(ring_s + fslot + br * BRANCH, fs[br]);  // one lane of the column pair's four
         fw[br] += 1024;
         fs[br] += 32 * SW;
       }
@@ -375,7 +380,7 @@ __global__ void __launch_bounds__(kQThreads, 1) int4_product_kernel(const QParam
       for (int i = warp; i < n * parts; i += kQWarps) {
         const int r = i / parts, c0 = (i - r * parts) * 128;
         const int pair = list[first + r];
-        const int64_t row = p.H ? pair / p.K : pair;
+        const int64_t row = MODE == DOWN ? pair : pair / p.K;
         const uint4* src = reinterpret_cast<const uint4*>(p.src + row * p.src_ld + (int64_t)sl * SL);
         uint4* dst = reinterpret_cast<uint4*>(xs + (size_t)r * pitch);
         uint4 v[4];
@@ -421,6 +426,7 @@ __global__ void __launch_bounds__(kQThreads, 1) int4_product_kernel(const QParam
 #pragma unroll 1
         for (int k = k0; k < k1; ++k) {
           cp_wait<PIECES - 2>();
+          __syncwarp();  // the scales are another lane's copies
           uint4 wv[NB][2];
           uint32_t sc[NB][SW];
 #pragma unroll
@@ -429,7 +435,7 @@ __global__ void __launch_bounds__(kQThreads, 1) int4_product_kernel(const QParam
             wv[br][0] = *reinterpret_cast<const uint4*>(at + lane * 16);
             wv[br][1] = *reinterpret_cast<const uint4*>(at + 512 + lane * 16);
 #pragma unroll
-            for (int j = 0; j < SW; ++j) sc[br][j] = reinterpret_cast<const uint32_t*>(at + 1024)[lane * SW + j];
+            for (int j = 0; j < SW; ++j) sc[br][j] = reinterpret_cast<const uint32_t*>(at + 1024)[g * SW + j];
           }
           slot = slot == (PIECES - 1) * ENTRY ? 0u : slot + ENTRY;
           fetch();
@@ -493,15 +499,20 @@ __global__ void __launch_bounds__(kQThreads, 1) int4_product_kernel(const QParam
             for (int w = 0; w < kQTeam; ++w)
               sum[br] += swap[(((team * kQTeam + w) * NB + br) * 4 + mate) * 32 + lane];
           }
-          const int tk = 8 * i + 2 * tq + (mate & 1), col = (u - seg * nt) * 16 + g + 8 * (mate >> 1);
+          const int tk = 8 * i + 2 * tq + (mate & 1), unit = u - seg * nt;
           if (tk < n) {
             const int pair = list[first + tk];
-            if (p.H) {
-              float hv = sum[0] / (1.f + expf(-sum[0]));
-              if constexpr (NB == 2) hv *= sum[NB - 1];
-              p.H[(int64_t)pair * p.N + col] = __float2bfloat16_rn(hv);
+            const int64_t at = (int64_t)(MODE == DOWN ? sl * p.pairs + pair : pair) * p.N;
+            if constexpr (MODE == GATED) {
+              const float hv = sum[0] / (1.f + expf(-sum[0])) * sum[1];
+              p.H[at + unit * 16 + g + 8 * (mate >> 1)] = __float2bfloat16_rn(hv);
             } else {
-              p.part[((int64_t)sl * p.pairs + pair) * p.N + col] = sum[0];
+#pragma unroll
+              for (int br = 0; br < NB; ++br) {
+                const int64_t o = at + (unit * 2 + br) * 16 + g + 8 * (mate >> 1);
+                if constexpr (MODE == SINGLE) p.H[o] = __float2bfloat16_rn(sum[br] / (1.f + expf(-sum[br])));
+                else p.part[o] = sum[br];
+              }
             }
           }
         }
@@ -549,10 +560,10 @@ __global__ void int4_combine_kernel(const float* __restrict__ part, const int32_
   *reinterpret_cast<uint2*>(y + (int64_t)t * d + c) = make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
 }
 
-// shared memory besides the token rows: the ring of a launch on nb matrices
-size_t ring_bytes(int nb, int group) { return (size_t)kQWarps * ring_depth(nb) * nb * (1024 + 128 * (128 / group)); }
-size_t fixed_bytes(int nb, int group) {
-  return align_up(ring_bytes(nb, group) + kQIntBytes, 16) + (size_t)kQWarps * nb * 128 * sizeof(float);
+// shared memory besides the token rows: ring, routing, the teams' sums
+size_t fixed_bytes(int group) {
+  return align_up((size_t)kQWarps * kQDepth * 2 * (1024 + 32 * (128 / group)) + kQIntBytes, 16) +
+         (size_t)kQWarps * 2 * 128 * sizeof(float);
 }
 // token columns are padded to whole MMAs in the table of group sums
 int pad_cols(int cols) { return cols <= 8 ? 8 : cols <= 16 ? 16 : 32; }
@@ -562,9 +573,9 @@ size_t token_bytes(int64_t len, int group, int rows) {
 
 // token columns of one pass over an expert: up to 32, as many rows of `len`
 // elements as shared memory holds
-int pass_cap(int64_t len, int nb, int group) {
+int pass_cap(int64_t len, int group) {
   int rows = 32;
-  while (rows > 0 && fixed_bytes(nb, group) + token_bytes(len, group, rows) > kQSmem) --rows;
+  while (rows > 0 && fixed_bytes(group) + token_bytes(len, group, rows) > kQSmem) --rows;
   return rows;
 }
 
@@ -579,8 +590,8 @@ int down_slices(const moeblaze_shape& s, int group, int tokens) {
   int64_t least = INT64_MAX;
   for (int n = 1; n <= blocks && n <= 64; ++n) {
     if (blocks % n) continue;
-    if (n < blocks && pass_cap(s.h / n, 1, group) < std::min(tokens, 16)) continue;
-    const int64_t units = used * (s.d / 16) * n, per_cta = (units + sm_count() - 1) / sm_count();
+    if (n < blocks && pass_cap(s.h / n, group) < std::min(tokens, 16)) continue;
+    const int64_t units = used * (s.d / 32) * n, per_cta = (units + sm_count() - 1) / sm_count();
     const int64_t rounds = (per_cta + kQTeams - 1) / kQTeams, pieces = (blocks / n + kQTeam - 1) / kQTeam;
     const int64_t cost = rounds * (pieces + 1);
     if (cost < least) {
@@ -613,39 +624,39 @@ cudaError_t launch_q(void (*kern)(Params...), unsigned grid, unsigned block, siz
   return cudaLaunchKernelEx(&cfg, kern, static_cast<Params>(args)...);
 }
 
-template <int NB, int GROUP>
+template <int MODE, int GROUP>
 moeblaze_status launch_product_g(QParams p, int tokens, cudaStream_t st) {
   const int64_t len = p.R / p.slices;
-  p.cap = pass_cap(len, NB, GROUP);
+  p.cap = pass_cap(len, GROUP);
   p.rows = std::min(p.cap, tokens);
-  const size_t sm = fixed_bytes(NB, GROUP) + token_bytes(len, GROUP, p.rows);
+  const size_t sm = fixed_bytes(GROUP) + token_bytes(len, GROUP, p.rows);
   auto run = [&](auto kern) -> moeblaze_status {
     MB_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm));
     // the down projection's h comes from the launch before it, its routing and weights from before that
-    MB_CUDA(launch_q(kern, (unsigned)sm_count(), kQThreads, sm, p.H == nullptr, st, p));
+    MB_CUDA(launch_q(kern, (unsigned)sm_count(), kQThreads, sm, MODE == DOWN, st, p));
     count_launch();
     return MOEBLAZE_OK;
   };
   switch (pad_cols(p.rows)) {
-    case 8: return run(int4_product_kernel<NB, 1, GROUP>);
-    case 16: return run(int4_product_kernel<NB, 2, GROUP>);
+    case 8: return run(int4_product_kernel<MODE, 1, GROUP>);
+    case 16: return run(int4_product_kernel<MODE, 2, GROUP>);
   }
-  return run(int4_product_kernel<NB, 4, GROUP>);
+  return run(int4_product_kernel<MODE, 4, GROUP>);
 }
 
-template <int NB>
+template <int MODE>
 moeblaze_status launch_product(const QParams& p, int group, int tokens, cudaStream_t st) {
   switch (group) {
-    case 32: return launch_product_g<NB, 32>(p, tokens, st);
-    case 64: return launch_product_g<NB, 64>(p, tokens, st);
+    case 32: return launch_product_g<MODE, 32>(p, tokens, st);
+    case 64: return launch_product_g<MODE, 64>(p, tokens, st);
   }
-  return launch_product_g<NB, 128>(p, tokens, st);
+  return launch_product_g<MODE, 128>(p, tokens, st);
 }
 
 }  // namespace
 
 bool int4_shape_ok(const moeblaze_shape& s, int group) {
-  return pass_cap(s.d, s.act == MOEBLAZE_SWIGLU ? 2 : 1, group) >= 1;
+  return pass_cap(s.d, group) >= 1;
 }
 
 size_t int4_ws_bytes(const moeblaze_shape& s, int group) {
@@ -683,7 +694,7 @@ moeblaze_status launch_int4_forward(const moeblaze_shape& s, const __nv_bfloat16
     p.N = s.h;
     p.slices = 1;
     p.H = H;
-    moeblaze_status r = sw ? launch_product<2>(p, w.group, tokens, st) : launch_product<1>(p, w.group, tokens, st);
+    moeblaze_status r = sw ? launch_product<GATED>(p, w.group, tokens, st) : launch_product<SINGLE>(p, w.group, tokens, st);
     if (r != MOEBLAZE_OK) return r;
     p.src = H;
     p.src_ld = s.h;
@@ -694,7 +705,7 @@ moeblaze_status launch_int4_forward(const moeblaze_shape& s, const __nv_bfloat16
     p.slices = down_slices(s, w.group, tokens);
     p.H = nullptr;
     p.part = part;
-    if ((r = launch_product<1>(p, w.group, tokens, st)) != MOEBLAZE_OK) return r;
+    if ((r = launch_product<DOWN>(p, w.group, tokens, st)) != MOEBLAZE_OK) return r;
     const int64_t n = (int64_t)tokens * s.d / 4;
     MB_CUDA(launch_q(int4_combine_kernel, (unsigned)((n + 127) / 128), 128, 0, true, st, (const float*)part,
                      ids + t0 * s.K, gates + t0 * s.K, tokens, (int)s.d, (int)s.E, (int)s.K, p.slices, y + t0 * s.d));
