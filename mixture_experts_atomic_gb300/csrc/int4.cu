@@ -96,7 +96,7 @@ __device__ __noinline__ int last_at_most(const int* table, int n, int v) {
 
 // relative time of a unit whose segment has n token columns: one MMA column
 // tile is hidden behind the weights' loads, more are not
-__device__ __forceinline__ int pass_weight(int n) { return n <= 8 ? 10 : n <= 16 ? 14 : n <= 24 ? 19 : 25; }
+__host__ __device__ __forceinline__ int pass_weight(int n) { return n <= 8 ? 10 : n <= 16 ? 14 : n <= 24 ? 19 : 25; }
 
 // barrier of one team of warps (barrier 0 is the CTA's)
 __device__ __forceinline__ void team_sync(int team) {
@@ -194,6 +194,7 @@ struct QParams {
   int slices;                // the reduction axis in slices of R / slices (DOWN; else 1)
   int cap;                   // token columns of one pass
   int rows;                  // token rows that shared memory holds (<= cap)
+  float inv_grid, inv_full, inv_nt;  // 1 / gridDim, 1 / the weight of a full pass, 1 / units of a segment
   __nv_bfloat16* H;          // GATED, SINGLE: h (pairs x N)
   float* part;               // DOWN: (slices x pairs x N)
 };
@@ -290,26 +291,68 @@ __global__ void __launch_bounds__(kQThreads, 1) int4_product_kernel(const QParam
   const int nt = p.N / (MODE == GATED ? 16 : 32);  // units of a segment
   const int SL = p.R / p.slices, kp = SL / 128, allp = p.R / 128;
   const int per_pass = p.slices * nt;
+  // A segment: pass `pi` of expert e, slice sl; its tiles are the CTA's units
+  // [base, end), counted from the CTA's first unit (base < 0 where another CTA
+  // has its first tiles).  Integer divisions are kept out of this start: they
+  // and a search per unit were 1 us of it.
+  struct Seg {
+    int id, base, end;  // id: e, 9 bits; pi, 10 bits (512 pairs at most); sl, 7 bits (64 slices at most)
+    __device__ int e() const { return id & 511; }
+    __device__ int pi() const { return (id >> 9) & 1023; }
+    __device__ int sl() const { return id >> 19; }
+  };
+  auto next_segment = [&](Seg& s) {
+    s.base = s.end;
+    s.end += nt;
+    int e = s.e(), pi = s.pi(), sl = s.sl() + 1;
+    if (sl == p.slices) {
+      sl = 0;
+      if (++pi == pre[e + 1] - pre[e]) {
+        pi = 0;
+        do ++e;
+        while (e + 1 < p.E && pre[e + 1] == pre[e]);
+      }
+    }
+    s.id = e | (pi << 9) | (sl << 19);
+  };
   // This CTA's units: an even share of the weights.  Lanes 0 and 1 map the
   // share's ends, blockIdx W / gridDim of the total weight W, to units; a
   // CTA's end and the next one's start are the same computation, which never
   // decreases from one to the next.
-  int u0, u1;
+  Seg start;
+  int units;
   {
-    const int share = wpre[p.E] * (int)(blockIdx.x + (lane & 1));
-    const int q = share / (int)gridDim.x, r = share % (int)gridDim.x;
-    int u = pre[p.E] * per_pass;
-    if (q < wpre[p.E]) {
-      const int e = last_at_most(wpre, p.E, q);
-      const int wf = pass_weight(p.cap), pass = min((q - wpre[e]) / wf, cnt[e] / p.cap);
-      const int n = min(p.cap, cnt[e] - pass * p.cap);
-      const float in = (float)((q - wpre[e] - pass * wf) * (int)gridDim.x + r) / (float)(pass_weight(n) * (int)gridDim.x);
-      u = (pre[e] + pass) * per_pass + min(per_pass, (int)(in * (float)per_pass));
+    const int W = wpre[p.E];
+    const float at = (float)W * ((float)(blockIdx.x + (lane & 1)) * p.inv_grid);
+    const int q = (int)at;
+    int e = p.E, pi = 0, off0 = 0, first = pre[p.E] * per_pass;
+    if (blockIdx.x + (lane & 1) < gridDim.x && q < W) {
+      e = last_at_most(wpre, p.E, q);
+      pi = min((int)((float)(q - wpre[e]) * p.inv_full), pre[e + 1] - pre[e] - 1);
+      const int n = min(p.cap, cnt[e] - pi * p.cap);
+      const float in = (at - (float)(wpre[e] + pi * pass_weight(p.cap))) / (float)pass_weight(n);
+      off0 = min(per_pass, max(0, (int)(in * (float)per_pass)));
+      first = (pre[e] + pi) * per_pass + off0;
     }
-    u0 = __shfl_sync(0xffffffffu, u, 0);
-    u1 = __shfl_sync(0xffffffffu, u, 1);
+    // the slice and tile of unit off0 of the pass
+    int sl = (int)((float)off0 * p.inv_nt);
+    if (sl * nt > off0) --sl;
+    if ((sl + 1) * nt <= off0) ++sl;
+    units = __shfl_sync(0xffffffffu, first, 1) - __shfl_sync(0xffffffffu, first, 0);
+    e = __shfl_sync(0xffffffffu, e, 0);
+    pi = __shfl_sync(0xffffffffu, pi, 0);
+    sl = __shfl_sync(0xffffffffu, sl, 0);
+    start.base = -(__shfl_sync(0xffffffffu, off0, 0) - sl * nt);
+    start.end = start.base + nt;
+    const bool over = sl == p.slices;  // the share begins with the next pass
+    if (over) {
+      --sl;
+      start.end = start.base;
+    }
+    start.id = e | (pi << 9) | (sl << 19);
+    if (over && units > 0) next_segment(start);
   }
-  if (u0 >= u1) {
+  if (units <= 0) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     return;
   }
@@ -319,18 +362,19 @@ __global__ void __launch_bounds__(kQThreads, 1) int4_product_kernel(const QParam
   const uint32_t ring_s = saddr(qsm) + warp * PIECES * ENTRY + 1024 + g * 4 * SW;
   const int team = warp / kQTeam, mate = warp % kQTeam;
   const int k0 = kp * mate / kQTeam, k1 = kp * (mate + 1) / kQTeam;  // this warp's pieces of a unit
-  int fu = u0 + team;
-  int left = 0;
+  int fu = team, left = 0;
+  Seg fseg = start;
   uint32_t fslot = 0;  // byte offset of the ring entry to fill
   const uint8_t* fw[NB];
   const uint8_t* fs[NB];
   auto fetch_unit = [&]() {
-    if (fu >= u1 || k0 == k1) return;
-    const int seg = fu / nt, tile = fu - seg * nt, sl = seg % p.slices, e = last_at_most(pre, p.E, seg / p.slices);
+    if (fu >= units || k0 == k1) return;
+    while (fu >= fseg.end) next_segment(fseg);
+    const int tile = fu - fseg.base;
 #pragma unroll
     for (int br = 0; br < NB; ++br) {
-      const int64_t row = MODE == GATED ? (int64_t)e * nt + tile : ((int64_t)e * nt + tile) * 2 + br;
-      const int64_t at = row * allp + sl * kp + k0;
+      const int64_t row = MODE == GATED ? (int64_t)fseg.e() * nt + tile : ((int64_t)fseg.e() * nt + tile) * 2 + br;
+      const int64_t at = row * allp + fseg.sl() * kp + k0;
       fw[br] = p.w[MODE == GATED ? br : 0] + at * 1024 + lane * 16;
       fs[br] = p.s[MODE == GATED ? br : 0] + at * (32 * SW) + g * (4 * SW);
     }
@@ -366,11 +410,10 @@ __global__ void __launch_bounds__(kQThreads, 1) int4_product_kernel(const QParam
   const int pitch = SL * 2 + 64;  // rows 16 banks apart: 2 rows x 64 bytes of a fragment load do not conflict
   float* nsx = reinterpret_cast<float*>(xs + (size_t)p.rows * pitch);  // [groups][8 NTL]: -136 sum x
   uint32_t slot = 0;
-  int u = u0 + team;
-  for (int seg = u0 / nt; seg * nt < u1; ++seg) {
-    const int pass = seg / p.slices, sl = seg % p.slices, e = last_at_most(pre, p.E, pass);
-    const int first = off[e] + (pass - pre[e]) * p.cap;
-    const int n = min(p.cap, off[e] + cnt[e] - first);
+  int u = team;
+  for (Seg seg = start;; next_segment(seg)) {
+    const int e = seg.e(), sl = seg.sl(), first = off[e] + seg.pi() * p.cap;
+    const int n = min(p.cap, cnt[e] - seg.pi() * p.cap);
     __syncthreads();  // every warp is done with the previous segment's rows
     // a warp per 1024 elements of a row: 8 elements a lane, four times, all
     // in flight together; their sums meet over the GROUP / 8 lanes of a group
@@ -405,7 +448,7 @@ __global__ void __launch_bounds__(kQThreads, 1) int4_product_kernel(const QParam
       }
     }
     __syncthreads();
-    const int send = min((seg + 1) * nt, u1);
+    const int send = min(seg.end, units);
     // the segment's units of this team, for T tiles of 8 token columns
     auto run_units = [&](auto tiles) {
       constexpr int T = decltype(tiles)::value;
@@ -499,7 +542,7 @@ __global__ void __launch_bounds__(kQThreads, 1) int4_product_kernel(const QParam
             for (int w = 0; w < kQTeam; ++w)
               sum[br] += swap[(((team * kQTeam + w) * NB + br) * 4 + mate) * 32 + lane];
           }
-          const int tk = 8 * i + 2 * tq + (mate & 1), unit = u - seg * nt;
+          const int tk = 8 * i + 2 * tq + (mate & 1), unit = u - seg.base;
           if (tk < n) {
             const int pair = list[first + tk];
             const int64_t at = (int64_t)(MODE == DOWN ? sl * p.pairs + pair : pair) * p.N;
@@ -523,6 +566,7 @@ __global__ void __launch_bounds__(kQThreads, 1) int4_product_kernel(const QParam
     else if (NTL == 2 || n <= 16) run_units(std::integral_constant<int, (NTL < 2 ? NTL : 2)>());
     else if (n <= 24) run_units(std::integral_constant<int, (NTL < 3 ? NTL : 3)>());
     else run_units(std::integral_constant<int, NTL>());
+    if (seg.end >= units) break;
   }
   cp_wait<0>();
 }
@@ -629,6 +673,9 @@ moeblaze_status launch_product_g(QParams p, int tokens, cudaStream_t st) {
   const int64_t len = p.R / p.slices;
   p.cap = pass_cap(len, GROUP);
   p.rows = std::min(p.cap, tokens);
+  p.inv_grid = 1.f / (float)sm_count();
+  p.inv_full = 1.f / (float)pass_weight(p.cap);
+  p.inv_nt = 1.f / (float)(p.N / (MODE == GATED ? 16 : 32));
   const size_t sm = fixed_bytes(GROUP) + token_bytes(len, GROUP, p.rows);
   auto run = [&](auto kern) -> moeblaze_status {
     MB_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm));
