@@ -42,6 +42,11 @@ constexpr int kQThreads = 512;
 constexpr int kQWarps = kQThreads / 32;
 constexpr int kQTeam = 4;                          // warps that share a unit's reduction rows
 constexpr int kQTeams = kQWarps / kQTeam;
+// token columns of a pass: two MMA column tiles.  An expert with more pairs is
+// passed over again, its weights read once more (from L2, where they fit):
+// three or four tiles at once spill (64 tokens at d 4096, h 14336, 8 experts:
+// 273 us against 263; 61 over 64 fine-grained experts 82 against 76).
+constexpr int kQCols = 16;
 constexpr int kQMaxTokens = 64;                    // tokens of one launch
 constexpr int kQMaxPairs = kQMaxTokens * kMaxK;    // (token, slot) pairs of one launch
 // What a launch computes.  A unit is two tiles, so that a token fragment
@@ -95,8 +100,8 @@ __device__ __noinline__ int last_at_most(const int* table, int n, int v) {
 }
 
 // relative time of a unit whose segment has n token columns: one MMA column
-// tile is hidden behind the weights' loads, more are not
-__host__ __device__ __forceinline__ int pass_weight(int n) { return n <= 8 ? 10 : n <= 16 ? 14 : n <= 24 ? 19 : 25; }
+// tile is hidden behind the weights' loads, two are not quite
+__host__ __device__ __forceinline__ int pass_weight(int n) { return n <= 8 ? 10 : 13; }
 
 // barrier of one team of warps (barrier 0 is the CTA's)
 __device__ __forceinline__ void team_sync(int team) {
@@ -563,8 +568,6 @@ __global__ void __launch_bounds__(kQThreads, 1) int4_product_kernel(const QParam
       }
     };
     if (NTL == 1 || n <= 8) run_units(std::integral_constant<int, 1>());
-    else if (NTL == 2 || n <= 16) run_units(std::integral_constant<int, (NTL < 2 ? NTL : 2)>());
-    else if (n <= 24) run_units(std::integral_constant<int, (NTL < 3 ? NTL : 3)>());
     else run_units(std::integral_constant<int, NTL>());
     if (seg.end >= units) break;
   }
@@ -610,15 +613,15 @@ size_t fixed_bytes(int group) {
          (size_t)kQWarps * 2 * 128 * sizeof(float);
 }
 // token columns are padded to whole MMAs in the table of group sums
-int pad_cols(int cols) { return cols <= 8 ? 8 : cols <= 16 ? 16 : 32; }
+int pad_cols(int cols) { return cols <= 8 ? 8 : 16; }
 size_t token_bytes(int64_t len, int group, int rows) {
   return (size_t)rows * (len * 2 + 64) + (size_t)(len / group) * pad_cols(rows) * sizeof(float);
 }
 
-// token columns of one pass over an expert: up to 32, as many rows of `len`
+// token columns of one pass over an expert: up to 16, as many rows of `len`
 // elements as shared memory holds
 int pass_cap(int64_t len, int group) {
-  int rows = 32;
+  int rows = kQCols;
   while (rows > 0 && fixed_bytes(group) + token_bytes(len, group, rows) > kQSmem) --rows;
   return rows;
 }
@@ -684,11 +687,7 @@ moeblaze_status launch_product_g(QParams p, int tokens, cudaStream_t st) {
     count_launch();
     return MOEBLAZE_OK;
   };
-  switch (pad_cols(p.rows)) {
-    case 8: return run(int4_product_kernel<MODE, 1, GROUP>);
-    case 16: return run(int4_product_kernel<MODE, 2, GROUP>);
-  }
-  return run(int4_product_kernel<MODE, 4, GROUP>);
+  return p.rows <= 8 ? run(int4_product_kernel<MODE, 1, GROUP>) : run(int4_product_kernel<MODE, 2, GROUP>);
 }
 
 template <int MODE>
