@@ -53,7 +53,7 @@ __device__ __forceinline__ float group_sum(float v) {
 }
 
 template <int VEC, int TE, int EPT>
-__device__ __forceinline__ void load_row(const float* __restrict__ row, int E, int te, bool on, float (&l)[EPT][VEC]) {
+__device__ __forceinline__ void load_row(const float* row, int E, int te, bool on, float (&l)[EPT][VEC]) {
 #pragma unroll
   for (int j = 0; j < EPT; ++j) {
     const int e = (j * TE + te) * VEC;
@@ -65,12 +65,30 @@ __device__ __forceinline__ void load_row(const float* __restrict__ row, int E, i
   }
 }
 
+// The losses from the sums, by one warp: n active tokens, count[e] slots and
+// P[e] = sum_t p_te of E experts, z = sum_t lse_t^2
+__device__ __forceinline__ void write_losses(int E, int K, int n, const int* count, const float* P, float z,
+                                             float* __restrict__ losses) {
+  const int lane = threadIdx.x & 31;
+  float b = 0.f;  // sum_e count_e P_e
+  for (int e = lane; e < E; e += 32) b = fmaf((float)count[e], P[e], b);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) b += __shfl_xor_sync(0xffffffffu, b, o);
+  if (lane == 0) {
+    const float inv = n > 0 ? 1.f / (float)n : 0.f;
+    losses[0] = ((float)E / (float)K) * (b * inv) * inv;
+    losses[1] = inv * z;
+  }
+}
+
 template <int VEC, int TE, int EPT, int U>
 __global__ void __launch_bounds__(kBalThreads) balance_fwd_kernel(const float* __restrict__ logits,
                                                                   const int32_t* __restrict__ ids,
                                                                   const uint8_t* __restrict__ valid, int64_t L, int E,
                                                                   int K, float* __restrict__ lse_out,
-                                                                  float* __restrict__ part) {
+                                                                  float* __restrict__ part,
+                                                                  float* __restrict__ losses,
+                                                                  int32_t* __restrict__ counts) {
   constexpr int GROUPS = kBalThreads / TE;  // tokens side by side in the CTA
   constexpr int KL = (kMaxK + TE - 1) / TE;  // slots a lane counts
   extern __shared__ float sm[];
@@ -168,50 +186,70 @@ __global__ void __launch_bounds__(kBalThreads) balance_fwd_kernel(const float* _
     as[warp] = na;
   }
   __syncthreads();
+  // a CTA's own sums: to the workspace, or, when it is the only one, on to the losses
+  const bool only = gridDim.x == 1;
   float* dst = part + (int64_t)blockIdx.x * bal_cols(E);
   for (int e = tid; e < E; e += kBalThreads) {
     float a = 0.f;
 #pragma unroll
     for (int w = 0; w < kBalWarps; ++w) a += ps[w * E + e];
-    dst[e] = a;
-    reinterpret_cast<int*>(dst)[E + 1 + e] = cs[e];
-  }
-  if (tid == 0) {
-    float z = 0.f;
-    int n = 0;
-#pragma unroll
-    for (int w = 0; w < kBalWarps; ++w) {
-      z += zs[w];
-      n += as[w];
+    if (only) {
+      ps[e] = a;  // (column e is this thread's alone)
+      counts[e] = cs[e];
+    } else {
+      dst[e] = a;
+      reinterpret_cast<int*>(dst)[E + 1 + e] = cs[e];
     }
-    dst[E] = z;
-    reinterpret_cast<int*>(dst)[2 * E + 1] = n;
+  }
+  if (only) __syncthreads();
+  if (tid < 32) {
+    float z = zs[tid];
+    int n = as[tid];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      z += __shfl_xor_sync(0xffffffffu, z, o);
+      n += __shfl_xor_sync(0xffffffffu, n, o);
+    }
+    if (only) {
+      if (tid == 0) counts[E] = n;
+      write_losses(E, K, n, cs, ps, z, losses);
+    } else if (tid == 0) {
+      dst[E] = z;
+      reinterpret_cast<int*>(dst)[2 * E + 1] = n;
+    }
   }
 }
 
 // One cluster adds the G partial rows up, each of its CTAs an equal range of
-// them, and its first CTA forms the two losses and the counts (the last one:
-// the active tokens).  Sums of positive fp32 numbers in trees of a few levels.
+// them, and its first CTA, in whose shared memory the others put their sums,
+// forms the two losses and the counts (the last one: the active tokens).
+// Sums of positive fp32 numbers in trees of a few levels.
 constexpr int kLossThreads = 512;
 constexpr int kLossCluster = 8;
-__global__ void __launch_bounds__(kLossThreads) balance_losses_kernel(const float* __restrict__ part, int G, int E,
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__global__ void __launch_bounds__(kLossThreads) balance_losses_kernel(const float* part, int G, int E,
                                                                       int K, float* __restrict__ losses,
                                                                       int32_t* __restrict__ counts) {
   extern __shared__ float fsm[];
   const int C = bal_cols(E);           // at most 1026 columns
   const int tid = threadIdx.x;
   const int rows = C >= kLossThreads ? 1 : kLossThreads / C;  // threads side by side on a column
-  float* col = fsm;                    // [rows][C]; the integer columns hold int bits
-  int rank, ranks;
+  float* all = fsm;                    // [kLossCluster][C] in the first CTA: every CTA's sums; then the whole sums
+  float* col = fsm + kLossCluster * C; // [rows][C]; the integer columns hold int bits
+  int rank;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
-  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(ranks));
-  const int g0 = G * rank / ranks, g1 = G * (rank + 1) / ranks;
+  const int g0 = G * rank / kLossCluster, g1 = G * (rank + 1) / kLossCluster;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  __syncthreads();
+  cluster_sync();  // the first CTA runs: its shared memory may be written
   asm volatile("griddepcontrol.wait;" ::: "memory");
   for (int i = tid; i < rows * C; i += kLossThreads) {
     const int c = i % C, r = i / C;
     float a = 0.f;
     int n = 0;
-#pragma unroll 4
+#pragma unroll 8
     for (int g = g0 + r; g < g1; g += rows) {
       const float v = part[(int64_t)g * C + c];
       if (c > E) n += __float_as_int(v);
@@ -223,6 +261,7 @@ __global__ void __launch_bounds__(kLossThreads) balance_losses_kernel(const floa
   auto add_up = [&](const float* p, int c, int n, int ld) {
     float a = 0.f;
     int k = 0;
+#pragma unroll 4
     for (int r = 0; r < n; ++r) {
       const float v = p[r * ld];
       if (c > E) k += __float_as_int(v);
@@ -231,92 +270,41 @@ __global__ void __launch_bounds__(kLossThreads) balance_losses_kernel(const floa
     return c > E ? __int_as_float(k) : a;
   };
   __syncthreads();
-  for (int c = tid; c < C; c += kLossThreads) col[c] = add_up(col + c, c, rows, C);
-  if (ranks > 1) {
-    // the first CTA reads the others' columns
-    __syncthreads();
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-    float v[3];
-    if (rank == 0) {
-      int q = 0;
-      for (int c = tid; c < C; c += kLossThreads, ++q) {
-        float a = 0.f;
-        int k = 0;
-        for (int r = 0; r < ranks; ++r) {
-          uint32_t at;
-          float x;
-          asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
-                       : "=r"(at)
-                       : "r"((uint32_t)__cvta_generic_to_shared(col + c)), "r"(r));
-          asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(at) : "memory");
-          if (c > E) k += __float_as_int(x);
-          else a += x;
-        }
-        v[q] = c > E ? __int_as_float(k) : a;
-      }
-    }
-    __syncthreads();
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-    if (rank != 0) return;
-    int q = 0;
-    for (int c = tid; c < C; c += kLossThreads, ++q) col[c] = v[q];
+  for (int c = tid; c < C; c += kLossThreads) {
+    uint32_t at;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;"
+                 : "=r"(at)
+                 : "r"((uint32_t)__cvta_generic_to_shared(all + rank * C + c)));
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(add_up(col + c, c, rows, C)) : "memory");
   }
   __syncthreads();
-  const int n = __float_as_int(col[2 * E + 1]);
-  for (int e = tid; e < E; e += kLossThreads) counts[e] = __float_as_int(col[E + 1 + e]);
-  if (tid == 0) counts[E] = n;
-  if (tid < 32) {
-    float b = 0.f;  // sum_e count_e (sum_t p_te)
-    for (int e = tid; e < E; e += 32) b = fmaf((float)__float_as_int(col[E + 1 + e]), col[e], b);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) b += __shfl_xor_sync(0xffffffffu, b, o);
-    if (tid == 0) {
-      const float inv = n > 0 ? 1.f / (float)n : 0.f;
-      losses[0] = ((float)E / (float)K) * (b * inv) * inv;
-      losses[1] = inv * col[E];
-    }
+  cluster_sync();
+  if (rank != 0) return;
+  for (int c = tid; c < C; c += kLossThreads) {
+    const float v = add_up(all + c, c, kLossCluster, C);
+    all[c] = v;  // (column c is this thread's alone)
+    if (c > E) counts[c - E - 1] = __float_as_int(v);  // counts[E] is the active tokens
   }
+  __syncthreads();
+  if (tid < 32)
+    write_losses(E, K, __float_as_int(all[2 * E + 1]), reinterpret_cast<const int*>(all) + E + 1, all, all[E], losses);
 }
 
 template <int VEC, int TE, int EPT, int U>
 __global__ void __launch_bounds__(kBwdThreads) balance_bwd_kernel(
-    const float* __restrict__ logits, const float* __restrict__ lse_in, const int32_t* __restrict__ counts,
-    const float* __restrict__ dloss, const int32_t* __restrict__ ids, const float* __restrict__ gates,
-    const float* __restrict__ dgates, int64_t L, int E, int K, float* __restrict__ dlogits) {
+    const float* logits, const float* lse_in, const int32_t* counts, const float* dloss, const int32_t* ids,
+    const float* gates, const float* dgates, int64_t L, int E, int K, float* dlogits) {
+  // (no __restrict__: what the kernel before has written must not be read ahead of the wait)
   constexpr int GROUPS = kBwdThreads / TE;
   constexpr int KL = (kMaxK + TE - 1) / TE;  // slots a lane holds
   constexpr int ROW = EPT * TE * VEC + 4;    // a group's row in shared memory (rows 4 banks apart)
   __shared__ __align__(16) float rows[GROUPS * ROW];
   const int tid = threadIdx.x, te = tid % TE, grp = tid / TE;
   float* row = rows + grp * ROW;
-  const int n = counts[E];
-  const float inv_n = n > 0 ? 1.f / (float)n : 0.f;
-  const float A = dloss[0] * (float)E * inv_n, Z = 2.f * dloss[1] * inv_n;
-  // loads relative to the mean load: the integer part of the difference is exact
-  __shared__ int total_s;
-  if (tid < 32) {
-    int a = 0;
-    for (int e = tid; e < E; e += 32) a += counts[e];
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
-    if (tid == 0) total_s = a;
-  }
-  __syncthreads();
-  // (in fp32 and integers: fp64 runs at 1/64 of its rate, and this is every CTA's start)
-  const int mean = total_s / E;
-  const float rest = (float)(total_s % E) / (float)E, scale = n > 0 ? 1.f / ((float)n * (float)K) : 0.f;
-  float f[EPT][VEC];
-#pragma unroll
-  for (int j = 0; j < EPT; ++j)
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-      const int e = (j * TE + te) * VEC + i;
-      f[j][i] = e < E ? ((float)(counts[e] - mean) - rest) * scale : 0.f;
-    }
-  for (int64_t t0 = (int64_t)blockIdx.x * GROUPS * U; t0 < L; t0 += (int64_t)gridDim.x * GROUPS * U) {
-    float l[U][EPT][VEC], lse[U], g[U][KL], dg[U][KL];
-    int id[U][KL];
-    bool act[U];
+  float l[U][EPT][VEC], lse[U], g[U][KL], dg[U][KL];
+  int id[U][KL];
+  bool act[U];
+  auto fetch = [&](int64_t t0) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int64_t t = t0 + u * GROUPS + grp;
@@ -332,6 +320,33 @@ __global__ void __launch_bounds__(kBwdThreads) balance_bwd_kernel(
         id[u][q] = in ? ids[t * K + k] : -1;
       }
     }
+  };
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // the first tokens are on their way while the loads are looked up
+  fetch((int64_t)blockIdx.x * GROUPS * U);
+  const int n = counts[E];
+  const float inv_n = n > 0 ? 1.f / (float)n : 0.f;
+  const float A = dloss[0] * (float)E * inv_n, Z = 2.f * dloss[1] * inv_n;
+  // loads relative to the mean load: the integer part of the difference is
+  // exact (in fp32 and integers: fp64 runs at 1/64 of its rate, and this is
+  // every CTA's start)
+  int total = 0;  // by every warp for itself
+  for (int e = tid & 31; e < E; e += 32) total += counts[e];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  const int mean = total / E;
+  const float rest = (float)(total % E) / (float)E, scale = n > 0 ? 1.f / ((float)n * (float)K) : 0.f;
+  float f[EPT][VEC];
+#pragma unroll
+  for (int j = 0; j < EPT; ++j)
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+      const int e = (j * TE + te) * VEC + i;
+      f[j][i] = e < E ? ((float)(counts[e] - mean) - rest) * scale : 0.f;
+    }
+  const int64_t step = (int64_t)gridDim.x * GROUPS * U;
+  for (int64_t t0 = (int64_t)blockIdx.x * GROUPS * U; t0 < L; t0 += step) {
+    if (t0 >= step) fetch(t0);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int64_t t = t0 + u * GROUPS + grp;
@@ -439,28 +454,28 @@ moeblaze_status fwd_layout(const moeblaze_shape& s, const float* logits, const i
   const int64_t G = bal_ctas(s.L, pass_tokens<kBalThreads, TE, U>(), kFwdPerSm);
   const size_t sm = sizeof(float) * ((size_t)kBalWarps * s.E + s.E + 2 * kBalWarps);
   auto kern = balance_fwd_kernel<VEC, TE, EPT, U>;
-  MB_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm));
-  kern<<<(unsigned)G, kBalThreads, sm, st>>>(logits, ids, valid, s.L, s.E, s.K, lse, part);
+  if (sm > 48 * 1024) MB_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm));
+  kern<<<(unsigned)G, kBalThreads, sm, st>>>(logits, ids, valid, s.L, s.E, s.K, lse, part, losses, counts);
   MB_CUDA(cudaGetLastError());
+  count_launch();
+  if (G == 1) return MOEBLAZE_OK;
   const int C = bal_cols(s.E), rows = C >= kLossThreads ? 1 : kLossThreads / C;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  // few partial rows: one CTA adds them up as fast
-  const unsigned cluster = G >= 4 * kLossCluster ? kLossCluster : 1;
-  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.x = kLossCluster;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  cfg.gridDim = dim3(cluster);
+  cfg.gridDim = dim3(kLossCluster);
   cfg.blockDim = dim3(kLossThreads);
-  cfg.dynamicSmemBytes = sizeof(float) * rows * C;
+  cfg.dynamicSmemBytes = sizeof(float) * (kLossCluster + rows) * C;
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   MB_CUDA(cudaLaunchKernelEx(&cfg, balance_losses_kernel, (const float*)part, (int)G, (int)s.E, (int)s.K, losses,
                              counts));
-  count_launch(2);
+  count_launch();
   return MOEBLAZE_OK;
 }
 
@@ -469,9 +484,18 @@ moeblaze_status bwd_layout(const moeblaze_shape& s, const float* logits, const f
                            const float* dloss, const int32_t* ids, const float* gates, const float* dgates,
                            float* dlogits, cudaStream_t st) {
   const int64_t G = bal_ctas(s.L, pass_tokens<kBwdThreads, TE, U>(), kBwdPerSm);
-  balance_bwd_kernel<VEC, TE, EPT, U><<<(unsigned)G, kBwdThreads, 0, st>>>(logits, lse, counts, dloss, ids, gates,
-                                                                           dgates, s.L, s.E, s.K, dlogits);
-  MB_CUDA(cudaGetLastError());
+  // it may be set up while the kernel before it runs (and waits for its end)
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3((unsigned)G);
+  cfg.blockDim = dim3(kBwdThreads);
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  MB_CUDA(cudaLaunchKernelEx(&cfg, balance_bwd_kernel<VEC, TE, EPT, U>, logits, lse, counts, dloss, ids, gates, dgates,
+                             (int64_t)s.L, (int)s.E, (int)s.K, dlogits));
   count_launch();
   return MOEBLAZE_OK;
 }

@@ -575,7 +575,7 @@ __global__ void __launch_bounds__(WARP ? 32 * kNormWarps : BUDGET, WARP ? 4 : 1)
 // dw and db from the CTAs' partial sums, in the order of the CTAs: 32 columns
 // per block, warp i of its 32 takes partials i, i + 32, ...
 constexpr int kWgradWarps = 32;
-__global__ void __launch_bounds__(32 * kWgradWarps) norm_wgrad_kernel(const float* __restrict__ part, int G, int d,
+__global__ void __launch_bounds__(32 * kWgradWarps) norm_wgrad_kernel(const float* part, int G, int d,
                                                          float* __restrict__ dw, float* __restrict__ db) {
   __shared__ float acc[kWgradWarps][32];
   const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
