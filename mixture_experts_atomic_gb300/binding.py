@@ -362,11 +362,13 @@ def _args(*specs):
     for spec in specs:
         t = spec[0]
         if t is not None:
-            if not t.is_cuda:
-                raise ValueError(f"{spec[1]}: must be a CUDA tensor")
             if current is None:
-                current = torch.cuda.current_device()
-            if t.get_device() != current:
+                if not t.is_cuda:
+                    raise ValueError(f"{spec[1]}: must be a CUDA tensor")
+                current = torch._C._cuda_getDevice()
+            if t.get_device() != current:  # -1 off the GPU
+                if not t.is_cuda:
+                    raise ValueError(f"{spec[1]}: must be a CUDA tensor")
                 raise ValueError(f"{spec[1]}: on {t.device}, but the current device is cuda:{current}")
 
 
@@ -382,9 +384,10 @@ def _bytes_arg(t, name: str, nbytes: int):
     """A caller-provided byte buffer: at least nbytes, contiguous, on the current CUDA device."""
     if not isinstance(t, torch.Tensor) or not t.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous tensor")
-    if t.numel() * t.element_size() < nbytes:
-        raise ValueError(f"{name}: {t.numel() * t.element_size()} bytes, needs {nbytes}")
-    _on_device((t, name))
+    if t.nbytes < nbytes:
+        raise ValueError(f"{name}: {t.nbytes} bytes, needs {nbytes}")
+    if not t.is_cuda or t.get_device() != torch._C._cuda_getDevice():
+        _on_device((t, name))
 
 
 def _weight_specs(shape: Shape, W1, W2, W3, prefix: str = ""):

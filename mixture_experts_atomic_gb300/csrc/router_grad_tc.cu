@@ -55,9 +55,11 @@ constexpr int dw_stage(int ep) { return (kGCols / 64 + dw_atoms(ep)) * 8192; }
 constexpr int dw_smem(int ep) { return kDwStages * dw_stage(ep) + 256 + 1024; }
 
 // ------------------------------------------------------------------ parts
-// rows of dl (L x E fp32) -> [hi | mid | lo], one thread per pair of columns;
-// part_b[block][e] = the block's tokens' sum.  Blocks past the tokens' split
-// Wr (d x E) -> [hi | mid].
+// rows of dl (L x E fp32) -> [hi | mid | lo], V columns a thread (one 16-byte
+// load where every row starts on one, else single floats), all of a thread's
+// rows in flight together; part_b[block][e] = the block's tokens' sum.
+// Blocks past the tokens' split Wr (d x E) -> [hi | mid].
+// (65536 x 64: 8.4 us, against 10.6 us with two columns and four rows.)
 __device__ __forceinline__ void allow_dependents();
 constexpr int kSplitThreads = 256;
 __device__ __forceinline__ void parts(float v, float& hi, float& mid, float& lo) {
@@ -66,58 +68,84 @@ __device__ __forceinline__ void parts(float v, float& hi, float& mid, float& lo)
   mid = __bfloat162float(__float2bfloat16_rn(r));
   lo = r - mid;  // exact; rounded when stored
 }
-template <int EP>
+template <int V>
+__device__ __forceinline__ void split_load(const float* row, int c, int E, bool on, float (&v)[V]) {
+  if constexpr (V == 4) {
+    float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (on && c < E) f = *reinterpret_cast<const float4*>(row + c);  // E is a multiple of 4
+    v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = on && c + i < E ? row[c + i] : 0.f;
+  }
+}
+template <int V>
+__device__ __forceinline__ void split_store(__nv_bfloat16* o, const float (&v)[V]) {
+  if constexpr (V == 4) *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+  else *reinterpret_cast<uint32_t*>(o) = pack_bf16x2(v[0], v[1]);
+}
+template <int EP, int V>
 __global__ void __launch_bounds__(kSplitThreads) split_kernel(const float* __restrict__ dl, const float* __restrict__ Wr,
                                                               int64_t L, int d, int E, int64_t rows, int tblocks,
                                                               __nv_bfloat16* __restrict__ dls,
                                                               __nv_bfloat16* __restrict__ ws,
                                                               float* __restrict__ part_b, int32_t* __restrict__ err) {
-  constexpr int PR = EP / 2, SIDE = kSplitThreads / PR;  // threads of a row, rows side by side
-  const int tid = threadIdx.x, c = (tid % PR) * 2, r0 = tid / PR;
+  constexpr int PR = EP / V, SIDE = kSplitThreads / PR;  // threads of a row, rows side by side
+  constexpr int U = EP / 8;                              // rows of a thread in flight
+  const int tid = threadIdx.x, c = (tid % PR) * V, r0 = tid / PR;
+  const float zero[V] = {};
   allow_dependents();
   if (blockIdx.x == 0 && tid == 0) *err = 0;
   if ((int)blockIdx.x < tblocks) {
     constexpr int W = dl_width(EP);
     const int64_t t0 = blockIdx.x * rows, t1 = min(L, t0 + rows);
-    float2 sum = make_float2(0.f, 0.f);
-#pragma unroll 4
-    for (int64_t t = t0 + r0; t < t1; t += SIDE) {
-      const float a = c < E ? dl[t * E + c] : 0.f, b = c + 1 < E ? dl[t * E + c + 1] : 0.f;
-      sum.x += a;
-      sum.y += b;
-      float ah, am, al, bh, bm, bl;
-      parts(a, ah, am, al);
-      parts(b, bh, bm, bl);
-      uint32_t* o = reinterpret_cast<uint32_t*>(dls + t * W);
-      o[c / 2] = pack_bf16x2(ah, bh);
-      o[(EP + c) / 2] = pack_bf16x2(am, bm);
-      o[(2 * EP + c) / 2] = pack_bf16x2(al, bl);
-      if (W > 3 * EP && c < W - 3 * EP) o[(3 * EP + c) / 2] = 0u;  // (W - 3 EP is EP or 0)
-    }
-    __shared__ float2 acc[kSplitThreads];
-    acc[tid] = sum;
-    __syncthreads();
-    if (tid < PR) {
-      float2 s = make_float2(0.f, 0.f);
-      for (int i = 0; i < SIDE; ++i) {
-        s.x += acc[i * PR + tid].x;
-        s.y += acc[i * PR + tid].y;
+    float sum[V] = {};
+    for (int64_t t = t0 + r0; t < t1; t += SIDE * U) {
+      float v[U][V];
+#pragma unroll
+      for (int u = 0; u < U; ++u) split_load<V>(dl + (t + u * SIDE) * E, c, E, t + u * SIDE < t1, v[u]);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (t + u * SIDE < t1) {
+          float hi[V], mid[V], lo[V];
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            sum[i] += v[u][i];
+            parts(v[u][i], hi[i], mid[i], lo[i]);
+          }
+          __nv_bfloat16* o = dls + (t + u * SIDE) * W + c;
+          split_store<V>(o, hi);
+          split_store<V>(o + EP, mid);
+          split_store<V>(o + 2 * EP, lo);
+          if (W > 3 * EP) split_store<V>(o + 3 * EP, zero);  // (W - 3 EP is EP or 0)
+        }
       }
-      if (c < E) part_b[(int64_t)blockIdx.x * E + c] = s.x;
-      if (c + 1 < E) part_b[(int64_t)blockIdx.x * E + c + 1] = s.y;
+    }
+    __shared__ float acc[SIDE][EP];
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[r0][c + i] = sum[i];
+    __syncthreads();
+    if (tid < E) {
+      float a = 0.f;
+#pragma unroll 8
+      for (int i = 0; i < SIDE; ++i) a += acc[i][tid];
+      part_b[(int64_t)blockIdx.x * E + tid] = a;
     }
   } else {
     constexpr int W = wr_width(EP);
     const int wblocks = (int)gridDim.x - tblocks;
     for (int j = ((int)blockIdx.x - tblocks) * SIDE + r0; j < d; j += wblocks * SIDE) {
-      const float a = c < E ? Wr[(int64_t)j * E + c] : 0.f, b = c + 1 < E ? Wr[(int64_t)j * E + c + 1] : 0.f;
-      float ah, am, al, bh, bm, bl;
-      parts(a, ah, am, al);
-      parts(b, bh, bm, bl);
-      uint32_t* o = reinterpret_cast<uint32_t*>(ws + (int64_t)j * W);
-      o[c / 2] = pack_bf16x2(ah, bh);
-      o[(EP + c) / 2] = pack_bf16x2(am, bm);
-      if (W > 2 * EP) o[(2 * EP + c) / 2] = o[(3 * EP + c) / 2] = 0u;  // EP = 16: 64 columns
+      float v[V], hi[V], mid[V], lo[V];
+      split_load<V>(Wr + (int64_t)j * E, c, E, true, v);
+#pragma unroll
+      for (int i = 0; i < V; ++i) parts(v[i], hi[i], mid[i], lo[i]);
+      __nv_bfloat16* o = ws + (int64_t)j * W + c;
+      split_store<V>(o, hi);
+      split_store<V>(o + EP, mid);
+      if (W > 2 * EP) {  // EP = 16: 64 columns
+        split_store<V>(o + 2 * EP, zero);
+        split_store<V>(o + 3 * EP, zero);
+      }
     }
   }
 }
@@ -324,21 +352,23 @@ __global__ void __launch_bounds__(kGThreads, 1) dx_kernel(const __grid_constant_
 // ------------------------------------------------------------------ dWr
 template <int EP>
 __global__ void __launch_bounds__(kGThreads, 1) dwr_kernel(const __grid_constant__ GParams p) {
-  // EP = 16, 32: the parts side by side, N = 3 EP columns.  EP = 64: hi | mid,
-  // N = 128, and a second MMA that adds lo to mid's columns (two accumulators
-  // of 3 x 64 do not fit; all three in 64 columns truncate the large hi sum
-  // three times as often, 1.8e-6 instead of 6e-7 of the norm)
-  constexpr int NA = kGCols / 64, NB = dw_atoms(EP), SB = dw_stage(EP), N = EP == 64 ? 128 : 3 * EP;
+  // The parts of dl side by side: N = 3 EP columns, an accumulator for each
+  // 128-column half of the tile.  EP = 16, 32: two of each, in turn.  EP = 64:
+  // one (two of 2 x 192 columns do not fit), and a half's sums are taken
+  // while the other half's products run.
+  constexpr int NA = kGCols / 64, NB = dw_atoms(EP), SB = dw_stage(EP), N = 3 * EP, BUFS = EP == 64 ? 1 : 2;
   extern __shared__ uint8_t g_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(g_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kDwStages * SB);  // full[4], empty[4], done, dfull[2], dempty[2]
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kDwStages + 5);
+  // full[4], empty[4], done, dfull[2][2], dempty[2][2] (buffer, half)
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kDwStages * SB);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kDwStages + 9);
   volatile int* abort_s = reinterpret_cast<volatile int*>(tmem_slot + 1);
   auto full = [&](int s) { return smem_u32(bars + s); };
   auto empty = [&](int s) { return smem_u32(bars + kDwStages + s); };
   const uint32_t done = smem_u32(bars + 2 * kDwStages);
-  auto dfull = [&](int b) { return smem_u32(bars + 2 * kDwStages + 1 + b); };
-  auto dempty = [&](int b) { return smem_u32(bars + 2 * kDwStages + 3 + b); };
+  auto dfull = [&](int b, int h) { return smem_u32(bars + 2 * kDwStages + 1 + 2 * b + h); };
+  auto dempty = [&](int b, int h) { return smem_u32(bars + 2 * kDwStages + 5 + 2 * b + h); };
+  auto acc_col = [](int b, int h) { return EP == 64 ? h * N : b * 256 + h * 128; };
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int m0 = (int)(blockIdx.x % p.tiles) * kGCols, split = (int)(blockIdx.x / p.tiles);
   const int64_t all = (p.L + kDwTokens - 1) / kDwTokens;
@@ -351,10 +381,11 @@ __global__ void __launch_bounds__(kGThreads, 1) dwr_kernel(const __grid_constant
       mbar_init(empty(s), 1);
     }
     mbar_init(done, 1);
-    for (int b = 0; b < 2; ++b) {
-      mbar_init(dfull(b), 1);
-      mbar_init(dempty(b), 8);
-    }
+    for (int b = 0; b < 2; ++b)
+      for (int h = 0; h < 2; ++h) {
+        mbar_init(dfull(b, h), 1);
+        mbar_init(dempty(b, h), 4);
+      }
     *abort_s = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -393,29 +424,30 @@ __global__ void __launch_bounds__(kGThreads, 1) dwr_kernel(const __grid_constant
       uint32_t ph = 0, dph = 0;
       bool ok = true;
       for (int64_t g = c0; ok && g < c1; g += kDwFlush) {
-        ok = wait_bounded(dempty(b), dph ^ 1u, abort_s, p.err, lim);
-        for (int64_t c = g; ok && c < min(c1, g + kDwFlush); ++c) {
+        const int64_t g1 = min(c1, g + kDwFlush);
+        for (int64_t c = g; ok && c < g1; ++c) {
           ok = wait_bounded(full(s), ph, abort_s, p.err, lim);
           if (!ok) break;
           tc_fence_after();
           const uint32_t sA = smem_u32(smem + s * SB), sB = sA + NA * 8192;
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {  // columns 0-127 and 128-255 of the tile
-              const uint64_t ad = smem_desc(sA + h * 16384 + kk * 2048, 8192, 1024);
-              const uint32_t acc = tmem + b * 256 + h * 128;
-              mma_bf16(acc, ad, smem_desc(sB + kk * 2048, 8192, 1024), idesc, (c > g || kk > 0) ? 1u : 0u);
-              if constexpr (EP == 64)
-                mma_bf16(acc + 64, ad, smem_desc(sB + 2 * 8192 + kk * 2048, 8192, 1024), instr_desc(64, true, true), 1u);
+          for (int h = 0; h < 2; ++h) {  // columns 0-127 and 128-255 of the tile
+            if (c == g) {
+              ok = ok && wait_bounded(dempty(b, h), dph ^ 1u, abort_s, p.err, lim);
+              if (!ok) break;
+              tc_fence_after();
             }
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              mma_bf16(tmem + acc_col(b, h), smem_desc(sA + h * 16384 + kk * 2048, 8192, 1024),
+                       smem_desc(sB + kk * 2048, 8192, 1024), idesc, (c > g || kk > 0) ? 1u : 0u);
+            if (c == g1 - 1) mma_commit(dfull(b, h));
+          }
+          if (!ok) break;
           mma_commit(empty(s));
           if (++s == kDwStages) { s = 0; ph ^= 1u; }
         }
-        if (!ok) break;
-        mma_commit(dfull(b));
-        b ^= 1;
-        if (b == 0) dph ^= 1u;
+        if (++b == BUFS) { b = 0; dph ^= 1u; }
       }
       mma_commit(done);
       wait_bounded(done, 0u, nullptr, nullptr, *abort_s ? kDrainNs : lim);
@@ -431,9 +463,9 @@ __global__ void __launch_bounds__(kGThreads, 1) dwr_kernel(const __grid_constant
     int b = 0;
     uint32_t dph = 0;
     for (int64_t g = c0; g < c1; g += kDwFlush) {
-      if (!__all_sync(0xffffffffu, wait_bounded(dfull(b), dph, abort_s, p.err, lim))) break;
+      if (!__all_sync(0xffffffffu, wait_bounded(dfull(b, half), dph, abort_s, p.err, lim))) break;
       tc_fence_after();
-      const uint32_t at = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(b * 256 + half * 128);
+      const uint32_t at = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)acc_col(b, half);
       if constexpr (EP == 16) {  // columns hi 0-15, mid 16-31, lo 32-47 (48-63: not used)
         uint32_t v[32], v2[32];
         MB_TMEM_LD32(at, v);
@@ -442,31 +474,26 @@ __global__ void __launch_bounds__(kGThreads, 1) dwr_kernel(const __grid_constant
 #pragma unroll
         for (int i = 0; i < 16; ++i)
           sum[i] += __uint_as_float(v[i]) + (__uint_as_float(v[16 + i]) + __uint_as_float(v2[i]));
-      } else if constexpr (EP == 32) {
-        uint32_t v[32], v2[32], v3[32];
-        MB_TMEM_LD32(at, v);
-        MB_TMEM_LD32(at + 32, v2);
-        MB_TMEM_LD32(at + 64, v3);
-        tmem_wait_ld();
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-          sum[i] += __uint_as_float(v[i]) + (__uint_as_float(v2[i]) + __uint_as_float(v3[i]));
       } else {
 #pragma unroll
         for (int e0 = 0; e0 < EP; e0 += 32) {
           uint32_t v[32], v2[32];
+          MB_TMEM_LD32(at + EP + e0, v);
+          MB_TMEM_LD32(at + 2 * EP + e0, v2);
+          tmem_wait_ld();
+          float small[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) small[i] = __uint_as_float(v[i]) + __uint_as_float(v2[i]);
           MB_TMEM_LD32(at + e0, v);
-          MB_TMEM_LD32(at + 64 + e0, v2);
           tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 32; ++i) sum[e0 + i] += __uint_as_float(v[i]) + __uint_as_float(v2[i]);
+          for (int i = 0; i < 32; ++i) sum[e0 + i] += __uint_as_float(v[i]) + small[i];
         }
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(dempty(b));
-      b ^= 1;
-      if (b == 0) dph ^= 1u;
+      if (lane == 0) mbar_arrive(dempty(b, half));
+      if (++b == BUFS) { b = 0; dph ^= 1u; }
     }
     const int m = m0 + half * 128 + quarter * 32 + lane;
     if (m < p.d) {
@@ -487,9 +514,8 @@ __global__ void __launch_bounds__(kGThreads, 1) dwr_kernel(const __grid_constant
 // ...; the last blocks take dbias, a lane a value.  A wait that ran out in the
 // kernels before leaves NaN, not a number that looks like a gradient.
 constexpr int kGrWarps = 8;
-__global__ void __launch_bounds__(32 * kGrWarps) grad_reduce_kernel(const float* __restrict__ part,
-                                                                    const float* __restrict__ part_b, int64_t n, int E,
-                                                                    int S, int SB, const int32_t* __restrict__ err,
+__global__ void __launch_bounds__(32 * kGrWarps) grad_reduce_kernel(const float* part, const float* part_b, int64_t n, int E,
+                                                                    int S, int SB, const int32_t* err,
                                                                     float* __restrict__ dWr,
                                                                     float* __restrict__ dbias) {
   __shared__ float4 acc[kGrWarps][32];
@@ -602,8 +628,9 @@ moeblaze_status launch_ep(const moeblaze_shape& s, const void* x, const float* W
   if (p.wait_ns == 0) p.wait_ns = kTimeoutNs;
 
   const int wblocks = dx ? std::max(1, std::min(sm_count(), s.d / 16)) : 0;
-  split_kernel<EP><<<(unsigned)(pl.tblocks + wblocks), kSplitThreads, 0, st>>>(dl, Wr, s.L, s.d, s.E, pl.rows,
-                                                                               pl.tblocks, dls, wsp, part_b, p.err);
+  auto split = s.E % 4 == 0 && ((uintptr_t)Wr & 15) == 0 ? split_kernel<EP, 4> : split_kernel<EP, 2>;
+  split<<<(unsigned)(pl.tblocks + wblocks), kSplitThreads, 0, st>>>(dl, Wr, s.L, s.d, s.E, pl.rows, pl.tblocks, dls, wsp,
+                                                                    part_b, p.err);
   MB_CUDA(cudaGetLastError());
   count_launch();
   if (dx) {
