@@ -313,20 +313,21 @@ __device__ __forceinline__ void copy_ahead(void* dst, const void* src) {
                : "memory");
 }
 
+constexpr int kBwdDepth = 4;
 // The backward's shapes.  WARP: four rows per CTA, a warp each; else a row per
 // CTA, of as many threads as its words need.  BUDGET: threads of an SM, which
 // set the registers a thread may have and the ring's depth (two rows at work,
 // the others on their way; with two, a row is fetched as soon as its place is
-// free).
-template <typename T, int NV, int BUDGET>
+// free).  RES: with a gradient dsum besides dy, a third array.
+template <typename T, int NV, int BUDGET, bool RES>
 constexpr int bwd_depth() {
-  constexpr int row = 3 * 16 * NV;  // bytes of a row a thread holds
+  constexpr int row = (RES ? 3 : 2) * 16 * NV;  // bytes of a row a thread holds
   constexpr int room = 200 * 1024 / BUDGET / row;
-  return room >= 4 ? 4 : room < 2 ? 2 : room;
+  return room >= kBwdDepth ? kBwdDepth : room < 2 ? 2 : room;
 }
-template <typename T, int NV, int BUDGET>
+template <typename T, int NV, int BUDGET, bool RES>
 constexpr size_t bwd_smem(int threads) {
-  return (size_t)bwd_depth<T, NV, BUDGET>() * 3 * 16 * NV * threads;
+  return (size_t)bwd_depth<T, NV, BUDGET, RES>() * (RES ? 3 : 2) * 16 * NV * threads;
 }
 
 // Rows that do not start on 16 bytes (SHIFT): the 16-byte words of a dense
@@ -340,14 +341,18 @@ constexpr size_t bwd_smem(int threads) {
 // THREADS: the CTA's threads where they are known here, 0 where not (the ring's
 // and the sums' places then cost instructions: 182 us against 194 us at
 // 32768 x 4096 bf16).
-template <typename T, int NV, bool WARP, int BUDGET, int THREADS, bool SHIFT>
+template <typename T, int NV, bool WARP, int BUDGET, int THREADS, bool SHIFT, bool RES>
 __global__ void __launch_bounds__(WARP ? 32 * kNormWarps : BUDGET, WARP ? 4 : 1) norm_bwd_kernel(
     const T* dy, const T* s, const float* __restrict__ mean, const float* __restrict__ rstd,
     const float* __restrict__ w, const T* dsum, int64_t L, int d, T* dx, float* __restrict__ part) {
-  constexpr int VEC = 16 / (int)sizeof(T), ROWS = WARP ? kNormWarps : 1, D = bwd_depth<T, NV, BUDGET>();
+  constexpr int VEC = 16 / (int)sizeof(T), ROWS = WARP ? kNormWarps : 1, A = RES ? 3 : 2,
+                D = bwd_depth<T, NV, BUDGET, RES>();
+  // D rows at a time, for constant places in the ring (32768 x 4096 bf16: 181
+  // against 185 us, 155 against 169 without dsum); two words a thread: slower
+  constexpr bool UNROLL = sizeof(T) == 2 && NV == 1;
   using V = Vec<T, VEC>;
   extern __shared__ __align__(16) uint8_t nsm[];
-  uint4* ring = reinterpret_cast<uint4*>(nsm);  // [D][3][NV][threads]: dy, s, dsum
+  uint4* ring = reinterpret_cast<uint4*>(nsm);  // [D][A][NV][threads]: dy, s and, with RES, dsum
   __shared__ float red[2][2][32];  // [buffer][sum][warp]
   const int tid = threadIdx.x, NT = WARP ? 32 * kNormWarps : THREADS ? THREADS : (int)blockDim.x, TPR = WARP ? 32 : NT;
   const int lane = WARP ? (tid & 31) : tid;
@@ -388,7 +393,7 @@ __global__ void __launch_bounds__(WARP ? 32 * kNormWarps : BUDGET, WARP ? 4 : 1)
     float f[NV][VEC];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      uint4 u = ring[((at * 3 + a) * NV + j) * NT + tid];
+      uint4 u = ring[((at * A + a) * NV + j) * NT + tid];
       if (SHIFT && clean) {
         u.x &= keep[j][0];
         u.y &= keep[j][1];
@@ -403,28 +408,33 @@ __global__ void __launch_bounds__(WARP ? 32 * kNormWarps : BUDGET, WARP ? 4 : 1)
   };
   // pieces past the row's end stay zero
 #pragma unroll
-  for (int q = 0; q < D * 3 * NV; ++q) ring[q * NT + tid] = make_uint4(0u, 0u, 0u, 0u);
+  for (int q = 0; q < D * A * NV; ++q) ring[q * NT + tid] = make_uint4(0u, 0u, 0u, 0u);
+  // the first element of this thread's word in the next row to fetch (SHIFT),
+  // kept from row to row; without SHIFT the place is formed anew for each row
+  // (a register pair less: 187 against 193 us at 32768 x 4096 bf16)
+  int64_t fo = first * d - shift + lane * VEC;
+  const int64_t stride = step * d;
   auto fetch = [&](int64_t t, int at) {
     if (t < L) {
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        const int c = lane + j * TPR;
-        if (c < nvec) {
-          const int64_t o = t * d - shift + c * VEC;
-          uint4* dst = ring + (at * 3 * NV + j) * NT + tid;
+        if (lane + j * TPR < nvec) {
+          const int64_t o = SHIFT ? fo + j * TPR * VEC : t * d + (lane + j * TPR) * VEC;
+          uint4* dst = ring + (at * A * NV + j) * NT + tid;
           if (SHIFT && o + VEC > L * d) {  // the tensor ends inside this word
             const int n = (int)(L * d - o) * (int)sizeof(T);
             copy_part(dst, dy + o, n);
             copy_part(dst + NV * NT, s + o, n);
-            if (dsum) copy_part(dst + 2 * NV * NT, dsum + o, n);
+            if (RES) copy_part(dst + 2 * NV * NT, dsum + o, n);
           } else {
             copy_ahead(dst, dy + o);
             copy_ahead(dst + NV * NT, s + o);
-            if (dsum) copy_ahead(dst + 2 * NV * NT, dsum + o);
+            if (RES) copy_ahead(dst + 2 * NV * NT, dsum + o);
           }
         }
       }
     }
+    if (SHIFT) fo += stride;
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
   // A row's two sums meet at the CTA's barrier.  They are formed one row
@@ -468,7 +478,8 @@ __global__ void __launch_bounds__(WARP ? 32 * kNormWarps : BUDGET, WARP ? 4 : 1)
       mine = make_float2(__shfl_sync(0xffffffffu, v, 0), __shfl_sync(0xffffffffu, v, 16));
     }
   };
-  // dx of row t, in ring slot `at`, from its sums
+  // dx of the next row, in ring slot `at`, from its sums
+  T* kept = dx + first * d - shift + lane * VEC;  // SHIFT: of the next row to finish
   auto finish = [&](int64_t t, int at, int buf, float rs, float off, float2 sums) {
     if constexpr (!WARP) {
       // lanes 0-15 add up the first sum over the warps, lanes 16-31 the second
@@ -489,18 +500,20 @@ __global__ void __launch_bounds__(WARP ? 32 * kNormWarps : BUDGET, WARP ? 4 : 1)
       }
       sums = make_float2(__shfl_sync(0xffffffffu, v, 0), __shfl_sync(0xffffffffu, v, 16));
     }
-    const float2 rs2 = both(rs), off2 = both(off), mg = both(-sums.x * inv_d), mgx = both(-sums.y * inv_d);
-    T* o = dx + t * d - shift;
+    // ds = rs (dy w - mg - (s rs + off) mgx) + r = rs (dy w + c0) + (s c1 + r)
+    const float mg = sums.x * inv_d, mgx = sums.y * inv_d;
+    const float2 rs2 = both(rs), c0 = both(fmaf(-off, mgx, -mg)), c1 = both(-rs * rs * mgx);
     float2 dv[P], sv[P], rv[P];
     // (a neighbour's elements give results that are not stored)
     read(at, 0, dv, false);
     read(at, 1, sv, false);
-    read(at, 2, rv, false);
+    if constexpr (RES) read(at, 2, rv, false);
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-      const float2 xh = __ffma2_rn(sv[i], rs2, off2);
-      rv[i] = __ffma2_rn(rs2, __ffma2_rn(xh, mgx, __ffma2_rn(dv[i], wv[i], mg)), rv[i]);
+      const float2 u = RES ? __ffma2_rn(sv[i], c1, rv[i]) : __fmul2_rn(sv[i], c1);
+      rv[i] = __ffma2_rn(rs2, __ffma2_rn(dv[i], wv[i], c0), u);
     }
+    T* out = SHIFT ? kept : dx + t * d + lane * VEC;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int c = lane + j * TPR;
@@ -510,17 +523,19 @@ __global__ void __launch_bounds__(WARP ? 32 * kNormWarps : BUDGET, WARP ? 4 : 1)
       if (SHIFT && edge) {
 #pragma unroll
         for (int i = 0; i < VEC; ++i)
-          if (inside(c * VEC + i - shift)) st_t(o[(int64_t)c * VEC + i], f[i]);
+          if (inside(c * VEC + i - shift)) st_t(out[j * TPR * VEC + i], f[i]);
       } else if (c < nvec) {
-        *reinterpret_cast<V*>(o + (int64_t)c * VEC) = from_floats<T, VEC>(f);
+        *reinterpret_cast<V*>(out + j * TPR * VEC) = from_floats<T, VEC>(f);
       }
     }
+    if (SHIFT) kept += stride;
   };
   asm volatile("cp.async.wait_group %0;" ::"n"(D - 1) : "memory");
   if (first < L) sum_up(0, 0);  // (whole warps, and whole CTAs where a CTA holds a row)
   if constexpr (!WARP) __syncthreads();
-  int buf = 0, slot = 0;
-  for (int64_t t = first; t < L; t += step, buf ^= 1) {
+  int buf = 0;
+  int64_t t = first;
+  auto row = [&](int slot, int next) {
     const float rs0 = rs, off0 = -mu * rs;
     const float2 sums = mine;
     mu = nmu;
@@ -529,13 +544,28 @@ __global__ void __launch_bounds__(WARP ? 32 * kNormWarps : BUDGET, WARP ? 4 : 1)
       nmu = mean[t + 2 * step];
       nrs = rstd[t + 2 * step];
     }
-    const int next = slot == D - 1 ? 0 : slot + 1;
     asm volatile("cp.async.wait_group %0;" ::"n"(D - 2) : "memory");
     if (t + step < L) sum_up(next, buf ^ 1);
     finish(t, slot, buf, rs0, off0, sums);
     fetch(t + (int64_t)D * step, slot);
     if constexpr (!WARP) __syncthreads();
-    slot = next;
+    t += step;
+    buf ^= 1;
+  };
+  if constexpr (UNROLL) {
+    while (t < L) {
+#pragma unroll
+      for (int slot = 0; slot < D; ++slot) {
+        if (t >= L) break;
+        row(slot, (slot + 1) % D);
+      }
+    }
+  } else {
+    for (int slot = 0; t < L;) {
+      const int next = slot == D - 1 ? 0 : slot + 1;
+      row(slot, next);
+      slot = next;
+    }
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
   float* pw = part + (int64_t)blockIdx.x * 2 * d;
@@ -583,8 +613,17 @@ __global__ void __launch_bounds__(32 * kWgradWarps) norm_wgrad_kernel(const floa
   float a = 0.f;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (c < 2 * d) {
-#pragma unroll 8
-    for (int g = wp; g < G; g += kWgradWarps) a += part[(int64_t)g * 2 * d + c];
+    // 16 in flight at a time, the last ones too
+    for (int g0 = wp; g0 < G; g0 += 16 * kWgradWarps) {
+      float v[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int g = g0 + i * kWgradWarps;
+        v[i] = g < G ? part[(int64_t)g * 2 * d + c] : 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) a += v[i];
+    }
   }
   acc[wp][lane] = a;
   __syncthreads();
@@ -709,12 +748,12 @@ moeblaze_status fwd_tile(const moeblaze_shape& s, const void* x, const void* res
   return MOEBLAZE_OK;
 }
 
-template <typename T, int NV, bool WARP, int BUDGET, int THREADS, bool SHIFT>
+template <typename T, int NV, bool WARP, int BUDGET, int THREADS, bool SHIFT, bool RES>
 moeblaze_status bwd_tile(const moeblaze_shape& s, const BwdShape& b, const void* dy, const void* sum, const float* mean,
                          const float* rstd, const float* w, const void* dsum, void* dx, float* dw, float* db,
                          float* part, cudaStream_t st) {
-  auto kern = norm_bwd_kernel<T, NV, WARP, BUDGET, THREADS, SHIFT>;
-  const size_t sm = bwd_smem<T, NV, BUDGET>(b.threads);
+  auto kern = norm_bwd_kernel<T, NV, WARP, BUDGET, THREADS, SHIFT, RES>;
+  const size_t sm = bwd_smem<T, NV, BUDGET, RES>(b.threads);
   MB_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm));
   kern<<<(unsigned)b.ctas, b.threads, sm, st>>>((const T*)dy, (const T*)sum, mean, rstd, w, (const T*)dsum, s.L, s.d,
                                                 (T*)dx, part);
@@ -743,13 +782,13 @@ moeblaze_status fwd_words(const moeblaze_shape& s, int n, const void* x, const v
 #undef MB_CALL
 }
 
-template <typename T, bool SHIFT>
+template <typename T, bool SHIFT, bool RES>
 moeblaze_status bwd_shaped(const moeblaze_shape& s, const BwdShape& b, const void* dy, const void* sum,
                            const float* mean, const float* rstd, const float* w, const void* dsum, void* dx, float* dw,
                            float* db, float* part, cudaStream_t st) {
   constexpr bool half = sizeof(T) == 2;
 #define MB_CALL(NV, WARP, BUDGET, THREADS) \
-  bwd_tile<T, NV, WARP, BUDGET, THREADS, SHIFT>(s, b, dy, sum, mean, rstd, w, dsum, dx, dw, db, part, st)
+  bwd_tile<T, NV, WARP, BUDGET, THREADS, SHIFT, RES>(s, b, dy, sum, mean, rstd, w, dsum, dx, dw, db, part, st)
   if (b.warp)
     return b.nv == (half ? 1 : 2) ? MB_CALL((half ? 1 : 2), true, 512, 0) : MB_CALL((half ? 2 : 4), true, 512, 0);
   if constexpr (half) {
@@ -801,8 +840,9 @@ moeblaze_status bwd_t(const moeblaze_shape& s, const void* dy, const void* sum, 
     count_launch(3);
     return launch_wgrad(part, (int)G, s.d, dw, db, st);
   }
-  return b.shift ? bwd_shaped<T, true>(s, b, dy, sum, mean, rstd, w, dsum, dx, dw, db, part, st)
-                 : bwd_shaped<T, false>(s, b, dy, sum, mean, rstd, w, dsum, dx, dw, db, part, st);
+  auto run = b.shift ? (dsum ? bwd_shaped<T, true, true> : bwd_shaped<T, true, false>)
+                     : (dsum ? bwd_shaped<T, false, true> : bwd_shaped<T, false, false>);
+  return run(s, b, dy, sum, mean, rstd, w, dsum, dx, dw, db, part, st);
 }
 
 }  // namespace
