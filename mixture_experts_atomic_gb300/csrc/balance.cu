@@ -249,11 +249,16 @@ __global__ void __launch_bounds__(kLossThreads) balance_losses_kernel(const floa
     const int c = i % C, r = i / C;
     float a = 0.f;
     int n = 0;
-#pragma unroll 8
-    for (int g = g0 + r; g < g1; g += rows) {
-      const float v = part[(int64_t)g * C + c];
-      if (c > E) n += __float_as_int(v);
-      else a += v;
+    // eight in flight at a time, the last ones too
+    for (int g = g0 + r; g < g1; g += 8 * rows) {
+      float v[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) v[u] = g + u * rows < g1 ? part[(int64_t)(g + u * rows) * C + c] : 0.f;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        if (c > E) n += __float_as_int(v[u]);
+        else a += v[u];
+      }
     }
     col[i] = c > E ? __int_as_float(n) : a;
   }

@@ -532,10 +532,18 @@ __global__ void __launch_bounds__(32 * kGrWarps) grad_reduce_kernel(const float*
   const int64_t i = weights ? ((int64_t)blockIdx.x * 32 + lane) * 4 : ((int64_t)blockIdx.x - blocks) * 32 + lane;
   if (weights) {
     if (i < n) {
-#pragma unroll 4
-      for (int s = wp; s < S; s += kGrWarps) {
-        const float4 v = *reinterpret_cast<const float4*>(part + s * n + i);
-        a.x += v.x; a.y += v.y; a.z += v.z; a.w += v.w;
+      // four in flight at a time, the last ones too
+      for (int s0 = wp; s0 < S; s0 += 4 * kGrWarps) {
+        float4 v[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int s = s0 + u * kGrWarps;
+          v[u] = s < S ? *reinterpret_cast<const float4*>(part + s * n + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          a.x += v[u].x; a.y += v[u].y; a.z += v[u].z; a.w += v[u].w;
+        }
       }
     }
   } else if (i < E) {
