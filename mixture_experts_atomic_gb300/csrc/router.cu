@@ -689,9 +689,10 @@ __global__ void __launch_bounds__(kBwThreads) router_bwd_small_kernel(
 // ------------------------------------------------------------------ dense logit gradients
 // dWr = x^T dl, dbias = sum_t dl[t], dx = dl Wr^T for a gradient dl (L,E) of
 // every logit (a loss on the logits, such as the load balance, reaches all
-// experts of a token, not the K chosen ones).
+// experts of a token, not the K chosen ones), where router_grad_tc does not
+// take it: fp32, and bf16 with more than 128 experts.
 //
-// Few experts (EP <= 16): one pass over x and dx.  A thread owns CPT = 64/EP
+// Few experts (EP <= 16, fp32): one pass over x and dx.  A thread owns CPT = 64/EP
 // columns with their rows of Wr and its partial dWr in registers (64 floats
 // each), so that a token costs it one piece of x, one of dx and the token's
 // dl row, which the CTA shares; the products are packed fp32x2 FMAs over
@@ -703,28 +704,15 @@ constexpr int dg_cpt() {
   return 64 / EP;
 }
 constexpr int kDgAhead = 8;  // pieces of x each thread has in flight
-template <typename T, int EP>
+template <int EP>
 constexpr size_t dg_smem() {
-  return 2 * (size_t)kRT * EP * sizeof(float2) + (size_t)kDgAhead * kDgThreads * dg_cpt<EP>() * sizeof(T);
+  return 2 * (size_t)kRT * EP * sizeof(float2) + (size_t)kDgAhead * kDgThreads * dg_cpt<EP>() * sizeof(float);
 }
 
-template <int BYTES>
-__device__ __forceinline__ void cp_piece(uint32_t dst, const void* src) {
-  if constexpr (BYTES == 8) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
-  } else {
-#pragma unroll
-    for (int q = 0; q < BYTES / 16; ++q) cp16(dst + 16 * q, static_cast<const char*>(src) + 16 * q, true);
-  }
-}
 template <int N>
-__device__ __forceinline__ void load_piece(const __nv_bfloat16* p, float (&v)[N]) {
+__device__ __forceinline__ void cp_piece(uint32_t dst, const float* src) {
 #pragma unroll
-  for (int q = 0; q < N / 4; ++q) {
-    const uint2 u = reinterpret_cast<const uint2*>(p)[q];
-    const float2 a = unpack_bf16x2(u.x), b = unpack_bf16x2(u.y);
-    v[4 * q] = a.x; v[4 * q + 1] = a.y; v[4 * q + 2] = b.x; v[4 * q + 3] = b.y;
-  }
+  for (int q = 0; q < N / 4; ++q) cp16(dst + 16 * q, src + 4 * q, true);
 }
 template <int N>
 __device__ __forceinline__ void load_piece(const float* p, float (&v)[N]) {
@@ -735,31 +723,23 @@ __device__ __forceinline__ void load_piece(const float* p, float (&v)[N]) {
   }
 }
 template <int N>
-__device__ __forceinline__ void store_piece(__nv_bfloat16* p, const float (&v)[N]) {
-  if constexpr (N == 8) {
-    store8(p, v);
-  } else {
-    *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
-  }
-}
-template <int N>
 __device__ __forceinline__ void store_piece(float* p, const float (&v)[N]) {
 #pragma unroll
   for (int q = 0; q < N / 4; ++q)
     reinterpret_cast<float4*>(p)[q] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
 }
 
-template <typename T, int EP>
-__global__ void __launch_bounds__(kDgThreads, 3) router_dense_small_kernel(const T* __restrict__ x,
+template <int EP>
+__global__ void __launch_bounds__(kDgThreads, 3) router_dense_small_kernel(const float* __restrict__ x,
                                                                            const float* __restrict__ Wr,
                                                                            const float* __restrict__ dl, int64_t L,
                                                                            int d, int E, int64_t split,
-                                                                           T* dx, bool add, float* __restrict__ part,
+                                                                           float* dx, bool add, float* __restrict__ part,
                                                                            float* __restrict__ part_b) {
-  constexpr int CPT = dg_cpt<EP>(), PB = CPT * (int)sizeof(T);
+  constexpr int CPT = dg_cpt<EP>(), PB = CPT * (int)sizeof(float);
   extern __shared__ __align__(16) uint8_t rsm[];
   float2* ds = reinterpret_cast<float2*>(rsm);           // 2 x [64 tokens][EP] (v, v), experts >= E zero
-  T* xs = reinterpret_cast<T*>(ds + 2 * kRT * EP);       // [kDgAhead][threads][CPT]: each thread's own pieces
+  float* xs = reinterpret_cast<float*>(ds + 2 * kRT * EP);       // [kDgAhead][threads][CPT]: each thread's own pieces
   const int tid = threadIdx.x;
   const int j = (blockIdx.x * kDgThreads + tid) * CPT;
   const bool jv = j < d;
@@ -774,7 +754,7 @@ __global__ void __launch_bounds__(kDgThreads, 3) router_dense_small_kernel(const
     }
   const int64_t ts = (int64_t)blockIdx.y * split, tend = min(L, ts + split);
   const int n = (int)(tend - ts);  // at least 1: the host makes no empty split
-  const T* xp = x + ts * d + j;    // the piece to copy next
+  const float* xp = x + ts * d + j;    // the piece to copy next
   const uint32_t xa = saddr(xs + tid * CPT);
   constexpr uint32_t XS = kDgThreads * PB;
   // chunk c of dl (64 tokens) into buffer c & 1: through registers, since both halves get a copy
@@ -794,11 +774,11 @@ __global__ void __launch_bounds__(kDgThreads, 3) router_dense_small_kernel(const
   load_dl(0);
 #pragma unroll
   for (int t = 0; t < kDgAhead; ++t) {
-    if (jv && t < n) cp_piece<PB>(xa + t * XS, xp);
+    if (jv && t < n) cp_piece<CPT>(xa + t * XS, xp);
     xp += d;
     cp_commit();
   }
-  T* op = dx ? dx + ts * d + j : nullptr;
+  float* op = dx ? dx + ts * d + j : nullptr;
   float bacc = 0.f;
   for (int c0 = 0; c0 < n; c0 += kRT) {
     const int c = c0 / kRT;
@@ -817,7 +797,7 @@ __global__ void __launch_bounds__(kDgThreads, 3) router_dense_small_kernel(const
         cp_wait<kDgAhead - 1>();
         float xv[CPT];
         load_piece(xs + (u * kDgThreads + tid) * CPT, xv);
-        if (jv && c0 + t8 + u + kDgAhead < n) cp_piece<PB>(xa + u * XS, xp);
+        if (jv && c0 + t8 + u + kDgAhead < n) cp_piece<CPT>(xa + u * XS, xp);
         xp += d;
         cp_commit();
         if (t8 + u < m) {
@@ -1204,11 +1184,11 @@ moeblaze_status dense_ep(const moeblaze_shape& s, const void* x, const float* Wr
   float* part_b = part + (size_t)S * s.d * s.E;
   const dim3 grid((unsigned)dense_col_blocks(s), (unsigned)S);
   if constexpr (EP <= 16) {
-    auto kern = router_dense_small_kernel<T, EP>;
-    const size_t sm = dg_smem<T, EP>();
+    auto kern = router_dense_small_kernel<EP>;
+    const size_t sm = dg_smem<EP>();
     MB_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm));
-    kern<<<grid, kDgThreads, sm, st>>>(static_cast<const T*>(x), Wr, dl, s.L, s.d, s.E, split, static_cast<T*>(dx), add,
-                                       part, part_b);
+    kern<<<grid, kDgThreads, sm, st>>>(static_cast<const float*>(x), Wr, dl, s.L, s.d, s.E, split,
+                                       static_cast<float*>(dx), add, part, part_b);
     MB_CUDA(cudaGetLastError());
     count_launch();
   } else {
@@ -1244,7 +1224,9 @@ moeblaze_status dense_ep(const moeblaze_shape& s, const void* x, const float* Wr
 template <typename T>
 moeblaze_status dense_t(const moeblaze_shape& s, const void* x, const float* Wr, const float* dl, float* dWr,
                         float* dbias, void* dx, bool add, void* ws, cudaStream_t st) {
-  switch (padded_experts(s.E)) {
+  // bf16 with fewer experts runs on the tensor cores
+  if constexpr (sizeof(T) == 2) return dense_ep<T, 256>(s, x, Wr, dl, dWr, dbias, dx, add, ws, st);
+  else switch (padded_experts(s.E)) {
     case 8: return dense_ep<T, 8>(s, x, Wr, dl, dWr, dbias, dx, add, ws, st);
     case 16: return dense_ep<T, 16>(s, x, Wr, dl, dWr, dbias, dx, add, ws, st);
     case 32: return dense_ep<T, 32>(s, x, Wr, dl, dWr, dbias, dx, add, ws, st);

@@ -1,5 +1,5 @@
 // The router's gradients from a dense gradient of its logits, on the tensor
-// cores (bf16 x, up to 64 experts):
+// cores (bf16 x, up to 128 experts):
 //
 //   dWr = x^T dl,  dx = dl Wr^T,  dbias = sum_t dl[t]
 //
@@ -13,7 +13,8 @@
 //
 // split_kernel writes dl's parts as rows [hi | mid | lo] of EP columns each
 // (EP = 16, 32 or 64 experts, padded to whole 64-column blocks), Wr's as
-// [hi | mid], and the CTAs' sums of dl for dbias.
+// [hi | mid], and the CTAs' sums of dl for dbias.  More than 64 experts are
+// two groups of 64, a group's parts side by side.
 //
 // dwr_kernel: a CTA owns 256 columns of x and a range of tokens; TMA brings
 // 64 tokens x (256 columns of x, the parts of dl) per stage, both operands
@@ -53,8 +54,10 @@ constexpr int dl_width(int ep) { return (3 * ep + 63) / 64 * 64; }
 constexpr int wr_width(int ep) { return (2 * ep + 63) / 64 * 64; }
 constexpr int dx_blocks(int ep) { return wr_width(ep) / 64; }   // 64-column blocks of hi | mid
 constexpr int dw_atoms(int ep) { return dl_width(ep) / 64; }
-constexpr int dx_smem(int ep) {  // Wr | token tiles | store staging | barriers | alignment
-  return dx_blocks(ep) * kGCols * 128 + kDxStages * dx_blocks(ep) * kDxTokens * 128 + 8 * 2 * 4096 + 256 + 1024;
+// columns of dx of a CTA: two groups' rows of Wr leave room for half as many
+constexpr int dx_cols(int groups) { return groups == 2 ? kGCols / 2 : kGCols; }
+constexpr int dx_smem(int ep, int groups) {  // Wr | token tiles | store staging | barriers | alignment
+  return groups * dx_blocks(ep) * dx_cols(groups) * 128 + kDxStages * dx_blocks(ep) * kDxTokens * 128 + 8 * 2 * 4096 + 256 + 1024;
 }
 constexpr int dw_stage(int ep) { return (kGCols / 64 + dw_atoms(ep)) * 8192; }
 constexpr int dw_smem(int ep) { return kDwStages * dw_stage(ep) + 256 + 1024; }
@@ -63,7 +66,8 @@ constexpr int dw_smem(int ep) { return kDwStages * dw_stage(ep) + 256 + 1024; }
 // rows of dl (L x E fp32) -> [hi | mid | lo], V columns a thread (one 16-byte
 // load where every row starts on one, else single floats), all of a thread's
 // rows in flight together; part_b[block][e] = the block's tokens' sum.
-// Blocks past the tokens' split Wr (d x E) -> [hi | mid].
+// Blocks past the tokens' split Wr (d x E) -> [hi | mid].  blockIdx.y: the group
+// of experts, gridDim.y of them.
 // (65536 x 64: 8.4 us, against 10.6 us with two columns and four rows.)
 __device__ __forceinline__ void allow_dependents();
 constexpr int kSplitThreads = 256;
@@ -77,7 +81,7 @@ template <int V>
 __device__ __forceinline__ void split_load(const float* row, int c, int E, bool on, float (&v)[V]) {
   if constexpr (V == 4) {
     float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (on && c < E) f = *reinterpret_cast<const float4*>(row + c);  // E is a multiple of 4
+    if (on && c < E) f = *reinterpret_cast<const float4*>(row + c);  // E is a multiple of 4, as the whole row's
     v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
   } else {
 #pragma unroll
@@ -98,17 +102,19 @@ __global__ void __launch_bounds__(kSplitThreads) split_kernel(const float* __res
   constexpr int PR = EP / V, SIDE = kSplitThreads / PR;  // threads of a row, rows side by side
   constexpr int U = EP / 8;                              // rows of a thread in flight
   const int tid = threadIdx.x, c = (tid % PR) * V, r0 = tid / PR;
+  const int g0 = 64 * (int)blockIdx.y, EG = min(EP, E - g0);  // the group's first expert, its experts
   const float zero[V] = {};
   allow_dependents();
-  if (blockIdx.x == 0 && tid == 0) *err = 0;
+  if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) *err = 0;
   if ((int)blockIdx.x < tblocks) {
     constexpr int W = dl_width(EP);
+    dls += blockIdx.y * W;
     const int64_t t0 = blockIdx.x * rows, t1 = min(L, t0 + rows);
     float sum[V] = {};
     for (int64_t t = t0 + r0; t < t1; t += SIDE * U) {
       float v[U][V];
 #pragma unroll
-      for (int u = 0; u < U; ++u) split_load<V>(dl + (t + u * SIDE) * E, c, E, t + u * SIDE < t1, v[u]);
+      for (int u = 0; u < U; ++u) split_load<V>(dl + (t + u * SIDE) * E + g0, c, EG, t + u * SIDE < t1, v[u]);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         if (t + u * SIDE < t1) {
@@ -118,7 +124,7 @@ __global__ void __launch_bounds__(kSplitThreads) split_kernel(const float* __res
             sum[i] += v[u][i];
             parts(v[u][i], hi[i], mid[i], lo[i]);
           }
-          __nv_bfloat16* o = dls + (t + u * SIDE) * W + c;
+          __nv_bfloat16* o = dls + (t + u * SIDE) * (gridDim.y * W) + c;
           split_store<V>(o, hi);
           split_store<V>(o + EP, mid);
           split_store<V>(o + 2 * EP, lo);
@@ -130,21 +136,22 @@ __global__ void __launch_bounds__(kSplitThreads) split_kernel(const float* __res
 #pragma unroll
     for (int i = 0; i < V; ++i) acc[r0][c + i] = sum[i];
     __syncthreads();
-    if (tid < E) {
+    if (tid < EG) {
       float a = 0.f;
 #pragma unroll 8
       for (int i = 0; i < SIDE; ++i) a += acc[i][tid];
-      part_b[(int64_t)blockIdx.x * E + tid] = a;
+      part_b[(int64_t)blockIdx.x * E + g0 + tid] = a;
     }
   } else {
     constexpr int W = wr_width(EP);
+    ws += blockIdx.y * W;
     const int wblocks = (int)gridDim.x - tblocks;
     for (int j = ((int)blockIdx.x - tblocks) * SIDE + r0; j < d; j += wblocks * SIDE) {
       float v[V], hi[V], mid[V], lo[V];
-      split_load<V>(Wr + (int64_t)j * E, c, E, true, v);
+      split_load<V>(Wr + (int64_t)j * E + g0, c, EG, true, v);
 #pragma unroll
       for (int i = 0; i < V; ++i) parts(v[i], hi[i], mid[i], lo[i]);
-      __nv_bfloat16* o = ws + (int64_t)j * W + c;
+      __nv_bfloat16* o = ws + (int64_t)j * (gridDim.y * W) + c;
       split_store<V>(o, hi);
       split_store<V>(o + EP, mid);
       if (W > 2 * EP) {  // EP = 16: 64 columns
@@ -158,7 +165,8 @@ __global__ void __launch_bounds__(kSplitThreads) split_kernel(const float* __res
 struct GParams {
   CUtensorMap tmA, tmB, tmO;  // dx: dl parts, Wr parts, dx;  dwr: x, dl parts
   int64_t L;
-  int d, E, tiles, splits;    // tiles: 256-column tiles; splits: CTAs per tile
+  int d, E, tiles, splits;    // tiles of columns; splits: CTAs per tile (and group)
+  int groups;                 // dwr: groups of 64 experts
   int64_t chunks;             // dwr: 64-token chunks of a split
   int add;                    // dx: added to what is there
   float* part;
@@ -187,12 +195,15 @@ __device__ __forceinline__ void tma_add_2d(const CUtensorMap* map, uint32_t src,
 }
 
 // ------------------------------------------------------------------ dx
-template <int EP>
+// A ring stage is one group's parts of a token tile; the groups of a tile
+// follow one another in the ring and add up in its accumulator.
+template <int EP, int GROUPS>
 __global__ void __launch_bounds__(kGThreads, 1) dx_kernel(const __grid_constant__ GParams p) {
-  constexpr int NB = dx_blocks(EP), SA = NB * kDxTokens * 128, SW = NB * kGCols * 128;
+  constexpr int NB = dx_blocks(EP), COLS = dx_cols(GROUPS);
+  constexpr int SA = NB * kDxTokens * 128, SG = NB * COLS * 128, SW = GROUPS * SG;
   extern __shared__ uint8_t g_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(g_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* sw = smem;                             // Wr: [block][256 rows][128 bytes]
+  uint8_t* sw = smem;                             // Wr: [group][block][COLS rows][128 bytes]
   uint8_t* sa = sw + SW;                          // ring: [stage][block][128 tokens][128 bytes]
   uint8_t* so = sa + kDxStages * SA;              // [warp][2][32 rows][128 bytes]
   uint64_t* bars = reinterpret_cast<uint64_t*>(so + 8 * 2 * 4096);
@@ -205,8 +216,8 @@ __global__ void __launch_bounds__(kGThreads, 1) dx_kernel(const __grid_constant_
   auto dfull = [&](int b) { return smem_u32(bars + 7 + b); };
   auto dempty = [&](int b) { return smem_u32(bars + 9 + b); };
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int n0 = (int)(blockIdx.x % p.tiles) * kGCols, split = (int)(blockIdx.x / p.tiles);
-  const int nw = min(kGCols, p.d - n0);  // a multiple of 64
+  const int n0 = (int)(blockIdx.x % p.tiles) * COLS, split = (int)(blockIdx.x / p.tiles);
+  const int nw = min(COLS, p.d - n0);  // a multiple of 64
   const int64_t tblocks = (p.L + kDxTokens - 1) / kDxTokens;
   const uint64_t lim = p.wait_ns;
   allow_dependents();
@@ -236,19 +247,24 @@ __global__ void __launch_bounds__(kGThreads, 1) dx_kernel(const __grid_constant_
     // ============================================================ TMA producer
     if (lane == 0) {
       mbar_expect_tx(wfull, (uint32_t)SW);
-      for (int b = 0; b < NB; ++b)
-        for (int r = 0; r < kGCols; r += 128)  // rows past d are filled with zeros
-          tma_load_2d(smem_u32(sw + b * kGCols * 128 + r * 128), &p.tmB, b * 64, n0 + r, wfull);
+      for (int b = 0; b < GROUPS * NB; ++b)
+        for (int r = 0; r < COLS; r += 128)  // rows past d are filled with zeros
+          tma_load_2d(smem_u32(sw + b * COLS * 128 + r * 128), &p.tmB, b * 64, n0 + r, wfull);
       int s = 0;
       uint32_t ph = 0, armed = 0, armed_par = 0;
-      for (int64_t t = split; t < tblocks; t += p.splits) {
-        if (!wait_bounded(empty(s), ph ^ 1u, abort_s, p.err, lim)) break;
-        mbar_expect_tx(full(s), (uint32_t)SA);
-        for (int b = 0; b < NB; ++b)
-          tma_load_2d(smem_u32(sa + s * SA + b * kDxTokens * 128), &p.tmA, b * 64, (int)(t * kDxTokens), full(s));
-        armed |= 1u << s;
-        armed_par = (armed_par & ~(1u << s)) | (ph << s);
-        if (++s == kDxStages) { s = 0; ph ^= 1u; }
+      bool ok = true;
+      for (int64_t t = split; ok && t < tblocks; t += p.splits) {
+        for (int g = 0; g < GROUPS; ++g) {
+          ok = wait_bounded(empty(s), ph ^ 1u, abort_s, p.err, lim);
+          if (!ok) break;
+          mbar_expect_tx(full(s), (uint32_t)SA);
+          for (int b = 0; b < NB; ++b)  // (a group's lo columns are not read)
+            tma_load_2d(smem_u32(sa + s * SA + b * kDxTokens * 128), &p.tmA, g * dl_width(EP) + b * 64,
+                        (int)(t * kDxTokens), full(s));
+          armed |= 1u << s;
+          armed_par = (armed_par & ~(1u << s)) | (ph << s);
+          if (++s == kDxStages) { s = 0; ph ^= 1u; }
+        }
       }
       // a CTA that gave up lets its copies in flight land before it exits
       if (*abort_s) {
@@ -266,29 +282,33 @@ __global__ void __launch_bounds__(kGThreads, 1) dx_kernel(const __grid_constant_
       uint32_t ph = 0, dph = 0;
       bool ok = wait_bounded(wfull, 0u, abort_s, p.err, lim);
       for (int64_t t = split; ok && t < tblocks; t += p.splits) {
-        ok = wait_bounded(dempty(b), dph ^ 1u, abort_s, p.err, lim) && wait_bounded(full(s), ph, abort_s, p.err, lim);
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t a0 = smem_u32(sa + s * SA);
-        // slice q (16 experts) of part h: 64-column block (h EP / 16 + q) / 4
-        auto da = [&](int h, int q) {
-          const int i = h * (EP / 16) + q;
-          return smem_desc(a0 + (i / 4) * kDxTokens * 128 + (i % 4) * 32, 16, 1024);
-        };
-        auto dw = [&](int h, int q) {
-          const int i = h * (EP / 16) + q;
-          return smem_desc(w0 + (i / 4) * kGCols * 128 + (i % 4) * 32, 16, 1024);
-        };
-        const uint32_t acc = tmem + b * 256;
+        ok = wait_bounded(dempty(b), dph ^ 1u, abort_s, p.err, lim);
+        for (int g = 0; ok && g < GROUPS; ++g) {
+          ok = wait_bounded(full(s), ph, abort_s, p.err, lim);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t a0 = smem_u32(sa + s * SA), wg = w0 + g * SG;
+          // slice q (16 experts) of part h: 64-column block (h EP / 16 + q) / 4
+          auto da = [&](int h, int q) {
+            const int i = h * (EP / 16) + q;
+            return smem_desc(a0 + (i / 4) * kDxTokens * 128 + (i % 4) * 32, 16, 1024);
+          };
+          auto dw = [&](int h, int q) {
+            const int i = h * (EP / 16) + q;
+            return smem_desc(wg + (i / 4) * COLS * 128 + (i % 4) * 32, 16, 1024);
+          };
+          const uint32_t acc = tmem + b * 256;
 #pragma unroll
-        for (int q = 0; q < EP / 16; ++q) {
-          mma_bf16(acc, da(0, q), dw(0, q), idesc, q > 0);
-          mma_bf16(acc, da(0, q), dw(1, q), idesc, 1u);
-          mma_bf16(acc, da(1, q), dw(0, q), idesc, 1u);
+          for (int q = 0; q < EP / 16; ++q) {
+            mma_bf16(acc, da(0, q), dw(0, q), idesc, g > 0 || q > 0);
+            mma_bf16(acc, da(0, q), dw(1, q), idesc, 1u);
+            mma_bf16(acc, da(1, q), dw(0, q), idesc, 1u);
+          }
+          mma_commit(empty(s));
+          if (++s == kDxStages) { s = 0; ph ^= 1u; }
         }
-        mma_commit(empty(s));
+        if (!ok) break;
         mma_commit(dfull(b));
-        if (++s == kDxStages) { s = 0; ph ^= 1u; }
         b ^= 1;
         if (b == 0) dph ^= 1u;
       }
@@ -309,7 +329,7 @@ __global__ void __launch_bounds__(kGThreads, 1) dx_kernel(const __grid_constant_
       if (!__all_sync(0xffffffffu, wait_bounded(dfull(b), dph, abort_s, p.err, lim))) break;
       tc_fence_after();
       const int64_t row0 = t * kDxTokens + quarter * 32;
-      for (int c = half * 128; c < half * 128 + 128; c += 64) {
+      for (int c = half * (COLS / 2); c < (half + 1) * (COLS / 2); c += 64) {
         if (c >= nw) break;
         uint32_t v[64];
         const uint32_t at = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(b * 256 + c);
@@ -375,7 +395,9 @@ __global__ void __launch_bounds__(kGThreads, 1) dwr_kernel(const __grid_constant
   auto dempty = [&](int b, int h) { return smem_u32(bars + 2 * kDwStages + 5 + 2 * b + h); };
   auto acc_col = [](int b, int h) { return EP == 64 ? h * N : b * 256 + h * 128; };
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int m0 = (int)(blockIdx.x % p.tiles) * kGCols, split = (int)(blockIdx.x / p.tiles);
+  // the groups of a tile and split side by side: the second finds x in L2
+  const int m0 = (int)(blockIdx.x % p.tiles) * kGCols, group = (int)(blockIdx.x / p.tiles) % p.groups;
+  const int split = (int)(blockIdx.x / p.tiles) / p.groups;
   const int64_t all = (p.L + kDwTokens - 1) / kDwTokens;
   const int64_t c0 = split * p.chunks, c1 = min(all, c0 + p.chunks);  // at least one: the host makes no empty split
   const uint64_t lim = p.wait_ns;
@@ -412,7 +434,7 @@ __global__ void __launch_bounds__(kGThreads, 1) dwr_kernel(const __grid_constant
         const uint32_t at = smem_u32(smem + s * SB);
         // tokens past L and columns past d are filled with zeros
         for (int a = 0; a < NA; ++a) tma_load_2d(at + a * 8192, &p.tmA, m0 + a * 64, (int)(c * kDwTokens), full(s));
-        for (int a = 0; a < NB; ++a) tma_load_2d(at + (NA + a) * 8192, &p.tmB, a * 64, (int)(c * kDwTokens), full(s));
+        for (int a = 0; a < NB; ++a) tma_load_2d(at + (NA + a) * 8192, &p.tmB, (group * NB + a) * 64, (int)(c * kDwTokens), full(s));
         armed |= 1u << s;
         armed_par = (armed_par & ~(1u << s)) | (ph << s);
         if (++s == kDwStages) { s = 0; ph ^= 1u; }
@@ -502,10 +524,11 @@ __global__ void __launch_bounds__(kGThreads, 1) dwr_kernel(const __grid_constant
     }
     const int m = m0 + half * 128 + quarter * 32 + lane;
     if (m < p.d) {
-      float* dst = p.part + ((int64_t)split * p.d + m) * p.E;
+      float* dst = p.part + ((int64_t)split * p.d + m) * p.E + group * 64;
+      const int n = min(EP, p.E - group * 64);
 #pragma unroll
       for (int e = 0; e < EP; ++e)
-        if (e < p.E) dst[e] = sum[e];
+        if (e < n) dst[e] = sum[e];
     }
   }
   tc_fence_before();
@@ -570,24 +593,27 @@ __global__ void __launch_bounds__(32 * kGrWarps) grad_reduce_kernel(const float*
   }
 }
 
-int padded(int E) { return E <= 16 ? 16 : E <= 32 ? 32 : 64; }
+int padded(int E) { return E <= 16 ? 16 : E <= 32 ? 32 : 64; }  // of a group
+int groups_of(int E) { return E <= 64 ? 1 : 2; }
 
 struct Plan {
-  int tiles, dw_splits, dx_splits, tblocks;
+  int groups, tiles, dw_splits, dx_tiles, dx_splits, tblocks;
   int64_t chunks, rows;  // chunks of a dWr split; tokens of a split_kernel block
   size_t dls, ws, part, part_b, err, bytes;  // offsets in the workspace
 };
 Plan plan_of(const moeblaze_shape& s) {
   Plan p;
   const int ep = padded(s.E);
+  p.groups = groups_of(s.E);
   p.tiles = (s.d + kGCols - 1) / kGCols;
   const int64_t all = (s.L + kDwTokens - 1) / kDwTokens;
-  int64_t S = std::max<int64_t>(1, sm_count() / p.tiles);
+  int64_t S = std::max<int64_t>(1, sm_count() / (p.tiles * p.groups));
   S = std::min(S, all);
   p.chunks = (all + S - 1) / S;
   p.dw_splits = (int)((all + p.chunks - 1) / p.chunks);
   const int64_t tb = (s.L + kDxTokens - 1) / kDxTokens;
-  p.dx_splits = (int)std::min<int64_t>(std::max<int64_t>(1, sm_count() / p.tiles), tb);
+  p.dx_tiles = (s.d + dx_cols(p.groups) - 1) / dx_cols(p.groups);
+  p.dx_splits = (int)std::min<int64_t>(std::max<int64_t>(1, sm_count() / p.dx_tiles), tb);
   p.rows = std::max<int64_t>(64, (s.L + 4 * sm_count() - 1) / (4 * sm_count()));
   p.tblocks = (int)((s.L + p.rows - 1) / p.rows);
   size_t o = 0;
@@ -596,8 +622,8 @@ Plan plan_of(const moeblaze_shape& s) {
     o += align_up(n, 256);
     return at;
   };
-  p.dls = take((size_t)s.L * dl_width(ep) * 2);
-  p.ws = take((size_t)s.d * wr_width(ep) * 2);
+  p.dls = take((size_t)s.L * p.groups * dl_width(ep) * 2);
+  p.ws = take((size_t)s.d * p.groups * wr_width(ep) * 2);
   p.part = take((size_t)p.dw_splits * s.d * s.E * sizeof(float));
   p.part_b = take((size_t)p.tblocks * s.E * sizeof(float));
   p.err = take(sizeof(int32_t));
@@ -620,7 +646,7 @@ cudaError_t launch_after(void (*kern)(Params...), int64_t grid, int block, size_
   return cudaLaunchKernelEx(&cfg, kern, static_cast<Params>(args)...);
 }
 
-template <int EP>
+template <int EP, int GROUPS>
 moeblaze_status launch_ep(const moeblaze_shape& s, const void* x, const float* Wr, const float* dl, float* dWr,
                           float* dbias, void* dx, bool add, void* ws, cudaStream_t st) {
   const Plan pl = plan_of(s);
@@ -633,7 +659,7 @@ moeblaze_status launch_ep(const moeblaze_shape& s, const void* x, const float* W
   p.L = s.L;
   p.d = s.d;
   p.E = s.E;
-  p.tiles = pl.tiles;
+  p.groups = GROUPS;
   p.part = reinterpret_cast<float*>(w + pl.part);
   p.err = reinterpret_cast<int32_t*>(w + pl.err);
   int withhold = 0;
@@ -642,28 +668,32 @@ moeblaze_status launch_ep(const moeblaze_shape& s, const void* x, const float* W
 
   const int wblocks = dx ? std::max(1, std::min(sm_count(), s.d / 16)) : 0;
   auto split = s.E % 4 == 0 && ((uintptr_t)Wr & 15) == 0 ? split_kernel<EP, 4> : split_kernel<EP, 2>;
-  split<<<(unsigned)(pl.tblocks + wblocks), kSplitThreads, 0, st>>>(dl, Wr, s.L, s.d, s.E, pl.rows, pl.tblocks, dls, wsp,
+  split<<<dim3((unsigned)(pl.tblocks + wblocks), GROUPS), kSplitThreads, 0, st>>>(dl, Wr, s.L, s.d, s.E, pl.rows, pl.tblocks, dls, wsp,
                                                                     part_b, p.err);
   MB_CUDA(cudaGetLastError());
   count_launch();
   if (dx) {
-    if (!make_map(&p.tmA, dls, dl_width(EP), (uint64_t)s.L, 64, kDxTokens) ||
-        !make_map(&p.tmB, wsp, wr_width(EP), (uint64_t)s.d, 64, 128) ||
+    if (!make_map(&p.tmA, dls, GROUPS * dl_width(EP), (uint64_t)s.L, 64, kDxTokens) ||
+        !make_map(&p.tmB, wsp, GROUPS * wr_width(EP), (uint64_t)s.d, 64, 128) ||
         !make_map(&p.tmO, dx, (uint64_t)s.d, (uint64_t)s.L, 64, 32))
       return MOEBLAZE_ERR_CUDA;
+    p.tiles = pl.dx_tiles;
     p.splits = pl.dx_splits;
     p.add = add ? 1 : 0;
-    MB_CUDA(cudaFuncSetAttribute(dx_kernel<EP>, cudaFuncAttributeMaxDynamicSharedMemorySize, dx_smem(EP)));
-    MB_CUDA(launch_after(dx_kernel<EP>, (int64_t)pl.tiles * pl.dx_splits, kGThreads, dx_smem(EP), st, p));
+    auto kern = dx_kernel<EP, GROUPS>;
+    constexpr int smem = dx_smem(EP, GROUPS);
+    MB_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+    MB_CUDA(launch_after(kern, (int64_t)pl.dx_tiles * pl.dx_splits, kGThreads, smem, st, p));
     count_launch();
   }
   if (!make_map(&p.tmA, x, (uint64_t)s.d, (uint64_t)s.L, 64, kDwTokens) ||
-      !make_map(&p.tmB, dls, dl_width(EP), (uint64_t)s.L, 64, kDwTokens))
+      !make_map(&p.tmB, dls, GROUPS * dl_width(EP), (uint64_t)s.L, 64, kDwTokens))
     return MOEBLAZE_ERR_CUDA;
+  p.tiles = pl.tiles;
   p.splits = pl.dw_splits;
   p.chunks = pl.chunks;
   MB_CUDA(cudaFuncSetAttribute(dwr_kernel<EP>, cudaFuncAttributeMaxDynamicSharedMemorySize, dw_smem(EP)));
-  MB_CUDA(launch_after(dwr_kernel<EP>, (int64_t)pl.tiles * pl.dw_splits, kGThreads, dw_smem(EP), st, p));
+  MB_CUDA(launch_after(dwr_kernel<EP>, (int64_t)pl.tiles * GROUPS * pl.dw_splits, kGThreads, dw_smem(EP), st, p));
   const int64_t n = (int64_t)s.d * s.E;
   MB_CUDA(launch_after(grad_reduce_kernel, (n + 127) / 128 + (s.E + 31) / 32, 32 * kGrWarps, 0, st, (const float*)p.part,
                        (const float*)part_b, n, (int)s.E, pl.dw_splits, pl.tblocks, (const int32_t*)p.err, dWr, dbias));
@@ -674,20 +704,18 @@ moeblaze_status launch_ep(const moeblaze_shape& s, const void* x, const float* W
 }  // namespace
 }  // namespace tc
 
-// whole TMA boxes of x, dl and Wr
-bool router_grad_tc(const moeblaze_shape& s) {
-  return s.dtype == MOEBLAZE_BF16 && s.E <= 64 && s.L >= 128 && s.d >= 256;
-}
+bool router_grad_tc(const moeblaze_shape& s) { return s.dtype == MOEBLAZE_BF16 && s.E <= 128 && s.L > 0; }
 
 size_t router_grad_tc_ws_bytes(const moeblaze_shape& s) { return tc::plan_of(s).bytes; }
 
 moeblaze_status launch_router_grad_tc(const moeblaze_shape& s, const void* x, const float* Wr, const float* dl, float* dWr,
                                       float* dbias, void* dx, bool add, void* ws, cudaStream_t st) {
+  if (tc::groups_of(s.E) == 2) return tc::launch_ep<64, 2>(s, x, Wr, dl, dWr, dbias, dx, add, ws, st);
   switch (tc::padded(s.E)) {
-    case 16: return tc::launch_ep<16>(s, x, Wr, dl, dWr, dbias, dx, add, ws, st);
-    case 32: return tc::launch_ep<32>(s, x, Wr, dl, dWr, dbias, dx, add, ws, st);
+    case 16: return tc::launch_ep<16, 1>(s, x, Wr, dl, dWr, dbias, dx, add, ws, st);
+    case 32: return tc::launch_ep<32, 1>(s, x, Wr, dl, dWr, dbias, dx, add, ws, st);
   }
-  return tc::launch_ep<64>(s, x, Wr, dl, dWr, dbias, dx, add, ws, st);
+  return tc::launch_ep<64, 1>(s, x, Wr, dl, dWr, dbias, dx, add, ws, st);
 }
 
 }  // namespace moeblaze

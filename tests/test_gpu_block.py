@@ -293,6 +293,13 @@ def test_router_grad(L, d, E, dt):
 
 
 @pytest.mark.parametrize("dt", [BF16, F32])
+@pytest.mark.parametrize("L,d,E", [(70, 64, 65), (1000, 576, 100), (4097, 320, 128), (2, 64, 128), (600, 128, 129),
+                                   (31, 192, 24), (2500, 1088, 33), (5000, 2048, 90)])
+def test_router_grad_groups_of_experts(L, d, E, dt):
+    test_router_grad(L, d, E, dt)
+
+
+@pytest.mark.parametrize("dt", [BF16, F32])
 @pytest.mark.parametrize("L,d,E", [(70, 64, 8), (333, 448, 64), (300, 320, 100), (1000, 576, 7)])
 def test_router_grad_added_to_a_gradient(L, d, E, dt):
     g = torch.Generator().manual_seed(L + d + E)
