@@ -61,6 +61,15 @@ __device__ __forceinline__ void load8(const float* p, float* v) {
   const float4 b = *reinterpret_cast<const float4*>(p + 4);
   v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
 }
+__device__ __forceinline__ void load4(const __nv_bfloat16* p, float (&v)[4]) {
+  const uint2 u = *reinterpret_cast<const uint2*>(p);
+  const float2 a = unpack_bf16x2(u.x), b = unpack_bf16x2(u.y);
+  v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
+}
+__device__ __forceinline__ void load4(const float* p, float (&v)[4]) {
+  const float4 u = *reinterpret_cast<const float4*>(p);
+  v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
+}
 __device__ __forceinline__ void store8(__nv_bfloat16* p, const float* v) {
   *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
                                             pack_bf16x2(v[6], v[7]));
@@ -852,123 +861,178 @@ __global__ void __launch_bounds__(kDgThreads, 3) router_dense_small_kernel(const
   if (blockIdx.x == 0 && tid < E) part_b[(int64_t)blockIdx.y * E + tid] = bacc;
 }
 
-// More experts: dx in tiles of 64 tokens x 64 columns with the tokens' dl
-// rows and the columns' rows of Wr staged whole (E is the reduction axis)
-template <typename T, int EP>
-__global__ void __launch_bounds__(kRThreads) router_dense_dx_kernel(const float* __restrict__ Wr,
-                                                                    const float* __restrict__ dl, int64_t L, int d,
-                                                                    int E, T* dx, bool add) {
-  constexpr int P = EP + 4;  // pitch: rows 1 apart start 4 banks apart, 16-byte multiples
-  extern __shared__ __align__(16) uint8_t rsm[];
-  float* ds = reinterpret_cast<float*>(rsm);  // [64 tokens][P]
-  float* ws = ds + kRT * P;                   // [64 columns][P]
-  const int tid = threadIdx.x, tr = tid >> 4, tc = tid & 15;
-  const int64_t t0 = (int64_t)blockIdx.y * kRT;
-  const int j0 = blockIdx.x * kRT;
-  for (int i = tid; i < kRT * EP; i += kRThreads) {
-    const int r = i / EP, e = i % EP;
-    ds[r * P + e] = e < E && t0 + r < L ? dl[(t0 + r) * E + e] : 0.f;
-    ws[r * P + e] = e < E ? Wr[(int64_t)(j0 + r) * E + e] : 0.f;
-  }
-  __syncthreads();
-  float2 acc[4][4];
-#pragma unroll
-  for (int a = 0; a < 4; ++a)
-#pragma unroll
-    for (int b = 0; b < 4; ++b) acc[a][b] = make_float2(0.f, 0.f);
-#pragma unroll 4
-  for (int e = 0; e < EP; e += 4) {
-    float4 dv[4], wv[4];
-#pragma unroll
-    for (int a = 0; a < 4; ++a) {
-      dv[a] = *reinterpret_cast<const float4*>(ds + (tr + 16 * a) * P + e);
-      wv[a] = *reinterpret_cast<const float4*>(ws + (tc + 16 * a) * P + e);
+// More experts: products of fp32 pairs out of shared memory, in CTAs of
+// COLS columns that walk over their tokens, the next tokens' rows copied
+// meanwhile.  A thread's tile is wide enough that the FMAs, not the loads
+// from shared memory, set the pace: 20000 x 2048 fp32 takes 172 us with 26
+// experts, 272 us with 55 and 453 us with 96 (293, 395 and 633 us with 64 x 64
+// tiles of 4 x 4 and 2 x 4 values a thread), 30 to 35 TFLOP/s.
+constexpr int kDtTokens = 64;   // tokens of a step of dx
+constexpr int kDwrTokens = 32;  // and of dWr
+template <int EP>
+constexpr int dense_cols() {
+  return EP >= 256 ? 64 : 128;
+}
+// rows [0, n) of ROWS rows of dl (or Wr) from row t0 on, pitch P; the rest
+// zeros.  16 bytes at a time where every row starts on 16
+template <int EP, int ROWS, int P>
+__device__ __forceinline__ void stage_dl(float* dst, const float* dl, int64_t t0, int64_t n, int E, int tid) {
+  if (E % 4 == 0 && (reinterpret_cast<uintptr_t>(dl) & 15) == 0) {
+    for (int i = tid; i < ROWS * EP / 4; i += kRThreads) {
+      const int r = i / (EP / 4), e = i % (EP / 4) * 4;
+      const bool ok = r < n && e < E;
+      cp16(saddr(dst + r * P + e), ok ? (const void*)(dl + (t0 + r) * E + e) : (const void*)dl, ok);
     }
-#pragma unroll
-    for (int a = 0; a < 4; ++a)
-#pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        acc[a][b] = __ffma2_rn(make_float2(dv[a].x, dv[a].y), make_float2(wv[b].x, wv[b].y), acc[a][b]);
-        acc[a][b] = __ffma2_rn(make_float2(dv[a].z, dv[a].w), make_float2(wv[b].z, wv[b].w), acc[a][b]);
-      }
-  }
-#pragma unroll
-  for (int a = 0; a < 4; ++a) {
-    const int64_t t = t0 + tr + 16 * a;
-    if (t >= L) continue;
-#pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      T* o = dx + t * d + j0 + tc + 16 * b;
-      const float v = acc[a][b].x + acc[a][b].y + (add ? to_f32(*o) : 0.f);
-      if constexpr (sizeof(T) == 2) *o = __float2bfloat16_rn(v);
-      else *o = v;
+  } else {
+    for (int i = tid; i < ROWS * EP; i += kRThreads) {
+      const int r = i / EP, e = i % EP;
+      const bool ok = r < n && e < E;
+      cp4(saddr(dst + r * P + e), ok ? (const void*)(dl + (t0 + r) * E + e) : (const void*)dl, ok);
     }
   }
 }
 
-// and dWr as the partial sums of a token split, 64 rows of Wr per CTA
+// dx: the columns' rows of Wr stay in shared memory; a warp holds 8 tokens x
+// all columns, a lane every 32nd column; pairs along the experts
+template <int EP>
+constexpr size_t dense_dx_smem() {
+  return (size_t)(dense_cols<EP>() + 2 * kDtTokens) * (EP + 4) * sizeof(float);
+}
 template <typename T, int EP>
-__global__ void __launch_bounds__(kRThreads) router_dense_dwr_kernel(const T* __restrict__ x,
+__global__ void __launch_bounds__(kRThreads, EP >= 128 ? 1 : 2) router_dense_dx_kernel(const float* __restrict__ Wr,
+                                                                       const float* __restrict__ dl, int64_t L, int d,
+                                                                       int E, int64_t split, T* dx, bool add) {
+  constexpr int P = EP + 4;  // pitch: rows 1 apart start 4 banks apart, 16-byte multiples
+  constexpr int COLS = dense_cols<EP>(), C = COLS / 32, R = kDtTokens / 8;
+  extern __shared__ __align__(16) uint8_t rsm[];
+  float* ws = reinterpret_cast<float*>(rsm);  // [COLS][P]
+  float* ds = ws + COLS * P;                  // 2 x [64 tokens][P]
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int j0 = blockIdx.x * COLS, cols = min(COLS, d - j0);
+  const int64_t ts = (int64_t)blockIdx.y * split, tend = min(L, ts + split);
+  stage_dl<EP, COLS, P>(ws, Wr, j0, cols, E, tid);
+  stage_dl<EP, kDtTokens, P>(ds, dl, ts, tend - ts, E, tid);
+  cp_commit();
+  int buf = 0;
+  for (int64_t t0 = ts; t0 < tend; t0 += kDtTokens, buf ^= 1) {
+    cp_wait<0>();
+    __syncthreads();  // the tokens are here, and the step before has been read
+    if (t0 + kDtTokens < tend)
+      stage_dl<EP, kDtTokens, P>(ds + (buf ^ 1) * kDtTokens * P, dl, t0 + kDtTokens, tend - t0 - kDtTokens, E, tid);
+    cp_commit();
+    const float* dr = ds + (buf * kDtTokens + warp * R) * P;
+    float2 acc[R][C];
+#pragma unroll
+    for (int a = 0; a < R; ++a)
+#pragma unroll
+      for (int b = 0; b < C; ++b) acc[a][b] = make_float2(0.f, 0.f);
+#pragma unroll 2
+    for (int e = 0; e < EP; e += 4) {
+      float4 wv[C];
+#pragma unroll
+      for (int b = 0; b < C; ++b) wv[b] = *reinterpret_cast<const float4*>(ws + (lane + 32 * b) * P + e);
+#pragma unroll
+      for (int a = 0; a < R; ++a) {
+        const float4 dv = *reinterpret_cast<const float4*>(dr + a * P + e);
+#pragma unroll
+        for (int b = 0; b < C; ++b) {
+          acc[a][b] = __ffma2_rn(make_float2(dv.x, dv.y), make_float2(wv[b].x, wv[b].y), acc[a][b]);
+          acc[a][b] = __ffma2_rn(make_float2(dv.z, dv.w), make_float2(wv[b].z, wv[b].w), acc[a][b]);
+        }
+      }
+    }
+#pragma unroll
+    for (int a = 0; a < R; ++a) {
+      const int64_t t = t0 + warp * R + a;
+      if (t >= tend) break;
+#pragma unroll
+      for (int b = 0; b < C; ++b) {
+        if (lane + 32 * b >= cols) continue;
+        T* o = dx + t * d + j0 + lane + 32 * b;
+        const float v = acc[a][b].x + acc[a][b].y + (add ? to_f32(*o) : 0.f);
+        if constexpr (sizeof(T) == 2) *o = __float2bfloat16_rn(v);
+        else *o = v;
+      }
+    }
+  }
+  cp_wait<0>();
+}
+
+// and dWr as the partial sums of a token split: a thread holds 4 experts and
+// every TR-th group of 4 columns; pairs of experts
+template <typename T, int EP>
+constexpr size_t dense_dwr_smem() {
+  return 2 * (size_t)kDwrTokens * (dense_cols<EP>() * sizeof(T) + EP * sizeof(float));
+}
+template <typename T, int EP>
+__global__ void __launch_bounds__(kRThreads, 2) router_dense_dwr_kernel(const T* __restrict__ x,
                                                                      const float* __restrict__ dl, int64_t L, int d,
                                                                      int E, int64_t split, float* __restrict__ part,
                                                                      float* __restrict__ part_b) {
-  using Ly = RLayout<EP>;
-  constexpr int S = 2, P = XPitch<T>::value, XS = kRT * P;
+  constexpr int COLS = dense_cols<EP>(), TE = EP / 4, TR = kRThreads / TE, Q = COLS / (4 * TR);
+  constexpr int V = 16 / (int)sizeof(T);  // elements of a copy
   extern __shared__ __align__(16) uint8_t rsm[];
-  T* xs = reinterpret_cast<T*>(rsm);                                // S x [64 tokens][P]
-  float* dd = reinterpret_cast<float*>(rsm + S * XS * sizeof(T));  // S x [64 tokens][EP]
-  const int tid = threadIdx.x, te = tid % Ly::TE, tr = tid / Ly::TE;
-  const int j0 = blockIdx.x * kRT;
+  T* xs = reinterpret_cast<T*>(rsm);                                    // 2 x [32 tokens][COLS]
+  float* dd = reinterpret_cast<float*>(xs + 2 * kDwrTokens * COLS);     // 2 x [32 tokens][EP]
+  const int tid = threadIdx.x, te = tid % TE, tr = tid / TE;
+  const int j0 = blockIdx.x * COLS, cols = min(COLS, d - j0);
   const int64_t ts = (int64_t)blockIdx.y * split, tend = min(L, ts + split);
-  const int nch = (int)((tend - ts + kRT - 1) / kRT);
-  float acc[Ly::RPT][Ly::EPT];
+  float2 acc[Q][4][2];
 #pragma unroll
-  for (int i = 0; i < Ly::RPT; ++i)
+  for (int q = 0; q < Q; ++q)
 #pragma unroll
-    for (int j = 0; j < Ly::EPT; ++j) acc[i][j] = 0.f;
+    for (int i = 0; i < 4; ++i) acc[q][i][0] = acc[q][i][1] = make_float2(0.f, 0.f);
   float bacc = 0.f;
-  auto stage = [&](int c) {
-    const int64_t c0 = ts + (int64_t)c * kRT;
-    stage_rows<T>(xs + (c % S) * XS, x, c0, tend, d, j0, tid);
-    float* dst = dd + (c % S) * kRT * EP;
-    for (int i = tid; i < kRT * EP; i += kRThreads) {
-      const int r = i / EP, e = i % EP;
-      const bool ok = c0 + r < tend && e < E;
-      cp4(saddr(dst + i), ok ? (const void*)(dl + (c0 + r) * E + e) : (const void*)dl, ok);
+  auto stage = [&](int64_t t0, int buf) {
+    T* dst = xs + buf * kDwrTokens * COLS;
+    for (int i = tid; i < kDwrTokens * COLS / V; i += kRThreads) {
+      const int r = i / (COLS / V), c = i % (COLS / V) * V;
+      const bool ok = t0 + r < tend && c < cols;
+      cp16(saddr(dst + r * COLS + c), ok ? (const void*)(x + (t0 + r) * d + j0 + c) : (const void*)x, ok);
     }
+    stage_dl<EP, kDwrTokens, EP>(dd + buf * kDwrTokens * EP, dl, t0, tend - t0, E, tid);
   };
-  if (nch > 0) stage(0);
+  stage(ts, 0);
   cp_commit();
-  for (int c = 0; c < nch; ++c) {
+  int buf = 0;
+  for (int64_t t0 = ts; t0 < tend; t0 += kDwrTokens, buf ^= 1) {
     cp_wait<0>();
     __syncthreads();
-    if (c + 1 < nch) stage(c + 1);
+    if (t0 + kDwrTokens < tend) stage(t0 + kDwrTokens, buf ^ 1);
     cp_commit();
-    const T* xa = xs + (c % S) * XS;
-    const float* db = dd + (c % S) * kRT * EP;
+    const T* xa = xs + buf * kDwrTokens * COLS;
+    const float* db = dd + buf * kDwrTokens * EP;
 #pragma unroll 4
-    for (int t = 0; t < kRT; ++t) {
-      float av[Ly::RPT], bv[Ly::EPT];
+    for (int t = 0; t < kDwrTokens; ++t) {
+      const float4 dv = *reinterpret_cast<const float4*>(db + t * EP + 4 * te);
+      const float2 d01 = make_float2(dv.x, dv.y), d23 = make_float2(dv.z, dv.w);
 #pragma unroll
-      for (int i = 0; i < Ly::RPT; ++i) av[i] = to_f32(xa[t * P + tr * Ly::RPT + i]);
+      for (int q = 0; q < Q; ++q) {
+        float xv[4];
+        load4(xa + t * COLS + (q * TR + tr) * 4, xv);
 #pragma unroll
-      for (int j = 0; j < Ly::EPT; ++j) bv[j] = db[t * EP + j * Ly::TE + te];
-#pragma unroll
-      for (int i = 0; i < Ly::RPT; ++i)
-#pragma unroll
-        for (int j = 0; j < Ly::EPT; ++j) acc[i][j] = fmaf(av[i], bv[j], acc[i][j]);
+        for (int i = 0; i < 4; ++i) {
+          const float2 x2 = make_float2(xv[i], xv[i]);
+          acc[q][i][0] = __ffma2_rn(x2, d01, acc[q][i][0]);
+          acc[q][i][1] = __ffma2_rn(x2, d23, acc[q][i][1]);
+        }
+      }
     }
     if (blockIdx.x == 0 && tid < EP)
-      for (int t = 0; t < kRT; ++t) bacc += db[t * EP + tid];
+      for (int t = 0; t < kDwrTokens; ++t) bacc += db[t * EP + tid];
   }
   cp_wait<0>();
-  float* dst = part + (int64_t)blockIdx.y * d * E;
+  float* dst = part + ((int64_t)blockIdx.y * d + j0) * E;
 #pragma unroll
-  for (int i = 0; i < Ly::RPT; ++i)
+  for (int q = 0; q < Q; ++q)
 #pragma unroll
-    for (int jj = 0; jj < Ly::EPT; ++jj) {
-      const int e = jj * Ly::TE + te;
-      if (e < E) dst[(int64_t)(j0 + tr * Ly::RPT + i) * E + e] = acc[i][jj];
+    for (int i = 0; i < 4; ++i) {
+      const int c = (q * TR + tr) * 4 + i;
+      if (c >= cols) continue;
+      const float v[4] = {acc[q][i][0].x, acc[q][i][0].y, acc[q][i][1].x, acc[q][i][1].y};
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (4 * te + j < E) dst[(int64_t)c * E + 4 * te + j] = v[j];
     }
   if (blockIdx.x == 0 && tid < E) part_b[(int64_t)blockIdx.y * E + tid] = bacc;
 }
@@ -1161,15 +1225,15 @@ moeblaze_status bwd_t(const moeblaze_shape& s, const void* x, const float* Wr, c
 // CTAs per SM (few experts) or a few waves (more), no empty split
 int64_t dense_col_blocks(const moeblaze_shape& s) {
   const int ep = padded_experts(s.E);
-  const int cols = ep <= 16 ? kDgThreads * (64 / ep) : kRT;
+  const int cols = ep <= 16 && s.dtype == MOEBLAZE_F32 ? kDgThreads * (64 / ep) : s.E > 128 ? 64 : 128;
   return (s.d + cols - 1) / cols;
 }
 int64_t dense_split(const moeblaze_shape& s) {
-  const int64_t jb = dense_col_blocks(s), per_sm = padded_experts(s.E) <= 16 ? 3 : 4;
-  const int64_t S = (per_sm * sm_count() + jb - 1) / jb;
-  const int64_t rows = (s.L + S - 1) / S;
-  if (padded_experts(s.E) <= 16) return rows < kRT ? kRT : rows;
-  return (rows + kRT - 1) / kRT * kRT;
+  const bool small = padded_experts(s.E) <= 16;
+  const int64_t jb = dense_col_blocks(s), per_sm = small ? 3 : 2;
+  int64_t S = std::max<int64_t>(1, per_sm * sm_count() / jb);
+  const int64_t rows = (s.L + S - 1) / S, step = small ? 1 : kDtTokens;
+  return std::max<int64_t>(small ? kRT : kDtTokens, (rows + step - 1) / step * step);
 }
 int64_t dense_splits(const moeblaze_shape& s) {
   const int64_t sp = dense_split(s);
@@ -1194,20 +1258,14 @@ moeblaze_status dense_ep(const moeblaze_shape& s, const void* x, const float* Wr
   } else {
     if (dx) {
       auto kern = router_dense_dx_kernel<T, EP>;
-      const size_t sm = 2 * (size_t)kRT * (EP + 4) * sizeof(float);
+      constexpr size_t sm = dense_dx_smem<EP>();
       MB_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm));
-      // grid.y is limited to 65535 blocks of 64 tokens
-      const int64_t most = (int64_t)65535 * kRT;
-      for (int64_t t = 0; t < s.L; t += most) {
-        const int64_t n = s.L - t < most ? s.L - t : most;
-        kern<<<dim3((unsigned)(s.d / kRT), (unsigned)((n + kRT - 1) / kRT)), kRThreads, sm, st>>>(
-            Wr, dl + t * s.E, n, s.d, s.E, static_cast<T*>(dx) + t * s.d, add);
-        MB_CUDA(cudaGetLastError());
-        count_launch();
-      }
+      kern<<<grid, kRThreads, sm, st>>>(Wr, dl, s.L, s.d, s.E, split, static_cast<T*>(dx), add);
+      MB_CUDA(cudaGetLastError());
+      count_launch();
     }
     auto kern = router_dense_dwr_kernel<T, EP>;
-    const size_t sm = 2 * ((size_t)kRT * XPitch<T>::value * sizeof(T) + (size_t)kRT * EP * sizeof(float));
+    constexpr size_t sm = dense_dwr_smem<T, EP>();
     MB_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm));
     kern<<<grid, kRThreads, sm, st>>>(static_cast<const T*>(x), dl, s.L, s.d, s.E, split, part, part_b);
     MB_CUDA(cudaGetLastError());
