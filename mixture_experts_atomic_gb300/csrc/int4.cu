@@ -574,35 +574,53 @@ __global__ void __launch_bounds__(kQThreads, 1) int4_product_kernel(const QParam
   cp_wait<0>();
 }
 
-// y[t] = sum_k g[t,k] sum_slices part, in that order
-__global__ void int4_combine_kernel(const float* __restrict__ part, const int32_t* __restrict__ ids,
+// y[t] = sum_k g[t,k] sum_slices part, in that order; KM slots (K <= KM) of
+// kMaxK / KM slices in flight together
+template <int KM>
+__global__ void int4_combine_kernel(const float* part, const int32_t* __restrict__ ids,
                                     const float* __restrict__ gates, int L, int d, int E, int K, int slices,
                                     __nv_bfloat16* __restrict__ y) {
+  constexpr int U = kMaxK / KM;
   const int64_t total = (int64_t)L * d / 4;
   const int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x;
   const int t = (int)(i / (d / 4)), c = (int)(i % (d / 4)) * 4;
   // the routing is the caller's: read while the products still run
-  float g[kMaxK];
-  bool on[kMaxK];
+  float g[KM];
+  bool on[KM];
 #pragma unroll
-  for (int k = 0; k < kMaxK; ++k) {
+  for (int k = 0; k < KM; ++k) {
     on[k] = i < total && k < K && (unsigned)ids[t * K + k] < (unsigned)E;
     g[k] = on[k] ? gates[t * K + k] : 0.f;
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (i >= total) return;
+  float4 v[KM];
+#pragma unroll
+  for (int k = 0; k < KM; ++k) v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+  const float* src = part + (int64_t)t * K * d + c;
+  const int64_t slice = (int64_t)L * K * d;
+  for (int s = 0; s < slices; s += U, src += U * slice) {
+    float4 q[U][KM];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int k = 0; k < KM; ++k) {
+        q[u][k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (on[k] && s + u < slices) q[u][k] = *reinterpret_cast<const float4*>(src + u * slice + (int64_t)k * d);
+      }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int k = 0; k < KM; ++k) {
+        v[k].x += q[u][k].x; v[k].y += q[u][k].y; v[k].z += q[u][k].z; v[k].w += q[u][k].w;
+      }
+  }
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-  for (int k = 0; k < kMaxK; ++k) {
-    if (!on[k]) continue;
-    const float* src = part + (int64_t)(t * K + k) * d + c;
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int s = 0; s < slices; ++s) {
-      const float4 q = *reinterpret_cast<const float4*>(src + (int64_t)s * L * K * d);
-      v.x += q.x; v.y += q.y; v.z += q.z; v.w += q.w;
-    }
-    o.x = fmaf(g[k], v.x, o.x); o.y = fmaf(g[k], v.y, o.y); o.z = fmaf(g[k], v.z, o.z); o.w = fmaf(g[k], v.w, o.w);
+  for (int k = 0; k < KM; ++k) {
+    if (!on[k]) continue;  // (an empty slot's gate may be anything)
+    o.x = fmaf(g[k], v[k].x, o.x); o.y = fmaf(g[k], v[k].y, o.y);
+    o.z = fmaf(g[k], v[k].z, o.z); o.w = fmaf(g[k], v[k].w, o.w);
   }
   *reinterpret_cast<uint2*>(y + (int64_t)t * d + c) = make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
 }
@@ -753,7 +771,8 @@ moeblaze_status launch_int4_forward(const moeblaze_shape& s, const __nv_bfloat16
     p.part = part;
     if ((r = launch_product<DOWN>(p, w.group, tokens, st)) != MOEBLAZE_OK) return r;
     const int64_t n = (int64_t)tokens * s.d / 4;
-    MB_CUDA(launch_q(int4_combine_kernel, (unsigned)((n + 127) / 128), 128, 0, true, st, (const float*)part,
+    auto combine = s.K <= 2 ? int4_combine_kernel<2> : int4_combine_kernel<kMaxK>;
+    MB_CUDA(launch_q(combine, (unsigned)((n + 127) / 128), 128, 0, true, st, (const float*)part,
                      ids + t0 * s.K, gates + t0 * s.K, tokens, (int)s.d, (int)s.E, (int)s.K, p.slices, y + t0 * s.d));
     count_launch();
   }
