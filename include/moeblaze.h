@@ -450,7 +450,8 @@ typedef struct {
  *            none but empty slots gets a row of zeros)
  *   gates    device (L,K) fp32       y device (L,d) bf16, overwritten
  *   ws       device moeblaze_int4_workspace_bytes(s, group) bytes
- * The weights are read once per 64 tokens: made for L up to a few tens.  Sums
+ * The weights are read once per 64 tokens and per 16 tokens of an expert
+ * (again from L2, where they fit): made for L up to a few tens.  Sums
  * are fp32 in a fixed order (repeatable to the bit); the hidden activations
  * are rounded to bf16 between the two products, as the matrix instructions
  * take them. */

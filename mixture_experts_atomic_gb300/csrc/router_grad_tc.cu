@@ -94,7 +94,7 @@ __device__ __forceinline__ void split_store(__nv_bfloat16* o, const float (&v)[V
   else *reinterpret_cast<uint32_t*>(o) = pack_bf16x2(v[0], v[1]);
 }
 template <int EP, int V>
-__global__ void __launch_bounds__(kSplitThreads) split_kernel(const float* __restrict__ dl, const float* __restrict__ Wr,
+__global__ void __launch_bounds__(kSplitThreads, 3) split_kernel(const float* __restrict__ dl, const float* __restrict__ Wr,
                                                               int64_t L, int d, int E, int64_t rows, int tblocks,
                                                               __nv_bfloat16* __restrict__ dls,
                                                               __nv_bfloat16* __restrict__ ws,
