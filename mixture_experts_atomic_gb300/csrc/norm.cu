@@ -97,7 +97,8 @@ constexpr int norm_threads() {
 // SHIFT: rows that do not start on 16 bytes.  A thread still loads the whole
 // words the row lies in, whose columns then begin `shift` before the row; the
 // first and the last word are shared with its neighbours and masked.  (With
-// pieces of one element instead: 290 us at 32768 x 1409 bf16.)
+// pieces of one element instead: 290 us at 32768 x 1409 bf16.)  For the rows
+// that norm_fwd_shift_kernel is not for.
 template <typename T, int TPR, int NV, bool SHIFT>
 __global__ void __launch_bounds__(norm_threads<TPR>()) norm_fwd_kernel(const T* x, const T* res,
                                                                         const float* __restrict__ w,
@@ -314,6 +315,156 @@ __device__ __forceinline__ void copy_part(void* dst, const void* src, int n) {
 __device__ __forceinline__ void copy_ahead(void* dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
                : "memory");
+}
+
+// Rows that do not start on 16 bytes, persistent: a CTA's (or a warp's) rows
+// are a multiple of VEC apart, so that their words begin at the same `shift`
+// before the row, and a thread keeps the w and b of its words' columns in
+// registers.  The rows to come are copied ahead into a ring of each thread's
+// own words.  Eight elements a thread; WARP: a row in a warp, four side by
+// side; RES: with a residual.
+// One CTA a row, which has to look its w and b up each time, against this, in
+// bf16: 41261 x 1700 121 and 88 us, with residual 166 and 121 us; 32768 x 1409
+// with residual 129 and 94 us; 131072 x 65 70 and 45 us.
+template <typename T, bool RES>
+constexpr int fwd_depth() {  // 192 KB of an SM's 1024 threads, at most six rows
+  constexpr int room = 192 / (16 * (RES ? 2 : 1) * ((int)sizeof(T) / 2));
+  return room < 6 ? room : 6;
+}
+template <typename T, bool RES>
+constexpr size_t fwd_shift_smem(int threads) {
+  return (size_t)fwd_depth<T, RES>() * (RES ? 2 : 1) * (sizeof(T) / 2) * 16 * threads;
+}
+template <typename T, bool WARP, bool RES>
+__global__ void __launch_bounds__(WARP ? 32 * kNormWarps : 1024, WARP ? 8 : 1) norm_fwd_shift_kernel(
+    const T* x, const T* res, const float* __restrict__ w, const float* __restrict__ b, int64_t L, int d, float eps,
+    T* sum, T* y, float* __restrict__ mean_out, float* __restrict__ rstd_out) {
+  constexpr int VEC = 16 / (int)sizeof(T), NV = 8 / VEC, N = 8, ROWS = WARP ? kNormWarps : 1;
+  constexpr int A = RES ? 2 : 1, D = fwd_depth<T, RES>();
+  using V = Vec<T, VEC>;
+  extern __shared__ __align__(16) uint8_t nsm[];
+  uint4* ring = reinterpret_cast<uint4*>(nsm);  // [D][A][NV][threads]: x and, with RES, the residual
+  __shared__ float red[2][32];
+  const int tid = threadIdx.x, NT = WARP ? 32 * kNormWarps : (int)blockDim.x, TPR = WARP ? 32 : NT, lane = WARP ? (tid & 31) : tid;
+  const int64_t step = (int64_t)gridDim.x * ROWS;
+  const int64_t first = (int64_t)blockIdx.x * ROWS + (WARP ? (tid >> 5) : 0);
+  if (first >= L) return;  // a whole warp or a whole CTA
+  const int shift = (int)((first * d) % VEC), nvec = (shift + d + VEC - 1) / VEC;
+  const int64_t end = L * d;
+  auto column = [&](int q) { return (lane + (q / VEC) * TPR) * VEC + q % VEC - shift; };  // of element q
+  auto inside = [&](int q) { return (unsigned)column(q) < (unsigned)d; };
+  float wv[N], bv[N];
+  bool edge = false;  // a word is shared with a neighbouring row
+#pragma unroll
+  for (int q = 0; q < N; ++q) {
+    wv[q] = inside(q) ? w[column(q)] : 0.f;
+    bv[q] = inside(q) && b ? b[column(q)] : 0.f;
+    edge = edge || (!inside(q) && lane + (q / VEC) * TPR < nvec);
+  }
+  int64_t o = first * d - shift + lane * VEC;  // the thread's first word in the row at work
+  const int64_t stride = step * d;
+  // pieces past the row's end stay zero
+#pragma unroll
+  for (int q = 0; q < D * A * NV; ++q) ring[q * NT + tid] = make_uint4(0u, 0u, 0u, 0u);
+  int64_t ft = first, fo = o;  // the next row to copy
+  auto fetch = [&](int at) {
+    if (ft < L) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        if (lane + j * TPR < nvec) {
+          const int64_t p = fo + j * TPR * VEC;
+          uint4* dst = ring + (at * A * NV + j) * NT + tid;
+          if (p + VEC > end) {  // the tensor ends inside this word
+            const int n = (int)(end - p) * (int)sizeof(T);
+            copy_part(dst, x + p, n);
+            if (RES) copy_part(dst + NV * NT, res + p, n);
+          } else {
+            copy_ahead(dst, x + p);
+            if (RES) copy_ahead(dst + NV * NT, res + p);
+          }
+        }
+      }
+    }
+    ft += step;
+    fo += stride;
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  auto store = [&](T* p, const float (&f)[N]) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      float g[VEC];
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) g[i] = f[j * VEC + i];
+      if (edge) {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i)
+          if (inside(j * VEC + i)) st_t(p[o + j * TPR * VEC + i], g[i]);
+      } else if (lane + j * TPR < nvec) {
+        *reinterpret_cast<V*>(p + o + j * TPR * VEC) = from_floats<T, VEC>(g);
+      }
+    }
+  };
+  const int warps = TPR / 32;
+  auto row_sum = [&](float v, float* r) {
+    v = warp_sum(v);
+    if constexpr (!WARP) {
+      if ((tid & 31) == 0) r[tid >> 5] = v;
+      __syncthreads();
+      v = warp_sum((tid & 31) < warps ? r[tid & 31] : 0.f);
+    }
+    return v;
+  };
+  const float inv_d = 1.f / (float)d;
+#pragma unroll
+  for (int i = 0; i < D; ++i) fetch(i);
+  int slot = 0;
+  for (int64_t t = first; t < L; t += step, o += stride) {
+    float s[N];
+    asm volatile("cp.async.wait_group %0;" ::"n"(D - 1) : "memory");
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      float f[VEC];
+      const uint4* at = ring + (slot * A * NV + j) * NT + tid;
+      const uint4 u = at[0];
+      to_floats(*reinterpret_cast<const V*>(&u), f);
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) s[j * VEC + i] = f[i];
+      if constexpr (RES) {
+        const uint4 v = at[NV * NT];
+        to_floats(*reinterpret_cast<const V*>(&v), f);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) s[j * VEC + i] += f[i];
+      }
+    }
+    fetch(slot);
+    slot = slot == D - 1 ? 0 : slot + 1;
+    // elements outside the row are kept at zero
+    if (edge) {
+#pragma unroll
+      for (int q = 0; q < N; ++q) s[q] = inside(q) ? s[q] : 0.f;
+    }
+    if (sum) store(sum, s);
+    float acc = 0.f;
+#pragma unroll
+    for (int q = 0; q < N; ++q) acc += s[q];
+    const float mu = row_sum(acc, red[0]) * inv_d;
+    acc = 0.f;
+#pragma unroll
+    for (int q = 0; q < N; ++q) {
+      s[q] = lane + (q / VEC) * TPR < nvec ? s[q] - mu : 0.f;
+      if (edge && !inside(q)) s[q] = 0.f;
+      acc = fmaf(s[q], s[q], acc);
+    }
+    const float rstd = 1.f / sqrtf(row_sum(acc, red[1]) * inv_d + eps);
+#pragma unroll
+    for (int q = 0; q < N; ++q) s[q] = fmaf(s[q] * rstd, wv[q], bv[q]);
+    store(y, s);
+    if (lane == 0) {
+      mean_out[t] = mu;
+      rstd_out[t] = rstd;
+    }
+  }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
 constexpr int kBwdDepth = 4;
@@ -770,17 +921,23 @@ template <typename T, bool SHIFT>
 moeblaze_status fwd_words(const moeblaze_shape& s, int n, const void* x, const void* res, const float* w,
                           const float* b, float eps, void* sum, void* y, float* mean, float* rstd, cudaStream_t st) {
 #define MB_CALL(TPR, NV) fwd_tile<T, TPR, NV, SHIFT>(s, x, res, w, b, eps, sum, y, mean, rstd, st)
-  if (n <= 32) return MB_CALL(32, 1);
-  if (n <= 64) return MB_CALL(32, 2);
-  if (n <= 128) return MB_CALL(32, 4);
-  if (n <= 256) return MB_CALL(128, 2);
-  if (n <= 384) return MB_CALL(128, 3);
-  // (without a residual twice the words a thread, for as many loads in flight:
-  // 105 us instead of 117 at 32768 x 4096 bf16)
-  if (n <= 512) return res ? MB_CALL(256, 2) : MB_CALL(128, 4);
-  if (n <= 768) return MB_CALL(256, 3);
-  if (n <= 1024) return MB_CALL(512, 2);
-  if (n <= 2048) return MB_CALL(1024, 2);
+  constexpr bool half = sizeof(T) == 2;
+  if constexpr (!SHIFT) {
+    if (n <= 32) return MB_CALL(32, 1);
+    if (n <= 64) return MB_CALL(32, 2);
+  }
+  if constexpr (!SHIFT || !half) {  // see fwd_t
+    if (n <= 128) return MB_CALL(32, 4);
+    if (n <= 256) return MB_CALL(128, 2);
+    if (n <= 384) return MB_CALL(128, 3);
+    // (without a residual twice the words a thread, for as many loads in flight:
+    // 105 us instead of 117 at 32768 x 4096 bf16)
+    if (n <= 512) return res ? MB_CALL(256, 2) : MB_CALL(128, 4);
+    if (n <= 768) return MB_CALL(256, 3);
+    if (n <= 1024) return MB_CALL(512, 2);
+  }
+  if constexpr (!SHIFT || half)
+    if (n <= 2048) return MB_CALL(1024, 2);
   return MB_CALL(1024, 4);
 #undef MB_CALL
 }
@@ -811,6 +968,30 @@ moeblaze_status bwd_shaped(const moeblaze_shape& s, const BwdShape& b, const voi
 #undef MB_CALL
 }
 
+// rows that do not start on 16 bytes, of up to 8192 elements
+template <typename T>
+moeblaze_status fwd_shift(const moeblaze_shape& s, int words, const void* x, const void* res, const float* w,
+                          const float* b, float eps, void* sum, void* y, float* mean, float* rstd, cudaStream_t st) {
+  constexpr int nv = (int)sizeof(T) / 2;  // words of a thread: 8 elements
+  const int threads = ((words + nv - 1) / nv + 31) / 32 * 32;
+  const bool warp = threads == 32;
+  const int64_t need = warp ? (s.L + kNormWarps - 1) / kNormWarps : s.L;
+  // (two CTAs of 545 to 576 threads still have their registers and rings)
+  int64_t g = (int64_t)(warp ? 8 : threads > 512 && threads <= 576 ? 2 : 1024 / threads) * sm_count();
+  g -= g % 8;  // a CTA's rows are a multiple of 8 apart (shift), unless each has one row
+  if (g > need) g = need;
+  auto kern = warp ? (res ? norm_fwd_shift_kernel<T, true, true> : norm_fwd_shift_kernel<T, true, false>)
+                   : (res ? norm_fwd_shift_kernel<T, false, true> : norm_fwd_shift_kernel<T, false, false>);
+  const int nt = warp ? 32 * kNormWarps : threads;
+  const size_t sm = res ? fwd_shift_smem<T, true>(nt) : fwd_shift_smem<T, false>(nt);
+  MB_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm));
+  kern<<<(unsigned)g, nt, sm, st>>>((const T*)x, (const T*)res, w, b, s.L, s.d, eps,
+                                                                  (T*)sum, (T*)y, mean, rstd);
+  MB_CUDA(cudaGetLastError());
+  count_launch();
+  return MOEBLAZE_OK;
+}
+
 template <typename T>
 moeblaze_status fwd_t(const moeblaze_shape& s, const void* x, const void* res, const float* w, const float* b,
                       float eps, void* sum, void* y, float* mean, float* rstd, cudaStream_t st) {
@@ -824,6 +1005,11 @@ moeblaze_status fwd_t(const moeblaze_shape& s, const void* x, const void* res, c
     count_launch();
     return MOEBLAZE_OK;
   }
+  // fp32 rows of 65 to 1024 words are as fast or faster with a CTA a row
+  // (20000 x 1001 with residual: 55 against 68 us; 8000 x 5001: 137 against 129)
+  constexpr bool half = sizeof(T) == 2;
+  if (shift && (half ? words <= 1024 : words <= 64 || (words > 1024 && words <= 2048)))
+    return fwd_shift<T>(s, words, x, res, w, b, eps, sum, y, mean, rstd, st);
   return shift ? fwd_words<T, true>(s, words, x, res, w, b, eps, sum, y, mean, rstd, st)
                : fwd_words<T, false>(s, words, x, res, w, b, eps, sum, y, mean, rstd, st);
 }
