@@ -145,6 +145,22 @@ def test_norm_in_place_sum_and_extremes():
     assert y[1].isnan().all() and y[2].isnan().any() and torch.equal(y[0], bf)
 
 
+@pytest.mark.parametrize("L,d,dt", [(9000, 65, BF16), (9000, 138, BF16), (4000, 1701, BF16), (700, 4100, BF16),
+                                    (700, 4700, BF16), (400, 8191, BF16), (9000, 35, F32), (9000, 133, F32),
+                                    (700, 4099, F32), (400, 8190, F32)])
+def test_norm_rows_that_share_words(L, d, dt):
+    """Rows that do not start on 16 bytes, several to a CTA; the sum written over the residual changes nothing else."""
+    for residual in (True, False):
+        test_norm_forward(L, d, dt, residual, True)
+        test_norm_backward(L, d, dt, residual)
+    x, res, w, b, _, _ = _norm_inputs(L, d, dt, d)
+    norm = LayerNorm(L, d, dt)
+    y, s, mean, rstd = (t.clone() for t in norm.forward(x, w, b, res))
+    B.layernorm_forward(norm.shape, x, res, w, b, norm.eps, res, norm.y, norm.mean, norm.rstd)
+    assert torch.equal(res, s) and torch.equal(norm.y, y)
+    assert torch.equal(norm.mean, mean) and torch.equal(norm.rstd, rstd)
+
+
 def test_norm_no_tokens_and_repeatable():
     norm = LayerNorm(0, 512, BF16)
     e = torch.empty(0, 512, dtype=BF16, device="cuda")
