@@ -46,8 +46,8 @@ namespace {
 
 constexpr int kQThreads = 512;
 constexpr int kQWarps = kQThreads / 32;
-constexpr int kQTeam = 4;                          // warps that share a unit's reduction rows
-constexpr int kQTeams = kQWarps / kQTeam;
+// warps that share a unit's reduction rows: 4, or 1 where a unit has few (see team_of)
+constexpr int kQTeam = 4;
 // token columns of a pass: two MMA column tiles.  An expert with more pairs is
 // passed over again, its weights read once more (from L2, where they fit):
 // three or four tiles at once spill (64 tokens at d 4096, h 14336, 8 experts:
@@ -110,8 +110,10 @@ __device__ __noinline__ int last_at_most(const int* table, int n, int v) {
 __host__ __device__ __forceinline__ int pass_weight(int n) { return n <= 8 ? 10 : 13; }
 
 // barrier of one team of warps (barrier 0 is the CTA's)
+template <int TEAM>
 __device__ __forceinline__ void team_sync(int team) {
-  asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "n"(kQTeam * 32) : "memory");
+  if constexpr (TEAM == 1) __syncwarp();
+  else asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "n"(TEAM * 32) : "memory");
 }
 
 // ------------------------------------------------------------------ layouts
@@ -212,15 +214,16 @@ struct QParams {
 
 // Work: segments (expert in use, pass of `cap` of its pairs, slice), each
 // with N / 16 tiles of a pair of matrices or N / 32 pairs of tiles; the units
-// are split by weight, contiguously, over the CTAs, and a CTA's units go round its teams of four
-// warps, which share a unit's reduction rows: a CTA's last round then costs a
-// quarter of a unit's time, and few units still keep every warp loading.  A
+// are split by weight, contiguously, over the CTAs, and a CTA's units go round
+// its teams of TEAM warps, which share a unit's reduction rows: with four a
+// CTA's last round costs a quarter of a unit's time, and few units still keep
+// every warp loading; with one no unit is too short to share.  A
 // segment's token rows are staged in shared memory; the packed weights
 // stream through a ring of cp.async pieces per warp, of which every lane
 // reads back only the bytes it copied itself (no barrier), and which runs on
 // across units and segments.  The team's sums meet in shared memory, in the
 // order of its warps.
-template <int MODE, int NTL, int GROUP>
+template <int MODE, int NTL, int GROUP, int TEAM>
 __global__ void __launch_bounds__(kQThreads, 1) int4_product_kernel(const QParams p) {
   constexpr int PIECES = kQDepth, NB = 2;
   constexpr int SW = 128 / GROUP;                   // groups, and scale words of a column pair, in a piece
@@ -371,8 +374,9 @@ __global__ void __launch_bounds__(kQThreads, 1) int4_product_kernel(const QParam
   // ---- the fetch head of this warp: unit, pieces left of it, addresses
   const uint32_t ring = saddr(qsm) + warp * PIECES * ENTRY + lane * 16;
   const uint32_t ring_s = saddr(qsm) + warp * PIECES * ENTRY + 1024 + g * 4 * SW;
-  const int team = warp / kQTeam, mate = warp % kQTeam;
-  const int k0 = kp * mate / kQTeam, k1 = kp * (mate + 1) / kQTeam;  // this warp's pieces of a unit
+  constexpr int TEAMS = kQWarps / TEAM;
+  const int team = warp / TEAM, mate = warp % TEAM;
+  const int k0 = kp * mate / TEAM, k1 = kp * (mate + 1) / TEAM;  // this warp's pieces of a unit
   int fu = team, left = 0;
   Seg fseg = start;
   uint32_t fslot = 0;  // byte offset of the ring entry to fill
@@ -402,7 +406,7 @@ __global__ void __launch_bounds__(kQThreads, 1) int4_product_kernel(const QParam
         fs[br] += 32 * SW;
       }
       if (--left == 0) {
-        fu += kQTeams;
+        fu += TEAMS;
         fetch_unit();
       }
     }
@@ -469,7 +473,7 @@ __global__ void __launch_bounds__(kQThreads, 1) int4_product_kernel(const QParam
 #pragma unroll
       for (int i = 0; i < T; ++i) xrow[i] = xs + (size_t)min(8 * i + g, n - 1) * pitch + tq * 16;
       const float* sums = nsx + 2 * tq;
-      for (; u < send; u += kQTeams) {
+      for (; u < send; u += TEAMS) {
         float acc[NB][T][4];
 #pragma unroll
         for (int br = 0; br < NB; ++br)
@@ -536,41 +540,42 @@ __global__ void __launch_bounds__(kQThreads, 1) int4_product_kernel(const QParam
         }
         // ---- the team's sums of 8 token columns at a time: accumulator v of
         // a lane is column n = 16 tile + g + 8 (v / 2), token 8 i + 2 tq + v % 2;
-        // warp v of the team adds up and stores accumulator v
+        // warp v of the team adds up and stores accumulator v (one warp: all four)
 #pragma unroll
         for (int i = 0; i < T; ++i) {
-          if (i > 0) team_sync(team);  // the tile before is read
+          if (i > 0) team_sync<TEAM>(team);  // the tile before is read
 #pragma unroll
           for (int br = 0; br < NB; ++br)
 #pragma unroll
             for (int v = 0; v < 4; ++v) swap[((warp * NB + br) * 4 + v) * 32 + lane] = acc[br][i][v];
-          team_sync(team);
-          float sum[NB];
+          team_sync<TEAM>(team);
 #pragma unroll
-          for (int br = 0; br < NB; ++br) {
-            sum[br] = 0.f;
+          for (int v = mate; v < 4; v += TEAM) {
+            float sum[NB];
 #pragma unroll
-            for (int w = 0; w < kQTeam; ++w)
-              sum[br] += swap[(((team * kQTeam + w) * NB + br) * 4 + mate) * 32 + lane];
-          }
-          const int tk = 8 * i + 2 * tq + (mate & 1), unit = u - seg.base;
-          if (tk < n) {
+            for (int br = 0; br < NB; ++br) {
+              sum[br] = 0.f;
+#pragma unroll
+              for (int w = 0; w < TEAM; ++w) sum[br] += swap[(((team * TEAM + w) * NB + br) * 4 + v) * 32 + lane];
+            }
+            const int tk = 8 * i + 2 * tq + (v & 1), unit = u - seg.base;
+            if (tk >= n) continue;
             const int pair = list[first + tk];
             const int64_t at = (int64_t)(MODE == DOWN ? sl * p.pairs + pair : pair) * p.N;
             if constexpr (MODE == GATED) {
               const float hv = sum[0] / (1.f + expf(-sum[0])) * sum[1];
-              p.H[at + unit * 16 + g + 8 * (mate >> 1)] = __float2bfloat16_rn(hv);
+              p.H[at + unit * 16 + g + 8 * (v >> 1)] = __float2bfloat16_rn(hv);
             } else {
 #pragma unroll
               for (int br = 0; br < NB; ++br) {
-                const int64_t o = at + (unit * 2 + br) * 16 + g + 8 * (mate >> 1);
+                const int64_t o = at + (unit * 2 + br) * 16 + g + 8 * (v >> 1);
                 if constexpr (MODE == SINGLE) p.H[o] = __float2bfloat16_rn(sum[br] / (1.f + expf(-sum[br])));
                 else p.part[o] = sum[br];
               }
             }
           }
         }
-        team_sync(team);  // the last tile is read before the next unit's sums overwrite it
+        team_sync<TEAM>(team);  // the last tile is read before the next unit's sums overwrite it
       }
     };
     if (NTL == 1 || n <= 8) run_units(std::integral_constant<int, 1>());
@@ -650,6 +655,23 @@ int pass_cap(int64_t len, int group) {
   return rows;
 }
 
+// The time of `units` units of `pieces` 128-row pieces on the GPU, in pieces,
+// with teams of `team` warps: a CTA's rounds, each a warp's pieces and about
+// one more for its start and end.
+int64_t team_cost(int64_t units, int pieces, int team) {
+  const int64_t per_cta = (units + sm_count() - 1) / sm_count(), teams = kQWarps / team;
+  return (per_cta + teams - 1) / teams * ((pieces + team - 1) / team + 1);
+}
+// One warp a unit where that is reckoned a fifth faster and has two rounds at
+// least: units of a few pieces, which four warps cannot share evenly.  (d 640,
+// h 11520, 47 experts, 42 tokens: 134 against 167 us; d 128, h 14336: 52 against
+// 79.  Everywhere: 134 against 118 us at d 4096, h 14336, 16 tokens.)
+int team_of(int64_t units, int pieces) {
+  return units >= 2 * kQWarps * sm_count() && 5 * team_cost(units, pieces, 1) < 4 * team_cost(units, pieces, kQTeam)
+             ? 1
+             : kQTeam;
+}
+
 // Slices of the down projection's reduction axis (whole 128-row pieces): the
 // teams' rounds times a warp's pieces of a unit, plus about a piece's time a
 // round for its start and end; slices whose token rows fit shared memory for
@@ -662,9 +684,7 @@ int down_slices(const moeblaze_shape& s, int group, int tokens) {
   for (int n = 1; n <= blocks && n <= 64; ++n) {
     if (blocks % n) continue;
     if (n < blocks && pass_cap(s.h / n, group) < std::min(tokens, 16)) continue;
-    const int64_t units = used * (s.d / 32) * n, per_cta = (units + sm_count() - 1) / sm_count();
-    const int64_t rounds = (per_cta + kQTeams - 1) / kQTeams, pieces = (blocks / n + kQTeam - 1) / kQTeam;
-    const int64_t cost = rounds * (pieces + 1);
+    const int64_t cost = team_cost(used * (s.d / 32) * n, blocks / n, kQTeam);
     if (cost < least) {
       least = cost;
       best = n;
@@ -703,6 +723,7 @@ moeblaze_status launch_product_g(QParams p, int tokens, cudaStream_t st) {
   p.inv_grid = 1.f / (float)sm_count();
   p.inv_full = 1.f / (float)pass_weight(p.cap);
   p.inv_nt = 1.f / (float)(p.N / (MODE == GATED ? 16 : 32));
+  const int team = team_of(std::min<int64_t>(p.E, p.pairs) * p.slices * (p.N / (MODE == GATED ? 16 : 32)), (int)(len / 128));
   const size_t sm = fixed_bytes(GROUP) + token_bytes(len, GROUP, p.rows);
   auto run = [&](auto kern) -> moeblaze_status {
     MB_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm));
@@ -711,7 +732,9 @@ moeblaze_status launch_product_g(QParams p, int tokens, cudaStream_t st) {
     count_launch();
     return MOEBLAZE_OK;
   };
-  return p.rows <= 8 ? run(int4_product_kernel<MODE, 1, GROUP>) : run(int4_product_kernel<MODE, 2, GROUP>);
+  if (team == 1)
+    return p.rows <= 8 ? run(int4_product_kernel<MODE, 1, GROUP, 1>) : run(int4_product_kernel<MODE, 2, GROUP, 1>);
+  return p.rows <= 8 ? run(int4_product_kernel<MODE, 1, GROUP, kQTeam>) : run(int4_product_kernel<MODE, 2, GROUP, kQTeam>);
 }
 
 template <int MODE>

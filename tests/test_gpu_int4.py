@@ -79,6 +79,18 @@ def test_int4_forward(L, d, h, E, K, act, group):
     assert torch.equal(a, ex.forward(x.cuda(), ids.cuda(), gates.cuda()))
 
 
+@pytest.mark.parametrize("L,d,h,E,K,act,group", [
+    (8, 128, 2560, 32, 4, "swiglu", 128),
+    (24, 128, 2560, 32, 4, "swiglu", 64),
+    (20, 256, 2688, 40, 2, "swiglu", 32),
+    (9, 128, 5120, 32, 4, "silu", 32),
+    (40, 5120, 128, 32, 1, "silu", 128),
+])
+def test_int4_units_of_a_warp(L, d, h, E, K, act, group):
+    """Many units of few rows: a warp takes one by itself."""
+    test_int4_forward(L, d, h, E, K, act, group)
+
+
 def test_int4_fewer_tokens_than_the_buffers_and_skew():
     d, h, E, K, group = 256, 384, 8, 2, 64
     x, ids, gates, mats = _problem(64, d, h, E, K, "swiglu", group, 5)
