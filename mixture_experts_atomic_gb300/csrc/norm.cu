@@ -560,6 +560,8 @@ __global__ void __launch_bounds__(WARP ? 32 * kNormWarps : BUDGET, WARP ? 4 : 1)
     for (int i = 0; i < P; ++i)
       v[i] = make_float2(f[2 * i / VEC][2 * i % VEC], f[(2 * i + 1) / VEC][(2 * i + 1) % VEC]);
   };
+  // (the threads' words lie side by side: a part of the ring of its own for each
+  // thread, whose places would be constants, measured 280 against 184 us)
   // pieces past the row's end stay zero
 #pragma unroll
   for (int q = 0; q < D * A * NV; ++q) ring[q * NT + tid] = make_uint4(0u, 0u, 0u, 0u);
