@@ -144,7 +144,7 @@ size_t router_dense_ws_bytes(const moeblaze_shape& s);
 moeblaze_status launch_router_dense(const moeblaze_shape& s, const void* x, const float* Wr, const float* dl, float* dWr,
                                     float* dbias, void* dx, bool add, void* ws, cudaStream_t st);
 
-// router_grad_tc.cu: the same on the tensor cores (bf16 x, E <= 64)
+// router_grad_tc.cu: the same on the tensor cores (bf16 x, E <= 128)
 bool router_grad_tc(const moeblaze_shape& s);
 size_t router_grad_tc_ws_bytes(const moeblaze_shape& s);
 moeblaze_status launch_router_grad_tc(const moeblaze_shape& s, const void* x, const float* Wr, const float* dl, float* dWr,

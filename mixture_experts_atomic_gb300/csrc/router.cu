@@ -1222,7 +1222,7 @@ moeblaze_status bwd_t(const moeblaze_shape& s, const void* x, const float* Wr, c
 }
 
 // column blocks and token splits of the dense gradient: about three resident
-// CTAs per SM (few experts) or a few waves (more), no empty split
+// CTAs per SM (few experts) or two (more), no empty split
 int64_t dense_col_blocks(const moeblaze_shape& s) {
   const int ep = padded_experts(s.E);
   const int cols = ep <= 16 && s.dtype == MOEBLAZE_F32 ? kDgThreads * (64 / ep) : s.E > 128 ? 64 : 128;
