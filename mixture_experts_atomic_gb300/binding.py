@@ -611,46 +611,60 @@ def router_backward(shape: Shape, x, Wr, topk_ids, gates, dgates, dWr, dbias, dx
     _check(st, "moeblaze_router_backward")
 
 
-def router_backward_logits(shape: Shape, x, Wr, dlogits, dWr, dbias, dx, ws=None, stream=None, accumulate=False):
+def router_backward_logits(shape: Shape, x, Wr, dlogits, dWr, dbias, dx, ws=None, stream=None, accumulate=False,
+                           own=None):
     """Router gradients from a dense gradient of its logits: fills dWr (d,E) fp32, dbias (E) fp32 and dx (L,d)
     (dbias and dx may be None); with accumulate dx is added to what is there.  `ws` is a device byte tensor of
-    moeblaze_router_backward_logits_workspace_bytes(shape) bytes (allocated here when None)."""
-    dt = _TORCH_DTYPE[shape.dtype]
-    _args((x, "x", (shape.L, shape.d), dt, False), (Wr, "Wr", (shape.d, shape.E), torch.float32, False),
-          (dlogits, "dlogits", (shape.L, shape.E), torch.float32, False),
-          (dWr, "dWr", (shape.d, shape.E), torch.float32, False), (dbias, "dbias", (shape.E,), torch.float32, True),
-          (dx, "dx", (shape.L, shape.d), dt, True))
-    n = moeblaze_router_backward_logits_workspace_bytes(shape)
-    if ws is None:
-        ws = _bytes(n, Wr.device)
-    _bytes_arg(ws, "ws", n)
+    moeblaze_router_backward_logits_workspace_bytes(shape) bytes (allocated here when None).
+    own: the workspace's bytes, when dWr, dbias and ws are buffers made for this shape on dWr's device."""
+    dt, L, d, E = _TORCH_DTYPE[shape.dtype], shape.L, shape.d, shape.E
+    specs = ((x, "x", (L, d), dt, False), (Wr, "Wr", (d, E), torch.float32, False),
+             (dlogits, "dlogits", (L, E), torch.float32, False), (dWr, "dWr", (d, E), torch.float32, False),
+             (dx, "dx", (L, d), dt, True))
+    if own is None:
+        specs += ((dbias, "dbias", (E,), torch.float32, True),)
+    _args(*specs)
+    n = own
+    if own is None:
+        n = moeblaze_router_backward_logits_workspace_bytes(shape)
+        if ws is None:
+            ws = _bytes(n, Wr.device)
+        _bytes_arg(ws, "ws", n)
     st = moeblaze_router_backward_logits(shape, _ptr(x), _ptr(Wr), _ptr(dlogits), _ptr(dWr), _ptr(dbias), _ptr(dx),
                                          accumulate, _ptr(ws), n, _stream(stream))
     _check(st, "moeblaze_router_backward_logits")
 
 
-def balance_forward(shape: Shape, logits, topk_ids, valid, losses, counts, lse, ws, stream=None):
+def balance_forward(shape: Shape, logits, topk_ids, valid, losses, counts, lse, ws, stream=None, own=None):
     """Load-balance and z loss of a router's logits: fills losses (2) fp32, counts (E+1) int32 (the last one the
-    active tokens) and lse (L) fp32.  valid: (L) uint8 or None."""
+    active tokens) and lse (L) fp32.  valid: (L) uint8 or None.
+    own: the workspace's bytes, when outputs and workspace are buffers made for this shape on losses' device."""
     L, E = shape.L, shape.E
-    _args((logits, "logits", (L, E), torch.float32, False), (topk_ids, "topk_ids", (L, shape.K), torch.int32, False),
-          (valid, "valid", (L,), torch.uint8, True), (losses, "losses", (2,), torch.float32, False),
-          (counts, "counts", (E + 1,), torch.int32, False), (lse, "lse", (L,), torch.float32, False))
-    n = moeblaze_balance_workspace_bytes(shape)
-    _bytes_arg(ws, "ws", n)
+    specs = ((logits, "logits", (L, E), torch.float32, False), (topk_ids, "topk_ids", (L, shape.K), torch.int32, False),
+             (valid, "valid", (L,), torch.uint8, True), (losses, "losses", (2,), torch.float32, False))
+    if own is None:
+        specs += ((counts, "counts", (E + 1,), torch.int32, False), (lse, "lse", (L,), torch.float32, False))
+    _args(*specs)
+    n = own
+    if own is None:
+        n = moeblaze_balance_workspace_bytes(shape)
+        _bytes_arg(ws, "ws", n)
     st = moeblaze_balance_forward(shape, _ptr(logits), _ptr(topk_ids), _ptr(valid), _ptr(losses), _ptr(counts),
                                   _ptr(lse), _ptr(ws), n, _stream(stream))
     _check(st, "moeblaze_balance_forward")
 
 
-def balance_backward(shape: Shape, logits, lse, counts, dlosses, topk_ids, gates, dgates, dlogits, stream=None):
+def balance_backward(shape: Shape, logits, lse, counts, dlosses, topk_ids, gates, dgates, dlogits, stream=None,
+                     own=False):
     """Gradient of the logits (L,E) fp32 from the gradients of the two losses and, when topk_ids, gates and dgates
-    are given (all or none), of the gates."""
+    are given (all or none), of the gates.  own: lse and counts are buffers made for this shape on dlogits' device."""
     L, E, K = shape.L, shape.E, shape.K
-    _args((logits, "logits", (L, E), torch.float32, False), (lse, "lse", (L,), torch.float32, False),
-          (counts, "counts", (E + 1,), torch.int32, False), (dlosses, "dlosses", (2,), torch.float32, False),
-          (topk_ids, "topk_ids", (L, K), torch.int32, True), (gates, "gates", (L, K), torch.float32, True),
-          (dgates, "dgates", (L, K), torch.float32, True), (dlogits, "dlogits", (L, E), torch.float32, False))
+    specs = ((logits, "logits", (L, E), torch.float32, False), (dlosses, "dlosses", (2,), torch.float32, False),
+             (topk_ids, "topk_ids", (L, K), torch.int32, True), (gates, "gates", (L, K), torch.float32, True),
+             (dgates, "dgates", (L, K), torch.float32, True), (dlogits, "dlogits", (L, E), torch.float32, False))
+    if not own:
+        specs += ((lse, "lse", (L,), torch.float32, False), (counts, "counts", (E + 1,), torch.int32, False))
+    _args(*specs)
     if L > 0 and len({topk_ids is None, gates is None, dgates is None}) != 1:
         raise ValueError("topk_ids, gates and dgates: give all three or none")
     st = moeblaze_balance_backward(shape, _ptr(logits), _ptr(lse), _ptr(counts), _ptr(dlosses), _ptr(topk_ids),
@@ -658,27 +672,36 @@ def balance_backward(shape: Shape, logits, lse, counts, dlosses, topk_ids, gates
     _check(st, "moeblaze_balance_backward")
 
 
-def layernorm_forward(shape: Shape, x, residual, weight, bias, eps, sum, y, mean, rstd, stream=None):
-    """Layer norm of x (+ residual): fills y (L,d), mean and rstd (L) fp32 and, unless None, sum (L,d)."""
+def layernorm_forward(shape: Shape, x, residual, weight, bias, eps, sum, y, mean, rstd, stream=None, own=False):
+    """Layer norm of x (+ residual): fills y (L,d), mean and rstd (L) fp32 and, unless None, sum (L,d).
+    own: the outputs are buffers made for this shape on y's device, and only y is looked at again."""
     dt, L, d = _TORCH_DTYPE[shape.dtype], shape.L, shape.d
-    _args((x, "x", (L, d), dt, False), (residual, "residual", (L, d), dt, True),
-          (weight, "weight", (d,), torch.float32, False), (bias, "bias", (d,), torch.float32, True),
-          (sum, "sum", (L, d), dt, True), (y, "y", (L, d), dt, False), (mean, "mean", (L,), torch.float32, False),
-          (rstd, "rstd", (L,), torch.float32, False))
+    specs = ((x, "x", (L, d), dt, False), (residual, "residual", (L, d), dt, True),
+             (weight, "weight", (d,), torch.float32, False), (bias, "bias", (d,), torch.float32, True),
+             (y, "y", (L, d), dt, False))
+    if not own:
+        specs += ((sum, "sum", (L, d), dt, True), (mean, "mean", (L,), torch.float32, False),
+                  (rstd, "rstd", (L,), torch.float32, False))
+    _args(*specs)
     st = moeblaze_layernorm_forward(shape, _ptr(x), _ptr(residual), _ptr(weight), _ptr(bias), eps, _ptr(sum), _ptr(y),
                                     _ptr(mean), _ptr(rstd), _stream(stream))
     _check(st, "moeblaze_layernorm_forward")
 
 
-def layernorm_backward(shape: Shape, dy, sum, mean, rstd, weight, dsum, dx, dweight, dbias, ws, stream=None):
-    """Layer norm backward: fills dx (L,d), dweight (d) fp32 and, unless None, dbias (d) fp32."""
+def layernorm_backward(shape: Shape, dy, sum, mean, rstd, weight, dsum, dx, dweight, dbias, ws, stream=None, own=None):
+    """Layer norm backward: fills dx (L,d), dweight (d) fp32 and, unless None, dbias (d) fp32.
+    own: the workspace's bytes, when outputs and workspace are buffers made for this shape on dx's device."""
     dt, L, d = _TORCH_DTYPE[shape.dtype], shape.L, shape.d
-    _args((dy, "dy", (L, d), dt, False), (sum, "sum", (L, d), dt, False), (mean, "mean", (L,), torch.float32, False),
-          (rstd, "rstd", (L,), torch.float32, False), (weight, "weight", (d,), torch.float32, False),
-          (dsum, "dsum", (L, d), dt, True), (dx, "dx", (L, d), dt, False),
-          (dweight, "dweight", (d,), torch.float32, False), (dbias, "dbias", (d,), torch.float32, True))
-    n = moeblaze_layernorm_backward_workspace_bytes(shape)
-    _bytes_arg(ws, "ws", n)
+    specs = ((dy, "dy", (L, d), dt, False), (sum, "sum", (L, d), dt, False), (mean, "mean", (L,), torch.float32, False),
+             (rstd, "rstd", (L,), torch.float32, False), (weight, "weight", (d,), torch.float32, False),
+             (dsum, "dsum", (L, d), dt, True), (dx, "dx", (L, d), dt, False))
+    n = own
+    if own is None:
+        specs += ((dweight, "dweight", (d,), torch.float32, False), (dbias, "dbias", (d,), torch.float32, True))
+    _args(*specs)
+    if own is None:
+        n = moeblaze_layernorm_backward_workspace_bytes(shape)
+        _bytes_arg(ws, "ws", n)
     st = moeblaze_layernorm_backward(shape, _ptr(dy), _ptr(sum), _ptr(mean), _ptr(rstd), _ptr(weight), _ptr(dsum),
                                      _ptr(dx), _ptr(dweight), _ptr(dbias), _ptr(ws), n, _stream(stream))
     _check(st, "moeblaze_layernorm_backward")

@@ -23,27 +23,33 @@ class LayerNorm:
         self.rstd = torch.empty((L,), **f32)
         self.dw = torch.empty((d,), **f32)
         self.db = torch.empty((d,), **f32)
+        # (what a call writes is kept here too, so that its checks, made once, hold whatever becomes of the names)
+        self._fwd = (self.y, self.mean, self.rstd)
+        self._bwd = (self.dw, self.db)
         self._s: Optional[torch.Tensor] = None
         self._dx: Optional[torch.Tensor] = None
         self._ws: Optional[torch.Tensor] = None
+        self._ws_bytes = B.moeblaze_layernorm_backward_workspace_bytes(self.shape)
 
     def forward(self, x, weight, bias=None, residual=None):
         """(y, s, mean, rstd) of s = x (+ residual); without a residual s is x itself."""
         s = None
+        y, mean, rstd = self._fwd
         if residual is not None:
             if self._s is None:
-                self._s = torch.empty_like(self.y)
+                self._s = torch.empty_like(y)
             s = self._s
-        B.layernorm_forward(self.shape, x, residual, weight, bias, self.eps, s, self.y, self.mean, self.rstd)
-        return self.y, (x if s is None else s), self.mean, self.rstd
+        B.layernorm_forward(self.shape, x, residual, weight, bias, self.eps, s, y, mean, rstd, own=True)
+        return y, (x if s is None else s), mean, rstd
 
     def backward(self, dy, s, mean, rstd, weight, dsum=None):
         """(dx, dweight, dbias); dsum is a gradient that reaches s besides the norm and is added to dx."""
         if self._dx is None:
-            self._dx = torch.empty_like(self.y)
-            self._ws = B._bytes(B.moeblaze_layernorm_backward_workspace_bytes(self.shape), self.y.device)
-        B.layernorm_backward(self.shape, dy, s, mean, rstd, weight, dsum, self._dx, self.dw, self.db, self._ws)
-        return self._dx, self.dw, self.db
+            self._dx = torch.empty_like(self._fwd[0])
+            self._ws = B._bytes(self._ws_bytes, self._dx.device)
+        dw, db = self._bwd
+        B.layernorm_backward(self.shape, dy, s, mean, rstd, weight, dsum, self._dx, dw, db, self._ws, own=self._ws_bytes)
+        return self._dx, dw, db
 
 
 class BalanceLoss:
@@ -59,19 +65,25 @@ class BalanceLoss:
         self.active = self._counts[E:]
         self._lse = torch.empty((L,), **f32)
         self.dlogits = torch.empty((L, E), **f32)
-        self._ws = B._bytes(B.moeblaze_balance_workspace_bytes(self.shape), device)
+        self._ws_bytes = B.moeblaze_balance_workspace_bytes(self.shape)
+        self._ws = B._bytes(self._ws_bytes, device)
+        self._out = (self.losses, self.dlogits)  # what the calls write, whatever becomes of the names
 
     def forward(self, logits, topk_ids, valid=None):
         """(losses, counts): losses = [balance, z]; valid (L) uint8 leaves tokens out."""
-        B.balance_forward(self.shape, logits, topk_ids, valid, self.losses, self._counts, self._lse, self._ws)
-        return self.losses, self.counts
+        losses = self._out[0]
+        B.balance_forward(self.shape, logits, topk_ids, valid, losses, self._counts, self._lse, self._ws,
+                          own=self._ws_bytes)
+        return losses, self.counts
 
     def backward(self, logits, dlosses, valid=None, topk_ids=None, gates=None, dgates=None):
         """dlogits after a forward on the same logits: of the losses, with gradients dlosses (2), and of the
         gates when topk_ids, gates and dgates are given.  The tokens left out are those the forward left out
         (valid is taken for symmetry and not read)."""
-        B.balance_backward(self.shape, logits, self._lse, self._counts, dlosses, topk_ids, gates, dgates, self.dlogits)
-        return self.dlogits
+        dlogits = self._out[1]
+        B.balance_backward(self.shape, logits, self._lse, self._counts, dlosses, topk_ids, gates, dgates, dlogits,
+                           own=True)
+        return dlogits
 
 
 class RouterGrad:
@@ -82,7 +94,9 @@ class RouterGrad:
         self._dx: Optional[torch.Tensor] = None
         self.dWr = torch.empty((d, E), dtype=torch.float32, device=device)
         self.dbias = torch.empty((E,), dtype=torch.float32, device=device)
-        self._ws = B._bytes(B.moeblaze_router_backward_logits_workspace_bytes(self.shape), device)
+        self._grads = (self.dWr, self.dbias)  # what a call writes, whatever becomes of the names
+        self._ws_bytes = B.moeblaze_router_backward_logits_workspace_bytes(self.shape)
+        self._ws = B._bytes(self._ws_bytes, device)
 
     def backward(self, x, Wr, dlogits, add_to=None):
         """(dx, dWr, dbias); with add_to (L,d) dx is added to it in place, and it is returned."""
@@ -91,9 +105,10 @@ class RouterGrad:
             if self._dx is None:
                 self._dx = torch.empty_like(x)
             dx = self._dx
-        B.router_backward_logits(self.shape, x, Wr, dlogits, self.dWr, self.dbias, dx, self._ws,
-                                 accumulate=add_to is not None)
-        return dx, self.dWr, self.dbias
+        dWr, dbias = self._grads
+        B.router_backward_logits(self.shape, x, Wr, dlogits, dWr, dbias, dx, self._ws,
+                                 accumulate=add_to is not None, own=self._ws_bytes)
+        return dx, dWr, dbias
 
 
 class MoEBlock:
