@@ -641,7 +641,7 @@ __global__ void __launch_bounds__(WARP ? 32 * kNormWarps : BUDGET, WARP ? 4 : 1)
       // lanes 0-15 add up the first sum over the warps, lanes 16-31 the second
       const float* r = red[buf][(tid >> 4) & 1];
       float v;
-      if constexpr (THREADS != 0) {
+      if constexpr (THREADS != 0 && (THREADS & (THREADS - 1)) == 0) {
         constexpr int W = THREADS / 32, H = W < 16 ? W : 16;
         v = r[tid & (H - 1)];
         if constexpr (W == 32) v += r[16 + (tid & 15)];
@@ -958,8 +958,13 @@ moeblaze_status bwd_shaped(const moeblaze_shape& s, const BwdShape& b, const voi
       if constexpr (!SHIFT) {
         switch (b.threads) {
           case 128: return MB_CALL(1, false, 1024, 128);
+          case 192: return MB_CALL(1, false, 1024, 192);
           case 256: return MB_CALL(1, false, 1024, 256);
+          case 320: return MB_CALL(1, false, 1024, 320);
+          case 448: return MB_CALL(1, false, 1024, 448);
           case 512: return MB_CALL(1, false, 1024, 512);
+          case 768: return MB_CALL(1, false, 1024, 768);
+          case 896: return MB_CALL(1, false, 1024, 896);
           case 1024: return MB_CALL(1, false, 1024, 1024);
         }
       }
