@@ -205,8 +205,7 @@ struct QParams {
   int pairs, E, K;
   int R, N;                  // reduction length and output columns of the matrices
   int slices;                // the reduction axis in slices of R / slices (DOWN; else 1)
-  int cap;                   // token columns of one pass
-  int rows;                  // token rows that shared memory holds (<= cap)
+  int cap;                   // token columns of one pass, and token rows that shared memory holds
   float inv_grid, inv_full, inv_nt;  // 1 / gridDim, 1 / the weight of a full pass, 1 / units of a segment
   __nv_bfloat16* H;          // GATED, SINGLE: h (pairs x N)
   float* part;               // DOWN: (slices x pairs x N)
@@ -423,7 +422,7 @@ __global__ void __launch_bounds__(kQThreads, 1) int4_product_kernel(const QParam
 
   // ---- segments
   const int pitch = SL * 2 + 64;  // rows 16 banks apart: 2 rows x 64 bytes of a fragment load do not conflict
-  float* nsx = reinterpret_cast<float*>(xs + (size_t)p.rows * pitch);  // [groups][8 NTL]: -136 sum x
+  float* nsx = reinterpret_cast<float*>(xs + (size_t)p.cap * pitch);  // [groups][8 NTL]: -136 sum x
   uint32_t slot = 0;
   int u = team;
   for (Seg seg = start;; next_segment(seg)) {
@@ -718,13 +717,14 @@ cudaError_t launch_q(void (*kern)(Params...), unsigned grid, unsigned block, siz
 template <int MODE, int GROUP>
 moeblaze_status launch_product_g(QParams p, int tokens, cudaStream_t st) {
   const int64_t len = p.R / p.slices;
-  p.cap = pass_cap(len, GROUP);
-  p.rows = std::min(p.cap, tokens);
+  // (no more columns than tokens, although a token that names an expert twice
+  // gives it more pairs than there are tokens: the rest is another pass)
+  p.cap = std::min(pass_cap(len, GROUP), tokens);
   p.inv_grid = 1.f / (float)sm_count();
   p.inv_full = 1.f / (float)pass_weight(p.cap);
   p.inv_nt = 1.f / (float)(p.N / (MODE == GATED ? 16 : 32));
   const int team = team_of(std::min<int64_t>(p.E, p.pairs) * p.slices * (p.N / (MODE == GATED ? 16 : 32)), (int)(len / 128));
-  const size_t sm = fixed_bytes(GROUP) + token_bytes(len, GROUP, p.rows);
+  const size_t sm = fixed_bytes(GROUP) + token_bytes(len, GROUP, p.cap);
   auto run = [&](auto kern) -> moeblaze_status {
     MB_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm));
     // the down projection's h comes from the launch before it, its routing and weights from before that
@@ -733,8 +733,8 @@ moeblaze_status launch_product_g(QParams p, int tokens, cudaStream_t st) {
     return MOEBLAZE_OK;
   };
   if (team == 1)
-    return p.rows <= 8 ? run(int4_product_kernel<MODE, 1, GROUP, 1>) : run(int4_product_kernel<MODE, 2, GROUP, 1>);
-  return p.rows <= 8 ? run(int4_product_kernel<MODE, 1, GROUP, kQTeam>) : run(int4_product_kernel<MODE, 2, GROUP, kQTeam>);
+    return p.cap <= 8 ? run(int4_product_kernel<MODE, 1, GROUP, 1>) : run(int4_product_kernel<MODE, 2, GROUP, 1>);
+  return p.cap <= 8 ? run(int4_product_kernel<MODE, 1, GROUP, kQTeam>) : run(int4_product_kernel<MODE, 2, GROUP, kQTeam>);
 }
 
 template <int MODE>

@@ -197,3 +197,25 @@ def test_int4_streams_and_graph():
         graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(y, want)
+
+
+@pytest.mark.parametrize("L,d,h,E,K,act,group", [
+    (1, 4096, 256, 4, 2, "swiglu", 128),
+    (1, 256, 384, 8, 8, "silu", 64),
+    (2, 640, 128, 3, 3, "swiglu", 32),
+    (3, 256, 256, 2, 2, "swiglu", 128),
+    (9, 128, 256, 8, 8, "swiglu", 64),
+    (64, 128, 128, 8, 8, "silu", 128),
+])
+def test_int4_tokens_that_name_an_expert_more_than_once(L, d, h, E, K, act, group):
+    """An expert may have more pairs than there are tokens: each slot counts."""
+    x, ids, gates, mats = _problem(L, d, h, E, K, act, group, 3 * L + K)
+    ex = Int4Experts(L, d, h, E, K, act, group)
+    _load(ex, mats)
+    for same in (E - 1, 0):
+        ids[:] = same
+        if L > 2:
+            ids[1, 0] = (same + 1) % E
+        y = ex.forward(x.cuda(), ids.cuda(), gates.cuda())
+        torch.cuda.synchronize()
+        _check(y, x, ids, gates, mats, group)
