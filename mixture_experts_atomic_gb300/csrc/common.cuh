@@ -169,7 +169,7 @@ moeblaze_status launch_balance_backward(const moeblaze_shape& s, const float* lo
                                         const float* gates, const float* dgates, float* dlogits, cudaStream_t st);
 
 // int4.cu
-bool int4_shape_ok(const moeblaze_shape& s, int group);  // a token row fits the products' shared memory
+bool int4_shape_ok(const moeblaze_shape& s, int group);  // a token's x, and a slice of its h, fit the products' shared memory
 size_t int4_ws_bytes(const moeblaze_shape& s, int group);
 moeblaze_status launch_int4_forward(const moeblaze_shape& s, const __nv_bfloat16* x, const int32_t* ids,
                                     const float* gates, const moeblaze_int4_experts& w, __nv_bfloat16* y, void* ws,

@@ -55,6 +55,7 @@ constexpr int kQTeam = 4;
 constexpr int kQCols = 16;
 constexpr int kQMaxTokens = 64;                    // tokens of one launch
 constexpr int kQMaxPairs = kQMaxTokens * kMaxK;    // (token, slot) pairs of one launch
+constexpr int kQSlices = 64;                       // slices of the down projection's reduction axis, at most
 // What a launch computes.  A unit is two tiles, so that a token fragment
 // serves two weight tiles: the same tile of W1 and W2 (GATED), or two
 // neighbouring tiles of one matrix (SINGLE: SiLU experts' W1; DOWN: W3).
@@ -204,7 +205,8 @@ struct QParams {
   const int32_t* ids;
   int pairs, E, K;
   int R, N;                  // reduction length and output columns of the matrices
-  int slices;                // the reduction axis in slices of R / slices (DOWN; else 1)
+  int slices;                // slices of the reduction axis (DOWN; else 1), at most kQSlices
+  int per, more;             // 128-row pieces of a slice: per + 1 in the first `more` slices, per in the others
   int cap;                   // token columns of one pass, and token rows that shared memory holds
   float inv_grid, inv_full, inv_nt;  // 1 / gridDim, 1 / the weight of a full pass, 1 / units of a segment
   __nv_bfloat16* H;          // GATED, SINGLE: h (pairs x N)
@@ -302,14 +304,17 @@ __global__ void __launch_bounds__(kQThreads, 1) int4_product_kernel(const QParam
   }
 
   const int nt = p.N / (MODE == GATED ? 16 : 32);  // units of a segment
-  const int SL = p.R / p.slices, kp = SL / 128, allp = p.R / 128;
+  const int allp = p.R / 128;
   const int per_pass = p.slices * nt;
+  // slice sl's first piece, and how many it has
+  auto first_piece = [&](int sl) { return MODE == DOWN ? sl * p.per + min(sl, p.more) : 0; };
+  auto pieces_of = [&](int sl) { return MODE == DOWN ? p.per + (sl < p.more ? 1 : 0) : allp; };
   // A segment: pass `pi` of expert e, slice sl; its tiles are the CTA's units
   // [base, end), counted from the CTA's first unit (base < 0 where another CTA
   // has its first tiles).  Integer divisions are kept out of this start: they
   // and a search per unit were 1 us of it.
   struct Seg {
-    int id, base, end;  // id: e, 9 bits; pi, 10 bits (512 pairs at most); sl, 7 bits (64 slices at most)
+    int id, base, end;  // id: e, 9 bits; pi, 10 bits (512 pairs at most); sl, 7 bits (kQSlices)
     __device__ int e() const { return id & 511; }
     __device__ int pi() const { return (id >> 9) & 1023; }
     __device__ int sl() const { return id >> 19; }
@@ -375,24 +380,32 @@ __global__ void __launch_bounds__(kQThreads, 1) int4_product_kernel(const QParam
   const uint32_t ring_s = saddr(qsm) + warp * PIECES * ENTRY + 1024 + g * 4 * SW;
   constexpr int TEAMS = kQWarps / TEAM;
   const int team = warp / TEAM, mate = warp % TEAM;
-  const int k0 = kp * mate / TEAM, k1 = kp * (mate + 1) / TEAM;  // this warp's pieces of a unit
+  // this warp's pieces of a unit of kp pieces: [share(kp, mate), share(kp, mate + 1))
+  auto share = [&](int kp, int m) { return (int)((unsigned)(kp * m) / TEAM); };
   int fu = team, left = 0;
   Seg fseg = start;
   uint32_t fslot = 0;  // byte offset of the ring entry to fill
   const uint8_t* fw[NB];
   const uint8_t* fs[NB];
   auto fetch_unit = [&]() {
-    if (fu >= units || k0 == k1) return;
-    while (fu >= fseg.end) next_segment(fseg);
+    int k0;
+    // (a warp may have no piece of a short slice's units)
+    for (;; fu += TEAMS) {
+      if (fu >= units) return;
+      while (fu >= fseg.end) next_segment(fseg);
+      const int kp = pieces_of(fseg.sl());
+      k0 = share(kp, mate);
+      left = share(kp, mate + 1) - k0;
+      if (left > 0) break;
+    }
     const int tile = fu - fseg.base;
 #pragma unroll
     for (int br = 0; br < NB; ++br) {
       const int64_t row = MODE == GATED ? (int64_t)fseg.e() * nt + tile : ((int64_t)fseg.e() * nt + tile) * 2 + br;
-      const int64_t at = row * allp + fseg.sl() * kp + k0;
+      const int64_t at = row * allp + first_piece(fseg.sl()) + k0;
       fw[br] = p.w[MODE == GATED ? br : 0] + at * 1024 + lane * 16;
       fs[br] = p.s[MODE == GATED ? br : 0] + at * (32 * SW) + g * (4 * SW);
     }
-    left = k1 - k0;
   };
   auto fetch = [&]() {
     if (left > 0) {
@@ -421,24 +434,26 @@ __global__ void __launch_bounds__(kQThreads, 1) int4_product_kernel(const QParam
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
   // ---- segments
-  const int pitch = SL * 2 + 64;  // rows 16 banks apart: 2 rows x 64 bytes of a fragment load do not conflict
+  // rows of the longest slice, 16 banks apart: 2 rows x 64 bytes of a fragment load do not conflict
+  const int pitch = pieces_of(0) * 256 + 64;
   float* nsx = reinterpret_cast<float*>(xs + (size_t)p.cap * pitch);  // [groups][8 NTL]: -136 sum x
   uint32_t slot = 0;
   int u = team;
   for (Seg seg = start;; next_segment(seg)) {
     const int e = seg.e(), sl = seg.sl(), first = off[e] + seg.pi() * p.cap;
-    const int n = min(p.cap, cnt[e] - seg.pi() * p.cap);
+    const int n = min(p.cap, cnt[e] - seg.pi() * p.cap), kp = pieces_of(sl);
+    const int k0 = share(kp, mate), k1 = share(kp, mate + 1);
     __syncthreads();  // every warp is done with the previous segment's rows
     // a warp per 1024 elements of a row: 8 elements a lane, four times, all
     // in flight together; their sums meet over the GROUP / 8 lanes of a group
     {
-      const int m = SL / 8, parts = (m + 127) / 128;  // m is a multiple of 16
+      const int m = kp * 16, parts = (m + 127) / 128;  // m is a multiple of 16
 #pragma unroll 1
       for (int i = warp; i < n * parts; i += kQWarps) {
         const int r = i / parts, c0 = (i - r * parts) * 128;
         const int pair = list[first + r];
         const int64_t row = MODE == DOWN ? pair : pair / p.K;
-        const uint4* src = reinterpret_cast<const uint4*>(p.src + row * p.src_ld + (int64_t)sl * SL);
+        const uint4* src = reinterpret_cast<const uint4*>(p.src + row * p.src_ld + (int64_t)first_piece(sl) * 128);
         uint4* dst = reinterpret_cast<uint4*>(xs + (size_t)r * pitch);
         uint4 v[4];
 #pragma unroll
@@ -674,21 +689,32 @@ int team_of(int64_t units, int pieces) {
 // Slices of the down projection's reduction axis (whole 128-row pieces): the
 // teams' rounds times a warp's pieces of a unit, plus about a piece's time a
 // round for its start and end; slices whose token rows fit shared memory for
-// the usual load (16 tokens of an expert) only, where there are such.
+// the usual load (16 tokens of an expert) only, unless the most there may be do
+// not.  Slices of one length, but where these come to more than kQEven (h / 128
+// has no divisor that fits) the first slices have a piece more than the others:
+// d 4096, 8 experts, K 2, 16 tokens, h 11008 in 4 slices against 43 of two pieces
+// 105 and 133 us, h 13696 in 7 against 107 of one 127 and 214 us.
+constexpr int kQEven = 16;
+int most_slices(const moeblaze_shape& s) { return std::min(s.h / 128, kQSlices); }
+int64_t slice_len(const moeblaze_shape& s, int n) { return 128 * (int64_t)((s.h / 128 + n - 1) / n); }
 int down_slices(const moeblaze_shape& s, int group, int tokens) {
-  const int blocks = s.h / 128;
+  const int most = most_slices(s);
   const int64_t used = std::min<int64_t>(s.E, (int64_t)tokens * s.K);
-  int best = blocks;
+  int best = most;
   int64_t least = INT64_MAX;
-  for (int n = 1; n <= blocks && n <= 64; ++n) {
-    if (blocks % n) continue;
-    if (n < blocks && pass_cap(s.h / n, group) < std::min(tokens, 16)) continue;
-    const int64_t cost = team_cost(used * (s.d / 32) * n, blocks / n, kQTeam);
+  auto look = [&](int n) {
+    const int64_t len = slice_len(s, n);
+    if (n < most && pass_cap(len, group) < std::min(tokens, 16)) return;
+    const int64_t cost = team_cost(used * (s.d / 32) * n, (int)(len / 128), kQTeam);
     if (cost < least) {
       least = cost;
       best = n;
     }
-  }
+  };
+  for (int n = 1; n <= most; ++n)
+    if (s.h / 128 % n == 0) look(n);
+  if (best > kQEven)
+    for (int n = 1; n <= most; ++n) look(n);
   return best;
 }
 
@@ -716,7 +742,10 @@ cudaError_t launch_q(void (*kern)(Params...), unsigned grid, unsigned block, siz
 
 template <int MODE, int GROUP>
 moeblaze_status launch_product_g(QParams p, int tokens, cudaStream_t st) {
-  const int64_t len = p.R / p.slices;
+  const int pieces = p.R / 128;
+  p.per = pieces / p.slices;
+  p.more = pieces % p.slices;
+  const int64_t len = 128 * (int64_t)(p.per + (p.more > 0));  // of the longest slice
   // (no more columns than tokens, although a token that names an expert twice
   // gives it more pairs than there are tokens: the rest is another pass)
   p.cap = std::min(pass_cap(len, GROUP), tokens);
@@ -749,7 +778,7 @@ moeblaze_status launch_product(const QParams& p, int group, int tokens, cudaStre
 }  // namespace
 
 bool int4_shape_ok(const moeblaze_shape& s, int group) {
-  return pass_cap(s.d, group) >= 1;
+  return pass_cap(s.d, group) >= 1 && pass_cap(slice_len(s, most_slices(s)), group) >= 1;
 }
 
 size_t int4_ws_bytes(const moeblaze_shape& s, int group) {

@@ -178,3 +178,24 @@ def test_binding_refuses_malformed_tensors():
         B.int4_pack(t(1, 96, 128, dt=torch.int8), t(1, 3, 128, dt=BF), 32)
     with pytest.raises(ValueError, match="scales: shape"):
         B.int4_pack(t(1, 128, 128, dt=torch.int8), t(1, 2, 128, dt=BF), 32)
+
+
+def _int4_slices(L, d, h, E, K, group):
+    """Slices of the down projection as the workspace has them: (slices x L K x d) fp32 behind h (L K x h) bf16,
+    both rounded up to 256 bytes (d a multiple of 128 makes the first exact)."""
+    n = B.moeblaze_int4_workspace_bytes(B.make_shape(L, d, h, E, K, B.BF16, "swiglu"), group)
+    hidden = (L * K * h * 2 + 255) // 256 * 256
+    assert n > hidden and (n - hidden) % (L * K * d * 4) == 0
+    return (n - hidden) // (L * K * d * 4)
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_int4_slices_are_bounded(group):
+    """A unit's number holds 64 slices; h / 128 need not have a divisor that fits."""
+    for blocks in (1, 2, 64, 65, 67, 86, 101, 107, 109, 127, 128, 1009, 4093, 4095, 4096, 4099):
+        for L in (1, 4, 16, 64):
+            assert 1 <= _int4_slices(L, 128, 128 * blocks, 8, 2, group) <= min(blocks, 64), (blocks, L)
+    # a slice of the widest h whose token row does not fit an SM is refused
+    assert B.moeblaze_int4_workspace_bytes(B.make_shape(1, 128, 1 << 22, 8, 2, B.BF16, "swiglu"), group) == 0
+    # and what one slice a piece cost, it no longer does: the partial sums of the widest layer stay below its weights
+    assert _int4_slices(64, 4096, 128 * 109, 8, 8, group) <= 16

@@ -219,3 +219,18 @@ def test_int4_tokens_that_name_an_expert_more_than_once(L, d, h, E, K, act, grou
         y = ex.forward(x.cuda(), ids.cuda(), gates.cuda())
         torch.cuda.synchronize()
         _check(y, x, ids, gates, mats, group)
+
+
+@pytest.mark.parametrize("L,d,h,E,K,act,group", [
+    (16, 128, 128 * 67, 2, 2, "swiglu", 64),
+    (20, 256, 128 * 107, 2, 1, "silu", 32),
+    (64, 128, 128 * 86, 3, 2, "swiglu", 128),
+    (5, 128, 128 * 131, 2, 2, "silu", 128),
+    (1, 256, 128 * 433, 2, 1, "swiglu", 128),
+    (16, 384, 128 * 73, 4, 1, "swiglu", 32),
+    (23, 1152, 128 * 59, 2, 2, "swiglu", 64),
+    (33, 128, 128 * 1031, 1, 1, "silu", 64),
+])
+def test_int4_reductions_in_unequal_slices(L, d, h, E, K, act, group):
+    """h / 128 without a divisor that fits: slices of n and n + 1 pieces."""
+    test_int4_forward(L, d, h, E, K, act, group)
