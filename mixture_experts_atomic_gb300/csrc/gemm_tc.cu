@@ -29,17 +29,9 @@
 // overlapped with the next tile's main loop (there is no second
 // accumulator), which the dH stage, with its heavy epilogue, does not repay.
 //
-// Paired stages (dH, when the reduction is at least 64 k-blocks long): the
-// kernel runs as clusters of two CTAs that take two 128-row tiles of one
-// expert at the same n-tile.  Both need the same weight tiles: each CTA
-// loads half of the boxes and multicasts them to both, halving the weight
-// bytes each SM pulls from L2.  A stage is free again once both CTAs' MMAs
-// have consumed it (their commits arrive in both CTAs), and the leader
-// (rank 0) claims the pair tiles and posts them into both CTAs' tile queues.
-//
 // Row space: an expert's routed rows form a segment of a padded row space,
 // [pad_off[e], pad_off[e+1]), 256-row aligned, so every 128-row M tile (and
-// every aligned pair of them: a wide tile, or a cluster pair's tiles)
+// every aligned pair of them: a wide tile)
 // belongs to one expert.  Row q of expert e with i = q - pad_off[e] < n_e is
 // routed row off[e]+i of token expert_token_indices[off[e]+i]; padding rows
 // gather a valid token and are zero where they feed a reduction.
@@ -87,9 +79,8 @@ constexpr int TMEM_COLS = 512;                // two 128 x 256 fp32 accumulators
 // bf16 (64-byte swizzle), a ring of them per epilogue warp
 constexpr int EPI_BUF_BYTES = 32 * 64;
 constexpr int EPI_STAGE_BYTES = 16 * EPI_BUF_BYTES;  // 32 KB
-// Launch variants of a stage: one CTA a tile, clusters of two CTAs sharing
-// the weight tiles (row stages), or wide tiles.
-enum Variant : int { SINGLE = 0, PAIRED = 1, WIDE = 2 };
+// Launch variants of a stage: 128-row or wide tiles.
+enum Variant : int { SINGLE = 0, WIDE = 1 };
 constexpr int BAR_BYTES = 512;                // mbarriers, TMEM address, abort flag, tile queue
 // Tiles are claimed dynamically: each CTA takes its first two tiles by its
 // index and every further one from a global counter, two tiles ahead of
@@ -112,21 +103,8 @@ __host__ __device__ constexpr bool is_fused(int m) {
 }
 __host__ __device__ constexpr bool fused_sw(int m) { return m == DOWN_SWIGLU || m == DW3_SWIGLU; }
 __host__ __device__ constexpr bool is_wgrad(int m) { return m == DW12 || m == DW1 || is_dw3(m); }
-// stages that can run as clusters of two CTAs sharing (multicasting) the
-// weight tiles; the host pairs them when the reduction is long
-__host__ __device__ constexpr bool pairable(int m) { return m == DH_SWIGLU || m == DH_SILU; }
-// Pairing pays off on long reductions with many tiles (measured: the
-// Mixtral-like layer's dH 6% faster); on a small layer the pairs' lockstep
-// costs more than the shared loads save.  The up projection, the stored-H
-// down projection and dX take wide tiles instead (faster there than pairs:
-// down 46.9 -> 33.8 ms, dX 84.1 -> 66.8 ms on the Mixtral-like layer).
-constexpr int kPairMinKblocks = 64;
-constexpr int kPairMinTilesPerSm = 16;
-inline bool pair_stage(int kblocks, int64_t tiles) {
-  return kblocks >= kPairMinKblocks && tiles >= (int64_t)kPairMinTilesPerSm * sm_count();
-}
 // Wide tiles for the row stages from 32 k-blocks a tile and 4 (128-row)
-// tiles per SM (measured against pair_stage's 64 and 16: the SiLU layer's
+// tiles per SM (measured against 64 and 16: the SiLU layer's
 // down 0.251 -> 0.223 ms and dX 0.243 -> 0.225 ms, the 64-expert layer's up
 // 3.93 -> 3.72 ms and dX 3.60 -> 3.40 ms).
 constexpr int kWideMinKblocks = 32;
@@ -368,14 +346,12 @@ struct Tile {
   int n_e;      // tokens routed to e
 };
 
-// Tile `tile` of the launch.  In the paired stages a tile id names a pair of
-// 128-row tiles of one expert (a 256-row slice of its padded segment) at one
-// n-tile, and `rank` picks this CTA's half.
-template <int MODE, bool PAIR, bool WIDE_T = false>
-__device__ __forceinline__ Tile decode(const Params& p, int64_t tile, int num_mt, int rank) {
+// Tile `tile` of the launch.
+template <int MODE, bool WIDE_T = false>
+__device__ __forceinline__ Tile decode(const Params& p, int64_t tile, int num_mt) {
   Tile t;
   constexpr int TN = tile_n(MODE);
-  constexpr int PM = PAIR || WIDE_T ? 2 : 1;
+  constexpr int PM = WIDE_T ? 2 : 1;
   int nt;
   if constexpr (is_wgrad(MODE)) {
     const int64_t per_e = (int64_t)p.m_tiles_w * p.n_tiles;
@@ -397,7 +373,7 @@ __device__ __forceinline__ Tile decode(const Params& p, int64_t tile, int num_mt
     t.pad0 = p.meta.pad_off[t.e];
     t.kblocks = (p.meta.pad_off[t.e + 1] - t.pad0) / BK;
   } else {
-    // groups of 16 m-tiles (8 pairs) walk the n-tiles together, so the weight
+    // groups of 16 m-tiles (8 wide ones) walk the n-tiles together, so the weight
     // tiles they share stay in L2
     constexpr int GM = 16 / PM;
     const int nmu = num_mt / PM;
@@ -405,7 +381,7 @@ __device__ __forceinline__ Tile decode(const Params& p, int64_t tile, int num_mt
     const int g = (int)(tile / per_g);
     const int r = (int)(tile % per_g);
     const int gm = min(GM, nmu - g * GM);
-    const int mt = (g * GM + r % gm) * PM + (PM == 2 ? rank : 0);
+    const int mt = (g * GM + r % gm) * PM;
     nt = r / gm;
     t.e = p.meta.tile_expert[mt];
     t.row0 = mt * BM;
@@ -450,7 +426,6 @@ __host__ __device__ constexpr bool cp_b(int m) { return is_dw3(m); }
 
 template <int MODE, int VAR>
 __global__ void __launch_bounds__(num_threads(MODE, VAR), 1) moe_gemm_kernel(const __grid_constant__ Params p) {
-  constexpr bool PAIR = VAR == PAIRED;
   // WIDE: 256-row weight-gradient tiles (two M=128 MMAs a k-step, one accumulator)
   constexpr bool WIDE_T = VAR == WIDE;
   static_assert(!WIDE_T || widenable(MODE), "stage has no wide tiles");
@@ -464,12 +439,7 @@ __global__ void __launch_bounds__(num_threads(MODE, VAR), 1) moe_gemm_kernel(con
   constexpr int MMA_WARP = mma_warp(MODE);
   constexpr int NST = stages_of(MODE, VAR), SB = stage_bytes_of(MODE, VAR);
   constexpr int LAG = NST - 2;  // cp.async groups a producer thread keeps in flight
-  // PAIR: clusters of two CTAs share the weight tiles (multicast) and the
-  // tile queue (filled by rank 0)
-  static_assert(!PAIR || pairable(MODE), "stage cannot run paired");
-  const int rank = PAIR ? (int)cluster_rank() : 0;
-  const int64_t cta0 = PAIR ? blockIdx.x / 2 : blockIdx.x;      // cluster (pair) index
-  const int64_t ncta = PAIR ? gridDim.x / 2 : gridDim.x;        // clusters (pairs) in the grid
+  const int64_t cta0 = blockIdx.x, ncta = gridDim.x;
   // A dispatch built for another (L, E, K) lays out its tables differently:
   // record the mismatch and read none of them (every thread reads the same
   // three header words, so the whole CTA leaves here together, before any
@@ -497,8 +467,8 @@ __global__ void __launch_bounds__(num_threads(MODE, VAR), 1) moe_gemm_kernel(con
       // full: the gathering producer threads (cp.async stages), the transform
       // warps (fused stages), else thread 0's arrive.expect_tx
       mbar_init(bar(s), FUSED || CP ? (CP ? PRODUCER_THREADS : 0) + transform_threads(MODE) : 1);
-      // empty: this CTA's MMA commit (and the peer's, when the pair shares the stage's weight tiles)
-      mbar_init(bar(4 + s), PAIR ? 2 : 1);
+      // empty: the MMA commit
+      mbar_init(bar(4 + s), 1);
       mbar_init(bar(48 + s), 1);
     }
     mbar_init(bar(8), 1);
@@ -510,9 +480,8 @@ __global__ void __launch_bounds__(num_threads(MODE, VAR), 1) moe_gemm_kernel(con
       mbar_init(bar(32 + i), 1);
       // readers of a queue slot: the producer warps (thread 0 alone in the
       // TMA-only stages), the transform warps (fused stages), the MMA thread
-      // and the four epilogue warps; in a pair rank 0's slot is also freed by
-      // the peer's readers (rank 1 posts nothing)
-      mbar_init(bar(40 + i), ((CP ? PRODUCER_WARPS : 1) + helper_warps(MODE) + 1 + EW) * (PAIR ? 2 : 1));
+      // and the epilogue warps
+      mbar_init(bar(40 + i), (CP ? PRODUCER_WARPS : 1) + helper_warps(MODE) + 1 + EW);
     }
     *abort_s = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -525,38 +494,31 @@ __global__ void __launch_bounds__(num_threads(MODE, VAR), 1) moe_gemm_kernel(con
   }
   tc_fence_before();
   __syncthreads();
-  if constexpr (PAIR) cluster_sync();  // the peer's barriers exist before any multicast or remote arrive
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
 
   const int num_mt = is_wgrad(MODE) ? 0 : *p.meta.num_m_tiles;
-  const int64_t total = is_wgrad(MODE) ? p.total_w : (int64_t)(num_mt / (PAIR || WIDE_T ? 2 : 1)) * p.n_tiles;
+  const int64_t total = is_wgrad(MODE) ? p.total_w : (int64_t)(num_mt / (WIDE_T ? 2 : 1)) * p.n_tiles;
   int32_t* err = p.meta.err;
   const uint64_t lim = p.wait_ns;
 
   // queue position j lives in slot j % TQ, phase (j / TQ) & 1
-  auto q_post = [&](int j, long long id) -> bool {  // thread 0 (of rank 0 in a pair)
+  auto q_post = [&](int j, long long id) -> bool {  // thread 0
     const int sl = j % TQ;
-    if (!wait_bounded<PAIR>(bar(40 + sl), (uint32_t)((j / TQ) & 1) ^ 1u, abort_s, err, lim)) return false;
+    if (!wait_bounded(bar(40 + sl), (uint32_t)((j / TQ) & 1) ^ 1u, abort_s, err, lim)) return false;
     tq[sl] = id;
     mbar_arrive(bar(32 + sl));
-    if constexpr (PAIR) {
-      // the same id in the peer's slot, then its full barrier (release at cluster scope)
-      st_cluster_u64(peer_addr(smem_u32((const void*)(tq + sl)), 1u), (unsigned long long)id);
-      mbar_arrive_cluster(peer_addr(bar(32 + sl), 1u));
-    }
     return true;
   };
   auto q_take = [&](int j) -> long long {  // one thread per reader; -1 once the CTA gives up
     const int sl = j % TQ;
-    if (!wait_bounded<PAIR>(bar(32 + sl), (uint32_t)(j / TQ) & 1u, abort_s, err, lim)) return -1;
+    if (!wait_bounded(bar(32 + sl), (uint32_t)(j / TQ) & 1u, abort_s, err, lim)) return -1;
     const long long id = tq[sl];
-    if (PAIR && rank == 1) mbar_arrive_cluster(peer_addr(bar(40 + sl), 0u));  // rank 0 owns the slots
-    else mbar_arrive(bar(40 + sl));
+    mbar_arrive(bar(40 + sl));
     return id;
   };
-  // tile of queue position j >= 2 (positions 0 and 1 are this CTA's (pair's)
-  // first two: cta0 and cta0 + ncta)
+  // tile of queue position j >= 2 (positions 0 and 1 are this CTA's first
+  // two: cta0 and cta0 + ncta)
   auto claim = [&]() -> long long { return 2ll * ncta + (long long)atomicAdd(p.sched, 1ull); };
 
   if (warp < PRODUCER_WARPS) {
@@ -603,17 +565,17 @@ __global__ void __launch_bounds__(num_threads(MODE, VAR), 1) moe_gemm_kernel(con
         }
         return id;
       };
-      if (pt == 0 && rank == 0 && q_post(0, cta0)) q_post(1, (long long)cta0 + ncta);
+      if (pt == 0 && q_post(0, cta0)) q_post(1, (long long)cta0 + ncta);
       long long tile = take(0);
       Tile t;
       if (tile >= 0 && tile < total) {
-        t = decode<MODE, PAIR, WIDE_T>(p, tile, num_mt, rank);
+        t = decode<MODE, WIDE_T>(p, tile, num_mt);
         load_tile_tokens(t, rtok, wtok);
       }
       ok = tile >= 0;
       for (int j = 0; ok && tile < total; ++j) {
         long long pending = 0;
-        if (pt == 0 && rank == 0) pending = claim();  // for position j + 2, posted after this tile's loads are issued
+        if (pt == 0) pending = claim();  // for position j + 2, posted after this tile's loads are issued
         const long long ntile = take(j + 1);
         if (ntile < 0) {
           ok = false;
@@ -621,7 +583,7 @@ __global__ void __launch_bounds__(num_threads(MODE, VAR), 1) moe_gemm_kernel(con
         }
         Tile tn;
         if (ntile < total) {
-          tn = decode<MODE, PAIR, WIDE_T>(p, ntile, num_mt, rank);
+          tn = decode<MODE, WIDE_T>(p, ntile, num_mt);
           load_tile_tokens(tn, rnext, wfirst);
         }
         const int nmma = is_dual(MODE) ? 2 * t.nw : t.nw;
@@ -677,15 +639,6 @@ __global__ void __launch_bounds__(num_threads(MODE, VAR), 1) moe_gemm_kernel(con
             }
             armed |= 1u << s;
             armed_par = (armed_par & ~(1u << s)) | (ph << s);
-            // box j of the weight tile both CTAs of a pair share: the CTA of
-            // rank j % 2 loads it for both (multicast); unpaired, this CTA
-            auto wbox = [&](int jb, uint32_t dst, const CUtensorMap* m, int c0, int c1, uint32_t b) {
-              if constexpr (PAIR) {
-                if ((jb & 1) == rank) tma_load_2d_mc(dst, m, c0, c1, b, (uint16_t)0x3);
-              } else {
-                tma_load_2d(dst, m, c0, c1, b);
-              }
-            };
             if constexpr (MODE == DOWN_H) {
 #pragma unroll
               for (int a = 0; a < AB / A_BYTES; ++a) tma_load_2d(sA + a * A_BYTES, &p.tmA, k0, t.row0 + a * BM, full);
@@ -711,23 +664,26 @@ __global__ void __launch_bounds__(num_threads(MODE, VAR), 1) moe_gemm_kernel(con
               }
             }
             if constexpr (MODE == UP_SWIGLU) {
-              wbox(0, sB, &p.tmB0, t.n0, t.e * p.d + k0, full);
-              wbox(1, sB + 8192, &p.tmB0, t.n0 + 64, t.e * p.d + k0, full);
-              wbox(2, sB + 16384, &p.tmB1, t.n0, t.e * p.d + k0, full);
-              wbox(3, sB + 24576, &p.tmB1, t.n0 + 64, t.e * p.d + k0, full);
+              tma_load_2d(sB, &p.tmB0, t.n0, t.e * p.d + k0, full);
+              tma_load_2d(sB + 8192, &p.tmB0, t.n0 + 64, t.e * p.d + k0, full);
+              tma_load_2d(sB + 16384, &p.tmB1, t.n0, t.e * p.d + k0, full);
+              tma_load_2d(sB + 24576, &p.tmB1, t.n0 + 64, t.e * p.d + k0, full);
             } else if constexpr (MODE == UP_SILU) {
-              for (int j = 0; j < t.nw / 64; ++j) wbox(j, sB + j * 8192, &p.tmB0, t.n0 + 64 * j, t.e * p.d + k0, full);
+              for (int j = 0; j < t.nw / 64; ++j)
+                tma_load_2d(sB + j * 8192, &p.tmB0, t.n0 + 64 * j, t.e * p.d + k0, full);
             } else if constexpr (is_down(MODE)) {
               const uint32_t wb = FUSED ? loaded : full;
-              for (int j = 0; j < t.nw / 64; ++j) wbox(j, sB + j * 8192, &p.tmB0, t.n0 + 64 * j, t.e * p.h + k0, wb);
+              for (int j = 0; j < t.nw / 64; ++j)
+                tma_load_2d(sB + j * 8192, &p.tmB0, t.n0 + 64 * j, t.e * p.h + k0, wb);
             } else if constexpr (MODE == DH_SWIGLU || MODE == DH_SILU) {
               for (int j = 0; j < t.nw / 128; ++j)
-                wbox(j, sB + j * 16384, &p.tmB0, k0, t.e * p.h + t.n0 + 128 * j, full);
+                tma_load_2d(sB + j * 16384, &p.tmB0, k0, t.e * p.h + t.n0 + 128 * j, full);
             } else if constexpr (MODE == DX) {
               const bool second = kb >= p.ksplit;
               const CUtensorMap* m = second ? &p.tmB1 : &p.tmB0;
               const int kc = second ? k0 - p.ksplit * BK : k0;
-              for (int j = 0; j < t.nw / 128; ++j) wbox(j, sB + j * 16384, m, kc, t.e * p.d + t.n0 + 128 * j, full);
+              for (int j = 0; j < t.nw / 128; ++j)
+                tma_load_2d(sB + j * 16384, m, kc, t.e * p.d + t.n0 + 128 * j, full);
             } else if constexpr (MODE == DW12) {
               tma_load_2d(sB, &p.tmB0, t.n0, t.pad0 + k0, full);
               tma_load_2d(sB + 8192, &p.tmB0, t.n0 + 64, t.pad0 + k0, full);
@@ -779,7 +735,7 @@ __global__ void __launch_bounds__(num_threads(MODE, VAR), 1) moe_gemm_kernel(con
           if (++s == NST) { s = 0; ph ^= 1u; }
         }
         if (!ok) break;
-        if (pt == 0 && rank == 0) ok = q_post(j + 2, pending);
+        if (pt == 0) ok = q_post(j + 2, pending);
         if constexpr (CP) {
           if (warp == 0) ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
         }
@@ -823,7 +779,7 @@ __global__ void __launch_bounds__(num_threads(MODE, VAR), 1) moe_gemm_kernel(con
         if (lane == 0) tile = q_take(j);
         tile = __shfl_sync(0xffffffffu, tile, 0);
         if (tile < 0 || tile >= total) break;
-        const Tile t = decode<MODE, PAIR, WIDE_T>(p, tile, num_mt, rank);
+        const Tile t = decode<MODE, WIDE_T>(p, tile, num_mt);
         for (int kb = 0; kb < t.kblocks; ++kb) {
           float g2[2] = {1.f, 1.f};
           if constexpr (is_dw3(MODE)) {
@@ -856,7 +812,7 @@ __global__ void __launch_bounds__(num_threads(MODE, VAR), 1) moe_gemm_kernel(con
       bool ok = true;
       long long tile = q_take(0);
       Tile t;
-      if (tile >= 0 && tile < total) t = decode<MODE, PAIR, WIDE_T>(p, tile, num_mt, rank);
+      if (tile >= 0 && tile < total) t = decode<MODE, WIDE_T>(p, tile, num_mt);
       for (int j = 0; ok; ++j) {
         if (tile < 0) {
           ok = false;
@@ -871,7 +827,7 @@ __global__ void __launch_bounds__(num_threads(MODE, VAR), 1) moe_gemm_kernel(con
         bool fetched = false;
         auto fetch_next = [&]() {
           ntile = q_take(j + 1);
-          if (ntile >= 0 && ntile < total) tn = decode<MODE, PAIR, WIDE_T>(p, ntile, num_mt, rank);
+          if (ntile >= 0 && ntile < total) tn = decode<MODE, WIDE_T>(p, ntile, num_mt);
           fetched = true;
         };
         const int nmma = is_dual(MODE) ? 2 * t.nw : t.nw;
@@ -904,8 +860,7 @@ __global__ void __launch_bounds__(num_threads(MODE, VAR), 1) moe_gemm_kernel(con
               mma_bf16(dcol, ad, bd, idesc, (kb | kk) ? 1u : 0u);
             }
           }
-          if constexpr (PAIR) mma_commit_mc(bar(4 + s), (uint16_t)0x3);  // frees the stage in both CTAs
-          else mma_commit(bar(4 + s));
+          mma_commit(bar(4 + s));
           if (++s == NST) { s = 0; ph ^= 1u; }
           if (kb == 0) fetch_next();
         }
@@ -934,7 +889,7 @@ __global__ void __launch_bounds__(num_threads(MODE, VAR), 1) moe_gemm_kernel(con
       if (lane == 0) tile = q_take(j);
       tile = __shfl_sync(0xffffffffu, tile, 0);
       if (tile < 0 || tile >= total) break;
-      const Tile t = decode<MODE, PAIR, WIDE_T>(p, tile, num_mt, rank);
+      const Tile t = decode<MODE, WIDE_T>(p, tile, num_mt);
       // Per-row context that does not depend on the accumulator is fetched
       // before waiting for it, so its latency overlaps the main loop.
       constexpr bool DH = MODE == DH_SWIGLU || MODE == DH_SILU;
@@ -1167,7 +1122,6 @@ __global__ void __launch_bounds__(num_threads(MODE, VAR), 1) moe_gemm_kernel(con
 
   tc_fence_before();
   __syncthreads();
-  if constexpr (PAIR) cluster_sync();  // no multicast or remote arrive is still headed for this CTA
   tc_fence_after();
   if (warp == MMA_WARP) {
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(TMEM_COLS) : "memory");
@@ -1176,44 +1130,15 @@ __global__ void __launch_bounds__(num_threads(MODE, VAR), 1) moe_gemm_kernel(con
 
 // ------------------------------------------------------------------ host side
 // Launch one GEMM stage.  `tiles_bound` bounds the number of 128-row tiles;
-// one CTA per SM, never more than there are tiles.  PAIR: clusters of two
-// CTAs on pairs of tiles (see the kernel).
+// one CTA per SM, never more than there are tiles.
 template <int MODE, int VAR = SINGLE>
 moeblaze_status launch(Params& p, int64_t tiles_bound, cudaStream_t st) {
   if (tiles_bound <= 0) return MOEBLAZE_OK;
   auto kern = moe_gemm_kernel<MODE, VAR>;
   constexpr int smem = smem_bytes_of(MODE, VAR);
   MB_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
-  if constexpr (VAR == PAIRED) {
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.gridDim = dim3((unsigned)(2 * (sm_count() / 2)));
-    cfg.blockDim = dim3(num_threads(MODE, VAR));
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    // as many clusters as can be resident at once, never more than pair tiles
-    static int resident[64][16] = {};
-    int dev = 0;
-    MB_CUDA(cudaGetDevice(&dev));
-    int& clusters = resident[dev & 63][MODE & 15];
-    if (clusters == 0) {
-      MB_CUDA(cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg));
-      if (clusters < 1) return MOEBLAZE_ERR_UNSUPPORTED;
-    }
-    const int64_t pairs = tiles_bound / 2 < clusters ? tiles_bound / 2 : clusters;
-    if (pairs < 1) return MOEBLAZE_OK;
-    cfg.gridDim = dim3((unsigned)(2 * pairs));
-    MB_CUDA(cudaLaunchKernelEx(&cfg, kern, p));
-  } else {
-    const int64_t g = tiles_bound < sm_count() ? tiles_bound : sm_count();
-    kern<<<(unsigned)g, num_threads(MODE, VAR), smem, st>>>(p);
-  }
+  const int64_t g = tiles_bound < sm_count() ? tiles_bound : sm_count();
+  kern<<<(unsigned)g, num_threads(MODE, VAR), smem, st>>>(p);
   MB_CUDA(cudaGetLastError());
   count_launch();
   return MOEBLAZE_OK;
@@ -1393,9 +1318,7 @@ moeblaze_status tc_backward(const moeblaze_shape& s, const __nv_bfloat16* dY, co
     if (sw && !make_map(&p.tmO2, B, s.h, rows, 32, 32, s64)) return MOEBLAZE_ERR_CUDA;
     if (!rec && !make_map(&p.tmO1, wsHg, s.h, rows, 32, 32, s64)) return MOEBLAZE_ERR_CUDA;
     const int64_t nt = mt_bound * p.n_tiles;
-    const bool pair = pair_stage(p.kblocks, nt);
-    moeblaze_status r = sw ? (pair ? launch<DH_SWIGLU, PAIRED>(p, nt, st) : launch<DH_SWIGLU>(p, nt, st))
-                           : (pair ? launch<DH_SILU, PAIRED>(p, nt, st) : launch<DH_SILU>(p, nt, st));
+    moeblaze_status r = sw ? launch<DH_SWIGLU>(p, nt, st) : launch<DH_SILU>(p, nt, st);
     if (r != MOEBLAZE_OK) return r;
   }
   stage_event(ev++, st);

@@ -25,8 +25,8 @@
 // into fp32 sums in the epilogue warps' registers, two accumulators in turn,
 // and stored at the end as the range's partial dWr.  65536 x 2048, 64 experts:
 // 55 us, 4.9 TB/s of x; an SM takes in about 35 bytes a clock, here 24 KB of
-// dl's parts for every 32 KB of x (dl multicast to pairs of CTAs: 57 us, the
-// same bytes arrive).  32768 x 4096, 8 experts: 42 us, 6.4 TB/s.
+// dl's parts for every 32 KB of x (one load of dl for pairs of CTAs: 57 us,
+// the same bytes arrive).  32768 x 4096, 8 experts: 42 us, 6.4 TB/s.
 //
 // dx_kernel: a CTA owns 256 columns of dx, whose rows of Wr stay in shared
 // memory, and walks over 128-token tiles, two TMEM accumulators in turn, so

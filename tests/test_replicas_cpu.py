@@ -42,3 +42,13 @@ def test_single_rank_needs_no_group():
     import bench
     assert bench.max_over_ranks(3.0, 1, torch.device("cpu")) == 3.0
     assert bench.job_tokens_per_s(1, 1000, 2.0) == 1000 / 2e-3
+
+
+def test_no_kernel_loads_for_another_cta():
+    """Replicas on several GPUs run the kernels that one runs alone: none of them has a TMA load (or commit) that
+    reaches the shared memory of more than one CTA."""
+    import glob
+    import mixture_experts_atomic_gb300 as pkg
+    files = glob.glob(os.path.join(os.path.dirname(pkg.__file__), "csrc", "*.cu*"))
+    assert len(files) >= 10
+    assert [f for f in files if "multicast" in open(f).read()] == []
