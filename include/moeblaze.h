@@ -368,6 +368,13 @@ MOEBLAZE_API moeblaze_status moeblaze_router_backward_logits(const moeblaze_shap
  *   given, + gates_k (dgates_k - sum_j gates_j dgates_j) on the chosen
  *   experts: the gates' softmax over the chosen logits.  Rows of tokens that
  *   are not active are 0.
+ * moeblaze_balance_backward_masked: the same, with
+ *   valid    device (L) uint8 or NULL: tokens for which it is zero are left
+ *            out as those that are not active are (the forward's mask need
+ *            not be given again: lse holds it)
+ *   gates_of_all  != 0: the gates' share reaches the rows of all tokens, those
+ *            left out of the losses too.  For a mask of the losses alone: the
+ *            layer routes every token, and its output depends on their gates.
  * Sums run in a fixed order: results are repeatable to the bit. */
 MOEBLAZE_API size_t moeblaze_balance_workspace_bytes(const moeblaze_shape* s);
 MOEBLAZE_API moeblaze_status moeblaze_balance_forward(const moeblaze_shape* s, const float* logits,
@@ -378,6 +385,12 @@ MOEBLAZE_API moeblaze_status moeblaze_balance_backward(const moeblaze_shape* s, 
                                                        const int32_t* counts, const float* dlosses,
                                                        const int32_t* topk_ids, const float* gates,
                                                        const float* dgates, float* dlogits, moeblaze_stream stream);
+MOEBLAZE_API moeblaze_status moeblaze_balance_backward_masked(const moeblaze_shape* s, const float* logits,
+                                                              const float* lse, const int32_t* counts,
+                                                              const float* dlosses, const uint8_t* valid,
+                                                              const int32_t* topk_ids, const float* gates,
+                                                              const float* dgates, int32_t gates_of_all,
+                                                              float* dlogits, moeblaze_stream stream);
 
 /* ---------------------------------------------------------------- layer norm
  * The norm in front of the layer (pre-norm block), with the residual sum, and

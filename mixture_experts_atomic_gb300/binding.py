@@ -37,7 +37,7 @@ EXPORTS = [
     "moeblaze_balance_forward", "moeblaze_balance_backward", "moeblaze_layernorm_forward",
     "moeblaze_layernorm_backward", "moeblaze_layernorm_backward_workspace_bytes", "moeblaze_int4_weight_bytes",
     "moeblaze_int4_scale_bytes", "moeblaze_int4_quantize", "moeblaze_int4_pack", "moeblaze_int4_dequantize",
-    "moeblaze_int4_workspace_bytes", "moeblaze_int4_forward",
+    "moeblaze_int4_workspace_bytes", "moeblaze_int4_forward", "moeblaze_balance_backward_masked",
 ]
 
 # fixed scratch of moeblaze_dispatch_build_static (MOEBLAZE_STATIC_SCRATCH_BYTES)
@@ -109,6 +109,7 @@ def lib():
         L.moeblaze_router_backward_logits.argtypes = [SP, P, P, P, P, P, P, ctypes.c_int32, P, sz, P]
         L.moeblaze_balance_forward.argtypes = [SP, P, P, P, P, P, P, P, sz, P]
         L.moeblaze_balance_backward.argtypes = [SP, P, P, P, P, P, P, P, P, P]
+        L.moeblaze_balance_backward_masked.argtypes = [SP, P, P, P, P, P, P, P, P, ctypes.c_int32, P, P]
         L.moeblaze_layernorm_forward.argtypes = [SP, P, P, P, P, ctypes.c_float, P, P, P, P, P]
         L.moeblaze_layernorm_backward.argtypes = [SP, P, P, P, P, P, P, P, P, P, P, sz, P]
         i32 = ctypes.c_int32
@@ -244,6 +245,12 @@ def moeblaze_balance_forward(shape, logits, topk_ids, valid, losses, counts, lse
 def moeblaze_balance_backward(shape, logits, lse, counts, dlosses, topk_ids, gates, dgates, dlogits, stream) -> int:
     return lib().moeblaze_balance_backward(ctypes.byref(shape), logits, lse, counts, dlosses, topk_ids, gates, dgates,
                                            dlogits, stream)
+
+
+def moeblaze_balance_backward_masked(shape, logits, lse, counts, dlosses, valid, topk_ids, gates, dgates, gates_of_all,
+                                     dlogits, stream) -> int:
+    return lib().moeblaze_balance_backward_masked(ctypes.byref(shape), logits, lse, counts, dlosses, valid, topk_ids,
+                                                  gates, dgates, int(gates_of_all), dlogits, stream)
 
 
 def moeblaze_layernorm_forward(shape, x, residual, weight, bias, eps, sum, y, mean, rstd, stream) -> int:
@@ -655,9 +662,10 @@ def balance_forward(shape: Shape, logits, topk_ids, valid, losses, counts, lse, 
 
 
 def balance_backward(shape: Shape, logits, lse, counts, dlosses, topk_ids, gates, dgates, dlogits, stream=None,
-                     own=False):
+                     own=False, gates_of_all=False):
     """Gradient of the logits (L,E) fp32 from the gradients of the two losses and, when topk_ids, gates and dgates
-    are given (all or none), of the gates.  own: lse and counts are buffers made for this shape on dlogits' device."""
+    are given (all or none), of the gates; gates_of_all: of the gates of tokens left out of the losses too.
+    own: lse and counts are buffers made for this shape on dlogits' device."""
     L, E, K = shape.L, shape.E, shape.K
     specs = ((logits, "logits", (L, E), torch.float32, False), (dlosses, "dlosses", (2,), torch.float32, False),
              (topk_ids, "topk_ids", (L, K), torch.int32, True), (gates, "gates", (L, K), torch.float32, True),
@@ -667,9 +675,10 @@ def balance_backward(shape: Shape, logits, lse, counts, dlosses, topk_ids, gates
     _args(*specs)
     if L > 0 and len({topk_ids is None, gates is None, dgates is None}) != 1:
         raise ValueError("topk_ids, gates and dgates: give all three or none")
-    st = moeblaze_balance_backward(shape, _ptr(logits), _ptr(lse), _ptr(counts), _ptr(dlosses), _ptr(topk_ids),
-                                   _ptr(gates), _ptr(dgates), _ptr(dlogits), _stream(stream))
-    _check(st, "moeblaze_balance_backward")
+    st = moeblaze_balance_backward_masked(shape, _ptr(logits), _ptr(lse), _ptr(counts), _ptr(dlosses), None,
+                                          _ptr(topk_ids), _ptr(gates), _ptr(dgates), gates_of_all, _ptr(dlogits),
+                                          _stream(stream))
+    _check(st, "moeblaze_balance_backward_masked")
 
 
 def layernorm_forward(shape: Shape, x, residual, weight, bias, eps, sum, y, mean, rstd, stream=None, own=False):

@@ -76,13 +76,13 @@ class BalanceLoss:
                           own=self._ws_bytes)
         return losses, self.counts
 
-    def backward(self, logits, dlosses, valid=None, topk_ids=None, gates=None, dgates=None):
+    def backward(self, logits, dlosses, valid=None, topk_ids=None, gates=None, dgates=None, gates_of_all=False):
         """dlogits after a forward on the same logits: of the losses, with gradients dlosses (2), and of the
         gates when topk_ids, gates and dgates are given.  The tokens left out are those the forward left out
-        (valid is taken for symmetry and not read)."""
+        (valid is taken for symmetry and not read): their rows are 0, or, with gates_of_all, the gates' share."""
         dlogits = self._out[1]
         B.balance_backward(self.shape, logits, self._lse, self._counts, dlosses, topk_ids, gates, dgates, dlogits,
-                           own=True)
+                           own=True, gates_of_all=gates_of_all)
         return dlogits
 
 
@@ -127,7 +127,7 @@ class MoEBlock:
 
     def forward(self, x, residual, p, valid=None):
         """(out, s, losses, counts).  p: dict of parameters: norm_w, norm_b (or None), Wr, bias (or None), W1, W2, W3.
-        valid (L) uint8: tokens that count for the losses."""
+        valid (L) uint8: tokens that count for the losses (all of them are routed and have a row of out)."""
         u, s, mean, rstd = self.norm.forward(x, p["norm_w"], p.get("norm_b"), residual)
         ids, gates = self.layer.route(u, p["Wr"], p.get("bias"), self.logits)
         losses, counts = self.loss.forward(self.logits, ids, valid)
@@ -143,7 +143,8 @@ class MoEBlock:
         u, s, mean, rstd, ids, gates = self._kept
         self._kept = None
         du, dW1, dW2, dW3, dgates = self.layer.backward(dout, u, gates, p["W1"], p.get("W2"), p["W3"])
-        dlogits = self.loss.backward(self.logits, dlosses, None, ids, gates, dgates)
+        # the mask is the losses' alone: the gates of every token made its row of out
+        dlogits = self.loss.backward(self.logits, dlosses, None, ids, gates, dgates, gates_of_all=True)
         du, dWr, dbias = self.grad.backward(u, p["Wr"], dlogits, add_to=du)
         dx, dnw, dnb = self.norm.backward(du, s, mean, rstd, p["norm_w"], dsum)
         return {"x": dx, "norm_w": dnw, "norm_b": dnb, "Wr": dWr, "bias": dbias, "W1": dW1, "W2": dW2, "W3": dW3}

@@ -497,10 +497,10 @@ moeblaze_status moeblaze_balance_forward(const moeblaze_shape* s, const float* l
                                 reinterpret_cast<cudaStream_t>(stream));
 }
 
-moeblaze_status moeblaze_balance_backward(const moeblaze_shape* s, const float* logits, const float* lse,
-                                          const int32_t* counts, const float* dlosses, const int32_t* topk_ids,
-                                          const float* gates, const float* dgates, float* dlogits,
-                                          moeblaze_stream stream) {
+moeblaze_status moeblaze_balance_backward_masked(const moeblaze_shape* s, const float* logits, const float* lse,
+                                                 const int32_t* counts, const float* dlosses, const uint8_t* valid,
+                                                 const int32_t* topk_ids, const float* gates, const float* dgates,
+                                                 int32_t gates_of_all, float* dlogits, moeblaze_stream stream) {
   moeblaze_status r = check_balance_shape(s);
   if (r != MOEBLAZE_OK) return r;
   if (!ok_ptr4(counts) || !ok_ptr4(dlosses)) return MOEBLAZE_ERR_INVALID_ARG;
@@ -509,8 +509,16 @@ moeblaze_status moeblaze_balance_backward(const moeblaze_shape* s, const float* 
     return MOEBLAZE_ERR_INVALID_ARG;
   if (s->L > 0 && (!ok_ptr(logits) || !ok_ptr4(lse) || !ok_ptr(dlogits))) return MOEBLAZE_ERR_INVALID_ARG;
   if (gates && (!ok_ptr4(gates) || !ok_ptr4(dgates) || !ok_ptr4(topk_ids))) return MOEBLAZE_ERR_INVALID_ARG;
-  return launch_balance_backward(*s, logits, lse, counts, dlosses, topk_ids, gates, dgates, dlogits,
-                                 reinterpret_cast<cudaStream_t>(stream));
+  return launch_balance_backward(*s, logits, lse, counts, dlosses, topk_ids, gates, dgates, valid, gates_of_all != 0,
+                                 dlogits, reinterpret_cast<cudaStream_t>(stream));
+}
+
+moeblaze_status moeblaze_balance_backward(const moeblaze_shape* s, const float* logits, const float* lse,
+                                          const int32_t* counts, const float* dlosses, const int32_t* topk_ids,
+                                          const float* gates, const float* dgates, float* dlogits,
+                                          moeblaze_stream stream) {
+  return moeblaze_balance_backward_masked(s, logits, lse, counts, dlosses, nullptr, topk_ids, gates, dgates, 0, dlogits,
+                                          stream);
 }
 
 size_t moeblaze_int4_weight_bytes(int32_t E, int32_t R, int32_t N) {

@@ -12,7 +12,8 @@
 //           (a, b the gradients of the two losses; the counts are piecewise
 //           constant) and, with the gates' gradients, on a token's chosen
 //           experts + g_k (dg_k - sum_j g_j dg_j)
-//   rows of tokens that are not active are zero.
+//   rows of tokens that are not active are zero, or have the gates' share
+//   alone (the mask is the losses': a token it leaves out is still routed).
 //
 // f_e - sum_j f_j p_tj cancels when the load is even; both sides are taken
 // relative to the mean load (sum_j p_tj = 1 leaves the difference as it is).
@@ -299,10 +300,13 @@ __global__ void __launch_bounds__(kLossThreads) balance_losses_kernel(const floa
     write_losses(E, K, __float_as_int(all[2 * E + 1]), reinterpret_cast<const int*>(all) + E + 1, all, all[E], losses);
 }
 
-template <int VEC, int TE, int EPT, int U>
+// MASK: with a mask of its own, or the gates' share of tokens that are out of
+// the losses (a variant of its own: 0.6 us more at 65536 x 64)
+template <int VEC, int TE, int EPT, int U, bool MASK>
 __global__ void __launch_bounds__(kBwdThreads) balance_bwd_kernel(
     const float* logits, const float* lse_in, const int32_t* counts, const float* dloss, const int32_t* ids,
-    const float* gates, const float* dgates, int64_t L, int E, int K, float* dlogits) {
+    const float* gates, const float* dgates, const uint8_t* valid, bool gates_of_all, int64_t L, int E, int K,
+    float* dlogits) {
   // (no __restrict__: what the kernel before has written must not be read ahead of the wait)
   constexpr int GROUPS = kBwdThreads / TE;
   constexpr int KL = (kMaxK + TE - 1) / TE;  // slots a lane holds
@@ -312,12 +316,13 @@ __global__ void __launch_bounds__(kBwdThreads) balance_bwd_kernel(
   float* row = rows + grp * ROW;
   float l[U][EPT][VEC], lse[U], g[U][KL], dg[U][KL];
   int id[U][KL];
-  bool act[U];
+  bool act[U], on[U];
   auto fetch = [&](int64_t t0) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int64_t t = t0 + u * GROUPS + grp;
       lse[u] = t < L ? lse_in[t] : -INFINITY;
+      if (MASK) on[u] = !valid || (t < L && valid[t]);
       // (the logits of a token that is not active are loaded and not used)
       load_row<VEC, TE, EPT>(logits + t * E, E, te, t < L, l[u]);
 #pragma unroll
@@ -359,7 +364,7 @@ __global__ void __launch_bounds__(kBwdThreads) balance_bwd_kernel(
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int64_t t = t0 + u * GROUPS + grp;
-      act[u] = !(lse[u] == -INFINITY);
+      act[u] = !(lse[u] == -INFINITY) && (!MASK || on[u]);
       float dot = 0.f;
 #pragma unroll
       for (int j = 0; j < EPT; ++j)
@@ -373,7 +378,10 @@ __global__ void __launch_bounds__(kBwdThreads) balance_bwd_kernel(
 #pragma unroll
       for (int j = 0; j < EPT; ++j)
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) l[u][j][i] *= fmaf(A, f[j][i] - dot, zl);
+        for (int i = 0; i < VEC; ++i) {
+          l[u][j][i] *= fmaf(A, f[j][i] - dot, zl);
+          if (MASK && !act[u]) l[u][j][i] = 0.f;
+        }
       if (gates) {
         // the chosen experts' share: the row goes through shared memory,
         // where the lane that holds a slot adds to that slot's expert, slot
@@ -412,7 +420,7 @@ __global__ void __launch_bounds__(kBwdThreads) balance_bwd_kernel(
           const int e = (j * TE + te) * VEC;
           FVec<VEC> o;
 #pragma unroll
-          for (int i = 0; i < VEC; ++i) o.v[i] = act[u] ? l[u][j][i] : 0.f;
+          for (int i = 0; i < VEC; ++i) o.v[i] = act[u] || (MASK && gates_of_all) ? l[u][j][i] : 0.f;
           if (e < E) *reinterpret_cast<FVec<VEC>*>(dlogits + t * E + e) = o;
         }
       }
@@ -491,7 +499,7 @@ moeblaze_status fwd_layout(const moeblaze_shape& s, const float* logits, const i
 template <int VEC, int TE, int EPT, int U>
 moeblaze_status bwd_layout(const moeblaze_shape& s, const float* logits, const float* lse, const int32_t* counts,
                            const float* dloss, const int32_t* ids, const float* gates, const float* dgates,
-                           float* dlogits, cudaStream_t st) {
+                           const uint8_t* valid, bool gates_of_all, float* dlogits, cudaStream_t st) {
   const int64_t G = bal_ctas(s.L, pass_tokens<kBwdThreads, TE, U>(), kBwdPerSm);
   // it may be set up while the kernel before it runs (and waits for its end)
   cudaLaunchConfig_t cfg = {};
@@ -503,8 +511,9 @@ moeblaze_status bwd_layout(const moeblaze_shape& s, const float* logits, const f
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  MB_CUDA(cudaLaunchKernelEx(&cfg, balance_bwd_kernel<VEC, TE, EPT, U>, logits, lse, counts, dloss, ids, gates, dgates,
-                             (int64_t)s.L, (int)s.E, (int)s.K, dlogits));
+  auto kern = valid || gates_of_all ? balance_bwd_kernel<VEC, TE, EPT, U, true> : balance_bwd_kernel<VEC, TE, EPT, U, false>;
+  MB_CUDA(cudaLaunchKernelEx(&cfg, kern, logits, lse, counts, dloss, ids, gates, dgates,
+                             valid, gates_of_all, (int64_t)s.L, (int)s.E, (int)s.K, dlogits));
   count_launch();
   return MOEBLAZE_OK;
 }
@@ -531,10 +540,11 @@ moeblaze_status launch_balance_forward(const moeblaze_shape& s, const float* log
 
 moeblaze_status launch_balance_backward(const moeblaze_shape& s, const float* logits, const float* lse,
                                         const int32_t* counts, const float* dloss, const int32_t* ids,
-                                        const float* gates, const float* dgates, float* dlogits, cudaStream_t st) {
+                                        const float* gates, const float* dgates, const uint8_t* valid,
+                                        bool gates_of_all, float* dlogits, cudaStream_t st) {
   if (s.L == 0) return MOEBLAZE_OK;
 #define MB_CALL(VEC, TE, EPT, U) \
-  bwd_layout<VEC, TE, EPT, U>(s, logits, lse, counts, dloss, ids, gates, dgates, dlogits, st)
+  bwd_layout<VEC, TE, EPT, U>(s, logits, lse, counts, dloss, ids, gates, dgates, valid, gates_of_all, dlogits, st)
   MB_BAL_LAYOUT(s.E, MB_CALL);
 #undef MB_CALL
 }

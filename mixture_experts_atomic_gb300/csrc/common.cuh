@@ -166,7 +166,8 @@ moeblaze_status launch_balance_forward(const moeblaze_shape& s, const float* log
                                        cudaStream_t st);
 moeblaze_status launch_balance_backward(const moeblaze_shape& s, const float* logits, const float* lse,
                                         const int32_t* counts, const float* dloss, const int32_t* ids,
-                                        const float* gates, const float* dgates, float* dlogits, cudaStream_t st);
+                                        const float* gates, const float* dgates, const uint8_t* valid,
+                                        bool gates_of_all, float* dlogits, cudaStream_t st);
 
 // int4.cu
 bool int4_shape_ok(const moeblaze_shape& s, int group);  // a token's x, and a slice of its h, fit the products' shared memory

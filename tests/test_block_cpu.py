@@ -199,3 +199,16 @@ def test_int4_slices_are_bounded(group):
     assert B.moeblaze_int4_workspace_bytes(B.make_shape(1, 128, 1 << 22, 8, 2, B.BF16, "swiglu"), group) == 0
     # and what one slice a piece cost, it no longer does: the partial sums of the widest layer stay below its weights
     assert _int4_slices(64, 4096, 128 * 109, 8, 8, group) <= 16
+
+
+def test_balance_masked_status():
+    sh = B.make_shape(8, 1, 0, 8, 2, F, "identity")
+
+    def bwd(lg=OKP, lse=OKP, c=OKP, dl=OKP, v=OKP, ids=OKP, g=OKP, dg=OKP, out=OKP):
+        return B.moeblaze_balance_backward_masked(sh, lg, lse, c, dl, v, ids, g, dg, 1, out, None)
+
+    for k in ("lg", "lse", "c", "dl", "out", "ids", "g", "dg"):
+        assert bwd(**{k: None}) == B.ERR_INVALID_ARG, k
+    assert bwd(lg=BAD) == B.ERR_INVALID_ARG
+    assert B.moeblaze_balance_backward_masked(B.make_shape(0, 1, 0, 8, 2, F, "identity"), None, None, OKP, OKP, None,
+                                              None, None, None, 1, None, None) == B.OK

@@ -483,3 +483,74 @@ def test_example_trains_and_serves():
     assert all(h[1] == h[1] for h in history)
     y4, y16 = m.serve(p, 7, 2, group=64)
     assert (y4.float() - y16.float()).abs().max() <= 2e-2 * y16.float().abs().max()
+
+
+def test_block_with_a_loss_mask_against_differences():
+    """A token left out of the losses is still routed: with a gradient at its output, its gates' gradient reaches
+    every parameter before them."""
+    L, d, h, E, K = 48, 64, 64, 4, 2
+    g = torch.Generator().manual_seed(26)
+    r = lambda *s: torch.randn(*s, generator=g)  # noqa: E731
+    p = {"norm_w": 1 + 0.1 * r(d), "norm_b": 0.1 * r(d), "Wr": r(d, E) / 8, "bias": 0.1 * r(E), "W1": r(E, d, h) / 8,
+         "W2": r(E, d, h) / 8, "W3": r(E, h, d) / 8}
+    x, res, dout, ds = r(L, d), r(L, d), r(L, d), r(L, d)
+    coef = (0.8, 0.05)
+    for valid in ((torch.arange(L) % 3 != 0).to(torch.uint8), torch.zeros(L, dtype=torch.uint8)):
+        dev = {k: v.cuda() for k, v in p.items()}
+        block = MoEBlock(L, d, h, E, K, F32)
+        out, s, losses, counts = block.forward(x.cuda(), res.cuda(), dev, valid.cuda())
+        ids = block._kept[4].cpu().long()
+        grads = block.backward(dout.cuda(), torch.tensor(coef, device="cuda"), dev, ds.cuda())
+        torch.cuda.synchronize()
+        on = valid.bool()
+        n = max(1, int(on.sum()))
+        f_e = torch.bincount(ids[on].flatten(), minlength=E).double() / (n * K)
+        assert torch.equal(counts.cpu().long(), torch.bincount(ids[on].flatten(), minlength=E))
+
+        def loss(q, xx):
+            u, ss, _, _ = R.norm(xx, res, q["norm_w"], q["norm_b"], 1e-5)
+            lg = u @ R.d64(q["Wr"]) + R.d64(q["bias"])
+            gt = torch.softmax(torch.gather(lg, 1, ids), 1)
+            hid = R.silu(torch.einsum("td,edh->teh", u, R.d64(q["W1"]))) * torch.einsum("td,edh->teh", u, R.d64(q["W2"]))
+            full = torch.einsum("teh,ehd->ted", hid, R.d64(q["W3"]))
+            y = (torch.gather(full, 1, ids[:, :, None].expand(L, K, d)) * gt[:, :, None]).sum(1)
+            pr, lse = torch.softmax(lg, 1)[on], torch.logsumexp(lg, 1)[on]
+            return float((y * dout.double()).sum() + coef[0] * E * (f_e * pr.sum(0) / n).sum()
+                         + coef[1] * (lse ** 2).sum() / n + (ss * ds.double()).sum())
+
+        q = {k: v.double() for k, v in p.items()}
+        step = 1e-5
+        for name, grad in grads.items():
+            v = r(*grad.shape).double()
+            if name == "x":
+                want = (loss(q, x.double() + step * v) - loss(q, x.double() - step * v)) / (2 * step)
+            else:
+                up, dn = dict(q), dict(q)
+                up[name], dn[name] = q[name] + step * v, q[name] - step * v
+                want = (loss(up, x.double()) - loss(dn, x.double())) / (2 * step)
+            got = float((R.d64(grad) * v).sum())
+            assert abs(got - want) <= 2e-5 * float((R.d64(grad).abs() * v.abs()).sum()), (name, got, want)
+
+
+def test_balance_gates_of_all():
+    """The gates' share of tokens that are out of the losses, with masks of both kinds; the others' rows as without."""
+    for L, E, K in ((5, 3, 2), (700, 8, 2), (333, 64, 6), (90, 100, 8), (70, 512, 8)):
+        lg, ids, gates, dg, valid = _balance_inputs(L, E, K, 9 * L)
+        lg[2] = -float("inf")
+        ids[3, 0] = -1
+        c = [t.cuda() for t in (lg, ids, gates, dg, valid)]
+        loss = BalanceLoss(L, E, K)
+        loss.forward(c[0], c[1], c[4])
+        dl = torch.tensor([0.7, -0.3], device="cuda")
+        some = loss.backward(c[0], dl, None, c[1], c[2], c[3]).clone()
+        every = loss.backward(c[0], dl, None, c[1], c[2], c[3], gates_of_all=True).cpu()
+        on = valid.bool() & (torch.arange(L) != 2)
+        assert torch.equal(every[on], some.cpu()[on]) and not some[~on.cuda()].any()
+        g, d = R.d64(gates), R.d64(dg)
+        sd, sa = (g * d).sum(1, keepdim=True), (g * d).abs().sum(1, keepdim=True)
+        want, scale = torch.zeros(L, E + 1).double(), torch.zeros(L, E + 1).double()
+        slot = torch.where(ids >= 0, ids, torch.tensor(E, dtype=torch.int32)).long()
+        want.scatter_add_(1, slot, g * (d - sd))
+        scale.scatter_add_(1, slot, g.abs() * (d.abs() + sa))
+        R.inside(every[~on], want[~on, :E], (K + 4) * U * scale[~on, :E] + 1e-30, "gates' share")
+        assert torch.equal(loss.backward(c[0], dl, gates_of_all=True), loss.backward(c[0], dl))
