@@ -17,8 +17,9 @@ class Int4Experts:
         """Buffers for up to max_tokens tokens a call; the weights come with load or quantize."""
         self.max_tokens, self.d, self.h, self.E, self.K = max_tokens, d, h, E, K
         self.act, self.group, self.device = act, group, device
-        # a call's scratch depends on its tokens, and repeats beyond 64 of them
-        ws = [B.moeblaze_int4_workspace_bytes(self._shape(t), group) for t in range(1, min(max_tokens, 64) + 1)]
+        # a call's scratch depends on its tokens: with 64 or more, on the 64 of a launch and on the rest of the last
+        # one, which may take more of it than 64 do
+        ws = [B.moeblaze_int4_workspace_bytes(self._shape(t), group) for t in range(1, min(max_tokens, 127) + 1)]
         if max_tokens > 0 and min(ws) == 0:
             raise B.MoEBlazeError(B.ERR_UNSUPPORTED, "moeblaze_int4_workspace_bytes")
         self._ws = B._bytes(max(ws, default=0), device)

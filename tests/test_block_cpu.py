@@ -212,3 +212,16 @@ def test_balance_masked_status():
     assert bwd(lg=BAD) == B.ERR_INVALID_ARG
     assert B.moeblaze_balance_backward_masked(B.make_shape(0, 1, 0, 8, 2, F, "identity"), None, None, OKP, OKP, None,
                                               None, None, None, 1, None, None) == B.OK
+
+
+@pytest.mark.parametrize("d,h,E,K,group", [(1024, 7168, 64, 1, 128), (128, 2944, 64, 3, 64), (128, 8704, 32, 1, 64),
+                                           (128, 4608, 128, 2, 32), (256, 384, 8, 2, 128), (128, 13696, 16, 4, 64)])
+def test_int4_buffers_hold_every_number_of_tokens(d, h, E, K, group):
+    """A batch of L <= max_tokens tokens never needs more scratch than the object made for max_tokens has."""
+    from mixture_experts_atomic_gb300.int4 import Int4Experts
+    need = {L: B.moeblaze_int4_workspace_bytes(B.make_shape(L, d, h, E, K, B.BF16, "swiglu"), group)
+            for L in range(1, 261)}
+    for most in (1, 5, 63, 64, 65, 67, 80, 100, 126, 127, 128, 200, 260):
+        have = Int4Experts(most, d, h, E, K, "swiglu", group, device="cpu")._ws.numel()
+        short = [L for L in range(1, most + 1) if need[L] > have]
+        assert not short, (most, short, have)
