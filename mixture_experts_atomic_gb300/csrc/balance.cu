@@ -465,13 +465,15 @@ constexpr int kBwdPerSm = 4;
     return CALL(1, 32, 16, 1);                            \
   } while (0)
 
+constexpr size_t fwd_smem(int E) { return sizeof(float) * ((size_t)kBalWarps * E + E + 2 * kBalWarps); }
+
 template <int VEC, int TE, int EPT, int U>
 moeblaze_status fwd_layout(const moeblaze_shape& s, const float* logits, const int32_t* ids, const uint8_t* valid,
                            float* losses, int32_t* counts, float* lse, float* part, cudaStream_t st) {
   const int64_t G = bal_ctas(s.L, pass_tokens<kBalThreads, TE, U>(), kFwdPerSm);
-  const size_t sm = sizeof(float) * ((size_t)kBalWarps * s.E + s.E + 2 * kBalWarps);
+  const size_t sm = fwd_smem(s.E);
   auto kern = balance_fwd_kernel<VEC, TE, EPT, U>;
-  if (sm > 48 * 1024) MB_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm));
+  if (sm > 48 * 1024) MB_CUDA(smem_limit(kern, fwd_smem(kMaxE)));
   kern<<<(unsigned)G, kBalThreads, sm, st>>>(logits, ids, valid, s.L, s.E, s.K, lse, part, losses, counts);
   MB_CUDA(cudaGetLastError());
   count_launch();

@@ -189,6 +189,14 @@ moeblaze_status launch_router_dispatch(const moeblaze_shape& s, const void* x, c
                                        int32_t* ids, float* gates, float* logits, const moeblaze_dispatch& out,
                                        void* ws, cudaStream_t st);
 
+// A kernel's limit of dynamic shared memory.  It belongs to the kernel, not to
+// a call, and another host thread may be about to launch the same kernel on
+// another shape: every call sets the same value, the largest the kernel takes.
+template <typename Kernel>
+inline cudaError_t smem_limit(Kernel kern, size_t largest) {
+  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)largest);
+}
+
 // shared helpers (abi.cu)
 int sm_count();
 void count_launch(int n = 1);

@@ -593,6 +593,13 @@ cudaError_t launch_dependent(void (*kern)(Params...), dim3 grid, dim3 block, siz
   return cudaLaunchKernelEx(&cfg, kern, static_cast<Params>(args)...);
 }
 
+// dynamic shared memory of K1 and K3
+constexpr size_t bitmap_smem(int E) { return (size_t)E * kRow * (sizeof(uint32_t) + sizeof(uint16_t)); }
+template <int KM>
+constexpr size_t scatter_smem(int E) {
+  return (size_t)(7 * E + 2) * sizeof(int32_t) + (size_t)kChunkTokens * KM * (sizeof(int32_t) + sizeof(uint16_t));
+}
+
 // K2 (large layers) and K3 for ids of at most KM slots per token, once K1
 // (or the router kernel that does K1's work) has written the packed slots
 // and the per-(expert, chunk) counts.
@@ -609,9 +616,8 @@ moeblaze_status run_tail(const moeblaze_shape& s, const moeblaze_dispatch& out, 
     MB_CUDA(cudaGetLastError());
     count_launch();
   }
-  const size_t sm3 = (size_t)(7 * E + 2) * sizeof(int32_t) + (size_t)kChunkTokens * KM * (sizeof(int32_t) + sizeof(uint16_t));
-  if (sm3 > 48 * 1024)
-    MB_CUDA(cudaFuncSetAttribute(scatter_kernel<KM>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm3));
+  const size_t sm3 = scatter_smem<KM>(E);
+  if (sm3 > 48 * 1024) MB_CUDA(smem_limit(scatter_kernel<KM>, scatter_smem<KM>(kMaxE)));
   MB_CUDA(launch_dependent(scatter_kernel<KM>, dim3((unsigned)C), dim3(kT3), sm3, st, L, E, K, (const int32_t*)w.packed,
                            C, (const int32_t*)w.base, scanned, (const int32_t*)meta.n_e, out.expert_token_indices,
                            out.expert_token_offsets, out.token_index_map, meta, mt));
@@ -626,9 +632,8 @@ moeblaze_status run_build(const moeblaze_shape& s, const int32_t* ids, const moe
                           const DispatchWs& w, const MetaView& meta, int64_t C, int64_t mt, cudaStream_t st) {
   const int E = s.E, K = s.K;
   const int64_t L = s.L;
-  const size_t sm1 = (size_t)E * kRow * (sizeof(uint32_t) + sizeof(uint16_t));
-  if (sm1 > 48 * 1024)
-    MB_CUDA(cudaFuncSetAttribute(bitmap_kernel<KM>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm1));
+  const size_t sm1 = bitmap_smem(E);
+  if (sm1 > 48 * 1024) MB_CUDA(smem_limit(bitmap_kernel<KM>, bitmap_smem(kMaxE)));
   bitmap_kernel<KM><<<(unsigned)C, kThreads, sm1, st>>>(ids, L, E, K, out.token_expert_indices, w.packed, w.base, C,
                                                         meta.err);
   MB_CUDA(cudaGetLastError());

@@ -261,10 +261,11 @@ moeblaze_status launch_identity_combine(const moeblaze_shape& s, const void* src
   const int64_t LK = s.L * s.K;
   const MetaView meta = meta_view(disp.meta, s.E);
   const dim3 grid((unsigned)((s.L + kWin - 1) / kWin));
+  // (a limit of the kernel need not be set: 32 KB at most, 48 are every kernel's)
+  static_assert(kStages * kWin * kMaxK * kChunkBytes <= 40 * 1024, "more than the default limit leaves");
   const size_t smem = kStages * (size_t)kWin * s.K * kChunkBytes;
   // one instance per element type and K range (the address tables are sized by the largest K)
   auto run = [&](auto kern, const auto* in, auto* out) -> moeblaze_status {
-    MB_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
     kern<<<grid, kThreads, smem, st>>>(in, disp.expert_token_indices, disp.token_index_map, gates, out, s.L, s.d, s.K,
                                        LK, meta.hdr, s.E, meta.err);
     MB_CUDA(cudaGetLastError());

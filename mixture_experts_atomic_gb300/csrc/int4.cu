@@ -755,7 +755,7 @@ moeblaze_status launch_product_g(QParams p, int tokens, cudaStream_t st) {
   const int team = team_of(std::min<int64_t>(p.E, p.pairs) * p.slices * (p.N / (MODE == GATED ? 16 : 32)), (int)(len / 128));
   const size_t sm = fixed_bytes(GROUP) + token_bytes(len, GROUP, p.cap);
   auto run = [&](auto kern) -> moeblaze_status {
-    MB_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm));
+    MB_CUDA(smem_limit(kern, kQSmem));
     // the down projection's h comes from the launch before it, its routing and weights from before that
     MB_CUDA(launch_q(kern, (unsigned)sm_count(), kQThreads, sm, MODE == DOWN, st, p));
     count_launch();

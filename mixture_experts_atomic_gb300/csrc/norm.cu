@@ -917,7 +917,7 @@ moeblaze_status bwd_tile(const moeblaze_shape& s, const BwdShape& b, const void*
                          float* part, cudaStream_t st) {
   auto kern = norm_bwd_kernel<T, NV, WARP, BUDGET, THREADS, SHIFT, RES>;
   const size_t sm = bwd_smem<T, NV, BUDGET, RES>(b.threads);
-  MB_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm));
+  MB_CUDA(smem_limit(kern, bwd_smem<T, NV, BUDGET, RES>(WARP ? 32 * kNormWarps : THREADS ? THREADS : BUDGET)));
   kern<<<(unsigned)b.ctas, b.threads, sm, st>>>((const T*)dy, (const T*)sum, mean, rstd, w, (const T*)dsum, s.L, s.d,
                                                 (T*)dx, part);
   MB_CUDA(cudaGetLastError());
@@ -999,7 +999,8 @@ moeblaze_status fwd_shift(const moeblaze_shape& s, int words, const void* x, con
                    : (res ? norm_fwd_shift_kernel<T, false, true> : norm_fwd_shift_kernel<T, false, false>);
   const int nt = warp ? 32 * kNormWarps : threads;
   const size_t sm = res ? fwd_shift_smem<T, true>(nt) : fwd_shift_smem<T, false>(nt);
-  MB_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm));
+  const int most = warp ? nt : 1024;
+  MB_CUDA(smem_limit(kern, res ? fwd_shift_smem<T, true>(most) : fwd_shift_smem<T, false>(most)));
   kern<<<(unsigned)g, nt, sm, st>>>((const T*)x, (const T*)res, w, b, s.L, s.d, eps,
                                                                   (T*)sum, (T*)y, mean, rstd);
   MB_CUDA(cudaGetLastError());

@@ -1126,7 +1126,7 @@ moeblaze_status fwd_ep(const moeblaze_shape& s, const void* x, const float* Wr, 
     const size_t wb = ((size_t)s.d * EP + (size_t)s.d / 2) * sizeof(float);
     if (wb <= kGemvWrBytes) {
       auto kern = router_fwd_gemv_kernel<T, EP>;
-      MB_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)wb));
+      MB_CUDA(smem_limit(kern, kGemvWrBytes));
       const int threads = 512;
       int64_t blocks = (s.L + (threads / 32) * 4 - 1) / ((threads / 32) * 4);
       if (blocks > (int64_t)sm_count()) blocks = sm_count();  // one persistent CTA per SM
