@@ -95,6 +95,34 @@ def test_norm_backward(L, d, dt, residual):
     R.inside(db, dbr, m * U * dya.sum(0), "db")
 
 
+@pytest.mark.parametrize("offset", [100.0, 1000.0])
+@pytest.mark.parametrize("residual", [True, False])
+@pytest.mark.parametrize("L,d,dt", [(300, 64, F32), (300, 96, F32), (300, 133, F32), (300, 1024, F32), (300, 1409, F32),
+                                    (40, 8190, F32), (40, 33000, F32), (300, 64, BF16), (300, 138, BF16), (300, 1024, BF16),
+                                    (300, 4096, BF16), (300, 5120, BF16), (300, 8191, BF16)])
+def test_norm_backward_of_rows_with_an_offset(L, d, dt, residual, offset):
+    """Rows whose offset is many times their spread: x - mean keeps what a difference of products would round off."""
+    x, _, w, _, dy, ds = _norm_inputs(L, d, dt, L * 5 + d, offset)
+    ds = ds if residual else None
+    _, _, mean, rstd = R.norm(x, None, w, None, 1e-5)
+    mean, rstd = mean.float().cuda(), rstd.float().cuda()
+    dx, dw, db = LayerNorm(L, d, dt).backward(dy, x, mean, rstd, w, ds)
+    torch.cuda.synchronize()
+    dxr, dwr, dbr, xh, g = R.norm_grad(dy, x, mean, rstd, w, ds)
+    n = 48 + d / 1024
+    rs = R.d64(rstd)[:, None]
+    gm, xm, gx = (v.abs().amax(1, keepdim=True) for v in (g, xh, g * xh))
+    exh = 2 * U * xm                                       # x - mean, and its product with rstd, rounded once each
+    mgx = (g * xh).mean(1, keepdim=True).abs()
+    e = rs * (n * U * gm + xm * (n * U * gx + gm * exh) + exh * mgx + 8 * U * (gm + xm * mgx))
+    tot = dxr.abs() + e
+    R.inside(dx, dxr, R.HALF[dt] * tot + e + 4 * U * tot + (4 * U * R.d64(ds).abs() if residual else 0), "dx")
+    m = 64 + L / 64
+    dya = R.d64(dy).abs()
+    R.inside(dw, dwr, m * U * (dya * xh.abs()).sum(0) + (dya * exh).sum(0), "dw")
+    R.inside(db, dbr, m * U * dya.sum(0), "db")
+
+
 def test_norm_gradient_against_differences():
     L, d = 6, 200
     x, _, w, b, dy, _ = _norm_inputs(L, d, F32, 3)
