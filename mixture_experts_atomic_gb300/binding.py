@@ -662,21 +662,22 @@ def balance_forward(shape: Shape, logits, topk_ids, valid, losses, counts, lse, 
 
 
 def balance_backward(shape: Shape, logits, lse, counts, dlosses, topk_ids, gates, dgates, dlogits, stream=None,
-                     own=False, gates_of_all=False):
+                     own=False, gates_of_all=False, valid=None):
     """Gradient of the logits (L,E) fp32 from the gradients of the two losses and, when topk_ids, gates and dgates
     are given (all or none), of the gates; gates_of_all: of the gates of tokens left out of the losses too.
+    valid: (L) uint8 or None, tokens left out besides those the forward left out.
     own: lse and counts are buffers made for this shape on dlogits' device."""
     L, E, K = shape.L, shape.E, shape.K
     specs = ((logits, "logits", (L, E), torch.float32, False), (dlosses, "dlosses", (2,), torch.float32, False),
-             (topk_ids, "topk_ids", (L, K), torch.int32, True), (gates, "gates", (L, K), torch.float32, True),
-             (dgates, "dgates", (L, K), torch.float32, True), (dlogits, "dlogits", (L, E), torch.float32, False))
+             (valid, "valid", (L,), torch.uint8, True), (topk_ids, "topk_ids", (L, K), torch.int32, True),
+             (gates, "gates", (L, K), torch.float32, True), (dgates, "dgates", (L, K), torch.float32, True), (dlogits, "dlogits", (L, E), torch.float32, False))
     if not own:
         specs += ((lse, "lse", (L,), torch.float32, False), (counts, "counts", (E + 1,), torch.int32, False))
     _args(*specs)
     if L > 0 and len({topk_ids is None, gates is None, dgates is None}) != 1:
         raise ValueError("topk_ids, gates and dgates: give all three or none")
-    st = moeblaze_balance_backward_masked(shape, _ptr(logits), _ptr(lse), _ptr(counts), _ptr(dlosses), None,
-                                          _ptr(topk_ids), _ptr(gates), _ptr(dgates), gates_of_all, _ptr(dlogits),
+    st = moeblaze_balance_backward_masked(shape, _ptr(logits), _ptr(lse), _ptr(counts), _ptr(dlosses),
+                                          _ptr(valid), _ptr(topk_ids), _ptr(gates), _ptr(dgates), gates_of_all, _ptr(dlogits),
                                           _stream(stream))
     _check(st, "moeblaze_balance_backward_masked")
 

@@ -67,6 +67,7 @@ class BalanceLoss:
         self.dlogits = torch.empty((L, E), **f32)
         self._ws_bytes = B.moeblaze_balance_workspace_bytes(self.shape)
         self._ws = B._bytes(self._ws_bytes, device)
+        self._ran = False  # until then there are no statistics for backward
         self._out = (self.losses, self.dlogits)  # what the calls write, whatever becomes of the names
 
     def forward(self, logits, topk_ids, valid=None):
@@ -74,15 +75,19 @@ class BalanceLoss:
         losses = self._out[0]
         B.balance_forward(self.shape, logits, topk_ids, valid, losses, self._counts, self._lse, self._ws,
                           own=self._ws_bytes)
+        self._ran = True
         return losses, self.counts
 
     def backward(self, logits, dlosses, valid=None, topk_ids=None, gates=None, dgates=None, gates_of_all=False):
         """dlogits after a forward on the same logits: of the losses, with gradients dlosses (2), and of the
         gates when topk_ids, gates and dgates are given.  The tokens left out are those the forward left out
-        (valid is taken for symmetry and not read): their rows are 0, or, with gates_of_all, the gates' share."""
+        (its mask need not be given again) and those that valid leaves out here: their rows are 0, or, with
+        gates_of_all, the gates' share."""
+        if not self._ran:
+            raise RuntimeError("BalanceLoss: run forward first")
         dlogits = self._out[1]
         B.balance_backward(self.shape, logits, self._lse, self._counts, dlosses, topk_ids, gates, dgates, dlogits,
-                           own=True, gates_of_all=gates_of_all)
+                           own=True, gates_of_all=gates_of_all, valid=valid)
         return dlogits
 
 

@@ -300,13 +300,13 @@ __global__ void __launch_bounds__(kLossThreads) balance_losses_kernel(const floa
     write_losses(E, K, __float_as_int(all[2 * E + 1]), reinterpret_cast<const int*>(all) + E + 1, all, all[E], losses);
 }
 
-// MASK: with a mask of its own, or the gates' share of tokens that are out of
-// the losses (a variant of its own: 0.6 us more at 65536 x 64)
-template <int VEC, int TE, int EPT, int U, bool MASK>
+// MASK: 1 with a mask of its own, 2 (with or without one) with the gates' share
+// of tokens that are out of the losses (variants of their own: 2 takes 0.6 us
+// more at 65536 x 64)
+template <int VEC, int TE, int EPT, int U, int MASK>
 __global__ void __launch_bounds__(kBwdThreads) balance_bwd_kernel(
     const float* logits, const float* lse_in, const int32_t* counts, const float* dloss, const int32_t* ids,
-    const float* gates, const float* dgates, const uint8_t* valid, bool gates_of_all, int64_t L, int E, int K,
-    float* dlogits) {
+    const float* gates, const float* dgates, const uint8_t* valid, int64_t L, int E, int K, float* dlogits) {
   // (no __restrict__: what the kernel before has written must not be read ahead of the wait)
   constexpr int GROUPS = kBwdThreads / TE;
   constexpr int KL = (kMaxK + TE - 1) / TE;  // slots a lane holds
@@ -380,7 +380,7 @@ __global__ void __launch_bounds__(kBwdThreads) balance_bwd_kernel(
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
           l[u][j][i] *= fmaf(A, f[j][i] - dot, zl);
-          if (MASK && !act[u]) l[u][j][i] = 0.f;
+          if (MASK == 2 && !act[u]) l[u][j][i] = 0.f;
         }
       if (gates) {
         // the chosen experts' share: the row goes through shared memory,
@@ -420,7 +420,7 @@ __global__ void __launch_bounds__(kBwdThreads) balance_bwd_kernel(
           const int e = (j * TE + te) * VEC;
           FVec<VEC> o;
 #pragma unroll
-          for (int i = 0; i < VEC; ++i) o.v[i] = act[u] || (MASK && gates_of_all) ? l[u][j][i] : 0.f;
+          for (int i = 0; i < VEC; ++i) o.v[i] = MASK == 2 || act[u] ? l[u][j][i] : 0.f;
           if (e < E) *reinterpret_cast<FVec<VEC>*>(dlogits + t * E + e) = o;
         }
       }
@@ -513,9 +513,11 @@ moeblaze_status bwd_layout(const moeblaze_shape& s, const float* logits, const f
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  auto kern = valid || gates_of_all ? balance_bwd_kernel<VEC, TE, EPT, U, true> : balance_bwd_kernel<VEC, TE, EPT, U, false>;
+  auto kern = gates_of_all ? balance_bwd_kernel<VEC, TE, EPT, U, 2>
+              : valid      ? balance_bwd_kernel<VEC, TE, EPT, U, 1>
+                           : balance_bwd_kernel<VEC, TE, EPT, U, 0>;
   MB_CUDA(cudaLaunchKernelEx(&cfg, kern, logits, lse, counts, dloss, ids, gates, dgates,
-                             valid, gates_of_all, (int64_t)s.L, (int)s.E, (int)s.K, dlogits));
+                             valid, (int64_t)s.L, (int)s.E, (int)s.K, dlogits));
   count_launch();
   return MOEBLAZE_OK;
 }

@@ -225,3 +225,9 @@ def test_int4_buffers_hold_every_number_of_tokens(d, h, E, K, group):
         have = Int4Experts(most, d, h, E, K, "swiglu", group, device="cpu")._ws.numel()
         short = [L for L in range(1, most + 1) if need[L] > have]
         assert not short, (most, short, have)
+
+
+def test_balance_backward_before_forward():
+    from mixture_experts_atomic_gb300.block import BalanceLoss
+    with pytest.raises(RuntimeError, match="run forward first"):
+        BalanceLoss(8, 4, 2, device="cpu").backward(torch.zeros(8, 4), torch.ones(2))

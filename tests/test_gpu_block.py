@@ -582,3 +582,28 @@ def test_balance_gates_of_all():
         scale.scatter_add_(1, slot, g.abs() * (d.abs() + sa))
         R.inside(every[~on], want[~on, :E], (K + 4) * U * scale[~on, :E] + 1e-30, "gates' share")
         assert torch.equal(loss.backward(c[0], dl, gates_of_all=True), loss.backward(c[0], dl))
+
+
+def test_balance_backward_mask():
+    """A mask given to backward leaves tokens out besides the forward's; a malformed one is refused."""
+    for L, E, K in ((40, 6, 2), (700, 8, 2), (333, 64, 6), (90, 130, 3)):
+        lg, ids, gates, dg, valid = _balance_inputs(L, E, K, 4 * L)
+        more = torch.ones(L, dtype=torch.uint8)
+        more[::3] = 0
+        c = [t.cuda() for t in (lg, ids, gates, dg, valid, more)]
+        loss = BalanceLoss(L, E, K)
+        dl = torch.tensor([0.7, -0.3], device="cuda")
+        loss.forward(c[0], c[1], c[4])
+        want = loss.backward(c[0], dl, None, *c[1:4]).clone()
+        assert torch.equal(loss.backward(c[0], dl, c[4], *c[1:4]), want)
+        share = loss.backward(c[0], dl, None, *c[1:4], gates_of_all=True).clone()
+        both = loss.backward(c[0], dl, c[5], *c[1:4], gates_of_all=True).clone()
+        out = loss.backward(c[0], dl, c[5], *c[1:4])
+        assert not out[::3].any() and torch.equal(out[more.bool()], want[more.bool()])
+        assert torch.equal(both[more.bool()], share[more.bool()])
+        gone = torch.zeros_like(valid).cuda()
+        assert torch.equal(both[::3], loss.backward(c[0], dl, gone, *c[1:4], gates_of_all=True)[::3])
+    with pytest.raises(ValueError, match="valid: dtype"):
+        loss.backward(c[0], dl, c[4].bool())
+    with pytest.raises(ValueError, match="valid: shape"):
+        loss.backward(c[0], dl, c[4][:-1])
