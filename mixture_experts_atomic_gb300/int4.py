@@ -33,13 +33,21 @@ class Int4Experts:
 
     def load(self, q1, s1, q2, s2, q3, s3):
         """Pack 4-bit weights: q1, q2 (E,d,h), q3 (E,h,d) int8 in -8..7 and their scales (E,R/group,N) bf16
-        (R the middle axis; q2, s2 None for SiLU).  The packed copies replace earlier ones in place."""
+        (R the middle axis; q2, s2 None for SiLU).  The packed copies replace earlier ones in place, all of them or,
+        when a tensor is refused, none."""
         mats = [("1", q1, s1, self.d, self.h), ("3", q3, s3, self.h, self.d)]
         if self.act == "swiglu":
             mats.append(("2", q2, s2, self.d, self.h))
+        specs = []
         for n, q, s, R, N in mats:
             if not isinstance(q, torch.Tensor) or tuple(q.shape) != (self.E, R, N):
                 raise ValueError(f"q{n}: expected a tensor of shape {(self.E, R, N)}")
+            specs += [(q, "q" + n, (self.E, R, N), torch.int8, False),
+                      (s, "s" + n, (self.E, R // self.group, N), torch.bfloat16, False)]
+        B._args(*specs)
+        for t, name, *_ in specs:
+            if t.device != self._ws.device:  # the products read the packed copies beside the buffers
+                raise ValueError(f"{name}: on {t.device}, but the buffers are on {self._ws.device}")
         for n, q, s, R, N in mats:
             old = self._packed.get(n, (None, None))
             self._packed[n] = B.int4_pack(q, s, self.group, *old)

@@ -231,3 +231,31 @@ def test_balance_backward_before_forward():
     from mixture_experts_atomic_gb300.block import BalanceLoss
     with pytest.raises(RuntimeError, match="run forward first"):
         BalanceLoss(8, 4, 2, device="cpu").backward(torch.zeros(8, 4), torch.ones(2))
+
+
+def test_int4_load_refuses_before_it_replaces(monkeypatch):
+    """A tensor that does not fit, whichever it is, leaves the weights that are loaded as they are."""
+    from mixture_experts_atomic_gb300.int4 import Int4Experts
+    E, d, h, G = 2, 128, 256, 64
+    ex = Int4Experts(4, d, h, E, 1, "swiglu", G, device="cpu")
+    packs = []
+    monkeypatch.setattr(B, "int4_pack", lambda q, s, group, *old: packs.append(1) or (q, s))
+    q = lambda r, n, dt=torch.int8: torch.zeros(E, r, n, dtype=dt)  # noqa: E731
+    s = lambda r, n, dt=BF: torch.ones(E, r // G, n, dtype=dt)  # noqa: E731
+    good = [q(d, h), s(d, h), q(d, h), s(d, h), q(h, d), s(h, d)]
+    for at, bad, msg in ((1, s(2 * d, h), "s1: shape"), (3, s(d, h, F), "s2: dtype"), (5, s(d, h), "s3: shape"),
+                         (5, None, "s3: a tensor"), (3, torch.ones(E, h, d // G, dtype=BF).transpose(1, 2), "s2: must be"),
+                         (4, q(h, d, torch.uint8), "q3: dtype"), (2, q(h, d), "q2: expected"), (0, None, "q1: expected"),
+                         (1, s(d, h), "must be a CUDA tensor")):
+        args = list(good)
+        args[at] = bad
+        with pytest.raises(ValueError, match=msg):
+            ex.load(*args)
+    assert not packs and ex._weights is None
+    # weights on another device than the buffers are refused too (their checks of the current device aside)
+    monkeypatch.setattr(B, "_args", lambda *specs: None)
+    with pytest.raises(ValueError, match="q1: on meta, but the buffers are on cpu"):
+        ex.load(*[t.to("meta") for t in good])
+    assert not packs
+    ex.load(*good)
+    assert len(packs) == 3
