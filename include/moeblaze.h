@@ -432,7 +432,9 @@ MOEBLAZE_API moeblaze_status moeblaze_layernorm_backward(const moeblaze_shape* s
  *
  * moeblaze_int4_quantize: W device (E,R,N) dtype -> q device (E,R,N) int8,
  *   scales device (E,R/group,N) bf16: scale = bf16(max |W| of the group / 7),
- *   q = round(W / scale) (to even) within -8..7; a group of zeros: scale 0, q 0.
+ *   q = round(W / scale) (to even) within -8..7; a group of zeros: scale 0, q 0;
+ *   a group with a NaN or an infinity: q 0 and a scale of NaN or infinity, so
+ *   that its weights, and what is computed with them, are NaN.
  * moeblaze_int4_pack: q and scales -> the layout the products read, device
  *   moeblaze_int4_weight_bytes and moeblaze_int4_scale_bytes bytes; done once
  *   when the weights are loaded.  Only the low 4 bits of q are kept.

@@ -126,12 +126,15 @@ __global__ void int4_quantize_kernel(const T* __restrict__ W, int64_t EG, int gr
   for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
     const int64_t eg = i / N, n = i % N, base = eg * group * N + n;
     float m = 0.f;
-    for (int r = 0; r < group; ++r) m = fmaxf(m, fabsf((float)W[base + (int64_t)r * N]));
+    for (int r = 0; r < group; ++r) {
+      const float a = fabsf((float)W[base + (int64_t)r * N]);
+      m = a > m || a != a ? a : m;  // a NaN stays: no number is above it
+    }
     const __nv_bfloat16 sb = __float2bfloat16_rn(m / 7.f);
     const float s = __bfloat162float(sb);
     scales[i] = sb;
     for (int r = 0; r < group; ++r) {
-      const float v = s > 0.f ? rintf((float)W[base + (int64_t)r * N] / s) : 0.f;
+      const float v = s > 0.f && s < INFINITY ? rintf((float)W[base + (int64_t)r * N] / s) : 0.f;
       q[base + (int64_t)r * N] = (int8_t)fminf(fmaxf(v, -8.f), 7.f);
     }
   }

@@ -234,3 +234,23 @@ def test_int4_tokens_that_name_an_expert_more_than_once(L, d, h, E, K, act, grou
 def test_int4_reductions_in_unequal_slices(L, d, h, E, K, act, group):
     """h / 128 without a divisor that fits: slices of n and n + 1 pieces."""
     test_int4_forward(L, d, h, E, K, act, group)
+
+
+@pytest.mark.parametrize("dt", [torch.float32, BF16])
+def test_int4_quantize_of_what_is_not_finite(dt):
+    """A NaN or an infinity shows: its group's weights are NaN, and so are the rows that meet them; others are not."""
+    E, d, h, group = 2, 128, 128, 64
+    g = torch.Generator().manual_seed(8)
+    W = torch.randn(E, d, h, generator=g)
+    W[0, 5, 7], W[0, 70, 9], W[0, 127, 11] = float("nan"), float("inf"), -float("inf")
+    W[0, 64:, 12] = float("nan")
+    ex = Int4Experts(2, d, h, E, 1, "silu", group)
+    W3 = torch.randn(E, h, d, generator=g) / 16
+    ex.quantize(W.to(dt).cuda(), None, W3.to(dt).cuda())
+    got = ex.dequantize()[0].cpu()
+    bad = torch.zeros(E, d, h, dtype=torch.bool)
+    bad[0, :64, 7] = bad[0, 64:, 9] = bad[0, 64:, 11] = bad[0, 64:, 12] = True
+    assert got[bad].isnan().all() and got[~bad].isfinite().all()
+    x = torch.randn(2, d, generator=g).to(BF16).cuda()
+    y = ex.forward(x, torch.tensor([[0], [1]], dtype=torch.int32, device="cuda"), torch.ones(2, 1, device="cuda")).cpu()
+    assert y[0].isnan().all() and y[1].isfinite().all()
