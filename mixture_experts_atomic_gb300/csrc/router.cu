@@ -264,7 +264,9 @@ __global__ void __launch_bounds__(kRThreads) router_fwd_kernel(const T* __restri
 // butterfly reduction completes; lane k of the warp then ranks token k's
 // logits (larger first, equal to the lower index) and writes its ids and
 // gates.  The x rows stream from HBM once, coalesced.
-template <typename T, int EP>
+// LG: as above (262144 x 4096, 8 experts: with a test for each token instead of
+// a variant 0.630 ms, not 0.611, for calls that want no logits)
+template <typename T, int EP, bool LG>
 __global__ void __launch_bounds__(512) router_fwd_gemv_kernel(const T* __restrict__ x, const float* __restrict__ Wr,
                                                               const float* __restrict__ bias, int64_t L, int d, int E,
                                                               int K, int32_t* __restrict__ ids,
@@ -351,7 +353,7 @@ __global__ void __launch_bounds__(512) router_fwd_gemv_kernel(const T* __restric
       float lg[EP];
 #pragma unroll
       for (int e = 0; e < EP; ++e) lg[e] = e < E ? acc[q][e] + (bias ? bias[e] : 0.f) : -FLT_MAX;
-      if (logits) {
+      if (LG) {
 #pragma unroll
         for (int e = 0; e < EP; ++e)
           if (e < E) logits[t * E + e] = lg[e];
@@ -1125,7 +1127,7 @@ moeblaze_status fwd_ep(const moeblaze_shape& s, const void* x, const float* Wr, 
   if constexpr (EP <= 16) {
     const size_t wb = ((size_t)s.d * EP + (size_t)s.d / 2) * sizeof(float);
     if (wb <= kGemvWrBytes) {
-      auto kern = router_fwd_gemv_kernel<T, EP>;
+      auto kern = logits ? router_fwd_gemv_kernel<T, EP, true> : router_fwd_gemv_kernel<T, EP, false>;
       MB_CUDA(smem_limit(kern, kGemvWrBytes));
       const int threads = 512;
       int64_t blocks = (s.L + (threads / 32) * 4 - 1) / ((threads / 32) * 4);
