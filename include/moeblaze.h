@@ -462,11 +462,17 @@ typedef struct {
  * bf16 x and y, SwiGLU or SiLU (others: MOEBLAZE_ERR_UNSUPPORTED).
  *   x        device (L,d) bf16       topk_ids device (L,K) int32: an id
  *            outside [0,E) is an empty slot and adds nothing (a token with
- *            none but empty slots gets a row of zeros)
+ *            none but empty slots gets a row of zeros), and an expert that a
+ *            token names more than once counts once for each slot
  *   gates    device (L,K) fp32       y device (L,d) bf16, overwritten
  *   ws       device moeblaze_int4_workspace_bytes(s, group) bytes
- * The weights are read once per 64 tokens and per 16 tokens of an expert
- * (again from L2, where they fit): made for L up to a few tens.  Sums
+ * d is limited by a token's row in an SM's shared memory (46208, 40320 and
+ * 31616 with groups of 128, 64 and 32), h by such a row of a 64th of it; wider
+ * ones are refused (workspace bytes 0).  The weights are read once per 64
+ * tokens and per pass (again from L2, where they fit): an expert's tokens go
+ * in passes of 16, or of as many rows of d as fit, groups of 128, 64 and 32:
+ * 16, 16 and 15 at d 2816; 12, 11 and 10 at 4096; 9, 9 and 8 at 5120; 6, 5 and
+ * 5 at 8192.  Made for L up to a few tens.  Sums
  * are fp32 in a fixed order (repeatable to the bit); the hidden activations
  * are rounded to bf16 between the two products, as the matrix instructions
  * take them. */

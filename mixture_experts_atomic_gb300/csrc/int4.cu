@@ -48,8 +48,10 @@ constexpr int kQThreads = 512;
 constexpr int kQWarps = kQThreads / 32;
 // warps that share a unit's reduction rows: 4, or 1 where a unit has few (see team_of)
 constexpr int kQTeam = 4;
-// token columns of a pass: two MMA column tiles.  An expert with more pairs is
-// passed over again, its weights read once more (from L2, where they fit):
+// token columns of a pass, at most: two MMA column tiles (fewer where as many
+// rows of the reduction's length do not fit shared memory: 12 at d 4096, group
+// 128).  An expert with more pairs is passed over again, its weights read once
+// more (from L2, where they fit):
 // three or four tiles at once spill (64 tokens at d 4096, h 14336, 8 experts:
 // 273 us against 263; 61 over 64 fine-grained experts 82 against 76).
 constexpr int kQCols = 16;
