@@ -252,9 +252,11 @@ MOEBLAZE_API moeblaze_status moeblaze_backward(const moeblaze_shape* s, const vo
  *   bias    device (E) fp32 or NULL
  *   topk_ids device (L,K) int32, overwritten: the K largest logits
  *           x[t].Wr[:,e] + bias[e], equal logits ordered by the lower expert
- *           index, slot 0 the largest
+ *           index, slot 0 the largest.  K different experts whatever the logits
+ *           hold: a NaN is above every number, -inf below (gate 0 beside others)
  *   gates   device (L,K) fp32, overwritten: the softmax over the K selected
- *           logits (they sum to 1 per token)
+ *           logits (they sum to 1 per token; NaN where a selected logit is NaN or
+ *           infinite, or all are -inf)
  * No scratch.  Ready to feed moeblaze_dispatch_build and moeblaze_forward. */
 MOEBLAZE_API moeblaze_status moeblaze_router_forward(const moeblaze_shape* s, const void* x, const float* Wr,
                                                      const float* bias, int32_t* topk_ids, float* gates,

@@ -182,6 +182,17 @@ moeblaze_status launch_int4_pack(int E, int R, int N, int group, const int8_t* q
 moeblaze_status launch_int4_dequantize(int E, int R, int N, int group, const void* packed, const void* packed_scales,
                                        void* W, cudaStream_t st);
 
+// A logit as an integer in the same order, and back: a total order, so that the
+// K largest are K different experts whatever the logits hold.  Equal logits
+// (0 and -0 too) have equal keys, -inf is above nothing, and a NaN, which a
+// comparison of floats would pass over, is above everything and reaches the
+// gates.  (An unselected slot would be an index far out of range.)
+__device__ __forceinline__ int logit_key(float v) {
+  const int i = __float_as_int(v + 0.f);
+  return i ^ ((i >> 31) & 0x7fffffff);
+}
+__device__ __forceinline__ float key_logit(int k) { return __int_as_float(k ^ ((k >> 31) & 0x7fffffff)); }
+
 // router_tc.cu: the router fused with the dispatch's first step (bf16 x, E <= 64)
 bool router_dispatch_fused(const moeblaze_shape& s);
 size_t router_dispatch_ws_bytes(const moeblaze_shape& s);

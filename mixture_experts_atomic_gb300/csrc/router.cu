@@ -18,7 +18,6 @@
 // chunks of every CTA are in flight.  The weight-gradient sums are split
 // over token ranges into per-split partials that a last kernel adds in a
 // fixed order, so every result is bitwise repeatable.
-#include <cfloat>
 #include <climits>
 
 #include "common.cuh"
@@ -194,7 +193,7 @@ __global__ void __launch_bounds__(kRThreads) router_fwd_kernel(const T* __restri
     const float b = (e < E && bias) ? bias[e] : 0.f;
 #pragma unroll
     for (int i = 0; i < Ly::RPT; ++i) {
-      acc[i][j] = e < E ? acc[i][j] + b : -FLT_MAX;
+      acc[i][j] += b;
       const int64_t t = t0 + tr * Ly::RPT + i;
       if (LG && e < E && t < L) logits[t * E + e] = acc[i][j];
     }
@@ -207,18 +206,19 @@ __global__ void __launch_bounds__(kRThreads) router_fwd_kernel(const T* __restri
   for (int i = 0; i < Ly::RPT; ++i) {
     uint32_t taken = 0;
     float selv[kMaxK];
-    int seli[kMaxK];
+    int seli[kMaxK], key[Ly::EPT];
+#pragma unroll
+    for (int j = 0; j < Ly::EPT; ++j) key[j] = logit_key(acc[i][j]);
 #pragma unroll
     for (int k = 0; k < kMaxK; ++k) {
       selv[k] = 0.f;
       seli[k] = 0;
       if (k < K) {
-        float bv = -FLT_MAX;
-        int bi = INT_MAX;
+        int bv = INT_MIN, bi = INT_MAX;
 #pragma unroll
         for (int j = 0; j < Ly::EPT; ++j) {
           const int e = j * Ly::TE + te;
-          const float a = acc[i][j];
+          const int a = key[j];
           if (!((taken >> j) & 1u) && e < E && (a > bv || (a == bv && e < bi))) {
             bv = a;
             bi = e;
@@ -226,14 +226,14 @@ __global__ void __launch_bounds__(kRThreads) router_fwd_kernel(const T* __restri
         }
 #pragma unroll
         for (int off = Ly::TE / 2; off > 0; off >>= 1) {
-          const float ov = __shfl_xor_sync(0xffffffffu, bv, off);
+          const int ov = __shfl_xor_sync(0xffffffffu, bv, off);
           const int oi = __shfl_xor_sync(0xffffffffu, bi, off);
           if (ov > bv || (ov == bv && oi < bi)) {
             bv = ov;
             bi = oi;
           }
         }
-        selv[k] = bv;
+        selv[k] = key_logit(bv);
         seli[k] = bi;
         if (bi % Ly::TE == te) taken |= 1u << (bi / Ly::TE);
       }
@@ -265,7 +265,7 @@ __global__ void __launch_bounds__(kRThreads) router_fwd_kernel(const T* __restri
 // logits (larger first, equal to the lower index) and writes its ids and
 // gates.  The x rows stream from HBM once, coalesced.
 // LG: as above (262144 x 4096, 8 experts: with a test for each token instead of
-// a variant 0.630 ms, not 0.611, for calls that want no logits)
+// a variant 0.630 ms, not 0.611, for calls that want none)
 template <typename T, int EP, bool LG>
 __global__ void __launch_bounds__(512) router_fwd_gemv_kernel(const T* __restrict__ x, const float* __restrict__ Wr,
                                                               const float* __restrict__ bias, int64_t L, int d, int E,
@@ -352,12 +352,15 @@ __global__ void __launch_bounds__(512) router_fwd_gemv_kernel(const T* __restric
       if (lane != q || t >= L) continue;
       float lg[EP];
 #pragma unroll
-      for (int e = 0; e < EP; ++e) lg[e] = e < E ? acc[q][e] + (bias ? bias[e] : 0.f) : -FLT_MAX;
+      for (int e = 0; e < EP; ++e) lg[e] = e < E ? acc[q][e] + (bias ? bias[e] : 0.f) : 0.f;
       if (LG) {
 #pragma unroll
         for (int e = 0; e < EP; ++e)
           if (e < E) logits[t * E + e] = lg[e];
       }
+      int key[EP];
+#pragma unroll
+      for (int e = 0; e < EP; ++e) key[e] = logit_key(lg[e]);
       uint32_t taken = 0;
       float selv[kMaxK], w[kMaxK], sum = 0.f;
       int seli[kMaxK];
@@ -366,15 +369,15 @@ __global__ void __launch_bounds__(512) router_fwd_gemv_kernel(const T* __restric
         selv[k] = 0.f;
         seli[k] = 0;
         if (k < K) {
-          float bv = -FLT_MAX;
-          int bi = INT_MAX;
+          // experts in ascending order: the first of the largest
+          int bv = INT_MIN, bi = __ffs(~taken) - 1;
 #pragma unroll
           for (int e = 0; e < EP; ++e)
-            if (!((taken >> e) & 1u) && e < E && (lg[e] > bv || (lg[e] == bv && e < bi))) {
-              bv = lg[e];
+            if (!((taken >> e) & 1u) && e < E && key[e] > bv) {
+              bv = key[e];
               bi = e;
             }
-          selv[k] = bv;
+          selv[k] = key_logit(bv);
           seli[k] = bi;
           taken |= 1u << bi;
         }

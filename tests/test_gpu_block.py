@@ -607,3 +607,38 @@ def test_balance_backward_mask():
         loss.backward(c[0], dl, c[4].bool())
     with pytest.raises(ValueError, match="valid: shape"):
         loss.backward(c[0], dl, c[4][:-1])
+
+
+@pytest.mark.parametrize("L,dt", [(300, BF16), (40, F32)])
+def test_block_with_tokens_that_are_not_finite(L, dt):
+    """Padding tokens that hold NaN or infinities, left out of the losses: the other tokens' rows and the losses are
+    those of a batch whose padding is finite."""
+    d, h, E, K = 128, 128, 8, 2
+    g = torch.Generator().manual_seed(41)
+    r = lambda *s: torch.randn(*s, generator=g)  # noqa: E731
+    p = {"norm_w": 1 + 0.1 * r(d), "norm_b": 0.1 * r(d), "Wr": r(d, E) / 8, "bias": 0.1 * r(E)}
+    dev = {k: v.cuda() for k, v in p.items()}
+    dev.update({k: (r(E, *s) / 11).to(dt).cuda() for k, s in (("W1", (d, h)), ("W2", (d, h)), ("W3", (h, d)))})
+    x, res, dout = (r(L, d).to(dt).cuda() for _ in range(3))
+    valid = torch.ones(L, dtype=torch.uint8, device="cuda")
+    valid[-9:] = 0
+    dout[-9:] = 0
+    dl = torch.tensor([0.01, 0.001], device="cuda")
+    on = valid.bool()
+    outs = []
+    for bad in (False, True):
+        xx = x.clone()
+        if bad:
+            xx[-1], xx[-2, 3], xx[-3, 5] = float("nan"), float("inf"), -float("inf")
+        block = MoEBlock(L, d, h, E, K, dt)
+        out, s, losses, counts = block.forward(xx, res, dev, valid)
+        grads = block.backward(dout, dl, dev)
+        assert block.layer.device_error() == 0
+        outs.append([t.clone() for t in (out[on], s[on], losses, counts, grads["x"][on])])
+    good, mixed = outs
+    assert mixed[0].isfinite().all() and mixed[4].isfinite().all()
+    for a, b in zip(good[1:4], mixed[1:4]):
+        assert torch.equal(a, b)
+    # (sums of two terms, the gate gradients by atomics: fp32 rounding, and bf16's)
+    for i in (0, 4):
+        assert (good[i].float() - mixed[i].float()).abs().max() <= 2.0 ** -7 * good[i].float().abs().max()

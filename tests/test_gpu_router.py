@@ -200,3 +200,51 @@ def test_router_then_layer_training_step(fused):
     assert O.rel_err(layer.y, y) <= 2e-2 and O.rel_err(layer.dX, dX) <= 2e-2
     assert O.rel_err(layer.dgates, dg) <= 2e-2
     assert O.rel_err(dWr, dWr_r) <= 2e-2 and O.rel_err(db, db_r) <= 2e-2 and O.rel_err(dxr, dxr_r) <= 2e-2
+
+
+@pytest.mark.parametrize("L,d,E,K,dt", [(200, 64, 8, 2, "bf16"), (300, 128, 12, 3, "bf16"), (257, 64, 33, 4, "f32"),
+                                        (300, 64, 64, 6, "bf16"), (1100, 192, 64, 8, "bf16"), (150, 64, 100, 8, "bf16"),
+                                        (140, 64, 200, 5, "f32"), (50, 64, 6, 4, "f32"), (130, 64, 3, 3, "bf16")])
+def test_router_selects_experts_whatever_the_logits_hold(L, d, E, K, dt):
+    """NaN and infinite tokens, experts masked by a bias of -inf until fewer than K are left, zeros of both signs:
+    the ids are K different experts, in the order of the kernel's own logits, and the dispatch they make is whole."""
+    from mixture_experts_atomic_gb300.layer import MoELayer
+    dtype = {"bf16": torch.bfloat16, "f32": torch.float32}[dt]
+    g = torch.Generator().manual_seed(E)
+    x = torch.randn(L, d, generator=g)
+    Wr = torch.randn(d, E, generator=g)
+    nan, inf = float("nan"), float("inf")
+    x[0, 1], x[1, 3], x[2, 5], x[4] = nan, inf, -inf, 0.0
+    x[5, 0], x[5, 1] = inf, -inf
+    x[L - 1] = nan
+    full, few = torch.randn(E, generator=g), torch.full((E,), -inf)
+    few[torch.randperm(E, generator=g)[:K - 1]] = 0.25
+    signed = torch.zeros(E)
+    signed[::2] = -0.0
+    lowest = torch.full((E,), torch.finfo(torch.float32).min)
+    xd, Wd = x.to(dtype).cuda(), Wr.cuda()
+    shape = B.make_shape(L, d, 128, E, K, dtype, "identity")
+    for bias in (None, full, few, torch.full((E,), -inf), torch.full((E,), nan), signed, lowest):
+        b = None if bias is None else bias.cuda()
+        for call in (B.router_forward, B.router_dispatch_build):
+            got = []
+            for logits in (torch.empty(L, E, device="cuda"), None):
+                ids = torch.full((L, K), -7, dtype=torch.int32, device="cuda")
+                gates = torch.empty(L, K, device="cuda")
+                call(shape, xd, Wd, b, ids, gates, logits=logits)
+                got.append((ids, gates, logits))
+            (ids, gates, lg), (ids0, gates0, _) = got
+            assert torch.equal(ids, ids0) and torch.equal(gates.view(torch.int32), gates0.view(torch.int32))
+            order = torch.sort(lg, dim=1, descending=True, stable=True).indices[:, :K]
+            assert torch.equal(ids.long(), order)
+            want = torch.softmax(torch.gather(lg.double(), 1, order), 1)
+            same = ((gates.double() - want).abs() <= 1e-5) | (gates.isnan() & want.isnan())
+            assert same.all(), (gates[~same.all(1)][:3], want[~same.all(1)][:3])
+            assert gates[0].isnan().all() and gates[L - 1].isnan().all()
+        layer = MoELayer(L, d, 0, E, K, dtype, "identity")
+        layer.route(xd, Wd, b)
+        idx, off, eids, pos = (t.cpu().long() for t in B.index_views(layer.shape, layer.disp))
+        assert layer.device_error() == 0 and int(off[-1]) == L * K
+        assert torch.equal(pos.flatten().sort().values, torch.arange(L * K))
+        assert torch.equal(off[1:] - off[:-1], torch.bincount(eids.flatten(), minlength=E))
+        assert torch.equal(idx[pos], torch.arange(L)[:, None].expand(L, K))
