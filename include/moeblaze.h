@@ -143,9 +143,11 @@ MOEBLAZE_API size_t moeblaze_backward_workspace_bytes(const moeblaze_shape* s);
  * moeblaze_dispatch_workspace_bytes(s) bytes (contents on entry ignored).
  * validate != 0: synchronise `stream` once and return
  * MOEBLAZE_ERR_BAD_ROUTING if any id is out of range or repeated within a
- * token.  With validate == 0 such ids leave the outputs unspecified (but all
- * writes stay inside the buffers) and the device error word records them
- * (see moeblaze_device_error).
+ * token.  With validate == 0 the device error word records such ids (see
+ * moeblaze_device_error); ids out of range are left out of the maps
+ * (token_index_map -1) and a repeated one is in them once, so that a forward
+ * or backward on them stays inside its buffers (its outputs for those tokens
+ * are unspecified).
  */
 MOEBLAZE_API moeblaze_status moeblaze_dispatch_build(const moeblaze_shape* s, const int32_t* topk_ids,
                                         const moeblaze_dispatch* out, void* ws, size_t ws_bytes,

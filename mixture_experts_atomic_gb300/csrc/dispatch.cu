@@ -513,12 +513,11 @@ __global__ void __launch_bounds__(kT3, KM <= 4 ? 5 : 1) scatter_kernel(int64_t L
   }
   __syncthreads();
   // expert_token_indices: the chunk's runs, one per expert, each contiguous
-  // in the output, written by consecutive threads.  A token with a repeated
-  // id leaves a staging entry unwritten, so a chunk with invalid routing
-  // skips this (its part of the output is unspecified; nothing is written
-  // outside the buffer).
-  if (!any_bad)
-    for (int j = tid; j < nstage; j += kT3) D1[delta[stage_e[j]] + j] = stage_t[j];
+  // in the output, written by consecutive threads.  Invalid routing too: every
+  // bit of the chunk's bitmap has a slot that staged it (an id out of range has
+  // no bit, the two slots of a repeated one stage the same entry), so the rows
+  // that the counts promise to the GEMMs all hold a token.
+  for (int j = tid; j < nstage; j += kT3) D1[delta[stage_e[j]] + j] = stage_t[j];
 
   // ---- GEMM metadata, split over the CTAs
   // tile -> expert: tile m belongs to the expert whose padded rows hold row

@@ -101,3 +101,45 @@ def test_validation_reports_bad_routing():
     neg[0, 0] = -3
     with pytest.raises(B.MoEBlazeError):
         layer.dispatch(neg.cuda(), validate=True)
+
+
+@pytest.mark.parametrize("L,d,h,E,K,act,dt", [(3000, 128, 128, 8, 2, "swiglu", "bf16"), (3000, 256, 0, 200, 4, "identity", "bf16"),
+                                              (130, 64, 48, 5, 3, "silu", "f32"), (70000, 128, 128, 500, 2, "silu", "bf16")])
+def test_layer_on_bad_routing_stays_inside_its_buffers(L, d, h, E, K, act, dt):
+    """Without validation ids out of range and repeated ones are recorded, the maps hold what is left, and the layer
+    runs on them: tokens whose ids are all good come out as without the bad ones."""
+    dtype = {"bf16": torch.bfloat16, "f32": torch.float32}[dt]
+    g = torch.Generator().manual_seed(L)
+    ids = torch.stack([torch.randperm(E, generator=g)[:K] for _ in range(L)]).int()
+    gates = torch.softmax(torch.randn(L, K, generator=g), 1).cuda()
+    r = lambda *s: (torch.randn(*s, generator=g) / 11).to(dtype).cuda()  # noqa: E731
+    W = (None, None, None) if act == "identity" else (r(E, d, h), r(E, d, h) if act == "swiglu" else None, r(E, h, d))
+    x, dY = r(L, d), r(L, d)
+    bad = ids.clone()
+    rows = torch.arange(0, L, 37)
+    for i, t in enumerate(rows.tolist()):
+        bad[t, i % K] = [-1, E, 2 ** 31 - 1, -2 ** 31, int(bad[t, (i + 1) % K])][i % 5]
+    left = [sorted({e for e in row if 0 <= e < E}) for row in bad.tolist()]
+    layer = MoELayer(L, d, h, E, K, dtype, act)
+    outs = []
+    for these in (ids, bad):
+        layer.disp.expert_token_indices.fill_(2 ** 31 - 1)
+        layer.dispatch(these.cuda())
+        y = layer.forward(x, gates, *W).clone()
+        dX = layer.backward(dY, x, gates, *W)[0].clone()
+        outs.append((y, dX))
+        assert layer.device_error() == (0 if these is ids else 1)
+    idx, off, _, pos = (t.cpu().long() for t in B.index_views(layer.shape, layer.disp))
+    want = [[] for _ in range(E)]
+    for t, es in enumerate(left):
+        for e in es:
+            want[e].append(t)
+    assert off[1:].sub(off[:-1]).tolist() == [len(w) for w in want]
+    assert idx[:int(off[-1])].tolist() == [t for w in want for t in w]
+    known = (bad >= 0) & (bad < E)
+    assert (pos[~known] == -1).all() and torch.equal(idx[pos[known]], torch.nonzero(known)[:, 0])
+    good = torch.ones(L, dtype=torch.bool)
+    good[rows] = False
+    for a, b in zip(*outs):
+        tol = 2.0 ** -7 if dtype == torch.bfloat16 else 1e-5
+        assert (a[good.cuda()].float() - b[good.cuda()].float()).abs().max() <= tol * a.float().abs().max()
