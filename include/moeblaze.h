@@ -68,7 +68,7 @@ typedef struct {
   int32_t d, h, E, K;
   int32_t dtype;  /* MOEBLAZE_F32 | MOEBLAZE_BF16 */
   int32_t act;    /* MOEBLAZE_SWIGLU | MOEBLAZE_SILU | MOEBLAZE_IDENTITY */
-  int32_t flags;  /* 0 or MOEBLAZE_RECOMPUTE_H; other bits: MOEBLAZE_ERR_INVALID_ARG */
+  int32_t flags;  /* 0, MOEBLAZE_RECOMPUTE_H or MOEBLAZE_CHECKPOINT_8BIT; other bits: MOEBLAZE_ERR_INVALID_ARG */
 } moeblaze_shape;
 
 /* MOEBLAZE_RECOMPUTE_H: keep no H = SiLU(A)*B (SiLU: SiLU(A)) and no
@@ -84,6 +84,20 @@ typedef struct {
  * the bf16 tolerance (SiLU is then evaluated as a/2 (1 + tanh(a/2)) with the
  * hardware tanh approximation). */
 #define MOEBLAZE_RECOMPUTE_H 1
+
+/* MOEBLAZE_CHECKPOINT_8BIT: keep A and B in 8 bits.  Applies to the bf16
+ * SwiGLU and SiLU layers, without MOEBLAZE_RECOMPUTE_H (MOEBLAZE_ERR_UNSUPPORTED
+ * for fp32 and for both flags; ignored by the identity layer, which keeps
+ * nothing).  Every 128 columns of a row share a step s = max|a| / 127, and what
+ * the backward reads in place of a is s rint(a / s); a block with a NaN or an
+ * infinity is NaN or infinite as a whole, one below 2^-100 is zero.  The
+ * forward's y is that of the default mode.  `saved` shrinks to 33/64 and holds
+ *   codes of A (int8, padded rows x h) | of B (SwiGLU) | steps of A (fp32,
+ *   padded rows x h/128) | of B
+ * (rows that belong to no token are unspecified).  The backward leaves it as
+ * it is, so that it can run again, and takes scratch for dA and dB in its
+ * place: one such scratch serves the layers of a model in turn. */
+#define MOEBLAZE_CHECKPOINT_8BIT 4
 
 /* The index structures of MoEBlaze (awesome-system-papers page, section
  * "免物化 token dispatch", data-structure table).  All device, int32,

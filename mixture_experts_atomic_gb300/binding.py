@@ -51,6 +51,8 @@ class Shape(ctypes.Structure):
 
 # moeblaze_shape.flags
 RECOMPUTE_H = 1
+CHECKPOINT_8BIT = 4
+CODE_BLOCK = 128  # columns that share a step of the 8-bit checkpoints
 
 
 class Dispatch(ctypes.Structure):
@@ -808,6 +810,17 @@ def saved_views(shape: Shape, layer: LayerBuffers, dtype):
     rows = padded_rows(shape)
     t = layer.saved[: rows * nb * h * es].view(dtype).view(nb, rows, h)
     return t[0], (t[1] if nb == 2 else None)
+
+
+def saved_codes(shape: Shape, layer: LayerBuffers):
+    """(qA, sA, qB, sB) views of the checkpoints in 8 bits (MOEBLAZE_CHECKPOINT_8BIT): codes (padded_rows, h) int8 and
+    steps (padded_rows, h/128) fp32; A stands for qA sA (qB and sB None for SiLU).  Rows of no token are unspecified."""
+    h, rows = shape.h, padded_rows(shape)
+    nb = 2 if shape.act == SWIGLU else 1
+    n = nb * rows * h
+    q = layer.saved[:n].view(torch.int8).view(nb, rows, h)
+    s = layer.saved[n:n + n // CODE_BLOCK * 4].view(torch.float32).view(nb, rows, h // CODE_BLOCK)
+    return (q[0], s[0]) + ((q[1], s[1]) if nb == 2 else (None, None))
 
 
 def meta_arrays(shape: Shape, disp: DispatchBuffers):

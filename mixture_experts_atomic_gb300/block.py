@@ -122,9 +122,10 @@ class MoEBlock:
     forward keeps what backward needs in the parts' buffers; one step is forward, then backward."""
 
     def __init__(self, L: int, d: int, h: int, E: int, K: int, dtype: torch.dtype, act: str = "swiglu",
-                 eps: float = 1e-5, device="cuda", recompute_h: bool = False):
+                 eps: float = 1e-5, device="cuda", recompute_h: bool = False, checkpoint8: bool = False):
+        """recompute_h, checkpoint8: what the layer keeps for its backward (see MoELayer)."""
         self.norm = LayerNorm(L, d, dtype, eps, device)
-        self.layer = MoELayer(L, d, h, E, K, dtype, act, device, recompute_h=recompute_h)
+        self.layer = MoELayer(L, d, h, E, K, dtype, act, device, recompute_h=recompute_h, checkpoint8=checkpoint8)
         self.loss = BalanceLoss(L, E, K, device)
         self.grad = RouterGrad(L, d, E, dtype, device)
         self.logits = torch.empty((L, E), dtype=torch.float32, device=device)

@@ -53,7 +53,11 @@ moeblaze_status check_shape(const moeblaze_shape* s) {
   if (s->act != MOEBLAZE_SWIGLU && s->act != MOEBLAZE_SILU && s->act != MOEBLAZE_IDENTITY)
     return MOEBLAZE_ERR_INVALID_ARG;
   if (s->act != MOEBLAZE_IDENTITY && s->h < 1) return MOEBLAZE_ERR_INVALID_ARG;
-  if (s->flags & ~MOEBLAZE_RECOMPUTE_H) return MOEBLAZE_ERR_INVALID_ARG;
+  if (s->flags & ~(MOEBLAZE_RECOMPUTE_H | MOEBLAZE_CHECKPOINT_8BIT)) return MOEBLAZE_ERR_INVALID_ARG;
+  // 8-bit checkpoints: not with the stages that take the saved bf16 tiles as an operand
+  if ((s->flags & MOEBLAZE_CHECKPOINT_8BIT) && s->act != MOEBLAZE_IDENTITY &&
+      (s->dtype != MOEBLAZE_BF16 || (s->flags & MOEBLAZE_RECOMPUTE_H)))
+    return MOEBLAZE_ERR_UNSUPPORTED;
   if (s->E > kMaxE || s->K > kMaxK) return MOEBLAZE_ERR_UNSUPPORTED;
   if (s->L * (int64_t)s->K + (int64_t)s->E * kRowPad >= (int64_t(1) << 31)) return MOEBLAZE_ERR_UNSUPPORTED;
   if (s->act == MOEBLAZE_IDENTITY) {
@@ -129,10 +133,15 @@ bool recompute_h(const moeblaze_shape* s) {
   return s->dtype == MOEBLAZE_BF16 && s->act != MOEBLAZE_IDENTITY && (s->flags & MOEBLAZE_RECOMPUTE_H);
 }
 
-// saved:            A | B (SwiGLU) (rows x h each); bf16 with recompute: | one fp32 gate per row
+bool checkpoint8(const moeblaze_shape* s) {
+  return s->act != MOEBLAZE_IDENTITY && (s->flags & MOEBLAZE_CHECKPOINT_8BIT);
+}
+
+// saved:            A | B (SwiGLU) (rows x h each); bf16 with recompute: | one fp32 gate per row;
+//                   8-bit checkpoints: codes of A | of B | an fp32 step per 128 codes
 // forward scratch:  H (rows x h; not when recomputed) | y32 (L x d fp32) + tile counters (bf16 only)
 // backward scratch: bf16: Hg (rows x h; not when recomputed) | dX32 (L x d fp32) + tile counters
-//                   (dA, dB overwrite the saved A, B);  fp32: dAB (rows x nb*h) | Hg (rows x h)
+//                   (dA, dB overwrite the saved A, B; 8-bit checkpoints: Hg | dA | dB | dX32);  fp32: dAB (rows x nb*h) | Hg (rows x h)
 size_t fwd_ws(const moeblaze_shape* s) {
   if (s->act == MOEBLAZE_IDENTITY) return 0;
   const int64_t rows = max_padded_rows(s->L * s->K, s->E);
@@ -144,10 +153,15 @@ size_t hg_bytes(const moeblaze_shape* s) {
   const int64_t rows = max_padded_rows(s->L * s->K, s->E);
   return recompute_h(s) ? 0 : align_up((size_t)rows * s->h * elem(s), 256);
 }
+size_t dab_bytes(const moeblaze_shape* s) {  // a multiple of 256: rows are
+  const int64_t rows = max_padded_rows(s->L * s->K, s->E);
+  return checkpoint8(s) ? (size_t)rows * nbranch(s) * s->h * 2 : 0;
+}
 size_t bwd_ws(const moeblaze_shape* s) {
   if (s->act == MOEBLAZE_IDENTITY) return 0;
   const int64_t rows = max_padded_rows(s->L * s->K, s->E);
-  if (s->dtype == MOEBLAZE_BF16) return hg_bytes(s) + align_up((size_t)s->L * s->d * 4, 256) + kSchedBytes;
+  if (s->dtype == MOEBLAZE_BF16)
+    return hg_bytes(s) + dab_bytes(s) + align_up((size_t)s->L * s->d * 4, 256) + kSchedBytes;
   return align_up((size_t)rows * nbranch(s) * s->h * elem(s), 256) + hg_bytes(s);
 }
 
@@ -206,6 +220,7 @@ size_t moeblaze_dispatch_workspace_bytes(const moeblaze_shape* s) {
 size_t moeblaze_saved_bytes(const moeblaze_shape* s) {
   if (check_shape(s) != MOEBLAZE_OK || s->act == MOEBLAZE_IDENTITY) return 0;
   const int64_t rows = max_padded_rows(s->L * s->K, s->E);
+  if (checkpoint8(s)) return (size_t)rows * nbranch(s) * (s->h + s->h / 128 * 4);
   return (size_t)rows * nbranch(s) * s->h * elem(s) + (recompute_h(s) ? (size_t)rows * 4 : 0);
 }
 
@@ -316,11 +331,12 @@ moeblaze_status moeblaze_backward(const moeblaze_shape* s, const void* dY, const
                          (float*)dW1, sw ? (float*)dW2 : nullptr, (float*)dW3, dgates, (float*)dAB, (float*)Hg, st);
   }
   // bf16: Hg (not when recomputed) | dX32; dA, dB go over the saved A, B
-  char* dX32 = w + hg_bytes(s);
+  char* dX32 = w + hg_bytes(s) + dab_bytes(s);
+  __nv_bfloat16* dAB = checkpoint8(s) ? (__nv_bfloat16*)(w + hg_bytes(s)) : nullptr;
   return tc_backward(*s, (const __nv_bfloat16*)dY, (const __nv_bfloat16*)x, gates, *disp, (const __nv_bfloat16*)W1,
                      sw ? (const __nv_bfloat16*)W2 : nullptr, (const __nv_bfloat16*)W3, (__nv_bfloat16*)saved,
                      (__nv_bfloat16*)dX, (__nv_bfloat16*)dW1, sw ? (__nv_bfloat16*)dW2 : nullptr, (__nv_bfloat16*)dW3,
-                     dgates, recompute_h(s) ? nullptr : (__nv_bfloat16*)w, (float*)dX32, st);
+                     dgates, recompute_h(s) ? nullptr : (__nv_bfloat16*)w, dAB, (float*)dX32, st);
 }
 
 moeblaze_status moeblaze_device_error(const moeblaze_shape* s, const moeblaze_dispatch* disp, int32_t* code,

@@ -120,7 +120,8 @@ moeblaze_status simt_backward(const moeblaze_shape& s, const float* dY, const fl
 
 // gemm_tc.cu (bf16 tensor-core path).  wsH / wsHg NULL selects the
 // recompute variants (MOEBLAZE_RECOMPUTE_H), which keep the row gates in
-// `saved`; the backward overwrites the saved A, B with dA, dB.
+// `saved`; the backward overwrites the saved A, B with dA, dB.  With
+// MOEBLAZE_CHECKPOINT_8BIT `saved` holds codes and dA, dB go to wsdAB.
 moeblaze_status tc_forward(const moeblaze_shape& s, const __nv_bfloat16* x, const float* gates,
                            const moeblaze_dispatch& disp, const __nv_bfloat16* W1, const __nv_bfloat16* W2,
                            const __nv_bfloat16* W3, __nv_bfloat16* y, __nv_bfloat16* saved, __nv_bfloat16* wsH,
@@ -129,7 +130,8 @@ moeblaze_status tc_backward(const moeblaze_shape& s, const __nv_bfloat16* dY, co
                             const float* gates, const moeblaze_dispatch& disp, const __nv_bfloat16* W1,
                             const __nv_bfloat16* W2, const __nv_bfloat16* W3, __nv_bfloat16* saved,
                             __nv_bfloat16* dX, __nv_bfloat16* dW1, __nv_bfloat16* dW2, __nv_bfloat16* dW3,
-                            float* dgates, __nv_bfloat16* wsHg, float* wsdX32, cudaStream_t st);
+                            float* dgates, __nv_bfloat16* wsHg, __nv_bfloat16* wsdAB, float* wsdX32,
+                            cudaStream_t st);
 
 // router.cu
 constexpr int kMaxRouterE = 256;

@@ -58,6 +58,10 @@
 // stage of the SwiGLU variants also holds the saved-B tile, so their ring
 // has 3 stages of 64 KB.
 //
+// With MOEBLAZE_CHECKPOINT_8BIT the up projection writes A and B as 8-bit
+// codes with a step for each 128 columns of a row (H is still formed from the
+// accumulators), and dH decodes them and writes dA, dB to scratch.
+//
 // Every mbarrier wait is bounded (globaltimer); on expiry the CTA records
 // kErrTimeout in the device error word, drains its own copies and MMAs with
 // bounded waits, frees TMEM and returns.
@@ -79,8 +83,11 @@ constexpr int TMEM_COLS = 512;                // two 128 x 256 fp32 accumulators
 // bf16 (64-byte swizzle), a ring of them per epilogue warp
 constexpr int EPI_BUF_BYTES = 32 * 64;
 constexpr int EPI_STAGE_BYTES = 16 * EPI_BUF_BYTES;  // 32 KB
-// Launch variants of a stage: 128-row or wide tiles.
-enum Variant : int { SINGLE = 0, WIDE = 1 };
+// Launch variants of a stage: 128-row or wide tiles; the up projection and dH
+// with checkpoints in 8 bits (MOEBLAZE_CHECKPOINT_8BIT).
+enum Variant : int { SINGLE = 0, WIDE = 1, CODES = 2, WIDE_CODES = 3 };
+__host__ __device__ constexpr bool wide_v(int v) { return (v & WIDE) != 0; }
+__host__ __device__ constexpr bool codes_v(int v) { return (v & CODES) != 0; }
 constexpr int BAR_BYTES = 512;                // mbarriers, TMEM address, abort flag, tile queue
 // Tiles are claimed dynamically: each CTA takes its first two tiles by its
 // index and every further one from a global counter, two tiles ahead of
@@ -122,7 +129,7 @@ __host__ __device__ constexpr int mma_warp(int m) { return PRODUCER_WARPS + help
 // Their TMA-store staging area stays 32 KB: two buffers a warp instead of
 // four.
 __host__ __device__ constexpr int epi_warps(int m, int v) {
-  return v == WIDE && (m == UP_SWIGLU || m == UP_SILU || m == DOWN_H || m == DX) ? 8 : 4;
+  return wide_v(v) && (m == UP_SWIGLU || m == UP_SILU || m == DOWN_H || m == DX) ? 8 : 4;
 }
 __host__ __device__ constexpr int num_threads(int m, int v = SINGLE) { return (mma_warp(m) + 1 + epi_warps(m, v)) * 32; }
 // threads that recompute the A operand of a fused stage
@@ -147,13 +154,13 @@ inline bool wide_stage(const moeblaze_shape& s, int out_rows, bool half_tail_ok)
 // stages add the saved-B tile (16 KB) to every stage and keep 3 of them;
 // wide tiles keep 3 stages of A (32 KB) + B (32 KB).  The fused stages and
 // the weight-gradient stages need no epilogue staging area.
-__host__ __device__ constexpr int a_bytes_of(int v) { return v == WIDE ? 2 * A_BYTES : A_BYTES; }
-__host__ __device__ constexpr int stages_of(int m, int v = SINGLE) { return fused_sw(m) || v == WIDE ? 3 : STAGES; }
+__host__ __device__ constexpr int a_bytes_of(int v) { return wide_v(v) ? 2 * A_BYTES : A_BYTES; }
+__host__ __device__ constexpr int stages_of(int m, int v = SINGLE) { return fused_sw(m) || wide_v(v) ? 3 : STAGES; }
 __host__ __device__ constexpr int stage_bytes_of(int m, int v = SINGLE) {
   return a_bytes_of(v) + B_MAX_BYTES + (fused_sw(m) ? A_BYTES : 0);
 }
 __host__ __device__ constexpr int epi_bytes_of(int m, int v = SINGLE) {
-  return is_fused(m) || (v == WIDE && is_wgrad(m)) ? 0 : EPI_STAGE_BYTES;
+  return is_fused(m) || (wide_v(v) && is_wgrad(m)) ? 0 : EPI_STAGE_BYTES;
 }
 __host__ __device__ constexpr int smem_bytes_of(int m, int v = SINGLE) {
   return stages_of(m, v) * stage_bytes_of(m, v) + epi_bytes_of(m, v) + 1024 + BAR_BYTES;
@@ -165,6 +172,25 @@ __host__ __device__ constexpr bool a_mn_major(int m) { return is_wgrad(m); }
 __host__ __device__ constexpr bool b_k_major(int m) { return m == DH_SWIGLU || m == DH_SILU || m == DX; }
 // columns per n-tile (per branch for the dual stages)
 __host__ __device__ constexpr int tile_n(int m) { return is_dual(m) ? 128 : 256; }
+
+// Checkpoints in 8 bits: a row's codes and, for each 128 of its columns, the
+// step they count, a 127th of the largest magnitude.
+//
+//   s = max|a| / 127     q = rint(a / s)     a~ = s q
+//
+// Signed integers rather than e4m3: on normal values the uniform step is off
+// by 0.6 % of their spread (rms), the three mantissa bits by 2.6 %.  A block
+// belongs to one epilogue thread (its row's 128 accumulator columns), which
+// reads it twice from TMEM, for the largest and for the codes: no exchange
+// between threads.  The largest is taken of the bit patterns, so a NaN counts
+// as larger than every number; it, or an infinity, makes the whole block NaN
+// or infinite.  Blocks below 2^-100 become zeros (127 / max|a| would overflow).
+struct Codes {
+  int8_t* q;
+  float* s;
+};
+constexpr int kCodeBlock = 128;
+constexpr uint32_t kCodeLeastBits = (127u - 100u) << 23;
 
 struct Params {
   CUtensorMap tmA;
@@ -192,6 +218,7 @@ struct Params {
   __nv_bfloat16* o2;
   const __nv_bfloat16* i0;
   const __nv_bfloat16* i1;
+  Codes c0, c1;     // the checkpoints A and B in 8 bits (CODES), written by the up projection and read by dH
   float* acc32;
   const __nv_bfloat16* gsrc;  // gathered tensor (x or dY), rows of gld elements
   int gld;
@@ -236,6 +263,40 @@ __device__ __forceinline__ void staged_store(StoreRing& ring, const CUtensorMap*
     bulk_commit();
   }
   ring.slot = (ring.slot + 1) % RING;
+}
+
+__device__ __forceinline__ uint32_t max_bits(uint32_t m, const uint32_t (&r)[32]) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i) m = max(m, r[i] & 0x7fffffffu);
+  return m;
+}
+// the step of a block whose largest magnitude has these bits, and what the
+// values are multiplied with to count it
+__device__ __forceinline__ float2 code_scales(uint32_t bits) {
+  const float m = __uint_as_float(bits);
+  return bits < kCodeLeastBits ? make_float2(0.f, 0.f) : make_float2(m / 127.f, 127.f / m);
+}
+// codes of four values: adding 1.5 * 2^23 rounds to an integer (ties to even)
+// and leaves it in the sum's low byte
+__device__ __forceinline__ uint32_t encode4(const float* v, float inv) {
+  uint32_t b[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) b[i] = __float_as_uint(fmaf(v[i], inv, 12582912.f));
+  return __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+}
+__device__ __forceinline__ void encode32(int8_t* q, const float* v, float inv) {
+  uint4* o = reinterpret_cast<uint4*>(q);
+  o[0] = make_uint4(encode4(v, inv), encode4(v + 4, inv), encode4(v + 8, inv), encode4(v + 12, inv));
+  o[1] = make_uint4(encode4(v + 16, inv), encode4(v + 20, inv), encode4(v + 24, inv), encode4(v + 28, inv));
+}
+// the values of 16 codes: code + 128 as the low bits of 2^23 + (code + 128)
+__device__ __forceinline__ void decode16(const uint4& u, float s, float* v) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const uint32_t b = __byte_perm(w[i / 4] ^ 0x80808080u, 0x4B000000u, 0x7440 + i % 4);
+    v[i] = (__uint_as_float(b) - 8388736.f) * s;
+  }
 }
 
 __device__ __forceinline__ void prefetch_l2(const void* p) {
@@ -427,8 +488,11 @@ __host__ __device__ constexpr bool cp_b(int m) { return is_dw3(m); }
 template <int MODE, int VAR>
 __global__ void __launch_bounds__(num_threads(MODE, VAR), 1) moe_gemm_kernel(const __grid_constant__ Params p) {
   // WIDE: 256-row weight-gradient tiles (two M=128 MMAs a k-step, one accumulator)
-  constexpr bool WIDE_T = VAR == WIDE;
+  constexpr bool WIDE_T = wide_v(VAR);
   static_assert(!WIDE_T || widenable(MODE), "stage has no wide tiles");
+  constexpr bool Q8 = codes_v(VAR);  // the checkpoints are 8-bit codes with scales
+  static_assert(!Q8 || MODE == UP_SWIGLU || MODE == UP_SILU || MODE == DH_SWIGLU || MODE == DH_SILU,
+                "stage has no checkpoints");
   constexpr int NACC = WIDE_T ? 1 : 2;  // accumulator buffers in TMEM
   constexpr int AB = a_bytes_of(VAR);   // A part of a stage
   constexpr int EW = epi_warps(MODE, VAR);                 // epilogue warps
@@ -901,6 +965,7 @@ __global__ void __launch_bounds__(num_threads(MODE, VAR), 1) moe_gemm_kernel(con
       bool valid_1 = false;
       float g_1 = 1.f;
       uint4 nA[4], nB[4];
+      float stepA[2] = {0.f, 0.f}, stepB[2] = {0.f, 0.f};  // of the tile's two blocks of codes
       if constexpr (!is_wgrad(MODE)) {
         q = t.row0 + r;
         valid = (q - t.pad0) < t.n_e;
@@ -917,7 +982,27 @@ __global__ void __launch_bounds__(num_threads(MODE, VAR), 1) moe_gemm_kernel(con
             if constexpr (MODE != DX) g_1 = gate_of(p, tok_1, t.e);
           }
         }
-        if constexpr (DH) {
+        if constexpr (DH && Q8) {
+          if (valid) {
+            const int64_t ro = (int64_t)q * p.h + t.n0;
+            const uint4* pa = reinterpret_cast<const uint4*>(p.c0.q + ro);
+            nA[0] = pa[0]; nA[1] = pa[1];
+            if constexpr (MODE == DH_SWIGLU) {
+              const uint4* pb = reinterpret_cast<const uint4*>(p.c1.q + ro);
+              nB[0] = pb[0]; nB[1] = pb[1];
+            }
+            if (t.nw > kCodeBlock) {  // the row's second line
+              prefetch_l2(p.c0.q + ro + kCodeBlock);
+              if constexpr (MODE == DH_SWIGLU) prefetch_l2(p.c1.q + ro + kCodeBlock);
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const int64_t so = (ro + (i * kCodeBlock < t.nw ? i * kCodeBlock : 0)) / kCodeBlock;
+              stepA[i] = p.c0.s[so];
+              if constexpr (MODE == DH_SWIGLU) stepB[i] = p.c1.s[so];
+            }
+          }
+        } else if constexpr (DH) {
           if (valid) {
             const uint4* pa = reinterpret_cast<const uint4*>(p.i0 + (int64_t)q * p.h + t.n0);
 #pragma unroll
@@ -958,7 +1043,48 @@ __global__ void __launch_bounds__(num_threads(MODE, VAR), 1) moe_gemm_kernel(con
             const uint32_t tb = tbase + hm * 256;
             const int wr = wrow0 + hm * BM;
             const bool vr = hm == 0 ? valid : (q + BM - t.pad0) < t.n_e;
-            if constexpr (MODE == UP_SWIGLU) {
+            if constexpr (Q8) {
+              // blocks of 128 columns: one of A and one of B (SwiGLU), or up to two of A
+              constexpr bool SW = MODE == UP_SWIGLU;
+              const int64_t row = q + hm * BM;
+              for (int blk = 0; blk < t.nw / kCodeBlock; ++blk) {
+                const uint32_t ta = tb + blk * kCodeBlock;
+                const int64_t at = row * p.h + t.n0 + blk * kCodeBlock;
+                uint32_t ma = 0u, mb = 0u;
+#pragma unroll 1
+                for (int c = 0; c < kCodeBlock / 32; ++c) {
+                  MB_TMEM_LD32(ta + 32 * c, ra);
+                  if constexpr (SW) MB_TMEM_LD32(ta + kCodeBlock + 32 * c, rb);
+                  tmem_wait_ld();
+                  ma = max_bits(ma, ra);
+                  if constexpr (SW) mb = max_bits(mb, rb);
+                }
+                const float2 sa = code_scales(ma), sb = code_scales(mb);
+                if (vr) {
+                  p.c0.s[at / kCodeBlock] = sa.x;
+                  if constexpr (SW) p.c1.s[at / kCodeBlock] = sb.x;
+                }
+#pragma unroll 1
+                for (int c = 0; c < kCodeBlock / 32; ++c) {
+                  MB_TMEM_LD32(ta + 32 * c, ra);
+                  if constexpr (SW) MB_TMEM_LD32(ta + kCodeBlock + 32 * c, rb);
+                  tmem_wait_ld();
+#pragma unroll
+                  for (int i = 0; i < 32; ++i) {
+                    va[i] = __uint_as_float(ra[i]);
+                    if constexpr (SW) vb[i] = __uint_as_float(rb[i]);
+                  }
+                  if (vr) {  // (dH reads the codes of routed rows only)
+                    encode32(p.c0.q + at + 32 * c, va, sa.y);
+                    if constexpr (SW) encode32(p.c1.q + at + 32 * c, vb, sb.y);
+                  }
+                  // H for the down projection, of the values themselves
+#pragma unroll
+                  for (int i = 0; i < 32; ++i) va[i] = va[i] * fast_sigmoid(va[i]) * (SW ? vb[i] : 1.f);
+                  staged_store<ER>(ring, &p.tmO2, t.n0 + blk * kCodeBlock + 32 * c, wr, va, vr, lane);
+                }
+              }
+            } else if constexpr (MODE == UP_SWIGLU) {
               for (int c = 0; c < t.nw / 32; ++c) {
                 MB_TMEM_LD32(tb + 32 * c, ra);
                 MB_TMEM_LD32(tb + 128 + 32 * c, rb);
@@ -1022,29 +1148,44 @@ __global__ void __launch_bounds__(num_threads(MODE, VAR), 1) moe_gemm_kernel(con
           const int64_t ro = (int64_t)q * p.h + t.n0;              // A, B rows
           const int nch = t.nw / 32;
           float dgp = 0.f;  // this tile's part of <H_row, dY W3^T> = <dY, Y_row>
+          constexpr int NW = Q8 ? 2 : 4;  // 16-byte words of a chunk
+          auto chunk = [&](const __nv_bfloat16* v, const Codes& q8, int c) {
+            return Q8 ? reinterpret_cast<const uint4*>(q8.q + ro + 32 * c) : reinterpret_cast<const uint4*>(v + ro + 32 * c);
+          };
           for (int c = 0; c < nch; ++c) {
             // chunk c of A (B) was loaded one step ahead; start loading chunk c+1
             uint4 cA[4], cB[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < NW; ++i) {
               cA[i] = nA[i];
               if constexpr (SW) cB[i] = nB[i];
             }
             if (valid && c + 1 < nch) {
-              const uint4* pa = reinterpret_cast<const uint4*>(p.i0 + ro + 32 * (c + 1));
+              const uint4* pa = chunk(p.i0, p.c0, c + 1);
 #pragma unroll
-              for (int i = 0; i < 4; ++i) nA[i] = pa[i];
+              for (int i = 0; i < NW; ++i) nA[i] = pa[i];
               if constexpr (SW) {
-                const uint4* pb = reinterpret_cast<const uint4*>(p.i1 + ro + 32 * (c + 1));
+                const uint4* pb = chunk(p.i1, p.c1, c + 1);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) nB[i] = pb[i];
+                for (int i = 0; i < NW; ++i) nB[i] = pb[i];
               }
             }
             MB_TMEM_LD32(tbase + 32 * c, ra);
             tmem_wait_ld();
             float A[32], B[32], dA[32], dB[32], Hg[32];
-            unpack_row32(cA, A);
-            if constexpr (SW) unpack_row32(cB, B);
+            if constexpr (Q8) {
+              const float sa = c < 4 ? stepA[0] : stepA[1];
+              decode16(cA[0], sa, A);
+              decode16(cA[1], sa, A + 16);
+              if constexpr (SW) {
+                const float sb = c < 4 ? stepB[0] : stepB[1];
+                decode16(cB[0], sb, B);
+                decode16(cB[1], sb, B + 16);
+              }
+            } else {
+              unpack_row32(cA, A);
+              if constexpr (SW) unpack_row32(cB, B);
+            }
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
               const float dH = g * __uint_as_float(ra[i]);
@@ -1151,6 +1292,16 @@ float* saved_row_gates(const __nv_bfloat16* saved, const moeblaze_shape& s) {
   return reinterpret_cast<float*>(const_cast<__nv_bfloat16*>(saved) + (int64_t)nb * rows * s.h);
 }
 
+// MOEBLAZE_CHECKPOINT_8BIT: the saved buffer is the codes of A | of B (SwiGLU) | A's steps | B's steps
+void saved_codes(void* saved, const moeblaze_shape& s, Codes* a, Codes* b) {
+  const int64_t rows = max_padded_rows(s.L * s.K, s.E), n = rows * s.h, ns = n / kCodeBlock;
+  const int nb = s.act == MOEBLAZE_SWIGLU ? 2 : 1;
+  int8_t* q = reinterpret_cast<int8_t*>(saved);
+  float* steps = reinterpret_cast<float*>(q + nb * n);
+  *a = Codes{q, steps};
+  *b = nb == 2 ? Codes{q + n, steps + ns} : Codes{nullptr, nullptr};
+}
+
 Params base_params(const moeblaze_shape& s, const moeblaze_dispatch& disp, const float* gates) {
   Params p;
   memset(&p, 0, sizeof(p));
@@ -1193,6 +1344,7 @@ moeblaze_status tc_forward(const moeblaze_shape& s, const __nv_bfloat16* x, cons
                            float* wsY32, cudaStream_t st) {
   const bool sw = s.act == MOEBLAZE_SWIGLU;
   const bool rec = wsH == nullptr;  // MOEBLAZE_RECOMPUTE_H: no H temporary; the row gates are kept in saved
+  const bool q8 = s.flags & MOEBLAZE_CHECKPOINT_8BIT;
   const int64_t LK = s.L * s.K;
   const int64_t rows = max_padded_rows(LK, s.E);
   const int64_t mt_bound = rows / BM;
@@ -1217,14 +1369,23 @@ moeblaze_status tc_forward(const moeblaze_shape& s, const __nv_bfloat16* x, cons
       p.o0 = A; p.o1 = B; p.o2 = wsH;
       p.sched = sched + 0;
       const CUtensorMapSwizzle s64 = CU_TENSOR_MAP_SWIZZLE_64B;
-      if (!make_map(&p.tmO0, A, s.h, rows, 32, 32, s64)) return MOEBLAZE_ERR_CUDA;
-      if (sw && !make_map(&p.tmO1, B, s.h, rows, 32, 32, s64)) return MOEBLAZE_ERR_CUDA;
+      if (q8) {
+        saved_codes(saved, s, &p.c0, &p.c1);
+      } else {
+        if (!make_map(&p.tmO0, A, s.h, rows, 32, 32, s64)) return MOEBLAZE_ERR_CUDA;
+        if (sw && !make_map(&p.tmO1, B, s.h, rows, 32, 32, s64)) return MOEBLAZE_ERR_CUDA;
+      }
       if (!rec && !make_map(&p.tmO2, wsH, s.h, rows, 32, 32, s64)) return MOEBLAZE_ERR_CUDA;
       // long reductions with many tiles: 256-row tiles (pairs of 128-row tiles of one expert)
       const int64_t nt = mt_bound * p.n_tiles;
       const bool wide = wide_rows(p.kblocks, nt);
-      moeblaze_status r = sw ? (wide ? launch<UP_SWIGLU, WIDE>(p, nt / 2, st) : launch<UP_SWIGLU>(p, nt, st))
-                             : (wide ? launch<UP_SILU, WIDE>(p, nt / 2, st) : launch<UP_SILU>(p, nt, st));
+      moeblaze_status r;
+      if (q8)
+        r = sw ? (wide ? launch<UP_SWIGLU, WIDE_CODES>(p, nt / 2, st) : launch<UP_SWIGLU, CODES>(p, nt, st))
+               : (wide ? launch<UP_SILU, WIDE_CODES>(p, nt / 2, st) : launch<UP_SILU, CODES>(p, nt, st));
+      else
+        r = sw ? (wide ? launch<UP_SWIGLU, WIDE>(p, nt / 2, st) : launch<UP_SWIGLU>(p, nt, st))
+               : (wide ? launch<UP_SILU, WIDE>(p, nt / 2, st) : launch<UP_SILU>(p, nt, st));
       if (r != MOEBLAZE_OK) return r;
     }
     stage_event(1, st);
@@ -1257,20 +1418,24 @@ moeblaze_status tc_backward(const moeblaze_shape& s, const __nv_bfloat16* dY, co
                             const float* gates, const moeblaze_dispatch& disp, const __nv_bfloat16* W1,
                             const __nv_bfloat16* W2, const __nv_bfloat16* W3, __nv_bfloat16* saved,
                             __nv_bfloat16* dX, __nv_bfloat16* dW1, __nv_bfloat16* dW2, __nv_bfloat16* dW3,
-                            float* dgates, __nv_bfloat16* wsHg, float* wsdX32, cudaStream_t st) {
+                            float* dgates, __nv_bfloat16* wsHg, __nv_bfloat16* wsdAB, float* wsdX32,
+                            cudaStream_t st) {
   // The saved A and B are read for the last time by the dH GEMM, which reads
   // and writes the same (row, column) positions, so its dA and dB overwrite
   // them in place and the dX and dW1|dW2 GEMMs read them from there.
   // Default: dH also stores Hg (scratch) for the dW3 GEMM, which runs last.
   // MOEBLAZE_RECOMPUTE_H (wsHg NULL): dW3 runs first, recomputing
   // Hg = g SiLU(A) B from the saved A, B and the row gates the forward kept.
+  // MOEBLAZE_CHECKPOINT_8BIT: the codes stay as they are, and dA and dB, which
+  // are bf16, have scratch of their own (wsdAB).
+  const bool q8 = s.flags & MOEBLAZE_CHECKPOINT_8BIT;
   const bool rec = wsHg == nullptr;
   const bool sw = s.act == MOEBLAZE_SWIGLU;
   const int64_t LK = s.L * s.K;
   const int64_t rows = max_padded_rows(LK, s.E);
   const int64_t mt_bound = rows / BM;
-  __nv_bfloat16* A = saved;                                  // A, then dA
-  __nv_bfloat16* B = sw ? saved + rows * s.h : nullptr;      // B, then dB
+  __nv_bfloat16* A = q8 ? wsdAB : saved;                 // A, then dA
+  __nv_bfloat16* B = sw ? A + rows * s.h : nullptr;      // B, then dB
   // dX32 and, behind it, the tile counters of the four launches start at zero
   const size_t dx32_bytes = (sizeof(float) * s.L * s.d + 255) / 256 * 256;
   unsigned long long* sched = reinterpret_cast<unsigned long long*>(reinterpret_cast<char*>(wsdX32) + dx32_bytes);
@@ -1311,6 +1476,7 @@ moeblaze_status tc_backward(const moeblaze_shape& s, const __nv_bfloat16* dY, co
     p.ksplit = p.kblocks;
     p.n_tiles = (s.h + 255) / 256;
     p.o1 = wsHg; p.i0 = A; p.i1 = B;
+    if (q8) saved_codes(saved, s, &p.c0, &p.c1);
     p.dg = dgates;
     p.sched = sched + 0;
     const CUtensorMapSwizzle s64 = CU_TENSOR_MAP_SWIZZLE_64B;
@@ -1318,7 +1484,8 @@ moeblaze_status tc_backward(const moeblaze_shape& s, const __nv_bfloat16* dY, co
     if (sw && !make_map(&p.tmO2, B, s.h, rows, 32, 32, s64)) return MOEBLAZE_ERR_CUDA;
     if (!rec && !make_map(&p.tmO1, wsHg, s.h, rows, 32, 32, s64)) return MOEBLAZE_ERR_CUDA;
     const int64_t nt = mt_bound * p.n_tiles;
-    moeblaze_status r = sw ? launch<DH_SWIGLU>(p, nt, st) : launch<DH_SILU>(p, nt, st);
+    moeblaze_status r = q8 ? (sw ? launch<DH_SWIGLU, CODES>(p, nt, st) : launch<DH_SILU, CODES>(p, nt, st))
+                           : (sw ? launch<DH_SWIGLU>(p, nt, st) : launch<DH_SILU>(p, nt, st));
     if (r != MOEBLAZE_OK) return r;
   }
   stage_event(ev++, st);

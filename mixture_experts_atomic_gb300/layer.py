@@ -13,10 +13,16 @@ from . import binding as B
 
 class MoELayer:
     def __init__(self, L: int, d: int, h: int, E: int, K: int, dtype: torch.dtype, act: str, device="cuda",
-                 with_dgates: bool = True, recompute_h: bool = False):
+                 with_dgates: bool = True, recompute_h: bool = False, checkpoint8: bool = False):
         """recompute_h: keep no H / Hg temporaries (MOEBLAZE_RECOMPUTE_H):
-        smaller scratch, the down projection and dW3 recompute them."""
-        self.shape = B.make_shape(L, d, h, E, K, dtype, act, B.RECOMPUTE_H if recompute_h else 0)
+        smaller scratch, the down projection and dW3 recompute them.
+        checkpoint8: keep A and B in 8 bits (MOEBLAZE_CHECKPOINT_8BIT): half
+        the bytes between forward and backward; the backward's scratch grows
+        by dA and dB.  bf16 without recompute_h."""
+        flags = (B.RECOMPUTE_H if recompute_h else 0) | (B.CHECKPOINT_8BIT if checkpoint8 else 0)
+        self.shape = B.make_shape(L, d, h, E, K, dtype, act, flags)
+        if checkpoint8 and act != "identity" and (recompute_h or dtype != torch.bfloat16):
+            raise ValueError("checkpoint8: needs bfloat16, without recompute_h")
         self.L, self.d, self.h, self.E, self.K = L, d, h, E, K
         self.dtype, self.act, self.device = dtype, act, device
         self.disp = B.alloc_dispatch(self.shape, device)
@@ -33,8 +39,10 @@ class MoELayer:
             self.dW3 = torch.empty((E, h, d), dtype=dtype, device=device)
 
     @classmethod
-    def for_config(cls, cfg, device="cuda", with_dgates: bool = True, recompute_h: bool = False):
-        return cls(cfg.L, cfg.d, cfg.h, cfg.E, cfg.K, cfg.torch_dtype, cfg.act, device, with_dgates, recompute_h)
+    def for_config(cls, cfg, device="cuda", with_dgates: bool = True, recompute_h: bool = False,
+                   checkpoint8: bool = False):
+        return cls(cfg.L, cfg.d, cfg.h, cfg.E, cfg.K, cfg.torch_dtype, cfg.act, device, with_dgates, recompute_h,
+                   checkpoint8)
 
     def dispatch(self, ids: torch.Tensor, validate: bool = False):
         B.dispatch_build(self.shape, ids, self.disp, validate=validate)
@@ -72,8 +80,11 @@ class MoELayer:
         self.backward(inp["dY"], inp["x"], inp["gates"], inp.get("W1"), inp.get("W2"), inp.get("W3"))
 
     def saved(self):
+        """(A, B), or with checkpoint8 the codes and steps (qA, sA, qB, sB)."""
         if self.act == "identity":
             return None, None
+        if self.shape.flags & B.CHECKPOINT_8BIT:
+            return B.saved_codes(self.shape, self.bufs)
         return B.saved_views(self.shape, self.bufs, self.dtype)
 
     def device_error(self) -> int:

@@ -1,0 +1,107 @@
+"""Definitions in fp64 of the operators in 8 bits, and bounds on what a kernel
+may be off (imported by the tests; shares nothing with the CUDA path).  All of
+it runs on whatever device its tensors are on."""
+from __future__ import annotations
+
+import torch
+
+U32 = 2.0 ** -24                                    # half a step of fp32, relative
+HALF = {torch.float32: 2.0 ** -24, torch.bfloat16: 2.0 ** -8, torch.float8_e4m3fn: 2.0 ** -4}
+BF = HALF[torch.bfloat16]
+
+
+def inside(got, want, tol, what):
+    """|got - want| <= tol elementwise (NaN fails), with the worst place in the message."""
+    got = got.detach().to(want.device).double()
+    bad = ~((got - want).abs() <= tol)
+    if bad.any():
+        i = tuple(torch.nonzero(bad)[0].tolist())
+        over = ((got - want).abs() / tol)[bad].max()
+        raise AssertionError(f"{what}: {int(bad.sum())} of {bad.numel()} outside, first at {i}: got {got[i]:.9g}, want "
+                             f"{want[i]:.9g}; worst {over:.3g} of the tolerance")
+
+
+def matmul_err(n):
+    """Relative to the sum of the terms' sizes: a sum of n products in fp32, each step off by a step at most (the tensor
+    memory truncates), and the products' own factors."""
+    return 2.0 * (n + 16) * U32
+
+
+def silu(a):
+    return a / (1.0 + torch.exp(-a))
+
+
+def layer_forward(x, ids, gates, W1, W2, W3):
+    """y of the bf16 layer and a bound on |y - kernel| before y's rounding: the hidden activations are rounded to bf16
+    once, everything else is fp32."""
+    x, gates = x.double(), gates.double()
+    L, K = ids.shape
+    E, d, h = W1.shape
+    y = torch.zeros(L, d, dtype=torch.float64, device=x.device)
+    bound = torch.zeros_like(y)
+    for e in range(E):
+        t, k = torch.nonzero(ids == e, as_tuple=True)
+        if t.numel() == 0:
+            continue
+        w1, w3 = W1[e].double(), W3[e].double()
+        a, aa = x[t] @ w1, x[t].abs() @ w1.abs()
+        hid, err = silu(a), 1.1 * aa * matmul_err(d)        # |silu'| <= 1.1
+        if W2 is not None:
+            w2 = W2[e].double()
+            b, ba = x[t] @ w2, x[t].abs() @ w2.abs()
+            err = err * b.abs() + hid.abs() * ba * matmul_err(d)
+            hid = hid * b
+        # (the sigmoid's fast exponential: a few steps of fp32, and |a| of them in the exponent)
+        herr = BF * hid.abs() + err + (16 + 4 * a.abs()) * U32 * hid.abs()
+        g = gates[t, k][:, None]
+        y.index_add_(0, t, g * (hid @ w3))
+        bound.index_add_(0, t, g.abs() * (herr @ w3.abs() + matmul_err(h) * (hid.abs() @ w3.abs())))
+    return y, bound
+
+
+def layer_backward(dY, x, ids, gates, W1, W2, W3, A, B):
+    """Gradients of the layer evaluated at the checkpoints A, B, per expert lists of (rows of e, h) values in the order
+    of torch.nonzero(ids == e), and bounds on what the kernels may be off before the outputs' own rounding: dA, dB and
+    g H are rounded to bf16 on their way between products."""
+    dY, x, gates = dY.double(), x.double(), gates.double()
+    L, K = ids.shape
+    E, d, h = W1.shape
+    out = {"dX": torch.zeros(L, d, dtype=torch.float64, device=x.device),
+           "dgates": torch.zeros(L, K, dtype=torch.float64, device=x.device)}
+    for n, w in (("dW1", W1), ("dW2", W2), ("dW3", W3)):
+        if w is not None:
+            out[n] = torch.zeros(w.shape, dtype=torch.float64, device=x.device)
+    tol = {n: torch.zeros_like(v) for n, v in out.items()}
+    for e in range(E):
+        t, k = torch.nonzero(ids == e, as_tuple=True)
+        if t.numel() == 0:
+            continue
+        w1, w3 = W1[e].double(), W3[e].double()
+        xe, dy, g = x[t], dY[t], gates[t, k][:, None]
+        a = A[e]
+        b = B[e] if W2 is not None else torch.ones_like(a)
+        fast = (16 + 4 * a.abs()) * U32                     # relative, of the sigmoid and what is formed from it
+        sig = 1.0 / (1.0 + torch.exp(-a))
+        act, slope = a * sig, sig * (1.0 + a * (1.0 - sig))
+        slope_size = sig * (1.0 + a.abs())
+        up, upa = dy @ w3.t(), dy.abs() @ w3.abs().t()
+        uerr = upa * matmul_err(d)
+        hid = act * b
+        out["dgates"][t, k] = (hid * up).sum(1)
+        tol["dgates"][t, k] = (hid.abs() * (uerr + (fast + h * U32) * up.abs())).sum(1) + 1e-30
+        gh = g * hid
+        out["dW3"][e] = gh.t() @ dy
+        tol["dW3"][e] = ((BF + fast) * gh.abs()).t() @ dy.abs() + matmul_err(len(t)) * (gh.abs().t() @ dy.abs())
+        dh, derr = g * up, g.abs() * uerr
+        da = dh * b * slope
+        daerr = BF * da.abs() + b.abs() * slope_size * (derr + fast * dh.abs())
+        parts = [("dW1", w1, da, daerr)]
+        if W2 is not None:
+            db = dh * act
+            parts.append(("dW2", W2[e].double(), db, BF * db.abs() + act.abs() * (derr + fast * dh.abs())))
+        for n, w, v, verr in parts:
+            out[n][e] = xe.t() @ v
+            tol[n][e] = xe.abs().t() @ verr + matmul_err(len(t)) * (xe.abs().t() @ v.abs())
+            out["dX"].index_add_(0, t, v @ w.t())
+            tol["dX"].index_add_(0, t, verr @ w.abs().t() + matmul_err(2 * h) * (v.abs() @ w.abs().t()))
+    return out, tol
