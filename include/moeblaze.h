@@ -440,6 +440,45 @@ MOEBLAZE_API moeblaze_status moeblaze_layernorm_backward(const moeblaze_shape* s
                                                          const void* dsum, void* dx, float* dweight, float* dbias,
                                                          void* ws, size_t ws_bytes, moeblaze_stream stream);
 
+/* ------------------------------------------------- root-mean-square norm
+ * The layer norm's sibling without mean and bias, with the residual sum and,
+ * where asked for, its rows in 8-bit floating point, and its backward.  Shape
+ * fields used: L, d, dtype (any d from 1 to 2^24; with q a multiple of 16,
+ * MOEBLAZE_ERR_UNSUPPORTED otherwise).
+ *   s = x (+ residual);  rstd = 1/sqrt(mean(s^2) + eps) of each row
+ *   y = s rstd weight
+ * in fp32, each output rounded once.
+ *   x, residual, sum  as moeblaze_layernorm_forward
+ *   weight       device (d) fp32, 16-byte aligned
+ *   y            device (L,d) dtype; NULL when only q is wanted
+ *   rstd         device (L) fp32
+ *   q, q_scales  device (L,d) e4m3 and (L, ceil(d/128)) fp32, or both NULL: y
+ *                in 8-bit rows (moeblaze_fp8_quantize_rows) of the fp32 values
+ * moeblaze_rmsnorm_backward: as moeblaze_layernorm_backward, of
+ *   dx = rstd (g - xh mean(g xh)) (+ dsum),  g = dy weight,  xh = s rstd
+ *   dweight = sum over the rows of dy xh, in a fixed order */
+MOEBLAZE_API moeblaze_status moeblaze_rmsnorm_forward(const moeblaze_shape* s, const void* x, const void* residual,
+                                                      const float* weight, float eps, void* sum, void* y, float* rstd,
+                                                      void* q, float* q_scales, moeblaze_stream stream);
+MOEBLAZE_API size_t moeblaze_rmsnorm_backward_workspace_bytes(const moeblaze_shape* s);
+MOEBLAZE_API moeblaze_status moeblaze_rmsnorm_backward(const moeblaze_shape* s, const void* dy, const void* sum,
+                                                       const float* rstd, const float* weight, const void* dsum,
+                                                       void* dx, float* dweight, void* ws, size_t ws_bytes,
+                                                       moeblaze_stream stream);
+
+/* ------------------------------------------------- rows in 8-bit floating point
+ * e4m3 rows with an fp32 scale for each 128 of their columns (the last block
+ * of a row may have fewer):
+ *   scale = 2^ceil(log2(max|x| / 448)), at least 2^-126    q = e4m3(x / scale)
+ * to nearest, ties to even; a block with a NaN or an infinity gets a scale of
+ * NaN.  dequantize takes any scales.
+ *   x device (L,d) dtype    q device (L,d) e4m3    scales device (L, ceil(d/128)) fp32
+ * d is a multiple of 16 (MOEBLAZE_ERR_UNSUPPORTED otherwise). */
+MOEBLAZE_API moeblaze_status moeblaze_fp8_quantize_rows(int64_t L, int32_t d, int32_t dtype, const void* x, void* q,
+                                                        float* scales, moeblaze_stream stream);
+MOEBLAZE_API moeblaze_status moeblaze_fp8_dequantize_rows(int64_t L, int32_t d, int32_t dtype, const void* q,
+                                                          const float* scales, void* x, moeblaze_stream stream);
+
 /* ------------------------------------------------- experts on 4-bit weights
  * The layer's forward for few tokens (serving) on 4-bit weights with a scale
  * for each group of reduction rows:

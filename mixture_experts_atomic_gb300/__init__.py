@@ -4,4 +4,4 @@ gather-fused tcgen05 expert GEMMs and fused combine, behind a C ABI.
 The compute path lives in ``libmoeblaze.so`` (built from ``csrc/``); the
 Python side (``binding``) only marshals pointers, sizes and streams.
 """
-__all__ = ["binding", "block", "inputs", "int4", "layer"]
+__all__ = ["binding", "block", "fp8", "inputs", "int4", "layer"]

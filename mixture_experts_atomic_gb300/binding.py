@@ -38,6 +38,8 @@ EXPORTS = [
     "moeblaze_layernorm_backward", "moeblaze_layernorm_backward_workspace_bytes", "moeblaze_int4_weight_bytes",
     "moeblaze_int4_scale_bytes", "moeblaze_int4_quantize", "moeblaze_int4_pack", "moeblaze_int4_dequantize",
     "moeblaze_int4_workspace_bytes", "moeblaze_int4_forward", "moeblaze_balance_backward_masked",
+    "moeblaze_rmsnorm_forward", "moeblaze_rmsnorm_backward", "moeblaze_rmsnorm_backward_workspace_bytes",
+    "moeblaze_fp8_quantize_rows", "moeblaze_fp8_dequantize_rows",
 ]
 
 # fixed scratch of moeblaze_dispatch_build_static (MOEBLAZE_STATIC_SCRATCH_BYTES)
@@ -114,13 +116,17 @@ def lib():
         L.moeblaze_balance_backward_masked.argtypes = [SP, P, P, P, P, P, P, P, P, ctypes.c_int32, P, P]
         L.moeblaze_layernorm_forward.argtypes = [SP, P, P, P, P, ctypes.c_float, P, P, P, P, P]
         L.moeblaze_layernorm_backward.argtypes = [SP, P, P, P, P, P, P, P, P, P, P, sz, P]
+        L.moeblaze_rmsnorm_forward.argtypes = [SP, P, P, P, ctypes.c_float, P, P, P, P, P, P]
+        L.moeblaze_rmsnorm_backward.argtypes = [SP, P, P, P, P, P, P, P, P, sz, P]
         i32 = ctypes.c_int32
+        for n in ["moeblaze_fp8_quantize_rows", "moeblaze_fp8_dequantize_rows"]:
+            getattr(L, n).argtypes = [ctypes.c_int64, i32, i32, P, P, P, P]
         L.moeblaze_int4_quantize.argtypes = [i32, i32, i32, i32, i32, P, P, P, P]
         L.moeblaze_int4_pack.argtypes = [i32, i32, i32, i32, P, P, P, P, P]
         L.moeblaze_int4_dequantize.argtypes = [i32, i32, i32, i32, P, P, P, P]
         L.moeblaze_int4_forward.argtypes = [SP, P, P, P, ctypes.POINTER(Int4Weights), P, P, sz, P]
         for n in ["moeblaze_router_backward_logits_workspace_bytes", "moeblaze_balance_workspace_bytes",
-                  "moeblaze_layernorm_backward_workspace_bytes"]:
+                  "moeblaze_layernorm_backward_workspace_bytes", "moeblaze_rmsnorm_backward_workspace_bytes"]:
             getattr(L, n).argtypes = [SP]
             getattr(L, n).restype = sz
         L.moeblaze_int4_workspace_bytes.argtypes = [SP, i32]
@@ -268,6 +274,28 @@ def moeblaze_layernorm_backward(shape, dy, sum, mean, rstd, weight, dsum, dx, dw
                                 stream) -> int:
     return lib().moeblaze_layernorm_backward(ctypes.byref(shape), dy, sum, mean, rstd, weight, dsum, dx, dweight,
                                              dbias, ws, ws_bytes, stream)
+
+
+def moeblaze_rmsnorm_forward(shape, x, residual, weight, eps, sum, y, rstd, q, q_scales, stream) -> int:
+    return lib().moeblaze_rmsnorm_forward(ctypes.byref(shape), x, residual, weight, eps, sum, y, rstd, q, q_scales,
+                                          stream)
+
+
+def moeblaze_rmsnorm_backward_workspace_bytes(shape: Shape) -> int:
+    return lib().moeblaze_rmsnorm_backward_workspace_bytes(ctypes.byref(shape))
+
+
+def moeblaze_rmsnorm_backward(shape, dy, sum, rstd, weight, dsum, dx, dweight, ws, ws_bytes, stream) -> int:
+    return lib().moeblaze_rmsnorm_backward(ctypes.byref(shape), dy, sum, rstd, weight, dsum, dx, dweight, ws, ws_bytes,
+                                           stream)
+
+
+def moeblaze_fp8_quantize_rows(L, d, dtype, x, q, scales, stream) -> int:
+    return lib().moeblaze_fp8_quantize_rows(L, d, dtype, x, q, scales, stream)
+
+
+def moeblaze_fp8_dequantize_rows(L, d, dtype, q, scales, x, stream) -> int:
+    return lib().moeblaze_fp8_dequantize_rows(L, d, dtype, q, scales, x, stream)
 
 
 def moeblaze_int4_weight_bytes(E: int, R: int, N: int) -> int:
@@ -717,6 +745,81 @@ def layernorm_backward(shape: Shape, dy, sum, mean, rstd, weight, dsum, dx, dwei
     st = moeblaze_layernorm_backward(shape, _ptr(dy), _ptr(sum), _ptr(mean), _ptr(rstd), _ptr(weight), _ptr(dsum),
                                      _ptr(dx), _ptr(dweight), _ptr(dbias), _ptr(ws), n, _stream(stream))
     _check(st, "moeblaze_layernorm_backward")
+
+
+def rmsnorm_forward(shape: Shape, x, residual, weight, eps, sum, y, rstd, q=None, q_scales=None, stream=None, own=False):
+    """Root-mean-square norm of x (+ residual): fills rstd (L) fp32, y (L,d) (None: only with q), unless None sum (L,d)
+    and, unless None, q (L,d) float8_e4m3fn with q_scales (L, ceil(d/128)) fp32.
+    own: the outputs are buffers made for this shape on rstd's device, and only rstd is looked at again."""
+    dt, L, d = _TORCH_DTYPE[shape.dtype], shape.L, shape.d
+    specs = ((x, "x", (L, d), dt, False), (residual, "residual", (L, d), dt, True),
+             (weight, "weight", (d,), torch.float32, False), (rstd, "rstd", (L,), torch.float32, False))
+    if not own:
+        specs += ((sum, "sum", (L, d), dt, True), (y, "y", (L, d), dt, q is not None),
+                  (q, "q", (L, d), torch.float8_e4m3fn, True),
+                  (q_scales, "q_scales", (L, blocks8(d)), torch.float32, q is None))
+    _args(*specs)
+    st = moeblaze_rmsnorm_forward(shape, _ptr(x), _ptr(residual), _ptr(weight), eps, _ptr(sum), _ptr(y), _ptr(rstd),
+                                  _ptr(q), _ptr(q_scales), _stream(stream))
+    _check(st, "moeblaze_rmsnorm_forward")
+
+
+def rmsnorm_backward(shape: Shape, dy, sum, rstd, weight, dsum, dx, dweight, ws, stream=None, own=None):
+    """Root-mean-square norm backward: fills dx (L,d) and dweight (d) fp32.
+    own: the workspace's bytes, when outputs and workspace are buffers made for this shape on dx's device."""
+    dt, L, d = _TORCH_DTYPE[shape.dtype], shape.L, shape.d
+    specs = ((dy, "dy", (L, d), dt, False), (sum, "sum", (L, d), dt, False), (rstd, "rstd", (L,), torch.float32, False),
+             (weight, "weight", (d,), torch.float32, False), (dsum, "dsum", (L, d), dt, True),
+             (dx, "dx", (L, d), dt, False))
+    n = own
+    if own is None:
+        specs += ((dweight, "dweight", (d,), torch.float32, False),)
+    _args(*specs)
+    if own is None:
+        n = moeblaze_rmsnorm_backward_workspace_bytes(shape)
+        _bytes_arg(ws, "ws", n)
+    st = moeblaze_rmsnorm_backward(shape, _ptr(dy), _ptr(sum), _ptr(rstd), _ptr(weight), _ptr(dsum), _ptr(dx),
+                                   _ptr(dweight), _ptr(ws), n, _stream(stream))
+    _check(st, "moeblaze_rmsnorm_backward")
+
+
+def blocks8(d: int) -> int:
+    """Blocks of 128 columns, each with a scale, of 8-bit rows of d columns."""
+    return (d + 127) // 128
+
+
+def fp8_quantize_rows(x, q=None, scales=None, stream=None):
+    """8-bit rows of x (L,d) bf16 or fp32: (q (L,d) float8_e4m3fn, scales (L, ceil(d/128)) fp32)."""
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        raise ValueError("x: expected a tensor of shape (L, d)")
+    if x.dtype not in DTYPE:
+        raise ValueError(f"x: dtype {x.dtype}, expected float32 or bfloat16")
+    L, d = x.shape
+    if d % 16 != 0:
+        raise MoEBlazeError(ERR_UNSUPPORTED, "moeblaze_fp8_quantize_rows")
+    _args((x, "x", (L, d), x.dtype, False))
+    q = torch.empty((L, d), dtype=torch.float8_e4m3fn, device=x.device) if q is None else q
+    scales = torch.empty((L, blocks8(d)), dtype=torch.float32, device=x.device) if scales is None else scales
+    _args((q, "q", (L, d), torch.float8_e4m3fn, False), (scales, "scales", (L, blocks8(d)), torch.float32, False))
+    st = moeblaze_fp8_quantize_rows(L, d, DTYPE[x.dtype], _ptr(x), _ptr(q), _ptr(scales), _stream(stream))
+    _check(st, "moeblaze_fp8_quantize_rows")
+    return q, scales
+
+
+def fp8_dequantize_rows(q, scales, dtype=torch.bfloat16, out=None, stream=None):
+    """What 8-bit rows q (L,d) with scales (L, ceil(d/128)) stand for, (L,d) bf16 or fp32, rounded once (with scales of
+    powers of two, as the quantiser's, exactly)."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 2:
+        raise ValueError("q: expected a tensor of shape (L, d)")
+    if dtype not in DTYPE:
+        raise ValueError(f"dtype {dtype}, expected float32 or bfloat16")
+    L, d = q.shape
+    _args((q, "q", (L, d), torch.float8_e4m3fn, False), (scales, "scales", (L, blocks8(d)), torch.float32, False))
+    out = torch.empty((L, d), dtype=dtype, device=q.device) if out is None else out
+    _args((out, "out", (L, d), dtype, False))
+    st = moeblaze_fp8_dequantize_rows(L, d, DTYPE[dtype], _ptr(q), _ptr(scales), _ptr(out), _stream(stream))
+    _check(st, "moeblaze_fp8_dequantize_rows")
+    return out
 
 
 def _int4_matrix(E: int, R: int, N: int, group: int, where: str):

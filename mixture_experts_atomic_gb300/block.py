@@ -1,4 +1,4 @@
-"""The pre-norm block around the layer: layer norm with the residual sum, the
+"""The pre-norm block around the layer: layer or RMS norm with the residual sum, the
 router with its losses, the layer, and the backward of it all.  Each class
 owns the buffers of one shape and runs on the current CUDA stream, as
 layer.MoELayer does; outputs are the object's own buffers, which the next call
@@ -50,6 +50,64 @@ class LayerNorm:
         dw, db = self._bwd
         B.layernorm_backward(self.shape, dy, s, mean, rstd, weight, dsum, self._dx, dw, db, self._ws, own=self._ws_bytes)
         return self._dx, dw, db
+
+
+class RMSNorm:
+    """Root-mean-square norm with the residual sum, its rows in 8 bits where wanted (forward8), and its backward."""
+
+    def __init__(self, L: int, d: int, dtype: torch.dtype, eps: float = 1e-5, device="cuda"):
+        self.shape = B.make_shape(L, d, 0, 1, 1, dtype, "identity")
+        self.L, self.d, self.dtype, self.eps = L, d, dtype, eps
+        self.y = torch.empty((L, d), dtype=dtype, device=device)
+        self.rstd = torch.empty((L,), dtype=torch.float32, device=device)
+        self.dw = torch.empty((d,), dtype=torch.float32, device=device)
+        # (what a call writes is kept here too, so that its checks, made once, hold whatever becomes of the names)
+        self._fwd = (self.y, self.rstd)
+        self._dw = self.dw
+        self._s: Optional[torch.Tensor] = None
+        self._q: Optional[tuple] = None
+        self._dx: Optional[torch.Tensor] = None
+        self._ws: Optional[torch.Tensor] = None
+        self._ws_bytes = B.moeblaze_rmsnorm_backward_workspace_bytes(self.shape)
+
+    def _sum(self, residual):
+        if residual is None:
+            return None
+        if self._s is None:
+            self._s = torch.empty_like(self._fwd[0])
+        return self._s
+
+    def forward(self, x, weight, residual=None):
+        """(y, s, rstd) of s = x (+ residual); without a residual s is x itself."""
+        s = self._sum(residual)
+        y, rstd = self._fwd
+        B.rmsnorm_forward(self.shape, x, residual, weight, self.eps, s, y, rstd, own=True)
+        return y, (x if s is None else s), rstd
+
+    def forward8(self, x, weight, residual=None, with_y: bool = True):
+        """(q, scales, y, s, rstd): the normed rows in 8-bit floating point too, q (L,d) float8_e4m3fn with scales
+        (L, ceil(d/128)) fp32, as fp8.Fp8Experts takes them; with_y=False leaves y out (None).  d is a multiple of 16."""
+        if self._q is None:
+            if self.d % 16 != 0:
+                raise ValueError(f"forward8: d {self.d} is not a multiple of 16")
+            dev = self._fwd[0].device
+            self._q = (torch.empty((self.L, self.d), dtype=torch.float8_e4m3fn, device=dev),
+                       torch.empty((self.L, B.blocks8(self.d)), dtype=torch.float32, device=dev))
+        q, scales = self._q
+        s = self._sum(residual)
+        y, rstd = self._fwd
+        if not with_y:
+            y = None
+        B.rmsnorm_forward(self.shape, x, residual, weight, self.eps, s, y, rstd, q, scales, own=True)
+        return q, scales, y, (x if s is None else s), rstd
+
+    def backward(self, dy, s, rstd, weight, dsum=None):
+        """(dx, dweight); dsum is a gradient that reaches s besides the norm and is added to dx."""
+        if self._dx is None:
+            self._dx = torch.empty_like(self._fwd[0])
+            self._ws = B._bytes(self._ws_bytes, self._dx.device)
+        B.rmsnorm_backward(self.shape, dy, s, rstd, weight, dsum, self._dx, self._dw, self._ws, own=self._ws_bytes)
+        return self._dx, self._dw
 
 
 class BalanceLoss:
@@ -117,14 +175,18 @@ class RouterGrad:
 
 
 class MoEBlock:
-    """s = x + residual;  out = MoE(LayerNorm(s)) (the caller adds s in its next norm), with the router's losses.
+    """s = x + residual;  out = MoE(Norm(s)) (the caller adds s in its next norm), with the router's losses.
 
     forward keeps what backward needs in the parts' buffers; one step is forward, then backward."""
 
     def __init__(self, L: int, d: int, h: int, E: int, K: int, dtype: torch.dtype, act: str = "swiglu",
-                 eps: float = 1e-5, device="cuda", recompute_h: bool = False, checkpoint8: bool = False):
-        """recompute_h, checkpoint8: what the layer keeps for its backward (see MoELayer)."""
-        self.norm = LayerNorm(L, d, dtype, eps, device)
+                 eps: float = 1e-5, device="cuda", recompute_h: bool = False, checkpoint8: bool = False,
+                 norm: str = "layer"):
+        """recompute_h, checkpoint8: what the layer keeps for its backward (see MoELayer); norm: "layer" or "rms"."""
+        if norm not in ("layer", "rms"):
+            raise ValueError(f"norm: {norm!r}, expected 'layer' or 'rms'")
+        self.rms = norm == "rms"
+        self.norm = (RMSNorm if self.rms else LayerNorm)(L, d, dtype, eps, device)
         self.layer = MoELayer(L, d, h, E, K, dtype, act, device, recompute_h=recompute_h, checkpoint8=checkpoint8)
         self.loss = BalanceLoss(L, E, K, device)
         self.grad = RouterGrad(L, d, E, dtype, device)
@@ -132,9 +194,14 @@ class MoEBlock:
         self._kept = None
 
     def forward(self, x, residual, p, valid=None):
-        """(out, s, losses, counts).  p: dict of parameters: norm_w, norm_b (or None), Wr, bias (or None), W1, W2, W3.
+        """(out, s, losses, counts).  p: dict of parameters: norm_w, norm_b (or None; layer norm), Wr, bias (or None), W1, W2, W3.
         valid (L) uint8: tokens that count for the losses (all of them are routed and have a row of out)."""
-        u, s, mean, rstd = self.norm.forward(x, p["norm_w"], p.get("norm_b"), residual)
+        if self.rms:
+            if p.get("norm_b") is not None:
+                raise ValueError("norm_b: the RMS norm has no bias")
+            (u, s, rstd), mean = self.norm.forward(x, p["norm_w"], residual), None
+        else:
+            u, s, mean, rstd = self.norm.forward(x, p["norm_w"], p.get("norm_b"), residual)
         ids, gates = self.layer.route(u, p["Wr"], p.get("bias"), self.logits)
         losses, counts = self.loss.forward(self.logits, ids, valid)
         out = self.layer.forward(u, gates, p["W1"], p.get("W2"), p["W3"])
@@ -142,7 +209,7 @@ class MoEBlock:
         return out, s, losses, counts
 
     def backward(self, dout, dlosses, p, dsum=None):
-        """Gradients as a dict: x (of x and of the residual alike), norm_w, norm_b, Wr, bias, W1, W2, W3.
+        """Gradients as a dict: x (of x and of the residual alike), norm_w, norm_b (layer norm), Wr, bias, W1, W2, W3.
         dout: of out; dlosses (2): of the two losses; dsum: what reaches s besides the norm."""
         if self._kept is None:
             raise RuntimeError("MoEBlock: run forward first")
@@ -152,5 +219,8 @@ class MoEBlock:
         # the mask is the losses' alone: the gates of every token made its row of out
         dlogits = self.loss.backward(self.logits, dlosses, None, ids, gates, dgates, gates_of_all=True)
         du, dWr, dbias = self.grad.backward(u, p["Wr"], dlogits, add_to=du)
+        if self.rms:
+            dx, dnw = self.norm.backward(du, s, rstd, p["norm_w"], dsum)
+            return {"x": dx, "norm_w": dnw, "Wr": dWr, "bias": dbias, "W1": dW1, "W2": dW2, "W3": dW3}
         dx, dnw, dnb = self.norm.backward(du, s, mean, rstd, p["norm_w"], dsum)
         return {"x": dx, "norm_w": dnw, "norm_b": dnb, "Wr": dWr, "bias": dbias, "W1": dW1, "W2": dW2, "W3": dW3}

@@ -1,7 +1,7 @@
 // extern "C" entry points of the moeblaze library (declared in
 // include/moeblaze.h): argument validation, scratch carving and the order of
 // the stages; every stage runs in the kernels of dispatch.cu, identity.cu,
-// simt.cu, gemm_tc.cu, router.cu, router_tc.cu, norm.cu, balance.cu and int4.cu.
+// simt.cu, gemm_tc.cu, router.cu, router_tc.cu, norm.cu, rmsnorm.cu, balance.cu, int4.cu and fp8.cu.
 #include <atomic>
 #include <cstring>
 
@@ -104,6 +104,14 @@ moeblaze_status check_norm_shape(const moeblaze_shape* s) {
 moeblaze_status check_balance_shape(const moeblaze_shape* s) {
   if (!s || s->L < 0 || s->E < 1 || s->K < 1 || s->K > s->E) return MOEBLAZE_ERR_INVALID_ARG;
   if (s->E > kMaxE || s->K > kMaxK || s->L * (int64_t)s->K >= (int64_t(1) << 31)) return MOEBLAZE_ERR_UNSUPPORTED;
+  return MOEBLAZE_OK;
+}
+
+// rows in 8-bit floating point and what they stand for
+moeblaze_status check_rows8(int64_t L, int d, int dtype, const void* x, const void* q, const void* scales) {
+  if (L < 0 || d < 1 || (dtype != MOEBLAZE_F32 && dtype != MOEBLAZE_BF16)) return MOEBLAZE_ERR_INVALID_ARG;
+  if (L >= (int64_t(1) << 31) || d > (1 << 24) || d % 16 != 0) return MOEBLAZE_ERR_UNSUPPORTED;
+  if (L > 0 && (!ok_ptr(x) || !ok_ptr(q) || !ok_ptr4(scales))) return MOEBLAZE_ERR_INVALID_ARG;
   return MOEBLAZE_OK;
 }
 
@@ -493,6 +501,53 @@ moeblaze_status moeblaze_layernorm_backward(const moeblaze_shape* s, const void*
   if (s->L > 0 && !ok_ptr(ws)) return MOEBLAZE_ERR_INVALID_ARG;
   return launch_layernorm_backward(*s, dy, sum, mean, rstd, weight, dsum, dx, dweight, dbias, ws,
                                    reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t moeblaze_rmsnorm_backward_workspace_bytes(const moeblaze_shape* s) {
+  if (check_norm_shape(s) != MOEBLAZE_OK) return 0;
+  return rmsnorm_ws_bytes(*s);
+}
+
+moeblaze_status moeblaze_rmsnorm_forward(const moeblaze_shape* s, const void* x, const void* residual,
+                                         const float* weight, float eps, void* sum, void* y, float* rstd, void* q,
+                                         float* q_scales, moeblaze_stream stream) {
+  moeblaze_status r = check_norm_shape(s);
+  if (r != MOEBLAZE_OK) return r;
+  if (!(eps >= 0.f) || !ok_ptr(weight) || (q != nullptr) != (q_scales != nullptr)) return MOEBLAZE_ERR_INVALID_ARG;
+  if (q && s->d % 16 != 0) return MOEBLAZE_ERR_UNSUPPORTED;
+  if (s->L > 0 && (!ok_ptr(x) || (y ? !ok_ptr(y) : !q) || !ok_ptr4(rstd) || (residual && !ok_ptr(residual)) ||
+                   (sum && !ok_ptr(sum)) || (q && (!ok_ptr(q) || !ok_ptr4(q_scales)))))
+    return MOEBLAZE_ERR_INVALID_ARG;
+  return launch_rmsnorm_forward(*s, x, residual, weight, eps, sum, y, rstd, q, q_scales,
+                                reinterpret_cast<cudaStream_t>(stream));
+}
+
+moeblaze_status moeblaze_rmsnorm_backward(const moeblaze_shape* s, const void* dy, const void* sum, const float* rstd,
+                                          const float* weight, const void* dsum, void* dx, float* dweight, void* ws,
+                                          size_t ws_bytes, moeblaze_stream stream) {
+  moeblaze_status r = check_norm_shape(s);
+  if (r != MOEBLAZE_OK) return r;
+  if (!ok_ptr(weight) || !ok_ptr4(dweight)) return MOEBLAZE_ERR_INVALID_ARG;
+  if (s->L > 0 && (!ok_ptr(dy) || !ok_ptr(sum) || !ok_ptr(dx) || !ok_ptr4(rstd) || (dsum && !ok_ptr(dsum))))
+    return MOEBLAZE_ERR_INVALID_ARG;
+  if (ws_bytes < rmsnorm_ws_bytes(*s)) return MOEBLAZE_ERR_WORKSPACE;
+  if (s->L > 0 && !ok_ptr(ws)) return MOEBLAZE_ERR_INVALID_ARG;
+  return launch_rmsnorm_backward(*s, dy, sum, rstd, weight, dsum, dx, dweight, ws,
+                                 reinterpret_cast<cudaStream_t>(stream));
+}
+
+moeblaze_status moeblaze_fp8_quantize_rows(int64_t L, int32_t d, int32_t dtype, const void* x, void* q, float* scales,
+                                           moeblaze_stream stream) {
+  const moeblaze_status r = check_rows8(L, d, dtype, x, q, scales);
+  if (r != MOEBLAZE_OK || L == 0) return r;
+  return launch_fp8_quantize_rows(L, d, dtype, x, q, scales, reinterpret_cast<cudaStream_t>(stream));
+}
+
+moeblaze_status moeblaze_fp8_dequantize_rows(int64_t L, int32_t d, int32_t dtype, const void* q, const float* scales,
+                                             void* x, moeblaze_stream stream) {
+  const moeblaze_status r = check_rows8(L, d, dtype, x, q, scales);
+  if (r != MOEBLAZE_OK || L == 0) return r;
+  return launch_fp8_dequantize_rows(L, d, dtype, q, scales, x, reinterpret_cast<cudaStream_t>(stream));
 }
 
 size_t moeblaze_balance_workspace_bytes(const moeblaze_shape* s) {

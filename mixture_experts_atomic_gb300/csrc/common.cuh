@@ -161,6 +161,21 @@ moeblaze_status launch_layernorm_backward(const moeblaze_shape& s, const void* d
                                           const float* rstd, const float* w, const void* dsum, void* dx, float* dw,
                                           float* db, void* ws, cudaStream_t st);
 
+// rmsnorm.cu
+size_t rmsnorm_ws_bytes(const moeblaze_shape& s);
+moeblaze_status launch_rmsnorm_forward(const moeblaze_shape& s, const void* x, const void* res, const float* w,
+                                       float eps, void* sum, void* y, float* rstd, void* q, float* q_scales,
+                                       cudaStream_t st);
+moeblaze_status launch_rmsnorm_backward(const moeblaze_shape& s, const void* dy, const void* sum, const float* rstd,
+                                        const float* w, const void* dsum, void* dx, float* dw, void* ws,
+                                        cudaStream_t st);
+
+// fp8.cu
+moeblaze_status launch_fp8_quantize_rows(int64_t L, int d, int dtype, const void* x, void* q, float* scales,
+                                         cudaStream_t st);
+moeblaze_status launch_fp8_dequantize_rows(int64_t L, int d, int dtype, const void* q, const float* scales, void* x,
+                                           cudaStream_t st);
+
 // balance.cu
 size_t balance_ws_bytes(const moeblaze_shape& s);
 moeblaze_status launch_balance_forward(const moeblaze_shape& s, const float* logits, const int32_t* ids,

@@ -105,3 +105,49 @@ def layer_backward(dY, x, ids, gates, W1, W2, W3, A, B):
             out["dX"].index_add_(0, t, v @ w.t())
             tol["dX"].index_add_(0, t, verr @ w.abs().t() + matmul_err(2 * h) * (v.abs() @ w.abs().t()))
     return out, tol
+
+
+def blocks(v):
+    """Row blocks of 128 columns of v (L,d): (L, ceil(d/128), 128), zeros behind the last column."""
+    L, d = v.shape
+    n = -(-d // 128)
+    return torch.nn.functional.pad(v, (0, 128 * n - d)).view(L, n, 128)
+
+
+def rows8(v):
+    """(codes as float64 values, scales) of v's blocks of 128 columns, by the definition: the scale the least power of
+    two (2^-126 or more) that brings the largest to at most 448; each value to the nearest e4m3 value, ties to the even
+    one; NaN scales for blocks with a NaN or an infinity."""
+    b = blocks(v.double())
+    top = b.abs().amax(2)
+    ok = top.isfinite()
+    f, e = torch.frexp(torch.where(ok, top, torch.ones_like(top)) / 448.0)
+    k = torch.where(f == 0.5, e - 1, e).clamp(min=-126)
+    k = torch.where(f == 0, torch.full_like(k, -126), k)    # (a block of zeros: frexp has no exponent for it)
+    s = (k.long() + 1023 << 52).view(torch.float64)
+    u = b / s[..., None]
+    _, ue = torch.frexp(torch.nan_to_num(u, 0, 0, 0))
+    step = ((ue - 4).clamp(min=-9).long() + 1023 << 52).view(torch.float64)
+    q = torch.round(u / step) * step
+    s = torch.where(ok, s, torch.full_like(s, float("nan")))
+    return q.flatten(1)[:, :v.shape[1]], s
+
+
+def grown(s, d):
+    """A scale for every column, (L,d) in fp64, of scales (L, ceil(d/128))."""
+    return s.double().repeat_interleave(128, dim=1)[:, :d]
+
+
+def rms(x, residual, w, eps):
+    s = x.double() if residual is None else x.double() + residual.double()
+    rstd = 1.0 / torch.sqrt((s * s).mean(1) + eps)
+    return s * rstd[:, None] * w.double(), s, rstd
+
+
+def rms_grad(dy, s, rstd, w, dsum):
+    """dx, dweight, and xh and g of the formulas."""
+    g, xh = dy.double() * w.double(), s.double() * rstd.double()[:, None]
+    dx = rstd.double()[:, None] * (g - xh * (g * xh).mean(1, keepdim=True))
+    if dsum is not None:
+        dx = dx + dsum.double()
+    return dx, (dy.double() * xh).sum(0), xh, g
