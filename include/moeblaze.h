@@ -479,6 +479,50 @@ MOEBLAZE_API moeblaze_status moeblaze_fp8_quantize_rows(int64_t L, int32_t d, in
 MOEBLAZE_API moeblaze_status moeblaze_fp8_dequantize_rows(int64_t L, int32_t d, int32_t dtype, const void* q,
                                                           const float* scales, void* x, moeblaze_stream stream);
 
+/* ------------------------------------------------- experts on 8-bit weights
+ * The layer's forward for serving, any number of tokens, on e4m3 weights with
+ * an fp32 scale for each 128 x 128 of them, and rows in 8-bit floating point.
+ * A matrix that maps R inputs to N outputs is held with its reduction inside:
+ *   q (E,N,R) e4m3, scales (E, N/128, R/128):  W[e][r][n] = q[e][n][r] scale
+ * quantize_weights makes it of W (E,R,N) (bf16 or fp32, the layer's layout),
+ * with scales of powers of two as quantize_rows; the products take any scales.
+ * R and N are multiples of 128, E <= 512. */
+typedef struct {
+  const void* q1;   /* (E,h,d): W1 */
+  const float* s1;  /* (E, h/128, d/128) */
+  const void* q2;   /* W2 (SwiGLU; NULL for SiLU) */
+  const float* s2;
+  const void* q3;   /* (E,d,h): W3 */
+  const float* s3;  /* (E, d/128, h/128) */
+} moeblaze_fp8_experts;
+
+MOEBLAZE_API moeblaze_status moeblaze_fp8_quantize_weights(int32_t E, int32_t R, int32_t N, int32_t dtype,
+                                                           const void* W, void* q, float* scales,
+                                                           moeblaze_stream stream);
+/* W device (E,R,N) bf16, each value rounded once */
+MOEBLAZE_API moeblaze_status moeblaze_fp8_dequantize_weights(int32_t E, int32_t R, int32_t N, const void* q,
+                                                             const float* scales, void* W, moeblaze_stream stream);
+
+/* moeblaze_fp8_forward:
+ *   y[t] = sum_k gates[t,k] expert_{topk_ids[t,k]}(x[t])
+ * Shape as moeblaze_forward with dtype MOEBLAZE_BF16 and a SwiGLU or SiLU
+ * expert (MOEBLAZE_ERR_UNSUPPORTED otherwise).
+ *   x        device (L,d): with x_scales (L, d/128) fp32 e4m3 rows, without
+ *            (NULL) bf16 rows, which are brought to 8 bits as quantize_rows does
+ *   topk_ids device (L,K) int32; an id outside [0,E) is an empty slot (its gate
+ *            is not read), one that a token names more than once counts once
+ *            for each slot; a token without any gives a row of zeros
+ *   gates    device (L,K) fp32       y device (L,d) bf16, overwritten
+ *   ws       device moeblaze_fp8_workspace_bytes(s) bytes
+ * Products are exact and summed in fp32; the hidden activations go to 8-bit
+ * rows between the two products.  Results are repeatable to the bit.  y is NaN
+ * where a bounded device-side wait ran out. */
+MOEBLAZE_API size_t moeblaze_fp8_workspace_bytes(const moeblaze_shape* s);
+MOEBLAZE_API moeblaze_status moeblaze_fp8_forward(const moeblaze_shape* s, const void* x, const float* x_scales,
+                                                  const int32_t* topk_ids, const float* gates,
+                                                  const moeblaze_fp8_experts* w, void* y, void* ws, size_t ws_bytes,
+                                                  moeblaze_stream stream);
+
 /* ------------------------------------------------- experts on 4-bit weights
  * The layer's forward for few tokens (serving) on 4-bit weights with a scale
  * for each group of reduction rows:

@@ -39,7 +39,8 @@ EXPORTS = [
     "moeblaze_int4_scale_bytes", "moeblaze_int4_quantize", "moeblaze_int4_pack", "moeblaze_int4_dequantize",
     "moeblaze_int4_workspace_bytes", "moeblaze_int4_forward", "moeblaze_balance_backward_masked",
     "moeblaze_rmsnorm_forward", "moeblaze_rmsnorm_backward", "moeblaze_rmsnorm_backward_workspace_bytes",
-    "moeblaze_fp8_quantize_rows", "moeblaze_fp8_dequantize_rows",
+    "moeblaze_fp8_quantize_rows", "moeblaze_fp8_dequantize_rows", "moeblaze_fp8_quantize_weights",
+    "moeblaze_fp8_dequantize_weights", "moeblaze_fp8_workspace_bytes", "moeblaze_fp8_forward",
 ]
 
 # fixed scratch of moeblaze_dispatch_build_static (MOEBLAZE_STATIC_SCRATCH_BYTES)
@@ -66,6 +67,11 @@ class Dispatch(ctypes.Structure):
 class Int4Weights(ctypes.Structure):
     _fields_ = [("w1", ctypes.c_void_p), ("s1", ctypes.c_void_p), ("w2", ctypes.c_void_p), ("s2", ctypes.c_void_p),
                 ("w3", ctypes.c_void_p), ("s3", ctypes.c_void_p), ("group", ctypes.c_int32)]
+
+
+class Fp8Weights(ctypes.Structure):
+    _fields_ = [("q1", ctypes.c_void_p), ("s1", ctypes.c_void_p), ("q2", ctypes.c_void_p), ("s2", ctypes.c_void_p),
+                ("q3", ctypes.c_void_p), ("s3", ctypes.c_void_p)]
 
 
 class MoEBlazeError(RuntimeError):
@@ -121,12 +127,16 @@ def lib():
         i32 = ctypes.c_int32
         for n in ["moeblaze_fp8_quantize_rows", "moeblaze_fp8_dequantize_rows"]:
             getattr(L, n).argtypes = [ctypes.c_int64, i32, i32, P, P, P, P]
+        L.moeblaze_fp8_quantize_weights.argtypes = [i32, i32, i32, i32, P, P, P, P]
+        L.moeblaze_fp8_dequantize_weights.argtypes = [i32, i32, i32, P, P, P, P]
+        L.moeblaze_fp8_forward.argtypes = [SP, P, P, P, P, ctypes.POINTER(Fp8Weights), P, P, sz, P]
         L.moeblaze_int4_quantize.argtypes = [i32, i32, i32, i32, i32, P, P, P, P]
         L.moeblaze_int4_pack.argtypes = [i32, i32, i32, i32, P, P, P, P, P]
         L.moeblaze_int4_dequantize.argtypes = [i32, i32, i32, i32, P, P, P, P]
         L.moeblaze_int4_forward.argtypes = [SP, P, P, P, ctypes.POINTER(Int4Weights), P, P, sz, P]
         for n in ["moeblaze_router_backward_logits_workspace_bytes", "moeblaze_balance_workspace_bytes",
-                  "moeblaze_layernorm_backward_workspace_bytes", "moeblaze_rmsnorm_backward_workspace_bytes"]:
+                  "moeblaze_layernorm_backward_workspace_bytes", "moeblaze_rmsnorm_backward_workspace_bytes",
+                  "moeblaze_fp8_workspace_bytes"]:
             getattr(L, n).argtypes = [SP]
             getattr(L, n).restype = sz
         L.moeblaze_int4_workspace_bytes.argtypes = [SP, i32]
@@ -296,6 +306,23 @@ def moeblaze_fp8_quantize_rows(L, d, dtype, x, q, scales, stream) -> int:
 
 def moeblaze_fp8_dequantize_rows(L, d, dtype, q, scales, x, stream) -> int:
     return lib().moeblaze_fp8_dequantize_rows(L, d, dtype, q, scales, x, stream)
+
+
+def moeblaze_fp8_quantize_weights(E, R, N, dtype, W, q, scales, stream) -> int:
+    return lib().moeblaze_fp8_quantize_weights(E, R, N, dtype, W, q, scales, stream)
+
+
+def moeblaze_fp8_dequantize_weights(E, R, N, q, scales, W, stream) -> int:
+    return lib().moeblaze_fp8_dequantize_weights(E, R, N, q, scales, W, stream)
+
+
+def moeblaze_fp8_workspace_bytes(shape: Shape) -> int:
+    return lib().moeblaze_fp8_workspace_bytes(ctypes.byref(shape))
+
+
+def moeblaze_fp8_forward(shape, x, x_scales, topk_ids, gates, weights, y, ws, ws_bytes, stream) -> int:
+    return lib().moeblaze_fp8_forward(ctypes.byref(shape), x, x_scales, topk_ids, gates, ctypes.byref(weights), y, ws,
+                                      ws_bytes, stream)
 
 
 def moeblaze_int4_weight_bytes(E: int, R: int, N: int) -> int:
@@ -820,6 +847,57 @@ def fp8_dequantize_rows(q, scales, dtype=torch.bfloat16, out=None, stream=None):
     st = moeblaze_fp8_dequantize_rows(L, d, DTYPE[dtype], _ptr(q), _ptr(scales), _ptr(out), _stream(stream))
     _check(st, "moeblaze_fp8_dequantize_rows")
     return out
+
+
+def fp8_quantize_weights(W, stream=None):
+    """8-bit weights of W (E,R,N) bf16 or fp32: (q (E,N,R) float8_e4m3fn, scales (E, N/128, R/128) fp32)."""
+    if not isinstance(W, torch.Tensor) or W.dim() != 3:
+        raise ValueError("W: expected a tensor of shape (E, R, N)")
+    if W.dtype not in DTYPE:
+        raise ValueError(f"W: dtype {W.dtype}, expected float32 or bfloat16")
+    E, R, N = W.shape
+    if E < 1 or R < 1 or N < 1 or R % 128 or N % 128:
+        raise MoEBlazeError(ERR_UNSUPPORTED, "moeblaze_fp8_quantize_weights")
+    _args((W, "W", (E, R, N), W.dtype, False))
+    q = torch.empty((E, N, R), dtype=torch.float8_e4m3fn, device=W.device)
+    s = torch.empty((E, N // 128, R // 128), dtype=torch.float32, device=W.device)
+    st = moeblaze_fp8_quantize_weights(E, R, N, DTYPE[W.dtype], _ptr(W), _ptr(q), _ptr(s), _stream(stream))
+    _check(st, "moeblaze_fp8_quantize_weights")
+    return q, s
+
+
+def fp8_dequantize_weights(q, scales, stream=None):
+    """The bf16 weights (E,R,N) that q (E,N,R) with scales (E, N/128, R/128) stands for."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q: expected a tensor of shape (E, N, R)")
+    E, N, R = q.shape
+    _args((q, "q", (E, N, R), torch.float8_e4m3fn, False),
+          (scales, "scales", (E, N // 128, R // 128), torch.float32, False))
+    W = torch.empty((E, R, N), dtype=torch.bfloat16, device=q.device)
+    st = moeblaze_fp8_dequantize_weights(E, R, N, _ptr(q), _ptr(scales), _ptr(W), _stream(stream))
+    _check(st, "moeblaze_fp8_dequantize_weights")
+    return W
+
+
+def fp8_forward(shape: Shape, x, x_scales, topk_ids, gates, weights: Fp8Weights, y, ws, ws_bytes=None, stream=None):
+    """The layer's forward on 8-bit weights: fills y (L,d) bf16.  x (L,d) bf16, or float8_e4m3fn with x_scales
+    (L, d/128) fp32.  `weights` holds device pointers that the caller keeps alive (see fp8.Fp8Experts).
+    ws_bytes: the workspace's bytes, when y and ws are buffers made for this shape (at least) on x's device."""
+    L, d, K = shape.L, shape.d, shape.K
+    rows = (x, "x", (L, d), torch.bfloat16, False)
+    if x_scales is not None:
+        rows = (x, "x", (L, d), torch.float8_e4m3fn, False)
+    specs = (rows, (x_scales, "x_scales", (L, blocks8(d)), torch.float32, True),
+             (topk_ids, "topk_ids", (L, K), torch.int32, False), (gates, "gates", (L, K), torch.float32, False),
+             (y, "y", (L, d), torch.bfloat16, False))
+    _args(*specs)
+    if ws_bytes is None:
+        ws_bytes = moeblaze_fp8_workspace_bytes(shape)
+        _bytes_arg(ws, "ws", ws_bytes)
+    st = moeblaze_fp8_forward(shape, _ptr(x), _ptr(x_scales), _ptr(topk_ids), _ptr(gates), weights, _ptr(y), _ptr(ws),
+                              ws_bytes, _stream(stream))
+    _check(st, "moeblaze_fp8_forward")
+    return y
 
 
 def _int4_matrix(E: int, R: int, N: int, group: int, where: str):

@@ -21,7 +21,7 @@ SRC = os.path.join(PKG, "csrc")
 OUT_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmoeblaze.so")
 SOURCES = ["abi.cu", "dispatch.cu", "identity.cu", "simt.cu", "gemm_tc.cu", "router.cu", "router_tc.cu", "norm.cu",
-           "balance.cu", "int4.cu", "router_grad_tc.cu", "rmsnorm.cu", "fp8.cu"]
+           "balance.cu", "int4.cu", "router_grad_tc.cu", "rmsnorm.cu", "fp8.cu", "fp8_tc.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "--expt-relaxed-constexpr", "-I", os.path.join(ROOT, "include")]
@@ -43,7 +43,7 @@ def _newer(src_files, target) -> bool:
 
 def build(verbose: bool = False, force: bool = False) -> str:
     os.makedirs(OUT_DIR, exist_ok=True)
-    headers = [os.path.join(SRC, h) for h in ("common.cuh", "tc_ptx.cuh", "eight.cuh", "norm_impl.cuh")]
+    headers = [os.path.join(SRC, h) for h in ("common.cuh", "tc_ptx.cuh", "eight.cuh", "norm_impl.cuh", "fp8.cuh")]
     headers.append(os.path.join(ROOT, "include", "moeblaze.h"))
     objs = []
     jobs = []

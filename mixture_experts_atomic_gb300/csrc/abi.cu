@@ -115,6 +115,25 @@ moeblaze_status check_rows8(int64_t L, int d, int dtype, const void* x, const vo
   return MOEBLAZE_OK;
 }
 
+// checks of one matrix of 8-bit weights and of the layer on them
+moeblaze_status check_fp8_matrix(int E, int R, int N) {
+  if (E < 1 || R < 1 || N < 1) return MOEBLAZE_ERR_INVALID_ARG;
+  // (a block of 128 x 128 each in the launch's grid; rows of all experts' matrices are counted in 32 bits)
+  if (E > kMaxE || R % 128 != 0 || N % 128 != 0 || N / 128 > 65535 || (int64_t)E * N > INT32_MAX - 256)
+    return MOEBLAZE_ERR_UNSUPPORTED;
+  return MOEBLAZE_OK;
+}
+moeblaze_status check_fp8_shape(const moeblaze_shape* s) {
+  const moeblaze_status r = check_shape(s);
+  if (r != MOEBLAZE_OK) return r;
+  if (s->act == MOEBLAZE_IDENTITY || s->dtype != MOEBLAZE_BF16) return MOEBLAZE_ERR_UNSUPPORTED;
+  if (check_fp8_matrix(s->E, s->d, s->h) != MOEBLAZE_OK || check_fp8_matrix(s->E, s->h, s->d) != MOEBLAZE_OK)
+    return MOEBLAZE_ERR_UNSUPPORTED;
+  // launches of a warp a token and of a thread for four of a row's columns
+  if (s->L * (int64_t)s->d >= (int64_t(1) << 40)) return MOEBLAZE_ERR_UNSUPPORTED;
+  return MOEBLAZE_OK;
+}
+
 // checks of one 4-bit matrix (E,R,N) and of the layer on such matrices
 moeblaze_status check_int4_matrix(int E, int R, int N, int group) {
   if (E < 1 || R < 1 || N < 1) return MOEBLAZE_ERR_INVALID_ARG;
@@ -548,6 +567,42 @@ moeblaze_status moeblaze_fp8_dequantize_rows(int64_t L, int32_t d, int32_t dtype
   const moeblaze_status r = check_rows8(L, d, dtype, x, q, scales);
   if (r != MOEBLAZE_OK || L == 0) return r;
   return launch_fp8_dequantize_rows(L, d, dtype, q, scales, x, reinterpret_cast<cudaStream_t>(stream));
+}
+
+moeblaze_status moeblaze_fp8_quantize_weights(int32_t E, int32_t R, int32_t N, int32_t dtype, const void* W, void* q,
+                                              float* scales, moeblaze_stream stream) {
+  const moeblaze_status r = check_fp8_matrix(E, R, N);
+  if (r != MOEBLAZE_OK) return r;
+  if ((dtype != MOEBLAZE_F32 && dtype != MOEBLAZE_BF16) || !ok_ptr(W) || !ok_ptr(q) || !ok_ptr4(scales))
+    return MOEBLAZE_ERR_INVALID_ARG;
+  return launch_fp8_quantize_weights(E, R, N, dtype, W, q, scales, reinterpret_cast<cudaStream_t>(stream));
+}
+
+moeblaze_status moeblaze_fp8_dequantize_weights(int32_t E, int32_t R, int32_t N, const void* q, const float* scales,
+                                                void* W, moeblaze_stream stream) {
+  const moeblaze_status r = check_fp8_matrix(E, R, N);
+  if (r != MOEBLAZE_OK) return r;
+  if (!ok_ptr(W) || !ok_ptr(q) || !ok_ptr4(scales)) return MOEBLAZE_ERR_INVALID_ARG;
+  return launch_fp8_dequantize_weights(E, R, N, q, scales, W, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t moeblaze_fp8_workspace_bytes(const moeblaze_shape* s) {
+  return check_fp8_shape(s) == MOEBLAZE_OK ? fp8_ws_bytes(*s) : 0;
+}
+
+moeblaze_status moeblaze_fp8_forward(const moeblaze_shape* s, const void* x, const float* x_scales,
+                                     const int32_t* topk_ids, const float* gates, const moeblaze_fp8_experts* w, void* y,
+                                     void* ws, size_t ws_bytes, moeblaze_stream stream) {
+  const moeblaze_status r = check_fp8_shape(s);
+  if (r != MOEBLAZE_OK) return r;
+  if (!w || !ok_ptr(w->q1) || !ok_ptr4(w->s1) || !ok_ptr(w->q3) || !ok_ptr4(w->s3)) return MOEBLAZE_ERR_INVALID_ARG;
+  if (s->act == MOEBLAZE_SWIGLU && (!ok_ptr(w->q2) || !ok_ptr4(w->s2))) return MOEBLAZE_ERR_INVALID_ARG;
+  if (s->L > 0 && (!ok_ptr(x) || !ok_ptr(y) || !ok_ptr4(topk_ids) || !ok_ptr4(gates) || (x_scales && !ok_ptr4(x_scales))))
+    return MOEBLAZE_ERR_INVALID_ARG;
+  if (ws_bytes < fp8_ws_bytes(*s)) return MOEBLAZE_ERR_WORKSPACE;
+  if (s->L > 0 && !ok_ptr(ws)) return MOEBLAZE_ERR_INVALID_ARG;
+  return launch_fp8_forward(*s, x, x_scales, topk_ids, gates, *w, (__nv_bfloat16*)y, ws,
+                            reinterpret_cast<cudaStream_t>(stream));
 }
 
 size_t moeblaze_balance_workspace_bytes(const moeblaze_shape* s) {

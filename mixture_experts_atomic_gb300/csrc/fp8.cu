@@ -1,6 +1,10 @@
-// Rows in 8-bit floating point (eight.cuh): quantising and widening.
+// Rows and weights in 8-bit floating point (eight.cuh): quantising and
+// widening; and the steps around the experts' products on them (fp8_tc.cu):
+// which row each slot takes, the rows themselves, and the sum of a token's
+// slots.
 #include "common.cuh"
 #include "eight.cuh"
+#include "fp8.cuh"
 
 namespace moeblaze {
 namespace {
@@ -87,12 +91,351 @@ __global__ void __launch_bounds__(kRowThreads) dequantize_rows_kernel(const uint
   }
 }
 
+// ------------------------------------------------------------------ weights
+// A block of 128 x 128 of W (R,N), transposed to q (N,R): 512 threads read rows
+// of it and write rows of its transpose, through shared memory in between.
+constexpr int kWThreads = 512, kWPitch = 132;
+template <typename T>
+__global__ void __launch_bounds__(kWThreads) quantize_weights_kernel(const T* __restrict__ W, int R, int N,
+                                                                     uint8_t* __restrict__ q, float* __restrict__ s) {
+  __shared__ uint32_t top;
+  __shared__ __align__(16) uint8_t t8[kBlock8 * kWPitch];  // [column][row]
+  const int r0 = blockIdx.x * kBlock8, n0 = blockIdx.y * kBlock8;
+  const int64_t e = blockIdx.z, base = e * R * N;
+  if (threadIdx.x == 0) top = 0u;
+  __syncthreads();
+  // thread: 8 columns of rows ty + 32 i
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  float v[4][8];
+  uint32_t m = 0u;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    load8(W + base + (int64_t)(r0 + 4 * ty + i) * N + n0 + 8 * tx, v[i]);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = max(m, abs_bits(v[i][j]));
+  }
+  m = __reduce_max_sync(0xffffffffu, m);
+  if ((threadIdx.x & 31) == 0) atomicMax(&top, m);
+  __syncthreads();
+  const Scale8 sc = scale8(top);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {  // four neighbouring rows of a column are four neighbouring bytes
+    const float c[4] = {v[0][j], v[1][j], v[2][j], v[3][j]};
+    *reinterpret_cast<uint32_t*>(t8 + (8 * tx + j) * kWPitch + 4 * ty) = e4m3x4(c, sc.inv);
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < kBlock8 * kBlock8 / 4; i += kWThreads) {
+    const int c = i >> 5, w = i & 31;
+    *reinterpret_cast<uint32_t*>(q + base + (int64_t)(n0 + c) * R + r0 + 4 * w) =
+        *reinterpret_cast<const uint32_t*>(t8 + c * kWPitch + 4 * w);
+  }
+  if (threadIdx.x == 0) s[(e * (N / kBlock8) + blockIdx.y) * (R / kBlock8) + blockIdx.x] = sc.s;
+}
+
+__global__ void __launch_bounds__(kWThreads) dequantize_weights_kernel(const uint8_t* __restrict__ q,
+                                                                       const float* __restrict__ s, int R, int N,
+                                                                       __nv_bfloat16* __restrict__ W) {
+  __shared__ __align__(16) uint8_t t8[kBlock8 * kWPitch];  // [column][row]
+  const int r0 = blockIdx.x * kBlock8, n0 = blockIdx.y * kBlock8;
+  const int64_t e = blockIdx.z, base = e * R * N;
+  for (int i = threadIdx.x; i < kBlock8 * kBlock8 / 4; i += kWThreads) {
+    const int c = i >> 5, w = i & 31;
+    *reinterpret_cast<uint32_t*>(t8 + c * kWPitch + 4 * w) =
+        *reinterpret_cast<const uint32_t*>(q + base + (int64_t)(n0 + c) * R + r0 + 4 * w);
+  }
+  __syncthreads();
+  const float sc = s[(e * (N / kBlock8) + blockIdx.y) * (R / kBlock8) + blockIdx.x];
+  for (int i = threadIdx.x; i < kBlock8 * kBlock8 / 2; i += kWThreads) {
+    const int r = i >> 6, c = 2 * (i & 63);
+    float v[4];
+    e4m3_values((uint32_t)t8[c * kWPitch + r] | (uint32_t)t8[(c + 1) * kWPitch + r] << 8, sc, v);
+    *reinterpret_cast<uint32_t*>(W + base + (int64_t)(r0 + r) * N + n0 + c) = pack_bf16x2(v[0], v[1]);
+  }
+}
+
+// ------------------------------------------------------------------ routing
+// Rows for the slots: an expert's slots take its rows in any order (what a row
+// holds does not depend on its neighbours, and the sum of a token's slots goes
+// by slot), an id outside [0,E) takes none.
+constexpr int kChunkSlots = 4096, kRouteThreads = 512;
+
+__device__ __forceinline__ void count_chunk(const int32_t* ids, int64_t n, int E, int chunk, int* hist) {
+  for (int e = threadIdx.x; e < E; e += kRouteThreads) hist[e] = 0;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kChunkSlots / kRouteThreads; ++i) {
+    const int64_t j = (int64_t)chunk * kChunkSlots + i * kRouteThreads + threadIdx.x;
+    if (j < n && (unsigned)ids[j] < (unsigned)E) atomicAdd(&hist[ids[j]], 1);
+  }
+  __syncthreads();
+}
+
+__global__ void __launch_bounds__(kRouteThreads) route_count_kernel(const int32_t* __restrict__ ids, int64_t n, int E,
+                                                                    int32_t* __restrict__ cnt) {
+  __shared__ int hist[kMaxE];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  count_chunk(ids, n, E, blockIdx.x, hist);
+  for (int e = threadIdx.x; e < E; e += kRouteThreads) cnt[(int64_t)blockIdx.x * E + e] = hist[e];
+}
+
+// ONE: the slots are one chunk, counted here
+template <bool ONE>
+__global__ void __launch_bounds__(kRouteThreads) route_place_kernel(const int32_t* __restrict__ ids, int64_t n, int E,
+                                                                    const int32_t* cnt, int chunks, int32_t* hdr,
+                                                                    int32_t* tile_e, int32_t* pos) {
+  static_assert(kMaxE <= kRouteThreads, "a thread an expert");
+  __shared__ int hist[kMaxE];
+  __shared__ int warp_sums[kRouteThreads / 32];
+  const int e = threadIdx.x, lane = e & 31, wp = e >> 5;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (ONE) count_chunk(ids, n, E, 0, hist);
+  else asm volatile("griddepcontrol.wait;" ::: "memory");
+  int all = 0, before = 0;
+  if (e < E) {
+    if (ONE) {
+      all = hist[e];
+    } else {
+#pragma unroll 8
+      for (int c = 0; c < chunks; ++c) {
+        const int v = cnt[(int64_t)c * E + e];
+        all += v;
+        before += c < (int)blockIdx.x ? v : 0;
+      }
+    }
+  }
+  // padded row offsets: an exclusive sum over the experts
+  const int tiles = (all + 255) / 256;
+  int sum = tiles;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, sum, o);
+    if (lane >= o) sum += v;
+  }
+  if (lane == 31) warp_sums[wp] = sum;
+  __syncthreads();
+  int base = 0, total = 0;
+#pragma unroll
+  for (int i = 0; i < kRouteThreads / 32; ++i) {
+    base += i < wp ? warp_sums[i] : 0;
+    total += warp_sums[i];
+  }
+  const int first = base + sum - tiles;  // the expert's first row tile
+  if (e < E) hist[e] = first * 256 + before;
+  if (blockIdx.x == 0) {
+    for (int i = 0; i < tiles; ++i) tile_e[first + i] = e;
+    if (e == 0) {
+      hdr[0] = 0;
+      hdr[1] = total;
+    }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < kChunkSlots; i += kRouteThreads) {
+    const int64_t j = (int64_t)blockIdx.x * kChunkSlots + i;
+    if (j >= n) break;
+    const int id = ids[j];
+    pos[j] = (unsigned)id < (unsigned)E ? atomicAdd(&hist[id], 1) : -1;
+  }
+}
+
+// A token's row to the row of each of its slots, a warp a token; bf16 rows are
+// quantised on the way (T = uint8_t: given in 8 bits, with scales sx).  Scales
+// go to (d/128, rows), where the products' threads, a row each, read them side
+// by side.
+template <typename T>
+__global__ void __launch_bounds__(256) gather_rows_kernel(const T* __restrict__ x, const float* __restrict__ sx,
+                                                          const int32_t* pos, int64_t L, int d, int K, int64_t rows,
+                                                          uint8_t* __restrict__ x8, float* __restrict__ s8) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int lane = threadIdx.x & 31;
+  const int64_t t = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (t >= L) return;
+  const int mine = lane < K ? pos[t * K + lane] : -1;
+  if (!__any_sync(0xffffffffu, mine >= 0)) return;
+  int to[kMaxK];
+#pragma unroll
+  for (int k = 0; k < kMaxK; ++k) to[k] = __shfl_sync(0xffffffffu, mine, k);  // -1 from K on
+  if constexpr (sizeof(T) == 1) {
+    const uint4* src = reinterpret_cast<const uint4*>(x + t * d);
+    for (int c = lane; c < d / 16; c += 32) {
+      const uint4 v = src[c];
+#pragma unroll
+      for (int k = 0; k < kMaxK; ++k)
+        if (to[k] >= 0) reinterpret_cast<uint4*>(x8 + (int64_t)to[k] * d)[c] = v;
+    }
+    for (int b = lane; b < d / kBlock8; b += 32) {
+      const float v = sx[t * (d / kBlock8) + b];
+#pragma unroll
+      for (int k = 0; k < kMaxK; ++k)
+        if (to[k] >= 0) s8[b * rows + to[k]] = v;
+    }
+  } else {
+    for (int c0 = 0; c0 < d / 8; c0 += 32) {  // 8 columns a lane, 16 lanes a block
+      const int c = c0 + lane;
+      float v[8];
+      uint32_t m = 0u;
+      if (c < d / 8) {
+        load8(x + t * d + 8 * c, v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = max(m, abs_bits(v[i]));
+      }
+#pragma unroll
+      for (int k = 8; k > 0; k >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, k));
+      const Scale8 sc = scale8(m);
+      uint2 o = make_uint2(0u, 0u);
+      if (c < d / 8) o = make_uint2(e4m3x4(v, sc.inv), e4m3x4(v + 4, sc.inv));
+#pragma unroll
+      for (int k = 0; k < kMaxK; ++k) {
+        if (to[k] >= 0 && c < d / 8) {
+          reinterpret_cast<uint2*>(x8 + (int64_t)to[k] * d)[c] = o;
+          if ((lane & 15) == 0) s8[(int64_t)(c >> 4) * rows + to[k]] = sc.s;
+        }
+      }
+    }
+  }
+}
+
+// y[t] = sum_k gates[t,k] Y[pos[t,k]], slot by slot; four columns a thread.
+// NaN where the products gave up (hdr[0]).
+__global__ void __launch_bounds__(256) combine_rows_kernel(const float* Y, const int32_t* hdr, const int32_t* pos,
+                                                           const float* __restrict__ gates, int64_t L, int d, int K,
+                                                           __nv_bfloat16* __restrict__ y) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int per_row = d / 4;
+  if (i >= L * per_row) return;
+  const int64_t t = i / per_row;
+  const int c = (int)(i - t * per_row);
+  float4 v[kMaxK];
+  float g[kMaxK];
+#pragma unroll
+  for (int k = 0; k < kMaxK; ++k) {
+    g[k] = 0.f;
+    v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int r = k < K ? pos[t * K + k] : -1;
+    if (r >= 0) {
+      g[k] = gates[t * K + k];
+      v[k] = reinterpret_cast<const float4*>(Y + (int64_t)r * d)[c];
+    }
+  }
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int k = 0; k < kMaxK; ++k) {
+    o.x = fmaf(g[k], v[k].x, o.x);
+    o.y = fmaf(g[k], v[k].y, o.y);
+    o.z = fmaf(g[k], v[k].z, o.z);
+    o.w = fmaf(g[k], v[k].w, o.w);
+  }
+  if (hdr[0]) o.x = o.y = o.z = o.w = __uint_as_float(0x7fffffffu);
+  reinterpret_cast<uint2*>(y)[i] = make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
+}
+
 unsigned row_blocks(int64_t threads) {
   const int64_t need = (threads + kRowThreads - 1) / kRowThreads, most = (int64_t)sm_count() * 16;
   return (unsigned)(need < most ? need : most);
 }
 
+// a launch that may start while the one before it still runs (it waits for its results itself)
+template <typename... P, typename... A>
+cudaError_t launch_dependent(void (*kern)(P...), int64_t grid, int threads, cudaStream_t st, A... a) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, static_cast<P>(a)...);
+}
+
+int64_t route_chunks(const moeblaze_shape& s) { return (s.L * s.K + kChunkSlots - 1) / kChunkSlots; }
+
+// places of a call's scratch; bytes: how many it takes (base may be null)
+Fp8Scratch scratch(const moeblaze_shape& s, void* base, size_t* bytes) {
+  Fp8Scratch w;
+  w.rows = max_padded_rows(s.L * s.K, s.E);
+  size_t at = 0;
+  auto take = [&](size_t n) {
+    char* p = static_cast<char*>(base) + at;
+    at += align_up(n, 256);
+    return static_cast<void*>(p);
+  };
+  w.hdr = (int32_t*)take(256);
+  w.cnt = (int32_t*)take(sizeof(int32_t) * route_chunks(s) * s.E);
+  w.tile_e = (int32_t*)take(sizeof(int32_t) * (w.rows / 256));
+  w.pos = (int32_t*)take(sizeof(int32_t) * s.L * s.K);
+  w.x8 = (uint8_t*)take((size_t)w.rows * s.d);
+  w.sx = (float*)take(sizeof(float) * w.rows * (s.d / kBlock8));
+  w.h8 = (uint8_t*)take((size_t)w.rows * s.h);
+  w.sh = (float*)take(sizeof(float) * w.rows * (s.h / kBlock8));
+  w.y = (float*)take(sizeof(float) * w.rows * s.d);
+  *bytes = at;
+  return w;
+}
+
 }  // namespace
+
+size_t fp8_ws_bytes(const moeblaze_shape& s) {
+  size_t n = 0;
+  if (s.L > 0) scratch(s, nullptr, &n);
+  return n;
+}
+
+moeblaze_status launch_fp8_forward(const moeblaze_shape& s, const void* x, const float* x_scales, const int32_t* ids,
+                                   const float* gates, const moeblaze_fp8_experts& w, __nv_bfloat16* y, void* ws,
+                                   cudaStream_t st) {
+  if (s.L == 0) return MOEBLAZE_OK;
+  size_t n = 0;
+  const Fp8Scratch sc = scratch(s, ws, &n);
+  const int64_t slots = s.L * s.K, chunks = route_chunks(s);
+  if (chunks == 1) {
+    route_place_kernel<true><<<1, kRouteThreads, 0, st>>>(ids, slots, s.E, sc.cnt, 1, sc.hdr, sc.tile_e, sc.pos);
+    MB_CUDA(cudaGetLastError());
+  } else {
+    route_count_kernel<<<(unsigned)chunks, kRouteThreads, 0, st>>>(ids, slots, s.E, sc.cnt);
+    MB_CUDA(cudaGetLastError());
+    MB_CUDA(launch_dependent(route_place_kernel<false>, chunks, kRouteThreads, st, ids, slots, s.E, sc.cnt, (int)chunks,
+                             sc.hdr, sc.tile_e, sc.pos));
+    count_launch();
+  }
+  const int64_t warps = (s.L + 7) / 8;
+  if (x_scales)
+    MB_CUDA(launch_dependent(gather_rows_kernel<uint8_t>, warps, 256, st, (const uint8_t*)x, x_scales, sc.pos, s.L, s.d,
+                             s.K, sc.rows, sc.x8, sc.sx));
+  else
+    MB_CUDA(launch_dependent(gather_rows_kernel<__nv_bfloat16>, warps, 256, st, (const __nv_bfloat16*)x, x_scales, sc.pos,
+                             s.L, s.d, s.K, sc.rows, sc.x8, sc.sx));
+  count_launch(2);
+  const moeblaze_status r = launch_fp8_products(s, w, sc, st);
+  if (r != MOEBLAZE_OK) return r;
+  MB_CUDA(launch_dependent(combine_rows_kernel, (s.L * (s.d / 4) + 255) / 256, 256, st, sc.y, sc.hdr, sc.pos, gates, s.L,
+                           s.d, s.K, y));
+  count_launch();
+  return MOEBLAZE_OK;
+}
+
+moeblaze_status launch_fp8_quantize_weights(int E, int R, int N, int dtype, const void* W, void* q, float* scales,
+                                            cudaStream_t st) {
+  const dim3 g((unsigned)(R / kBlock8), (unsigned)(N / kBlock8), (unsigned)E);
+  if (dtype == MOEBLAZE_BF16)
+    quantize_weights_kernel<<<g, kWThreads, 0, st>>>((const __nv_bfloat16*)W, R, N, (uint8_t*)q, scales);
+  else
+    quantize_weights_kernel<<<g, kWThreads, 0, st>>>((const float*)W, R, N, (uint8_t*)q, scales);
+  MB_CUDA(cudaGetLastError());
+  count_launch();
+  return MOEBLAZE_OK;
+}
+
+moeblaze_status launch_fp8_dequantize_weights(int E, int R, int N, const void* q, const float* scales, void* W,
+                                              cudaStream_t st) {
+  const dim3 g((unsigned)(R / kBlock8), (unsigned)(N / kBlock8), (unsigned)E);
+  dequantize_weights_kernel<<<g, kWThreads, 0, st>>>((const uint8_t*)q, scales, R, N, (__nv_bfloat16*)W);
+  MB_CUDA(cudaGetLastError());
+  count_launch();
+  return MOEBLAZE_OK;
+}
 
 moeblaze_status launch_fp8_quantize_rows(int64_t L, int d, int dtype, const void* x, void* q, float* scales,
                                          cudaStream_t st) {

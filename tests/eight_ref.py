@@ -151,3 +151,49 @@ def rms_grad(dy, s, rstd, w, dsum):
     if dsum is not None:
         dx = dx + dsum.double()
     return dx, (dy.double() * xh).sum(0), xh, g
+
+
+def matrix8(q, s):
+    """What one e4m3 matrix (N,R) with scales (N/128, R/128) stands for, (R,N) in fp64."""
+    return (q.double() * s.double().repeat_interleave(128, 0).repeat_interleave(128, 1)).t()
+
+
+def experts8(x, ids, gates, mats):
+    """y (L,d) of 8-bit rows' values x (fp64) through 8-bit experts, and a bound on |y - kernel| before y's rounding.
+    mats: (q1, s1, q2, s2, q3, s3).  The hidden activations go to 8-bit rows by the definition; the kernel's are off by
+    fp32's roundings, which can push one over a border between two codes: what it may then be is what the bound counts."""
+    q1, s1, q2, s2, q3, s3 = mats
+    E, h, d = q1.shape
+    L, K = ids.shape
+    y = torch.zeros(L, d, dtype=torch.float64, device=x.device)
+    bound = torch.zeros_like(y)
+    for e in range(E):
+        t, k = torch.nonzero(ids == e, as_tuple=True)
+        if t.numel() == 0:
+            continue
+        w1, w3 = matrix8(q1[e], s1[e]), matrix8(q3[e], s3[e])
+        a, err = x[t] @ w1, 1.1 * (x[t].abs() @ w1.abs()) * matmul_err(d)
+        hid = silu(a)
+        if q2 is not None:
+            w2 = matrix8(q2[e], s2[e])
+            b = x[t] @ w2
+            err = err * b.abs() + hid.abs() * (x[t].abs() @ w2.abs()) * matmul_err(d)
+            hid = hid * b
+        err = err + (16 + 4 * a.abs()) * U32 * hid.abs()
+        codes, s = rows8(hid)
+        sc = grown(s, h)
+        val = codes * sc
+        off = torch.zeros_like(val)
+        for v in (hid - err, hid + err):                # the codes at the ends, at the block's scale
+            u = (v / sc).clamp(-448, 448)
+            _, ue = torch.frexp(u)
+            step = ((ue - 4).clamp(min=-9).long() + 1023 << 52).view(torch.float64)
+            off = torch.maximum(off, (torch.round(u / step) * step * sc - val).abs())
+        # a block whose largest value is next to a border between scales: subnormals round at twice, or half, the step
+        top, terr = blocks(hid).abs().amax(2), blocks(err).amax(2)
+        edge = ((top - terr <= 224 * s) | (top + terr > 448 * s)) & (s > 2.0 ** -126)
+        off = off + grown(edge.double() * s * 2.0 ** -9, h)
+        g = gates[t, k].double()[:, None]
+        y.index_add_(0, t, g * (val @ w3))
+        bound.index_add_(0, t, g.abs() * (off @ w3.abs() + matmul_err(h) * ((val.abs() + off) @ w3.abs())))
+    return y, bound + matmul_err(K) * y.abs()
