@@ -21,7 +21,8 @@ SRC = os.path.join(PKG, "csrc")
 OUT_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmoeblaze.so")
 SOURCES = ["abi.cu", "dispatch.cu", "identity.cu", "simt.cu", "gemm_tc.cu", "router.cu", "router_tc.cu", "norm.cu",
-           "balance.cu", "int4.cu", "router_grad_tc.cu", "rmsnorm.cu", "fp8.cu", "fp8_tc.cu"]
+           "balance.cu", "int4.cu", "router_grad_tc.cu", "rmsnorm.cu", "fp8.cu", "fp8_tc.cu",
+           "fp8_few.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "--expt-relaxed-constexpr", "-I", os.path.join(ROOT, "include")]

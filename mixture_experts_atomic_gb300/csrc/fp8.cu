@@ -375,12 +375,47 @@ Fp8Scratch scratch(const moeblaze_shape& s, void* base, size_t* bytes) {
   return w;
 }
 
+Fp8FewScratch few_scratch(const moeblaze_shape& s, void* base, size_t* bytes) {
+  Fp8FewScratch w;
+  w.rows = few_max_rows(s);
+  size_t at = 0;
+  auto take = [&](size_t n) {
+    char* p = static_cast<char*>(base) + at;
+    at += align_up(n, 256);
+    return static_cast<void*>(p);
+  };
+  w.hdr = (int32_t*)take(256);
+  w.entries = (int32_t*)take(16 * few_max_entries(s));
+  w.cnt = (int32_t*)take(sizeof(int32_t) * few_max_entries(s) * (few_tiles_up(s) + few_tiles_down(s)));
+  w.pos = (int32_t*)take(sizeof(int32_t) * s.L * s.K);
+  w.x8 = (uint8_t*)take((size_t)w.rows * s.d);
+  w.sx = (float*)take(sizeof(float) * w.rows * (s.d / kBlock8));
+  w.h8 = (uint8_t*)take((size_t)w.rows * s.h);
+  w.sh = (float*)take(sizeof(float) * w.rows * (s.h / kBlock8));
+  w.y = (float*)take(sizeof(float) * w.rows * s.d);
+  w.parts = (float*)take(sizeof(float) * sm_count() * 2 * 2 * few_part_tokens(s) * 128);
+  *bytes = at;
+  return w;
+}
+
+// The most tokens a call of this shape takes the path for few tokens with: the
+// slots fit its table, and the used experts have about a tile of them.
+constexpr int kFewPerExpert = 16;
+int64_t few_tokens(const moeblaze_shape& s) {
+  const int64_t slots = kFewPerExpert * (int64_t)s.E < kFewSlots ? kFewPerExpert * (int64_t)s.E : kFewSlots;
+  return slots / s.K;
+}
+
 }  // namespace
 
+// of any call of at most s.L tokens
 size_t fp8_ws_bytes(const moeblaze_shape& s) {
-  size_t n = 0;
-  if (s.L > 0) scratch(s, nullptr, &n);
-  return n;
+  size_t n = 0, m = 0;
+  moeblaze_shape f = s;
+  f.L = s.L < few_tokens(s) ? s.L : few_tokens(s);
+  if (f.L > 0) few_scratch(f, nullptr, &n);
+  if (s.L > few_tokens(s)) scratch(s, nullptr, &m);
+  return n > m ? n : m;
 }
 
 moeblaze_status launch_fp8_forward(const moeblaze_shape& s, const void* x, const float* x_scales, const int32_t* ids,
@@ -388,6 +423,15 @@ moeblaze_status launch_fp8_forward(const moeblaze_shape& s, const void* x, const
                                    cudaStream_t st) {
   if (s.L == 0) return MOEBLAZE_OK;
   size_t n = 0;
+  const int64_t combine = (s.L * (s.d / 4) + 255) / 256;
+  if (s.L <= few_tokens(s)) {
+    const Fp8FewScratch sc = few_scratch(s, ws, &n);
+    const moeblaze_status r = launch_fp8_few(s, x, x_scales, ids, w, sc, st);
+    if (r != MOEBLAZE_OK) return r;
+    MB_CUDA(launch_dependent(combine_rows_kernel, combine, 256, st, sc.y, sc.hdr, sc.pos, gates, s.L, s.d, s.K, y));
+    count_launch();
+    return MOEBLAZE_OK;
+  }
   const Fp8Scratch sc = scratch(s, ws, &n);
   const int64_t slots = s.L * s.K, chunks = route_chunks(s);
   if (chunks == 1) {
@@ -410,8 +454,7 @@ moeblaze_status launch_fp8_forward(const moeblaze_shape& s, const void* x, const
   count_launch(2);
   const moeblaze_status r = launch_fp8_products(s, w, sc, st);
   if (r != MOEBLAZE_OK) return r;
-  MB_CUDA(launch_dependent(combine_rows_kernel, (s.L * (s.d / 4) + 255) / 256, 256, st, sc.y, sc.hdr, sc.pos, gates, s.L,
-                           s.d, s.K, y));
+  MB_CUDA(launch_dependent(combine_rows_kernel, combine, 256, st, sc.y, sc.hdr, sc.pos, gates, s.L, s.d, s.K, y));
   count_launch();
   return MOEBLAZE_OK;
 }

@@ -373,19 +373,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) fp8_gemm
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(TMEM_COLS) : "memory");
 }
 
-// 2-D map of a row-major (rows x cols) byte matrix, boxes of 128 x 128
-bool byte_map(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows) {
-  EncodeTiledFn enc = encode_fn();
-  if (!enc) return false;
-  cuuint64_t dims[2] = {cols, rows};
-  cuuint64_t strides[1] = {cols};
-  cuuint32_t box[2] = {128, 128};
-  cuuint32_t es[2] = {1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, es,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 // the row scales (blocks, rows), boxes of one block of 128 rows
 bool scale_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t blocks) {
   EncodeTiledFn enc = encode_fn();
@@ -442,9 +429,9 @@ moeblaze_status launch_fp8_products(const moeblaze_shape& s, const moeblaze_fp8_
   p.N = s.h;
   p.kblocks = s.d / BK;
   p.n_tiles = sw ? s.h / 128 : (s.h + 255) / 256;
-  if (!byte_map(&p.tmA, ws.x8, s.d, ws.rows) || !scale_map(&p.tmS, ws.sx, ws.rows, s.d / BK) ||
-      !byte_map(&p.tmB0, w.q1, s.d, (uint64_t)s.E * s.h) ||
-      (sw && !byte_map(&p.tmB1, w.q2, s.d, (uint64_t)s.E * s.h)))
+  if (!byte_map(&p.tmA, ws.x8, s.d, ws.rows, 128) || !scale_map(&p.tmS, ws.sx, ws.rows, s.d / BK) ||
+      !byte_map(&p.tmB0, w.q1, s.d, (uint64_t)s.E * s.h, 128) ||
+      (sw && !byte_map(&p.tmB1, w.q2, s.d, (uint64_t)s.E * s.h, 128)))
     return MOEBLAZE_ERR_CUDA;
   moeblaze_status r = sw ? launch<UP_SWIGLU>(p, mt * p.n_tiles, st) : launch<UP_SILU>(p, mt * p.n_tiles, st);
   if (r != MOEBLAZE_OK) return r;
@@ -453,8 +440,8 @@ moeblaze_status launch_fp8_products(const moeblaze_shape& s, const moeblaze_fp8_
   p.N = s.d;
   p.kblocks = s.h / BK;
   p.n_tiles = (s.d + 255) / 256;
-  if (!byte_map(&p.tmA, ws.h8, s.h, ws.rows) || !scale_map(&p.tmS, ws.sh, ws.rows, s.h / BK) ||
-      !byte_map(&p.tmB0, w.q3, s.h, (uint64_t)s.E * s.d))
+  if (!byte_map(&p.tmA, ws.h8, s.h, ws.rows, 128) || !scale_map(&p.tmS, ws.sh, ws.rows, s.h / BK) ||
+      !byte_map(&p.tmB0, w.q3, s.h, (uint64_t)s.E * s.d, 128))
     return MOEBLAZE_ERR_CUDA;
   return launch<DOWN>(p, mt * p.n_tiles, st);
 }

@@ -72,6 +72,19 @@ SHAPES = [
     (12, 1408, 7168, 2, 2, "silu", None),
     (4, 14336, 128, 2, 1, "swiglu", None),
     (900, 2048, 1408, 8, 2, "swiglu", None),
+    # few tokens (at most 512 slots, 16 an expert): several tiles of an expert's tokens, tiles in parts, and the next
+    # number of tokens, which goes the other way
+    (64, 256, 512, 8, 2, "swiglu", 3),
+    (65, 256, 512, 8, 2, "swiglu", 3),
+    (64, 384, 640, 8, 2, "silu", 5),
+    (32, 2048, 256, 4, 2, "silu", 1),
+    (85, 128, 128, 64, 6, "swiglu", 9),
+    (86, 128, 128, 64, 6, "swiglu", 9),
+    (33, 640, 896, 30, 3, "silu", None),
+    (3, 2048, 2816, 16, 4, "swiglu", None),
+    (1, 4096, 4096, 2, 1, "silu", None),
+    (16, 128, 128, 1, 1, "swiglu", None),
+    (17, 128, 128, 1, 1, "swiglu", None),
 ]
 
 
@@ -144,7 +157,7 @@ def test_fp8_fewer_tokens_than_the_buffers_and_rows_behind():
         assert bool((ex._y[n:] == 3.0).all())                # rows behind the last token stay as they were
 
 
-@pytest.mark.parametrize("L", [3, 900])
+@pytest.mark.parametrize("L", [3, 60, 900])
 def test_fp8_graph_stream_and_two_objects(L):
     """A captured forward replays on new inputs; two objects on two streams at once do not meet."""
     d, h, E, K = 256, 512, 8, 2
@@ -231,9 +244,10 @@ def test_fp8_serving_chain():
     assert float((y.double() - y16.double()).norm() / y16.double().norm()) <= 2 ** -4
 
 
-def test_fp8_wait_limit():
+@pytest.mark.parametrize("L", [8, 600])
+def test_fp8_wait_limit(L):
     """A product whose first stage is never loaded gives up after the wait limit: y is NaN, and the next call is whole."""
-    L, d, h, E, K = 600, 256, 1024, 4, 2
+    d, h, E, K = 256, 1024, 4, 2
     x, ids, gates, mats = _problem(L, d, h, E, K, "swiglu", 9)
     ex = Fp8Experts(L, d, h, E, K)
     ex.load(*mats)
