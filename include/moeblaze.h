@@ -488,20 +488,26 @@ MOEBLAZE_API moeblaze_status moeblaze_fp8_dequantize_rows(int64_t L, int32_t d, 
  * with scales of powers of two as quantize_rows; the products take any scales.
  * R and N are multiples of 128, E <= 512. */
 typedef struct {
-  const void* q1;   /* (E,h,d): W1 */
+  const void* q1;   /* W1: (E,h,d), packed by moeblaze_fp8_pack */
   const float* s1;  /* (E, h/128, d/128) */
   const void* q2;   /* W2 (SwiGLU; NULL for SiLU) */
   const float* s2;
-  const void* q3;   /* (E,d,h): W3 */
+  const void* q3;   /* W3: (E,d,h) */
   const float* s3;  /* (E, d/128, h/128) */
 } moeblaze_fp8_experts;
 
 MOEBLAZE_API moeblaze_status moeblaze_fp8_quantize_weights(int32_t E, int32_t R, int32_t N, int32_t dtype,
                                                            const void* W, void* q, float* scales,
                                                            moeblaze_stream stream);
-/* W device (E,R,N) bf16, each value rounded once */
+/* the layout the products read, in as many bytes: 128 x 128 after 128 x 128 of
+ * q, in the order of their scales; packed must not be q itself */
+MOEBLAZE_API moeblaze_status moeblaze_fp8_pack(int32_t E, int32_t R, int32_t N, const void* q, void* packed,
+                                               moeblaze_stream stream);
+/* of q, or (packed != 0) of the packed layout: W device (E,R,N) bf16, each value
+ * rounded once */
 MOEBLAZE_API moeblaze_status moeblaze_fp8_dequantize_weights(int32_t E, int32_t R, int32_t N, const void* q,
-                                                             const float* scales, void* W, moeblaze_stream stream);
+                                                             int32_t packed, const float* scales, void* W,
+                                                             moeblaze_stream stream);
 
 /* moeblaze_fp8_forward:
  *   y[t] = sum_k gates[t,k] expert_{topk_ids[t,k]}(x[t])

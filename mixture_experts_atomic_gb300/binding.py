@@ -40,7 +40,7 @@ EXPORTS = [
     "moeblaze_int4_workspace_bytes", "moeblaze_int4_forward", "moeblaze_balance_backward_masked",
     "moeblaze_rmsnorm_forward", "moeblaze_rmsnorm_backward", "moeblaze_rmsnorm_backward_workspace_bytes",
     "moeblaze_fp8_quantize_rows", "moeblaze_fp8_dequantize_rows", "moeblaze_fp8_quantize_weights",
-    "moeblaze_fp8_dequantize_weights", "moeblaze_fp8_workspace_bytes", "moeblaze_fp8_forward",
+    "moeblaze_fp8_dequantize_weights", "moeblaze_fp8_workspace_bytes", "moeblaze_fp8_forward", "moeblaze_fp8_pack",
 ]
 
 # fixed scratch of moeblaze_dispatch_build_static (MOEBLAZE_STATIC_SCRATCH_BYTES)
@@ -128,7 +128,8 @@ def lib():
         for n in ["moeblaze_fp8_quantize_rows", "moeblaze_fp8_dequantize_rows"]:
             getattr(L, n).argtypes = [ctypes.c_int64, i32, i32, P, P, P, P]
         L.moeblaze_fp8_quantize_weights.argtypes = [i32, i32, i32, i32, P, P, P, P]
-        L.moeblaze_fp8_dequantize_weights.argtypes = [i32, i32, i32, P, P, P, P]
+        L.moeblaze_fp8_pack.argtypes = [i32, i32, i32, P, P, P]
+        L.moeblaze_fp8_dequantize_weights.argtypes = [i32, i32, i32, P, i32, P, P, P]
         L.moeblaze_fp8_forward.argtypes = [SP, P, P, P, P, ctypes.POINTER(Fp8Weights), P, P, sz, P]
         L.moeblaze_int4_quantize.argtypes = [i32, i32, i32, i32, i32, P, P, P, P]
         L.moeblaze_int4_pack.argtypes = [i32, i32, i32, i32, P, P, P, P, P]
@@ -312,8 +313,12 @@ def moeblaze_fp8_quantize_weights(E, R, N, dtype, W, q, scales, stream) -> int:
     return lib().moeblaze_fp8_quantize_weights(E, R, N, dtype, W, q, scales, stream)
 
 
-def moeblaze_fp8_dequantize_weights(E, R, N, q, scales, W, stream) -> int:
-    return lib().moeblaze_fp8_dequantize_weights(E, R, N, q, scales, W, stream)
+def moeblaze_fp8_pack(E, R, N, q, packed, stream) -> int:
+    return lib().moeblaze_fp8_pack(E, R, N, q, packed, stream)
+
+
+def moeblaze_fp8_dequantize_weights(E, R, N, q, packed, scales, W, stream) -> int:
+    return lib().moeblaze_fp8_dequantize_weights(E, R, N, q, int(packed), scales, W, stream)
 
 
 def moeblaze_fp8_workspace_bytes(shape: Shape) -> int:
@@ -866,15 +871,41 @@ def fp8_quantize_weights(W, stream=None):
     return q, s
 
 
+def fp8_pack(q, packed=None, stream=None):
+    """The layout the 8-bit products read, of q (E,N,R): a float8_e4m3fn tensor (E, N/128, R/128, 128, 128)."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q: expected a tensor of shape (E, N, R)")
+    E, N, R = q.shape
+    if E < 1 or R < 1 or N < 1 or R % 128 or N % 128:
+        raise MoEBlazeError(ERR_UNSUPPORTED, "moeblaze_fp8_pack")
+    _args((q, "q", (E, N, R), torch.float8_e4m3fn, False))
+    if packed is None:
+        packed = torch.empty((E, N // 128, R // 128, 128, 128), dtype=torch.float8_e4m3fn, device=q.device)
+    _args((packed, "packed", (E, N // 128, R // 128, 128, 128), torch.float8_e4m3fn, False))
+    st = moeblaze_fp8_pack(E, R, N, _ptr(q), _ptr(packed), _stream(stream))
+    _check(st, "moeblaze_fp8_pack")
+    return packed
+
+
 def fp8_dequantize_weights(q, scales, stream=None):
-    """The bf16 weights (E,R,N) that q (E,N,R) with scales (E, N/128, R/128) stands for."""
+    """The bf16 weights (E,R,N) that q (E,N,R), or its packed layout (fp8_pack), with scales (E, N/128, R/128) stands
+    for."""
+    if isinstance(q, torch.Tensor) and q.dim() == 5:
+        E, nb, rb = q.shape[:3]
+        N, R = 128 * nb, 128 * rb
+        _args((q, "q", (E, nb, rb, 128, 128), torch.float8_e4m3fn, False),
+              (scales, "scales", (E, nb, rb), torch.float32, False))
+        W = torch.empty((E, R, N), dtype=torch.bfloat16, device=q.device)
+        st = moeblaze_fp8_dequantize_weights(E, R, N, _ptr(q), True, _ptr(scales), _ptr(W), _stream(stream))
+        _check(st, "moeblaze_fp8_dequantize_weights")
+        return W
     if not isinstance(q, torch.Tensor) or q.dim() != 3:
         raise ValueError("q: expected a tensor of shape (E, N, R)")
     E, N, R = q.shape
     _args((q, "q", (E, N, R), torch.float8_e4m3fn, False),
           (scales, "scales", (E, N // 128, R // 128), torch.float32, False))
     W = torch.empty((E, R, N), dtype=torch.bfloat16, device=q.device)
-    st = moeblaze_fp8_dequantize_weights(E, R, N, _ptr(q), _ptr(scales), _ptr(W), _stream(stream))
+    st = moeblaze_fp8_dequantize_weights(E, R, N, _ptr(q), False, _ptr(scales), _ptr(W), _stream(stream))
     _check(st, "moeblaze_fp8_dequantize_weights")
     return W
 

@@ -118,8 +118,8 @@ moeblaze_status check_rows8(int64_t L, int d, int dtype, const void* x, const vo
 // checks of one matrix of 8-bit weights and of the layer on them
 moeblaze_status check_fp8_matrix(int E, int R, int N) {
   if (E < 1 || R < 1 || N < 1) return MOEBLAZE_ERR_INVALID_ARG;
-  // (a block of 128 x 128 each in the launch's grid; rows of all experts' matrices are counted in 32 bits)
-  if (E > kMaxE || R % 128 != 0 || N % 128 != 0 || N / 128 > 65535 || (int64_t)E * N > INT32_MAX - 256)
+  // (a block of 128 x 128 each in the launch's grid; the blocks' rows are counted in 32 bits, with a block past the end)
+  if (E > kMaxE || R % 128 != 0 || N % 128 != 0 || N / 128 > 65535 || (int64_t)E * (N + 128) >= INT32_MAX / (R / 128))
     return MOEBLAZE_ERR_UNSUPPORTED;
   return MOEBLAZE_OK;
 }
@@ -578,12 +578,19 @@ moeblaze_status moeblaze_fp8_quantize_weights(int32_t E, int32_t R, int32_t N, i
   return launch_fp8_quantize_weights(E, R, N, dtype, W, q, scales, reinterpret_cast<cudaStream_t>(stream));
 }
 
-moeblaze_status moeblaze_fp8_dequantize_weights(int32_t E, int32_t R, int32_t N, const void* q, const float* scales,
-                                                void* W, moeblaze_stream stream) {
+moeblaze_status moeblaze_fp8_pack(int32_t E, int32_t R, int32_t N, const void* q, void* packed, moeblaze_stream stream) {
+  const moeblaze_status r = check_fp8_matrix(E, R, N);
+  if (r != MOEBLAZE_OK) return r;
+  if (!ok_ptr(q) || !ok_ptr(packed)) return MOEBLAZE_ERR_INVALID_ARG;
+  return launch_fp8_pack(E, R, N, q, packed, reinterpret_cast<cudaStream_t>(stream));
+}
+
+moeblaze_status moeblaze_fp8_dequantize_weights(int32_t E, int32_t R, int32_t N, const void* q, int32_t packed,
+                                                const float* scales, void* W, moeblaze_stream stream) {
   const moeblaze_status r = check_fp8_matrix(E, R, N);
   if (r != MOEBLAZE_OK) return r;
   if (!ok_ptr(W) || !ok_ptr(q) || !ok_ptr4(scales)) return MOEBLAZE_ERR_INVALID_ARG;
-  return launch_fp8_dequantize_weights(E, R, N, q, scales, W, reinterpret_cast<cudaStream_t>(stream));
+  return launch_fp8_dequantize_weights(E, R, N, q, packed != 0, scales, W, reinterpret_cast<cudaStream_t>(stream));
 }
 
 size_t moeblaze_fp8_workspace_bytes(const moeblaze_shape* s) {

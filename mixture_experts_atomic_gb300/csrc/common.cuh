@@ -177,7 +177,8 @@ moeblaze_status launch_fp8_dequantize_rows(int64_t L, int d, int dtype, const vo
                                            cudaStream_t st);
 moeblaze_status launch_fp8_quantize_weights(int E, int R, int N, int dtype, const void* W, void* q, float* scales,
                                             cudaStream_t st);
-moeblaze_status launch_fp8_dequantize_weights(int E, int R, int N, const void* q, const float* scales, void* W,
+moeblaze_status launch_fp8_pack(int E, int R, int N, const void* q, void* packed, cudaStream_t st);
+moeblaze_status launch_fp8_dequantize_weights(int E, int R, int N, const void* q, bool packed, const float* scales, void* W,
                                               cudaStream_t st);
 size_t fp8_ws_bytes(const moeblaze_shape& s);
 moeblaze_status launch_fp8_forward(const moeblaze_shape& s, const void* x, const float* x_scales, const int32_t* ids,

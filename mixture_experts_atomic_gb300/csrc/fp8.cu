@@ -132,6 +132,25 @@ __global__ void __launch_bounds__(kWThreads) quantize_weights_kernel(const T* __
   if (threadIdx.x == 0) s[(e * (N / kBlock8) + blockIdx.y) * (R / kBlock8) + blockIdx.x] = sc.s;
 }
 
+// The layout the products read: blocks of 128 x 128 one after the other, each
+// output's 128 bytes side by side.  A CTA that walks along the reduction then
+// reads 16 KB after 16 KB of neighbouring memory, in place of 128 bytes from each
+// of 128 rows (one token, d 4096, h 14336: the down projection, whose rows are
+// 14 KB apart, ran at 2.0 TB/s so).
+__global__ void __launch_bounds__(256) pack_weights_kernel(const uint4* __restrict__ q, int R, int N,
+                                                           uint4* __restrict__ out) {
+  const int64_t e = blockIdx.z;
+  const uint4* src = q + (e * N + (int64_t)blockIdx.y * kBlock8) * (R / 16) + blockIdx.x * (kBlock8 / 16);
+  uint4* dst = out + ((e * (N / kBlock8) + blockIdx.y) * (R / kBlock8) + blockIdx.x) * (kBlock8 * kBlock8 / 16);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int j = threadIdx.x + 256 * i;
+    dst[j] = src[(int64_t)(j >> 3) * (R / 16) + (j & 7)];
+  }
+}
+
+// PACKED: of the layout above
+template <bool PACKED>
 __global__ void __launch_bounds__(kWThreads) dequantize_weights_kernel(const uint8_t* __restrict__ q,
                                                                        const float* __restrict__ s, int R, int N,
                                                                        __nv_bfloat16* __restrict__ W) {
@@ -140,8 +159,8 @@ __global__ void __launch_bounds__(kWThreads) dequantize_weights_kernel(const uin
   const int64_t e = blockIdx.z, base = e * R * N;
   for (int i = threadIdx.x; i < kBlock8 * kBlock8 / 4; i += kWThreads) {
     const int c = i >> 5, w = i & 31;
-    *reinterpret_cast<uint32_t*>(t8 + c * kWPitch + 4 * w) =
-        *reinterpret_cast<const uint32_t*>(q + base + (int64_t)(n0 + c) * R + r0 + 4 * w);
+    const int64_t at = PACKED ? ((int64_t)(n0 * (R / kBlock8) + r0) + c) * kBlock8 + 4 * w : (int64_t)(n0 + c) * R + r0 + 4 * w;
+    *reinterpret_cast<uint32_t*>(t8 + c * kWPitch + 4 * w) = *reinterpret_cast<const uint32_t*>(q + base + at);
   }
   __syncthreads();
   const float sc = s[(e * (N / kBlock8) + blockIdx.y) * (R / kBlock8) + blockIdx.x];
@@ -471,10 +490,19 @@ moeblaze_status launch_fp8_quantize_weights(int E, int R, int N, int dtype, cons
   return MOEBLAZE_OK;
 }
 
-moeblaze_status launch_fp8_dequantize_weights(int E, int R, int N, const void* q, const float* scales, void* W,
+moeblaze_status launch_fp8_pack(int E, int R, int N, const void* q, void* packed, cudaStream_t st) {
+  const dim3 g((unsigned)(R / kBlock8), (unsigned)(N / kBlock8), (unsigned)E);
+  pack_weights_kernel<<<g, 256, 0, st>>>((const uint4*)q, R, N, (uint4*)packed);
+  MB_CUDA(cudaGetLastError());
+  count_launch();
+  return MOEBLAZE_OK;
+}
+
+moeblaze_status launch_fp8_dequantize_weights(int E, int R, int N, const void* q, bool packed, const float* scales, void* W,
                                               cudaStream_t st) {
   const dim3 g((unsigned)(R / kBlock8), (unsigned)(N / kBlock8), (unsigned)E);
-  dequantize_weights_kernel<<<g, kWThreads, 0, st>>>((const uint8_t*)q, scales, R, N, (__nv_bfloat16*)W);
+  auto kern = packed ? dequantize_weights_kernel<true> : dequantize_weights_kernel<false>;
+  kern<<<g, kWThreads, 0, st>>>((const uint8_t*)q, scales, R, N, (__nv_bfloat16*)W);
   MB_CUDA(cudaGetLastError());
   count_launch();
   return MOEBLAZE_OK;

@@ -65,4 +65,10 @@ inline bool byte_map(CUtensorMap* m, const void* base, uint64_t cols, uint64_t r
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// packed weights: a block of 128 x 128 is 128 rows of 128 bytes, row
+// ((e N/128 + n/128) R/128 + r/128) 128 + n % 128
+inline bool weight_map(CUtensorMap* m, const void* base, int E, int N, int R) {
+  return byte_map(m, base, 128, (uint64_t)E * N * (R / 128), 128);
+}
+
 }  // namespace moeblaze

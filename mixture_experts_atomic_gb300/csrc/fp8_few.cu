@@ -45,7 +45,7 @@ enum Mode : int { UP_SWIGLU = 0, UP_SILU, DOWN };
 
 struct FewParams {
   CUtensorMap tmX;   // tokens (rows, R) bytes, boxes of 16 rows
-  CUtensorMap tmW0;  // weights (E N, R) bytes, boxes of 128 rows
+  CUtensorMap tmW0;  // packed weights
   CUtensorMap tmW1;  // W2 (SwiGLU)
   const int32_t* meta;   // hdr: [1] entries; entries of {expert, first row, tokens, 0}
   const int4* entries;
@@ -176,9 +176,11 @@ __global__ void __launch_bounds__(THREADS, 2) fp8_few_kernel(const __grid_consta
         const uint32_t full = bar(B_FULL + s), dst = smem_base + s * STAGE_BYTES;
         mbar_expect_tx(full, (w.two ? 2 : 1) * W_BYTES + w.chunks * (16 * BK + 64));
         used |= 1u << s;
-        const int r = w.e * p.N + w.m * (MODE == UP_SWIGLU ? 128 : 256);
-        tma_load_2d(dst, &p.tmW0, w.kb * BK, r, full);
-        if (w.two) tma_load_2d(dst + W_BYTES, MODE == UP_SWIGLU ? &p.tmW1 : &p.tmW0, w.kb * BK, MODE == UP_SWIGLU ? r : r + 128, full);
+        const int64_t blk = (int64_t)w.e * (p.N / 128) + w.m * (MODE == UP_SWIGLU ? 1 : 2);
+        const int r = (int)((blk * p.kblocks + w.kb) * 128);
+        tma_load_2d(dst, &p.tmW0, 0, r, full);
+        if (w.two)
+          tma_load_2d(dst + W_BYTES, MODE == UP_SWIGLU ? &p.tmW1 : &p.tmW0, 0, MODE == UP_SWIGLU ? r : r + p.kblocks * 128, full);
       };
       auto tokens = [&](const Place<MODE>& w, int s, int slot) {
         const uint32_t full = bar(B_FULL + s), dst = smem_base + s * STAGE_BYTES + 2 * W_BYTES;
@@ -601,9 +603,8 @@ moeblaze_status launch_fp8_few(const moeblaze_shape& s, const void* x, const flo
   p.N = s.h;
   p.kblocks = s.d / BK;
   p.tiles = up;
-  const uint64_t wrows = (uint64_t)s.E * s.h;
-  if (!byte_map(&p.tmX, ws.x8, s.d, ws.rows, 16) || !byte_map(&p.tmW0, w.q1, s.d, wrows, 128) ||
-      (sw && !byte_map(&p.tmW1, w.q2, s.d, wrows, 128)))
+  if (!byte_map(&p.tmX, ws.x8, s.d, ws.rows, 16) || !weight_map(&p.tmW0, w.q1, s.E, s.h, s.d) ||
+      (sw && !weight_map(&p.tmW1, w.q2, s.E, s.h, s.d)))
     return MOEBLAZE_ERR_CUDA;
   const int ctas = sm_count();
   moeblaze_status r = sw ? launch_few<UP_SWIGLU>(p, ctas, st) : launch_few<UP_SILU>(p, ctas, st);
@@ -615,7 +616,7 @@ moeblaze_status launch_fp8_few(const moeblaze_shape& s, const void* x, const flo
   p.N = s.d;
   p.kblocks = s.h / BK;
   p.tiles = down;
-  if (!byte_map(&p.tmX, ws.h8, s.h, ws.rows, 16) || !byte_map(&p.tmW0, w.q3, s.h, (uint64_t)s.E * s.d, 128))
+  if (!byte_map(&p.tmX, ws.h8, s.h, ws.rows, 16) || !weight_map(&p.tmW0, w.q3, s.E, s.d, s.h))
     return MOEBLAZE_ERR_CUDA;
   return launch_few<DOWN>(p, ctas, st);
 }

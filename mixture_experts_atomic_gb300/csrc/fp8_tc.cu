@@ -60,7 +60,7 @@ enum Mode : int { UP_SWIGLU = 0, UP_SILU, DOWN };
 
 struct Params {
   CUtensorMap tmA;   // rows (rows, R) bytes
-  CUtensorMap tmB0;  // weights (E N, R) bytes
+  CUtensorMap tmB0;  // packed weights
   CUtensorMap tmB1;  // W2 (SwiGLU)
   CUtensorMap tmS;   // rows' scales (R/128, rows) fp32
   const int32_t* hdr;
@@ -197,14 +197,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) fp8_gemm
         const Tile t = decode(p, tile, num_mt);
         const CUtensorMap* mb = MODE == UP_SWIGLU && rank ? &p.tmB1 : &p.tmB0;
         const int arow = t.row0 + (int)rank * BM;
-        const int brow = t.e * p.N + (MODE == UP_SWIGLU ? t.n0 * 128 : t.n0 * 256 + (int)rank * 128);
+        // (past the last block of a matrix lies the next one's, or nothing: what it gives is not kept)
+        const int64_t blk = (int64_t)t.e * (p.N / 128) + (MODE == UP_SWIGLU ? t.n0 : t.n0 * 2 + (int)rank);
+        const int brow = (int)(blk * p.kblocks * 128);
         for (int kb = 0; kb < p.kblocks; ++kb) {
           if (!(ok = wait_bounded(bar(B_EMPTY + s), ph ^ 1u, abort_s, p.err, p.wait_ns))) break;
           const uint32_t full = lead(B_FULL + s), dst = smem_base + s * STAGE_BYTES;
           if (!(MODE == DOWN && p.withhold && tile == first && kb == 0)) {
             arrive_expect_pair(full, STAGE_BYTES + BM * 4);
             tma_load_pair(dst, &p.tmA, kb * BK, arow, full);
-            tma_load_pair(dst + TILE_BYTES, mb, kb * BK, brow, full);
+            tma_load_pair(dst + TILE_BYTES, mb, 0, brow + kb * 128, full);
             tma_load_pair(smem_u32(scales + slot * BM), &p.tmS, arow, kb, full);
             used |= 1u << s;
           }
@@ -430,8 +432,8 @@ moeblaze_status launch_fp8_products(const moeblaze_shape& s, const moeblaze_fp8_
   p.kblocks = s.d / BK;
   p.n_tiles = sw ? s.h / 128 : (s.h + 255) / 256;
   if (!byte_map(&p.tmA, ws.x8, s.d, ws.rows, 128) || !scale_map(&p.tmS, ws.sx, ws.rows, s.d / BK) ||
-      !byte_map(&p.tmB0, w.q1, s.d, (uint64_t)s.E * s.h, 128) ||
-      (sw && !byte_map(&p.tmB1, w.q2, s.d, (uint64_t)s.E * s.h, 128)))
+      !weight_map(&p.tmB0, w.q1, s.E, s.h, s.d) ||
+      (sw && !weight_map(&p.tmB1, w.q2, s.E, s.h, s.d)))
     return MOEBLAZE_ERR_CUDA;
   moeblaze_status r = sw ? launch<UP_SWIGLU>(p, mt * p.n_tiles, st) : launch<UP_SILU>(p, mt * p.n_tiles, st);
   if (r != MOEBLAZE_OK) return r;
@@ -441,7 +443,7 @@ moeblaze_status launch_fp8_products(const moeblaze_shape& s, const moeblaze_fp8_
   p.kblocks = s.h / BK;
   p.n_tiles = (s.d + 255) / 256;
   if (!byte_map(&p.tmA, ws.h8, s.h, ws.rows, 128) || !scale_map(&p.tmS, ws.sh, ws.rows, s.h / BK) ||
-      !byte_map(&p.tmB0, w.q3, s.h, (uint64_t)s.E * s.d, 128))
+      !weight_map(&p.tmB0, w.q3, s.E, s.d, s.h))
     return MOEBLAZE_ERR_CUDA;
   return launch<DOWN>(p, mt * p.n_tiles, st);
 }

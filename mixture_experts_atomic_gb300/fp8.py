@@ -33,7 +33,7 @@ class Fp8Experts:
             raise B.MoEBlazeError(B.ERR_UNSUPPORTED, "moeblaze_fp8_workspace_bytes")
         self._ws = B._bytes(n, device)
         self._y = torch.empty((max_tokens, d), dtype=torch.bfloat16, device=device)
-        self._kept: Optional[tuple] = None
+        self._packed: dict = {}
         self._weights: Optional[B.Fp8Weights] = None
         self._shapes: dict = {}
 
@@ -41,14 +41,12 @@ class Fp8Experts:
         return B.make_shape(L, self.d, self.h, self.E, self.K, torch.bfloat16, self.act)
 
     def load(self, q1, s1, q2, s2, q3, s3):
-        """Take weights as they are (no copy; they are read by every forward): q1, q2 (E,h,d), q3 (E,d,h)
-        float8_e4m3fn, each output's row along the reduction, and fp32 scales (E,N/128,R/128) of each 128 x 128
-        (q2, s2 None for SiLU).  All of them or, when a tensor is refused, none."""
+        """Pack 8-bit weights: q1, q2 (E,h,d), q3 (E,d,h) float8_e4m3fn, each output's row along the reduction, and
+        fp32 scales (E,N/128,R/128) of each 128 x 128 (q2, s2 None for SiLU).  The copies replace earlier ones in
+        place, all of them or, when a tensor is refused, none."""
         mats = [("1", q1, s1, self.h, self.d), ("3", q3, s3, self.d, self.h)]
         if self.act == "swiglu":
             mats.insert(1, ("2", q2, s2, self.h, self.d))
-        else:
-            q2 = s2 = None
         specs = []
         for n, q, s, N, R in mats:
             specs += [(q, "q" + n, (self.E, N, R), torch.float8_e4m3fn, False),
@@ -57,8 +55,13 @@ class Fp8Experts:
         for t, name, *_ in specs:
             if t.device != self._ws.device:  # the products read the weights beside the buffers
                 raise ValueError(f"{name}: on {t.device}, but the buffers are on {self._ws.device}")
-        self._kept = (q1, s1, q2, s2, q3, s3)
-        self._weights = B.Fp8Weights(*[B._ptr(t) for t in self._kept])
+        for n, q, s, N, R in mats:
+            old = self._packed.get(n)
+            packed = B.fp8_pack(q, None if old is None else old[0])
+            self._packed[n] = (packed, s.clone() if old is None else old[1].copy_(s))
+        p = {n: tuple(t.data_ptr() for t in v) for n, v in self._packed.items()}
+        w1, w2, w3 = p["1"], p.get("2", (None, None)), p["3"]
+        self._weights = B.Fp8Weights(w1[0], w1[1], w2[0], w2[1], w3[0], w3[1])
 
     def quantize(self, W1, W2, W3):
         """Quantise bf16 or fp32 weights in the layer's layout (W2 None for SiLU)."""
@@ -69,10 +72,9 @@ class Fp8Experts:
 
     def dequantize(self):
         """(W1, W2, W3) in bf16, as MoELayer.forward takes them (W2 None for SiLU)."""
-        if self._kept is None:
+        if self._weights is None:
             raise RuntimeError("Fp8Experts: load or quantize weights first")
-        q1, s1, q2, s2, q3, s3 = self._kept
-        return tuple(None if q is None else B.fp8_dequantize_weights(q, s) for q, s in ((q1, s1), (q2, s2), (q3, s3)))
+        return tuple(B.fp8_dequantize_weights(*self._packed[n]) if n in self._packed else None for n in "123")
 
     def forward(self, x, topk_ids, gates, x_scales=None) -> torch.Tensor:
         """y (L,d) for the L <= max_tokens rows of x: bf16, or 8-bit rows with their scales (RMSNorm.forward8,

@@ -7,6 +7,7 @@ import torch
 
 from mixture_experts_atomic_gb300 import binding as B
 from mixture_experts_atomic_gb300.block import MoEBlock, RMSNorm
+from mixture_experts_atomic_gb300.fp8 import Fp8Experts
 from mixture_experts_atomic_gb300.layer import MoELayer
 
 BF, F = torch.bfloat16, torch.float32
@@ -137,3 +138,77 @@ def test_rms_and_rows8_binding_refusals():
         norm.forward8(torch.zeros(4, 72, dtype=BF), torch.ones(72))
     with pytest.raises(ValueError, match="norm"):
         MoEBlock(4, 128, 128, 2, 1, BF, device="cpu", norm="batch")
+
+
+def _fp8_weights(**over):
+    return B.Fp8Weights(**{**{k: OKP.value for k in ("q1", "s1", "q2", "s2", "q3", "s3")}, **over})
+
+
+def test_fp8_status():
+    sh = lambda L=8, d=128, h=256, E=4, K=2, dt=BF, act="swiglu", fl=0: B.make_shape(L, d, h, E, K, dt, act, fl)  # noqa: E731
+    need = B.moeblaze_fp8_workspace_bytes
+    assert need(sh()) > 0 and need(sh(L=0)) == 0
+    sizes = [need(sh(L=L)) for L in (1, 2, 16, 31, 32, 33, 64, 100, 1000, 5000)]
+    assert sizes == sorted(sizes)                            # buffers for max_tokens hold every smaller call
+    for bad in (sh(dt=F), sh(act="identity"), sh(K=5), sh(L=-1), sh(d=64), sh(h=130), sh(E=513), sh(E=512, h=1 << 22)):
+        assert need(bad) == 0
+
+    def fwd(s, x=OKP, xs=None, ids=OKP, g=OKP, w=None, y=OKP, ws=OKP, n=1 << 40):
+        return B.moeblaze_fp8_forward(s, x, xs, ids, g, w or _fp8_weights(), y, ws, n, None)
+
+    assert fwd(sh(dt=F)) == B.ERR_UNSUPPORTED and fwd(sh(act="identity")) == B.ERR_UNSUPPORTED
+    assert fwd(sh(K=5)) == B.ERR_INVALID_ARG
+    for k in ("x", "ids", "g", "y", "ws"):
+        assert fwd(sh(), **{k: None}) == B.ERR_INVALID_ARG, k
+    for k in ("x", "y", "ws"):
+        assert fwd(sh(), **{k: BAD}) == B.ERR_INVALID_ARG, k
+    for k in ("q1", "s1", "q2", "s2", "q3", "s3"):
+        assert fwd(sh(), w=_fp8_weights(**{k: None})) == B.ERR_INVALID_ARG, k
+    for k in ("q1", "q2", "q3"):
+        assert fwd(sh(), w=_fp8_weights(**{k: BAD.value})) == B.ERR_INVALID_ARG, k
+    assert fwd(sh(), n=need(sh()) - 1) == B.ERR_WORKSPACE
+    assert fwd(sh(L=0), x=None, ids=None, g=None, y=None, ws=None) == B.OK
+    assert B.moeblaze_fp8_quantize_weights(2, 128, 200, B.BF16, OKP, OKP, OKP, None) == B.ERR_UNSUPPORTED
+    assert B.moeblaze_fp8_quantize_weights(0, 128, 128, B.BF16, OKP, OKP, OKP, None) == B.ERR_INVALID_ARG
+    assert B.moeblaze_fp8_quantize_weights(2, 128, 128, 5, OKP, OKP, OKP, None) == B.ERR_INVALID_ARG
+    assert B.moeblaze_fp8_quantize_weights(2, 128, 128, B.F32, BAD, OKP, OKP, None) == B.ERR_INVALID_ARG
+    assert B.moeblaze_fp8_pack(2, 128, 128, OKP, BAD, None) == B.ERR_INVALID_ARG
+    assert B.moeblaze_fp8_pack(2, 100, 128, OKP, OKP, None) == B.ERR_UNSUPPORTED
+    assert B.moeblaze_fp8_dequantize_weights(2, 128, 128, None, 0, OKP, OKP, None) == B.ERR_INVALID_ARG
+    assert B.moeblaze_fp8_dequantize_weights(513, 128, 128, OKP, 1, OKP, OKP, None) == B.ERR_UNSUPPORTED
+
+
+def test_fp8_binding_refusals():
+    f8 = torch.float8_e4m3fn
+    with pytest.raises(B.MoEBlazeError):
+        Fp8Experts(8, 100, 128, 4, 2, device="cpu")
+    ex = Fp8Experts(8, 128, 256, 4, 2, device="cpu")
+    z = lambda *s, dt=f8: torch.zeros(*s, dtype=dt)  # noqa: E731
+    x, ids, g = z(3, 128, dt=BF), z(3, 2, dt=torch.int32), z(3, 2, dt=F)
+    with pytest.raises(RuntimeError, match="load"):
+        ex.forward(x, ids, g)
+    with pytest.raises(RuntimeError, match="load"):
+        ex.dequantize()
+    ok = [z(4, 256, 128), z(4, 2, 1, dt=F), z(4, 256, 128), z(4, 2, 1, dt=F), z(4, 128, 256), z(4, 1, 2, dt=F)]
+    for i, bad in ((0, z(4, 128, 256)), (1, z(4, 1, 2, dt=F)), (2, None), (3, z(4, 2, 1, dt=BF)), (4, z(4, 128, 256, dt=BF)),
+                   (5, z(4, 2, 1, dt=F)), (0, z(4, 128, 256).transpose(1, 2))):
+        args = list(ok)
+        args[i] = bad
+        with pytest.raises(ValueError):
+            ex.load(*args)
+    with pytest.raises(ValueError, match="CUDA"):
+        ex.load(*ok)
+    assert ex._weights is None
+    ex._weights = _fp8_weights()
+    with pytest.raises(ValueError, match="at most 8"):
+        ex.forward(z(9, 128, dt=BF), z(9, 2, dt=torch.int32), z(9, 2, dt=F))
+    for a in ((x.float(), ids, g), (x, ids.long(), g), (x, ids, g[:2]), (x[:, :64], ids, g), (z(3, 128), ids, g),
+              (x, ids, g, z(3, 1, dt=F)), (z(3, 128), ids, g, z(3, 2, dt=F))):
+        with pytest.raises(ValueError):
+            ex.forward(*a)
+    with pytest.raises(ValueError):
+        B.fp8_quantize_weights(z(128, 128, dt=BF))
+    with pytest.raises(ValueError):
+        B.fp8_quantize_weights(z(1, 128, 128, dt=torch.half))
+    with pytest.raises(B.MoEBlazeError):
+        B.fp8_pack(z(1, 100, 128))

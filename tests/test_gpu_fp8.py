@@ -211,6 +211,9 @@ def test_quantize_weights_to_the_bit(E, K, N, dt):
     back = B.fp8_dequantize_weights(q, s)
     want = torch.stack([R.matrix8(q[e], s[e]) for e in range(E)])
     assert torch.equal(back.double(), want)                  # four bits of mantissa: exact
+    packed = B.fp8_pack(q)
+    assert torch.equal(packed.view(torch.uint8), q.view(torch.uint8).view(E, N // 128, 128, K // 128, 128).transpose(2, 3))
+    assert torch.equal(B.fp8_dequantize_weights(packed, s), back)
     any_s = s * 0.7
     want = torch.stack([R.matrix8(q[e].float(), any_s[e]) for e in range(E)]).float().to(BF16)
     off = (B.fp8_dequantize_weights(q, any_s).double() - want.double()).abs()
@@ -218,6 +221,33 @@ def test_quantize_weights_to_the_bit(E, K, N, dt):
     W[0, 5, 7] = float("nan")
     q, s = B.fp8_quantize_weights(W)
     assert bool(s[0, 0, 0].isnan()) and not bool(s[1:].isnan().any())
+
+
+def test_fp8_load_replaces_weights_in_place():
+    """A graph captured on one set of weights runs on the next one loaded; a refused tensor leaves all as they were."""
+    L, d, h, E, K = 20, 256, 384, 4, 2
+    x, ids, gates, mats = _problem(L, d, h, E, K, "swiglu", 1)
+    _, _, _, mats2 = _problem(L, d, h, E, K, "swiglu", 2)
+    ex, other = Fp8Experts(L, d, h, E, K), Fp8Experts(L, d, h, E, K)
+    ex.load(*mats)
+    other.load(*mats2)
+    want, want2 = ex.forward(x, ids, gates).clone(), other.forward(x, ids, gates).clone()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = ex.forward(x, ids, gates)
+    for bad in (0, 3, 5):
+        broken = list(mats2)
+        broken[bad] = broken[bad][:, :1].contiguous()
+        with pytest.raises(ValueError):
+            ex.load(*broken)
+    graph.replay()
+    assert torch.equal(y, want)
+    ex.load(*mats2)
+    for m in mats2:
+        m.view(torch.uint8).zero_()                          # the object keeps copies
+    graph.replay()
+    assert torch.equal(y, want2)
 
 
 def test_fp8_serving_chain():
@@ -235,7 +265,8 @@ def test_fp8_serving_chain():
     ids, gates = torch.empty(L, K, dtype=torch.int32, device="cuda"), torch.empty(L, K, device="cuda")
     B.router_forward(shape, u, r(d, E) / d ** 0.5, None, ids, gates)
     y = ex.forward(q, ids, gates, s)
-    want, bound = R.experts8(q.double() * R.grown(s, d), ids, gates, ex._kept)
+    mats = [m for w in W for m in B.fp8_quantize_weights(w)]
+    want, bound = R.experts8(q.double() * R.grown(s, d), ids, gates, mats)
     R.inside(y, want, bound + R.BF * (want.abs() + bound) + 1e-30, "y")
     layer = MoELayer(L, d, h, E, K, BF16, "swiglu")
     layer.dispatch(ids)
