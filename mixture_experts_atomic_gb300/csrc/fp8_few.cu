@@ -332,10 +332,14 @@ __global__ void __launch_bounds__(THREADS, 2) fp8_few_kernel(const __grid_consta
         };
         float* mine = part(blockIdx.x, k0 == 0 ? 1 : 0);
 #pragma unroll
-        for (int half = 0; half < 2; ++half)
+        for (int k = 0; k < TOKENS / 16; ++k)
+          if (k < w.chunks) {
 #pragma unroll
-          for (int i = 0; i < TOKENS; ++i)
-            if (i < 16 * w.chunks) __stcg(mine + (half * p.part_tokens + i) * 128, acc[half][i]);
+            for (int i = 16 * k; i < 16 * k + 16; ++i) {
+              __stcg(mine + i * 128, acc[0][i]);
+              __stcg(mine + (p.part_tokens + i) * 128, acc[1][i]);
+            }
+          }
         __threadfence();
         if (!(ok = sync())) break;
         // the CTAs that share the tile: block x belongs to CTA ((x + 1) ctas - 1) / total
@@ -349,11 +353,22 @@ __global__ void __launch_bounds__(THREADS, 2) fp8_few_kernel(const __grid_consta
         for (int i = 0; i < TOKENS; ++i) acc[0][i] = acc[1][i] = 0.f;
         for (int64_t c = c0; c <= c1; ++c) {
           const float* q = part(c, c == c0 ? 1 : 0);
+          // (32 loads in flight: one after the other they took 25 us of a token's 122)
 #pragma unroll
-          for (int half = 0; half < 2; ++half)
+          for (int k = 0; k < TOKENS / 16; ++k)
+            if (k < w.chunks) {
+              float v[2][16];
 #pragma unroll
-            for (int i = 0; i < TOKENS; ++i)
-              if (i < 16 * w.chunks) acc[half][i] += __ldcg(q + (half * p.part_tokens + i) * 128);
+              for (int i = 0; i < 16; ++i) {
+                v[0][i] = __ldcg(q + (16 * k + i) * 128);
+                v[1][i] = __ldcg(q + (p.part_tokens + 16 * k + i) * 128);
+              }
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                acc[0][16 * k + i] += v[0][i];
+                acc[1][16 * k + i] += v[1][i];
+              }
+            }
         }
       }
       if constexpr (MODE == DOWN) {
