@@ -110,10 +110,14 @@ __device__ __forceinline__ void mma_pair(uint32_t tmem_d, uint64_t a, uint64_t b
 __device__ __forceinline__ void commit_at(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
-// at the same place in both CTAs: a commit each
-__device__ __forceinline__ void commit_pair(uint32_t bar) {
-  commit_at(peer_addr(bar, 0));
-  commit_at(peer_addr(bar, 1));
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(one));
+  return one != 0;
 }
 
 struct Tile {
@@ -158,7 +162,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) fp8_gemm
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(bar(B_FULL + s), 2);    // both CTAs' producers
-      mbar_init(bar(B_EMPTY + s), 1);   // the commit
+      mbar_init(bar(B_EMPTY + s), 1);   // a scaling warp that has seen the stage's MMAs end
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(bar(B_TFULL + b), 1);
@@ -215,33 +219,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) fp8_gemm
         }
       }
       // what is in flight lands before the CTA leaves: each stage used is
-      // released once more by its last MMAs, or the wait runs out
+      // released once more after its last MMAs, or the wait runs out
       for (int i = 0; i < STAGES; ++i) {
         if (used & (1u << s)) wait_bounded(bar(B_EMPTY + s), ph ^ 1u, nullptr, nullptr, ok ? p.wait_ns : kDrainNs);
         if (++s == STAGES) { s = 0; ph ^= 1u; }
       }
-    } else if (warp == 1 && lane == 0 && rank == 0) {
+    } else if (warp == 1 && rank == 0) {
       // ================================================================ MMA issuer
+      // The whole warp walks along, so that what it computes is uniform, and one
+      // lane issues.  (One lane alone in the loop took 1240 cycles a block, of
+      // them 430 for four MMAs and 270 for four commits; a stage's release is
+      // left to the scaling warps, which see the same MMAs end.)
       int s = 0, buf = 0;
+      const bool one = elect_one();
       uint32_t ph = 0, bph = 0;
       bool ok = true;
+      const uint32_t tfull[2][2] = {{peer_addr(bar(B_TFULL), 0), peer_addr(bar(B_TFULL), 1)},
+                                    {peer_addr(bar(B_TFULL + 1), 0), peer_addr(bar(B_TFULL + 1), 1)}};
       for (int tile = first; ok && tile < total; tile += step) {
         for (int kb = 0; kb < p.kblocks; ++kb) {
-          if (!(ok = wait_bounded(bar(B_TEMPTY + buf), bph ^ 1u, abort_s, p.err, p.wait_ns))) break;
-          if (!(ok = wait_bounded(bar(B_FULL + s), ph, abort_s, p.err, p.wait_ns))) break;
+          ok = wait_bounded(bar(B_TEMPTY + buf), bph ^ 1u, abort_s, p.err, p.wait_ns) &&
+               wait_bounded(bar(B_FULL + s), ph, abort_s, p.err, p.wait_ns);
+          if (!(ok = __all_sync(0xffffffffu, ok ? 1 : 0) != 0)) break;
           tc_fence_after();
-          const uint32_t a = smem_base + s * STAGE_BYTES, b = a + TILE_BYTES;
+          const uint64_t a = smem_desc(smem_base + s * STAGE_BYTES, 16, 1024);
+          const uint64_t b = a + (TILE_BYTES >> 4);  // (addresses in units of 16 bytes, below 2^18)
+          if (one) {
 #pragma unroll
-          for (int kk = 0; kk < BK / 32; ++kk)
-            mma_pair(tmem_base + buf * 256, smem_desc(a + kk * 32, 16, 1024), smem_desc(b + kk * 32, 16, 1024), kk ? 1u : 0u);
-          commit_pair(bar(B_EMPTY + s));
-          commit_pair(bar(B_TFULL + buf));
+            for (int kk = 0; kk < BK / 32; ++kk) mma_pair(tmem_base + buf * 256, a + 2 * kk, b + 2 * kk, kk ? 1u : 0u);
+            commit_at(tfull[buf][0]);
+            commit_at(tfull[buf][1]);
+          }
+          __syncwarp();
           if (++s == STAGES) { s = 0; ph ^= 1u; }
           if (++buf == 2) { buf = 0; bph ^= 1u; }
         }
       }
       // all MMAs retire before TMEM is released
-      commit_at(lead(B_DRAIN));
+      if (one) commit_at(lead(B_DRAIN));
+      __syncwarp();
       wait_bounded(bar(B_DRAIN), 0, nullptr, nullptr, ok ? p.wait_ns : kDrainNs);
     }
     __syncwarp();
@@ -252,7 +268,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) fp8_gemm
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
     // column of chunk c (32 columns) in an accumulator
     auto col = [&](int c) { return MODE == UP_SWIGLU ? c * 128 + part * 32 : part * 64 + c * 32; };
-    int buf = 0, turn = 0, slot = 0;
+    int buf = 0, turn = 0, slot = 0, stage = 0;
     uint32_t bph = 0;
     bool ok = true;
     for (int tile = first; tile < total; tile += step, turn ^= 1) {
@@ -286,6 +302,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) fp8_gemm
         const float m1 = MODE == UP_SWIGLU ? __shfl_sync(0xffffffffu, cw1, kb & 31) : m0;
         ok = __all_sync(0xffffffffu, wait_bounded(bar(B_TFULL + buf), bph, abort_s, p.err, p.wait_ns) ? 1 : 0) != 0;
         if (!ok) break;
+        if (warp == 4 && lane == 0) mbar_arrive(bar(B_EMPTY + stage));
+        stage = stage == STAGES - 1 ? 0 : stage + 1;
         // (landed: the MMAs waited for the stage that it came with)
         const float sr = scales[slot * BM + r];
         slot = slot == SLOTS - 1 ? 0 : slot + 1;
