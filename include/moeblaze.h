@@ -516,12 +516,13 @@ MOEBLAZE_API moeblaze_status moeblaze_fp8_dequantize_weights(int32_t E, int32_t 
  *   x        device (L,d): with x_scales (L, d/128) fp32 e4m3 rows, without
  *            (NULL) bf16 rows, which are brought to 8 bits as quantize_rows does
  *   topk_ids device (L,K) int32; an id outside [0,E) is an empty slot (its gate
- *            is not read), one that a token names more than once counts once
- *            for each slot; a token without any gives a row of zeros
+ *            does not count, NaN or not), one that a token names more than once
+ *            counts once for each slot; a token without any gives a row of zeros
  *   gates    device (L,K) fp32       y device (L,d) bf16, overwritten
  *   ws       device moeblaze_fp8_workspace_bytes(s) bytes
  * Products are exact and summed in fp32; the hidden activations go to 8-bit
- * rows between the two products.  Results are repeatable to the bit.  y is NaN
+ * rows between the two products, and with many tokens a slot's row is rounded
+ * to fp16 before the sum over its token's slots.  Results are repeatable to the bit.  y is NaN
  * where a bounded device-side wait ran out. */
 MOEBLAZE_API size_t moeblaze_fp8_workspace_bytes(const moeblaze_shape* s);
 MOEBLAZE_API moeblaze_status moeblaze_fp8_forward(const moeblaze_shape* s, const void* x, const float* x_scales,

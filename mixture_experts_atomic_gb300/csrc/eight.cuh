@@ -42,6 +42,13 @@ __device__ __forceinline__ Scale8 scale8(uint32_t bits) {
   return Scale8{__uint_as_float((uint32_t)k << 23), __uint_as_float((uint32_t)(254 - k) << 23)};
 }
 
+// the same for fp16: the largest comes to 2^14 or more
+__device__ __forceinline__ Scale8 scale16(uint32_t bits) {
+  if (bits >= 0x7f800000u) return Scale8{__uint_as_float(0x7fffffffu), 0.f};
+  const int k = max((int)(bits >> 23) - 14, 1);
+  return Scale8{__uint_as_float((uint32_t)k << 23), __uint_as_float((uint32_t)(254 - k) << 23)};
+}
+
 // four values, the first in the low byte
 __device__ __forceinline__ uint32_t e4m3x4(const float* v, float inv) {
   const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[0] * inv, v[1] * inv), __NV_SATFINITE, __NV_E4M3);

@@ -314,39 +314,60 @@ __global__ void __launch_bounds__(256) gather_rows_kernel(const T* __restrict__ 
   }
 }
 
-// y[t] = sum_k gates[t,k] Y[pos[t,k]], slot by slot; four columns a thread.
-// NaN where the products gave up (hdr[0]).
-__global__ void __launch_bounds__(256) combine_rows_kernel(const float* Y, const int32_t* hdr, const int32_t* pos,
-                                                           const float* __restrict__ gates, int64_t L, int d, int K,
-                                                           __nv_bfloat16* __restrict__ y) {
+// y[t] = sum_k gates[t,k] Y[pos[t,k]], slot by slot; eight columns a thread.
+// Y fp32, or fp16 with scales sy (d/128, rows).  NaN where the products gave up
+// (hdr[0]).  KM: slots whose loads are in flight together (all of them).
+// Bound by HBM: 8192 x 4096, 2 slots: 200 MB.
+__device__ __forceinline__ void eight(const float* p, float* v) { load8(p, v); }
+__device__ __forceinline__ void eight(const __half* p, float* v) {
+  const uint4 u = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+    v[2 * i] = f.x;
+    v[2 * i + 1] = f.y;
+  }
+}
+template <typename T, int KM>
+__global__ void __launch_bounds__(256) combine_rows_kernel(const T* Y, const float* sy, int64_t rows, const int32_t* hdr,
+                                                           const int32_t* pos, const float* __restrict__ gates, int64_t L,
+                                                           int d, int K, __nv_bfloat16* __restrict__ y) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int per_row = d / 4;
+  const int per_row = d / 8;
   if (i >= L * per_row) return;
-  const int64_t t = i / per_row;
+  const int64_t t = i <= 0xffffffffll ? (uint32_t)i / (uint32_t)per_row : i / per_row;
   const int c = (int)(i - t * per_row);
-  float4 v[kMaxK];
-  float g[kMaxK];
+  float v[KM][8], g[KM];
+  int r[KM];
 #pragma unroll
-  for (int k = 0; k < kMaxK; ++k) {
-    g[k] = 0.f;
-    v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-    const int r = k < K ? pos[t * K + k] : -1;
-    if (r >= 0) {
-      g[k] = gates[t * K + k];
-      v[k] = reinterpret_cast<const float4*>(Y + (int64_t)r * d)[c];
-    }
-  }
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int k = 0; k < KM; ++k) r[k] = k < K ? pos[t * K + k] : -1;
 #pragma unroll
-  for (int k = 0; k < kMaxK; ++k) {
-    o.x = fmaf(g[k], v[k].x, o.x);
-    o.y = fmaf(g[k], v[k].y, o.y);
-    o.z = fmaf(g[k], v[k].z, o.z);
-    o.w = fmaf(g[k], v[k].w, o.w);
+  for (int k = 0; k < KM; ++k) {
+    // (an empty slot reads row 0 and leaves it: branches around the loads would
+    // put one behind the other, 221 in place of 85 us at 16000 x 2048, 6 slots)
+    const int64_t row = max(r[k], 0);
+    const float gate = k < K ? gates[t * K + k] : 0.f;
+    const float scale = sizeof(T) == 2 ? sy[(int64_t)(c / (kBlock8 / 8)) * rows + row] : 1.f;
+    eight(Y + row * d + 8 * c, v[k]);
+    g[k] = r[k] >= 0 ? gate * scale : 0.f;
   }
-  if (hdr[0]) o.x = o.y = o.z = o.w = __uint_as_float(0x7fffffffu);
-  reinterpret_cast<uint2*>(y)[i] = make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
+#pragma unroll
+  for (int k = 0; k < KM; ++k)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[k][j] = r[k] >= 0 ? v[k][j] : 0.f;
+  float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int k = 0; k < KM; ++k)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) o[j] = fmaf(g[k], v[k][j], o[j]);
+  if (hdr[0]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) o[j] = __uint_as_float(0x7fffffffu);
+  }
+  reinterpret_cast<uint4*>(y)[i] = make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]),
+                                              pack_bf16x2(o[6], o[7]));
 }
 
 unsigned row_blocks(int64_t threads) {
@@ -389,7 +410,8 @@ Fp8Scratch scratch(const moeblaze_shape& s, void* base, size_t* bytes) {
   w.sx = (float*)take(sizeof(float) * w.rows * (s.d / kBlock8));
   w.h8 = (uint8_t*)take((size_t)w.rows * s.h);
   w.sh = (float*)take(sizeof(float) * w.rows * (s.h / kBlock8));
-  w.y = (float*)take(sizeof(float) * w.rows * s.d);
+  w.y = (__half*)take(sizeof(__half) * w.rows * s.d);
+  w.sy = (float*)take(sizeof(float) * w.rows * (s.d / kBlock8));
   *bytes = at;
   return w;
 }
@@ -417,6 +439,12 @@ Fp8FewScratch few_scratch(const moeblaze_shape& s, void* base, size_t* bytes) {
   return w;
 }
 
+template <typename T>
+auto combine_kernel(int K) {
+  return K <= 2 ? combine_rows_kernel<T, 2> : K <= 4 ? combine_rows_kernel<T, 4>
+       : K <= 6 ? combine_rows_kernel<T, 6> : combine_rows_kernel<T, kMaxK>;
+}
+
 // The most tokens a call of this shape takes the path for few tokens with: the
 // slots fit its table, and the used experts have about a tile of them.
 constexpr int kFewPerExpert = 16;
@@ -442,12 +470,13 @@ moeblaze_status launch_fp8_forward(const moeblaze_shape& s, const void* x, const
                                    cudaStream_t st) {
   if (s.L == 0) return MOEBLAZE_OK;
   size_t n = 0;
-  const int64_t combine = (s.L * (s.d / 4) + 255) / 256;
+  const int64_t combine = (s.L * (s.d / 8) + 255) / 256;
   if (s.L <= few_tokens(s)) {
     const Fp8FewScratch sc = few_scratch(s, ws, &n);
     const moeblaze_status r = launch_fp8_few(s, x, x_scales, ids, w, sc, st);
     if (r != MOEBLAZE_OK) return r;
-    MB_CUDA(launch_dependent(combine_rows_kernel, combine, 256, st, sc.y, sc.hdr, sc.pos, gates, s.L, s.d, s.K, y));
+    MB_CUDA(launch_dependent(combine_kernel<float>(s.K), combine, 256, st, sc.y, (const float*)nullptr, sc.rows, sc.hdr,
+                             sc.pos, gates, s.L, s.d, s.K, y));
     count_launch();
     return MOEBLAZE_OK;
   }
@@ -473,7 +502,8 @@ moeblaze_status launch_fp8_forward(const moeblaze_shape& s, const void* x, const
   count_launch(2);
   const moeblaze_status r = launch_fp8_products(s, w, sc, st);
   if (r != MOEBLAZE_OK) return r;
-  MB_CUDA(launch_dependent(combine_rows_kernel, combine, 256, st, sc.y, sc.hdr, sc.pos, gates, s.L, s.d, s.K, y));
+  MB_CUDA(launch_dependent(combine_kernel<__half>(s.K), combine, 256, st, sc.y, sc.sy, sc.rows, sc.hdr, sc.pos, gates, s.L,
+                           s.d, s.K, y));
   count_launch();
   return MOEBLAZE_OK;
 }

@@ -1,6 +1,8 @@
 // What the 8-bit experts' steps share: the scratch of one call.
 #pragma once
 
+#include <cuda_fp16.h>
+
 #include "common.cuh"
 #include "tc_ptx.cuh"
 
@@ -17,7 +19,8 @@ struct Fp8Scratch {
   float* sx;         // (d/128, rows)
   uint8_t* h8;       // (rows, h)
   float* sh;         // (h/128, rows)
-  float* y;          // (rows, d)
+  __half* y;         // (rows, d), with a scale for each 128 columns
+  float* sy;         // (d/128, rows)
   int64_t rows;
 };
 

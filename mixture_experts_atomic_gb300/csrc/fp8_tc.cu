@@ -15,17 +15,17 @@
 // reduction brings 32 KB to an SM for 8.4 MFLOP; one CTA with a 128 x 256 tile
 // would take 48 KB, and what L2 delivers to the SMs is what bounds such tiles.
 // Each block of the reduction goes to one of two TMEM accumulators of 256
-// columns, which sixteen warps read back, scale and add to their registers (64
+// columns, which eight warps read back, scale and add to their registers (128
 // a thread) while the other one is computed: 512 cycles of tensor pipe beside
 // 256 of TMEM reads and 128 of packed FMAs.
 //
 //   warp 0        producer: TMA loads of both operands (each CTA its own; all of
 //                 a stage's loads complete on rank 0's barrier)
 //   warp 1        TMEM allocation; in rank 0 the MMA issuer
-//   warps 4-19    scaling: a row a thread, 32 columns of A and 32 of B (SwiGLU)
-//                 or 64 columns; then the tile's epilogue
-// The first warpgroup gives registers to the others (setmaxnreg: 56 + 4 x 104 a
-// thread, of 5 x 96 at launch).
+//   warps 4-11    scaling: a row a thread, 64 columns of A and 64 of B (SwiGLU)
+//                 or 128 columns; then the tile's epilogue
+// The first warpgroup gives registers to the others (setmaxnreg: 40 + 2 x 232 a
+// thread, of 3 x 168 at launch).
 //
 // Row space: an expert's rows are a segment of a padded row space, 256-row
 // aligned (fp8.cu); padding rows hold anything, and what they give is not read.
@@ -45,10 +45,10 @@ constexpr int BM = 128, BK = 128;              // rows of a CTA; a block of the 
 constexpr int TILE_BYTES = BM * BK;            // 16 KB of either operand
 constexpr int STAGES = 6;
 constexpr int STAGE_BYTES = 2 * TILE_BYTES;
-constexpr int SCALE_WARPS = 16;
+constexpr int SCALE_WARPS = 8;
 constexpr int THREADS = 128 + 32 * SCALE_WARPS;
 constexpr int TMEM_COLS = 512;
-constexpr int XCHG_BYTES = 2 * 4 * BM * 4;     // largest magnitudes of a row's four parts, of two tiles in turn
+constexpr int XCHG_BYTES = 2 * 2 * BM * 4;     // largest magnitudes of a row's two parts, of two tiles in turn
 // A block's row scales come with its stage, but are read when its sums are: they
 // have a ring of their own.  The loads of block i + 8 wait for the MMAs of block
 // i + 2, which wait for block i's sums to be read, scales and all.
@@ -69,8 +69,8 @@ struct Params {
   const float* s0;   // weights' scales (E, N/128, R/128)
   const float* s1;
   uint8_t* h8;       // up: H8 (rows, N)
-  float* sh;         // up: its scales (N/128, rows)
-  float* y;          // down: (rows, N) fp32
+  float* sh;         // scales of H8 or y (N/128, rows)
+  __half* y;         // down: (rows, N)
   int64_t rows;
   int N, kblocks, n_tiles;
   uint64_t wait_ns;
@@ -135,9 +135,10 @@ __device__ __forceinline__ Tile decode(const Params& p, int tile, int num_mt) {
   return t;
 }
 
-__device__ __forceinline__ void st_v8(float* p, const float* v) {
-  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]),
-               "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+// a whole sector of a row (rows lie far apart: 16 bytes would be half of one)
+__device__ __forceinline__ void store32(void* p, const uint32_t* v) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                : "memory");
 }
 
@@ -191,7 +192,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) fp8_gemm
   const int first = blockIdx.x / 2, step = gridDim.x / 2;
 
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
     if (warp == 0 && lane == 0) {
       // ================================================================ producer
       int s = 0, slot = 0;
@@ -238,8 +239,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) fp8_gemm
                                     {peer_addr(bar(B_TFULL + 1), 0), peer_addr(bar(B_TFULL + 1), 1)}};
       for (int tile = first; ok && tile < total; tile += step) {
         for (int kb = 0; kb < p.kblocks; ++kb) {
-          ok = wait_bounded(bar(B_TEMPTY + buf), bph ^ 1u, abort_s, p.err, p.wait_ns) &&
-               wait_bounded(bar(B_FULL + s), ph, abort_s, p.err, p.wait_ns);
+          ok = wait_bounded(bar(B_FULL + s), ph, abort_s, p.err, p.wait_ns) &&
+               wait_bounded(bar(B_TEMPTY + buf), bph ^ 1u, abort_s, p.err, p.wait_ns);
           if (!(ok = __all_sync(0xffffffffu, ok ? 1 : 0) != 0)) break;
           tc_fence_after();
           const uint64_t a = smem_desc(smem_base + s * STAGE_BYTES, 16, 1024);
@@ -247,8 +248,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) fp8_gemm
           if (one) {
 #pragma unroll
             for (int kk = 0; kk < BK / 32; ++kk) mma_pair(tmem_base + buf * 256, a + 2 * kk, b + 2 * kk, kk ? 1u : 0u);
-            commit_at(tfull[buf][0]);
             commit_at(tfull[buf][1]);
+            commit_at(tfull[buf][0]);
           }
           __syncwarp();
           if (++s == STAGES) { s = 0; ph ^= 1u; }
@@ -263,11 +264,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) fp8_gemm
     __syncwarp();
   } else {
     // ================================================================ scaling and epilogue
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
     const int quarter = warp & 3, part = (warp - 4) >> 2, r = quarter * 32 + lane;
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
     // column of chunk c (32 columns) in an accumulator
-    auto col = [&](int c) { return MODE == UP_SWIGLU ? c * 128 + part * 32 : part * 64 + c * 32; };
+    auto col = [&](int c) { return MODE == UP_SWIGLU ? (c >> 1) * 128 + part * 64 + (c & 1) * 32 : part * 128 + c * 32; };
     int buf = 0, turn = 0, slot = 0, stage = 0;
     uint32_t bph = 0;
     bool ok = true;
@@ -276,14 +277,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) fp8_gemm
       const int q = t.row0 + (int)rank * BM + r;
       const int nb = p.N / kBlock8;
       // the block of this thread's columns (SwiGLU: the tile's, in both matrices)
-      const int blk = MODE == UP_SWIGLU ? t.n0 : t.n0 * 2 + (part >> 1);
+      const int blk = MODE == UP_SWIGLU ? t.n0 : t.n0 * 2 + part;
       const bool in = MODE == UP_SWIGLU || blk < nb;
       const int64_t so = ((int64_t)t.e * nb + (in ? blk : nb - 1)) * p.kblocks;
       const float* w0 = p.s0 + so;
       const float* w1 = MODE == UP_SWIGLU ? p.s1 + so : nullptr;
-      float2 acc[32];
+      float2 acc[64];
 #pragma unroll
-      for (int i = 0; i < 32; ++i) acc[i] = make_float2(0.f, 0.f);
+      for (int i = 0; i < 64; ++i) acc[i] = make_float2(0.f, 0.f);
       // the weights' scales: 32 blocks' at a time, one a lane, handed round by shuffles
       float cw0 = 0.f, cw1 = 0.f, nw0, nw1 = 0.f;
       auto fetch_w = [&](int kb) {
@@ -309,52 +310,68 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) fp8_gemm
         slot = slot == SLOTS - 1 ? 0 : slot + 1;
         tc_fence_after();
         const uint32_t tb = tmem_base + lanes + buf * 256;
-        uint32_t ra[16];  // (16 columns at a time: 32 want 16 registers more, which spill; 0.89 against 1.10 ms)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          MB_TMEM_LD16(tb + col(c >> 1) + 16 * (c & 1), ra);
-          tmem_wait_ld();
-          if (c == 3) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) arrive_pair(lead(B_TEMPTY + buf));
-          }
+        uint32_t ra[32], rb[32];
+        auto add = [&](const uint32_t (&v)[32], int c) {
           const float m = sr * (c < 2 ? m0 : m1);
           const float2 mm = make_float2(m, m);
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            acc[c * 8 + i] = __ffma2_rn(make_float2(__uint_as_float(ra[2 * i]), __uint_as_float(ra[2 * i + 1])), mm,
-                                         acc[c * 8 + i]);
-        }
+          for (int i = 0; i < 16; ++i)
+            acc[c * 16 + i] = __ffma2_rn(make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), mm, acc[c * 16 + i]);
+        };
+        MB_TMEM_LD32(tb + col(0), ra);
+        MB_TMEM_LD32(tb + col(1), rb);
+        tmem_wait_ld();
+        add(ra, 0);
+        add(rb, 1);
+        MB_TMEM_LD32(tb + col(2), ra);
+        MB_TMEM_LD32(tb + col(3), rb);
+        tmem_wait_ld();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_pair(lead(B_TEMPTY + buf));
+        add(ra, 2);
+        add(rb, 3);
         if (++buf == 2) { buf = 0; bph ^= 1u; }
       }
       if (!ok) break;
       // (a block of the last half tile that does not exist is computed and left)
       if constexpr (MODE == DOWN) {
         if (in) {
-          float* dst = p.y + (int64_t)q * p.N + blk * kBlock8 + (part & 1) * 64;
+          // fp16 at a power of two that brings the largest to 2^14 or more: a
+          // rounding of 2^-11 in front of the 2^-8 of y's own, at half of fp32's
+          // bytes, which the combine step reads again
+          uint32_t m = 0u;
 #pragma unroll
-          for (int i = 0; i < 32; i += 4) {
-            const float v[8] = {acc[i].x, acc[i].y, acc[i + 1].x, acc[i + 1].y, acc[i + 2].x, acc[i + 2].y, acc[i + 3].x,
-                                acc[i + 3].y};
-            st_v8(dst + 2 * i, v);
+          for (int i = 0; i < 64; ++i) m = max(m, max(abs_bits(acc[i].x), abs_bits(acc[i].y)));
+          const Scale8 sc = scale16(m);
+          __half* dst = p.y + (int64_t)q * p.N + blk * kBlock8;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            uint32_t o[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const __half2 h = __floats2half2_rn(acc[8 * i + j].x * sc.inv, acc[8 * i + j].y * sc.inv);
+              o[j] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+            store32(dst + 16 * i, o);
           }
+          p.sh[(int64_t)blk * p.rows + q] = sc.s;
         }
       } else {
         constexpr bool SW = MODE == UP_SWIGLU;
-        constexpr int NH = SW ? 16 : 32;  // pairs of hidden columns of this thread
+        constexpr int NH = SW ? 32 : 64;  // pairs of hidden columns of this thread
         uint32_t m = 0u;
 #pragma unroll
         for (int i = 0; i < NH; ++i) {
           float2 a = acc[i];
           a.x = a.x * __fdividef(1.f, 1.f + __expf(-a.x));
           a.y = a.y * __fdividef(1.f, 1.f + __expf(-a.y));
-          if constexpr (SW) a = __fmul2_rn(a, acc[16 + i]);
+          if constexpr (SW) a = __fmul2_rn(a, acc[32 + i]);
           acc[i] = a;
           m = max(m, max(abs_bits(a.x), abs_bits(a.y)));
         }
-        {  // the block's other columns are the other parts'
-          uint32_t* x = xchg + turn * 4 * BM;
+        if constexpr (SW) {  // the block's other 64 columns are the other part's
+          uint32_t* x = xchg + turn * 2 * BM;
           x[part * BM + r] = m;
           mbar_arrive(bar(B_XCHG));
           // (an mbarrier, so that this wait is bounded too)
@@ -362,25 +379,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) fp8_gemm
           ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
           if (!ok) break;
           (void)mbar_try(bar(B_XCHG), (uint32_t)turn);
-          if constexpr (SW) m = max(max(x[r], x[BM + r]), max(x[2 * BM + r], x[3 * BM + r]));
-          else m = max(m, x[(part ^ 1) * BM + r]);
+          m = max(x[r], x[BM + r]);
         }
         const Scale8 sc = scale8(m);
         if (in) {
-          const int c0 = blk * kBlock8 + (SW ? part * 32 : (part & 1) * 64);
-          uint4* dst = reinterpret_cast<uint4*>(p.h8 + (int64_t)q * p.N + c0);
+          const int c0 = blk * kBlock8 + (SW ? part * 64 : 0);
+          uint8_t* dst = p.h8 + (int64_t)q * p.N + c0;
 #pragma unroll
-          for (int i = 0; i < NH / 8; ++i) {
-            uint32_t o[4];
+          for (int i = 0; i < NH / 16; ++i) {
+            uint32_t o[8];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float v[4] = {acc[8 * i + 2 * j].x, acc[8 * i + 2 * j].y, acc[8 * i + 2 * j + 1].x,
-                                  acc[8 * i + 2 * j + 1].y};
+            for (int j = 0; j < 8; ++j) {
+              const float2* a = &acc[16 * i + 2 * j];
+              const float v[4] = {a[0].x, a[0].y, a[1].x, a[1].y};
               o[j] = e4m3x4(v, sc.inv);
             }
-            dst[i] = make_uint4(o[0], o[1], o[2], o[3]);
+            store32(dst + 32 * i, o);
           }
-          if (SW ? part == 0 : (part & 1) == 0) p.sh[(int64_t)blk * p.rows + q] = sc.s;
+          if (!SW || part == 0) p.sh[(int64_t)blk * p.rows + q] = sc.s;
         }
       }
     }
@@ -457,6 +473,7 @@ moeblaze_status launch_fp8_products(const moeblaze_shape& s, const moeblaze_fp8_
   if (r != MOEBLAZE_OK) return r;
   p.s0 = w.s3;
   p.y = ws.y;
+  p.sh = ws.sy;
   p.N = s.d;
   p.kblocks = s.h / BK;
   p.n_tiles = (s.d + 255) / 256;

@@ -194,6 +194,11 @@ def experts8(x, ids, gates, mats):
         edge = ((top - terr <= 224 * s) | (top + terr > 448 * s)) & (s > 2.0 ** -126)
         off = off + grown(edge.double() * s * 2.0 ** -9, h)
         g = gates[t, k].double()[:, None]
-        y.index_add_(0, t, g * (val @ w3))
-        bound.index_add_(0, t, g.abs() * (off @ w3.abs() + matmul_err(h) * ((val.abs() + off) @ w3.abs())))
+        out = val @ w3
+        err = off @ w3.abs() + matmul_err(h) * ((val.abs() + off) @ w3.abs())
+        y.index_add_(0, t, g * out)
+        # each slot's row waits for the others in fp16 (prompts): half a step of it, 2^-11 of the value.  (At its scale
+        # the block's largest is 2^14 or more, and subnormals' half step 2^-25, 2^-39 of the largest: the sum's own
+        # bound above is larger.)
+        bound.index_add_(0, t, g.abs() * (err + 2.0 ** -11 * (out.abs() + err)))
     return y, bound + matmul_err(K) * y.abs()
