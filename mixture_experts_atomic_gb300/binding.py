@@ -829,10 +829,10 @@ def fp8_quantize_rows(x, q=None, scales=None, stream=None):
     L, d = x.shape
     if d % 16 != 0:
         raise MoEBlazeError(ERR_UNSUPPORTED, "moeblaze_fp8_quantize_rows")
-    _args((x, "x", (L, d), x.dtype, False))
+    _args((x, "x", (L, d), x.dtype, False), (q, "q", (L, d), torch.float8_e4m3fn, True),
+          (scales, "scales", (L, blocks8(d)), torch.float32, True))
     q = torch.empty((L, d), dtype=torch.float8_e4m3fn, device=x.device) if q is None else q
     scales = torch.empty((L, blocks8(d)), dtype=torch.float32, device=x.device) if scales is None else scales
-    _args((q, "q", (L, d), torch.float8_e4m3fn, False), (scales, "scales", (L, blocks8(d)), torch.float32, False))
     st = moeblaze_fp8_quantize_rows(L, d, DTYPE[x.dtype], _ptr(x), _ptr(q), _ptr(scales), _stream(stream))
     _check(st, "moeblaze_fp8_quantize_rows")
     return q, scales
@@ -846,9 +846,9 @@ def fp8_dequantize_rows(q, scales, dtype=torch.bfloat16, out=None, stream=None):
     if dtype not in DTYPE:
         raise ValueError(f"dtype {dtype}, expected float32 or bfloat16")
     L, d = q.shape
-    _args((q, "q", (L, d), torch.float8_e4m3fn, False), (scales, "scales", (L, blocks8(d)), torch.float32, False))
+    _args((q, "q", (L, d), torch.float8_e4m3fn, False), (scales, "scales", (L, blocks8(d)), torch.float32, False),
+          (out, "out", (L, d), dtype, True))
     out = torch.empty((L, d), dtype=dtype, device=q.device) if out is None else out
-    _args((out, "out", (L, d), dtype, False))
     st = moeblaze_fp8_dequantize_rows(L, d, DTYPE[dtype], _ptr(q), _ptr(scales), _ptr(out), _stream(stream))
     _check(st, "moeblaze_fp8_dequantize_rows")
     return out

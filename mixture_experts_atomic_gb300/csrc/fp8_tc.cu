@@ -135,13 +135,6 @@ __device__ __forceinline__ Tile decode(const Params& p, int tile, int num_mt) {
   return t;
 }
 
-// a whole sector of a row (rows lie far apart: 16 bytes would be half of one)
-__device__ __forceinline__ void store32(void* p, const uint32_t* v) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
-               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-               : "memory");
-}
-
 template <int MODE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) fp8_gemm_kernel(const __grid_constant__ Params p) {
   extern __shared__ uint8_t smem_raw[];
@@ -353,7 +346,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) fp8_gemm
               const __half2 h = __floats2half2_rn(acc[8 * i + j].x * sc.inv, acc[8 * i + j].y * sc.inv);
               o[j] = *reinterpret_cast<const uint32_t*>(&h);
             }
-            store32(dst + 16 * i, o);
+            store_sector(dst + 16 * i, o);
           }
           p.sh[(int64_t)blk * p.rows + q] = sc.s;
         }
@@ -394,7 +387,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) fp8_gemm
               const float v[4] = {a[0].x, a[0].y, a[1].x, a[1].y};
               o[j] = e4m3x4(v, sc.inv);
             }
-            store32(dst + 32 * i, o);
+            store_sector(dst + 32 * i, o);
           }
           if (!SW || part == 0) p.sh[(int64_t)blk * p.rows + q] = sc.s;
         }

@@ -285,9 +285,10 @@ __device__ __forceinline__ uint32_t encode4(const float* v, float inv) {
   return __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
 }
 __device__ __forceinline__ void encode32(int8_t* q, const float* v, float inv) {
-  uint4* o = reinterpret_cast<uint4*>(q);
-  o[0] = make_uint4(encode4(v, inv), encode4(v + 4, inv), encode4(v + 8, inv), encode4(v + 12, inv));
-  o[1] = make_uint4(encode4(v + 16, inv), encode4(v + 20, inv), encode4(v + 24, inv), encode4(v + 28, inv));
+  uint32_t u[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) u[i] = encode4(v + 4 * i, inv);
+  store_sector(q, u);
 }
 // the values of 16 codes: code + 128 as the low bits of 2^23 + (code + 128)
 __device__ __forceinline__ void decode16(const uint4& u, float s, float* v) {
@@ -357,17 +358,16 @@ __device__ __forceinline__ void red_add_v4(float* p, float a, float b, float c, 
   asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p), "f"(a), "f"(b), "f"(c), "f"(d) : "memory");
 }
 
-// store 32 consecutive fp32 values as bf16 (64 bytes, 16-byte aligned)
+// store 32 consecutive fp32 values as bf16 (64 bytes, 16-byte aligned), a sector
+// at a time (16 bytes at a time: dW1 || dW2 of 16384 tokens, d 2048, h 1408, 6 of
+// 64 experts 1.29 ms instead of 1.17)
 __device__ __forceinline__ void store_row32(__nv_bfloat16* p, const float* v) {
-  uint4* q = reinterpret_cast<uint4*>(p);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    uint4 u;
-    u.x = pack_bf16x2(v[8 * i + 0], v[8 * i + 1]);
-    u.y = pack_bf16x2(v[8 * i + 2], v[8 * i + 3]);
-    u.z = pack_bf16x2(v[8 * i + 4], v[8 * i + 5]);
-    u.w = pack_bf16x2(v[8 * i + 6], v[8 * i + 7]);
-    q[i] = u;
+  for (int i = 0; i < 2; ++i) {
+    uint32_t u[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) u[j] = pack_bf16x2(v[16 * i + 2 * j], v[16 * i + 2 * j + 1]);
+    store_sector(p + 16 * i, u);
   }
 }
 __device__ __forceinline__ void store_zero32(__nv_bfloat16* p) {

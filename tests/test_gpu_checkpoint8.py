@@ -170,6 +170,32 @@ def test_checkpoint8_odd_values():
     assert not bool(got["dW3"][1].isfinite().any())
 
 
+@pytest.mark.parametrize("eight", [False, True])
+def test_layer_in_buffers_that_start_on_16_bytes(eight):
+    """Pointers need 16-byte alignment, not more: every buffer of the C call moved by 16 bytes gives the same bits."""
+    L, d, h, E, K = 300, 256, 384, 5, 2
+    p = _problem(L, d, h, E, K, "swiglu", 9)
+    layer = MoELayer(L, d, h, E, K, BF16, "swiglu", checkpoint8=eight)
+    y = _forward(layer, p).clone()
+    want = {k: v.clone() for k, v in _backward(layer, p).items()}
+
+    def moved(t):
+        raw = torch.zeros(t.nbytes + 16, dtype=torch.uint8, device="cuda")
+        out = raw[16:].view(t.dtype).view(t.shape)
+        assert out.data_ptr() % 32 == 16
+        return out.copy_(t)
+
+    other = MoELayer(L, d, h, E, K, BF16, "swiglu", checkpoint8=eight)
+    for n in ("y", "dX", "dW1", "dW2", "dW3", "dgates"):
+        setattr(other, n, moved(getattr(other, n)))
+    other.bufs = B.LayerBuffers(*[moved(t) for t in (other.bufs.saved, other.bufs.fwd_ws, other.bufs.bwd_ws)])
+    q = {k: v if k in ("ids", "gates") else moved(v) for k, v in p.items()}
+    assert torch.equal(_forward(other, q), y)
+    got = _backward(other, q)
+    for n in ("dX", "dW1", "dW2", "dW3"):
+        assert torch.equal(got[n], want[n]), n
+
+
 def test_checkpoint8_empty_batch():
     p = _problem(0, 128, 256, 4, 2, "swiglu", 5)
     layer = MoELayer(0, 128, 256, 4, 2, BF16, "swiglu", checkpoint8=True)

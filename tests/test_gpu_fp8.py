@@ -223,6 +223,28 @@ def test_quantize_weights_to_the_bit(E, K, N, dt):
     assert bool(s[0, 0, 0].isnan()) and not bool(s[1:].isnan().any())
 
 
+@pytest.mark.parametrize("L,act", [(5, "swiglu"), (700, "swiglu"), (700, "silu")])
+def test_fp8_in_buffers_that_start_on_16_bytes(L, act):
+    d, h, E, K = 256, 384, 4, 2
+    x, ids, gates, mats = _problem(L, d, h, E, K, act, 3)
+    ex = Fp8Experts(L, d, h, E, K, act)
+    ex.load(*mats)
+    want = ex.forward(x, ids, gates).clone()
+
+    def moved(t):
+        raw = torch.zeros(t.nbytes + 16, dtype=torch.uint8, device="cuda")
+        out = raw[16:].view(t.dtype).view(t.shape)
+        assert out.data_ptr() % 32 == 16
+        out.view(torch.uint8).copy_(t.view(torch.uint8))
+        return out
+
+    packed = {n: (moved(q), moved(s)) for n, (q, s) in ex._packed.items()}
+    args = [t.data_ptr() if t is not None else None for n in "123" for t in packed.get(n, (None, None))]
+    y, ws = moved(want), moved(ex._ws)
+    got = B.fp8_forward(ex._shape(L), moved(x), None, ids, gates, B.Fp8Weights(*args), y, ws)
+    assert torch.equal(got, want)
+
+
 def test_fp8_load_replaces_weights_in_place():
     """A graph captured on one set of weights runs on the next one loaded; a refused tensor leaves all as they were."""
     L, d, h, E, K = 20, 256, 384, 4, 2
