@@ -110,16 +110,6 @@ __device__ __forceinline__ void mma_pair(uint32_t tmem_d, uint64_t a, uint64_t b
 __device__ __forceinline__ void commit_at(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ bool elect_one() {
-  uint32_t one;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "elect.sync _|p, 0xffffffff;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(one));
-  return one != 0;
-}
-
 struct Tile {
   int e, row0, n0;  // row0: of the pair's 256 rows
 };

@@ -868,13 +868,24 @@ __global__ void __launch_bounds__(num_threads(MODE, VAR), 1) moe_gemm_kernel(con
     }
   } else if (warp == MMA_WARP) {
     // ================================================================ MMA issuer
-    if (lane == 0) {
+    // The whole warp walks along, so that addresses and descriptors are uniform,
+    // and one lane issues: an MMA then takes less to issue than to run.
+    {
+      const bool one = elect_one();
+      auto take = [&](int j) -> long long {
+        long long id = 0;
+        if (lane == 0) id = q_take(j);
+        return __shfl_sync(0xffffffffu, id, 0);
+      };
+      auto wait = [&](uint32_t b, uint32_t parity) -> bool {
+        return __all_sync(0xffffffffu, wait_bounded(b, parity, abort_s, err, lim) ? 1 : 0) != 0;
+      };
       int s = 0;
       uint32_t ph = 0;
       int abuf = 0;
       uint32_t aph = 0;
       bool ok = true;
-      long long tile = q_take(0);
+      long long tile = take(0);
       Tile t;
       if (tile >= 0 && tile < total) t = decode<MODE, WIDE_T>(p, tile, num_mt);
       for (int j = 0; ok; ++j) {
@@ -890,53 +901,53 @@ __global__ void __launch_bounds__(num_threads(MODE, VAR), 1) moe_gemm_kernel(con
         Tile tn;
         bool fetched = false;
         auto fetch_next = [&]() {
-          ntile = q_take(j + 1);
+          ntile = take(j + 1);
           if (ntile >= 0 && ntile < total) tn = decode<MODE, WIDE_T>(p, ntile, num_mt);
           fetched = true;
         };
         const int nmma = is_dual(MODE) ? 2 * t.nw : t.nw;
         const uint32_t idesc = instr_desc(nmma, a_mn_major(MODE), !b_k_major(MODE));
-        ok = wait_bounded(bar(10 + abuf), aph ^ 1u, abort_s, err, lim);
+        ok = wait(bar(10 + abuf), aph ^ 1u);
         if (!ok) break;
         tc_fence_after();
         const uint32_t dcol = tmem_base + abuf * 256;
         for (int kb = 0; kb < t.kblocks; ++kb) {
-          ok = wait_bounded(bar(s), ph, abort_s, err, lim);
+          ok = wait(bar(s), ph);
           if (!ok) break;
           tc_fence_after();
           const uint32_t sA = smem_base + s * SB;
-          const uint32_t sB = sA + AB;
+          // descriptors of the stage; the steps' addresses follow in units of 16
+          // bytes (shared memory ends below their field's range)
+          const uint64_t ad0 = a_mn_major(MODE) ? smem_desc(sA, 8192, 1024) : smem_desc(sA, 16, 1024);
+          const uint64_t bd0 = b_k_major(MODE) ? smem_desc(sA + AB, 16, 1024) : smem_desc(sA + AB, 8192, 1024);
+          constexpr uint32_t ASTEP = (a_mn_major(MODE) ? 2048 : 32) >> 4, BSTEP = (b_k_major(MODE) ? 32 : 2048) >> 4;
+          if (one) {
 #pragma unroll
-          for (int kk = 0; kk < BK / 16; ++kk) {
-            const uint64_t bd = b_k_major(MODE) ? smem_desc(sB + kk * 32, 16, 1024) : smem_desc(sB + kk * 2048, 8192, 1024);
-            if constexpr (WIDE_T) {
-              // rows 0-127 and 128-255 of the tile (MN-major A: atoms 0-1 and
-              // 2-3; K-major A: 16 KB apart) into accumulator columns 0 and 256
+            for (int kk = 0; kk < BK / 16; ++kk) {
+              // wide tiles: rows 0-127 and 128-255 of the tile (MN-major A: atoms
+              // 0-1 and 2-3; K-major A: 16 KB apart) into accumulator columns 0
+              // and 256
 #pragma unroll
-              for (int hm = 0; hm < 2; ++hm) {
-                const uint64_t ad = a_mn_major(MODE) ? smem_desc(sA + hm * 16384 + kk * 2048, 8192, 1024)
-                                                     : smem_desc(sA + hm * 16384 + kk * 32, 16, 1024);
-                mma_bf16(dcol + hm * 256, ad, bd, idesc, (kb | kk) ? 1u : 0u);
-              }
-            } else {
-              const uint64_t ad =
-                  a_mn_major(MODE) ? smem_desc(sA + kk * 2048, 8192, 1024) : smem_desc(sA + kk * 32, 16, 1024);
-              mma_bf16(dcol, ad, bd, idesc, (kb | kk) ? 1u : 0u);
+              for (int hm = 0; hm < (WIDE_T ? 2 : 1); ++hm)
+                mma_bf16(dcol + hm * 256, ad0 + kk * ASTEP + hm * (16384 >> 4), bd0 + kk * BSTEP, idesc, (kb | kk) ? 1u : 0u);
             }
+            mma_commit(bar(4 + s));
           }
-          mma_commit(bar(4 + s));
+          __syncwarp();
           if (++s == NST) { s = 0; ph ^= 1u; }
           if (kb == 0) fetch_next();
         }
         if (!ok) break;
-        mma_commit(bar(8 + abuf));
+        if (one) mma_commit(bar(8 + abuf));
+        __syncwarp();
         if (++abuf == NACC) { abuf = 0; aph ^= 1u; }
         if (!fetched) fetch_next();
         tile = ntile;
         t = tn;
       }
-      // all MMAs issued by this thread retire before TMEM is released
-      mma_commit(bar(12));
+      // all MMAs issued by this warp retire before TMEM is released
+      if (one) mma_commit(bar(12));
+      __syncwarp();
       wait_bounded(bar(12), 0, nullptr, nullptr, ok ? lim : kDrainNs);
     }
     __syncwarp();
