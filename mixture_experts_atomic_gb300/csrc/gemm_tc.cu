@@ -22,7 +22,7 @@
 // descending order of expert load), so skewed expert loads balance.
 //
 // Wide tiles (up, down with stored H and dX from 32 k-blocks a tile; weight
-// gradients from 4,096 routed rows per expert): one CTA takes 256
+// gradients from 256 routed rows per expert): one CTA takes 256
 // output rows, as two M=128 MMAs per 16-deep step that share every B tile,
 // into one 512-column accumulator.  A k-block then brings 64 KB for
 // 8.4 MFLOP instead of 48 KB for 4.2; the price is that the epilogue is not
@@ -141,14 +141,24 @@ __host__ __device__ constexpr int transform_threads(int m) { return helper_warps
 __host__ __device__ constexpr bool widenable(int m) {
   return m == DW12 || m == DW1 || m == DW3_H || m == UP_SWIGLU || m == UP_SILU || m == DOWN_H || m == DX;
 }
-// Measured: from 4,096 routed rows per expert (64 k-blocks a tile) the wide
-// tiles are 20-23% faster on dW1 (dW1 || dW2) and dW3 than 128-row tiles.
-constexpr int64_t kWideMinRows = 4096;  // routed rows per expert (on average) from which wide tiles are used
+// Measured, 128-row against wide tiles, ms of dW1 (dW1 || dW2) and dW3:
+//   1,750 rows an expert (d 4096, h 14336, 8)  3.15, 1.91   2.53, 1.41
+//   1,536 (d 2048, h 1408, 64)                 1.15, 0.67   0.90, 0.53
+//   384 (the same)                             0.46, 0.28   0.41, 0.25
+//   250 (d 4096, h 14336, 8)                   0.97, 0.60   0.90, 0.49
+//   375 (SiLU, d 1024, h 4096, 8)              0.064, 0.072 0.062, 0.064
+//   175 (the same)                             0.043, 0.045 0.045, 0.045
+//   500 (d 512, h 512, 4: 32 wide tiles)       0.016, 0.018 0.021, 0.021
+// So from 256 rows an expert where the wide tiles still fill the SMs, and from
+// 4,096 always: half as many SMs with tiles of twice the work.
+constexpr int64_t kWideMinRows = 256, kWideAlwaysRows = 4096;  // routed rows per expert, on average
 // out_rows: rows of the weight gradient.  A last tile of 128 rows is allowed
 // where the A operand comes by TMA (dW3: the rows past the end load as zeros
 // and are not stored); the gathered A of dW1 needs whole 256-row tiles.
-inline bool wide_stage(const moeblaze_shape& s, int out_rows, bool half_tail_ok) {
-  return out_rows % (half_tail_ok ? BM : 2 * BM) == 0 && (int64_t)s.L * s.K >= kWideMinRows * s.E;
+inline bool wide_stage(const moeblaze_shape& s, int out_rows, int n_tiles, bool half_tail_ok) {
+  if (out_rows % (half_tail_ok ? BM : 2 * BM) != 0) return false;
+  const int64_t rows = s.L * s.K, tiles = (int64_t)((out_rows + 2 * BM - 1) / (2 * BM)) * n_tiles * s.E;
+  return rows >= kWideAlwaysRows * s.E || (rows >= kWideMinRows * s.E && tiles >= sm_count());
 }
 // The ring: 4 stages of A (16 KB) + B operand (32 KB); the fused SwiGLU
 // stages add the saved-B tile (16 KB) to every stage and keep 3 of them;
@@ -1461,9 +1471,9 @@ moeblaze_status tc_backward(const moeblaze_shape& s, const __nv_bfloat16* dY, co
     p.gsrc = dY;
     p.gld = s.d;
     p.N = s.d;
-    const bool wide = !rec && wide_stage(s, s.h, true);
-    p.m_tiles_w = wide ? (s.h + 2 * BM - 1) / (2 * BM) : s.h / BM;
     p.n_tiles = (s.d + 255) / 256;
+    const bool wide = !rec && wide_stage(s, s.h, p.n_tiles, true);
+    p.m_tiles_w = wide ? (s.h + 2 * BM - 1) / (2 * BM) : s.h / BM;
     p.total_w = (int64_t)s.E * p.m_tiles_w * p.n_tiles;
     p.o0 = dW3;
     p.sched = sched + 3;
@@ -1524,9 +1534,9 @@ moeblaze_status tc_backward(const moeblaze_shape& s, const __nv_bfloat16* dY, co
     if (!make_map(&p.tmB0, A, s.h, rows, 64, 64)) return MOEBLAZE_ERR_CUDA;
     if (sw && !make_map(&p.tmB1, B, s.h, rows, 64, 64)) return MOEBLAZE_ERR_CUDA;
     p.N = s.h;
-    const bool wide = wide_stage(s, s.d, false);
-    p.m_tiles_w = s.d / (wide ? 2 * BM : BM);
     p.n_tiles = sw ? s.h / 128 : (s.h + 255) / 256;
+    const bool wide = wide_stage(s, s.d, p.n_tiles, false);
+    p.m_tiles_w = s.d / (wide ? 2 * BM : BM);
     p.total_w = (int64_t)s.E * p.m_tiles_w * p.n_tiles;
     p.o0 = dW1; p.o1 = dW2;
     p.sched = sched + 2;

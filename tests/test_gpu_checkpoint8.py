@@ -96,6 +96,8 @@ SHAPES = [
     (2048, 128, 640, 64, 2, "silu", None),
     (10000, 2048, 512, 4, 2, "swiglu", 1),        # 256-row tiles of the up projection
     (10000, 2048, 384, 4, 2, "silu", None),
+    (1300, 1024, 1408, 8, 2, "swiglu", None),     # 256-row tiles of the weight gradients at 325 rows an expert
+    (1300, 1024, 2560, 8, 2, "silu", 5),
 ]
 
 
