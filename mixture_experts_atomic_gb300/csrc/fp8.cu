@@ -77,16 +77,18 @@ __global__ void __launch_bounds__(kRowThreads) dequantize_rows_kernel(const uint
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
     for (int k = 0; k < 4; ++k) e4m3_values(w[k], sc, v + 4 * k);
+    uint32_t o[8];
     if constexpr (sizeof(T) == 2) {
-      uint4* o = reinterpret_cast<uint4*>(x) + 2 * i;
 #pragma unroll
-      for (int k = 0; k < 2; ++k)
-        o[k] = make_uint4(pack_bf16x2(v[8 * k], v[8 * k + 1]), pack_bf16x2(v[8 * k + 2], v[8 * k + 3]),
-                          pack_bf16x2(v[8 * k + 4], v[8 * k + 5]), pack_bf16x2(v[8 * k + 6], v[8 * k + 7]));
+      for (int k = 0; k < 8; ++k) o[k] = pack_bf16x2(v[2 * k], v[2 * k + 1]);
+      store_sector(x + 16 * i, o);
     } else {
-      float4* o = reinterpret_cast<float4*>(x) + 4 * i;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) o[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) o[k] = __float_as_uint(v[8 * h + k]);
+        store_sector(x + 16 * i + 8 * h, o);
+      }
     }
   }
 }
@@ -276,11 +278,19 @@ __global__ void __launch_bounds__(256) gather_rows_kernel(const T* __restrict__ 
   for (int k = 0; k < kMaxK; ++k) to[k] = __shfl_sync(0xffffffffu, mine, k);  // -1 from K on
   if constexpr (sizeof(T) == 1) {
     const uint4* src = reinterpret_cast<const uint4*>(x + t * d);
-    for (int c = lane; c < d / 16; c += 32) {
-      const uint4 v = src[c];
+    constexpr int U = 4;  // words of a lane on their way
+    for (int c0 = lane; c0 < d / 16; c0 += 32 * U) {
+      uint4 v[U];
 #pragma unroll
-      for (int k = 0; k < kMaxK; ++k)
-        if (to[k] >= 0) reinterpret_cast<uint4*>(x8 + (int64_t)to[k] * d)[c] = v;
+      for (int u = 0; u < U; ++u)
+        if (c0 + 32 * u < d / 16) v[u] = src[c0 + 32 * u];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (c0 + 32 * u < d / 16) {
+#pragma unroll
+          for (int k = 0; k < kMaxK; ++k)
+            if (to[k] >= 0) reinterpret_cast<uint4*>(x8 + (int64_t)to[k] * d)[c0 + 32 * u] = v[u];
+        }
     }
     for (int b = lane; b < d / kBlock8; b += 32) {
       const float v = sx[t * (d / kBlock8) + b];
@@ -289,25 +299,32 @@ __global__ void __launch_bounds__(256) gather_rows_kernel(const T* __restrict__ 
         if (to[k] >= 0) s8[b * rows + to[k]] = v;
     }
   } else {
-    for (int c0 = 0; c0 < d / 8; c0 += 32) {  // 8 columns a lane, 16 lanes a block
-      const int c = c0 + lane;
-      float v[8];
-      uint32_t m = 0u;
-      if (c < d / 8) {
-        load8(x + t * d + 8 * c, v);
+    constexpr int U = 4;
+    for (int c0 = 0; c0 < d / 8; c0 += 32 * U) {  // 8 columns a lane, 16 lanes a block
+      float v[U][8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) m = max(m, abs_bits(v[i]));
+      for (int u = 0; u < U; ++u) {
+        const int c = c0 + 32 * u + lane;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[u][i] = 0.f;
+        if (c < d / 8) load8(x + t * d + 8 * c, v[u]);
       }
 #pragma unroll
-      for (int k = 8; k > 0; k >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, k));
-      const Scale8 sc = scale8(m);
-      uint2 o = make_uint2(0u, 0u);
-      if (c < d / 8) o = make_uint2(e4m3x4(v, sc.inv), e4m3x4(v + 4, sc.inv));
+      for (int u = 0; u < U; ++u) {
+        const int c = c0 + 32 * u + lane;
+        uint32_t m = 0u;
 #pragma unroll
-      for (int k = 0; k < kMaxK; ++k) {
-        if (to[k] >= 0 && c < d / 8) {
-          reinterpret_cast<uint2*>(x8 + (int64_t)to[k] * d)[c] = o;
-          if ((lane & 15) == 0) s8[(int64_t)(c >> 4) * rows + to[k]] = sc.s;
+        for (int i = 0; i < 8; ++i) m = max(m, abs_bits(v[u][i]));
+#pragma unroll
+        for (int k = 8; k > 0; k >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, k));
+        const Scale8 sc = scale8(m);
+        const uint2 o = make_uint2(e4m3x4(v[u], sc.inv), e4m3x4(v[u] + 4, sc.inv));
+#pragma unroll
+        for (int k = 0; k < kMaxK; ++k) {
+          if (to[k] >= 0 && c < d / 8) {
+            reinterpret_cast<uint2*>(x8 + (int64_t)to[k] * d)[c] = o;
+            if ((lane & 15) == 0) s8[(int64_t)(c >> 4) * rows + to[k]] = sc.s;
+          }
         }
       }
     }
