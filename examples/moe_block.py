@@ -5,8 +5,12 @@
 train(): steps of a pre-norm MoE block (layer norm with the residual sum,
 router with its balance and z loss, dropless experts) with a plain gradient
 step on every parameter, captured once as a CUDA graph and replayed.
+With norm="rms" and checkpoint8 the block has a root-mean-square norm and
+keeps its checkpoints in 8 bits.
 serve(): the trained experts quantised to 4 bits, and a decode batch sent
 through norm, router and 4-bit experts.
+serve8(): the experts in 8-bit floating point, on rows that the RMS norm
+leaves in 8 bits: a prompt, or a decode batch.
 """
 from __future__ import annotations
 
@@ -19,24 +23,28 @@ import torch
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 
 from mixture_experts_atomic_gb300 import binding as B  # noqa: E402
-from mixture_experts_atomic_gb300.block import LayerNorm, MoEBlock  # noqa: E402
+from mixture_experts_atomic_gb300.block import LayerNorm, MoEBlock, RMSNorm  # noqa: E402
+from mixture_experts_atomic_gb300.fp8 import Fp8Experts, dequantize_rows  # noqa: E402
 from mixture_experts_atomic_gb300.int4 import Int4Experts  # noqa: E402
 
 
-def parameters(d, h, E, dtype, seed=0):
+def parameters(d, h, E, dtype, seed=0, norm="layer"):
     g = torch.Generator(device="cuda").manual_seed(seed)
     r = lambda *s: torch.randn(*s, device="cuda", generator=g)  # noqa: E731
-    return {"norm_w": torch.ones(d, device="cuda"), "norm_b": torch.zeros(d, device="cuda"),
-            "Wr": r(d, E) / d ** 0.5, "bias": torch.zeros(E, device="cuda"),
-            "W1": (r(E, d, h) / d ** 0.5).to(dtype), "W2": (r(E, d, h) / d ** 0.5).to(dtype),
-            "W3": (r(E, h, d) / h ** 0.5).to(dtype)}
+    p = {"norm_w": torch.ones(d, device="cuda")}
+    if norm == "layer":
+        p["norm_b"] = torch.zeros(d, device="cuda")
+    p.update({"Wr": r(d, E) / d ** 0.5, "bias": torch.zeros(E, device="cuda"),
+              "W1": (r(E, d, h) / d ** 0.5).to(dtype), "W2": (r(E, d, h) / d ** 0.5).to(dtype),
+              "W3": (r(E, h, d) / h ** 0.5).to(dtype)})
+    return p
 
 
-def train(L, d, h, E, K, steps, lr=0.05, dtype=torch.bfloat16):
+def train(L, d, h, E, K, steps, lr=0.05, dtype=torch.bfloat16, norm="layer", checkpoint8=False):
     """The block learns to map x to a fixed target; returns (parameters, history) with the mean squared error, the
     balance loss and the largest expert's share of the slots of each step."""
-    p = parameters(d, h, E, dtype)
-    block = MoEBlock(L, d, h, E, K, dtype)
+    p = parameters(d, h, E, dtype, norm=norm)
+    block = MoEBlock(L, d, h, E, K, dtype, norm=norm, checkpoint8=checkpoint8)
     g = torch.Generator(device="cuda").manual_seed(1)
     x, res = (torch.randn(L, d, device="cuda", generator=g).to(dtype) for _ in range(2))
     target = torch.randn(L, d, device="cuda", generator=g) * 0.5
@@ -87,6 +95,22 @@ def serve(p, tokens, K, group=128):
     return y, layer.forward(u, gates, *experts.dequantize())
 
 
+def serve8(p, tokens, K):
+    """tokens rows on the 8-bit experts; returns (y in 8 bits, y of the bf16 layer on the rows and weights that the
+    8 bits stand for)."""
+    from mixture_experts_atomic_gb300.layer import MoELayer
+    E, d, h = p["W1"].shape
+    experts = Fp8Experts(tokens, d, h, E, K, "swiglu")
+    experts.quantize(p["W1"], p["W2"], p["W3"])
+    norm = RMSNorm(tokens, d, torch.bfloat16)
+    x, res = (torch.randn(tokens, d, device="cuda").to(torch.bfloat16) for _ in range(2))
+    q, scales, u, _, _ = norm.forward8(x, p["norm_w"], res)
+    layer = MoELayer(tokens, d, h, E, K, torch.bfloat16, "swiglu")
+    ids, gates = layer.route(u, p["Wr"], p["bias"])
+    y = experts.forward(q, ids, gates, scales)
+    return y, layer.forward(dequantize_rows(q, scales), gates, *experts.dequantize())
+
+
 def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("--tokens", type=int, default=4096)
@@ -98,6 +122,12 @@ def main():
     y4, y16 = serve(p, 16, 2)
     print("4-bit experts against the bf16 layer on the same weights: rel %.2e"
           % float((y4.float() - y16.float()).norm() / y16.float().norm()))
+    p, history = train(a.tokens, 512, 1024, 8, 2, a.steps, norm="rms", checkpoint8=True)
+    print("RMS norm, checkpoints in 8 bits: last step's mse %.4f" % history[-1][0])
+    for tokens in (a.tokens, 16):
+        y8, y16 = serve8(p, tokens, 2)
+        print("%d tokens: 8-bit experts against the bf16 layer on the same rows and weights: rel %.2e"
+              % (tokens, float((y8.float() - y16.float()).norm() / y16.float().norm())))
 
 
 if __name__ == "__main__":

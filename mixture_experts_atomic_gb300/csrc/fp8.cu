@@ -462,9 +462,15 @@ auto combine_kernel(int K) {
        : K <= 6 ? combine_rows_kernel<T, 6> : combine_rows_kernel<T, kMaxK>;
 }
 
-// The most tokens a call of this shape takes the path for few tokens with: the
-// slots fit its table, and the used experts have about a tile of them.
-constexpr int kFewPerExpert = 16;
+// The most tokens a call of this shape takes the path for few tokens with: its
+// experts have less than a tile of 32 on average, and the slots fit its table.
+// Both paths, us (few | prompts), by slots an expert:
+//   d 4096, h 14336, 2 of 8     16  269 | 335    24  274 | 336    32  365 | 338
+//   d 2048, h 1408, 6 of 64     8   131 | 183    16  149 | 185    24  160 | 185
+//   d 2048, h 1024, 8 of 256    4   300 | 481     8  312 | 481
+//   d 1024, h 4096, 1 of 16     8    73 |  80    16   81 |  81    32  115 |  81
+//   d 1024, h 1024, 2 of 4      2    28 |  27    16   31 |  28
+constexpr int kFewPerExpert = 24;
 int64_t few_tokens(const moeblaze_shape& s) {
   const int64_t slots = kFewPerExpert * (int64_t)s.E < kFewSlots ? kFewPerExpert * (int64_t)s.E : kFewSlots;
   return slots / s.K;

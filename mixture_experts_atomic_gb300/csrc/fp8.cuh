@@ -31,7 +31,7 @@ moeblaze_status launch_fp8_products(const moeblaze_shape& s, const moeblaze_fp8_
 // Few tokens.  Segments padded to 16 rows; an entry of the table is at most
 // kFewTile tokens of one expert.
 constexpr int kFewTile = 32;
-constexpr int kFewSlots = 512;  // L K at most
+constexpr int kFewSlots = 4096;  // L K at most
 struct Fp8FewScratch {
   int32_t* hdr;      // [0] error word, [1] entries
   int32_t* entries;  // {expert, first row, tokens, 0}

@@ -3,10 +3,11 @@
 //
 // The tensor cores take the weights as the M operand: a 128 x 128 block of them
 // (or two, of W1 and W2, or of neighbouring output rows) against 16 or 32
-// tokens; an expert with more has several tiles of them.  As for prompts (fp8_tc.cu) the sum over a block of the reduction is
-// scaled and added to fp32 registers: an output row a thread, its tokens side by
-// side.  A tile's 128 hidden columns are one block of 8-bit rows, so that its
-// scale is a maximum over the tile's threads.
+// tokens; an expert with more has several tiles of them.  As for prompts
+// (fp8_tc.cu) the sum over a block of the reduction is scaled and added to fp32
+// registers: an output row a thread, its tokens side by side.  A tile's 128 hidden
+// columns are one block of 8-bit rows, so that its scale is a maximum over the
+// tile's threads.
 //
 // Work is cut into blocks of the reduction of all tiles of all used experts, in
 // one row, of which every CTA takes an equal run (one token of 2 of 8 experts,
@@ -17,6 +18,16 @@
 // Half an SM's shared memory and TMEM a CTA: the down projection's CTAs are
 // resident beside the up projection's, and load their first weights while that
 // ends.
+//
+// Measured, the whole call: d 4096, h 14336, 2 of 8 experts 1 token 89 us (352 MB:
+// 4.0 TB/s), 16 tokens 204 us (1.41 GB: 6.9 TB/s); d 2048, h 1408, 6 of 64, 61
+// tokens 98 to 112 us.  At one token the weights stream at 7.1 TB/s from 8 us on,
+// where rows, table and first loads have come; the CTAs end between 38 and 47 us,
+// the down projection has its rows 8 us later, and the sum of the slots takes 5.
+// Beside it: weights not packed in blocks 260 against 239 us (16 tokens); a tile's
+// parts added one load after another 122 against 90 us (one token); all four steps
+// in one launch with barriers over the grid 94 to 99 us (one token), 214 to 219
+// (16 tokens), 96 to 99 (61 tokens).
 #include "common.cuh"
 #include "eight.cuh"
 #include "fp8.cuh"
@@ -36,6 +47,10 @@ constexpr int STAGE_BYTES = 2 * W_BYTES + X_BYTES;
 constexpr int SLOTS = STAGES + NBUF;        // of the tokens' scales: see fp8_tc.cu
 constexpr int THREADS = 192, SCALE_THREADS = 128;
 constexpr int TMEM_COLS = 256;              // NBUF x (32 + 32)
+// Blocks of a CTA's run, at least: shorter ones end sooner, but their parts take
+// longer to add up (one token, d 1024, h 4096, 1 of 16: 42, 31, 30, 31 us with 1,
+// 2, 4 and 8; d 512, h 512, 2 of 8: 25, 25, 22, 29).
+constexpr int kMinRun = 4;
 static_assert(NBUF * 2 * TOKENS <= TMEM_COLS, "TMEM");
 constexpr int RED_BYTES = 2 * 2 * 4 * TOKENS * 4;  // [turn][half][warp][token]
 constexpr int SMEM = STAGES * STAGE_BYTES + SLOTS * TOKENS * 4 + RED_BYTES + 1024 + 256;
@@ -162,7 +177,7 @@ __global__ void __launch_bounds__(THREADS, 2) fp8_few_kernel(const __grid_consta
   if (MODE != DOWN) asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int64_t total = (int64_t)__ldcg(p.meta + 1) * p.tiles * p.kblocks;
-  const int64_t ctas = min((int64_t)gridDim.x, total);  // those with work: a block each at least
+  const int64_t ctas = min((int64_t)gridDim.x, (total + kMinRun - 1) / kMinRun);  // those with work
   const bool idle = blockIdx.x >= ctas;
   const int64_t begin = idle ? 0 : total * blockIdx.x / ctas, end = idle ? 0 : total * (blockIdx.x + 1) / ctas;
 
@@ -447,7 +462,7 @@ moeblaze_status launch_few(const FewParams& p, int ctas, cudaStream_t st) {
 // ------------------------------------------------------------------ rows
 // A CTA a token: which row each of its slots takes, and its row to those rows;
 // the first CTA writes the table of the used experts besides.  Every CTA counts
-// all slots for itself (there are at most 512).  An expert's rows come in the
+// all slots for itself (there are at most 4096).  An expert's rows come in the
 // order of its slots, its segment is padded to 16 rows.
 constexpr int kPrepThreads = 256;
 template <typename T>
