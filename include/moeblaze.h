@@ -135,7 +135,8 @@ MOEBLAZE_API size_t moeblaze_dispatch_workspace_bytes(const moeblaze_shape* s);
 /* Activations kept from forward to backward: A = x W1 and (SwiGLU) B = x W2,
  * expert-major with each expert's rows padded to a multiple of 256, in the
  * layer dtype (bf16 with MOEBLAZE_RECOMPUTE_H: followed by one fp32 gate per
- * padded row).  0 for the identity expert. */
+ * padded row; with MOEBLAZE_CHECKPOINT_8BIT: codes and steps).  0 for the
+ * identity expert. */
 MOEBLAZE_API size_t moeblaze_saved_bytes(const moeblaze_shape* s);
 MOEBLAZE_API size_t moeblaze_forward_workspace_bytes(const moeblaze_shape* s);
 MOEBLAZE_API size_t moeblaze_backward_workspace_bytes(const moeblaze_shape* s);
@@ -234,7 +235,8 @@ MOEBLAZE_API moeblaze_status moeblaze_forward(const moeblaze_shape* s, const voi
  *           the last reader of A and B, writes dA and dB over them in place
  *           (no separate (rows x 2h) gradient buffer), so after the call it
  *           no longer holds the forward's activations; run the forward again
- *           before another backward.  fp32: left unchanged.
+ *           before another backward.  fp32, and bf16 with
+ *           MOEBLAZE_CHECKPOINT_8BIT: left unchanged.
  *   dX      device (L,d) dtype, overwritten
  *   dW1,dW2 device (E,d,h) dtype, overwritten  dW3 device (E,h,d) dtype, overwritten
  *           (dW2 NULL for SiLU; all three NULL for identity)
@@ -486,7 +488,8 @@ MOEBLAZE_API moeblaze_status moeblaze_fp8_dequantize_rows(int64_t L, int32_t d, 
  *   q (E,N,R) e4m3, scales (E, N/128, R/128):  W[e][r][n] = q[e][n][r] scale
  * quantize_weights makes it of W (E,R,N) (bf16 or fp32, the layer's layout),
  * with scales of powers of two as quantize_rows; the products take any scales.
- * R and N are multiples of 128, E <= 512. */
+ * R and N are multiples of 128 below 2^23, E <= 512, and E (N + 128) R / 128
+ * below 2^31 (MOEBLAZE_ERR_UNSUPPORTED otherwise). */
 typedef struct {
   const void* q1;   /* W1: (E,h,d), packed by moeblaze_fp8_pack */
   const float* s1;  /* (E, h/128, d/128) */
@@ -631,7 +634,9 @@ MOEBLAZE_API int64_t moeblaze_kernel_launches(void);
  *
  * moeblaze_set_fault_injection: later calls made from the calling thread run
  * their bf16 expert GEMMs with `wait_limit_ns` as the limit of every bounded
- * device-side wait (> 0; 0 restores the default of 4 s).  With withhold != 0
+ * device-side wait (> 0; 0 restores the default of 4 s), and so do the products
+ * of moeblaze_fp8_forward, whose second one withhold != 0 stops in the same way
+ * (y is then NaN).  With withhold != 0
  * the down projection of a later moeblaze_forward (default mode, not
  * MOEBLAZE_RECOMPUTE_H) issues nothing for the first stage of each CTA's
  * first tile, so that stage's barrier is never completed: the CTA's MMA wait

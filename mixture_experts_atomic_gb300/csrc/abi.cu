@@ -119,7 +119,8 @@ moeblaze_status check_rows8(int64_t L, int d, int dtype, const void* x, const vo
 moeblaze_status check_fp8_matrix(int E, int R, int N) {
   if (E < 1 || R < 1 || N < 1) return MOEBLAZE_ERR_INVALID_ARG;
   // (a block of 128 x 128 each in the launch's grid; the blocks' rows are counted in 32 bits, with a block past the end)
-  if (E > kMaxE || R % 128 != 0 || N % 128 != 0 || N / 128 > 65535 || (int64_t)E * (N + 128) >= INT32_MAX / (R / 128))
+  if (E > kMaxE || R % 128 != 0 || N % 128 != 0 || N / 128 > 65535 || R / 128 > 65535 ||
+      (int64_t)E * (N + 128) >= INT32_MAX / (R / 128))
     return MOEBLAZE_ERR_UNSUPPORTED;
   return MOEBLAZE_OK;
 }

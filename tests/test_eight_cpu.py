@@ -212,3 +212,14 @@ def test_fp8_binding_refusals():
         B.fp8_quantize_weights(z(1, 128, 128, dt=torch.half))
     with pytest.raises(B.MoEBlazeError):
         B.fp8_pack(z(1, 100, 128))
+
+
+def test_fp8_matrix_limits():
+    """Sizes whose blocks would not fit a launch's grid or 32 bits are refused, whichever of the two is long."""
+    long = 1 << 23
+    for call in (lambda E, R, N: B.moeblaze_fp8_pack(E, R, N, OKP, None, None),
+                 lambda E, R, N: B.moeblaze_fp8_quantize_weights(E, R, N, B.BF16, None, OKP, OKP, None),
+                 lambda E, R, N: B.moeblaze_fp8_dequantize_weights(E, R, N, None, 1, OKP, OKP, None)):
+        assert call(1, long, 128) == B.ERR_UNSUPPORTED and call(1, 128, long) == B.ERR_UNSUPPORTED
+        assert call(512, 1 << 15, 1 << 15) == B.ERR_UNSUPPORTED
+        assert call(1, long - 128, 128) == B.ERR_INVALID_ARG     # (in range: the missing pointer is what is refused)
