@@ -480,6 +480,8 @@ auto combine_kernel(int K) {
 //   d 2048, h 1408, 6 of 64     8   131 | 183    16  149 | 185    24  160 | 185
 //   d 2048, h 1024, 8 of 256    4   300 | 481     8  312 | 481
 //   d 1024, h 4096, 1 of 16     8    73 |  80    16   81 |  81    32  115 |  81
+//   d 512, h 512, 8 of 256      2    78 | 107    16  112 | 125
+//   d 256, h 512, 4 of 128      8    46 |  57    24   59 |  60
 //   d 1024, h 1024, 2 of 4      2    28 |  27    16   31 |  28
 constexpr int kFewPerExpert = 24;
 int64_t few_tokens(const moeblaze_shape& s) {
