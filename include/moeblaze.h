@@ -453,7 +453,8 @@ MOEBLAZE_API moeblaze_status moeblaze_layernorm_backward(const moeblaze_shape* s
  *   x, residual, sum  as moeblaze_layernorm_forward
  *   weight       device (d) fp32, 16-byte aligned
  *   y            device (L,d) dtype; NULL when only q is wanted
- *   rstd         device (L) fp32
+ *   rstd         device (L) fp32; infinite where it is above fp32's largest (rows
+ *                below 2^-128 with eps 0), y then being what the formula gives
  *   q, q_scales  device (L,d) e4m3 and (L, ceil(d/128)) fp32, or both NULL: y
  *                in 8-bit rows (moeblaze_fp8_quantize_rows) of the fp32 values
  * moeblaze_rmsnorm_backward: as moeblaze_layernorm_backward, of

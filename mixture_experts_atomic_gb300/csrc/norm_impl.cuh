@@ -96,9 +96,24 @@ __device__ __forceinline__ float row_sum(float v, float* red) {
 }
 
 // RMS: a mean of squares that fp32 does not hold, or holds with few digits (and
-// no eps in front of it), is formed again of values times 2^-64 or 2^64.
+// no eps in front of it), is formed again of values times `sum`.  2^-80 leaves
+// room for every row: squares below 2^96, 2^24 columns of them below 2^120; and
+// 2^100 as well, for rows whose mean is below 2^-100: squares of fp32's smallest
+// value are 2^-98, all of a row below 2^124.  The row itself goes on times `row`
+// and `rstd` as 1 / sqrt(mean + eps) times rstd: neither it nor its elements
+// leave the normal numbers where y does not (rstd alone is subnormal for values
+// near fp32's largest, and infinite below 2^-128).
 __device__ __forceinline__ bool out_of_range(float ms) { return !(ms <= 3.402823466e38f) || ms < 0x1p-100f; }
-__device__ __forceinline__ float into_range(float ms) { return ms < 1.f ? 0x1p64f : 0x1p-64f; }
+struct Range {
+  float sum, row, rstd;  // sum = row rstd
+};
+__device__ __forceinline__ Range into_range(float ms) {
+  return ms < 1.f ? Range{0x1p100f, 0x1p100f, 1.f} : Range{0x1p-80f, 0x1p-16f, 0x1p-64f};
+}
+// what the row times r.row is multiplied with; mean: of the squares of the row times r.sum
+__device__ __forceinline__ float rstd_in_range(const Range& r, float mean, float eps) {
+  return r.rstd / sqrtf(mean + eps * r.sum * r.sum);
+}
 
 constexpr int kNormWarps = 4;  // rows per CTA when a warp holds a row
 
@@ -222,15 +237,23 @@ __global__ void __launch_bounds__(norm_threads<TPR>()) norm_fwd_kernel(const T* 
     }
   }
   const float ms = row_sum<TPR>(acc, red[1]) * inv_d + eps;
-  float rstd = 1.f / sqrtf(ms);
+  float rstd = 1.f / sqrtf(ms), of_row = 1.f;
   if (RMS && out_of_range(ms)) {  // (the same for all of the row's threads)
-    const float f = into_range(ms);
+    const Range r = into_range(ms);
     acc = 0.f;
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) acc = fmaf(s[j][i] * f, s[j][i] * f, acc);
-    rstd = f / sqrtf(row_sum<TPR>(acc, red[0]) * inv_d + eps * f * f);
+      for (int i = 0; i < VEC; ++i) {
+        acc = fmaf(s[j][i] * r.sum, s[j][i] * r.sum, acc);
+        s[j][i] *= r.row;
+      }
+    rstd = rstd_in_range(r, row_sum<TPR>(acc, red[0]) * inv_d, eps);
+    of_row = r.row;
+  }
+  if (lane == 0) {
+    if (!RMS) mean_out[t] = mu;
+    rstd_out[t] = rstd * of_row;
   }
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
@@ -298,10 +321,6 @@ __global__ void __launch_bounds__(norm_threads<TPR>()) norm_fwd_kernel(const T* 
       }
     }
   }
-  if (lane == 0) {
-    if (!RMS) mean_out[t] = mu;
-    rstd_out[t] = rstd;
-  }
 }
 
 // rows wider than the register tiles: the row is read again for each of the
@@ -327,12 +346,13 @@ __global__ void __launch_bounds__(1024) norm_fwd_wide_kernel(const T* x, const T
     acc = fmaf(v, v, acc);
   }
   const float ms = row_sum<1024>(acc, red[1]) / (float)d + eps;
-  float rstd = 1.f / sqrtf(ms);
+  float rstd = 1.f / sqrtf(ms), of_row = 1.f;
   if (RMS && out_of_range(ms)) {
-    const float f = into_range(ms);
+    const Range r = into_range(ms);
     acc = 0.f;
-    for (int c = threadIdx.x; c < d; c += 1024) acc = fmaf(at(c) * f, at(c) * f, acc);
-    rstd = f / sqrtf(row_sum<1024>(acc, red[0]) / (float)d + eps * f * f);
+    for (int c = threadIdx.x; c < d; c += 1024) acc = fmaf(at(c) * r.sum, at(c) * r.sum, acc);
+    rstd = rstd_in_range(r, row_sum<1024>(acc, red[0]) / (float)d, eps);
+    of_row = r.row;
   }
   if constexpr (Q8) {  // a warp takes a block, a lane four neighbouring columns of it
     const int lane = threadIdx.x & 31;
@@ -345,7 +365,7 @@ __global__ void __launch_bounds__(1024) norm_fwd_wide_kernel(const T* x, const T
         for (int i = 0; i < 4; ++i) {
           const float v = at(c + i);
           if (sum) st_t(sum[o + c + i], v);
-          f[i] = v * rstd * w[c + i];
+          f[i] = v * of_row * rstd * w[c + i];
           if (y) st_t(y[o + c + i], f[i]);
           m = max(m, abs_bits(f[i]));
         }
@@ -360,12 +380,12 @@ __global__ void __launch_bounds__(1024) norm_fwd_wide_kernel(const T* x, const T
     for (int c = threadIdx.x; c < d; c += 1024) {
       const float v = at(c);
       if (sum) st_t(sum[o + c], v);
-      st_t(y[o + c], fmaf((v - mu) * rstd, w[c], b ? b[c] : 0.f));
+      st_t(y[o + c], fmaf((v - mu) * of_row * rstd, w[c], b ? b[c] : 0.f));
     }
   }
   if (threadIdx.x == 0) {
     if (!RMS) mean_out[blockIdx.x] = mu;
-    rstd_out[blockIdx.x] = rstd;
+    rstd_out[blockIdx.x] = rstd * of_row;
   }
 }
 
@@ -545,22 +565,26 @@ __global__ void __launch_bounds__(WARP ? 32 * kNormWarps : 1024, WARP ? 8 : 1) n
     // behind the barrier that follows its readers)
     if (RMS) turn ^= 1;
     const float ms = row_sum(acc, red[RMS ? turn : 1]) * inv_d + eps;
-    float rstd = 1.f / sqrtf(ms);
+    float rstd = 1.f / sqrtf(ms), of_row = 1.f;
     if (RMS && out_of_range(ms)) {
-      const float f = into_range(ms);
+      const Range r = into_range(ms);
       acc = 0.f;
 #pragma unroll
-      for (int q = 0; q < N; ++q) acc = fmaf(s[q] * f, s[q] * f, acc);
+      for (int q = 0; q < N; ++q) {
+        acc = fmaf(s[q] * r.sum, s[q] * r.sum, acc);
+        s[q] *= r.row;
+      }
       turn ^= 1;
-      rstd = f / sqrtf(row_sum(acc, red[turn]) * inv_d + eps * f * f);
+      rstd = rstd_in_range(r, row_sum(acc, red[turn]) * inv_d, eps);
+      of_row = r.row;
+    }
+    if (lane == 0) {
+      if (!RMS) mean_out[t] = mu;
+      rstd_out[t] = rstd * of_row;
     }
 #pragma unroll
     for (int q = 0; q < N; ++q) s[q] = fmaf(s[q] * rstd, wv[q], bv[q]);
     store(y, s);
-    if (lane == 0) {
-      if (!RMS) mean_out[t] = mu;
-      rstd_out[t] = rstd;
-    }
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
