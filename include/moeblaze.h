@@ -96,7 +96,8 @@ typedef struct {
  *   padded rows x h/128) | of B
  * (rows that belong to no token are unspecified).  The backward leaves it as
  * it is, so that it can run again, and takes scratch for dA and dB in its
- * place: one such scratch serves the layers of a model in turn. */
+ * place, so that the mode saves memory where one such scratch serves the
+ * layers of a model in turn (from three layers on). */
 #define MOEBLAZE_CHECKPOINT_8BIT 4
 
 /* The index structures of MoEBlaze (awesome-system-papers page, section

@@ -551,10 +551,20 @@ class LayerBuffers:
     bwd_ws: torch.Tensor
 
 
-def alloc_layer(shape: Shape, device="cuda") -> LayerBuffers:
-    return LayerBuffers(_bytes(moeblaze_saved_bytes(shape), device),
-                        _bytes(moeblaze_forward_workspace_bytes(shape), device),
-                        _bytes(moeblaze_backward_workspace_bytes(shape), device))
+def alloc_layer(shape: Shape, device="cuda", scratch: Optional[LayerBuffers] = None) -> LayerBuffers:
+    """The buffers of one layer.  scratch: another layer's, whose fwd_ws and bwd_ws this one then uses too (nothing
+    in them outlives a call, so layers that run in turn may)."""
+    need = (("fwd_ws", moeblaze_forward_workspace_bytes(shape)), ("bwd_ws", moeblaze_backward_workspace_bytes(shape)))
+    saved = _bytes(moeblaze_saved_bytes(shape), device)
+    if scratch is None:
+        return LayerBuffers(saved, *[_bytes(n, device) for _, n in need])
+    for name, n in need:
+        t = getattr(scratch, name)
+        if t.nbytes < n:
+            raise ValueError(f"scratch: {name} has {t.nbytes} bytes, this layer needs {n}")
+        if t.device != saved.device:
+            raise ValueError(f"scratch: on {t.device}, but the layer is on {saved.device}")
+    return LayerBuffers(saved, scratch.fwd_ws, scratch.bwd_ws)
 
 
 def forward(shape: Shape, x, gates, disp: DispatchBuffers, W1, W2, W3, y, layer: LayerBuffers, stream=None):

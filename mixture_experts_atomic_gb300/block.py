@@ -181,13 +181,15 @@ class MoEBlock:
 
     def __init__(self, L: int, d: int, h: int, E: int, K: int, dtype: torch.dtype, act: str = "swiglu",
                  eps: float = 1e-5, device="cuda", recompute_h: bool = False, checkpoint8: bool = False,
-                 norm: str = "layer"):
-        """recompute_h, checkpoint8: what the layer keeps for its backward (see MoELayer); norm: "layer" or "rms"."""
+                 norm: str = "layer", scratch: Optional["MoEBlock"] = None):
+        """recompute_h, checkpoint8: what the layer keeps for its backward; scratch: a block whose layer's scratch this
+        one's uses too (see MoELayer); norm: "layer" or "rms"."""
         if norm not in ("layer", "rms"):
             raise ValueError(f"norm: {norm!r}, expected 'layer' or 'rms'")
         self.rms = norm == "rms"
         self.norm = (RMSNorm if self.rms else LayerNorm)(L, d, dtype, eps, device)
-        self.layer = MoELayer(L, d, h, E, K, dtype, act, device, recompute_h=recompute_h, checkpoint8=checkpoint8)
+        self.layer = MoELayer(L, d, h, E, K, dtype, act, device, recompute_h=recompute_h, checkpoint8=checkpoint8,
+                              scratch=None if scratch is None else scratch.layer)
         self.loss = BalanceLoss(L, E, K, device)
         self.grad = RouterGrad(L, d, E, dtype, device)
         self.logits = torch.empty((L, E), dtype=torch.float32, device=device)

@@ -13,12 +13,18 @@ from . import binding as B
 
 class MoELayer:
     def __init__(self, L: int, d: int, h: int, E: int, K: int, dtype: torch.dtype, act: str, device="cuda",
-                 with_dgates: bool = True, recompute_h: bool = False, checkpoint8: bool = False):
+                 with_dgates: bool = True, recompute_h: bool = False, checkpoint8: bool = False,
+                 scratch: Optional["MoELayer"] = None):
         """recompute_h: keep no H / Hg temporaries (MOEBLAZE_RECOMPUTE_H):
         smaller scratch, the down projection and dW3 recompute them.
         checkpoint8: keep A and B in 8 bits (MOEBLAZE_CHECKPOINT_8BIT): half
         the bytes between forward and backward; the backward's scratch grows
-        by dA and dB.  bf16 without recompute_h."""
+        by dA and dB, so that it saves memory where layers share that
+        scratch.  bf16 without recompute_h.
+        scratch: a layer of this size at least, on the same device, whose
+        scratch this one uses in place of its own: for a model's layers, whose
+        forwards and backwards run one after the other (one stream, or streams
+        that wait for each other; graphs of them are not replayed at once)."""
         flags = (B.RECOMPUTE_H if recompute_h else 0) | (B.CHECKPOINT_8BIT if checkpoint8 else 0)
         self.shape = B.make_shape(L, d, h, E, K, dtype, act, flags)
         if checkpoint8 and act != "identity" and (recompute_h or dtype != torch.bfloat16):
@@ -26,7 +32,7 @@ class MoELayer:
         self.L, self.d, self.h, self.E, self.K = L, d, h, E, K
         self.dtype, self.act, self.device = dtype, act, device
         self.disp = B.alloc_dispatch(self.shape, device)
-        self.bufs = B.alloc_layer(self.shape, device)
+        self.bufs = B.alloc_layer(self.shape, device, None if scratch is None else scratch.bufs)
         self.y = torch.empty((L, d), dtype=dtype, device=device)
         self.dX = torch.empty((L, d), dtype=dtype, device=device)
         # gate gradients (for a router's backward): optional extra output
@@ -40,9 +46,9 @@ class MoELayer:
 
     @classmethod
     def for_config(cls, cfg, device="cuda", with_dgates: bool = True, recompute_h: bool = False,
-                   checkpoint8: bool = False):
+                   checkpoint8: bool = False, scratch: Optional["MoELayer"] = None):
         return cls(cfg.L, cfg.d, cfg.h, cfg.E, cfg.K, cfg.torch_dtype, cfg.act, device, with_dgates, recompute_h,
-                   checkpoint8)
+                   checkpoint8, scratch)
 
     def dispatch(self, ids: torch.Tensor, validate: bool = False):
         B.dispatch_build(self.shape, ids, self.disp, validate=validate)
