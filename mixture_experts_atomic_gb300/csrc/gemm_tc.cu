@@ -22,7 +22,7 @@
 // descending order of expert load), so skewed expert loads balance.
 //
 // Wide tiles (up, down with stored H and dX from 32 k-blocks a tile; weight
-// gradients from 256 routed rows per expert): one CTA takes 256
+// gradients from 256 routed rows per expert, see wide_stage): one CTA takes 256
 // output rows, as two M=128 MMAs per 16-deep step that share every B tile,
 // into one 512-column accumulator.  A k-block then brings 64 KB for
 // 8.4 MFLOP instead of 48 KB for 4.2; the price is that the epilogue is not
@@ -148,17 +148,31 @@ __host__ __device__ constexpr bool widenable(int m) {
 //   250 (d 4096, h 14336, 8)                   0.97, 0.60   0.90, 0.49
 //   375 (SiLU, d 1024, h 4096, 8)              0.064, 0.072 0.062, 0.064
 //   175 (the same)                             0.043, 0.045 0.045, 0.045
-//   500 (d 512, h 512, 4: 32 wide tiles)       0.016, 0.018 0.021, 0.021
-// So from 256 rows an expert where the wide tiles still fill the SMs, and from
-// 4,096 always: half as many SMs with tiles of twice the work.
-constexpr int64_t kWideMinRows = 256, kWideAlwaysRows = 4096;  // routed rows per expert, on average
+// With few tiles the rounds of the SMs decide: a wide tile takes about 1.65 times
+// as long as a 128-row one and there are half as many.  us, by wide tiles on 152
+// SMs (SiLU, d 1024; so from half an SM's worth of tiles up to one, and from one
+// and a half):
+//   64  (h 2048, 2)   256 rows 18, 20   20, 21    700  21, 22   25, 26    5,000  66, 69    83, 92
+//   96  (h 1536, 4)   256      21, 23   19, 21    700  29, 32   28, 28
+//   128 (h 2048, 4)   256      22, 25   21, 21    700  32, 35   29, 30
+//   176 (h 1024, 11)  256      27, 29   31, 31    700  40, 43   44, 46    5,000  203, 198  189, 192
+//   192 (h 4096, 3)   256      30, 33   30, 31    700  41, 45   41, 43
+//   208 (h 1024, 13)  256      29, 31   32, 31    700  42, 46   47, 50    5,000  216, 214  210, 209
+//   240 (h 3840, 4)   256      33, 37   32, 34    700  47, 51   44, 47
+//   320 (h 5120, 4)   256      40, 47   44, 43    700  60, 63   54, 56
+// From 4,096 rows an expert the wide tiles win as soon as they occupy more than
+// half of the SMs (160, d 512: 203, 201 against 190, 195 us).
+constexpr int64_t kWideMinRows = 256, kWideLongRows = 4096;  // routed rows per expert, on average
 // out_rows: rows of the weight gradient.  A last tile of 128 rows is allowed
 // where the A operand comes by TMA (dW3: the rows past the end load as zeros
 // and are not stored); the gathered A of dW1 needs whole 256-row tiles.
 inline bool wide_stage(const moeblaze_shape& s, int out_rows, int n_tiles, bool half_tail_ok) {
   if (out_rows % (half_tail_ok ? BM : 2 * BM) != 0) return false;
-  const int64_t rows = s.L * s.K, tiles = (int64_t)((out_rows + 2 * BM - 1) / (2 * BM)) * n_tiles * s.E;
-  return rows >= kWideAlwaysRows * s.E || (rows >= kWideMinRows * s.E && tiles >= sm_count());
+  const int64_t rows = s.L * s.K, per = (int64_t)n_tiles * s.E, sms = sm_count();
+  const int64_t narrow = out_rows / BM * per, tiles = (out_rows + 2 * BM - 1) / (2 * BM) * per;
+  if (rows < kWideMinRows * s.E) return false;
+  if (rows >= kWideLongRows * s.E) return 2 * tiles > sms;
+  return 33 * ((tiles + sms - 1) / sms) < 20 * ((narrow + sms - 1) / sms);
 }
 // The ring: 4 stages of A (16 KB) + B operand (32 KB); the fused SwiGLU
 // stages add the saved-B tile (16 KB) to every stage and keep 3 of them;
