@@ -473,19 +473,45 @@ auto combine_kernel(int K) {
        : K <= 6 ? combine_rows_kernel<T, 6> : combine_rows_kernel<T, kMaxK>;
 }
 
-// The most tokens a call of this shape takes the path for few tokens with: its
-// experts have less than a tile of 32 on average, and the slots fit its table.
-// Both paths, us (few | prompts), by slots an expert:
-//   d 4096, h 14336, 2 of 8     16  269 | 335    24  274 | 336    32  365 | 338
-//   d 2048, h 1408, 6 of 64     8   131 | 183    16  149 | 185    24  160 | 185
-//   d 2048, h 1024, 8 of 256    4   300 | 481     8  312 | 481
-//   d 1024, h 4096, 1 of 16     8    73 |  80    16   81 |  81    32  115 |  81
-//   d 512, h 512, 8 of 256      2    78 | 107    16  112 | 125
-//   d 256, h 512, 4 of 128      8    46 |  57    24   59 |  60
-//   d 1024, h 1024, 2 of 4      2    28 |  27    16   31 |  28
-constexpr int kFewPerExpert = 24;
+// The most tokens a call of this shape takes the path for few tokens with, by
+// slots an expert.  That path reads an expert's weights once for each 32 of its
+// tokens, the prompts' once for each 256; it has more than 32 where the average is
+// high or the routing uneven.  Both paths, us (few | prompts), slots drawn evenly,
+// and with experts as unequal as exp of a normal number:
+//   d 4096, h 14336, 2 of 8     16  263 | 350, 287 | 343   20  269 | 351, 285 | 317   24  281 | 351, 350 | 351
+//   d 4096, h 1536, 8 of 128    16  454 | 657, 470 | 492   20  468 | 659, 502 | 515   24  485 | 666, 574 | 534
+//   d 4096, h 14336, 2 of 8, SiLU  16  216 | 241, 222 | 234   20  221 | 241, 253 | 237   24  224 | 241, 263 | 241
+//   d 2048, h 1408, 6 of 64     16  142 | 189, 145 | 153   20  148 | 188, 160 | 156   24  155 | 188, 174 | 159
+//   d 2048, h 8192, 2 of 8      16  111 | 123, 120 | 122   20  114 | 124, 132 | 122   24  119 | 124, 130 | 112
+//   d 1024, h 2816, 1 of 200     8  364 | 541, 269 | 252   12  397 | 543, 329 | 281   16  426 | 546, 399 | 303
+//   d 1024, h 4096, 1 of 16      8   70 | 79,   69 | 66    12   74 | 79,   76 | 69    16   78 | 79,   78 | 70
+//   d 1024, h 2048, 2 of 32      8   70 | 84,   69 | 68    12   75 | 84,   72 | 67    16   78 | 85,   81 | 75
+//   d 512, h 512, 8 of 256       8   88 | 118,  86 | 77    12   98 | 119, 101 | 86    16  108 | 121, 114 | 92
+//   d 256, h 512, 4 of 128       8   45 | 54,   44 | 41    12   50 | 55,   47 | 45    16   52 | 55,   53 | 42
+// So up to where one routing loses as much as the other gains: 20, and 12 where a
+// tile of the prompts' up projection has fewer than 16 blocks.  Where all slots fall
+// on one of many experts the prompts' path is up to four times as fast (d 1024, h
+// 2816, 1 of 200, 12 slots an expert: 187 | 48).
+constexpr int kFewLong = 20, kFewShort = 12, kLongBlocks = 16;
+// Layers so small that the prompts' path has few rounds of short tiles are its own
+// with one token already: rounds of tiles over the pairs of SMs, by the blocks of a
+// tile and three for its end, of both products (few | prompts at 2 and 8 slots):
+//   18  d 512, h 1024, 2 of 8    23 | 22, 24 | 22      33  d 512, h 2048, 2 of 8    25 | 31, 26 | 32
+//   22  d 1024, h 1024, 2 of 4   26 | 24, 27 | 24      33  d 2048, h 512, 2 of 16   31 | 37, 33 | 38
+//   26  d 1024, h 1536, 2 of 4   27 | 26, 28 | 26      38  d 2048, h 2048, 1 of 1   27 | 32, 27 | 32
+//   30  d 1536, h 1536, 1 of 2   26 | 28, 28 | 29      46  d 1024, h 4096, 1 of 1   27 | 33, 28 | 33
+// SiLU, whose up projection has half as many tiles:
+//   30  d 1024, h 2048, 2 of 8   37 | 32, 37 | 32      57  d 1024, h 4096, 2 of 8   48 | 45, 50 | 46
+//   38  d 2048, h 2048, 1 of 2   35 | 34, 36 | 34      66  d 2048, h 1408, 4 of 16  58 | 56, 58 | 59
+constexpr int64_t kSmallSwiglu = 28, kSmallSilu = 60;
 int64_t few_tokens(const moeblaze_shape& s) {
-  const int64_t slots = kFewPerExpert * (int64_t)s.E < kFewSlots ? kFewPerExpert * (int64_t)s.E : kFewSlots;
+  const bool sw = s.act == MOEBLAZE_SWIGLU;
+  const int64_t pairs = sm_count() / 2;
+  const int64_t up = (int64_t)s.E * (sw ? s.h / 128 : (s.h + 255) / 256), down = (int64_t)s.E * ((s.d + 255) / 256);
+  const int64_t blocks = (up + pairs - 1) / pairs * (s.d / kBlock8 + 3) + (down + pairs - 1) / pairs * (s.h / kBlock8 + 3);
+  if (blocks < (sw ? kSmallSwiglu : kSmallSilu)) return 0;
+  const int64_t per = s.d / kBlock8 >= kLongBlocks ? kFewLong : kFewShort;
+  const int64_t slots = per * s.E < kFewSlots ? per * s.E : kFewSlots;
   return slots / s.K;
 }
 

@@ -1,5 +1,6 @@
-// The experts' products on 8-bit floating-point weights, for few tokens: every
-// used expert's weights are read once, and that is what the time goes to.
+// The experts' products on 8-bit floating-point weights, for few tokens: a used
+// expert's weights are read once for each 32 of its tokens, so once for most, and
+// that is what the time goes to (fp8.cu: from when on not).
 //
 // The tensor cores take the weights as the M operand: a 128 x 128 block of them
 // (or two, of W1 and W2, or of neighbouring output rows) against 16 or 32
