@@ -130,7 +130,7 @@ moeblaze_status check_fp8_shape(const moeblaze_shape* s) {
   if (s->act == MOEBLAZE_IDENTITY || s->dtype != MOEBLAZE_BF16) return MOEBLAZE_ERR_UNSUPPORTED;
   if (check_fp8_matrix(s->E, s->d, s->h) != MOEBLAZE_OK || check_fp8_matrix(s->E, s->h, s->d) != MOEBLAZE_OK)
     return MOEBLAZE_ERR_UNSUPPORTED;
-  // launches of a warp a token and of a thread for four of a row's columns
+  // launches of a warp a token and of a thread for eight of a row's columns
   if (s->L * (int64_t)s->d >= (int64_t(1) << 40)) return MOEBLAZE_ERR_UNSUPPORTED;
   return MOEBLAZE_OK;
 }

@@ -5,8 +5,8 @@
 //
 // The scale is a power of two, so that dividing by it is exact and the values
 // round once, as e4m3 does at any scale; what a power of two leaves unused of
-// the range, one binade at most, is at its small end (2^-15 to 2^-16 of the
-// block's largest).  Whoever reads rows takes any fp32 scale.
+// the range, one binade at most, is at its small end (the least normal value is
+// 2^-14 to 2^-15 of the block's largest, the least of all 2^-17 to 2^-18).  Whoever reads rows takes any fp32 scale.
 //
 // A NaN or an infinity makes the scale NaN, and with it the block: e4m3 has no
 // infinity, and the conversion would make it 448.  The largest magnitude is

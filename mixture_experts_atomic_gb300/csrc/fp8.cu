@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(kWThreads) quantize_weights_kernel(const T* __
   const int64_t e = blockIdx.z, base = e * R * N;
   if (threadIdx.x == 0) top = 0u;
   __syncthreads();
-  // thread: 8 columns of rows ty + 32 i
+  // thread: 8 columns of rows 4 ty + i
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   float v[4][8];
   uint32_t m = 0u;

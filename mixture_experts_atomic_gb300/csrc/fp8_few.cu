@@ -21,8 +21,8 @@
 // ends.
 //
 // Measured, the whole call: d 4096, h 14336, 2 of 8 experts 1 token 89 us (352 MB:
-// 4.0 TB/s), 16 tokens 204 us (1.41 GB: 6.9 TB/s); d 2048, h 1408, 6 of 64, 61
-// tokens 98 to 112 us.  At one token the weights stream at 7.1 TB/s from 8 us on,
+// 4.0 TB/s), 16 tokens 186 to 214 us, by how many experts the draw uses (all eight:
+// 1.41 GB, 6.6 TB/s); d 2048, h 1408, 6 of 64, 61 tokens 97 to 114 us.  At one token the weights stream at 7.1 TB/s from 8 us on,
 // where rows, table and first loads have come; the CTAs end between 38 and 47 us,
 // the down projection has its rows 8 us later, and the sum of the slots takes 5.
 // Beside it: weights not packed in blocks 260 against 239 us (16 tokens); a tile's

@@ -19,9 +19,10 @@
 // a thread) while the other one is computed: 512 cycles of tensor pipe beside
 // 256 of TMEM reads and 128 of packed FMAs.
 //
-// Measured: 8192 tokens, d 4096, h 14336, 2 of 8: up 1.58 and down 0.73 ms (2.43
-// and 2.64 PFLOP/s; 1.9 is the bf16 peak of a plain product), 2.57 ms in all;
-// d 2048, h 1408, 6 of 64, 16384 tokens 1.02 ms.  The tensor pipe is busy for half
+// Measured: 8192 tokens, d 4096, h 14336, 2 of 8: up 1.60 and down 0.73 ms (2.41
+// and 2.64 PFLOP/s; 1.9 is the bf16 peak of a plain product), 2.42 ms in all, 2.58
+// to 2.64 in runs that last (the power cap); d 2048, h 1408, 6 of 64, 16000 tokens
+// 1.02 to 1.06 ms.  The tensor pipe is busy for half
 // of the time: a block takes 800 to 950 cycles, from the MMAs' end over the commit,
 // the reads of TMEM and the arrivals on the other SM to the next MMAs into that
 // accumulator.  (With half of each accumulator read, which is wrong, 2.8 PFLOP/s.)
